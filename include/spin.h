@@ -327,6 +327,104 @@ int spin_select_noalloc(const float* summ, const uint16_t* q, int32_t units, int
  * memory mapped for the device. */
 int spin_measure_host_read(const void* host, int64_t bytes, int32_t ctas_per_sm, double* gbs, spin_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The 8-bit paged cache: keys and values that stay in HBM, appended with the position
+ * rotation on the way and attended in place. No counterpart on the SPIN pages; its pages
+ * are per KV head and hold one 64-token partition, as everywhere in this library, so the
+ * partitions that Select picks (spin_select_noalloc, over the summaries the append writes)
+ * go straight into the attention as a page list.
+ *
+ * One spin_kv8 describes one layer's cache. The caller owns every array of it; the calls
+ * allocate nothing, keep nothing between calls, and may be captured into CUDA graphs.
+ * Request b holds len = past[b] + new tokens after a step's append. Tokens 64p .. 64p+63
+ * of KV head h with 64(p+1) <= len are page table[b][h][p] of the pool, in e4m3 with one
+ * power-of-two scale for the keys and one for the values; the newest len % 64 tokens are
+ * rows 0 .. of the request's tail, in bf16. A page is quantised once, when its last token
+ * arrives, from the bf16 rows: how the tokens were split into calls changes no bit of it.
+ *
+ * Streams. All work is asynchronous on `stream`. Calls that write one cache, and calls
+ * that read what they wrote, must be ordered on one stream or by events; so must calls
+ * that share a workspace.
+ *
+ * Errors. Arguments are checked on the host (SPIN_ERR_INVALID, nothing enqueued). What
+ * only the device can see sets bits in *error: a request whose past, cu_new or lengths are
+ * out of range is left out by both calls (its rows are not written), a page id outside the
+ * pool is not written by the append and not attended by the attention.
+ * spin_kv8_status turns the word into a status. */
+typedef struct spin_kv8 {
+  int32_t batch;            /* 1 <= B <= 16384 requests */
+  int32_t q_heads;          /* Hq; Hq % Hkv == 0 and Hq / Hkv <= SPIN_MAX_GROUP */
+  int32_t kv_heads;         /* 1 <= Hkv <= 4096 */
+  int32_t max_pages;        /* entries of a table row, 1 .. 2^24: a request may hold 64 * max_pages + 63 tokens */
+  int64_t n_pages;          /* pages of the pool, 1 .. 2^24 */
+  uint8_t* pages;           /* [n_pages][2][64][128] e4m3, keys then values; 128-byte aligned */
+  float* scales;            /* [n_pages][2]: value = code * scale. The append writes the smallest power of two
+                               s >= 2^-64 with max|x| <= 448 s; the attention takes any positive scale. NaN:
+                               the half held a value that was not finite, and every query that sees a token of
+                               the page gets NaN. 8-byte aligned */
+  uint16_t* tails;          /* bf16 [batch][kv_heads][2][64][128], keys then values; 16-byte aligned */
+  float* summaries;         /* fp32 [batch][kv_heads][max_pages][128]: the mean (rotated, bf16) key of each page, in the
+                               layout spin_select_noalloc reads; NULL: not wanted. 16-byte aligned */
+  const int32_t* table;     /* [batch][kv_heads][max_pages] page ids. The append needs the entries of the pages it
+                               completes (each its own page), the attention those of every page it attends;
+                               other entries are not read */
+  uint32_t* error;          /* device error word; bits are only ever set */
+  int32_t device;           /* CUDA device ordinal of all of these */
+  int32_t rot_dim;          /* dimensions of a head that are rotated: 0 .. 128, a multiple of 16 */
+  int32_t interleaved;      /* 0: dimension j pairs with j + rot_dim / 2; 1: 2j pairs with 2j + 1 */
+  int32_t reserved;         /* 0 */
+  const double* inv_freq;   /* host [rot_dim / 2]: the angle of pair j is position * inv_freq[j] radians, taken modulo
+                               a turn in 64-bit integers, so far positions lose nothing. Read during the call */
+} spin_kv8;
+
+/* The new tokens of one step, the same for every layer. Device arrays; host bounds. */
+typedef struct spin_kv8_step {
+  const int32_t* past;      /* [batch] tokens in the cache before the step, >= 0 */
+  const int32_t* cu_new;    /* [batch + 1] request b's new tokens are rows cu_new[b] .. cu_new[b+1] - 1, ascending from
+                               0; none is allowed. Rows from cu_new[batch] on are padding: read and written by nothing */
+  int32_t total_new;        /* rows of q, k, v and out: cu_new[batch] <= total_new */
+  int32_t max_new;          /* no request has more new tokens than this, 1 .. 2^20 */
+} spin_kv8_step;
+
+/* Rows of bf16 heads in device memory: element (t, h, d) at ptr + t * token_stride + h *
+ * head_stride + d. Strides in elements, multiples of 8; ptr 16-byte aligned. */
+typedef struct spin_rows {
+  void* ptr;
+  int64_t token_stride;
+  int64_t head_stride;
+} spin_rows;
+
+/* Rotates the step's queries and keys by their positions and appends its keys and values:
+ * q_out = rotated q (may be q itself), pages, scales, summaries and tails as described
+ * above. The position of request b's i-th new token is past[b] + i, or positions[row]
+ * (device int32 [total_new], may be NULL). q, q_out: [total_new][q_heads]; k, v:
+ * [total_new][kv_heads]. q and q_out may both be NULL (keys and values alone). Rotated
+ * values are rounded to bf16 once; a key of a page goes to e4m3 from that bf16 value. */
+int spin_kv8_append(const spin_kv8* cache, const spin_kv8_step* step, const spin_rows* q, const spin_rows* q_out,
+                    const spin_rows* k, const spin_rows* v, const int32_t* positions, spin_stream_t stream);
+
+/* Bytes of device workspace that any spin_kv8_attend on this cache needs. */
+int spin_kv8_workspace(const spin_kv8* cache, int64_t* bytes);
+
+/* Attention of the step's queries over the cache as it is after the step's append: row i
+ * of request b sees the tokens at 0 .. past[b] + i. sel (device int32
+ * [batch * kv_heads][topk], may be NULL): only the pages listed for the unit, and the
+ * tail; -1, and any page that is not complete, is no page; a page must not be listed twice.
+ * q: rotated bf16 [total_new][q_heads]; out: bf16 [total_new][q_heads] = softmax(scale *
+ * q K^T) V, zeros where a row sees nothing. Softmax statistics and sums are fp32; the
+ * products run on fp16 operands, which hold e4m3 codes exactly, queries and tail rows to
+ * 2^-24 of their row's or 16-token group's largest value, and probabilities to 2^-11 of themselves.
+ * workspace: device memory of spin_kv8_workspace bytes, 16-byte aligned; needs no
+ * initialisation and holds nothing between calls. */
+int spin_kv8_attend(const spin_kv8* cache, const spin_kv8_step* step, const spin_rows* q, const spin_rows* out,
+                    float scale, const int32_t* sel, int32_t topk, void* workspace, int64_t workspace_bytes,
+                    spin_stream_t stream);
+
+/* Waits for `stream`, then turns the error word into a status: SPIN_ERR_CAPACITY (a
+ * request outgrew its table row), SPIN_ERR_INVALID (lengths or page ids out of range),
+ * SPIN_ERR_TIMEOUT (a bounded device wait ran out), else SPIN_OK. The word stays set. */
+int spin_kv8_status(const spin_kv8* cache, spin_stream_t stream);
+
 /* Releases everything the context owns (synchronises first). NULL is a no-op. */
 void spin_destroy(spin_ctx* ctx);
 

@@ -39,7 +39,8 @@ SPIN_NOALLOC_MAX_SCORES_DEFAULT = 1 << 20  # SPIN_NOALLOC_MAX_SCORES in include/
 # Every symbol include/spin.h declares.
 EXPORTS = ("spin_create", "spin_index_offload", "spin_index_offload_parts", "spin_append_kv", "spin_set_buffer", "spin_decode_step", "spin_decode_step_host", "spin_stats",
            "spin_debug_export", "spin_debug_read_page", "spin_debug_summaries", "spin_destroy", "spin_last_error",
-           "spin_select_noalloc", "spin_measure_host_read")
+           "spin_select_noalloc", "spin_measure_host_read", "spin_kv8_append", "spin_kv8_workspace", "spin_kv8_attend",
+           "spin_kv8_status")
 
 
 class SpinError(RuntimeError):
@@ -66,6 +67,44 @@ class spin_config(ctypes.Structure):
         ("append_tokens", ctypes.c_int32),
         ("max_partitions", ctypes.c_int32),
         ("max_context", ctypes.c_int64),
+    ]
+
+
+class spin_kv8(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("q_heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("n_pages", ctypes.c_int64),
+        ("pages", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("tails", ctypes.c_void_p),
+        ("summaries", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("error", ctypes.c_void_p),
+        ("device", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("inv_freq", ctypes.c_void_p),
+    ]
+
+
+class spin_kv8_step(ctypes.Structure):
+    _fields_ = [
+        ("past", ctypes.c_void_p),
+        ("cu_new", ctypes.c_void_p),
+        ("total_new", ctypes.c_int32),
+        ("max_new", ctypes.c_int32),
+    ]
+
+
+class spin_rows(ctypes.Structure):
+    _fields_ = [
+        ("ptr", ctypes.c_void_p),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
     ]
 
 
@@ -140,6 +179,16 @@ def load(build_if_missing: bool = True):
             L.spin_select_noalloc.restype = ctypes.c_int
             L.spin_measure_host_read.argtypes = [vp, i64, i32, ctypes.POINTER(ctypes.c_double), vp]
             L.spin_measure_host_read.restype = ctypes.c_int
+            # Structures of the 8-bit cache go by address (void pointers), so that callers on a hot
+            # path can keep one and pass it again.
+            L.spin_kv8_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
+            L.spin_kv8_append.restype = ctypes.c_int
+            L.spin_kv8_workspace.argtypes = [vp, ctypes.POINTER(i64)]
+            L.spin_kv8_workspace.restype = ctypes.c_int
+            L.spin_kv8_attend.argtypes = [vp, vp, vp, vp, ctypes.c_float, vp, i32, vp, i64, vp]
+            L.spin_kv8_attend.restype = ctypes.c_int
+            L.spin_kv8_status.argtypes = [vp, vp]
+            L.spin_kv8_status.restype = ctypes.c_int
             L.spin_last_error.argtypes = [vp]
             L.spin_last_error.restype = ctypes.c_char_p
             _lib = L
@@ -224,6 +273,31 @@ def spin_measure_host_read(host_ptr: int, nbytes: int, ctas_per_sm: int = 1, str
     g = ctypes.c_double(0.0)
     _check(load().spin_measure_host_read(host_ptr, nbytes, ctas_per_sm, ctypes.byref(g), stream))
     return g.value
+
+
+def _at(struct):
+    return None if struct is None else ctypes.addressof(struct)
+
+
+def spin_kv8_append(cache, step, q, q_out, k, v, positions_ptr=None, stream: int = 0):
+    """cache: spin_kv8; step: spin_kv8_step; q, q_out (or None), k, v: spin_rows."""
+    _check(load().spin_kv8_append(_at(cache), _at(step), _at(q), _at(q_out), _at(k), _at(v), positions_ptr, stream))
+
+
+def spin_kv8_workspace(cache) -> int:
+    n = ctypes.c_int64(0)
+    _check(load().spin_kv8_workspace(_at(cache), ctypes.byref(n)))
+    return n.value
+
+
+def spin_kv8_attend(cache, step, q, out, scale: float, sel_ptr, topk: int, workspace_ptr, workspace_bytes: int,
+                    stream: int = 0):
+    _check(load().spin_kv8_attend(_at(cache), _at(step), _at(q), _at(out), scale, sel_ptr, topk, workspace_ptr,
+                                  workspace_bytes, stream))
+
+
+def spin_kv8_status(cache, stream: int = 0):
+    _check(load().spin_kv8_status(_at(cache), stream))
 
 
 def spin_last_error(ctx=None) -> str:
