@@ -362,7 +362,8 @@ typedef struct spin_kv8 {
                                s >= 2^-64 with max|x| <= 448 s; the attention takes any positive scale. NaN:
                                the half held a value that was not finite, and every query that sees a token of
                                the page gets NaN. 8-byte aligned */
-  uint16_t* tails;          /* bf16 [batch][kv_heads][2][64][128], keys then values; 16-byte aligned */
+  uint16_t* tails;          /* bf16 [batch][kv_heads][2][64][128], keys then values; a value that is not finite makes
+                               NaN of every query that sees its token. 16-byte aligned */
   float* summaries;         /* fp32 [batch][kv_heads][max_pages][128]: the mean (rotated, bf16) key of each page, in the
                                layout spin_select_noalloc reads; NULL: not wanted. 16-byte aligned */
   const int32_t* table;     /* [batch][kv_heads][max_pages] page ids. The append needs the entries of the pages it

@@ -77,6 +77,9 @@ kv8_attend_simple_kernel(const Kv8Args a, const Rows q, const Rows out, float sc
       for (int u = 0; u < 2; ++u) {
         const int row = u * 32 + lane;
         float x = 0.f;
+        if (is_tail && row < rows)  // a value that is not finite makes NaN of every row that sees its token
+          for (int d = 0; d < kD; ++d)
+            x += bf(tail[row * kD + d]) * 0.f + bf(tail[kPart * kD + row * kD + d]) * 0.f;
         if (row < rows)
           for (int d = 0; d < kD; ++d) x += s_q[g][d] * (is_tail ? bf(tail[row * kD + d]) : e4m3(page[row * kD + d]));
         s[u] = row < rows ? x * ks * scale : -INFINITY;

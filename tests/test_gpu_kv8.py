@@ -393,8 +393,7 @@ def test_attend_all_zero_keys_and_values():
 @pytest.mark.parametrize("what", ["key", "value"])
 @pytest.mark.parametrize("x", [math.nan, math.inf, -math.inf])
 def test_attend_values_that_are_not_finite(where, what, x):
-    """A NaN, or an infinite value: a query that sees the token (its page, once complete) gets NaN, one
-    that does not is exact. An infinite key in the tail has an infinite score, of either sign."""
+    """A query that sees the token (its page, once complete) gets NaN; one that does not is exact."""
     p = Pair(1, 1, 2, 6, rot=0, seed=17)
     n = 64 * 3 + 30
     k, v = p.rand(n, 1, D), p.rand(n, 1, D)
