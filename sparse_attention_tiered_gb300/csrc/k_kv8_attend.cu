@@ -1,149 +1,723 @@
 // spin_kv8_attend: exact attention over the 8-bit paged cache.
 //
-// One CTA per (new token, KV head): four warps take pages in turn, a lane scores two tokens of
-// a page against the group's queries, then every lane gathers four dimensions of the values.
-// Running maximum and sum per query head and warp, joined at the end.
-#include "kv8.cuh"
+// Few rows a unit (single tokens, a few drafted ones) read the whole cache once: 256 bytes a
+// token and KV head against 4 * 128 * G flops, far below the tensor cores' rate, so the kernel is
+// built to keep the memory busy. One persistent CTA per SM takes an equal share of all pages of
+// all units in order (a unit may begin and end inside CTAs' shares). A producer warp streams pages
+// into a ring of 16 KB slots with one TMA copy each; eight consumer warps take them, four to a
+// page with 16 tokens each, every warp with a softmax state and output of its own. Those are
+// joined through shared memory at the end of a unit, and over CTAs by a second launch.
+//
+// Arithmetic. m16n8k16 products on fp16 operands with fp32 sums: rows x dimensions x tokens for
+// the scores, rows x tokens x dimensions for the output. Codes go to fp16 exactly; queries and
+// tail rows are scaled by a power of two into fp16's range. Each 64-token page has scales k and v:
+// with z = score * k * log2(e) + log2(v), the running maximum M of z (not of the score) and
+// P = 2^(z - M + 14), the output's weight is P and the softmax sum's is P / v. So blocks whose
+// values differ by any factor share one fp16 range, whose 28 binary orders below the largest weight
+// are normal numbers.
+//
+// Operand layout. The k index of a product and the n index may be permuted as long as both
+// operands agree, which is chosen so that no byte has to move between lanes: a lane's 16-byte chunk
+// of a key row is its own k indices of four products, and 16 bytes of a value row its n index of 16
+// products. With the copy's 128-byte swizzle and tokens in the order 0 5 2 7 4 1 6 3, all of these
+// 16-byte loads touch every bank once. Values need two tokens of one dimension side by side: one
+// byte permutation for two such pairs.
+#include "kv8_dev.cuh"
 
 namespace spin {
 
 namespace {
 
-constexpr int kWarps = 4;
+using namespace kv8;
 
-__device__ __forceinline__ float bf(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+constexpr int kConsWarps = 8;                           // two groups of four, a page each
+constexpr int kDecThreads = (kConsWarps + 4) * 32;      // and the producer's warpgroup, one warp of which works
+constexpr int kSlots = 8;                               // 16 KB each
+constexpr int kMaxCtas = 160;
+constexpr int kAccPad = 144;                            // floats of a row in the join: 4 x (32 + 4)
+constexpr int kMaxTileRows = 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kShift = 14.f;                          // weights reach 2^14
 
-__device__ __forceinline__ float e4m3(uint8_t c) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)c));
-  const uint16_t h = (uint16_t)r;
-  float f;
-  asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(h));
-  return f;
+struct SlotMeta {
+  float kfac;  // score factor: page scale * softmax scale * log2(e)
+  float vlog;  // log2 of the values' scale
+  float vinv;  // 1 / the values' scale
+  int pos0;    // position of its first token; -1: nothing to do
+};
+
+struct DecSmem {
+  uint64_t full[kSlots], empty[kSlots];
+  SlotMeta meta[kSlots];
+  int64_t scratch[36];
+  float m[kConsWarps][16], l[kConsWarps][16];
+  int abort;
+};
+
+constexpr size_t kRingBytes = (size_t)kSlots * kKv8PageBytes;
+constexpr size_t kJoinBytes = (size_t)kConsWarps * 16 * kAccPad * 4;
+
+template <int MT>
+constexpr size_t dec_smem_bytes() {
+  return 1024 + kRingBytes + kJoinBytes + (MT > 1 ? 8 * MT * 512 : 0) + sizeof(DecSmem);
 }
 
-__global__ void __launch_bounds__(kWarps * 32)
-kv8_attend_simple_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, const int32_t* sel, int topk) {
-  __shared__ float s_q[kMaxGroup][kD];
-  __shared__ float s_p[kWarps][kMaxGroup][kPart];
-  __shared__ float s_acc[kWarps][kMaxGroup][kD];
-  __shared__ float s_m[kWarps][kMaxGroup], s_l[kWarps][kMaxGroup];
-  const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int b = 0;
-  for (int lo = 0, n = a.B; n > 0;) {  // the last b with cu[b] <= t
-    const int half = n / 2;
-    if (a.cu[lo + half] <= t) {
-      b = lo + half;
-      lo += half + 1;
-      n -= half + 1;
-    } else {
-      n = half;
+// First item of CTA c of n, and the CTA that has item x.
+__device__ __forceinline__ int64_t share_start(int64_t total, int c, int n) { return total * c / n; }
+__device__ __forceinline__ int share_of(int64_t total, int64_t x, int n) { return (int)(((x + 1) * n - 1) / total); }
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"r"(kConsWarps * 32) : "memory"); }
+
+// A warp's softmax state of MT x 16 rows: lane (g, t) has rows g and g + 8 of each, and of them
+// dimensions 32 t .. 32 t + 31 of the output: element e of o[j] is row g + 8 (e / 2), dimension
+// 32 t + 16 (e % 2) + j.
+template <int MT>
+struct State {
+  float o[MT][16][4];
+  float m[MT][2], l[MT][2];
+};
+
+// Scores z of one row half (four tokens' worth in a lane) go in, fp16 weights come out.
+template <int MT>
+__device__ __forceinline__ void softmax_step(State<MT>& st, float (&z)[MT][2][4], float vinv, uint4 (&p)[MT]) {
+  float top[MT][2];
+  bool grew = false;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float x = fmaxf(fmaxf(z[mt][0][2 * r], z[mt][0][2 * r + 1]), fmaxf(z[mt][1][2 * r], z[mt][1][2 * r + 1]));
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+      top[mt][r] = fmaxf(st.m[mt][r], x);
+      grew |= top[mt][r] > st.m[mt][r];
     }
+  if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float f = top[mt][r] == -INFINITY ? 1.f : ex2(st.m[mt][r] - top[mt][r]);
+        st.m[mt][r] = top[mt][r];
+        st.l[mt][r] *= f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          st.o[mt][j][2 * r] *= f;
+          st.o[mt][j][2 * r + 1] *= f;
+        }
+      }
   }
-  int row0, n_new, past;
-  if (!kv8_request(a, b, tid == 0, row0, n_new, past) || t < row0 || t >= row0 + n_new) return;
-  const int64_t unit = (int64_t)b * a.Hkv + h;
-  const int len = past + n_new, full = len >> 6, seen = past + (t - row0) + 1;
-  for (int i = tid; i < a.G * kD; i += kWarps * 32)
-    s_q[i / kD][i % kD] = bf(q.p[(int64_t)t * q.ts + (int64_t)(h * a.G + i / kD) * q.hs + i % kD]);
-  __syncthreads();
-  float m[kMaxGroup], l[kMaxGroup], acc[kMaxGroup][4];
-  for (int g = 0; g < a.G; ++g) {
-    m[g] = -INFINITY;
-    l[g] = acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float base = (st.m[mt][r] == -INFINITY ? 0.f : st.m[mt][r]) - kShift;
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float& x = z[mt][i][2 * r + e];
+          x = x == -INFINITY ? 0.f : ex2(x - base);
+          s += x;
+        }
+      st.l[mt][r] += s == 0.f ? 0.f : s * vinv;  // a row that sees nothing here takes nothing of a NaN page
+    }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+    p[mt] = make_uint4(pack_half2(z[mt][0][0], z[mt][0][1]), pack_half2(z[mt][0][2], z[mt][0][3]),
+                       pack_half2(z[mt][1][0], z[mt][1][1]), pack_half2(z[mt][1][2], z[mt][1][3]));
+}
+
+// z = score * factor + vlog for the tokens a row may see, else -inf. pos[i][e]: position of the
+// lane's token of column e in token tile i.
+template <int MT>
+__device__ __forceinline__ void finish_scores(float (&z)[MT][2][4], const float (&qs)[MT][2], float kfac, float vlog,
+                                              bool masked, int pos0, const int (&see)[MT][2], int lane) {
+  const int t = lane & 3;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = e >> 1;
+        float x = fmaf(z[mt][i][e], kfac * qs[mt][r], vlog);
+        if (masked) {
+          const int tok = pos0 + i * 8 + ((e & 1) ? (2 * t) ^ 5 : 2 * t);
+          if (tok >= see[mt][r]) x = -INFINITY;
+        }
+        z[mt][i][e] = x;
+      }
+}
+
+template <int MT>
+__global__ void __launch_bounds__(kDecThreads, 1)
+kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, const Rows q, const Rows out, float scale,
+                  const int32_t* __restrict__ sel, int topk, float* __restrict__ partials) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  float* join = reinterpret_cast<float*>(ring + kRingBytes);
+  uint4* qfrag = reinterpret_cast<uint4*>(ring + kRingBytes + kJoinBytes);  // [8][MT][32], MT > 1 only
+  DecSmem& sm = *reinterpret_cast<DecSmem*>(ring + kRingBytes + kJoinBytes + (MT > 1 ? 8 * MT * 512 : 0));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kRows = 16 * MT;
+  const int first_row = (int)blockIdx.y * kRows;
+  volatile int* abort = &sm.abort;
+
+  if (tid == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(smem_u32(&sm.full[s]), 1);
+      mbar_init(smem_u32(&sm.empty[s]), 4);
+    }
+    sm.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  const int items = sel ? topk + 1 : full + 1;  // the last one: the tail
-  for (int it = warp; it < items; it += kWarps) {
-    const bool is_tail = it == items - 1;
-    const int p = is_tail ? full : sel ? sel[unit * topk + it] : it;
-    if (!is_tail && (p < 0 || p >= full)) continue;
-    const int rows = min(is_tail ? len & (kPart - 1) : kPart, seen - p * kPart);  // seen by this token
-    if (rows <= 0) continue;
-    const uint8_t* page = nullptr;
-    const uint16_t* tail = a.tails + unit * kPageElems;
-    float ks = 1.f, vs = 1.f;
-    if (!is_tail) {
-      const int id = a.table[unit * a.max_pages + p];
-      if (id < 0 || (int64_t)id >= a.n_pages) {
-        if (lane == 0) atomicOr(a.err, kErrIndex);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int ctas = gridDim.x, cta = blockIdx.x;
+  const bool report = cta == 0 && blockIdx.y == 0;
+  const Place pl = locate(a, first_row, kRows, topk, report, sm.scratch,
+                          [&](int64_t total) { return share_start(total, cta, ctas); });
+  const int64_t start = share_start(pl.total, cta, ctas), stop = share_start(pl.total, cta + 1, ctas);
+  if (start >= stop) return;
+
+  // 384 threads x 168 registers at launch: 128 x 56 + 256 x 224.
+  if (warp >= kConsWarps) {
+    // ------------------------------ producer ------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp != kConsWarps) return;
+    if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
+    uint32_t slot = 0, round = 0;  // the next slot, and how often the ring has been filled
+    bool ok = true;
+    int b = pl.b;
+    int64_t item = start, before = pl.before;
+    while (item < stop) {
+      const Unit u = unit_of(a, b, first_row, kRows, topk, false);
+      if (u.items == 0 || item >= before + (int64_t)u.items * a.Hkv) {
+        before += (int64_t)u.items * a.Hkv;
+        ++b;
         continue;
       }
-      page = a.pages + (int64_t)id * kKv8PageBytes;
-      ks = a.scales[2 * (int64_t)id];
-      vs = a.scales[2 * (int64_t)id + 1];
-    }
-    for (int g = 0; g < a.G; ++g) {
-      float s[2];
-      for (int u = 0; u < 2; ++u) {
-        const int row = u * 32 + lane;
-        float x = 0.f;
-        if (is_tail && row < rows)  // a value that is not finite makes NaN of every row that sees its token
-          for (int d = 0; d < kD; ++d)
-            x += bf(tail[row * kD + d]) * 0.f + bf(tail[kPart * kD + row * kD + d]) * 0.f;
-        if (row < rows)
-          for (int d = 0; d < kD; ++d) x += s_q[g][d] * (is_tail ? bf(tail[row * kD + d]) : e4m3(page[row * kD + d]));
-        s[u] = row < rows ? x * ks * scale : -INFINITY;
+      const int h = (int)((item - before) / u.items);
+      const int64_t unit = (int64_t)b * a.Hkv + h;
+      const int from = (int)(item - before - (int64_t)h * u.items);
+      const int to = (int)min((int64_t)u.items, from + (stop - item));
+      item += to - from;
+      // 32 page ids and scales at a time, a batch ahead of the copies
+      int id = -1, pos = -1;
+      float2 sc = make_float2(1.f, 1.f);
+      auto look = [&](int i) {
+        id = pos = -1;
+        if (i < min(to, u.pages)) {
+          const int p = topk ? sel[unit * topk + i] : i;
+          if (p >= 0 && p < u.full) {
+            id = a.table[unit * a.max_pages + p];
+            if (id < 0 || (int64_t)id >= a.n_pages) {
+              atomicOr(a.err, (uint32_t)kErrIndex);
+              id = -1;
+            } else {
+              pos = p * kPart;
+              sc = *reinterpret_cast<const float2*>(a.scales + 2 * (int64_t)id);
+            }
+          }
+        }
+      };
+      look(from + lane);
+      for (int base = from; base < min(to, u.pages); base += 32) {
+        const int my_id = id, my_pos = pos;
+        const float2 my_sc = sc;
+        look(base + 32 + lane);
+        const int n = min(32, min(to, u.pages) - base);
+        for (int i = 0; i < n; ++i) {
+          if (lane == i) {
+            const uint32_t full = smem_u32(&sm.full[slot]);
+            ok = ok && mbar_wait(smem_u32(&sm.empty[slot]), (round & 1) ^ 1, abort, a.err);
+            if (ok) {
+              if (my_id >= 0) tma_page(smem_u32(ring) + slot * kKv8PageBytes, &map, my_id, full);
+              sm.meta[slot] = SlotMeta{my_sc.x * scale * kLog2e, scale_log2(my_sc.y), 1.f / my_sc.y, my_pos};
+              mbar_arrive_expect_tx(full, my_id >= 0 ? kKv8PageBytes : 0);
+            }
+          }
+          __syncwarp();  // slots are filled in order: a lane that ran ahead would take a phase for a later one
+          if (++slot == kSlots) slot = 0, ++round;
+        }
+        ok = __all_sync(0xffffffffu, ok);
       }
-      float top = fmaxf(s[0], s[1]);
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float m2 = fmaxf(m[g], top);
-      const float base = m2 == -INFINITY ? 0.f : m2;  // every score NaN
-      const float keep = expf(m[g] - base);
-      float sum = 0.f;
-      for (int u = 0; u < 2; ++u) {
-        const float pr = u * 32 + lane < rows ? expf(s[u] - base) : 0.f;
-        s_p[warp][g][u * 32 + lane] = pr;
-        sum += pr;
+      if (to > u.pages) {  // the tail: keys in one slot, values in the next
+        for (int i = 0; i < 2; ++i) {
+          if (lane == 0) {
+            const uint32_t full = smem_u32(&sm.full[slot]);
+            const uint32_t bytes = u.tail * kD * 2;
+            ok = ok && mbar_wait(smem_u32(&sm.empty[slot]), (round & 1) ^ 1, abort, a.err);
+            if (ok) {
+              bulk_copy(smem_u32(ring) + slot * kKv8PageBytes, a.tails + unit * kPageElems + i * kPart * kD, bytes, full);
+              sm.meta[slot] = SlotMeta{scale * kLog2e, 0.f, 1.f, u.full * kPart};
+              mbar_arrive_expect_tx(full, bytes);
+            }
+          }
+          __syncwarp();
+          if (++slot == kSlots) slot = 0, ++round;
+        }
+        ok = __all_sync(0xffffffffu, ok);
       }
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      l[g] = l[g] * keep + sum;
-      m[g] = m2;
-      for (int d = 0; d < 4; ++d) acc[g][d] *= keep;
     }
-    __syncwarp();
-    for (int row = 0; row < rows; ++row) {
-      float x[4];
-      for (int d = 0; d < 4; ++d) {
-        const int at = kPart * kD + row * kD + lane * 4 + d;
-        x[d] = vs * (is_tail ? bf(tail[at]) : e4m3(page[at]));
+    // No copy may be in flight when the CTA's shared memory goes: every slot is waited for, whether
+    // or not the consumers got to it. (A slot that was never filled has nothing to wait for.)
+    if (lane == 0 && !ok) {
+      for (uint32_t s = 0; s < kSlots; ++s) {
+        const uint32_t fills = round + (s < slot ? 1 : 0);
+        int no_abort = 0;
+        if (fills) mbar_wait(smem_u32(&sm.full[s]), (fills - 1) & 1, &no_abort, a.err);
       }
-      for (int g = 0; g < a.G; ++g)
-        for (int d = 0; d < 4; ++d) acc[g][d] += s_p[warp][g][row] * x[d];
     }
-    __syncwarp();
+    return;
   }
-  for (int g = 0; g < a.G; ++g) {
-    for (int d = 0; d < 4; ++d) s_acc[warp][g][lane * 4 + d] = acc[g][d];
-    if (lane == 0) {
-      s_m[warp][g] = m[g];
-      s_l[warp][g] = l[g];
+
+  // ------------------------------ consumers ------------------------------
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+  const int g = lane >> 2, t = lane & 3;
+  const int group = warp >> 2, quarter = warp & 3;
+  const int pg = (g & 1) ? g ^ 4 : g;                // token order 0 5 2 7 4 1 6 3
+  State<MT> st;
+  uint32_t slot = 0, round = 0;
+  bool ok = true;
+  int b = pl.b, turn = 0;
+  int64_t item = start, before = pl.before;
+  while (item < stop) {
+    const Unit u = unit_of(a, b, first_row, kRows, topk, false);
+    if (u.items == 0 || item >= before + (int64_t)u.items * a.Hkv) {
+      before += (int64_t)u.items * a.Hkv;
+      ++b;
+      continue;
+    }
+    const int h = (int)((item - before) / u.items);
+    const int from = (int)(item - before - (int64_t)h * u.items);
+    const int to = (int)min((int64_t)u.items, from + (stop - item));
+    item += to - from;
+    const int rows = min(kRows, u.n_new * a.G - first_row);
+
+    // Queries: lane (g, t) holds dimensions 16 t .. and 64 + 16 t .. of its rows, four to a product.
+    uint4 qa[MT][8];
+    float qs[MT][2];
+    int see[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = mt * 16 + r * 8 + g;
+        const int i = (first_row + row) / a.G, head = h * a.G + (first_row + row) - i * a.G;
+        uint32_t w[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) w[x] = 0;
+        see[mt][r] = 0;
+        if (row < rows) {
+          see[mt][r] = u.past + i + 1;
+          const uint4* src = reinterpret_cast<const uint4*>(q.p + (int64_t)(u.row0 + i) * q.ts + (int64_t)head * q.hs);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<uint4*>(w + 4 * x) = src[(x >> 1) * 8 + 2 * t + (x & 1)];
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) top = __vmaxu2(top, w[x] & 0x7fff7fffu);
+        top = max(top & 0xffffu, top >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = half_exponent(top);
+        const float f = pow2(15 - e);
+        qs[mt][r] = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e - 15);
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const uint32_t v = pack_half2(lo_f(w[x]) * f, hi_f(w[x]) * f);
+          uint32_t* dst = reinterpret_cast<uint32_t*>(&qa[mt][x >> 1]);
+          dst[(x & 1) * 2 + r] = v;
+        }
+      }
+    if (MT > 1) {  // too many for registers: the same for all warps, in shared memory
+      consumers_sync();
+      if (warp == 0)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) qfrag[(k * MT + mt) * 32 + lane] = qa[mt][k];
+      consumers_sync();
+    }
+    auto query = [&](int mt, int k) -> uint4 { return MT > 1 ? qfrag[(k * MT + mt) * 32 + lane] : qa[mt][k]; };
+
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        st.m[mt][r] = -INFINITY;
+        st.l[mt][r] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) st.o[mt][j][2 * r] = st.o[mt][j][2 * r + 1] = 0.f;
+      }
+
+    for (int it = from; it < to; ++it, turn ^= 1) {
+      if (it < u.pages) {
+        if (turn == group) {
+          ok = mbar_wait(smem_u32(&sm.full[slot]), round & 1, abort, a.err) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          const SlotMeta me = sm.meta[slot];
+          if (ok && me.pos0 >= 0) {
+            const uint32_t keys = smem_u32(ring) + slot * kKv8PageBytes + quarter * 16 * kD;
+            const uint32_t vals = keys + kKv8HalfBytes;
+            float z[MT][2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t at = keys + (i * 8 + pg) * kD;
+              const uint4 c0 = lds128(at + ((t ^ pg) << 4)), c1 = lds128(at + (((t + 4) ^ pg) << 4));
+              const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) z[mt][i][0] = z[mt][i][1] = z[mt][i][2] = z[mt][i][3] = 0.f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t b0 = e4m3x2_half2(w[k], false), b1 = e4m3x2_half2(w[k], true);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) mma_f16(z[mt][i], query(mt, k), b0, b1);
+              }
+            }
+            uint4 vr[4];  // value rows 2 t, (2 t) ^ 5, and those 8 further
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int row = (x & 1) ? (2 * t) ^ 5 : 2 * t;
+              vr[x] = lds128(vals + ((x >> 1) * 8 + row) * kD + ((g ^ row) << 4));
+            }
+            const int pos = me.pos0 + quarter * 16;
+            finish_scores<MT>(z, qs, me.kfac, me.vlog, me.pos0 + kPart > u.past + 1, pos, see, lane);
+            uint4 p[MT];
+            softmax_step<MT>(st, z, me.vinv, p);
+            const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vr[0]);
+            const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vr[1]);
+            const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vr[2]);
+            const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vr[3]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {  // dimensions 4 x + 2 y, 4 x + 2 y + 1 of the lane's 16
+                const uint32_t lo = __byte_perm(v0[x], v1[x], y ? 0x7362 : 0x5140);
+                const uint32_t hi = __byte_perm(v2[x], v3[x], y ? 0x7362 : 0x5140);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t b0 = e4m3x2_half2(lo, e), b1 = e4m3x2_half2(hi, e);
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt) mma_f16(st.o[mt][4 * x + 2 * y + e], p[mt], b0, b1);
+                }
+              }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.empty[slot]));
+        }
+        if (++slot == kSlots) slot = 0, ++round;
+        continue;
+      }
+      // The tail. Rows are bf16; each warp scales its 16 tokens' keys, and values, by a power of two.
+      const uint32_t s1 = slot + 1 == kSlots ? 0 : slot + 1, r1 = slot + 1 == kSlots ? round + 1 : round;
+      if (turn == group) {
+        ok = mbar_wait(smem_u32(&sm.full[slot]), round & 1, abort, a.err) && ok;
+        ok = mbar_wait(smem_u32(&sm.full[s1]), r1 & 1, abort, a.err) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        const SlotMeta me = sm.meta[slot];
+        const int have = u.tail - quarter * 16;  // of this warp's tokens
+        if (ok && have > 0) {
+          const uint32_t keys = smem_u32(ring) + slot * kKv8PageBytes + quarter * 16 * kD * 2;
+          const uint32_t vals = smem_u32(ring) + s1 * kKv8PageBytes + quarter * 16 * kD * 2;
+          uint32_t bad[2][2];  // tokens of the lane's columns that hold something not finite
+          // keys: per token tile, 16 + 16 dimensions of the lane's token
+          uint4 kr[2][4];
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t wrong = 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (i * 8 + pg < have) w = lds128(keys + (i * 8 + pg) * kD * 2 + ((x >> 1) * 8 + 2 * t + (x & 1)) * 16);
+              uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const uint32_t inf_lo = (ww[y] & 0x7f80u) == 0x7f80u, inf_hi = (ww[y] & 0x7f800000u) == 0x7f800000u;
+                wrong |= inf_lo | inf_hi;
+                if (inf_lo) ww[y] &= 0xffff0000u;
+                if (inf_hi) ww[y] &= 0x0000ffffu;
+                top = __vmaxu2(top, ww[y] & 0x7fff7fffu);
+              }
+              kr[i][x] = w;
+            }
+            const uint32_t who = __ballot_sync(0xffffffffu, wrong != 0);
+            bad[i][0] = who >> (8 * t) & 0xfu;
+            bad[i][1] = who >> (8 * t + 4) & 0xfu;
+          }
+          top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+          const int ke = half_exponent(top);
+          const float kf = pow2(15 - ke);
+          float z[MT][2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) z[mt][i][0] = z[mt][i][1] = z[mt][i][2] = z[mt][i][3] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t* ww = reinterpret_cast<const uint32_t*>(&kr[i][k >> 1]);
+              const uint32_t w0 = ww[(k & 1) * 2], w1 = ww[(k & 1) * 2 + 1];
+              const uint32_t b0 = pack_half2(lo_f(w0) * kf, hi_f(w0) * kf), b1 = pack_half2(lo_f(w1) * kf, hi_f(w1) * kf);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mma_f16(z[mt][i], query(mt, k), b0, b1);
+            }
+          }
+          // values: four tokens' 16 dimensions
+          uint4 vr[4][2];
+          top = 0;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int row = (x >> 1) * 8 + ((x & 1) ? (2 * t) ^ 5 : 2 * t);
+            uint32_t wrong = 0;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (row < have) w = lds128(vals + row * kD * 2 + (2 * g + y) * 16);
+              uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t inf_lo = (ww[c] & 0x7f80u) == 0x7f80u, inf_hi = (ww[c] & 0x7f800000u) == 0x7f800000u;
+                wrong |= inf_lo | inf_hi;
+                if (inf_lo) ww[c] &= 0xffff0000u;
+                if (inf_hi) ww[c] &= 0x0000ffffu;
+                top = __vmaxu2(top, ww[c] & 0x7fff7fffu);
+              }
+              vr[x][y] = w;
+            }
+            const uint32_t who = __ballot_sync(0xffffffffu, wrong != 0);
+            bad[x >> 1][x & 1] |= who & (0x11111111u << t);
+          }
+          top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+          const int ve = half_exponent(top);
+          const float vf = pow2(15 - ve);
+          finish_scores<MT>(z, qs, me.kfac * pow2(ke - 15), (float)(ve - 15), true, me.pos0 + quarter * 16, see, lane);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (bad[i][e & 1] && z[mt][i][e] != -INFINITY) z[mt][i][e] = __uint_as_float(0x7fc00000u);
+          uint4 p[MT];
+          softmax_step<MT>(st, z, vf, p);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {  // words of two dimensions
+            const uint32_t w0 = reinterpret_cast<const uint32_t*>(&vr[0][y >> 2])[y & 3];
+            const uint32_t w1 = reinterpret_cast<const uint32_t*>(&vr[1][y >> 2])[y & 3];
+            const uint32_t w2 = reinterpret_cast<const uint32_t*>(&vr[2][y >> 2])[y & 3];
+            const uint32_t w3 = reinterpret_cast<const uint32_t*>(&vr[3][y >> 2])[y & 3];
+            const uint32_t b0 = pack_half2(lo_f(w0) * vf, lo_f(w1) * vf), b1 = pack_half2(lo_f(w2) * vf, lo_f(w3) * vf);
+            const uint32_t d0 = pack_half2(hi_f(w0) * vf, hi_f(w1) * vf), d1 = pack_half2(hi_f(w2) * vf, hi_f(w3) * vf);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma_f16(st.o[mt][2 * y], p[mt], b0, b1);
+              mma_f16(st.o[mt][2 * y + 1], p[mt], d0, d1);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sm.empty[slot]));
+          mbar_arrive(smem_u32(&sm.empty[s1]));
+        }
+      }
+      slot = s1;
+      round = r1;
+      if (++slot == kSlots) slot = 0, ++round;
+    }
+
+    // ---- the unit's part of this CTA is done: join the warps' states, 16 rows at a time ----
+    const bool whole = from == 0 && to == u.items;
+    const int pslot = 2 * ((int)blockIdx.y * ctas + cta) + (from == 0 ? 1 : 0);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      if (mt * 16 >= rows) break;
+      consumers_sync();  // the join area is free again
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float l = st.l[mt][r];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        const int row = r * 8 + g;
+        if (t == 0) {
+          sm.m[warp][row] = st.m[mt][r];
+          sm.l[warp][row] = l;
+        }
+        float* dst = join + (warp * 16 + row) * kAccPad + t * 36;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int j = 0; j < 16; j += 4)
+            *reinterpret_cast<float4*>(dst + 16 * e + j) =
+                make_float4(st.o[mt][j][2 * r + e], st.o[mt][j + 1][2 * r + e], st.o[mt][j + 2][2 * r + e], st.o[mt][j + 3][2 * r + e]);
+      }
+      consumers_sync();
+      const int row = tid >> 4, d0 = (tid & 15) * 8;
+      if (mt * 16 + row < rows) {
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kConsWarps; ++w) M = fmaxf(M, sm.m[w][row]);
+        const float base = M == -INFINITY ? 0.f : M;
+        float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kConsWarps; ++w) {
+          const float f = ex2(sm.m[w][row] - base);
+          L += sm.l[w][row] * f;
+          const float* src = join + (w * 16 + row) * kAccPad + (d0 >> 5) * 36 + (d0 & 31);
+          const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
+          o[0] += x.x * f, o[1] += x.y * f, o[2] += x.z * f, o[3] += x.w * f;
+          o[4] += y.x * f, o[5] += y.y * f, o[6] += y.z * f, o[7] += y.w * f;
+        }
+        if (whole) {
+          const int i = (first_row + mt * 16 + row) / a.G, head = h * a.G + (first_row + mt * 16 + row) - i * a.G;
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          uint4 y;
+          uint32_t* yy = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * x] * inv, o[2 * x + 1] * inv);
+            yy[x] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          *reinterpret_cast<uint4*>(out.p + (int64_t)(u.row0 + i) * out.ts + (int64_t)head * out.hs + d0) = y;
+        } else {
+          float* dst = partials + ((int64_t)pslot * kMaxTileRows + mt * 16 + row) * kPartialStride;
+          if (d0 == 0) *reinterpret_cast<float2*>(dst) = make_float2(M, L);
+          *reinterpret_cast<float4*>(dst + 4 + d0) = make_float4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<float4*>(dst + 8 + d0) = make_float4(o[4], o[5], o[6], o[7]);
+        }
+      }
     }
   }
+}
+
+// Joins the parts of the units that several CTAs shared. CTA (c, row) looks after the unit that
+// begins in share c and goes on in the next, if there is one; parts are added in their order.
+constexpr int kJoinThreads = 128;
+
+__global__ void __launch_bounds__(kJoinThreads)
+kv8_join_kernel(const Kv8Args a, const Rows out, int tile_rows, int topk, int ctas, const float* __restrict__ partials) {
+  __shared__ int64_t scratch[36];
+  __shared__ float s_m[kJoinThreads / 32], s_l[kJoinThreads / 32], s_o[kJoinThreads / 32][kD];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c = blockIdx.x, tile = (int)blockIdx.y / tile_rows, row = (int)blockIdx.y % tile_rows;
+  const int first_row = tile * tile_rows;
+  const Place pl = locate(a, first_row, tile_rows, topk, false, scratch,
+                          [&](int64_t total) { return share_start(total, c + 1, ctas) - 1; });
+  const int64_t start = share_start(pl.total, c, ctas), stop = share_start(pl.total, c + 1, ctas);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this launch must not end before the first
+  if (start >= stop || pl.b >= a.B) return;
+  const Unit u = unit_of(a, pl.b, first_row, tile_rows, topk, false);
+  const int h = (int)((stop - 1 - pl.before) / u.items);
+  const int64_t begin = pl.before + (int64_t)h * u.items, end = begin + u.items;
+  if (begin < start || end <= stop || row >= u.n_new * a.G - first_row) return;
+  const int last = share_of(pl.total, end - 1, ctas);
+
+  const float* mine = partials + (int64_t)row * kPartialStride;
+  constexpr int64_t kSlotFloats = (int64_t)kMaxTileRows * kPartialStride;
+  float M = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int x = c + warp; x <= last; x += kJoinThreads / 32) {
+    if (share_start(pl.total, x, ctas) >= share_start(pl.total, x + 1, ctas)) continue;  // fewer items than CTAs
+    const float* p = mine + (int64_t)(2 * (tile * ctas + x) + (x == c ? 1 : 0)) * kSlotFloats;
+    const float m = p[0], l = p[1];
+    const float4 y = *reinterpret_cast<const float4*>(p + 4 + 4 * lane);
+    const float m2 = fmaxf(M, m), base = m2 == -INFINITY ? 0.f : m2;
+    const float f = ex2(M - base), k = ex2(m - base);
+    M = m2;
+    L = L * f + l * k;
+    o = make_float4(o.x * f + y.x * k, o.y * f + y.y * k, o.z * f + y.z * k, o.w * f + y.w * k);
+  }
+  if (lane == 0) {
+    s_m[warp] = M;
+    s_l[warp] = L;
+  }
+  *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = o;
   __syncthreads();
-  for (int i = tid; i < a.G * kD; i += kWarps * 32) {
-    const int g = i / kD, d = i % kD;
-    float top = -INFINITY;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][g]);
-    const float base = top == -INFINITY ? 0.f : top;
-    float L = 0.f, o = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = expf(s_m[w][g] - base);
-      L += s_l[w][g] * f;
-      o += s_acc[w][g][d] * f;
-    }
-    const __nv_bfloat16 y = __float2bfloat16_rn(L == 0.f ? 0.f : o / L);
-    out.p[(int64_t)t * out.ts + (int64_t)(h * a.G + g) * out.hs + d] = *reinterpret_cast<const uint16_t*>(&y);
+  float top = -INFINITY;
+  for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, s_m[w]);
+  const float base = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, x = 0.f;
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    const float f = ex2(s_m[w] - base);
+    sum += s_l[w] * f;
+    x += s_o[w][tid] * f;
   }
+  const int i = (first_row + row) / a.G, head = h * a.G + (first_row + row) - i * a.G;
+  const __nv_bfloat16 y = __float2bfloat16_rn(sum == 0.f ? 0.f : x / sum);
+  out.p[(int64_t)(u.row0 + i) * out.ts + (int64_t)head * out.hs + tid] = *reinterpret_cast<const uint16_t*>(&y);
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+// The pool as [n_pages][128 rows][128 bytes], a box of one page.
+cudaError_t page_map(const Kv8Args& a, CUtensorMap* m) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return cudaErrorSymbolNotFound;
+  const cuuint64_t dims[3] = {kD, 2 * kPart, (cuuint64_t)a.n_pages};
+  const cuuint64_t strides[2] = {kD, kKv8PageBytes};
+  const cuuint32_t box[3] = {kD, 2 * kPart, 1}, step[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.pages, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <int MT>
+cudaError_t launch_decode(const Kv8Args& a, const CUtensorMap& map, const Rows& q, const Rows& out, float scale,
+                          const int32_t* sel, int topk, float* partials, int sm_count, cudaStream_t st) {
+  const int rows = 16 * MT;
+  const int64_t tiles = ((int64_t)a.max_new * a.G + rows - 1) / rows;
+  if (tiles > 65535 / rows) return cudaErrorInvalidConfiguration;
+  const int sms = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+  const int ctas = tiles >= sms ? 1 : (int)(sms / tiles);  // a tile; ctas > 1 only if all of them fit the workspace
+  cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dec_smem_bytes<MT>());
+  if (e != cudaSuccess) return e;
+  kv8_decode_kernel<MT><<<dim3((unsigned)ctas, (unsigned)tiles), kDecThreads, dec_smem_bytes<MT>(), st>>>(
+      a, map, q, out, scale, sel, topk, partials);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || ctas == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(tiles * rows));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its look at the lengths overlaps the first launch
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv8_join_kernel, a, out, rows, topk, ctas, (const float*)partials);
 }
 
 }  // namespace
 
-int64_t kv8_attend_workspace(const Kv8Args&) { return 16; }
+int64_t kv8_attend_workspace(const Kv8Args&) { return (int64_t)2 * kMaxCtas * kMaxTileRows * kPartialStride * 4; }
 
 cudaError_t launch_kv8_attend(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const int32_t* sel,
-                              int topk, void*, int, cudaStream_t st) {
-  kv8_attend_simple_kernel<<<dim3((unsigned)a.total_new, (unsigned)a.Hkv), kWarps * 32, 0, st>>>(a, q, out, scale, sel, topk);
-  return cudaGetLastError();
+                              int topk, void* workspace, int sm_count, cudaStream_t st) {
+  CUtensorMap map;
+  const cudaError_t e = page_map(a, &map);
+  if (e != cudaSuccess) return e;
+  float* partials = static_cast<float*>(workspace);
+  if ((int64_t)a.max_new * a.G <= 16) return launch_decode<1>(a, map, q, out, scale, sel, topk, partials, sm_count, st);
+  return launch_decode<2>(a, map, q, out, scale, sel, topk, partials, sm_count, st);
 }
 
 }  // namespace spin

@@ -1,0 +1,210 @@
+// Device code shared by the attention kernels of the 8-bit paged cache: barriers and copies,
+// conversions, and the split of a call's work over its CTAs.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "kv8.cuh"
+
+namespace spin {
+namespace kv8 {
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t tx) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(tx) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+// Waits until the phase with this parity has completed. Bounded: after kWaitNs, or once another
+// wait of the CTA has run out, it returns false with *abort (shared memory) set.
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+  const unsigned long long t0 = now_ns();
+  for (uint32_t it = 0; it < (1u << 30); ++it) {
+    if (mbar_try(bar, parity)) return true;
+    if (*abort) return false;
+    if ((it & 63u) == 63u && now_ns() - t0 > kWaitNs) break;
+  }
+  *abort = 1;
+  atomicOr(err, (uint32_t)kErrTimeout);
+  return false;
+}
+
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+  if (mbar_try(bar, parity)) return true;
+  return mbar_wait_slow(bar, parity, abort, err);
+}
+
+// A whole page [2][64] rows of 128 bytes, 16-byte chunk c of row r at chunk c ^ (r & 7).
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(0), "r"(page), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+// Two e4m3 codes to two halves, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t w, bool high) {
+  uint32_t r;
+  const uint16_t c = (uint16_t)(high ? w >> 16 : w);
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// 2^n for a whole n in the normal range.
+__device__ __forceinline__ float pow2(int n) { return __uint_as_float((uint32_t)(n + 127) << 23); }
+
+// The exponent e, clamped to [-60, 128], that puts bf16 values of up to `amax` (its bits, finite) below 2^e:
+// times 2^(15 - e) they use fp16's whole range, so that every bf16 down to 2^-29 of the largest is exact.
+__device__ __forceinline__ int half_exponent(uint32_t amax) { return max((int)(amax >> 7) - 126, -60); }
+
+// log2 of a page's scale: exact for powers of two.
+__device__ __forceinline__ float scale_log2(float s) {
+  const uint32_t u = __float_as_uint(s);
+  if (s != s) return s;
+  return (float)((int)(u >> 23 & 255u) - 127) + __log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u));
+}
+
+// ---------------------------------------------------------------------------
+// The split of a call's work. A unit is one (request, KV head); a tile is a block of its rows (row r:
+// token r / G, head r % G). Per tile, a unit's items are the pages that the tile's last token may see
+// (or its list of pages), then the tail; the items of all units lie in one row, and CTA c of P takes
+// those from c W / P on.
+// ---------------------------------------------------------------------------
+struct Unit {  // of one request: the same for all of its heads
+  int row0, n_new, past;
+  int full;     // complete pages
+  int tail;     // tokens of the tail
+  int pages;    // entries of the page list
+  int items;    // pages, and one for the tail if the tile sees it
+};
+
+__device__ __forceinline__ Unit unit_of(const Kv8Args& a, int b, int first_row, int rows, int topk, bool report) {
+  Unit u;
+  const bool ok = kv8_request(a, b, report, u.row0, u.n_new, u.past);
+  const int len = u.past + u.n_new;
+  u.full = ok ? len >> 6 : 0;
+  u.tail = ok ? len & (kPart - 1) : 0;
+  u.pages = u.items = 0;
+  if (!ok || (int64_t)u.n_new * a.G <= first_row) return u;  // the tile has no row of this request
+  const int last = min(u.n_new, (first_row + rows - 1) / a.G + 1);  // tokens up to the tile's last row
+  const int seen = u.past + last;
+  u.pages = topk ? topk : min(u.full, (seen + kPart - 1) >> 6);
+  u.items = u.pages + (u.tail && seen > u.full * kPart ? 1 : 0);
+  return u;
+}
+
+struct Place {
+  int64_t total;   // items of all units
+  int b;           // request of the item looked for
+  int64_t before;  // items of the requests before it
+};
+
+// The request of item `at(total)` for every thread of the CTA (n threads, scratch of 32 + 4 words
+// each of 8 bytes). Each thread adds up a run of requests; the one whose run holds the item walks it.
+template <typename At>
+__device__ __forceinline__ Place locate(const Kv8Args& a, int first_row, int rows, int topk, bool report, int64_t* scratch, At at) {
+  const int tid = threadIdx.x, n = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = n >> 5;
+  const int run = (a.B + n - 1) / n, b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += unit_of(a, b, first_row, rows, topk, report).items;
+  mine *= a.Hkv;
+  int64_t sum = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += x;
+  }
+  if (lane == 31) scratch[warp] = sum;
+  __syncthreads();
+  int64_t base = 0, total = 0;
+  for (int w = 0; w < warps; ++w) {
+    const int64_t x = scratch[w];
+    if (w < warp) base += x;
+    total += x;
+  }
+  const int64_t lo = base + sum - mine, want = at(total);
+  if (tid == 0) {
+    scratch[32] = a.B;
+    scratch[33] = total;
+  }
+  __syncthreads();
+  if (want >= lo && want < lo + mine) {
+    int64_t before = lo;
+    for (int b = b0; b < b1; ++b) {
+      const int64_t m = (int64_t)unit_of(a, b, first_row, rows, topk, false).items * a.Hkv;
+      if (want < before + m) {
+        scratch[32] = b;
+        scratch[33] = before;
+        break;
+      }
+      before += m;
+    }
+  }
+  __syncthreads();
+  return Place{total, (int)scratch[32], scratch[33]};
+}
+
+}  // namespace kv8
+}  // namespace spin
