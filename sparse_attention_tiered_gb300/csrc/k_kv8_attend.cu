@@ -30,12 +30,11 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kConsWarps = 8;                           // two groups of four, a page each
-constexpr int kDecThreads = (kConsWarps + 4) * 32;      // and the producer's warpgroup, one warp of which works
-constexpr int kSlots = 8;                               // 16 KB each
+constexpr int kSlots = 10;          // of the ring, 16 KB each
 constexpr int kMaxCtas = 160;
-constexpr int kAccPad = 144;                            // floats of a row in the join: 4 x (32 + 4)
+constexpr int kAccPad = 144;        // floats of a row in the join: 4 x (32 + 4)
 constexpr int kMaxTileRows = 32;
+constexpr int kMaxConsWarps = 12;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kShift = 14.f;                          // weights reach 2^14
 
@@ -46,27 +45,44 @@ struct SlotMeta {
   int pos0;    // position of its first token; -1: nothing to do
 };
 
+// The kernel's forms: MT tiles of 16 rows, of which the last has its upper half in use (R = 2) or
+// not (R = 1: at most 8 rows, the usual group). Consumer warps come in groups of four; registers
+// allow three groups with one tile's output and two with two tiles'. The fourth warpgroup (or third)
+// is the producer's, of which one warp works. Registers: 512 threads x 128 at launch = 128 x 56 +
+// 384 x 152, or 384 x 168 = 128 x 56 + 256 x 224.
+template <int MT>
+struct Dec {
+  static constexpr int kGroups = MT == 1 ? 3 : 2;
+  static constexpr int kWarps = 4 * kGroups;
+  static constexpr int kThreads = (kWarps + 4) * 32;
+  static constexpr size_t kJoinBytes = (size_t)kWarps * 8 * kAccPad * 4;
+  static constexpr size_t kQBytes = (size_t)8 * MT * 512;
+};
+
 struct DecSmem {
   uint64_t full[kSlots], empty[kSlots];
   SlotMeta meta[kSlots];
   int64_t scratch[36];
-  float m[kConsWarps][16], l[kConsWarps][16];
+  float m[kMaxConsWarps][8], l[kMaxConsWarps][8];
   int abort;
 };
 
 constexpr size_t kRingBytes = (size_t)kSlots * kKv8PageBytes;
-constexpr size_t kJoinBytes = (size_t)kConsWarps * 16 * kAccPad * 4;
 
 template <int MT>
 constexpr size_t dec_smem_bytes() {
-  return 1024 + kRingBytes + kJoinBytes + (MT > 1 ? 8 * MT * 512 : 0) + sizeof(DecSmem);
+  return 1024 + kRingBytes + Dec<MT>::kJoinBytes + Dec<MT>::kQBytes + sizeof(DecSmem);
 }
+static_assert(dec_smem_bytes<1>() <= 232448 && dec_smem_bytes<2>() <= 232448, "shared memory of a CTA");
 
 // First item of CTA c of n, and the CTA that has item x.
 __device__ __forceinline__ int64_t share_start(int64_t total, int c, int n) { return total * c / n; }
 __device__ __forceinline__ int share_of(int64_t total, int64_t x, int n) { return (int)(((x + 1) * n - 1) / total); }
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"r"(kConsWarps * 32) : "memory"); }
+template <int MT>
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(Dec<MT>::kWarps * 32) : "memory");
+}
 
 // A warp's softmax state of MT x 16 rows: lane (g, t) has rows g and g + 8 of each, and of them
 // dimensions 32 t .. 32 t + 31 of the output: element e of o[j] is row g + 8 (e / 2), dimension
@@ -77,15 +93,15 @@ struct State {
   float m[MT][2], l[MT][2];
 };
 
-// Scores z of one row half (four tokens' worth in a lane) go in, fp16 weights come out.
-template <int MT>
+// Takes the lane's scores z (four tokens of each of its rows) into the state; fp16 weights come out.
+template <int MT, int R>
 __device__ __forceinline__ void softmax_step(State<MT>& st, float (&z)[MT][2][4], float vinv, uint4 (&p)[MT]) {
-  float top[MT][2];
+  float top[MT][R];
   bool grew = false;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < R; ++r) {
       float x = fmaxf(fmaxf(z[mt][0][2 * r], z[mt][0][2 * r + 1]), fmaxf(z[mt][1][2 * r], z[mt][1][2 * r + 1]));
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -96,7 +112,7 @@ __device__ __forceinline__ void softmax_step(State<MT>& st, float (&z)[MT][2][4]
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < R; ++r) {
         const float f = top[mt][r] == -INFINITY ? 1.f : ex2(st.m[mt][r] - top[mt][r]);
         st.m[mt][r] = top[mt][r];
         st.l[mt][r] *= f;
@@ -108,60 +124,53 @@ __device__ __forceinline__ void softmax_step(State<MT>& st, float (&z)[MT][2][4]
       }
   }
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int mt = 0; mt < MT; ++mt) {
+    uint32_t w[2][2] = {};  // [row half][token tile]
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float base = (st.m[mt][r] == -INFINITY ? 0.f : st.m[mt][r]) - kShift;
-      float s = 0.f;
+    for (int r = 0; r < R; ++r) {
+      const float base = st.m[mt][r] == -INFINITY ? -kShift : st.m[mt][r] - kShift;
+      float y[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& x = z[mt][i][2 * r + e];
-          x = x == -INFINITY ? 0.f : ex2(x - base);
-          s += x;
-        }
+      for (int e = 0; e < 4; ++e) y[e] = ex2(z[mt][e >> 1][2 * r + (e & 1)] - base);  // a hidden token's z is -inf
+      const float s = (y[0] + y[1]) + (y[2] + y[3]);
       st.l[mt][r] += s == 0.f ? 0.f : s * vinv;  // a row that sees nothing here takes nothing of a NaN page
+      w[r][0] = pack_half2(y[0], y[1]);
+      w[r][1] = pack_half2(y[2], y[3]);
     }
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-    p[mt] = make_uint4(pack_half2(z[mt][0][0], z[mt][0][1]), pack_half2(z[mt][0][2], z[mt][0][3]),
-                       pack_half2(z[mt][1][0], z[mt][1][1]), pack_half2(z[mt][1][2], z[mt][1][3]));
+    p[mt] = make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]);
+  }
 }
 
-// z = score * factor + vlog for the tokens a row may see, else -inf. pos[i][e]: position of the
-// lane's token of column e in token tile i.
-template <int MT>
+// z = score * factor + vlog for the tokens a row may see, else -inf. `tok`: position of the warp's first token.
+template <int MT, int R>
 __device__ __forceinline__ void finish_scores(float (&z)[MT][2][4], const float (&qs)[MT][2], float kfac, float vlog,
-                                              bool masked, int pos0, const int (&see)[MT][2], int lane) {
-  const int t = lane & 3;
+                                              bool masked, int tok, const int (&see)[MT][2], int t) {
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int r = 0; r < R; ++r) {
+      const float f = kfac * qs[mt][r];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int r = e >> 1;
-        float x = fmaf(z[mt][i][e], kfac * qs[mt][r], vlog);
-        if (masked) {
-          const int tok = pos0 + i * 8 + ((e & 1) ? (2 * t) ^ 5 : 2 * t);
-          if (tok >= see[mt][r]) x = -INFINITY;
-        }
-        z[mt][i][e] = x;
+        float& x = z[mt][e >> 1][2 * r + (e & 1)];
+        x = fmaf(x, f, vlog);
+        if (masked && tok + (e >> 1) * 8 + ((e & 1) ? (2 * t) ^ 5 : 2 * t) >= see[mt][r]) x = -INFINITY;
       }
+    }
 }
 
-template <int MT>
-__global__ void __launch_bounds__(kDecThreads, 1)
+template <int MT, int R>
+__global__ void __launch_bounds__(Dec<MT>::kThreads, 1)
 kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, const Rows q, const Rows out, float scale,
                   const int32_t* __restrict__ sel, int topk, float* __restrict__ partials) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  float* join = reinterpret_cast<float*>(ring + kRingBytes);
-  uint4* qfrag = reinterpret_cast<uint4*>(ring + kRingBytes + kJoinBytes);  // [8][MT][32], MT > 1 only
-  DecSmem& sm = *reinterpret_cast<DecSmem*>(ring + kRingBytes + kJoinBytes + (MT > 1 ? 8 * MT * 512 : 0));
+  float* join = reinterpret_cast<float*>(ring + kRingBytes);  // [warps][8 rows][kAccPad]
+  uint4* qfrag = reinterpret_cast<uint4*>(ring + kRingBytes + Dec<MT>::kJoinBytes);  // [8][MT][32]
+  DecSmem& sm = *reinterpret_cast<DecSmem*>(ring + kRingBytes + Dec<MT>::kJoinBytes + Dec<MT>::kQBytes);
+  constexpr int kConsWarps = Dec<MT>::kWarps;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kRows = 16 * MT;
+  constexpr int kRows = R == 1 ? 8 : 16 * MT;
   const int first_row = (int)blockIdx.y * kRows;
   volatile int* abort = &sm.abort;
 
@@ -181,7 +190,6 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
   const int64_t start = share_start(pl.total, cta, ctas), stop = share_start(pl.total, cta + 1, ctas);
   if (start >= stop) return;
 
-  // 384 threads x 168 registers at launch: 128 x 56 + 256 x 224.
   if (warp >= kConsWarps) {
     // ------------------------------ producer ------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -274,7 +282,8 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
   }
 
   // ------------------------------ consumers ------------------------------
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+  if (MT == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+  else asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
   const int g = lane >> 2, t = lane & 3;
   const int group = warp >> 2, quarter = warp & 3;
   const int pg = (g & 1) ? g ^ 4 : g;                // token order 0 5 2 7 4 1 6 3
@@ -296,20 +305,22 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
     item += to - from;
     const int rows = min(kRows, u.n_new * a.G - first_row);
 
-    // Queries: lane (g, t) holds dimensions 16 t .. and 64 + 16 t .. of its rows, four to a product.
-    uint4 qa[MT][8];
+    // Queries, as the products want them: lane (g, t) holds dimensions 16 t .. and 64 + 16 t .. of its
+    // rows, four to a product. Every warp works out the rows' factors, warp 0 leaves the operands in
+    // shared memory. (All warps are past the last unit's products: they have joined its state.)
     float qs[MT][2];
     int see[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
+        qs[mt][r] = 1.f;
+        see[mt][r] = 0;
         const int row = mt * 16 + r * 8 + g;
         const int i = (first_row + row) / a.G, head = h * a.G + (first_row + row) - i * a.G;
         uint32_t w[16];
 #pragma unroll
         for (int x = 0; x < 16; ++x) w[x] = 0;
-        see[mt][r] = 0;
         if (row < rows) {
           see[mt][r] = u.past + i + 1;
           const uint4* src = reinterpret_cast<const uint4*>(q.p + (int64_t)(u.row0 + i) * q.ts + (int64_t)head * q.hs);
@@ -326,23 +337,14 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
         const int e = half_exponent(top);
         const float f = pow2(15 - e);
         qs[mt][r] = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e - 15);
+        if (warp == 0)
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const uint32_t v = pack_half2(lo_f(w[x]) * f, hi_f(w[x]) * f);
-          uint32_t* dst = reinterpret_cast<uint32_t*>(&qa[mt][x >> 1]);
-          dst[(x & 1) * 2 + r] = v;
-        }
+          for (int x = 0; x < 16; ++x)
+            reinterpret_cast<uint32_t*>(&qfrag[((x >> 1) * MT + mt) * 32 + lane])[(x & 1) * 2 + r] =
+                pack_half2(lo_f(w[x]) * f, hi_f(w[x]) * f);
       }
-    if (MT > 1) {  // too many for registers: the same for all warps, in shared memory
-      consumers_sync();
-      if (warp == 0)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) qfrag[(k * MT + mt) * 32 + lane] = qa[mt][k];
-      consumers_sync();
-    }
-    auto query = [&](int mt, int k) -> uint4 { return MT > 1 ? qfrag[(k * MT + mt) * 32 + lane] : qa[mt][k]; };
+    consumers_sync<MT>();
+    auto query = [&](int mt, int k) -> uint4 { return qfrag[(k * MT + mt) * 32 + lane]; };
 
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -354,7 +356,7 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
         for (int j = 0; j < 16; ++j) st.o[mt][j][2 * r] = st.o[mt][j][2 * r + 1] = 0.f;
       }
 
-    for (int it = from; it < to; ++it, turn ^= 1) {
+    for (int it = from; it < to; ++it, turn = turn + 1 == Dec<MT>::kGroups ? 0 : turn + 1) {
       if (it < u.pages) {
         if (turn == group) {
           ok = mbar_wait(smem_u32(&sm.full[slot]), round & 1, abort, a.err) && ok;
@@ -363,21 +365,37 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
           if (ok && me.pos0 >= 0) {
             const uint32_t keys = smem_u32(ring) + slot * kKv8PageBytes + quarter * 16 * kD;
             const uint32_t vals = keys + kKv8HalfBytes;
-            float z[MT][2][4];
+            uint4 kr[2][2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint32_t at = keys + (i * 8 + pg) * kD;
-              const uint4 c0 = lds128(at + ((t ^ pg) << 4)), c1 = lds128(at + (((t + 4) ^ pg) << 4));
-              const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) z[mt][i][0] = z[mt][i][1] = z[mt][i][2] = z[mt][i][3] = 0.f;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const uint32_t b0 = e4m3x2_half2(w[k], false), b1 = e4m3x2_half2(w[k], true);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) mma_f16(z[mt][i], query(mt, k), b0, b1);
-              }
+              kr[i][0] = lds128(at + ((t ^ pg) << 4));
+              kr[i][1] = lds128(at + (((t + 4) ^ pg) << 4));
             }
+            float z[MT][2][4], z1[MT][2][4];  // even and odd products apart: shorter chains
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[mt][i][e] = z1[mt][i][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                const uint4 qk = query(mt, k);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint32_t w = reinterpret_cast<const uint32_t*>(&kr[i][k >> 2])[k & 3];
+                  mma_f16(k & 1 ? z1[mt][i] : z[mt][i], qk, e4m3x2_half2(w, false), e4m3x2_half2(w, true));
+                }
+              }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 2 * R; ++e) z[mt][i][e] += z1[mt][i][e];
             uint4 vr[4];  // value rows 2 t, (2 t) ^ 5, and those 8 further
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -385,9 +403,9 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
               vr[x] = lds128(vals + ((x >> 1) * 8 + row) * kD + ((g ^ row) << 4));
             }
             const int pos = me.pos0 + quarter * 16;
-            finish_scores<MT>(z, qs, me.kfac, me.vlog, me.pos0 + kPart > u.past + 1, pos, see, lane);
+            finish_scores<MT, R>(z, qs, me.kfac, me.vlog, me.pos0 + kPart > u.past + 1, pos, see, t);
             uint4 p[MT];
-            softmax_step<MT>(st, z, me.vinv, p);
+            softmax_step<MT, R>(st, z, me.vinv, p);
             const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vr[0]);
             const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vr[1]);
             const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vr[2]);
@@ -494,7 +512,7 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
           top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
           const int ve = half_exponent(top);
           const float vf = pow2(15 - ve);
-          finish_scores<MT>(z, qs, me.kfac * pow2(ke - 15), (float)(ve - 15), true, me.pos0 + quarter * 16, see, lane);
+          finish_scores<MT, R>(z, qs, me.kfac * pow2(ke - 15), (float)(ve - 15), true, me.pos0 + quarter * 16, see, t);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -503,7 +521,7 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
               for (int e = 0; e < 4; ++e)
                 if (bad[i][e & 1] && z[mt][i][e] != -INFINITY) z[mt][i][e] = __uint_as_float(0x7fc00000u);
           uint4 p[MT];
-          softmax_step<MT>(st, z, vf, p);
+          softmax_step<MT, R>(st, z, vf, p);
 #pragma unroll
           for (int y = 0; y < 8; ++y) {  // words of two dimensions
             const uint32_t w0 = reinterpret_cast<const uint32_t*>(&vr[0][y >> 2])[y & 3];
@@ -530,64 +548,54 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
       if (++slot == kSlots) slot = 0, ++round;
     }
 
-    // ---- the unit's part of this CTA is done: join the warps' states, 16 rows at a time ----
+    // ---- the unit's part of this CTA is done: join the warps' states, 8 rows at a time ----
     const bool whole = from == 0 && to == u.items;
     const int pslot = 2 * ((int)blockIdx.y * ctas + cta) + (from == 0 ? 1 : 0);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (mt * 16 >= rows) break;
-      consumers_sync();  // the join area is free again
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float l = st.l[mt][r];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        const int row = r * 8 + g;
-        if (t == 0) {
-          sm.m[warp][row] = st.m[mt][r];
-          sm.l[warp][row] = l;
-        }
-        float* dst = join + (warp * 16 + row) * kAccPad + t * 36;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int j = 0; j < 16; j += 4)
-            *reinterpret_cast<float4*>(dst + 16 * e + j) =
-                make_float4(st.o[mt][j][2 * r + e], st.o[mt][j + 1][2 * r + e], st.o[mt][j + 2][2 * r + e], st.o[mt][j + 3][2 * r + e]);
+    for (int part = 0; part < 2 * MT; ++part) {
+      const int mt = part >> 1, r = part & 1;
+      if (part * 8 >= rows) break;
+      consumers_sync<MT>();  // the join area is free again
+      float l = st.l[mt][r];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (t == 0) {
+        sm.m[warp][g] = st.m[mt][r];
+        sm.l[warp][g] = l;
       }
-      consumers_sync();
-      const int row = tid >> 4, d0 = (tid & 15) * 8;
-      if (mt * 16 + row < rows) {
+      float* dst = join + (warp * 8 + g) * kAccPad + t * 36;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+          *reinterpret_cast<float4*>(dst + 16 * e + j) =
+              make_float4(st.o[mt][j][2 * r + e], st.o[mt][j + 1][2 * r + e], st.o[mt][j + 2][2 * r + e], st.o[mt][j + 3][2 * r + e]);
+      consumers_sync<MT>();
+      const int at = tid >> 5, d0 = lane * 4, row = part * 8 + at;  // a warp a row, four dimensions a lane
+      if (at < 8 && row < rows) {
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kConsWarps; ++w) M = fmaxf(M, sm.m[w][row]);
+        for (int w = 0; w < kConsWarps; ++w) M = fmaxf(M, sm.m[w][at]);
         const float base = M == -INFINITY ? 0.f : M;
-        float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        float L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kConsWarps; ++w) {
-          const float f = ex2(sm.m[w][row] - base);
-          L += sm.l[w][row] * f;
-          const float* src = join + (w * 16 + row) * kAccPad + (d0 >> 5) * 36 + (d0 & 31);
-          const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
-          o[0] += x.x * f, o[1] += x.y * f, o[2] += x.z * f, o[3] += x.w * f;
-          o[4] += y.x * f, o[5] += y.y * f, o[6] += y.z * f, o[7] += y.w * f;
+          const float f = ex2(sm.m[w][at] - base);
+          L += sm.l[w][at] * f;
+          const float4 x = *reinterpret_cast<const float4*>(join + (w * 8 + at) * kAccPad + (d0 >> 5) * 36 + (d0 & 31));
+          o = make_float4(o.x + x.x * f, o.y + x.y * f, o.z + x.z * f, o.w + x.w * f);
         }
         if (whole) {
-          const int i = (first_row + mt * 16 + row) / a.G, head = h * a.G + (first_row + mt * 16 + row) - i * a.G;
+          const int i = (first_row + row) / a.G, head = h * a.G + (first_row + row) - i * a.G;
           const float inv = L == 0.f ? 0.f : 1.f / L;
-          uint4 y;
-          uint32_t* yy = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * x] * inv, o[2 * x + 1] * inv);
-            yy[x] = *reinterpret_cast<const uint32_t*>(&v);
-          }
-          *reinterpret_cast<uint4*>(out.p + (int64_t)(u.row0 + i) * out.ts + (int64_t)head * out.hs + d0) = y;
+          const __nv_bfloat162 v0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), v1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+          *reinterpret_cast<uint2*>(out.p + (int64_t)(u.row0 + i) * out.ts + (int64_t)head * out.hs + d0) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
         } else {
-          float* dst = partials + ((int64_t)pslot * kMaxTileRows + mt * 16 + row) * kPartialStride;
-          if (d0 == 0) *reinterpret_cast<float2*>(dst) = make_float2(M, L);
-          *reinterpret_cast<float4*>(dst + 4 + d0) = make_float4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<float4*>(dst + 8 + d0) = make_float4(o[4], o[5], o[6], o[7]);
+          float* to_part = partials + ((int64_t)pslot * kMaxTileRows + row) * kPartialStride;
+          if (lane == 0) *reinterpret_cast<float2*>(to_part) = make_float2(M, L);
+          *reinterpret_cast<float4*>(to_part + 4 + d0) = o;
         }
       }
     }
@@ -680,17 +688,17 @@ cudaError_t page_map(const Kv8Args& a, CUtensorMap* m) {
              : cudaErrorInvalidValue;
 }
 
-template <int MT>
+template <int MT, int R>
 cudaError_t launch_decode(const Kv8Args& a, const CUtensorMap& map, const Rows& q, const Rows& out, float scale,
                           const int32_t* sel, int topk, float* partials, int sm_count, cudaStream_t st) {
-  const int rows = 16 * MT;
+  const int rows = R == 1 ? 8 : 16 * MT;
   const int64_t tiles = ((int64_t)a.max_new * a.G + rows - 1) / rows;
   if (tiles > 65535 / rows) return cudaErrorInvalidConfiguration;
   const int sms = sm_count < kMaxCtas ? sm_count : kMaxCtas;
   const int ctas = tiles >= sms ? 1 : (int)(sms / tiles);  // a tile; ctas > 1 only if all of them fit the workspace
-  cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dec_smem_bytes<MT>());
+  cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<MT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dec_smem_bytes<MT>());
   if (e != cudaSuccess) return e;
-  kv8_decode_kernel<MT><<<dim3((unsigned)ctas, (unsigned)tiles), kDecThreads, dec_smem_bytes<MT>(), st>>>(
+  kv8_decode_kernel<MT, R><<<dim3((unsigned)ctas, (unsigned)tiles), Dec<MT>::kThreads, dec_smem_bytes<MT>(), st>>>(
       a, map, q, out, scale, sel, topk, partials);
   e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
@@ -716,8 +724,9 @@ cudaError_t launch_kv8_attend(const Kv8Args& a, const Rows& q, const Rows& out, 
   const cudaError_t e = page_map(a, &map);
   if (e != cudaSuccess) return e;
   float* partials = static_cast<float*>(workspace);
-  if ((int64_t)a.max_new * a.G <= 16) return launch_decode<1>(a, map, q, out, scale, sel, topk, partials, sm_count, st);
-  return launch_decode<2>(a, map, q, out, scale, sel, topk, partials, sm_count, st);
+  if ((int64_t)a.max_new * a.G <= 8) return launch_decode<1, 1>(a, map, q, out, scale, sel, topk, partials, sm_count, st);
+  if ((int64_t)a.max_new * a.G <= 16) return launch_decode<1, 2>(a, map, q, out, scale, sel, topk, partials, sm_count, st);
+  return launch_decode<2, 2>(a, map, q, out, scale, sel, topk, partials, sm_count, st);
 }
 
 }  // namespace spin
