@@ -30,11 +30,11 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kSlots = 10;          // of the ring, 16 KB each
 constexpr int kMaxCtas = 160;
 constexpr int kAccPad = 144;        // floats of a row in the join: 4 x (32 + 4)
 constexpr int kMaxTileRows = 32;
 constexpr int kMaxConsWarps = 12;
+constexpr int kMaxSlots = 10;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kShift = 14.f;                          // weights reach 2^14
 
@@ -53,29 +53,46 @@ struct SlotMeta {
 template <int MT>
 struct Dec {
   static constexpr int kGroups = MT == 1 ? 3 : 2;
+  static constexpr int kPer = MT == 1 ? 3 : 5;  // slots of a group's ring, 16 KB each
+  static constexpr int kSlots = kGroups * kPer;
   static constexpr int kWarps = 4 * kGroups;
   static constexpr int kThreads = (kWarps + 4) * 32;
+  static constexpr size_t kRingBytes = (size_t)kSlots * kKv8PageBytes;
   static constexpr size_t kJoinBytes = (size_t)kWarps * 8 * kAccPad * 4;
   static constexpr size_t kQBytes = (size_t)8 * MT * 512;
 };
 
 struct DecSmem {
-  uint64_t full[kSlots], empty[kSlots];
-  SlotMeta meta[kSlots];
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  SlotMeta meta[kMaxSlots];
   int64_t scratch[36];
   float m[kMaxConsWarps][8], l[kMaxConsWarps][8];
   int abort;
 };
 
-constexpr size_t kRingBytes = (size_t)kSlots * kKv8PageBytes;
-
 template <int MT>
 constexpr size_t dec_smem_bytes() {
-  return 1024 + kRingBytes + Dec<MT>::kJoinBytes + Dec<MT>::kQBytes + sizeof(DecSmem);
+  return 1024 + Dec<MT>::kRingBytes + Dec<MT>::kJoinBytes + Dec<MT>::kQBytes + sizeof(DecSmem);
 }
 static_assert(dec_smem_bytes<1>() <= 232448 && dec_smem_bytes<2>() <= 232448, "shared memory of a CTA");
 
-// First item of CTA c of n, and the CTA that has item x.
+// What a CTA does of the unit that holds the place `at` of its request, with `left` of its share to go.
+struct Part {
+  int h, from, to;  // items [from, to) of head h; none where from >= to
+  int64_t took;
+};
+
+__device__ __forceinline__ Part part_of(const Unit& u, int64_t at, int64_t left) {
+  Part x;
+  x.h = (int)(at / u.weight);
+  const int f = (int)(at - (int64_t)x.h * u.weight), t = (int)min((int64_t)u.weight, f + left);
+  x.took = t - f;
+  x.from = max(0, f - kUnitCost);
+  x.to = max(0, t - kUnitCost);
+  return x;
+}
+
+// The first place of CTA c's share of n, and the CTA whose share has place x.
 __device__ __forceinline__ int64_t share_start(int64_t total, int c, int n) { return total * c / n; }
 __device__ __forceinline__ int share_of(int64_t total, int64_t x, int n) { return (int)(((x + 1) * n - 1) / total); }
 
@@ -165,9 +182,10 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
                   const int32_t* __restrict__ sel, int topk, float* __restrict__ partials) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  float* join = reinterpret_cast<float*>(ring + kRingBytes);  // [warps][8 rows][kAccPad]
-  uint4* qfrag = reinterpret_cast<uint4*>(ring + kRingBytes + Dec<MT>::kJoinBytes);  // [8][MT][32]
-  DecSmem& sm = *reinterpret_cast<DecSmem*>(ring + kRingBytes + Dec<MT>::kJoinBytes + Dec<MT>::kQBytes);
+  float* join = reinterpret_cast<float*>(ring + Dec<MT>::kRingBytes);  // [warps][8 rows][kAccPad]
+  uint4* qfrag = reinterpret_cast<uint4*>(ring + Dec<MT>::kRingBytes + Dec<MT>::kJoinBytes);  // [8][MT][32]
+  DecSmem& sm = *reinterpret_cast<DecSmem*>(ring + Dec<MT>::kRingBytes + Dec<MT>::kJoinBytes + Dec<MT>::kQBytes);
+  constexpr int kGroups = Dec<MT>::kGroups, kPer = Dec<MT>::kPer;
   constexpr int kConsWarps = Dec<MT>::kWarps;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kRows = R == 1 ? 8 : 16 * MT;
@@ -175,7 +193,7 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
   volatile int* abort = &sm.abort;
 
   if (tid == 0) {
-    for (int s = 0; s < kSlots; ++s) {
+    for (int s = 0; s < Dec<MT>::kSlots; ++s) {
       mbar_init(smem_u32(&sm.full[s]), 1);
       mbar_init(smem_u32(&sm.empty[s]), 4);
     }
@@ -195,22 +213,37 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp != kConsWarps) return;
     if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
-    uint32_t slot = 0, round = 0;  // the next slot, and how often the ring has been filled
+    // Items go to the groups in turn, each with a ring of its own: next[0] is the next slot of the group
+    // whose turn it is, with the ring's parity above bit 8. (In one ring for all, a group could reach a
+    // slot whose last copy, another group's, had not landed yet, and take that phase for its own.)
+    uint32_t next[kGroups];
+#pragma unroll
+    for (int x = 0; x < kGroups; ++x) next[x] = x * kPer;
+    auto step = [&]() {
+      const uint32_t s = next[0] & 255u, p = next[0] >> 8;
+      next[0] = s % kPer == kPer - 1 ? (s - (kPer - 1)) | (p ^ 1) << 8 : s + 1 | p << 8;
+    };
+    auto pass = [&]() {
+      const uint32_t first = next[0];
+#pragma unroll
+      for (int x = 0; x + 1 < kGroups; ++x) next[x] = next[x + 1];
+      next[kGroups - 1] = first;
+    };
     bool ok = true;
     int b = pl.b;
-    int64_t item = start, before = pl.before;
-    while (item < stop) {
+    int64_t at = start, before = pl.before;
+    while (at < stop) {
       const Unit u = unit_of(a, b, first_row, kRows, topk, false);
-      if (u.items == 0 || item >= before + (int64_t)u.items * a.Hkv) {
-        before += (int64_t)u.items * a.Hkv;
+      if (u.weight == 0 || at >= before + (int64_t)u.weight * a.Hkv) {
+        before += (int64_t)u.weight * a.Hkv;
         ++b;
         continue;
       }
-      const int h = (int)((item - before) / u.items);
-      const int64_t unit = (int64_t)b * a.Hkv + h;
-      const int from = (int)(item - before - (int64_t)h * u.items);
-      const int to = (int)min((int64_t)u.items, from + (stop - item));
-      item += to - from;
+      const Part x = part_of(u, at - before, stop - at);
+      at += x.took;
+      const int from = x.from, to = x.to;
+      if (from >= to) continue;
+      const int64_t unit = (int64_t)b * a.Hkv + x.h;
       // 32 page ids and scales at a time, a batch ahead of the copies
       int id = -1, pos = -1;
       float2 sc = make_float2(1.f, 1.f);
@@ -237,9 +270,10 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
         look(base + 32 + lane);
         const int n = min(32, min(to, u.pages) - base);
         for (int i = 0; i < n; ++i) {
+          const uint32_t slot = next[0] & 255u, parity = next[0] >> 8;
           if (lane == i) {
             const uint32_t full = smem_u32(&sm.full[slot]);
-            ok = ok && mbar_wait(smem_u32(&sm.empty[slot]), (round & 1) ^ 1, abort, a.err);
+            ok = ok && mbar_wait(smem_u32(&sm.empty[slot]), parity ^ 1, abort, a.err);
             if (ok) {
               if (my_id >= 0) tma_page(smem_u32(ring) + slot * kKv8PageBytes, &map, my_id, full);
               sm.meta[slot] = SlotMeta{my_sc.x * scale * kLog2e, scale_log2(my_sc.y), 1.f / my_sc.y, my_pos};
@@ -247,16 +281,18 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
             }
           }
           __syncwarp();  // slots are filled in order: a lane that ran ahead would take a phase for a later one
-          if (++slot == kSlots) slot = 0, ++round;
+          step();
+          pass();
         }
         ok = __all_sync(0xffffffffu, ok);
       }
       if (to > u.pages) {  // the tail: keys in one slot, values in the next
         for (int i = 0; i < 2; ++i) {
+          const uint32_t slot = next[0] & 255u, parity = next[0] >> 8;
           if (lane == 0) {
             const uint32_t full = smem_u32(&sm.full[slot]);
             const uint32_t bytes = u.tail * kD * 2;
-            ok = ok && mbar_wait(smem_u32(&sm.empty[slot]), (round & 1) ^ 1, abort, a.err);
+            ok = ok && mbar_wait(smem_u32(&sm.empty[slot]), parity ^ 1, abort, a.err);
             if (ok) {
               bulk_copy(smem_u32(ring) + slot * kKv8PageBytes, a.tails + unit * kPageElems + i * kPart * kD, bytes, full);
               sm.meta[slot] = SlotMeta{scale * kLog2e, 0.f, 1.f, u.full * kPart};
@@ -264,18 +300,20 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
             }
           }
           __syncwarp();
-          if (++slot == kSlots) slot = 0, ++round;
+          step();
         }
+        pass();
         ok = __all_sync(0xffffffffu, ok);
       }
     }
-    // No copy may be in flight when the CTA's shared memory goes: every slot is waited for, whether
-    // or not the consumers got to it. (A slot that was never filled has nothing to wait for.)
+    // No copy may be in flight when the CTA's shared memory goes. The consumers wait for every slot
+    // that was filled, unless a wait ran out: then the phase in flight, if any, is waited for here.
     if (lane == 0 && !ok) {
-      for (uint32_t s = 0; s < kSlots; ++s) {
-        const uint32_t fills = round + (s < slot ? 1 : 0);
-        int no_abort = 0;
-        if (fills) mbar_wait(smem_u32(&sm.full[s]), (fills - 1) & 1, &no_abort, a.err);
+      const unsigned long long t0 = now_ns();
+      for (int x = 0; x < Dec<MT>::kSlots; ++x)
+        while (now_ns() - t0 < kWaitNs / 4 && !mbar_try(smem_u32(&sm.full[x]), 0) && !mbar_try(smem_u32(&sm.full[x]), 1)) {
+        }
+      while (now_ns() - t0 < kWaitNs / 4) {
       }
     }
     return;
@@ -288,21 +326,24 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
   const int group = warp >> 2, quarter = warp & 3;
   const int pg = (g & 1) ? g ^ 4 : g;                // token order 0 5 2 7 4 1 6 3
   State<MT> st;
-  uint32_t slot = 0, round = 0;
+  uint32_t slot = group * kPer, parity = 0;  // of the group's own ring
+  auto step = [&]() {
+    if (++slot == (group + 1) * kPer) slot = group * kPer, parity ^= 1;
+  };
   bool ok = true;
   int b = pl.b, turn = 0;
-  int64_t item = start, before = pl.before;
-  while (item < stop) {
+  int64_t at = start, before = pl.before;
+  while (at < stop) {
     const Unit u = unit_of(a, b, first_row, kRows, topk, false);
-    if (u.items == 0 || item >= before + (int64_t)u.items * a.Hkv) {
-      before += (int64_t)u.items * a.Hkv;
+    if (u.weight == 0 || at >= before + (int64_t)u.weight * a.Hkv) {
+      before += (int64_t)u.weight * a.Hkv;
       ++b;
       continue;
     }
-    const int h = (int)((item - before) / u.items);
-    const int from = (int)(item - before - (int64_t)h * u.items);
-    const int to = (int)min((int64_t)u.items, from + (stop - item));
-    item += to - from;
+    const Part x = part_of(u, at - before, stop - at);
+    at += x.took;
+    const int from = x.from, to = x.to, h = x.h;
+    if (from >= to) continue;
     const int rows = min(kRows, u.n_new * a.G - first_row);
 
     // Queries, as the products want them: lane (g, t) holds dimensions 16 t .. and 64 + 16 t .. of its
@@ -356,10 +397,11 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
         for (int j = 0; j < 16; ++j) st.o[mt][j][2 * r] = st.o[mt][j][2 * r + 1] = 0.f;
       }
 
-    for (int it = from; it < to; ++it, turn = turn + 1 == Dec<MT>::kGroups ? 0 : turn + 1) {
+    for (int it = from; it < to; ++it, turn = turn + 1 == kGroups ? 0 : turn + 1) {
+      if (turn != group) continue;
       if (it < u.pages) {
-        if (turn == group) {
-          ok = mbar_wait(smem_u32(&sm.full[slot]), round & 1, abort, a.err) && ok;
+        {
+          ok = mbar_wait(smem_u32(&sm.full[slot]), parity, abort, a.err) && ok;
           ok = __all_sync(0xffffffffu, ok);
           const SlotMeta me = sm.meta[slot];
           if (ok && me.pos0 >= 0) {
@@ -427,19 +469,21 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sm.empty[slot]));
         }
-        if (++slot == kSlots) slot = 0, ++round;
+        step();
         continue;
       }
       // The tail. Rows are bf16; each warp scales its 16 tokens' keys, and values, by a power of two.
-      const uint32_t s1 = slot + 1 == kSlots ? 0 : slot + 1, r1 = slot + 1 == kSlots ? round + 1 : round;
-      if (turn == group) {
-        ok = mbar_wait(smem_u32(&sm.full[slot]), round & 1, abort, a.err) && ok;
-        ok = mbar_wait(smem_u32(&sm.full[s1]), r1 & 1, abort, a.err) && ok;
+      const uint32_t s0 = slot, p0 = parity;
+      step();
+      const uint32_t s1 = slot;
+      {
+        ok = mbar_wait(smem_u32(&sm.full[s0]), p0, abort, a.err) && ok;
+        ok = mbar_wait(smem_u32(&sm.full[s1]), parity, abort, a.err) && ok;
         ok = __all_sync(0xffffffffu, ok);
-        const SlotMeta me = sm.meta[slot];
+        const SlotMeta me = sm.meta[s0];
         const int have = u.tail - quarter * 16;  // of this warp's tokens
         if (ok && have > 0) {
-          const uint32_t keys = smem_u32(ring) + slot * kKv8PageBytes + quarter * 16 * kD * 2;
+          const uint32_t keys = smem_u32(ring) + s0 * kKv8PageBytes + quarter * 16 * kD * 2;
           const uint32_t vals = smem_u32(ring) + s1 * kKv8PageBytes + quarter * 16 * kD * 2;
           uint32_t bad[2][2];  // tokens of the lane's columns that hold something not finite
           // keys: per token tile, 16 + 16 dimensions of the lane's token
@@ -539,13 +583,11 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
         }
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&sm.empty[slot]));
+          mbar_arrive(smem_u32(&sm.empty[s0]));
           mbar_arrive(smem_u32(&sm.empty[s1]));
         }
       }
-      slot = s1;
-      round = r1;
-      if (++slot == kSlots) slot = 0, ++round;
+      step();
     }
 
     // ---- the unit's part of this CTA is done: join the warps' states, 8 rows at a time ----
@@ -571,19 +613,19 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
           *reinterpret_cast<float4*>(dst + 16 * e + j) =
               make_float4(st.o[mt][j][2 * r + e], st.o[mt][j + 1][2 * r + e], st.o[mt][j + 2][2 * r + e], st.o[mt][j + 3][2 * r + e]);
       consumers_sync<MT>();
-      const int at = tid >> 5, d0 = lane * 4, row = part * 8 + at;  // a warp a row, four dimensions a lane
-      if (at < 8 && row < rows) {
+      const int mine = tid >> 5, d0 = lane * 4, row = part * 8 + mine;  // a warp a row, four dimensions a lane
+      if (mine < 8 && row < rows) {
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kConsWarps; ++w) M = fmaxf(M, sm.m[w][at]);
+        for (int w = 0; w < kConsWarps; ++w) M = fmaxf(M, sm.m[w][mine]);
         const float base = M == -INFINITY ? 0.f : M;
         float L = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kConsWarps; ++w) {
-          const float f = ex2(sm.m[w][at] - base);
-          L += sm.l[w][at] * f;
-          const float4 x = *reinterpret_cast<const float4*>(join + (w * 8 + at) * kAccPad + (d0 >> 5) * 36 + (d0 & 31));
+          const float f = ex2(sm.m[w][mine] - base);
+          L += sm.l[w][mine] * f;
+          const float4 x = *reinterpret_cast<const float4*>(join + (w * 8 + mine) * kAccPad + (d0 >> 5) * 36 + (d0 & 31));
           o = make_float4(o.x + x.x * f, o.y + x.y * f, o.z + x.z * f, o.w + x.w * f);
         }
         if (whole) {
@@ -602,14 +644,15 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
   }
 }
 
-// Joins the parts of the units that several CTAs shared. CTA (c, row) looks after the unit that
-// begins in share c and goes on in the next, if there is one; parts are added in their order.
+// Joins the parts of the units that several CTAs shared. CTA (c, row) looks after the unit whose first
+// item is in share c and whose last is not, if there is one. Parts are added in a fixed order.
 constexpr int kJoinThreads = 128;
 
 __global__ void __launch_bounds__(kJoinThreads)
 kv8_join_kernel(const Kv8Args a, const Rows out, int tile_rows, int topk, int ctas, const float* __restrict__ partials) {
+  constexpr int kWarps = kJoinThreads / 32;
   __shared__ int64_t scratch[36];
-  __shared__ float s_m[kJoinThreads / 32], s_l[kJoinThreads / 32], s_o[kJoinThreads / 32][kD];
+  __shared__ float s_w[kMaxCtas], s_m[kWarps], s_l[kWarps], s_o[kWarps][kD];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x, tile = (int)blockIdx.y / tile_rows, row = (int)blockIdx.y % tile_rows;
   const int first_row = tile * tile_rows;
@@ -619,40 +662,57 @@ kv8_join_kernel(const Kv8Args a, const Rows out, int tile_rows, int topk, int ct
   asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this launch must not end before the first
   if (start >= stop || pl.b >= a.B) return;
   const Unit u = unit_of(a, pl.b, first_row, tile_rows, topk, false);
-  const int h = (int)((stop - 1 - pl.before) / u.items);
-  const int64_t begin = pl.before + (int64_t)h * u.items, end = begin + u.items;
-  if (begin < start || end <= stop || row >= u.n_new * a.G - first_row) return;
-  const int last = share_of(pl.total, end - 1, ctas);
+  const int h = (int)((stop - 1 - pl.before) / u.weight);
+  const int64_t begin = pl.before + (int64_t)h * u.weight + kUnitCost, end = begin + u.items;
+  if (begin < start || begin >= stop || end <= stop || row >= u.n_new * a.G - first_row) return;
+  const int n = share_of(pl.total, end - 1, ctas) - c + 1;  // at most kMaxCtas
 
   const float* mine = partials + (int64_t)row * kPartialStride;
   constexpr int64_t kSlotFloats = (int64_t)kMaxTileRows * kPartialStride;
+  auto part = [&](int x) { return mine + (int64_t)(2 * (tile * ctas + c + x) + (x == 0 ? 1 : 0)) * kSlotFloats; };
+  constexpr int kMost = (kMaxCtas + kJoinThreads - 1) / kJoinThreads;
+  float2 ml[kMost];
   float M = -INFINITY, L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int x = c + warp; x <= last; x += kJoinThreads / 32) {
-    if (share_start(pl.total, x, ctas) >= share_start(pl.total, x + 1, ctas)) continue;  // fewer items than CTAs
-    const float* p = mine + (int64_t)(2 * (tile * ctas + x) + (x == c ? 1 : 0)) * kSlotFloats;
-    const float m = p[0], l = p[1];
-    const float4 y = *reinterpret_cast<const float4*>(p + 4 + 4 * lane);
-    const float m2 = fmaxf(M, m), base = m2 == -INFINITY ? 0.f : m2;
-    const float f = ex2(M - base), k = ex2(m - base);
-    M = m2;
-    L = L * f + l * k;
-    o = make_float4(o.x * f + y.x * k, o.y * f + y.y * k, o.z * f + y.z * k, o.w * f + y.w * k);
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int x = i * kJoinThreads + tid;
+    ml[i] = make_float2(-INFINITY, 0.f);
+    // with fewer items than CTAs some shares are empty
+    if (x < n && share_start(pl.total, c + x, ctas) < share_start(pl.total, c + x + 1, ctas))
+      ml[i] = *reinterpret_cast<const float2*>(part(x));
+    M = fmaxf(M, ml[i].x);
   }
-  if (lane == 0) {
-    s_m[warp] = M;
-    s_l[warp] = L;
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) s_m[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
+  const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int x = i * kJoinThreads + tid;
+    const float f = ex2(ml[i].x - base);
+    L += ml[i].y * f;
+    if (x < n) s_w[x] = f;
+  }
+  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (lane == 0) s_l[warp] = L;
+  __syncthreads();
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int x = warp; x < n; x += kWarps) {
+    const float f = s_w[x];
+    if (f == 0.f) continue;  // also a share that is empty: nothing was written there
+    const float4 y = *reinterpret_cast<const float4*>(part(x) + 4 + 4 * lane);
+    o = make_float4(o.x + y.x * f, o.y + y.y * f, o.z + y.z * f, o.w + y.w * f);
   }
   *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = o;
   __syncthreads();
-  float top = -INFINITY;
-  for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, s_m[w]);
-  const float base = top == -INFINITY ? 0.f : top;
   float sum = 0.f, x = 0.f;
-  for (int w = 0; w < kJoinThreads / 32; ++w) {
-    const float f = ex2(s_m[w] - base);
-    sum += s_l[w] * f;
-    x += s_o[w][tid] * f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    sum += s_l[w];
+    x += s_o[w][tid];
   }
   const int i = (first_row + row) / a.G, head = h * a.G + (first_row + row) - i * a.G;
   const __nv_bfloat16 y = __float2bfloat16_rn(sum == 0.f ? 0.f : x / sum);

@@ -45,7 +45,7 @@ constexpr unsigned long long kWaitNs = 2000000000ull;
 
 // Waits until the phase with this parity has completed. Bounded: after kWaitNs, or once another
 // wait of the CTA has run out, it returns false with *abort (shared memory) set.
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+__device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   const unsigned long long t0 = now_ns();
   for (uint32_t it = 0; it < (1u << 30); ++it) {
     if (mbar_try(bar, parity)) return true;
@@ -130,15 +130,19 @@ __device__ __forceinline__ float scale_log2(float s) {
 // ---------------------------------------------------------------------------
 // The split of a call's work. A unit is one (request, KV head); a tile is a block of its rows (row r:
 // token r / G, head r % G). Per tile, a unit's items are the pages that the tile's last token may see
-// (or its list of pages), then the tail; the items of all units lie in one row, and CTA c of P takes
-// those from c W / P on.
+// (or its list of pages), then the tail. The items of all units lie in one row, each unit's behind
+// kUnitCost places that stand for the work of beginning and ending it, and CTA c of P takes the places
+// from c W / P on.
 // ---------------------------------------------------------------------------
+constexpr int kUnitCost = 4;
+
 struct Unit {  // of one request: the same for all of its heads
   int row0, n_new, past;
   int full;     // complete pages
   int tail;     // tokens of the tail
   int pages;    // entries of the page list
   int items;    // pages, and one for the tail if the tile sees it
+  int weight;   // items + kUnitCost, or 0
 };
 
 __device__ __forceinline__ Unit unit_of(const Kv8Args& a, int b, int first_row, int rows, int topk, bool report) {
@@ -147,29 +151,30 @@ __device__ __forceinline__ Unit unit_of(const Kv8Args& a, int b, int first_row, 
   const int len = u.past + u.n_new;
   u.full = ok ? len >> 6 : 0;
   u.tail = ok ? len & (kPart - 1) : 0;
-  u.pages = u.items = 0;
+  u.pages = u.items = u.weight = 0;
   if (!ok || (int64_t)u.n_new * a.G <= first_row) return u;  // the tile has no row of this request
   const int last = min(u.n_new, (first_row + rows - 1) / a.G + 1);  // tokens up to the tile's last row
   const int seen = u.past + last;
   u.pages = topk ? topk : min(u.full, (seen + kPart - 1) >> 6);
   u.items = u.pages + (u.tail && seen > u.full * kPart ? 1 : 0);
+  u.weight = u.items ? u.items + kUnitCost : 0;
   return u;
 }
 
 struct Place {
-  int64_t total;   // items of all units
-  int b;           // request of the item looked for
-  int64_t before;  // items of the requests before it
+  int64_t total;   // places of all units
+  int b;           // request of the place looked for
+  int64_t before;  // places of the requests before it
 };
 
-// The request of item `at(total)` for every thread of the CTA (n threads, scratch of 32 + 4 words
-// each of 8 bytes). Each thread adds up a run of requests; the one whose run holds the item walks it.
+// The request of place `at(total)` for every thread of the CTA (n threads, scratch of 32 + 4 words
+// each of 8 bytes). Each thread adds up a run of requests; the one whose run holds the place walks it.
 template <typename At>
 __device__ __forceinline__ Place locate(const Kv8Args& a, int first_row, int rows, int topk, bool report, int64_t* scratch, At at) {
   const int tid = threadIdx.x, n = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = n >> 5;
   const int run = (a.B + n - 1) / n, b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += unit_of(a, b, first_row, rows, topk, report).items;
+  for (int b = b0; b < b1; ++b) mine += unit_of(a, b, first_row, rows, topk, report).weight;
   mine *= a.Hkv;
   int64_t sum = mine;
   for (int o = 1; o < 32; o <<= 1) {
@@ -193,7 +198,7 @@ __device__ __forceinline__ Place locate(const Kv8Args& a, int first_row, int row
   if (want >= lo && want < lo + mine) {
     int64_t before = lo;
     for (int b = b0; b < b1; ++b) {
-      const int64_t m = (int64_t)unit_of(a, b, first_row, rows, topk, false).items * a.Hkv;
+      const int64_t m = (int64_t)unit_of(a, b, first_row, rows, topk, false).weight * a.Hkv;
       if (want < before + m) {
         scratch[32] = b;
         scratch[33] = before;
