@@ -22,7 +22,11 @@
 // products. With the copy's 128-byte swizzle and tokens in the order 0 5 2 7 4 1 6 3, all of these
 // 16-byte loads touch every bank once. Values need two tokens of one dimension side by side: one
 // byte permutation for two such pairs.
-#include "kv8_dev.cuh"
+#include "kv8_join.cuh"
+
+#ifndef FEW_ROWS
+#define FEW_ROWS 16
+#endif
 
 namespace spin {
 
@@ -30,12 +34,10 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kMaxCtas = 160;
 constexpr int kAccPad = 144;        // floats of a row in the join: 4 x (32 + 4)
 constexpr int kMaxTileRows = 32;
 constexpr int kMaxConsWarps = 12;
 constexpr int kMaxSlots = 10;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kShift = 14.f;                          // weights reach 2^14
 
 struct SlotMeta {
@@ -75,26 +77,6 @@ constexpr size_t dec_smem_bytes() {
   return 1024 + Dec<MT>::kRingBytes + Dec<MT>::kJoinBytes + Dec<MT>::kQBytes + sizeof(DecSmem);
 }
 static_assert(dec_smem_bytes<1>() <= 232448 && dec_smem_bytes<2>() <= 232448, "shared memory of a CTA");
-
-// What a CTA does of the unit that holds the place `at` of its request, with `left` of its share to go.
-struct Part {
-  int h, from, to;  // items [from, to) of head h; none where from >= to
-  int64_t took;
-};
-
-__device__ __forceinline__ Part part_of(const Unit& u, int64_t at, int64_t left) {
-  Part x;
-  x.h = (int)(at / u.weight);
-  const int f = (int)(at - (int64_t)x.h * u.weight), t = (int)min((int64_t)u.weight, f + left);
-  x.took = t - f;
-  x.from = max(0, f - kUnitCost);
-  x.to = max(0, t - kUnitCost);
-  return x;
-}
-
-// The first place of CTA c's share of n, and the CTA whose share has place x.
-__device__ __forceinline__ int64_t share_start(int64_t total, int c, int n) { return total * c / n; }
-__device__ __forceinline__ int share_of(int64_t total, int64_t x, int n) { return (int)(((x + 1) * n - 1) / total); }
 
 template <int MT>
 __device__ __forceinline__ void consumers_sync() {
@@ -203,8 +185,10 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int ctas = gridDim.x, cta = blockIdx.x;
   const bool report = cta == 0 && blockIdx.y == 0;
-  const Place pl = locate(a, first_row, kRows, topk, report, sm.scratch,
-                          [&](int64_t total) { return share_start(total, cta, ctas); });
+  const Place pl = locate(
+      a.B, sm.scratch,
+      [&](int x, bool first) { return (int64_t)unit_of(a, x, first_row, kRows, topk, report && first).weight * a.Hkv; },
+      [&](int64_t total) { return share_start(total, cta, ctas); });
   const int64_t start = share_start(pl.total, cta, ctas), stop = share_start(pl.total, cta + 1, ctas);
   if (start >= stop) return;
 
@@ -644,79 +628,23 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
   }
 }
 
-// Joins the parts of the units that several CTAs shared. CTA (c, row) looks after the unit whose first
-// item is in share c and whose last is not, if there is one. Parts are added in a fixed order.
-constexpr int kJoinThreads = 128;
-
+// Joins the parts of the units that several CTAs shared. CTA (c, y) looks after the unit whose first
+// item is in share c and whose last is not, if there is one, and of its rows after y, y + gridDim.y ..
+// Parts are added in a fixed order.
 __global__ void __launch_bounds__(kJoinThreads)
 kv8_join_kernel(const Kv8Args a, const Rows out, int tile_rows, int topk, int ctas, const float* __restrict__ partials) {
-  constexpr int kWarps = kJoinThreads / 32;
   __shared__ int64_t scratch[36];
-  __shared__ float s_w[kMaxCtas], s_m[kWarps], s_l[kWarps], s_o[kWarps][kD];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int c = blockIdx.x, tile = (int)blockIdx.y / tile_rows, row = (int)blockIdx.y % tile_rows;
-  const int first_row = tile * tile_rows;
-  const Place pl = locate(a, first_row, tile_rows, topk, false, scratch,
-                          [&](int64_t total) { return share_start(total, c + 1, ctas) - 1; });
-  const int64_t start = share_start(pl.total, c, ctas), stop = share_start(pl.total, c + 1, ctas);
+  const int c = blockIdx.x;
+  const int tile = blockIdx.z, first_row = tile * tile_rows;
+  const Place pl = locate(
+      a.B, scratch, [&](int x, bool) { return (int64_t)unit_of(a, x, first_row, tile_rows, topk, false).weight * a.Hkv; },
+      [&](int64_t total) { return share_start(total, c + 1, ctas) - 1; });
+  const int64_t stop = share_start(pl.total, c + 1, ctas);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this launch must not end before the first
-  if (start >= stop || pl.b >= a.B) return;
+  if (share_start(pl.total, c, ctas) >= stop || pl.b >= a.B) return;
   const Unit u = unit_of(a, pl.b, first_row, tile_rows, topk, false);
-  const int h = (int)((stop - 1 - pl.before) / u.weight);
-  const int64_t begin = pl.before + (int64_t)h * u.weight + kUnitCost, end = begin + u.items;
-  if (begin < start || begin >= stop || end <= stop || row >= u.n_new * a.G - first_row) return;
-  const int n = share_of(pl.total, end - 1, ctas) - c + 1;  // at most kMaxCtas
-
-  const float* mine = partials + (int64_t)row * kPartialStride;
-  constexpr int64_t kSlotFloats = (int64_t)kMaxTileRows * kPartialStride;
-  auto part = [&](int x) { return mine + (int64_t)(2 * (tile * ctas + c + x) + (x == 0 ? 1 : 0)) * kSlotFloats; };
-  constexpr int kMost = (kMaxCtas + kJoinThreads - 1) / kJoinThreads;
-  float2 ml[kMost];
-  float M = -INFINITY, L = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMost; ++i) {
-    const int x = i * kJoinThreads + tid;
-    ml[i] = make_float2(-INFINITY, 0.f);
-    // with fewer items than CTAs some shares are empty
-    if (x < n && share_start(pl.total, c + x, ctas) < share_start(pl.total, c + x + 1, ctas))
-      ml[i] = *reinterpret_cast<const float2*>(part(x));
-    M = fmaxf(M, ml[i].x);
-  }
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_m[warp] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
-  const float base = M == -INFINITY ? 0.f : M;
-#pragma unroll
-  for (int i = 0; i < kMost; ++i) {
-    const int x = i * kJoinThreads + tid;
-    const float f = ex2(ml[i].x - base);
-    L += ml[i].y * f;
-    if (x < n) s_w[x] = f;
-  }
-  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  if (lane == 0) s_l[warp] = L;
-  __syncthreads();
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int x = warp; x < n; x += kWarps) {
-    const float f = s_w[x];
-    if (f == 0.f) continue;  // also a share that is empty: nothing was written there
-    const float4 y = *reinterpret_cast<const float4*>(part(x) + 4 + 4 * lane);
-    o = make_float4(o.x + y.x * f, o.y + y.y * f, o.z + y.z * f, o.w + y.w * f);
-  }
-  *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = o;
-  __syncthreads();
-  float sum = 0.f, x = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    sum += s_l[w];
-    x += s_o[w][tid];
-  }
-  const int i = (first_row + row) / a.G, head = h * a.G + (first_row + row) - i * a.G;
-  const __nv_bfloat16 y = __float2bfloat16_rn(sum == 0.f ? 0.f : x / sum);
-  out.p[(int64_t)(u.row0 + i) * out.ts + (int64_t)head * out.hs + tid] = *reinterpret_cast<const uint16_t*>(&y);
+  join_parts(a, out, u, pl, pl.before, first_row, tile_rows, c, ctas, partials + (int64_t)tile * ctas * 2 * kMaxTileRows * kPartialStride,
+             kMaxTileRows);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -753,7 +681,7 @@ cudaError_t launch_decode(const Kv8Args& a, const CUtensorMap& map, const Rows& 
                           const int32_t* sel, int topk, float* partials, int sm_count, cudaStream_t st) {
   const int rows = R == 1 ? 8 : 16 * MT;
   const int64_t tiles = ((int64_t)a.max_new * a.G + rows - 1) / rows;
-  if (tiles > 65535 / rows) return cudaErrorInvalidConfiguration;
+  if (tiles > 65535) return cudaErrorInvalidConfiguration;
   const int sms = sm_count < kMaxCtas ? sm_count : kMaxCtas;
   const int ctas = tiles >= sms ? 1 : (int)(sms / tiles);  // a tile; ctas > 1 only if all of them fit the workspace
   cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<MT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dec_smem_bytes<MT>());
@@ -763,7 +691,7 @@ cudaError_t launch_decode(const Kv8Args& a, const CUtensorMap& map, const Rows& 
   e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(tiles * rows));
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)rows, (unsigned)tiles);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -776,14 +704,18 @@ cudaError_t launch_decode(const Kv8Args& a, const CUtensorMap& map, const Rows& 
 
 }  // namespace
 
-int64_t kv8_attend_workspace(const Kv8Args&) { return (int64_t)2 * kMaxCtas * kMaxTileRows * kPartialStride * 4; }
+int64_t kv8_attend_workspace(const Kv8Args&) {
+  const int64_t few = (int64_t)2 * kMaxCtas * kMaxTileRows * kPartialStride * 4, many = kv8_prefill_workspace();
+  return few > many ? few : many;
+}
 
 cudaError_t launch_kv8_attend(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const int32_t* sel,
                               int topk, void* workspace, int sm_count, cudaStream_t st) {
+  float* partials = static_cast<float*>(workspace);
+  if ((int64_t)a.max_new * a.G > FEW_ROWS) return launch_kv8_prefill(a, q, out, scale, sel, topk, partials, sm_count, st);
   CUtensorMap map;
   const cudaError_t e = page_map(a, &map);
   if (e != cudaSuccess) return e;
-  float* partials = static_cast<float*>(workspace);
   if ((int64_t)a.max_new * a.G <= 8) return launch_decode<1, 1>(a, map, q, out, scale, sel, topk, partials, sm_count, st);
   if ((int64_t)a.max_new * a.G <= 16) return launch_decode<1, 2>(a, map, q, out, scale, sel, topk, partials, sm_count, st);
   return launch_decode<2, 2>(a, map, q, out, scale, sel, topk, partials, sm_count, st);

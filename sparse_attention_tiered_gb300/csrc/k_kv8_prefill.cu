@@ -1,0 +1,704 @@
+// spin_kv8_attend for many rows a unit: prompt chunks, and drafted tokens of a large group.
+//
+// With M = 128 rows of queries per tile a page costs 4 * 128 * 128 * 64 flops and 16 KB, so the tensor
+// cores are what can be busy: one persistent CTA per SM holds 256 rows (two tiles) of one unit and
+// takes two pages (128 tokens) a step. All products are tcgen05.mma on fp16 operands with fp32
+// accumulators in tensor memory:
+//   S_t[128 x 128] = Q_t (shared memory) K^T (shared memory), 8 products of depth 16,
+//   O_t[128 x 128] += P_t (tensor memory, in the place of S_t) V (shared memory, tokens as depth).
+// Roles, by warp:
+//   0-3, 4-7  softmax of tile 0 and 1, one row a thread: scores out of tensor memory, running maximum,
+//             fp16 weights back into it; the output rescaled only when the maximum has grown by
+//             more than 2^8, which is rare, so that O stays where it is; rows stored at the end;
+//   8-11      codes from HBM to fp16 in shared memory, 128-byte swizzled. A page's loads are in
+//             registers one step ahead of their use, so no shared memory holds codes;
+//   12        issues the products: P_0 V, S_0, P_1 V, S_1 of each step, so that one tile's softmax
+//             runs under the other's products.
+// Tensor memory: O_0, O_1, S_0, S_1 of 128 columns each. Shared memory: Q_0, Q_1 and two steps of
+// K and of V, 32 KB each.
+//
+// The arithmetic is that of the few-row kernel: z = score * k * log2(e) + log2(v) per page, weights
+// 2^(z - M + 6) with M at most 2^8 below the maximum, the softmax sum takes weight / v.
+#include "kv8_join.cuh"
+
+namespace spin {
+
+namespace {
+
+using namespace kv8;
+
+constexpr int kTile = 128;
+constexpr int kBlockRows = 2 * kTile;
+constexpr int kStep = 2 * kPart;  // tokens of a step
+constexpr int kThreads = 512;
+constexpr int kLoadWarp = 8, kMmaWarp = 12;
+constexpr float kUp = 6.f;     // weights reach 2^kUp times ..
+constexpr float kSlack = 8.f;  // .. 2^kSlack before the output is rescaled
+constexpr int kPlane = 32768;  // K or V: [2 planes of 64 dimensions][2 steps][128 tokens][128 bytes]
+constexpr uint32_t kColO = 0, kColS = 256;
+
+// What the softmax warps have to know of a step's tokens, by groups of 16.
+struct StepMeta {
+  float kfac[8];       // score factor, without the row's
+  float vlog[8], vinv[8];
+  uint32_t bad[4];     // bit per token: it holds a value that is not finite
+  int pos[2], count[2];  // position of each page's first token, tokens it holds (0: no page)
+};
+
+struct Smem {
+  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2];
+  StepMeta meta[4];  // by step mod 4: a softmax warp may be two steps behind the loaders, which run one ahead
+  int64_t scratch[36];
+  uint32_t tmem;
+  int abort;
+};
+
+constexpr size_t kQBytes = (size_t)kBlockRows * kD * 2;       // 64 KB: [tile][2 planes][128 rows][128 bytes]
+constexpr size_t kKvBytes = (size_t)2 * kPlane;               // 64 KB each
+constexpr size_t kSmemBytes = 1024 + kQBytes + 2 * kKvBytes + sizeof(Smem);
+static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
+
+// Shared memory descriptor of a 128-byte swizzled operand: 8-row groups `sbo` bytes apart, and for an
+// operand whose rows are the depth, 64-element blocks `lbo` bytes apart.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+
+// fp16 x fp16 -> fp32, M = 128; b_rows_depth: B is stored with its depth as rows.
+constexpr uint32_t shape(int n, bool b_rows_depth) {
+  return 1u << 4 | (b_rows_depth ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(kTile >> 4) << 24;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+
+// The barrier is arrived at once all products issued so far are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define SPIN_R8(a, i) "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3]), "+r"(a[i + 4]), "+r"(a[i + 5]), "+r"(a[i + 6]), "+r"(a[i + 7])
+#define SPIN_W8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), "=r"(a[i + 5]), "=r"(a[i + 6]), "=r"(a[i + 7])
+#define SPIN_I8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
+
+// 32 columns of the warp's 32 lanes, one lane a thread. The values are there after tmem_loaded().
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : SPIN_W8(r, 0), SPIN_W8(r, 8), SPIN_W8(r, 16), SPIN_W8(r, 24)
+      : "r"(addr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::SPIN_I8(r, 0),
+      SPIN_I8(r, 8), SPIN_I8(r, 16), SPIN_I8(r, 24), "r"(addr)
+      : "memory");
+}
+
+// After tmem_loaded(): uses of the loaded registers stay behind it.
+__device__ __forceinline__ void settle32(uint32_t* r) {
+  asm volatile("" : SPIN_R8(r, 0), SPIN_R8(r, 8), SPIN_R8(r, 16), SPIN_R8(r, 24));
+}
+
+// One row block of one head, and the part of its items that this CTA does.
+struct Segment {
+  Unit u;
+  int first_row, h, from, to;
+  int steps;       // of two items each
+  int limit[2];    // items that a tile's last row may see; 0: the tile has no rows
+  __device__ __forceinline__ bool active(int tile, int step) const { return from + 2 * step < min(to, limit[tile]); }
+};
+
+// Walks the CTA's share; every role does so for itself, in step.
+struct Walk {
+  int b, block;
+  int64_t at, stop, before;
+  __device__ __forceinline__ bool next(const Kv8Args& a, int topk, Segment& s) {
+    while (at < stop) {
+      const Unit u = unit_of(a, b, block * kBlockRows, kBlockRows, topk, false);
+      if (u.weight == 0) {  // the request has no more rows
+        ++b;
+        block = 0;
+        if (b >= a.B) return false;
+        continue;
+      }
+      if (at >= before + (int64_t)u.weight * a.Hkv) {
+        before += (int64_t)u.weight * a.Hkv;
+        ++block;
+        continue;
+      }
+      const Part x = part_of(u, at - before, stop - at);
+      at += x.took;
+      if (x.from >= x.to) continue;
+      s.u = u;
+      s.first_row = block * kBlockRows;
+      s.h = x.h;
+      s.from = x.from;
+      s.to = x.to;
+      s.steps = (x.to - x.from + 1) / 2;
+      for (int t = 0; t < 2; ++t) s.limit[t] = unit_of(a, b, s.first_row + t * kTile, kTile, topk, false).items;
+      return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ int64_t blocks_weight(const Kv8Args& a, int b, int topk, bool report) {
+  int64_t sum = 0;
+  for (int block = 0;; ++block) {
+    const int w = unit_of(a, b, block * kBlockRows, kBlockRows, topk, report && block == 0).weight;
+    if (w == 0) return sum * a.Hkv;
+    sum += w;
+  }
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__global__ void __launch_bounds__(kThreads, 1)
+kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, const int32_t* __restrict__ sel, int topk,
+                   float* __restrict__ partials) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sq = smem_u32(base), sk = sq + (uint32_t)kQBytes, sv = sk + (uint32_t)kKvBytes;
+  Smem& sm = *reinterpret_cast<Smem*>(base + kQBytes + 2 * kKvBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort = &sm.abort;
+  const int ctas = gridDim.x, cta = blockIdx.x;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.q_full[i]), 4);
+      mbar_init(smem_u32(&sm.k_full[i]), 4);
+      mbar_init(smem_u32(&sm.v_full[i]), 4);
+      mbar_init(smem_u32(&sm.p_full[i]), 4);
+      mbar_init(smem_u32(&sm.k_empty[i]), 1);
+      mbar_init(smem_u32(&sm.v_empty[i]), 1);
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.pv_done[i]), 1);
+    }
+    sm.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tmem_before();
+  const Place pl = locate(
+      a.B, sm.scratch, [&](int x, bool first) { return blocks_weight(a, x, topk, first && cta == 0); },
+      [&](int64_t total) { return share_start(total, cta, ctas); });
+  tmem_after();
+  const uint32_t tmem = sm.tmem;
+  Walk walk{pl.b, 0, share_start(pl.total, cta, ctas), share_start(pl.total, cta + 1, ctas), pl.before};
+  Segment s;
+  bool ok = true;
+  // 512 threads x 128 registers at launch = 256 x 176 + 128 x 112 + 128 x 48.
+
+  if (warp < kLoadWarp) {
+    // ------------------------------ softmax, a row a thread ------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    const int tile = warp >> 2, quad = warp & 3;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t S = lanes + kColS + tile * kTile, O = lanes + kColO + tile * kTile;
+    uint32_t done = 0;    // steps of this tile so far
+    uint32_t count = 0;   // steps of the CTA so far
+    while (walk.next(a, topk, s)) {
+      const int row = s.first_row + tile * kTile + quad * 32 + lane;
+      const bool mine = row < s.u.n_new * a.G;
+      const int i = row / a.G, head = s.h * a.G + row - i * a.G;
+      const int see = mine ? s.u.past + i + 1 : 0x7fffffff;  // rows that are not there see all: no masks for them
+      float qs = 1.f;
+      const int my_steps = s.limit[tile] ? max(0, (min(s.to, s.limit[tile]) - s.from + 1) / 2) : 0;
+      if (my_steps) {
+        // the row: 64 words, its largest element, fp16 with the factor in qs; scale's sign goes here
+        const uint4* src = reinterpret_cast<const uint4*>(q.p + (int64_t)(s.u.row0 + i) * q.ts + (int64_t)head * q.hs);
+        uint4 w[16];
+        uint32_t top = 0;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          w[x] = mine ? src[x] : make_uint4(0, 0, 0, 0);
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[x].x & 0x7fff7fffu, w[x].y & 0x7fff7fffu),
+                                       __vmaxu2(w[x].z & 0x7fff7fffu, w[x].w & 0x7fff7fffu)));
+        }
+        top = max(top & 0xffffu, top >> 16);
+        const int e = half_exponent(top);
+        const float f = scale < 0.f ? -pow2(15 - e) : pow2(15 - e);
+        qs = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e - 15);
+        const int r = quad * 32 + lane;
+        const uint32_t dst = sq + tile * (kTile * kD * 2) + r * 128;
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          sts128(dst + (x >> 3) * (kTile * 128) + (((x & 7) ^ (r & 7)) << 4), pack_half2(lo_f(w[x].x) * f, hi_f(w[x].x) * f),
+                 pack_half2(lo_f(w[x].y) * f, hi_f(w[x].y) * f), pack_half2(lo_f(w[x].z) * f, hi_f(w[x].z) * f),
+                 pack_half2(lo_f(w[x].w) * f, hi_f(w[x].w) * f));
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[tile]));
+      }
+
+      float M = -INFINITY, L = 0.f;
+      for (int step = 0; step < my_steps; ++step, ++done) {
+        ok = ok && mbar_wait(smem_u32(&sm.s_full[tile]), done & 1, abort, a.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
+        const StepMeta& me = sm.meta[(count + step) & 3];
+        const int halves = s.from + 2 * step + 1 < s.to ? 2 : 1;
+        if (s.from + 2 * step + halves > s.u.pages) {  // the tail's values have a scale of their own, known once loaded
+          const uint32_t c = count + step;
+          ok = ok && mbar_wait(smem_u32(&sm.v_full[c & 1]), c >> 1 & 1, abort, a.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) continue;
+        }
+        tmem_after();
+        uint32_t x[64];
+        // the largest z of the row's visible tokens, page by page
+        float top = -INFINITY;
+        int vis[2];
+        bool plain[2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          vis[hf] = hf < halves ? min(see - me.pos[hf], me.count[hf]) : 0;
+          plain[hf] = __all_sync(0xffffffffu, vis[hf] >= kPart) && (me.bad[2 * hf] | me.bad[2 * hf + 1]) == 0;
+        }
+        // Scores of a page into x: of all tokens where `plain`, else the final z with -inf for hidden tokens.
+        auto fetch = [&](int hf) {
+          tmem_load32(S + hf * kPart, x);
+          tmem_load32(S + hf * kPart + 32, x + 32);
+          tmem_loaded();
+          settle32(x);
+          settle32(x + 32);
+          if (!plain[hf]) {
+#pragma unroll
+            for (int c = 0; c < kPart; ++c) {
+              const int grp = hf * 4 + c / 16;
+              float z = fmaf(__uint_as_float(x[c]), me.kfac[grp] * qs, me.vlog[grp]);
+              if (me.bad[hf * 2 + c / 32] >> (c & 31) & 1u) z = __uint_as_float(0x7fc00000u);
+              x[c] = __float_as_uint(c < vis[hf] ? z : -INFINITY);
+            }
+          }
+        };
+        auto largest = [&](int hf) {
+#pragma unroll
+          for (int grp = 0; grp < 4; ++grp) {
+            float m = __uint_as_float(x[grp * 16]);
+#pragma unroll
+            for (int c = 1; c < 16; ++c) m = fmaxf(m, __uint_as_float(x[grp * 16 + c]));
+            top = fmaxf(top, plain[hf] ? fmaf(m, me.kfac[hf * 4 + grp] * qs, me.vlog[hf * 4 + grp]) : m);
+          }
+        };
+        if (halves == 2) {
+          fetch(0);
+          largest(0);
+        }
+        const int last = halves - 1;
+        fetch(last);
+        largest(last);
+        const float m2 = fmaxf(M, top);
+        if (m2 > M + kSlack || (M == -INFINITY && m2 != -INFINITY)) {
+          top = m2;
+        } else {
+          top = M;
+        }
+        if (__any_sync(0xffffffffu, top != M)) {
+          const float f = top == M ? 1.f : ex2(M - top);  // 0 for a row that saw nothing yet
+          if (step > 0) {  // rare after the first step: the output so far, once its products are done
+            ok = ok && mbar_wait(smem_u32(&sm.pv_done[tile]), (done - 1) & 1, abort, a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) continue;
+            tmem_after();
+            for (int c = 0; c < kD; c += 32) {
+              uint32_t y[32];
+              tmem_load32(O + c, y);
+              tmem_loaded();
+              settle32(y);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+              tmem_store32(O + c, y);
+            }
+            tmem_stored();
+          }
+          L *= f;
+          M = top;
+        }
+        const float ref = (M == -INFINITY ? 0.f : M) - kUp;
+        auto weigh = [&](int hf) {  // fp16 weights of a page, into the first 32 columns of its scores
+          uint32_t p[32];
+#pragma unroll
+          for (int grp = 0; grp < 4; ++grp) {
+            const float k = plain[hf] ? me.kfac[hf * 4 + grp] * qs : 1.f;
+            const float c0 = plain[hf] ? me.vlog[hf * 4 + grp] - ref : -ref;
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              const float y0 = ex2(fmaf(__uint_as_float(x[grp * 16 + c]), k, c0));
+              const float y1 = ex2(fmaf(__uint_as_float(x[grp * 16 + c + 1]), k, c0));
+              sum0 += y0;
+              sum1 += y1;
+              p[grp * 8 + c / 2] = pack_half2(y0, y1);
+            }
+            const float sum = sum0 + sum1;
+            L += sum == 0.f ? 0.f : sum * me.vinv[hf * 4 + grp];  // nothing of a NaN page that the row does not see
+          }
+          tmem_store32(S + hf * kPart, p);
+        };
+        weigh(last);
+        if (halves == 2) {
+          fetch(0);
+          weigh(0);
+        }
+        tmem_stored();
+        tmem_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[tile]));
+      }
+      count += s.steps;
+
+      // ---- the row's end ----
+      if (s.limit[tile]) {
+        if (my_steps) {
+          ok = ok && mbar_wait(smem_u32(&sm.pv_done[tile]), (done - 1) & 1, abort, a.err);
+          ok = __all_sync(0xffffffffu, ok);
+          tmem_after();
+        }
+        const bool whole = s.from == 0 && s.to == s.u.items;
+        const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+        float* part = partials + ((int64_t)(2 * cta + (s.from == 0 ? 1 : 0)) * kBlockRows + tile * kTile + quad * 32 + lane) * kPartialStride;
+        if (!whole && mine) *reinterpret_cast<float2*>(part) = make_float2(M, L);
+        __syncwarp();
+        if (my_steps && ok) {
+          uint16_t* dst = out.p + (int64_t)(s.u.row0 + i) * out.ts + (int64_t)head * out.hs;
+          for (int c = 0; c < kD; c += 32) {
+            uint32_t y[32];
+            tmem_load32(O + c, y);
+            tmem_loaded();
+            settle32(y);
+            if (mine && whole) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(y[k + 2 * e]) * inv, __uint_as_float(y[k + 2 * e + 1]) * inv);
+                  w[e] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+                *reinterpret_cast<uint4*>(dst + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else if (mine) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)
+                *reinterpret_cast<uint4*>(part + 4 + c + k) = make_uint4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+            }
+            __syncwarp();
+          }
+          tmem_before();
+        }
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    // ------------------------------ loaders ------------------------------
+    // Warp w has rows 16 w .. 16 w + 15 of every page; lane (r, c) of them rows r, r + 4 .., bytes 16 c ...
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    const int w4 = warp - kLoadWarp, r4 = lane >> 3, c8 = lane & 7;
+    uint32_t count = 0;
+    while (walk.next(a, topk, s)) {
+      const int64_t unit = (int64_t)walk.b * a.Hkv + s.h;
+      int id = -1, pos = -1, id_base = s.from;
+      float2 sc = make_float2(1.f, 1.f);
+      auto look = [&](int first) {  // page ids and scales of 32 items
+        id_base = first;
+        const int it = first + lane;
+        id = pos = -1;
+        if (it < min(s.to, s.u.pages)) {
+          const int p = topk ? sel[unit * topk + it] : it;
+          if (p >= 0 && p < s.u.full) {
+            id = a.table[unit * a.max_pages + p];
+            if (id < 0 || (int64_t)id >= a.n_pages) {
+              if (w4 == 0) atomicOr(a.err, (uint32_t)kErrIndex);
+              id = -1;
+            } else {
+              pos = p * kPart;
+              sc = *reinterpret_cast<const float2*>(a.scales + 2 * (int64_t)id);
+            }
+          }
+        }
+      };
+      uint4 raw[8];  // keys or values of two pages, four rows each
+      auto load = [&](int step, int half) {
+#pragma unroll
+        for (int pg = 0; pg < 2; ++pg) {
+          const int it = s.from + 2 * step + pg;
+          if (it >= id_base + 32) look(it);
+          const int page = it < s.u.pages && it < s.to ? __shfl_sync(0xffffffffu, id, it - id_base) : -1;
+          const uint8_t* src = a.pages + (int64_t)page * kKv8PageBytes + half * kKv8HalfBytes + (w4 * 16 + r4) * kD + c8 * 16;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            raw[pg * 4 + x] = page >= 0 ? __ldcg(reinterpret_cast<const uint4*>(src + x * 4 * kD)) : make_uint4(0, 0, 0, 0);
+        }
+      };
+      // codes in raw -> fp16 rows of page pg in the operand at `at`
+      auto put_page = [&](uint32_t at, int pg) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int row = w4 * 16 + x * 4 + r4;
+          const uint4 v = raw[pg * 4 + x];
+          const uint32_t dst = at + (c8 >> 2) * kPlane + (pg * kPart + row) * 128;
+          const int ch = (c8 & 3) * 2;
+          sts128(dst + (((ch + 0) ^ (row & 7)) << 4), e4m3x2_half2(v.x, false), e4m3x2_half2(v.x, true), e4m3x2_half2(v.y, false), e4m3x2_half2(v.y, true));
+          sts128(dst + (((ch + 1) ^ (row & 7)) << 4), e4m3x2_half2(v.z, false), e4m3x2_half2(v.z, true), e4m3x2_half2(v.w, false), e4m3x2_half2(v.w, true));
+        }
+      };
+      // The tail's keys or values as page pg: the warp's 16 rows scaled by a power of two.
+      auto put_tail = [&](uint32_t at, int pg, int half, StepMeta& me) {
+        const uint16_t* src = a.tails + unit * kPageElems + half * kPart * kD;
+        uint4 v[4][2];
+        uint32_t top = 0, wrong = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int row = w4 * 16 + x * 4 + r4;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            uint4 t = make_uint4(0, 0, 0, 0);
+            if (row < s.u.tail) t = __ldcg(reinterpret_cast<const uint4*>(src + row * kD + c8 * 16) + y);
+            uint32_t* tt = reinterpret_cast<uint32_t*>(&t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool lo = (tt[e] & 0x7f80u) == 0x7f80u, hi = (tt[e] & 0x7f800000u) == 0x7f800000u;
+              if (lo) tt[e] &= 0xffff0000u;
+              if (hi) tt[e] &= 0x0000ffffu;
+              if (lo || hi) wrong |= 1u << (x * 4 + r4);
+              top = __vmaxu2(top, tt[e] & 0x7fff7fffu);
+            }
+            v[x][y] = t;
+          }
+        }
+        top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+        wrong = __reduce_or_sync(0xffffffffu, wrong);
+        const int e = half_exponent(top);
+        const float f = pow2(15 - e);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int row = w4 * 16 + x * 4 + r4;
+          const uint32_t dst = at + (c8 >> 2) * kPlane + (pg * kPart + row) * 128;
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            sts128(dst + ((((c8 & 3) * 2 + y) ^ (row & 7)) << 4), pack_half2(lo_f(v[x][y].x) * f, hi_f(v[x][y].x) * f),
+                   pack_half2(lo_f(v[x][y].y) * f, hi_f(v[x][y].y) * f), pack_half2(lo_f(v[x][y].z) * f, hi_f(v[x][y].z) * f),
+                   pack_half2(lo_f(v[x][y].w) * f, hi_f(v[x][y].w) * f));
+        }
+        if (lane == 0) {
+          if (half == 0) {
+            me.kfac[pg * 4 + w4] = fabsf(scale) * kLog2e * pow2(e - 15);
+          } else {
+            me.vlog[pg * 4 + w4] = (float)(e - 15);
+            me.vinv[pg * 4 + w4] = f;
+          }
+          if (wrong) atomicOr(&me.bad[pg * 2 + (w4 >> 1)], wrong << (16 * (w4 & 1)));
+        }
+      };
+      auto put = [&](uint32_t at, int step, int half, StepMeta& me) {
+#pragma unroll
+        for (int pg = 0; pg < 2; ++pg) {
+          const int it = s.from + 2 * step + pg;
+          if (it >= s.to) break;
+          if (it < s.u.pages) put_page(at, pg);
+          else put_tail(at, pg, half, me);
+        }
+      };
+      look(s.from);
+      load(0, 0);
+      for (int step = 0; step < s.steps; ++step, ++count) {
+        const uint32_t slot = count & 1, parity = count >> 1 & 1;
+        StepMeta& me = sm.meta[count & 3];
+        // keys
+        ok = ok && mbar_wait(smem_u32(&sm.k_empty[slot]), parity ^ 1, abort, a.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          // what the softmax has to know; warp 0's lanes 0 and 1 for one page each
+          if (lane == 0) {
+            if ((w4 & 1) == 0) {
+#pragma unroll
+              for (int pg = 0; pg < 2; ++pg) me.bad[pg * 2 + (w4 >> 1)] = 0;
+            }
+          }
+#pragma unroll
+          for (int pg = 0; pg < 2; ++pg) {
+            const int it = s.from + 2 * step + pg;
+            if (it >= s.to) {
+              if (w4 == 0 && lane == 0) me.count[pg] = 0, me.pos[pg] = 0;
+              continue;
+            }
+            if (it >= s.u.pages) {
+              if (w4 == 0 && lane == 0) me.count[pg] = s.u.tail, me.pos[pg] = s.u.full * kPart;
+              continue;
+            }
+            if (it >= id_base + 32) look(it);
+            const int p = __shfl_sync(0xffffffffu, pos, it - id_base);
+            const float kx = __shfl_sync(0xffffffffu, sc.x, it - id_base), vx = __shfl_sync(0xffffffffu, sc.y, it - id_base);
+            if (lane == 0) {
+              me.kfac[pg * 4 + w4] = p >= 0 ? kx * fabsf(scale) * kLog2e : 0.f;
+              me.vlog[pg * 4 + w4] = p >= 0 ? scale_log2(vx) : 0.f;
+              me.vinv[pg * 4 + w4] = p >= 0 ? 1.f / vx : 1.f;
+              if (w4 == 0) me.count[pg] = p >= 0 ? kPart : 0, me.pos[pg] = max(p, 0);
+            }
+          }
+          // (the flags of a tail are set by its warps after they are cleared: one barrier)
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+          put(sk + slot * 16384, step, 0, me);
+          proxy_fence();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.k_full[slot]));
+        } else {
+          asm volatile("bar.sync 2, 128;" ::: "memory");
+        }
+        load(step, 1);
+        ok = ok && mbar_wait(smem_u32(&sm.v_empty[slot]), parity ^ 1, abort, a.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          put(sv + slot * 16384, step, 1, me);
+          proxy_fence();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.v_full[slot]));
+        }
+        if (step + 1 < s.steps) load(step + 1, 0);
+      }
+    }
+  } else {
+    // ------------------------------ products ------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == kMmaWarp && lane == 0) {
+      uint32_t count = 0, segs[2] = {0, 0}, done[2] = {0, 0};
+      auto scores = [&](int tile, uint32_t c, int pages) {
+        const uint32_t d = tmem + kColS + tile * kTile;
+        const uint32_t at = sq + tile * (kTile * kD * 2), bt = sk + (c & 1) * 16384;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ss(d, operand(at + (k >> 2) * (kTile * 128) + (k & 3) * 32, 16, 1024),
+                 operand(bt + (k >> 2) * kPlane + (k & 3) * 32, 16, 1024), pages == 2 ? shape(kStep, false) : shape(kPart, false), k > 0);
+        mma_commit(smem_u32(&sm.s_full[tile]));
+      };
+      while (walk.next(a, topk, s)) {
+        auto pages_of = [&](int step) { return min(2, s.to - s.from - 2 * step); };
+        ok = ok && mbar_wait(smem_u32(&sm.k_full[count & 1]), count >> 1 & 1, abort, a.err);
+        for (int t = 0; t < 2; ++t)
+          if (s.active(t, 0)) {
+            ok = ok && mbar_wait(smem_u32(&sm.q_full[t]), segs[t]++ & 1, abort, a.err);
+            tmem_after();
+            if (ok) scores(t, count, pages_of(0));
+          }
+        if (ok) mma_commit(smem_u32(&sm.k_empty[count & 1]));
+        for (int step = 0; step < s.steps; ++step, ++count) {
+          const int pages = pages_of(step);
+          const bool more = step + 1 < s.steps;
+          ok = ok && mbar_wait(smem_u32(&sm.v_full[count & 1]), count >> 1 & 1, abort, a.err);
+          if (more) ok = ok && mbar_wait(smem_u32(&sm.k_full[(count + 1) & 1]), (count + 1) >> 1 & 1, abort, a.err);
+          for (int t = 0; t < 2; ++t) {
+            if (s.active(t, step)) {
+              ok = ok && mbar_wait(smem_u32(&sm.p_full[t]), done[t]++ & 1, abort, a.err);
+              tmem_after();
+              if (ok) {
+                const uint32_t d = tmem + kColO + t * kTile, p = tmem + kColS + t * kTile;
+                for (int k = 0; k < 4 * pages; ++k)
+                  mma_ts(d, p + (k >> 2) * kPart + (k & 3) * 8, operand(sv + (count & 1) * 16384 + k * 2048, kPlane, 1024),
+                         shape(kD, true), step > 0 || k > 0);
+                mma_commit(smem_u32(&sm.pv_done[t]));
+              }
+            }
+            if (t == 1 && ok) mma_commit(smem_u32(&sm.v_empty[count & 1]));
+            if (more && s.active(t, step + 1) && ok) scores(t, count + 1, pages_of(step + 1));
+          }
+          if (more && ok) mma_commit(smem_u32(&sm.k_empty[(count + 1) & 1]));
+        }
+      }
+      // The last arrivals have landed before the CTA's shared memory goes.
+      if (count > 0) {
+        ok = ok && mbar_wait(smem_u32(&sm.k_empty[(count - 1) & 1]), (count - 1) >> 1 & 1, abort, a.err);
+        ok = ok && mbar_wait(smem_u32(&sm.v_empty[(count - 1) & 1]), (count - 1) >> 1 & 1, abort, a.err);
+      }
+    }
+    __syncwarp();
+  }
+  tmem_before();
+  __syncthreads();
+  tmem_after();
+  if (warp == kMmaWarp) {
+    if (*abort) {  // products may be in flight: give them time to end before their memory goes
+      const unsigned long long t0 = now_ns();
+      while (now_ns() - t0 < kWaitNs / 8) {
+      }
+    }
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+__global__ void __launch_bounds__(kJoinThreads)
+kv8_prefill_join_kernel(const Kv8Args a, const Rows out, int topk, int ctas, const float* __restrict__ partials) {
+  __shared__ int64_t scratch[36];
+  const int c = blockIdx.x;
+  const Place pl = locate(
+      a.B, scratch, [&](int x, bool) { return blocks_weight(a, x, topk, false); },
+      [&](int64_t total) { return share_start(total, c + 1, ctas) - 1; });
+  const int64_t stop = share_start(pl.total, c + 1, ctas);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this launch must not end before the first
+  if (share_start(pl.total, c, ctas) >= stop || pl.b >= a.B) return;
+  int64_t before = pl.before;
+  for (int block = 0;; ++block) {
+    const Unit u = unit_of(a, pl.b, block * kBlockRows, kBlockRows, topk, false);
+    if (u.weight == 0) return;
+    if (stop - 1 < before + (int64_t)u.weight * a.Hkv) {
+      join_parts(a, out, u, pl, before, block * kBlockRows, kBlockRows, c, ctas, partials, kBlockRows);
+      return;
+    }
+    before += (int64_t)u.weight * a.Hkv;
+  }
+}
+
+}  // namespace
+
+int64_t kv8_prefill_workspace() { return (int64_t)2 * kMaxCtas * kBlockRows * kPartialStride * 4; }
+
+cudaError_t launch_kv8_prefill(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const int32_t* sel,
+                               int topk, float* partials, int sm_count, cudaStream_t st) {
+  const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+  cudaError_t e = cudaFuncSetAttribute(kv8_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kv8_prefill_kernel<<<ctas, kThreads, kSmemBytes, st>>>(a, q, out, scale, sel, topk, partials);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || ctas == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas, 16);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv8_prefill_join_kernel, a, out, topk, ctas, (const float*)partials);
+}
+
+}  // namespace spin

@@ -58,6 +58,9 @@ cudaError_t launch_kv8_append(const Kv8Args& a, const RopeArgs& r, const Rows& q
                               const Rows& v, int sm_count, cudaStream_t st);
 cudaError_t launch_kv8_attend(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const int32_t* sel,
                               int topk, void* workspace, int sm_count, cudaStream_t st);
+cudaError_t launch_kv8_prefill(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const int32_t* sel,
+                               int topk, float* partials, int sm_count, cudaStream_t st);
 int64_t kv8_attend_workspace(const Kv8Args& a);
+int64_t kv8_prefill_workspace();
 
 }  // namespace spin

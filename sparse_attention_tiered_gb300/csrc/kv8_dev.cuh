@@ -167,15 +167,14 @@ struct Place {
   int64_t before;  // places of the requests before it
 };
 
-// The request of place `at(total)` for every thread of the CTA (n threads, scratch of 32 + 4 words
-// each of 8 bytes). Each thread adds up a run of requests; the one whose run holds the place walks it.
-template <typename At>
-__device__ __forceinline__ Place locate(const Kv8Args& a, int first_row, int rows, int topk, bool report, int64_t* scratch, At at) {
+// The request of place `at(total)` for every thread of the CTA, where request b has weight(b) places
+// (scratch: 34 words). Each thread adds up a run of requests; the one whose run holds the place walks it.
+template <typename Weight, typename At>
+__device__ __forceinline__ Place locate(int requests, int64_t* scratch, Weight weight, At at) {
   const int tid = threadIdx.x, n = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = n >> 5;
-  const int run = (a.B + n - 1) / n, b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
+  const int run = (requests + n - 1) / n, b0 = min(requests, tid * run), b1 = min(requests, b0 + run);
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += unit_of(a, b, first_row, rows, topk, report).weight;
-  mine *= a.Hkv;
+  for (int b = b0; b < b1; ++b) mine += weight(b, true);
   int64_t sum = mine;
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
@@ -191,14 +190,14 @@ __device__ __forceinline__ Place locate(const Kv8Args& a, int first_row, int row
   }
   const int64_t lo = base + sum - mine, want = at(total);
   if (tid == 0) {
-    scratch[32] = a.B;
+    scratch[32] = requests;
     scratch[33] = total;
   }
   __syncthreads();
   if (want >= lo && want < lo + mine) {
     int64_t before = lo;
     for (int b = b0; b < b1; ++b) {
-      const int64_t m = (int64_t)unit_of(a, b, first_row, rows, topk, false).weight * a.Hkv;
+      const int64_t m = weight(b, false);
       if (want < before + m) {
         scratch[32] = b;
         scratch[33] = before;
@@ -209,6 +208,26 @@ __device__ __forceinline__ Place locate(const Kv8Args& a, int first_row, int row
   }
   __syncthreads();
   return Place{total, (int)scratch[32], scratch[33]};
+}
+
+// The first place of CTA c's share of n, and the CTA whose share has place x.
+__device__ __forceinline__ int64_t share_start(int64_t total, int c, int n) { return total * c / n; }
+__device__ __forceinline__ int share_of(int64_t total, int64_t x, int n) { return (int)(((x + 1) * n - 1) / total); }
+
+// What a CTA does of the unit that holds the place `at` of its request (or row block), with `left` of its share to go.
+struct Part {
+  int h, from, to;  // items [from, to) of head h; none where from >= to
+  int64_t took;
+};
+
+__device__ __forceinline__ Part part_of(const Unit& u, int64_t at, int64_t left) {
+  Part x;
+  x.h = (int)(at / u.weight);
+  const int f = (int)(at - (int64_t)x.h * u.weight), t = (int)min((int64_t)u.weight, f + left);
+  x.took = t - f;
+  x.from = max(0, f - kUnitCost);
+  x.to = max(0, t - kUnitCost);
+  return x;
 }
 
 }  // namespace kv8
