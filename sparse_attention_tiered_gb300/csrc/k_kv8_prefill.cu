@@ -12,6 +12,7 @@
 //             more than 2^8, which is rare, so that O stays where it is; rows stored at the end;
 //   8-11      codes from HBM to fp16 in shared memory, 128-byte swizzled. A page's loads are in
 //             registers one step ahead of their use, so no shared memory holds codes;
+//   13        walks the CTA's share of the work and announces its segments;
 //   12        issues the products: P_0 V, S_0, P_1 V, S_1 of each step, so that one tile's softmax
 //             runs under the other's products.
 // Tensor memory: O_0, O_1, S_0, S_1 of 128 columns each. Shared memory: Q_0, Q_1 and two steps of
@@ -19,6 +20,8 @@
 //
 // The arithmetic is that of the few-row kernel: z = score * k * log2(e) + log2(v) per page, weights
 // 2^(z - M + 6) with M at most 2^8 below the maximum, the softmax sum takes weight / v.
+#include <type_traits>
+
 #include "kv8_join.cuh"
 
 namespace spin {
@@ -31,11 +34,23 @@ constexpr int kTile = 128;
 constexpr int kBlockRows = 2 * kTile;
 constexpr int kStep = 2 * kPart;  // tokens of a step
 constexpr int kThreads = 512;
-constexpr int kLoadWarp = 8, kMmaWarp = 12;
+constexpr int kLoadWarp = 8, kMmaWarp = 12, kPlanWarp = 13;
+constexpr int kSegReaders = 13;  // warps that read a segment: softmax, loaders, products
 constexpr float kUp = 6.f;     // weights reach 2^kUp times ..
 constexpr float kSlack = 8.f;  // .. 2^kSlack before the output is rescaled
 constexpr int kPlane = 32768;  // K or V: [2 planes of 64 dimensions][2 steps][128 tokens][128 bytes]
 constexpr uint32_t kColO = 0, kColS = 256;
+
+// One row block of one head, and the part of its items that this CTA does.
+struct Segment {
+  Unit u;
+  int b, h, first_row, from, to;
+  int steps;           // of two items each; 0: the share is done
+  int limit0, limit1;  // items that a tile's last row may see; 0: the tile has no rows
+  __device__ __forceinline__ int limit(int tile) const { return tile ? limit1 : limit0; }
+  __device__ __forceinline__ bool active(int tile, int step) const { return from + 2 * step < min(to, limit(tile)); }
+};
+constexpr int kSegments = 4;  // announced ahead
 
 // What the softmax warps have to know of a step's tokens, by groups of 16.
 struct StepMeta {
@@ -46,8 +61,10 @@ struct StepMeta {
 };
 
 struct Smem {
+  uint64_t seg_full[kSegments], seg_empty[kSegments];
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2];
   StepMeta meta[4];  // by step mod 4: a softmax warp may be two steps behind the loaders, which run one ahead
+  Segment segs[kSegments];
   int64_t scratch[36];
   uint32_t tmem;
   int abort;
@@ -120,48 +137,43 @@ __device__ __forceinline__ void settle32(uint32_t* r) {
   asm volatile("" : SPIN_R8(r, 0), SPIN_R8(r, 8), SPIN_R8(r, 16), SPIN_R8(r, 24));
 }
 
-// One row block of one head, and the part of its items that this CTA does.
-struct Segment {
-  Unit u;
-  int first_row, h, from, to;
-  int steps;       // of two items each
-  int limit[2];    // items that a tile's last row may see; 0: the tile has no rows
-  __device__ __forceinline__ bool active(int tile, int step) const { return from + 2 * step < min(to, limit[tile]); }
-};
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : SPIN_W8(r, 0), SPIN_W8(r, 8)
+      : "r"(addr)
+      : "memory");
+}
 
-// Walks the CTA's share; every role does so for itself, in step.
-struct Walk {
-  int b, block;
-  int64_t at, stop, before;
-  __device__ __forceinline__ bool next(const Kv8Args& a, int topk, Segment& s) {
-    while (at < stop) {
-      const Unit u = unit_of(a, b, block * kBlockRows, kBlockRows, topk, false);
-      if (u.weight == 0) {  // the request has no more rows
-        ++b;
-        block = 0;
-        if (b >= a.B) return false;
-        continue;
-      }
-      if (at >= before + (int64_t)u.weight * a.Hkv) {
-        before += (int64_t)u.weight * a.Hkv;
-        ++block;
-        continue;
-      }
-      const Part x = part_of(u, at - before, stop - at);
-      at += x.took;
-      if (x.from >= x.to) continue;
-      s.u = u;
-      s.first_row = block * kBlockRows;
-      s.h = x.h;
-      s.from = x.from;
-      s.to = x.to;
-      s.steps = (x.to - x.from + 1) / 2;
-      for (int t = 0; t < 2; ++t) s.limit[t] = unit_of(a, b, s.first_row + t * kTile, kTile, topk, false).items;
-      return true;
-    }
-    return false;
-  }
-};
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::SPIN_I8(r, 0),
+      SPIN_I8(r, 8), "r"(addr)
+      : "memory");
+}
+
+__device__ __forceinline__ void settle16(uint32_t* r) { asm volatile("" : SPIN_R8(r, 0), SPIN_R8(r, 8)); }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t twice(float x) { return pack2(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
 
 __device__ __forceinline__ int64_t blocks_weight(const Kv8Args& a, int b, int topk, bool report) {
   int64_t sum = 0;
@@ -190,6 +202,10 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
   const int ctas = gridDim.x, cta = blockIdx.x;
 
   if (tid == 0) {
+    for (int i = 0; i < kSegments; ++i) {
+      mbar_init(smem_u32(&sm.seg_full[i]), 1);
+      mbar_init(smem_u32(&sm.seg_empty[i]), kSegReaders);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.q_full[i]), 4);
       mbar_init(smem_u32(&sm.k_full[i]), 4);
@@ -214,9 +230,14 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       [&](int64_t total) { return share_start(total, cta, ctas); });
   tmem_after();
   const uint32_t tmem = sm.tmem;
-  Walk walk{pl.b, 0, share_start(pl.total, cta, ctas), share_start(pl.total, cta + 1, ctas), pl.before};
-  Segment s;
   bool ok = true;
+  uint32_t seg = 0;  // segments read so far
+  auto next = [&]() {  // the next segment is there and is not the end
+    ok = ok && mbar_wait(smem_u32(&sm.seg_full[seg % kSegments]), seg / kSegments & 1, abort, a.err);
+    ok = __all_sync(__activemask(), ok);
+    return ok && sm.segs[seg % kSegments].steps > 0;
+  };
+  auto leave = [&]() { mbar_arrive(smem_u32(&sm.seg_empty[seg++ % kSegments])); };
   // 512 threads x 128 registers at launch = 256 x 176 + 128 x 112 + 128 x 48.
 
   if (warp < kLoadWarp) {
@@ -227,13 +248,14 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
     const uint32_t S = lanes + kColS + tile * kTile, O = lanes + kColO + tile * kTile;
     uint32_t done = 0;    // steps of this tile so far
     uint32_t count = 0;   // steps of the CTA so far
-    while (walk.next(a, topk, s)) {
+    while (next()) {
+      const Segment& s = sm.segs[seg % kSegments];
       const int row = s.first_row + tile * kTile + quad * 32 + lane;
       const bool mine = row < s.u.n_new * a.G;
       const int i = row / a.G, head = s.h * a.G + row - i * a.G;
       const int see = mine ? s.u.past + i + 1 : 0x7fffffff;  // rows that are not there see all: no masks for them
       float qs = 1.f;
-      const int my_steps = s.limit[tile] ? max(0, (min(s.to, s.limit[tile]) - s.from + 1) / 2) : 0;
+      const int my_steps = s.limit(tile) ? max(0, (min(s.to, s.limit(tile)) - s.from + 1) / 2) : 0;
       if (my_steps) {
         // the row: 64 words, its largest element, fp16 with the factor in qs; scale's sign goes here
         const uint4* src = reinterpret_cast<const uint4*>(q.p + (int64_t)(s.u.row0 + i) * q.ts + (int64_t)head * q.hs);
@@ -275,55 +297,55 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           if (!ok) continue;
         }
         tmem_after();
+        // Of each page: the tokens that the row sees, and whether all rows see all of them.
+        const int vis0 = min(see - me.pos[0], me.count[0]), vis1 = halves == 2 ? min(see - me.pos[1], me.count[1]) : 0;
+        const bool plain0 = __all_sync(0xffffffffu, vis0 >= kPart) && (me.bad[0] | me.bad[1]) == 0;
+        const bool plain1 = __all_sync(0xffffffffu, vis1 >= kPart) && (me.bad[2] | me.bad[3]) == 0;
         uint32_t x[64];
-        // the largest z of the row's visible tokens, page by page
         float top = -INFINITY;
-        int vis[2];
-        bool plain[2];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          vis[hf] = hf < halves ? min(see - me.pos[hf], me.count[hf]) : 0;
-          plain[hf] = __all_sync(0xffffffffu, vis[hf] >= kPart) && (me.bad[2 * hf] | me.bad[2 * hf + 1]) == 0;
-        }
-        // Scores of a page into x: of all tokens where `plain`, else the final z with -inf for hidden tokens.
-        auto fetch = [&](int hf) {
+        // Scores of a page into x; where not `plain` the final z, with -inf for hidden tokens.
+        auto fetch = [&](auto page) {
+          constexpr int hf = decltype(page)::value;
           tmem_load32(S + hf * kPart, x);
           tmem_load32(S + hf * kPart + 32, x + 32);
           tmem_loaded();
           settle32(x);
           settle32(x + 32);
-          if (!plain[hf]) {
+          if (!(hf ? plain1 : plain0)) {
+            const int vis = hf ? vis1 : vis0;
 #pragma unroll
             for (int c = 0; c < kPart; ++c) {
-              const int grp = hf * 4 + c / 16;
-              float z = fmaf(__uint_as_float(x[c]), me.kfac[grp] * qs, me.vlog[grp]);
+              float z = fmaf(__uint_as_float(x[c]), me.kfac[hf * 4 + c / 16] * qs, me.vlog[hf * 4 + c / 16]);
               if (me.bad[hf * 2 + c / 32] >> (c & 31) & 1u) z = __uint_as_float(0x7fc00000u);
-              x[c] = __float_as_uint(c < vis[hf] ? z : -INFINITY);
+              x[c] = __float_as_uint(c < vis ? z : -INFINITY);
             }
           }
         };
-        auto largest = [&](int hf) {
+        auto largest = [&](auto page) {
+          constexpr int hf = decltype(page)::value;
 #pragma unroll
           for (int grp = 0; grp < 4; ++grp) {
-            float m = __uint_as_float(x[grp * 16]);
+            float m = __uint_as_float(x[grp * 16]), n = __uint_as_float(x[grp * 16 + 1]);
 #pragma unroll
-            for (int c = 1; c < 16; ++c) m = fmaxf(m, __uint_as_float(x[grp * 16 + c]));
-            top = fmaxf(top, plain[hf] ? fmaf(m, me.kfac[hf * 4 + grp] * qs, me.vlog[hf * 4 + grp]) : m);
+            for (int c = 2; c < 16; c += 4) {
+              m = fmaxf(fmaxf(m, __uint_as_float(x[grp * 16 + c])), c + 2 < 16 ? __uint_as_float(x[grp * 16 + c + 2]) : m);
+              n = fmaxf(fmaxf(n, __uint_as_float(x[grp * 16 + c + 1])), c + 3 < 16 ? __uint_as_float(x[grp * 16 + c + 3]) : n);
+            }
+            m = fmaxf(m, n);
+            if (hf ? plain1 : plain0) m = fmaf(m, me.kfac[hf * 4 + grp] * qs, me.vlog[hf * 4 + grp]);
+            top = fmaxf(top, m);
           }
         };
+        const std::integral_constant<int, 0> first{};
+        const std::integral_constant<int, 1> second{};
+        fetch(first);
+        largest(first);
         if (halves == 2) {
-          fetch(0);
-          largest(0);
+          fetch(second);
+          largest(second);
         }
-        const int last = halves - 1;
-        fetch(last);
-        largest(last);
-        const float m2 = fmaxf(M, top);
-        if (m2 > M + kSlack || (M == -INFINITY && m2 != -INFINITY)) {
-          top = m2;
-        } else {
-          top = M;
-        }
+        top = fmaxf(M, top);
+        if (!(top > M + kSlack || (M == -INFINITY && top != -INFINITY))) top = M;
         if (__any_sync(0xffffffffu, top != M)) {
           const float f = top == M ? 1.f : ex2(M - top);  // 0 for a row that saw nothing yet
           if (step > 0) {  // rare after the first step: the output so far, once its products are done
@@ -331,14 +353,15 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) continue;
             tmem_after();
-            for (int c = 0; c < kD; c += 32) {
-              uint32_t y[32];
-              tmem_load32(O + c, y);
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 16) {
+              uint32_t y[16];
+              tmem_load16(O + c, y);
               tmem_loaded();
-              settle32(y);
+              settle16(y);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
-              tmem_store32(O + c, y);
+              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+              tmem_store16(O + c, y);
             }
             tmem_stored();
           }
@@ -346,31 +369,36 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           M = top;
         }
         const float ref = (M == -INFINITY ? 0.f : M) - kUp;
-        auto weigh = [&](int hf) {  // fp16 weights of a page, into the first 32 columns of its scores
+        auto weigh = [&](auto page) {  // fp16 weights of a page, into the first 32 columns of its scores
+          constexpr int hf = decltype(page)::value;
           uint32_t p[32];
 #pragma unroll
           for (int grp = 0; grp < 4; ++grp) {
-            const float k = plain[hf] ? me.kfac[hf * 4 + grp] * qs : 1.f;
-            const float c0 = plain[hf] ? me.vlog[hf * 4 + grp] - ref : -ref;
-            float sum0 = 0.f, sum1 = 0.f;
+            const bool plain = hf ? plain1 : plain0;
+            const uint64_t k2 = twice(plain ? me.kfac[hf * 4 + grp] * qs : 1.f);
+            const uint64_t c2 = twice(plain ? me.vlog[hf * 4 + grp] - ref : -ref);
+            uint64_t sum2 = 0;
 #pragma unroll
             for (int c = 0; c < 16; c += 2) {
-              const float y0 = ex2(fmaf(__uint_as_float(x[grp * 16 + c]), k, c0));
-              const float y1 = ex2(fmaf(__uint_as_float(x[grp * 16 + c + 1]), k, c0));
-              sum0 += y0;
-              sum1 += y1;
+              float y0, y1;
+              unpack2(fma2(pack2(x[grp * 16 + c], x[grp * 16 + c + 1]), k2, c2), y0, y1);
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              sum2 = add2(sum2, pack2(__float_as_uint(y0), __float_as_uint(y1)));
               p[grp * 8 + c / 2] = pack_half2(y0, y1);
             }
-            const float sum = sum0 + sum1;
+            float s0, s1;
+            unpack2(sum2, s0, s1);
+            const float sum = s0 + s1;
             L += sum == 0.f ? 0.f : sum * me.vinv[hf * 4 + grp];  // nothing of a NaN page that the row does not see
           }
           tmem_store32(S + hf * kPart, p);
         };
-        weigh(last);
         if (halves == 2) {
-          fetch(0);
-          weigh(0);
+          weigh(second);
+          fetch(first);
         }
+        weigh(first);
         tmem_stored();
         tmem_before();
         __syncwarp();
@@ -379,7 +407,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       count += s.steps;
 
       // ---- the row's end ----
-      if (s.limit[tile]) {
+      if (s.limit(tile)) {
         if (my_steps) {
           ok = ok && mbar_wait(smem_u32(&sm.pv_done[tile]), (done - 1) & 1, abort, a.err);
           ok = __all_sync(0xffffffffu, ok);
@@ -418,6 +446,9 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           tmem_before();
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[seg % kSegments]));
+      ++seg;
     }
   } else if (warp < kMmaWarp) {
     // ------------------------------ loaders ------------------------------
@@ -425,8 +456,9 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
     asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
     const int w4 = warp - kLoadWarp, r4 = lane >> 3, c8 = lane & 7;
     uint32_t count = 0;
-    while (walk.next(a, topk, s)) {
-      const int64_t unit = (int64_t)walk.b * a.Hkv + s.h;
+    while (next()) {
+      const Segment& s = sm.segs[seg % kSegments];
+      const int64_t unit = (int64_t)s.b * a.Hkv + s.h;
       int id = -1, pos = -1, id_base = s.from;
       float2 sc = make_float2(1.f, 1.f);
       auto look = [&](int first) {  // page ids and scales of 32 items
@@ -447,8 +479,8 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           }
         }
       };
-      uint4 raw[8];  // keys or values of two pages, four rows each
-      auto load = [&](int step, int half) {
+      uint4 keys[8], vals[8];  // of two pages, four rows each: a step ahead of their use
+      auto load = [&](uint4 (&raw)[8], int step, int half) {
 #pragma unroll
         for (int pg = 0; pg < 2; ++pg) {
           const int it = s.from + 2 * step + pg;
@@ -461,7 +493,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         }
       };
       // codes in raw -> fp16 rows of page pg in the operand at `at`
-      auto put_page = [&](uint32_t at, int pg) {
+      auto put_page = [&](const uint4 (&raw)[8], uint32_t at, int pg) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int row = w4 * 16 + x * 4 + r4;
@@ -475,41 +507,40 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       // The tail's keys or values as page pg: the warp's 16 rows scaled by a power of two.
       auto put_tail = [&](uint32_t at, int pg, int half, StepMeta& me) {
         const uint16_t* src = a.tails + unit * kPageElems + half * kPart * kD;
-        uint4 v[4][2];
-        uint32_t top = 0, wrong = 0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        // Twice over the rows (they are in L1 by then), to hold no more than one of them.
+        auto row_of = [&](int x, int y, uint32_t& wrong) {
           const int row = w4 * 16 + x * 4 + r4;
+          uint4 t = make_uint4(0, 0, 0, 0);
+          if (row < s.u.tail) t = *(reinterpret_cast<const uint4*>(src + row * kD + c8 * 16) + y);
+          uint32_t* tt = reinterpret_cast<uint32_t*>(&t);
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            uint4 t = make_uint4(0, 0, 0, 0);
-            if (row < s.u.tail) t = __ldcg(reinterpret_cast<const uint4*>(src + row * kD + c8 * 16) + y);
-            uint32_t* tt = reinterpret_cast<uint32_t*>(&t);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const bool lo = (tt[e] & 0x7f80u) == 0x7f80u, hi = (tt[e] & 0x7f800000u) == 0x7f800000u;
-              if (lo) tt[e] &= 0xffff0000u;
-              if (hi) tt[e] &= 0x0000ffffu;
-              if (lo || hi) wrong |= 1u << (x * 4 + r4);
-              top = __vmaxu2(top, tt[e] & 0x7fff7fffu);
-            }
-            v[x][y] = t;
+          for (int e = 0; e < 4; ++e) {
+            const bool lo = (tt[e] & 0x7f80u) == 0x7f80u, hi = (tt[e] & 0x7f800000u) == 0x7f800000u;
+            if (lo) tt[e] &= 0xffff0000u;
+            if (hi) tt[e] &= 0x0000ffffu;
+            if (lo || hi) wrong |= 1u << (x * 4 + r4);
           }
+          return t;
+        };
+        uint32_t top = 0, wrong = 0;
+#pragma unroll 1
+        for (int x = 0; x < 8; ++x) {
+          const uint4 t = row_of(x >> 1, x & 1, wrong);
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(t.x & 0x7fff7fffu, t.y & 0x7fff7fffu), __vmaxu2(t.z & 0x7fff7fffu, t.w & 0x7fff7fffu)));
         }
         top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
         wrong = __reduce_or_sync(0xffffffffu, wrong);
         const int e = half_exponent(top);
         const float f = pow2(15 - e);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int row = w4 * 16 + x * 4 + r4;
-          const uint32_t dst = at + (c8 >> 2) * kPlane + (pg * kPart + row) * 128;
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-            sts128(dst + ((((c8 & 3) * 2 + y) ^ (row & 7)) << 4), pack_half2(lo_f(v[x][y].x) * f, hi_f(v[x][y].x) * f),
-                   pack_half2(lo_f(v[x][y].y) * f, hi_f(v[x][y].y) * f), pack_half2(lo_f(v[x][y].z) * f, hi_f(v[x][y].z) * f),
-                   pack_half2(lo_f(v[x][y].w) * f, hi_f(v[x][y].w) * f));
+#pragma unroll 1
+        for (int x = 0; x < 8; ++x) {
+          const uint4 t = row_of(x >> 1, x & 1, wrong);
+          const int row = w4 * 16 + (x >> 1) * 4 + r4;
+          sts128(at + (c8 >> 2) * kPlane + (pg * kPart + row) * 128 + ((((c8 & 3) * 2 + (x & 1)) ^ (row & 7)) << 4),
+                 pack_half2(lo_f(t.x) * f, hi_f(t.x) * f), pack_half2(lo_f(t.y) * f, hi_f(t.y) * f),
+                 pack_half2(lo_f(t.z) * f, hi_f(t.z) * f), pack_half2(lo_f(t.w) * f, hi_f(t.w) * f));
         }
+        wrong = __reduce_or_sync(0xffffffffu, wrong);
         if (lane == 0) {
           if (half == 0) {
             me.kfac[pg * 4 + w4] = fabsf(scale) * kLog2e * pow2(e - 15);
@@ -520,17 +551,18 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           if (wrong) atomicOr(&me.bad[pg * 2 + (w4 >> 1)], wrong << (16 * (w4 & 1)));
         }
       };
-      auto put = [&](uint32_t at, int step, int half, StepMeta& me) {
+      auto put = [&](const uint4 (&raw)[8], uint32_t at, int step, int half, StepMeta& me) {
 #pragma unroll
         for (int pg = 0; pg < 2; ++pg) {
           const int it = s.from + 2 * step + pg;
           if (it >= s.to) break;
-          if (it < s.u.pages) put_page(at, pg);
+          if (it < s.u.pages) put_page(raw, at, pg);
           else put_tail(at, pg, half, me);
         }
       };
       look(s.from);
-      load(0, 0);
+      load(keys, 0, 0);
+      load(vals, 0, 1);
       for (int step = 0; step < s.steps; ++step, ++count) {
         const uint32_t slot = count & 1, parity = count >> 1 & 1;
         StepMeta& me = sm.meta[count & 3];
@@ -568,30 +600,33 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           }
           // (the flags of a tail are set by its warps after they are cleared: one barrier)
           asm volatile("bar.sync 2, 128;" ::: "memory");
-          put(sk + slot * 16384, step, 0, me);
+          put(keys, sk + slot * 16384, step, 0, me);
           proxy_fence();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sm.k_full[slot]));
         } else {
           asm volatile("bar.sync 2, 128;" ::: "memory");
         }
-        load(step, 1);
+        if (step + 1 < s.steps) load(keys, step + 1, 0);
         ok = ok && mbar_wait(smem_u32(&sm.v_empty[slot]), parity ^ 1, abort, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
-          put(sv + slot * 16384, step, 1, me);
+          put(vals, sv + slot * 16384, step, 1, me);
           proxy_fence();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sm.v_full[slot]));
         }
-        if (step + 1 < s.steps) load(step + 1, 0);
+        if (step + 1 < s.steps) load(vals, step + 1, 1);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[seg % kSegments]));
+      ++seg;
     }
   } else {
     // ------------------------------ products ------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == kMmaWarp && lane == 0) {
-      uint32_t count = 0, segs[2] = {0, 0}, done[2] = {0, 0};
+      uint32_t count = 0, q_phase = 0, p_phase = 0;  // phases: a bit per tile
       auto scores = [&](int tile, uint32_t c, int pages) {
         const uint32_t d = tmem + kColS + tile * kTile;
         const uint32_t at = sq + tile * (kTile * kD * 2), bt = sk + (c & 1) * 16384;
@@ -601,12 +636,14 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
                  operand(bt + (k >> 2) * kPlane + (k & 3) * 32, 16, 1024), pages == 2 ? shape(kStep, false) : shape(kPart, false), k > 0);
         mma_commit(smem_u32(&sm.s_full[tile]));
       };
-      while (walk.next(a, topk, s)) {
+      while (next()) {
+        const Segment& s = sm.segs[seg % kSegments];
         auto pages_of = [&](int step) { return min(2, s.to - s.from - 2 * step); };
         ok = ok && mbar_wait(smem_u32(&sm.k_full[count & 1]), count >> 1 & 1, abort, a.err);
         for (int t = 0; t < 2; ++t)
           if (s.active(t, 0)) {
-            ok = ok && mbar_wait(smem_u32(&sm.q_full[t]), segs[t]++ & 1, abort, a.err);
+            ok = ok && mbar_wait(smem_u32(&sm.q_full[t]), q_phase >> t & 1, abort, a.err);
+            q_phase ^= 1u << t;
             tmem_after();
             if (ok) scores(t, count, pages_of(0));
           }
@@ -618,7 +655,8 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           if (more) ok = ok && mbar_wait(smem_u32(&sm.k_full[(count + 1) & 1]), (count + 1) >> 1 & 1, abort, a.err);
           for (int t = 0; t < 2; ++t) {
             if (s.active(t, step)) {
-              ok = ok && mbar_wait(smem_u32(&sm.p_full[t]), done[t]++ & 1, abort, a.err);
+              ok = ok && mbar_wait(smem_u32(&sm.p_full[t]), p_phase >> t & 1, abort, a.err);
+              p_phase ^= 1u << t;
               tmem_after();
               if (ok) {
                 const uint32_t d = tmem + kColO + t * kTile, p = tmem + kColS + t * kTile;
@@ -633,11 +671,51 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           }
           if (more && ok) mma_commit(smem_u32(&sm.k_empty[(count + 1) & 1]));
         }
+        leave();
       }
       // The last arrivals have landed before the CTA's shared memory goes.
       if (count > 0) {
         ok = ok && mbar_wait(smem_u32(&sm.k_empty[(count - 1) & 1]), (count - 1) >> 1 & 1, abort, a.err);
         ok = ok && mbar_wait(smem_u32(&sm.v_empty[(count - 1) & 1]), (count - 1) >> 1 & 1, abort, a.err);
+      }
+    }
+    if (warp == kPlanWarp && lane == 0) {
+      int b = pl.b, block = 0;
+      int64_t at = share_start(pl.total, cta, ctas), before = pl.before;
+      const int64_t stop = share_start(pl.total, cta + 1, ctas);
+      for (bool more = true; more && ok; ++seg) {
+        Segment s;
+        s.steps = 0;
+        while (at < stop && b < a.B) {
+          s.u = unit_of(a, b, block * kBlockRows, kBlockRows, topk, false);
+          if (s.u.weight == 0) {  // the request has no more rows
+            ++b;
+            block = 0;
+            continue;
+          }
+          if (at >= before + (int64_t)s.u.weight * a.Hkv) {
+            before += (int64_t)s.u.weight * a.Hkv;
+            ++block;
+            continue;
+          }
+          const Part x = part_of(s.u, at - before, stop - at);
+          at += x.took;
+          if (x.from >= x.to) continue;
+          s.b = b;
+          s.h = x.h;
+          s.first_row = block * kBlockRows;
+          s.from = x.from;
+          s.to = x.to;
+          s.steps = (x.to - x.from + 1) / 2;
+          s.limit0 = unit_of(a, b, s.first_row, kTile, topk, false).items;
+          s.limit1 = unit_of(a, b, s.first_row + kTile, kTile, topk, false).items;
+          break;
+        }
+        more = s.steps > 0;
+        ok = ok && mbar_wait(smem_u32(&sm.seg_empty[seg % kSegments]), (seg / kSegments & 1) ^ 1, abort, a.err);
+        if (!ok) break;
+        sm.segs[seg % kSegments] = s;
+        mbar_arrive(smem_u32(&sm.seg_full[seg % kSegments]));
       }
     }
     __syncwarp();
