@@ -20,8 +20,6 @@
 //
 // The arithmetic is that of the few-row kernel: z = score * k * log2(e) + log2(v) per page, weights
 // 2^(z - M + 6) with M at most 2^8 below the maximum, the softmax sum takes weight / v.
-#include <type_traits>
-
 #include "kv8_join.cuh"
 
 namespace spin {
@@ -56,7 +54,7 @@ constexpr int kSegments = 4;  // announced ahead
 struct StepMeta {
   float kfac[8];       // score factor, without the row's
   float vlog[8], vinv[8];
-  uint32_t bad[4];     // bit per token: it holds a value that is not finite
+  uint32_t bad[4];     // bit per token: a row that sees it is NaN (the other numbers are finite all the same)
   int pos[2], count[2];  // position of each page's first token, tokens it holds (0: no page)
 };
 
@@ -255,6 +253,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       const int i = row / a.G, head = s.h * a.G + row - i * a.G;
       const int see = mine ? s.u.past + i + 1 : 0x7fffffff;  // rows that are not there see all: no masks for them
       float qs = 1.f;
+      bool poison = false;  // the row's result is NaN
       const int my_steps = s.limit(tile) ? max(0, (min(s.to, s.limit(tile)) - s.from + 1) / 2) : 0;
       if (my_steps) {
         // the row: 64 words, its largest element, fp16 with the factor in qs; scale's sign goes here
@@ -270,7 +269,8 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         top = max(top & 0xffffu, top >> 16);
         const int e = half_exponent(top);
         const float f = scale < 0.f ? -pow2(15 - e) : pow2(15 - e);
-        qs = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e - 15);
+        qs = top >= 0x7f80u ? 1.f : pow2(e - 15);
+        poison = top >= 0x7f80u;
         const int r = quad * 32 + lane;
         const uint32_t dst = sq + tile * (kTile * kD * 2) + r * 128;
 #pragma unroll
@@ -297,52 +297,40 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           if (!ok) continue;
         }
         tmem_after();
-        // Of each page: the tokens that the row sees, and whether all rows see all of them.
-        const int vis0 = min(see - me.pos[0], me.count[0]), vis1 = halves == 2 ? min(see - me.pos[1], me.count[1]) : 0;
-        const bool plain0 = __all_sync(0xffffffffu, vis0 >= kPart) && (me.bad[0] | me.bad[1]) == 0;
-        const bool plain1 = __all_sync(0xffffffffu, vis1 >= kPart) && (me.bad[2] | me.bad[3]) == 0;
         uint32_t x[64];
         float top = -INFINITY;
-        // Scores of a page into x; where not `plain` the final z, with -inf for hidden tokens.
-        auto fetch = [&](auto page) {
-          constexpr int hf = decltype(page)::value;
+        // Scores of a page into x; -inf for tokens that the row does not see, where there are any in the warp.
+        auto fetch = [&](int hf) {
           tmem_load32(S + hf * kPart, x);
           tmem_load32(S + hf * kPart + 32, x + 32);
+          const int vis = min(see - me.pos[hf], me.count[hf]);
           tmem_loaded();
           settle32(x);
           settle32(x + 32);
-          if (!(hf ? plain1 : plain0)) {
-            const int vis = hf ? vis1 : vis0;
+          if (__any_sync(0xffffffffu, vis < kPart)) {
 #pragma unroll
-            for (int c = 0; c < kPart; ++c) {
-              float z = fmaf(__uint_as_float(x[c]), me.kfac[hf * 4 + c / 16] * qs, me.vlog[hf * 4 + c / 16]);
-              if (me.bad[hf * 2 + c / 32] >> (c & 31) & 1u) z = __uint_as_float(0x7fc00000u);
-              x[c] = __float_as_uint(c < vis ? z : -INFINITY);
-            }
+            for (int c = 0; c < kPart; ++c) x[c] = c < vis ? x[c] : 0xff800000u;
           }
+          return vis;
         };
-        auto largest = [&](auto page) {
-          constexpr int hf = decltype(page)::value;
+        // The factor of a group's scores; not 0, which would make NaN of a hidden token's -inf.
+        auto factor = [&](int grp) { return fmaxf(me.kfac[grp] * qs, 1e-37f); };
+#pragma unroll 1
+        for (int hf = 0; hf < halves; ++hf) {
+          const int vis = fetch(hf);
+          const uint32_t b0 = me.bad[2 * hf], b1 = me.bad[2 * hf + 1];
+          if (b0 | b1) poison |= ((vis < 32 ? b0 & ((1u << max(vis, 0)) - 1u) : b0) | (vis < 64 ? b1 & ((1u << max(vis - 32, 0)) - 1u) : b1)) != 0;
 #pragma unroll
           for (int grp = 0; grp < 4; ++grp) {
             float m = __uint_as_float(x[grp * 16]), n = __uint_as_float(x[grp * 16 + 1]);
 #pragma unroll
-            for (int c = 2; c < 16; c += 4) {
-              m = fmaxf(fmaxf(m, __uint_as_float(x[grp * 16 + c])), c + 2 < 16 ? __uint_as_float(x[grp * 16 + c + 2]) : m);
-              n = fmaxf(fmaxf(n, __uint_as_float(x[grp * 16 + c + 1])), c + 3 < 16 ? __uint_as_float(x[grp * 16 + c + 3]) : n);
+            for (int c = 2; c < 14; c += 4) {
+              m = fmaxf(fmaxf(m, __uint_as_float(x[grp * 16 + c])), __uint_as_float(x[grp * 16 + c + 2]));
+              n = fmaxf(fmaxf(n, __uint_as_float(x[grp * 16 + c + 1])), __uint_as_float(x[grp * 16 + c + 3]));
             }
-            m = fmaxf(m, n);
-            if (hf ? plain1 : plain0) m = fmaf(m, me.kfac[hf * 4 + grp] * qs, me.vlog[hf * 4 + grp]);
-            top = fmaxf(top, m);
+            m = fmaxf(m, fmaxf(n, fmaxf(__uint_as_float(x[grp * 16 + 14]), __uint_as_float(x[grp * 16 + 15]))));
+            top = fmaxf(top, fmaf(m, factor(hf * 4 + grp), me.vlog[hf * 4 + grp]));
           }
-        };
-        const std::integral_constant<int, 0> first{};
-        const std::integral_constant<int, 1> second{};
-        fetch(first);
-        largest(first);
-        if (halves == 2) {
-          fetch(second);
-          largest(second);
         }
         top = fmaxf(M, top);
         if (!(top > M + kSlack || (M == -INFINITY && top != -INFINITY))) top = M;
@@ -369,14 +357,13 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           M = top;
         }
         const float ref = (M == -INFINITY ? 0.f : M) - kUp;
-        auto weigh = [&](auto page) {  // fp16 weights of a page, into the first 32 columns of its scores
-          constexpr int hf = decltype(page)::value;
+#pragma unroll 1
+        for (int hf = halves - 1; hf >= 0; --hf) {  // fp16 weights of a page, into the first 32 columns of its scores
+          if (hf != halves - 1) fetch(hf);
           uint32_t p[32];
 #pragma unroll
           for (int grp = 0; grp < 4; ++grp) {
-            const bool plain = hf ? plain1 : plain0;
-            const uint64_t k2 = twice(plain ? me.kfac[hf * 4 + grp] * qs : 1.f);
-            const uint64_t c2 = twice(plain ? me.vlog[hf * 4 + grp] - ref : -ref);
+            const uint64_t k2 = twice(factor(hf * 4 + grp)), c2 = twice(me.vlog[hf * 4 + grp] - ref);
             uint64_t sum2 = 0;
 #pragma unroll
             for (int c = 0; c < 16; c += 2) {
@@ -389,16 +376,10 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
             }
             float s0, s1;
             unpack2(sum2, s0, s1);
-            const float sum = s0 + s1;
-            L += sum == 0.f ? 0.f : sum * me.vinv[hf * 4 + grp];  // nothing of a NaN page that the row does not see
+            L = fmaf(s0 + s1, me.vinv[hf * 4 + grp], L);
           }
           tmem_store32(S + hf * kPart, p);
-        };
-        if (halves == 2) {
-          weigh(second);
-          fetch(first);
         }
-        weigh(first);
         tmem_stored();
         tmem_before();
         __syncwarp();
@@ -407,6 +388,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       count += s.steps;
 
       // ---- the row's end ----
+      if (poison) L = __uint_as_float(0x7fc00000u);
       if (s.limit(tile)) {
         if (my_steps) {
           ok = ok && mbar_wait(smem_u32(&sm.pv_done[tile]), (done - 1) & 1, abort, a.err);
@@ -552,13 +534,10 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         }
       };
       auto put = [&](const uint4 (&raw)[8], uint32_t at, int step, int half, StepMeta& me) {
-#pragma unroll
-        for (int pg = 0; pg < 2; ++pg) {
-          const int it = s.from + 2 * step + pg;
-          if (it >= s.to) break;
-          if (it < s.u.pages) put_page(raw, at, pg);
-          else put_tail(at, pg, half, me);
-        }
+        const int it = s.from + 2 * step, tail = s.u.pages - it;  // the tail's place, if it is in this step
+        if (tail > 0) put_page(raw, at, 0);
+        if (tail > 1 && it + 1 < s.to) put_page(raw, at, 1);
+        if (tail <= 1 && it + tail < s.to) put_tail(at, tail, half, me);
       };
       look(s.from);
       load(keys, 0, 0);
@@ -592,9 +571,11 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
             const int p = __shfl_sync(0xffffffffu, pos, it - id_base);
             const float kx = __shfl_sync(0xffffffffu, sc.x, it - id_base), vx = __shfl_sync(0xffffffffu, sc.y, it - id_base);
             if (lane == 0) {
-              me.kfac[pg * 4 + w4] = p >= 0 ? kx * fabsf(scale) * kLog2e : 0.f;
-              me.vlog[pg * 4 + w4] = p >= 0 ? scale_log2(vx) : 0.f;
-              me.vinv[pg * 4 + w4] = p >= 0 ? 1.f / vx : 1.f;
+              const bool good = p >= 0 && kx == kx && vx == vx;
+              me.kfac[pg * 4 + w4] = good ? kx * fabsf(scale) * kLog2e : 0.f;
+              me.vlog[pg * 4 + w4] = good ? scale_log2(vx) : 0.f;
+              me.vinv[pg * 4 + w4] = good ? 1.f / vx : 1.f;
+              if ((w4 & 1) == 0 && p >= 0 && !good) me.bad[pg * 2 + (w4 >> 1)] = 0xffffffffu;
               if (w4 == 0) me.count[pg] = p >= 0 ? kPart : 0, me.pos[pg] = max(p, 0);
             }
           }
