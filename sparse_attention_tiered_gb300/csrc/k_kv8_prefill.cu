@@ -10,10 +10,11 @@
 //   0-3, 4-7  softmax of tile 0 and 1, one row a thread: scores out of tensor memory, running maximum,
 //             fp16 weights back into it; the output rescaled only when the maximum has grown by
 //             more than 2^8, which is rare, so that O stays where it is; rows stored at the end;
-//   8-11      codes from HBM to fp16 in shared memory, 128-byte swizzled. A page's loads are in
-//             registers one step ahead of their use, so no shared memory holds codes;
-//   13        walks the CTA's share of the work and announces its segments;
-//   12        issues the products: P_0 V, S_0, P_1 V, S_1 of each step, so that one tile's softmax
+//   8-11      keys from HBM to fp16 in shared memory, 128-byte swizzled. A step's loads are in registers
+//             one step ahead of their use, so no shared memory holds codes;
+//   12-15     values, likewise;
+//   17        walks the CTA's share of the work and announces its segments;
+//   16        issues the products: P_0 V, S_0, P_1 V, S_1 of each step, so that one tile's softmax
 //             runs under the other's products.
 // Tensor memory: O_0, O_1, S_0, S_1 of 128 columns each. Shared memory: Q_0, Q_1 and two steps of
 // K and of V, 32 KB each.
@@ -31,9 +32,9 @@ using namespace kv8;
 constexpr int kTile = 128;
 constexpr int kBlockRows = 2 * kTile;
 constexpr int kStep = 2 * kPart;  // tokens of a step
-constexpr int kThreads = 512;
-constexpr int kLoadWarp = 8, kMmaWarp = 12, kPlanWarp = 13;
-constexpr int kSegReaders = 13;  // warps that read a segment: softmax, loaders, products
+constexpr int kThreads = 640;
+constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16, kPlanWarp = 17;
+constexpr int kSegReaders = 17;  // warps that read a segment: softmax, loaders, products
 constexpr float kUp = 6.f;     // weights reach 2^kUp times ..
 constexpr float kSlack = 8.f;  // .. 2^kSlack before the output is rescaled
 constexpr int kPlane = 32768;  // K or V: [2 planes of 64 dimensions][2 steps][128 tokens][128 bytes]
@@ -51,10 +52,12 @@ struct Segment {
 constexpr int kSegments = 4;  // announced ahead
 
 // What the softmax warps have to know of a step's tokens, by groups of 16.
-struct StepMeta {
+struct alignas(8) StepMeta {
   float kfac[8];       // score factor, without the row's
   float vlog[8], vinv[8];
-  uint32_t bad[4];     // bit per token: a row that sees it is NaN (the other numbers are finite all the same)
+  // Bit per token: a row that sees it is NaN (the other numbers are finite all the same). From the value
+  // loaders only where the page is the tail.
+  uint16_t bad_keys[8], bad_vals[8];
   int pos[2], count[2];  // position of each page's first token, tokens it holds (0: no page)
 };
 
@@ -84,23 +87,39 @@ constexpr uint32_t shape(int n, bool b_rows_depth) {
   return 1u << 4 | (b_rows_depth ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(kTile >> 4) << 24;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// One product of depth 16, issued by the lane that has `leader` set. The whole warp runs the code around it
+// together, with operands' descriptors that are sums of a base and constants: they stay in uniform
+// registers, where an issue from divergent code would move them there for every product.
+template <bool ADD>
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "n"(ADD ? 1 : 0), "r"(leader)
       : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+template <bool ADD>
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "n"(ADD ? 1 : 0), "r"(leader)
       : "memory");
 }
 
 // The barrier is arrived at once all products issued so far are done.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(leader)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r;
 }
 
 __device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -195,7 +214,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sq = smem_u32(base), sk = sq + (uint32_t)kQBytes, sv = sk + (uint32_t)kKvBytes;
   Smem& sm = *reinterpret_cast<Smem*>(base + kQBytes + 2 * kKvBytes);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   volatile int* abort = &sm.abort;
   const int ctas = gridDim.x, cta = blockIdx.x;
 
@@ -232,15 +251,14 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
   uint32_t seg = 0;  // segments read so far
   auto next = [&]() {  // the next segment is there and is not the end
     ok = ok && mbar_wait(smem_u32(&sm.seg_full[seg % kSegments]), seg / kSegments & 1, abort, a.err);
-    ok = __all_sync(__activemask(), ok);
+    ok = __all_sync(0xffffffffu, ok);
     return ok && sm.segs[seg % kSegments].steps > 0;
   };
-  auto leave = [&]() { mbar_arrive(smem_u32(&sm.seg_empty[seg++ % kSegments])); };
-  // 512 threads x 128 registers at launch = 256 x 176 + 128 x 112 + 128 x 48.
+  // 640 threads x 96 registers at launch = 256 x 152 + 256 x 64 + 128 x 48.
 
-  if (warp < kLoadWarp) {
+  if (warp < kKeyWarp) {
     // ------------------------------ softmax, a row a thread ------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     const int tile = warp >> 2, quad = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t S = lanes + kColS + tile * kTile, O = lanes + kColO + tile * kTile;
@@ -318,7 +336,12 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
 #pragma unroll 1
         for (int hf = 0; hf < halves; ++hf) {
           const int vis = fetch(hf);
-          const uint32_t b0 = me.bad[2 * hf], b1 = me.bad[2 * hf + 1];
+          uint2 bad = *reinterpret_cast<const uint2*>(&me.bad_keys[4 * hf]);
+          if (s.from + 2 * step + hf == s.u.pages) {
+            const uint2 more = *reinterpret_cast<const uint2*>(&me.bad_vals[4 * hf]);
+            bad = make_uint2(bad.x | more.x, bad.y | more.y);
+          }
+          const uint32_t b0 = bad.x, b1 = bad.y;
           if (b0 | b1) poison |= ((vis < 32 ? b0 & ((1u << max(vis, 0)) - 1u) : b0) | (vis < 64 ? b1 & ((1u << max(vis - 32, 0)) - 1u) : b1)) != 0;
 #pragma unroll
           for (int grp = 0; grp < 4; ++grp) {
@@ -433,21 +456,27 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       ++seg;
     }
   } else if (warp < kMmaWarp) {
-    // ------------------------------ loaders ------------------------------
-    // Warp w has rows 16 w .. 16 w + 15 of every page; lane (r, c) of them rows r, r + 4 .., bytes 16 c ...
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
-    const int w4 = warp - kLoadWarp, r4 = lane >> 3, c8 = lane & 7;
+    // ------------------------------ loaders: four warps of keys, four of values ------------------------------
+    // Warp w has rows 16 w .. 16 w + 15 of every page. In load x, eight lanes have 64 bytes of two neighbouring
+    // rows each: their 16-byte stores then fall on eight different columns of the swizzle.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    const int half = warp >= kValueWarp ? 1 : 0;
+    const int w4 = warp & 3, c4 = lane & 3, row0 = w4 * 16 + (lane >> 3) * 2 + (lane >> 2 & 1);
+    const uint32_t operand0 = half ? sv : sk;
+    uint64_t* full = half ? sm.v_full : sm.k_full;
+    uint64_t* empty = half ? sm.v_empty : sm.k_empty;
     uint32_t count = 0;
     while (next()) {
       const Segment& s = sm.segs[seg % kSegments];
       const int64_t unit = (int64_t)s.b * a.Hkv + s.h;
+      const int pages = min(s.to, s.u.pages);
       int id = -1, pos = -1, id_base = s.from;
       float2 sc = make_float2(1.f, 1.f);
-      auto look = [&](int first) {  // page ids and scales of 32 items
+      auto look = [&](int first) {  // page ids of 32 items, and for the keys' warps their scales
         id_base = first;
         const int it = first + lane;
         id = pos = -1;
-        if (it < min(s.to, s.u.pages)) {
+        if (it < pages) {
           const int p = topk ? sel[unit * topk + it] : it;
           if (p >= 0 && p < s.u.full) {
             id = a.table[unit * a.max_pages + p];
@@ -456,67 +485,68 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
               id = -1;
             } else {
               pos = p * kPart;
-              sc = *reinterpret_cast<const float2*>(a.scales + 2 * (int64_t)id);
+              if (!half) sc = *reinterpret_cast<const float2*>(a.scales + 2 * (int64_t)id);
             }
           }
         }
       };
-      uint4 keys[8], vals[8];  // of two pages, four rows each: a step ahead of their use
-      auto load = [&](uint4 (&raw)[8], int step, int half) {
+      uint4 raw[8];  // of two pages, four loads each
+      auto load = [&](int step) {  // (32 items are a whole number of steps)
+        const int it = s.from + 2 * step;
+        if (it >= id_base + 32) look(it);
 #pragma unroll
         for (int pg = 0; pg < 2; ++pg) {
-          const int it = s.from + 2 * step + pg;
-          if (it >= id_base + 32) look(it);
-          const int page = it < s.u.pages && it < s.to ? __shfl_sync(0xffffffffu, id, it - id_base) : -1;
-          const uint8_t* src = a.pages + (int64_t)page * kKv8PageBytes + half * kKv8HalfBytes + (w4 * 16 + r4) * kD + c8 * 16;
+          const int page = it + pg < pages ? __shfl_sync(0xffffffffu, id, it + pg - id_base) : -1;
+          const uint8_t* src = a.pages + (int64_t)page * kKv8PageBytes + half * kKv8HalfBytes + row0 * kD + c4 * 16;
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            raw[pg * 4 + x] = page >= 0 ? __ldcg(reinterpret_cast<const uint4*>(src + x * 4 * kD)) : make_uint4(0, 0, 0, 0);
+            raw[pg * 4 + x] = page >= 0 ? __ldcg(reinterpret_cast<const uint4*>(src + (x >> 1) * 8 * kD + (x & 1) * 64))
+                                        : make_uint4(0, 0, 0, 0);
         }
       };
-      // codes in raw -> fp16 rows of page pg in the operand at `at`
-      auto put_page = [&](const uint4 (&raw)[8], uint32_t at, int pg) {
+      auto put_page = [&](uint32_t at, int pg) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int row = w4 * 16 + x * 4 + r4;
+          const int row = row0 + (x >> 1) * 8;
           const uint4 v = raw[pg * 4 + x];
-          const uint32_t dst = at + (c8 >> 2) * kPlane + (pg * kPart + row) * 128;
-          const int ch = (c8 & 3) * 2;
-          sts128(dst + (((ch + 0) ^ (row & 7)) << 4), e4m3x2_half2(v.x, false), e4m3x2_half2(v.x, true), e4m3x2_half2(v.y, false), e4m3x2_half2(v.y, true));
-          sts128(dst + (((ch + 1) ^ (row & 7)) << 4), e4m3x2_half2(v.z, false), e4m3x2_half2(v.z, true), e4m3x2_half2(v.w, false), e4m3x2_half2(v.w, true));
+          const uint32_t dst = at + (x & 1) * kPlane + (pg * kPart + row) * 128;
+          sts128(dst + (((c4 * 2 + 0) ^ (row & 7)) << 4), e4m3x2_half2(v.x, false), e4m3x2_half2(v.x, true),
+                 e4m3x2_half2(v.y, false), e4m3x2_half2(v.y, true));
+          sts128(dst + (((c4 * 2 + 1) ^ (row & 7)) << 4), e4m3x2_half2(v.z, false), e4m3x2_half2(v.z, true),
+                 e4m3x2_half2(v.w, false), e4m3x2_half2(v.w, true));
         }
       };
-      // The tail's keys or values as page pg: the warp's 16 rows scaled by a power of two.
-      auto put_tail = [&](uint32_t at, int pg, int half, StepMeta& me) {
+      // The tail as page pg: the warp's 16 rows scaled by a power of two. Twice over the rows (they are in
+      // L1 by then), to hold no more than one of them.
+      auto put_tail = [&](uint32_t at, int pg, StepMeta& me) {
         const uint16_t* src = a.tails + unit * kPageElems + half * kPart * kD;
-        // Twice over the rows (they are in L1 by then), to hold no more than one of them.
-        auto row_of = [&](int x, int y, uint32_t& wrong) {
-          const int row = w4 * 16 + x * 4 + r4;
+        const int r4 = lane >> 3, c8 = lane & 7;
+        uint32_t wrong = 0, top = 0;
+        auto row_of = [&](int x) {
+          const int row = w4 * 16 + (x >> 1) * 4 + r4;
           uint4 t = make_uint4(0, 0, 0, 0);
-          if (row < s.u.tail) t = *(reinterpret_cast<const uint4*>(src + row * kD + c8 * 16) + y);
+          if (row < s.u.tail) t = *(reinterpret_cast<const uint4*>(src + row * kD + c8 * 16) + (x & 1));
           uint32_t* tt = reinterpret_cast<uint32_t*>(&t);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const bool lo = (tt[e] & 0x7f80u) == 0x7f80u, hi = (tt[e] & 0x7f800000u) == 0x7f800000u;
             if (lo) tt[e] &= 0xffff0000u;
             if (hi) tt[e] &= 0x0000ffffu;
-            if (lo || hi) wrong |= 1u << (x * 4 + r4);
+            if (lo || hi) wrong |= 1u << ((x >> 1) * 4 + r4);
           }
           return t;
         };
-        uint32_t top = 0, wrong = 0;
 #pragma unroll 1
         for (int x = 0; x < 8; ++x) {
-          const uint4 t = row_of(x >> 1, x & 1, wrong);
+          const uint4 t = row_of(x);
           top = __vmaxu2(top, __vmaxu2(__vmaxu2(t.x & 0x7fff7fffu, t.y & 0x7fff7fffu), __vmaxu2(t.z & 0x7fff7fffu, t.w & 0x7fff7fffu)));
         }
         top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-        wrong = __reduce_or_sync(0xffffffffu, wrong);
         const int e = half_exponent(top);
         const float f = pow2(15 - e);
 #pragma unroll 1
         for (int x = 0; x < 8; ++x) {
-          const uint4 t = row_of(x >> 1, x & 1, wrong);
+          const uint4 t = row_of(x);
           const int row = w4 * 16 + (x >> 1) * 4 + r4;
           sts128(at + (c8 >> 2) * kPlane + (pg * kPart + row) * 128 + ((((c8 & 3) * 2 + (x & 1)) ^ (row & 7)) << 4),
                  pack_half2(lo_f(t.x) * f, hi_f(t.x) * f), pack_half2(lo_f(t.y) * f, hi_f(t.y) * f),
@@ -524,80 +554,54 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         }
         wrong = __reduce_or_sync(0xffffffffu, wrong);
         if (lane == 0) {
-          if (half == 0) {
-            me.kfac[pg * 4 + w4] = fabsf(scale) * kLog2e * pow2(e - 15);
-          } else {
+          if (half) {
             me.vlog[pg * 4 + w4] = (float)(e - 15);
             me.vinv[pg * 4 + w4] = f;
+            me.bad_vals[pg * 4 + w4] = (uint16_t)wrong;
+          } else {
+            me.kfac[pg * 4 + w4] = fabsf(scale) * kLog2e * pow2(e - 15);
+            me.bad_keys[pg * 4 + w4] = (uint16_t)wrong;
           }
-          if (wrong) atomicOr(&me.bad[pg * 2 + (w4 >> 1)], wrong << (16 * (w4 & 1)));
         }
-      };
-      auto put = [&](const uint4 (&raw)[8], uint32_t at, int step, int half, StepMeta& me) {
-        const int it = s.from + 2 * step, tail = s.u.pages - it;  // the tail's place, if it is in this step
-        if (tail > 0) put_page(raw, at, 0);
-        if (tail > 1 && it + 1 < s.to) put_page(raw, at, 1);
-        if (tail <= 1 && it + tail < s.to) put_tail(at, tail, half, me);
       };
       look(s.from);
-      load(keys, 0, 0);
-      load(vals, 0, 1);
+      load(0);
       for (int step = 0; step < s.steps; ++step, ++count) {
-        const uint32_t slot = count & 1, parity = count >> 1 & 1;
+        const uint32_t slot = count & 1, at = operand0 + slot * 16384;
+        const int it = s.from + 2 * step, tail = s.u.pages - it;  // the tail's place, if it is in this step
         StepMeta& me = sm.meta[count & 3];
-        // keys
-        ok = ok && mbar_wait(smem_u32(&sm.k_empty[slot]), parity ^ 1, abort, a.err);
+        ok = ok && mbar_wait(smem_u32(&empty[slot]), (count >> 1 & 1) ^ 1, abort, a.err);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
-          // what the softmax has to know; warp 0's lanes 0 and 1 for one page each
-          if (lane == 0) {
-            if ((w4 & 1) == 0) {
+          if (!half) {  // what the softmax has to know of the pages
 #pragma unroll
-              for (int pg = 0; pg < 2; ++pg) me.bad[pg * 2 + (w4 >> 1)] = 0;
+            for (int pg = 0; pg < 2; ++pg) {
+              if (it + pg < pages) {
+                const int p = __shfl_sync(0xffffffffu, pos, it + pg - id_base);
+                const float kx = __shfl_sync(0xffffffffu, sc.x, it + pg - id_base);
+                const float vx = __shfl_sync(0xffffffffu, sc.y, it + pg - id_base);
+                if (lane == 0) {
+                  const bool good = p >= 0 && kx == kx && vx == vx;
+                  me.kfac[pg * 4 + w4] = good ? kx * fabsf(scale) * kLog2e : 0.f;
+                  me.vlog[pg * 4 + w4] = good ? scale_log2(vx) : 0.f;
+                  me.vinv[pg * 4 + w4] = good ? 1.f / vx : 1.f;
+                  me.bad_keys[pg * 4 + w4] = p >= 0 && !good ? 0xffffu : 0u;
+                  if (w4 == 0) me.count[pg] = p >= 0 ? kPart : 0, me.pos[pg] = max(p, 0);
+                }
+              } else if (w4 == 0 && lane == 0) {
+                me.count[pg] = it + pg < s.to ? s.u.tail : 0;
+                me.pos[pg] = s.u.full * kPart;
+              }
             }
           }
-#pragma unroll
-          for (int pg = 0; pg < 2; ++pg) {
-            const int it = s.from + 2 * step + pg;
-            if (it >= s.to) {
-              if (w4 == 0 && lane == 0) me.count[pg] = 0, me.pos[pg] = 0;
-              continue;
-            }
-            if (it >= s.u.pages) {
-              if (w4 == 0 && lane == 0) me.count[pg] = s.u.tail, me.pos[pg] = s.u.full * kPart;
-              continue;
-            }
-            if (it >= id_base + 32) look(it);
-            const int p = __shfl_sync(0xffffffffu, pos, it - id_base);
-            const float kx = __shfl_sync(0xffffffffu, sc.x, it - id_base), vx = __shfl_sync(0xffffffffu, sc.y, it - id_base);
-            if (lane == 0) {
-              const bool good = p >= 0 && kx == kx && vx == vx;
-              me.kfac[pg * 4 + w4] = good ? kx * fabsf(scale) * kLog2e : 0.f;
-              me.vlog[pg * 4 + w4] = good ? scale_log2(vx) : 0.f;
-              me.vinv[pg * 4 + w4] = good ? 1.f / vx : 1.f;
-              if ((w4 & 1) == 0 && p >= 0 && !good) me.bad[pg * 2 + (w4 >> 1)] = 0xffffffffu;
-              if (w4 == 0) me.count[pg] = p >= 0 ? kPart : 0, me.pos[pg] = max(p, 0);
-            }
-          }
-          // (the flags of a tail are set by its warps after they are cleared: one barrier)
-          asm volatile("bar.sync 2, 128;" ::: "memory");
-          put(keys, sk + slot * 16384, step, 0, me);
+          if (tail > 0) put_page(at, 0);
+          if (tail > 1 && it + 1 < s.to) put_page(at, 1);
+          if (tail <= 1 && it + tail < s.to) put_tail(at, tail, me);
           proxy_fence();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.k_full[slot]));
-        } else {
-          asm volatile("bar.sync 2, 128;" ::: "memory");
+          if (lane == 0) mbar_arrive(smem_u32(&full[slot]));
         }
-        if (step + 1 < s.steps) load(keys, step + 1, 0);
-        ok = ok && mbar_wait(smem_u32(&sm.v_empty[slot]), parity ^ 1, abort, a.err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-          put(vals, sv + slot * 16384, step, 1, me);
-          proxy_fence();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.v_full[slot]));
-        }
-        if (step + 1 < s.steps) load(vals, step + 1, 1);
+        if (step + 1 < s.steps) load(step + 1);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[seg % kSegments]));
@@ -606,58 +610,74 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
   } else {
     // ------------------------------ products ------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp == kMmaWarp && lane == 0) {
+    if (warp == kMmaWarp) {
+      const uint32_t leader = elect();
+      auto wait = [&](const uint64_t& bar, uint32_t parity) {
+        ok = ok && mbar_wait(smem_u32(&bar), parity, abort, a.err);
+        ok = __all_sync(0xffffffffu, ok);
+      };
       uint32_t count = 0, q_phase = 0, p_phase = 0;  // phases: a bit per tile
+      const uint64_t dq = operand(sq, 16, 1024), dk = operand(sk, 16, 1024), dv = operand(sv, kPlane, 1024);
       auto scores = [&](int tile, uint32_t c, int pages) {
         const uint32_t d = tmem + kColS + tile * kTile;
-        const uint32_t at = sq + tile * (kTile * kD * 2), bt = sk + (c & 1) * 16384;
+        const uint64_t q0 = dq + tile * (kTile * kD * 2 >> 4), k0 = dk + (c & 1) * (16384 >> 4);
+        const uint32_t idesc = pages == 2 ? shape(kStep, false) : shape(kPart, false);
+        mma_ss<false>(leader, d, q0, k0, idesc);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ss(d, operand(at + (k >> 2) * (kTile * 128) + (k & 3) * 32, 16, 1024),
-                 operand(bt + (k >> 2) * kPlane + (k & 3) * 32, 16, 1024), pages == 2 ? shape(kStep, false) : shape(kPart, false), k > 0);
-        mma_commit(smem_u32(&sm.s_full[tile]));
+        for (int k = 1; k < 8; ++k)
+          mma_ss<true>(leader, d, q0 + ((k >> 2) * (kTile * 128 >> 4) + (k & 3) * 2), k0 + ((k >> 2) * (kPlane >> 4) + (k & 3) * 2), idesc);
+        mma_commit(leader, smem_u32(&sm.s_full[tile]));
+      };
+      auto values = [&](int tile, uint32_t c, int pages, bool add) {
+        const uint32_t d = tmem + kColO + tile * kTile, p = tmem + kColS + tile * kTile;
+        const uint64_t v0 = dv + (c & 1) * (16384 >> 4);
+        if (add) mma_ts<true>(leader, d, p, v0, shape(kD, true));
+        else mma_ts<false>(leader, d, p, v0, shape(kD, true));
+#pragma unroll
+        for (int k = 1; k < 4; ++k) mma_ts<true>(leader, d, p + k * 8, v0 + k * (2048 >> 4), shape(kD, true));
+        if (pages == 2) {
+#pragma unroll
+          for (int k = 4; k < 8; ++k) mma_ts<true>(leader, d, p + kPart + (k - 4) * 8, v0 + k * (2048 >> 4), shape(kD, true));
+        }
+        mma_commit(leader, smem_u32(&sm.pv_done[tile]));
       };
       while (next()) {
         const Segment& s = sm.segs[seg % kSegments];
         auto pages_of = [&](int step) { return min(2, s.to - s.from - 2 * step); };
-        ok = ok && mbar_wait(smem_u32(&sm.k_full[count & 1]), count >> 1 & 1, abort, a.err);
+        wait(sm.k_full[count & 1], count >> 1 & 1);
         for (int t = 0; t < 2; ++t)
           if (s.active(t, 0)) {
-            ok = ok && mbar_wait(smem_u32(&sm.q_full[t]), q_phase >> t & 1, abort, a.err);
+            wait(sm.q_full[t], q_phase >> t & 1);
             q_phase ^= 1u << t;
             tmem_after();
             if (ok) scores(t, count, pages_of(0));
           }
-        if (ok) mma_commit(smem_u32(&sm.k_empty[count & 1]));
+        if (ok) mma_commit(leader, smem_u32(&sm.k_empty[count & 1]));
         for (int step = 0; step < s.steps; ++step, ++count) {
           const int pages = pages_of(step);
           const bool more = step + 1 < s.steps;
-          ok = ok && mbar_wait(smem_u32(&sm.v_full[count & 1]), count >> 1 & 1, abort, a.err);
-          if (more) ok = ok && mbar_wait(smem_u32(&sm.k_full[(count + 1) & 1]), (count + 1) >> 1 & 1, abort, a.err);
+          wait(sm.v_full[count & 1], count >> 1 & 1);
+          if (more) wait(sm.k_full[(count + 1) & 1], (count + 1) >> 1 & 1);
           for (int t = 0; t < 2; ++t) {
             if (s.active(t, step)) {
-              ok = ok && mbar_wait(smem_u32(&sm.p_full[t]), p_phase >> t & 1, abort, a.err);
+              wait(sm.p_full[t], p_phase >> t & 1);
               p_phase ^= 1u << t;
               tmem_after();
-              if (ok) {
-                const uint32_t d = tmem + kColO + t * kTile, p = tmem + kColS + t * kTile;
-                for (int k = 0; k < 4 * pages; ++k)
-                  mma_ts(d, p + (k >> 2) * kPart + (k & 3) * 8, operand(sv + (count & 1) * 16384 + k * 2048, kPlane, 1024),
-                         shape(kD, true), step > 0 || k > 0);
-                mma_commit(smem_u32(&sm.pv_done[t]));
-              }
+              if (ok) values(t, count, pages, step > 0);
             }
-            if (t == 1 && ok) mma_commit(smem_u32(&sm.v_empty[count & 1]));
+            if (t == 1 && ok) mma_commit(leader, smem_u32(&sm.v_empty[count & 1]));
             if (more && s.active(t, step + 1) && ok) scores(t, count + 1, pages_of(step + 1));
           }
-          if (more && ok) mma_commit(smem_u32(&sm.k_empty[(count + 1) & 1]));
+          if (more && ok) mma_commit(leader, smem_u32(&sm.k_empty[(count + 1) & 1]));
         }
-        leave();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[seg % kSegments]));
+        ++seg;
       }
       // The last arrivals have landed before the CTA's shared memory goes.
       if (count > 0) {
-        ok = ok && mbar_wait(smem_u32(&sm.k_empty[(count - 1) & 1]), (count - 1) >> 1 & 1, abort, a.err);
-        ok = ok && mbar_wait(smem_u32(&sm.v_empty[(count - 1) & 1]), (count - 1) >> 1 & 1, abort, a.err);
+        wait(sm.k_empty[(count - 1) & 1], (count - 1) >> 1 & 1);
+        wait(sm.v_empty[(count - 1) & 1], (count - 1) >> 1 & 1);
       }
     }
     if (warp == kPlanWarp && lane == 0) {
