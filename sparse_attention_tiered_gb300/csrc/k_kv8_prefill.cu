@@ -193,11 +193,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
 }
 
 __device__ __forceinline__ int64_t blocks_weight(const Kv8Args& a, int b, int topk, bool report) {
+  Unit u = request_of(a, b, report);
   int64_t sum = 0;
   for (int block = 0;; ++block) {
-    const int w = unit_of(a, b, block * kBlockRows, kBlockRows, topk, report && block == 0).weight;
-    if (w == 0) return sum * a.Hkv;
-    sum += w;
+    set_rows(a, u, block * kBlockRows, kBlockRows, topk);
+    if (u.weight == 0) return sum * a.Hkv;
+    sum += u.weight;
   }
 }
 
@@ -684,13 +685,14 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       int b = pl.b, block = 0;
       int64_t at = share_start(pl.total, cta, ctas), before = pl.before;
       const int64_t stop = share_start(pl.total, cta + 1, ctas);
+      Segment s;
+      s.u = request_of(a, min(b, a.B - 1), false);
       for (bool more = true; more && ok; ++seg) {
-        Segment s;
         s.steps = 0;
         while (at < stop && b < a.B) {
-          s.u = unit_of(a, b, block * kBlockRows, kBlockRows, topk, false);
+          set_rows(a, s.u, block * kBlockRows, kBlockRows, topk);
           if (s.u.weight == 0) {  // the request has no more rows
-            ++b;
+            if (++b < a.B) s.u = request_of(a, b, false);
             block = 0;
             continue;
           }
@@ -708,8 +710,11 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           s.from = x.from;
           s.to = x.to;
           s.steps = (x.to - x.from + 1) / 2;
-          s.limit0 = unit_of(a, b, s.first_row, kTile, topk, false).items;
-          s.limit1 = unit_of(a, b, s.first_row + kTile, kTile, topk, false).items;
+          Unit t = s.u;
+          set_rows(a, t, s.first_row, kTile, topk);
+          s.limit0 = t.items;
+          set_rows(a, t, s.first_row + kTile, kTile, topk);
+          s.limit1 = t.items;
           break;
         }
         more = s.steps > 0;
@@ -745,8 +750,9 @@ kv8_prefill_join_kernel(const Kv8Args a, const Rows out, int topk, int ctas, con
   asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this launch must not end before the first
   if (share_start(pl.total, c, ctas) >= stop || pl.b >= a.B) return;
   int64_t before = pl.before;
+  Unit u = request_of(a, pl.b, false);
   for (int block = 0;; ++block) {
-    const Unit u = unit_of(a, pl.b, block * kBlockRows, kBlockRows, topk, false);
+    set_rows(a, u, block * kBlockRows, kBlockRows, topk);
     if (u.weight == 0) return;
     if (stop - 1 < before + (int64_t)u.weight * a.Hkv) {
       join_parts(a, out, u, pl, before, block * kBlockRows, kBlockRows, c, ctas, partials, kBlockRows);
@@ -769,7 +775,7 @@ cudaError_t launch_kv8_prefill(const Kv8Args& a, const Rows& q, const Rows& out,
   e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, 16);
+  cfg.gridDim = dim3((unsigned)ctas, 16);  // of a block's 256 rows
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];

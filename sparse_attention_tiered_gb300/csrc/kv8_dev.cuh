@@ -44,13 +44,18 @@ __device__ __forceinline__ unsigned long long now_ns() {
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
 // Waits until the phase with this parity has completed. Bounded: after kWaitNs, or once another
-// wait of the CTA has run out, it returns false with *abort (shared memory) set.
+// wait of the CTA has run out, it returns false with *abort (shared memory) set. A try suspends the
+// thread for a while by itself; the timer, which is slow to read, is looked at every 1024 of them.
 __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
-  const unsigned long long t0 = now_ns();
-  for (uint32_t it = 0; it < (1u << 30); ++it) {
+  unsigned long long t0 = 0;
+  for (uint32_t it = 1; it < (1u << 30); ++it) {
     if (mbar_try(bar, parity)) return true;
-    if (*abort) return false;
-    if ((it & 63u) == 63u && now_ns() - t0 > kWaitNs) break;
+    if ((it & 1023u) == 0) {
+      if (*abort) return false;
+      const unsigned long long t = now_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitNs) break;
+    }
   }
   *abort = 1;
   atomicOr(err, (uint32_t)kErrTimeout);
@@ -145,19 +150,31 @@ struct Unit {  // of one request: the same for all of its heads
   int weight;   // items + kUnitCost, or 0
 };
 
-__device__ __forceinline__ Unit unit_of(const Kv8Args& a, int b, int first_row, int rows, int topk, bool report) {
+// A request's numbers; n_new and the rest 0 where they are out of range.
+__device__ __forceinline__ Unit request_of(const Kv8Args& a, int b, bool report) {
   Unit u;
   const bool ok = kv8_request(a, b, report, u.row0, u.n_new, u.past);
   const int len = u.past + u.n_new;
   u.full = ok ? len >> 6 : 0;
   u.tail = ok ? len & (kPart - 1) : 0;
   u.pages = u.items = u.weight = 0;
-  if (!ok || (int64_t)u.n_new * a.G <= first_row) return u;  // the tile has no row of this request
-  const int last = min(u.n_new, (first_row + rows - 1) / a.G + 1);  // tokens up to the tile's last row
+  return u;
+}
+
+// The items that a block of rows of the request has.
+__device__ __forceinline__ void set_rows(const Kv8Args& a, Unit& u, int first_row, int rows, int topk) {
+  u.pages = u.items = u.weight = 0;
+  if ((int64_t)u.n_new * a.G <= first_row) return;  // the block has no row of this request
+  const int last = min(u.n_new, (first_row + rows - 1) / a.G + 1);  // tokens up to the block's last row
   const int seen = u.past + last;
   u.pages = topk ? topk : min(u.full, (seen + kPart - 1) >> 6);
   u.items = u.pages + (u.tail && seen > u.full * kPart ? 1 : 0);
   u.weight = u.items ? u.items + kUnitCost : 0;
+}
+
+__device__ __forceinline__ Unit unit_of(const Kv8Args& a, int b, int first_row, int rows, int topk, bool report) {
+  Unit u = request_of(a, b, report);
+  set_rows(a, u, first_row, rows, topk);
   return u;
 }
 

@@ -27,6 +27,41 @@ __device__ __forceinline__ void join_parts(const Kv8Args& a, const Rows& out, co
   const int n = share_of(pl.total, end - 1, ctas) - c + 1;  // at most kMaxCtas
   const int rows = min(tile_rows, u.n_new * a.G - first_row);
   const int64_t part_floats = (int64_t)stride * kPartialStride;
+  auto empty = [&](int x) {  // with fewer places than CTAs some shares are
+    return share_start(pl.total, c + x, ctas) >= share_start(pl.total, c + x + 1, ctas);
+  };
+  if (n <= 4) {  // a row a warp
+    for (int row = blockIdx.y * kWarps + warp; row < rows; row += gridDim.y * kWarps) {
+      float M = -INFINITY, L = 0.f;
+      float2 ml[4];
+      float4 y[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        ml[x] = make_float2(-INFINITY, 0.f);
+        y[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (x < n && !empty(x)) {
+          const float* part = partials + (int64_t)(2 * (c + x) + (x == 0 ? 1 : 0)) * part_floats + (int64_t)row * kPartialStride;
+          ml[x] = *reinterpret_cast<const float2*>(part);
+          y[x] = *reinterpret_cast<const float4*>(part + 4 + 4 * lane);  // (not written where nothing was seen)
+        }
+        M = fmaxf(M, ml[x].x);
+      }
+      const float base = M == -INFINITY ? 0.f : M;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float f = ex2(ml[x].x - base);
+        L += ml[x].y * f;
+        if (f != 0.f) o = make_float4(o.x + y[x].x * f, o.y + y[x].y * f, o.z + y[x].z * f, o.w + y[x].w * f);
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const int i = (first_row + row) / a.G, head = h * a.G + (first_row + row) - i * a.G;
+      const __nv_bfloat162 v0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), v1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+      *reinterpret_cast<uint2*>(out.p + (int64_t)(u.row0 + i) * out.ts + (int64_t)head * out.hs + 4 * lane) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
+    }
+    return;
+  }
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     const float* mine = partials + (int64_t)row * kPartialStride;
     auto part = [&](int x) { return mine + (int64_t)(2 * (c + x) + (x == 0 ? 1 : 0)) * part_floats; };
@@ -37,9 +72,7 @@ __device__ __forceinline__ void join_parts(const Kv8Args& a, const Rows& out, co
     for (int i = 0; i < kMost; ++i) {
       const int x = i * kJoinThreads + tid;
       ml[i] = make_float2(-INFINITY, 0.f);
-      // with fewer places than CTAs some shares are empty
-      if (x < n && share_start(pl.total, c + x, ctas) < share_start(pl.total, c + x + 1, ctas))
-        ml[i] = *reinterpret_cast<const float2*>(part(x));
+      if (x < n && !empty(x)) ml[i] = *reinterpret_cast<const float2*>(part(x));
       M = fmaxf(M, ml[i].x);
     }
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
