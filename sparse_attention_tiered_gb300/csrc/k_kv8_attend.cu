@@ -22,7 +22,7 @@
 // products. With the copy's 128-byte swizzle and tokens in the order 0 5 2 7 4 1 6 3, all of these
 // 16-byte loads touch every bank once. Values need two tokens of one dimension side by side: one
 // byte permutation for two such pairs.
-#include "kv8_join.cuh"
+#include "kv8_dev.cuh"
 
 #ifndef FEW_ROWS
 #define FEW_ROWS 16
@@ -161,7 +161,7 @@ __device__ __forceinline__ void finish_scores(float (&z)[MT][2][4], const float 
 template <int MT, int R>
 __global__ void __launch_bounds__(Dec<MT>::kThreads, 1)
 kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, const Rows q, const Rows out, float scale,
-                  const int32_t* __restrict__ sel, int topk, float* __restrict__ partials) {
+                  const int32_t* __restrict__ sel, int topk, JoinRecord* __restrict__ records, float* __restrict__ partials) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   float* join = reinterpret_cast<float*>(ring + Dec<MT>::kRingBytes);  // [warps][8 rows][kAccPad]
@@ -190,7 +190,11 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
       [&](int x, bool first) { return (int64_t)unit_of(a, x, first_row, kRows, topk, report && first).weight * a.Hkv; },
       [&](int64_t total) { return share_start(total, cta, ctas); });
   const int64_t start = share_start(pl.total, cta, ctas), stop = share_start(pl.total, cta + 1, ctas);
-  if (start >= stop) return;
+  JoinRecord* record = records + (ctas > 1 ? (int)blockIdx.y * ctas + cta : 0);  // one CTA a tile: never read
+  if (start >= stop) {
+    if (tid == 0) *record = JoinRecord{};
+    return;
+  }
 
   if (warp >= kConsWarps) {
     // ------------------------------ producer ------------------------------
@@ -213,6 +217,7 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
       for (int x = 0; x + 1 < kGroups; ++x) next[x] = next[x + 1];
       next[kGroups - 1] = first;
     };
+    JoinRecord open = JoinRecord{};
     bool ok = true;
     int b = pl.b;
     int64_t at = start, before = pl.before;
@@ -227,6 +232,8 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
       at += x.took;
       const int from = x.from, to = x.to;
       if (from >= to) continue;
+      if (from == 0 && to < u.items)
+        open = record_of(u, x.h, first_row, pl.total, before + (int64_t)(x.h + 1) * u.weight, cta, ctas);
       const int64_t unit = (int64_t)b * a.Hkv + x.h;
       // 32 page ids and scales at a time, a batch ahead of the copies
       int id = -1, pos = -1;
@@ -290,6 +297,7 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
         ok = __all_sync(0xffffffffu, ok);
       }
     }
+    if (lane == 0) *record = open;
     // No copy may be in flight when the CTA's shared memory goes. The consumers wait for every slot
     // that was filled, unless a wait ran out: then the phase in flight, if any, is waited for here.
     if (lane == 0 && !ok) {
@@ -628,25 +636,6 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
   }
 }
 
-// Joins the parts of the units that several CTAs shared. CTA (c, y) looks after the unit whose first
-// item is in share c and whose last is not, if there is one, and of its rows after y, y + gridDim.y ..
-// Parts are added in a fixed order.
-__global__ void __launch_bounds__(kJoinThreads)
-kv8_join_kernel(const Kv8Args a, const Rows out, int tile_rows, int topk, int ctas, const float* __restrict__ partials) {
-  __shared__ int64_t scratch[36];
-  const int c = blockIdx.x;
-  const int tile = blockIdx.z, first_row = tile * tile_rows;
-  const Place pl = locate(
-      a.B, scratch, [&](int x, bool) { return (int64_t)unit_of(a, x, first_row, tile_rows, topk, false).weight * a.Hkv; },
-      [&](int64_t total) { return share_start(total, c + 1, ctas) - 1; });
-  const int64_t stop = share_start(pl.total, c + 1, ctas);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this launch must not end before the first
-  if (share_start(pl.total, c, ctas) >= stop || pl.b >= a.B) return;
-  const Unit u = unit_of(a, pl.b, first_row, tile_rows, topk, false);
-  join_parts(a, out, u, pl, pl.before, first_row, tile_rows, c, ctas, partials + (int64_t)tile * ctas * 2 * kMaxTileRows * kPartialStride,
-             kMaxTileRows);
-}
-
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -678,7 +667,7 @@ cudaError_t page_map(const Kv8Args& a, CUtensorMap* m) {
 
 template <int MT, int R>
 cudaError_t launch_decode(const Kv8Args& a, const CUtensorMap& map, const Rows& q, const Rows& out, float scale,
-                          const int32_t* sel, int topk, float* partials, int sm_count, cudaStream_t st) {
+                          const int32_t* sel, int topk, void* workspace, int sm_count, cudaStream_t st) {
   const int rows = R == 1 ? 8 : 16 * MT;
   const int64_t tiles = ((int64_t)a.max_new * a.G + rows - 1) / rows;
   if (tiles > 65535) return cudaErrorInvalidConfiguration;
@@ -687,38 +676,29 @@ cudaError_t launch_decode(const Kv8Args& a, const CUtensorMap& map, const Rows& 
   cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<MT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dec_smem_bytes<MT>());
   if (e != cudaSuccess) return e;
   kv8_decode_kernel<MT, R><<<dim3((unsigned)ctas, (unsigned)tiles), Dec<MT>::kThreads, dec_smem_bytes<MT>(), st>>>(
-      a, map, q, out, scale, sel, topk, partials);
+      a, map, q, out, scale, sel, topk, static_cast<JoinRecord*>(workspace),
+      reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes));
   e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)rows, (unsigned)tiles);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its look at the lengths overlaps the first launch
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_join_kernel, a, out, rows, topk, ctas, (const float*)partials);
+  return launch_kv8_join(a, out, ctas, (int)tiles, rows, workspace, kMaxTileRows, st);
 }
 
 }  // namespace
 
 int64_t kv8_attend_workspace(const Kv8Args&) {
   const int64_t few = (int64_t)2 * kMaxCtas * kMaxTileRows * kPartialStride * 4, many = kv8_prefill_workspace();
-  return few > many ? few : many;
+  return (int64_t)kRecordBytes + (few > many ? few : many);
 }
 
 cudaError_t launch_kv8_attend(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const int32_t* sel,
                               int topk, void* workspace, int sm_count, cudaStream_t st) {
-  float* partials = static_cast<float*>(workspace);
-  if ((int64_t)a.max_new * a.G > FEW_ROWS) return launch_kv8_prefill(a, q, out, scale, sel, topk, partials, sm_count, st);
+  if ((int64_t)a.max_new * a.G > FEW_ROWS) return launch_kv8_prefill(a, q, out, scale, sel, topk, workspace, sm_count, st);
   CUtensorMap map;
   const cudaError_t e = page_map(a, &map);
   if (e != cudaSuccess) return e;
-  if ((int64_t)a.max_new * a.G <= 8) return launch_decode<1, 1>(a, map, q, out, scale, sel, topk, partials, sm_count, st);
-  if ((int64_t)a.max_new * a.G <= 16) return launch_decode<1, 2>(a, map, q, out, scale, sel, topk, partials, sm_count, st);
-  return launch_decode<2, 2>(a, map, q, out, scale, sel, topk, partials, sm_count, st);
+  if ((int64_t)a.max_new * a.G <= 8) return launch_decode<1, 1>(a, map, q, out, scale, sel, topk, workspace, sm_count, st);
+  if ((int64_t)a.max_new * a.G <= 16) return launch_decode<1, 2>(a, map, q, out, scale, sel, topk, workspace, sm_count, st);
+  return launch_decode<2, 2>(a, map, q, out, scale, sel, topk, workspace, sm_count, st);
 }
 
 }  // namespace spin

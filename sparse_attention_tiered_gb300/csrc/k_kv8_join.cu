@@ -1,0 +1,136 @@
+// The join of partial attention results over the 8-bit paged cache, for the units that several CTAs of
+// an attention launch shared. A CTA that begins such a unit leaves a record of it; every sharer
+// leaves a partial (M, L, -, -, o[128]) per row: weights relative to 2^M, their sum, the weighted
+// values. Parts are added in a fixed order. The launch waits for the attention launch by a programmatic
+// dependency, so it is resident when that ends.
+#include "kv8_dev.cuh"
+
+namespace spin {
+
+namespace {
+
+using namespace kv8;
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+
+// CTA (c, y): rows y, y + gridDim.y, .. (or as many warps' rows) of the unit that share c begins.
+__global__ void __launch_bounds__(kThreads)
+kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ records, const float* __restrict__ partials,
+                int part_rows) {
+  __shared__ float s_w[kMaxCtas], s_m[kWarps], s_l[kWarps], s_o[kWarps][kD];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this launch must not end before the first
+  const JoinRecord r = records[c];
+  const int n = r.parts;
+  if (n == 0) return;
+  const int rows = min(part_rows, r.n_new * G - r.first_row);
+  const int64_t part_floats = (int64_t)part_rows * kPartialStride;
+  const int share = c % ctas;  // of its tile
+  auto empty = [&](int x) {    // with fewer places than CTAs some shares are
+    return share_start(r.total, share + x, ctas) >= share_start(r.total, share + x + 1, ctas);
+  };
+  auto part = [&](int x, int row) {
+    return partials + (int64_t)(2 * (c + x) + (x == 0 ? 1 : 0)) * part_floats + (int64_t)row * kPartialStride;
+  };
+  auto dst = [&](int row) {
+    const int i = (r.first_row + row) / G, head = r.h * G + (r.first_row + row) - i * G;
+    return out.p + (int64_t)(r.row0 + i) * out.ts + (int64_t)head * out.hs;
+  };
+  if (n <= 4) {  // a row a warp
+    for (int row = blockIdx.y * kWarps + warp; row < rows; row += gridDim.y * kWarps) {
+      float M = -INFINITY, L = 0.f;
+      float2 ml[4];
+      float4 y[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        ml[x] = make_float2(-INFINITY, 0.f);
+        y[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (x < n && !empty(x)) {
+          ml[x] = *reinterpret_cast<const float2*>(part(x, row));
+          y[x] = *reinterpret_cast<const float4*>(part(x, row) + 4 + 4 * lane);  // (not written where nothing was seen)
+        }
+        M = fmaxf(M, ml[x].x);
+      }
+      const float base = M == -INFINITY ? 0.f : M;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float f = ex2(ml[x].x - base);
+        L += ml[x].y * f;
+        if (f != 0.f) o = make_float4(o.x + y[x].x * f, o.y + y[x].y * f, o.z + y[x].z * f, o.w + y[x].w * f);
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const __nv_bfloat162 v0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), v1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+      *reinterpret_cast<uint2*>(dst(row) + 4 * lane) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
+    }
+    return;
+  }
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {  // a row a CTA
+    constexpr int kMost = (kMaxCtas + kThreads - 1) / kThreads;
+    float2 ml[kMost];
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      const int x = i * kThreads + tid;
+      ml[i] = make_float2(-INFINITY, 0.f);
+      if (x < n && !empty(x)) ml[i] = *reinterpret_cast<const float2*>(part(x, row));
+      M = fmaxf(M, ml[i].x);
+    }
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    __syncthreads();  // the last row's sums have been read
+    if (lane == 0) s_m[warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
+    const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      const int x = i * kThreads + tid;
+      const float f = ex2(ml[i].x - base);
+      L += ml[i].y * f;
+      if (x < n) s_w[x] = f;
+    }
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) s_l[warp] = L;
+    __syncthreads();
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int x = warp; x < n; x += kWarps) {
+      const float f = s_w[x];
+      if (f == 0.f) continue;  // nothing seen there, or an empty share, which wrote nothing
+      const float4 y = *reinterpret_cast<const float4*>(part(x, row) + 4 + 4 * lane);
+      o = make_float4(o.x + y.x * f, o.y + y.y * f, o.z + y.z * f, o.w + y.w * f);
+    }
+    *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = o;
+    __syncthreads();
+    float sum = 0.f, x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      sum += s_l[w];
+      x += s_o[w][tid];
+    }
+    const __nv_bfloat16 y = __float2bfloat16_rn(sum == 0.f ? 0.f : x / sum);
+    dst(row)[tid] = *reinterpret_cast<const uint16_t*>(&y);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_join(const Kv8Args& a, const Rows& out, int ctas, int tiles, int rows, void* workspace,
+                            int part_rows, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(ctas * tiles), (unsigned)rows);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv8_join_kernel, a.G, out, ctas, (const JoinRecord*)workspace,
+                            (const float*)(static_cast<uint8_t*>(workspace) + kRecordBytes), part_rows);
+}
+
+}  // namespace spin

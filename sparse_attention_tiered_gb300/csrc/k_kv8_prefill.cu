@@ -21,7 +21,7 @@
 //
 // The arithmetic is that of the few-row kernel: z = score * k * log2(e) + log2(v) per page, weights
 // 2^(z - M + 6) with M at most 2^8 below the maximum, the softmax sum takes weight / v.
-#include "kv8_join.cuh"
+#include "kv8_dev.cuh"
 
 namespace spin {
 
@@ -141,14 +141,6 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* r) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::SPIN_I8(r, 0),
-      SPIN_I8(r, 8), SPIN_I8(r, 16), SPIN_I8(r, 24), "r"(addr)
-      : "memory");
-}
-
 // After tmem_loaded(): uses of the loaded registers stay behind it.
 __device__ __forceinline__ void settle32(uint32_t* r) {
   asm volatile("" : SPIN_R8(r, 0), SPIN_R8(r, 8), SPIN_R8(r, 16), SPIN_R8(r, 24));
@@ -193,13 +185,25 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
 }
 
 __device__ __forceinline__ int64_t blocks_weight(const Kv8Args& a, int b, int topk, bool report) {
-  Unit u = request_of(a, b, report);
+  const Unit u = request_of(a, b, report);
+  const int64_t rows = (int64_t)u.n_new * a.G;
+  // set_rows() block after block, the division by G carried along
+  int token = (kBlockRows - 1) / a.G, rest = (kBlockRows - 1) - token * a.G;
+  const int token_step = kBlockRows / a.G, rest_step = kBlockRows - token_step * a.G;
   int64_t sum = 0;
-  for (int block = 0;; ++block) {
-    set_rows(a, u, block * kBlockRows, kBlockRows, topk);
-    if (u.weight == 0) return sum * a.Hkv;
-    sum += u.weight;
+  for (int64_t row = 0; row < rows; row += kBlockRows) {
+    const int seen = u.past + min(u.n_new, token + 1);
+    const int pages = topk ? topk : min(u.full, (seen + kPart - 1) >> 6);
+    const int items = pages + (u.tail && seen > u.full * kPart ? 1 : 0);
+    sum += items ? items + kUnitCost : 0;
+    token += token_step;
+    rest += rest_step;
+    if (rest >= a.G) {
+      rest -= a.G;
+      ++token;
+    }
   }
+  return sum * a.Hkv;
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -210,7 +214,7 @@ __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.
 
 __global__ void __launch_bounds__(kThreads, 1)
 kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, const int32_t* __restrict__ sel, int topk,
-                   float* __restrict__ partials) {
+                   JoinRecord* __restrict__ records, float* __restrict__ partials) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sq = smem_u32(base), sk = sq + (uint32_t)kQBytes, sv = sk + (uint32_t)kKvBytes;
@@ -316,36 +320,24 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           if (!ok) continue;
         }
         tmem_after();
-        uint32_t x[64];
+        // Scores pass through two sets of 32 registers, twice: for their maximum and for the weights. The next
+        // set is on its way while one is worked on.
+        uint32_t xa[32], xb[32];
         float top = -INFINITY;
-        // Scores of a page into x; -inf for tokens that the row does not see, where there are any in the warp.
-        auto fetch = [&](int hf) {
-          tmem_load32(S + hf * kPart, x);
-          tmem_load32(S + hf * kPart + 32, x + 32);
-          const int vis = min(see - me.pos[hf], me.count[hf]);
-          tmem_loaded();
-          settle32(x);
-          settle32(x + 32);
-          if (__any_sync(0xffffffffu, vis < kPart)) {
+        auto vis_of = [&](int hf) { return min(see - me.pos[hf], me.count[hf]); };  // tokens of a page that the row sees
+        auto hide = [&](uint32_t* x, int vis) {
 #pragma unroll
-            for (int c = 0; c < kPart; ++c) x[c] = c < vis ? x[c] : 0xff800000u;
-          }
-          return vis;
+          for (int c = 0; c < 32; ++c) x[c] = c < vis ? x[c] : 0xff800000u;
         };
-        // The factor of a group's scores; not 0, which would make NaN of a hidden token's -inf.
-        auto factor = [&](int grp) { return fmaxf(me.kfac[grp] * qs, 1e-37f); };
-#pragma unroll 1
-        for (int hf = 0; hf < halves; ++hf) {
-          const int vis = fetch(hf);
-          uint2 bad = *reinterpret_cast<const uint2*>(&me.bad_keys[4 * hf]);
-          if (s.from + 2 * step + hf == s.u.pages) {
-            const uint2 more = *reinterpret_cast<const uint2*>(&me.bad_vals[4 * hf]);
-            bad = make_uint2(bad.x | more.x, bad.y | more.y);
-          }
-          const uint32_t b0 = bad.x, b1 = bad.y;
-          if (b0 | b1) poison |= ((vis < 32 ? b0 & ((1u << max(vis, 0)) - 1u) : b0) | (vis < 64 ? b1 & ((1u << max(vis - 32, 0)) - 1u) : b1)) != 0;
+        // The factors of a set's two groups of scores: not 0, which would make NaN of a hidden token's -inf.
+        auto factors = [&](int g) {
+          const float2 k = *reinterpret_cast<const float2*>(&me.kfac[g]);
+          return make_float2(fmaxf(k.x * qs, 1e-37f), fmaxf(k.y * qs, 1e-37f));
+        };
+        auto largest = [&](const uint32_t* x, int g) {
+          const float2 k = factors(g), v = *reinterpret_cast<const float2*>(&me.vlog[g]);
 #pragma unroll
-          for (int grp = 0; grp < 4; ++grp) {
+          for (int grp = 0; grp < 2; ++grp) {
             float m = __uint_as_float(x[grp * 16]), n = __uint_as_float(x[grp * 16 + 1]);
 #pragma unroll
             for (int c = 2; c < 14; c += 4) {
@@ -353,8 +345,34 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
               n = fmaxf(fmaxf(n, __uint_as_float(x[grp * 16 + c + 1])), __uint_as_float(x[grp * 16 + c + 3]));
             }
             m = fmaxf(m, fmaxf(n, fmaxf(__uint_as_float(x[grp * 16 + 14]), __uint_as_float(x[grp * 16 + 15]))));
-            top = fmaxf(top, fmaf(m, factor(hf * 4 + grp), me.vlog[hf * 4 + grp]));
+            top = fmaxf(top, fmaf(m, grp ? k.y : k.x, grp ? v.y : v.x));
           }
+        };
+        tmem_load32(S, xa);
+        tmem_loaded();
+        settle32(xa);
+#pragma unroll 1
+        for (int hf = 0; hf < halves; ++hf) {
+          tmem_load32(S + hf * kPart + 32, xb);
+          const int vis = vis_of(hf);
+          uint2 bad = *reinterpret_cast<const uint2*>(&me.bad_keys[4 * hf]);
+          if (s.from + 2 * step + hf == s.u.pages) {
+            const uint2 more = *reinterpret_cast<const uint2*>(&me.bad_vals[4 * hf]);
+            bad = make_uint2(bad.x | more.x, bad.y | more.y);
+          }
+          if (bad.x | bad.y)
+            poison |= ((vis < 32 ? bad.x & ((1u << max(vis, 0)) - 1u) : bad.x) |
+                       (vis < 64 ? bad.y & ((1u << max(vis - 32, 0)) - 1u) : bad.y)) != 0;
+          const bool some = __any_sync(0xffffffffu, vis < kPart);
+          if (some) hide(xa, vis);
+          largest(xa, hf * 4);
+          tmem_loaded();
+          settle32(xb);
+          tmem_load32(hf + 1 < halves ? S + kPart : S, xa);  // the next page, or the first again
+          if (some) hide(xb, vis - 32);
+          largest(xb, hf * 4 + 2);
+          tmem_loaded();
+          settle32(xa);
         }
         top = fmaxf(M, top);
         if (!(top > M + kSlack || (M == -INFINITY && top != -INFINITY))) top = M;
@@ -381,13 +399,13 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           M = top;
         }
         const float ref = (M == -INFINITY ? 0.f : M) - kUp;
-#pragma unroll 1
-        for (int hf = halves - 1; hf >= 0; --hf) {  // fp16 weights of a page, into the first 32 columns of its scores
-          if (hf != halves - 1) fetch(hf);
-          uint32_t p[32];
+        auto weigh = [&](const uint32_t* x, int g, uint32_t to) {  // fp16 weights of 32 scores, into 16 columns
+          const float2 k = factors(g), v = *reinterpret_cast<const float2*>(&me.vlog[g]);
+          const float2 w = *reinterpret_cast<const float2*>(&me.vinv[g]);
+          uint32_t p[16];
 #pragma unroll
-          for (int grp = 0; grp < 4; ++grp) {
-            const uint64_t k2 = twice(factor(hf * 4 + grp)), c2 = twice(me.vlog[hf * 4 + grp] - ref);
+          for (int grp = 0; grp < 2; ++grp) {
+            const uint64_t k2 = twice(grp ? k.y : k.x), c2 = twice((grp ? v.y : v.x) - ref);
             uint64_t sum2 = 0;
 #pragma unroll
             for (int c = 0; c < 16; c += 2) {
@@ -400,9 +418,24 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
             }
             float s0, s1;
             unpack2(sum2, s0, s1);
-            L = fmaf(s0 + s1, me.vinv[hf * 4 + grp], L);
+            L = fmaf(s0 + s1, grp ? w.y : w.x, L);
           }
-          tmem_store32(S + hf * kPart, p);
+          tmem_store16(to, p);
+        };
+#pragma unroll 1
+        for (int hf = 0; hf < halves; ++hf) {  // into the first 32 columns of the page's scores
+          tmem_load32(S + hf * kPart + 32, xb);
+          const int vis = vis_of(hf);
+          const bool some = __any_sync(0xffffffffu, vis < kPart);
+          if (some) hide(xa, vis);
+          weigh(xa, hf * 4, S + hf * kPart);
+          tmem_loaded();
+          settle32(xb);
+          if (hf + 1 < halves) tmem_load32(S + kPart, xa);
+          if (some) hide(xb, vis - 32);
+          weigh(xb, hf * 4 + 2, S + hf * kPart + 16);
+          tmem_loaded();
+          settle32(xa);
         }
         tmem_stored();
         tmem_before();
@@ -685,6 +718,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       int b = pl.b, block = 0;
       int64_t at = share_start(pl.total, cta, ctas), before = pl.before;
       const int64_t stop = share_start(pl.total, cta + 1, ctas);
+      JoinRecord open = JoinRecord{};
       Segment s;
       s.u = request_of(a, min(b, a.B - 1), false);
       for (bool more = true; more && ok; ++seg) {
@@ -704,6 +738,8 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           const Part x = part_of(s.u, at - before, stop - at);
           at += x.took;
           if (x.from >= x.to) continue;
+          if (x.from == 0 && x.to < s.u.items)
+            open = record_of(s.u, x.h, block * kBlockRows, pl.total, before + (int64_t)(x.h + 1) * s.u.weight, cta, ctas);
           s.b = b;
           s.h = x.h;
           s.first_row = block * kBlockRows;
@@ -723,6 +759,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         sm.segs[seg % kSegments] = s;
         mbar_arrive(smem_u32(&sm.seg_full[seg % kSegments]));
       }
+      records[cta] = open;
     }
     __syncwarp();
   }
@@ -739,51 +776,20 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
   }
 }
 
-__global__ void __launch_bounds__(kJoinThreads)
-kv8_prefill_join_kernel(const Kv8Args a, const Rows out, int topk, int ctas, const float* __restrict__ partials) {
-  __shared__ int64_t scratch[36];
-  const int c = blockIdx.x;
-  const Place pl = locate(
-      a.B, scratch, [&](int x, bool) { return blocks_weight(a, x, topk, false); },
-      [&](int64_t total) { return share_start(total, c + 1, ctas) - 1; });
-  const int64_t stop = share_start(pl.total, c + 1, ctas);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this launch must not end before the first
-  if (share_start(pl.total, c, ctas) >= stop || pl.b >= a.B) return;
-  int64_t before = pl.before;
-  Unit u = request_of(a, pl.b, false);
-  for (int block = 0;; ++block) {
-    set_rows(a, u, block * kBlockRows, kBlockRows, topk);
-    if (u.weight == 0) return;
-    if (stop - 1 < before + (int64_t)u.weight * a.Hkv) {
-      join_parts(a, out, u, pl, before, block * kBlockRows, kBlockRows, c, ctas, partials, kBlockRows);
-      return;
-    }
-    before += (int64_t)u.weight * a.Hkv;
-  }
-}
-
 }  // namespace
 
 int64_t kv8_prefill_workspace() { return (int64_t)2 * kMaxCtas * kBlockRows * kPartialStride * 4; }
 
 cudaError_t launch_kv8_prefill(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const int32_t* sel,
-                               int topk, float* partials, int sm_count, cudaStream_t st) {
+                               int topk, void* workspace, int sm_count, cudaStream_t st) {
   const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
   cudaError_t e = cudaFuncSetAttribute(kv8_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
-  kv8_prefill_kernel<<<ctas, kThreads, kSmemBytes, st>>>(a, q, out, scale, sel, topk, partials);
+  kv8_prefill_kernel<<<ctas, kThreads, kSmemBytes, st>>>(a, q, out, scale, sel, topk, static_cast<JoinRecord*>(workspace),
+                                                         reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes));
   e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, 16);  // of a block's 256 rows
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_prefill_join_kernel, a, out, topk, ctas, (const float*)partials);
+  return launch_kv8_join(a, out, ctas, 1, 16, workspace, kBlockRows, st);
 }
 
 }  // namespace spin

@@ -247,5 +247,21 @@ __device__ __forceinline__ Part part_of(const Unit& u, int64_t at, int64_t left)
   return x;
 }
 
+// What a CTA leaves of a unit that it begins and does not end (parts 0: there is none), in the
+// workspace's first bytes; the partials follow, two blocks of rows for each share: number 2 x for the
+// unit that share x found begun, 2 x + 1 for the one that it began.
+struct JoinRecord {
+  int64_t total;  // places of all units
+  int32_t parts, row0, n_new, h, first_row, reserved;
+};
+constexpr int kMaxCtas = 160;  // CTAs that a call's work is split over, at most
+constexpr size_t kRecordBytes = kMaxCtas * sizeof(JoinRecord);
+constexpr float kLog2e = 1.4426950408889634f;
+
+// `end`: the place behind the unit's last.
+__device__ __forceinline__ JoinRecord record_of(const Unit& u, int h, int first_row, int64_t total, int64_t end, int cta, int ctas) {
+  return JoinRecord{total, share_of(total, end - 1, ctas) - cta + 1, u.row0, u.n_new, h, first_row, 0};
+}
+
 }  // namespace kv8
 }  // namespace spin
