@@ -7,9 +7,11 @@
 //   S_t[128 x 128] = Q_t (shared memory) K^T (shared memory), 8 products of depth 16,
 //   O_t[128 x 128] += P_t (tensor memory, in the place of S_t) V (shared memory, tokens as depth).
 // Roles, by warp:
-//   0-3, 4-7  softmax of tile 0 and 1, one row a thread: scores out of tensor memory, running maximum,
-//             fp16 weights back into it; the output rescaled only when the maximum has grown by
-//             more than 2^8, which is rare, so that O stays where it is; rows stored at the end;
+//   0-3, 4-7  softmax of tile 0 and 1, one row a thread: scores out of tensor memory, fp16 weights back into
+//             it, relative to a reference that is the maximum of the row's first step. A later step looks
+//             for no maximum: its sums say whether a weight may have left fp16's range, and then,
+//             which is rare, the reference is raised and what was added up so far scaled. Rows are
+//             stored at the end;
 //   8-11      keys from HBM to fp16 in shared memory, 128-byte swizzled. A step's loads are in registers
 //             one step ahead of their use, so no shared memory holds codes;
 //   12-15     values, likewise;
@@ -20,7 +22,7 @@
 // K and of V, 32 KB each.
 //
 // The arithmetic is that of the few-row kernel: z = score * k * log2(e) + log2(v) per page, weights
-// 2^(z - M + 6) with M at most 2^8 below the maximum, the softmax sum takes weight / v.
+// 2^(z - M + 6), the softmax sum takes weight / v. M is the reference: weights up to 2^15 are let pass.
 #include "kv8_dev.cuh"
 
 namespace spin {
@@ -35,8 +37,8 @@ constexpr int kStep = 2 * kPart;  // tokens of a step
 constexpr int kThreads = 640;
 constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16, kPlanWarp = 17;
 constexpr int kSegReaders = 17;  // warps that read a segment: softmax, loaders, products
-constexpr float kUp = 6.f;     // weights reach 2^kUp times ..
-constexpr float kSlack = 8.f;  // .. 2^kSlack before the output is rescaled
+constexpr float kUp = 6.f;          // a weight at the reference is 2^kUp
+constexpr float kMostSum = 32768.f;  // of 64 weights: none of them is above it
 constexpr int kPlane = 32768;  // K or V: [2 planes of 64 dimensions][2 steps][128 tokens][128 bytes]
 constexpr uint32_t kColO = 0, kColS = 256;
 
@@ -52,7 +54,7 @@ struct Segment {
 constexpr int kSegments = 4;  // announced ahead
 
 // What the softmax warps have to know of a step's tokens, by groups of 16.
-struct alignas(8) StepMeta {
+struct alignas(16) StepMeta {
   float kfac[8];       // score factor, without the row's
   float vlog[8], vinv[8];
   // Bit per token: a row that sees it is NaN (the other numbers are finite all the same). From the value
@@ -146,14 +148,6 @@ __device__ __forceinline__ void settle32(uint32_t* r) {
   asm volatile("" : SPIN_R8(r, 0), SPIN_R8(r, 8), SPIN_R8(r, 16), SPIN_R8(r, 24));
 }
 
-__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : SPIN_W8(r, 0), SPIN_W8(r, 8)
-      : "r"(addr)
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::SPIN_I8(r, 0),
@@ -161,7 +155,19 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
-__device__ __forceinline__ void settle16(uint32_t* r) { asm volatile("" : SPIN_R8(r, 0), SPIN_R8(r, 8)); }
+__device__ __forceinline__ void tmem_load8(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : SPIN_W8(r, 0)
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::SPIN_I8(r, 0), "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void settle8(uint32_t* r) { asm volatile("" : SPIN_R8(r, 0)); }
 
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
@@ -259,11 +265,11 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
     ok = __all_sync(0xffffffffu, ok);
     return ok && sm.segs[seg % kSegments].steps > 0;
   };
-  // 640 threads x 96 registers at launch = 256 x 152 + 256 x 64 + 128 x 48.
+  // 640 threads x 96 registers at launch = 256 x 144 + 256 x 72 + 128 x 48.
 
   if (warp < kKeyWarp) {
     // ------------------------------ softmax, a row a thread ------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     const int tile = warp >> 2, quad = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t S = lanes + kColS + tile * kTile, O = lanes + kColO + tile * kTile;
@@ -320,122 +326,133 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           if (!ok) continue;
         }
         tmem_after();
-        // Scores pass through two sets of 32 registers, twice: for their maximum and for the weights. The next
-        // set is on its way while one is worked on.
-        uint32_t xa[32], xb[32];
-        float top = -INFINITY;
-        auto vis_of = [&](int hf) { return min(see - me.pos[hf], me.count[hf]); };  // tokens of a page that the row sees
-        auto hide = [&](uint32_t* x, int vis) {
+        // A page's 64 scores at a time. A group of 16 tokens has one scale; what the groups need is read as
+        // vectors, once: a warp alone on its scheduler waits for every dependent instruction.
+        uint32_t x[kPart];
+        float4 fac, vlog;
+        auto tokens = [&](int hf) { return min(see - me.pos[hf], me.count[hf]); };  // that the row sees
+        auto fetch = [&](int hf) {
+          tmem_load32(S + hf * kPart, x);
+          tmem_load32(S + hf * kPart + 32, x + 32);
+          fac = *reinterpret_cast<const float4*>(&me.kfac[4 * hf]);
+          vlog = *reinterpret_cast<const float4*>(&me.vlog[4 * hf]);
+          // not 0, which would make NaN of a hidden token's -inf
+          fac = make_float4(fmaxf(fac.x * qs, 1e-37f), fmaxf(fac.y * qs, 1e-37f), fmaxf(fac.z * qs, 1e-37f), fmaxf(fac.w * qs, 1e-37f));
+          const int vis = tokens(hf);
+          const bool some = __any_sync(0xffffffffu, vis < kPart);
+          tmem_loaded();
+          settle32(x);
+          settle32(x + 32);
+          if (some) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) x[c] = c < vis ? x[c] : 0xff800000u;
-        };
-        // The factors of a set's two groups of scores: not 0, which would make NaN of a hidden token's -inf.
-        auto factors = [&](int g) {
-          const float2 k = *reinterpret_cast<const float2*>(&me.kfac[g]);
-          return make_float2(fmaxf(k.x * qs, 1e-37f), fmaxf(k.y * qs, 1e-37f));
-        };
-        auto largest = [&](const uint32_t* x, int g) {
-          const float2 k = factors(g), v = *reinterpret_cast<const float2*>(&me.vlog[g]);
-#pragma unroll
-          for (int grp = 0; grp < 2; ++grp) {
-            float m = __uint_as_float(x[grp * 16]), n = __uint_as_float(x[grp * 16 + 1]);
-#pragma unroll
-            for (int c = 2; c < 14; c += 4) {
-              m = fmaxf(fmaxf(m, __uint_as_float(x[grp * 16 + c])), __uint_as_float(x[grp * 16 + c + 2]));
-              n = fmaxf(fmaxf(n, __uint_as_float(x[grp * 16 + c + 1])), __uint_as_float(x[grp * 16 + c + 3]));
-            }
-            m = fmaxf(m, fmaxf(n, fmaxf(__uint_as_float(x[grp * 16 + 14]), __uint_as_float(x[grp * 16 + 15]))));
-            top = fmaxf(top, fmaf(m, grp ? k.y : k.x, grp ? v.y : v.x));
+            for (int c = 0; c < kPart; ++c) x[c] = c < vis ? x[c] : 0xff800000u;
           }
         };
-        tmem_load32(S, xa);
-        tmem_loaded();
-        settle32(xa);
+        auto largest = [&]() {
+          float m[4];
+#pragma unroll
+          for (int grp = 0; grp < 4; ++grp) {
+            m[grp] = __uint_as_float(x[grp * 16]);
+#pragma unroll
+            for (int c = 1; c < 16; ++c) m[grp] = fmaxf(m[grp], __uint_as_float(x[grp * 16 + c]));
+          }
+          return fmaxf(fmaxf(fmaf(m[0], fac.x, vlog.x), fmaf(m[1], fac.y, vlog.y)), fmaxf(fmaf(m[2], fac.z, vlog.z), fmaf(m[3], fac.w, vlog.w)));
+        };
+        // What was added up so far, times f: L, the output once its products are done, the weights of the step's
+        // first page if that is done. (f is 1 for some rows, a power of two for the others.)
+        auto rescale = [&](float f, bool page) {
+          L *= f;
+          uint32_t y[8];
+          if (step > 0) {
+            ok = ok && mbar_wait(smem_u32(&sm.pv_done[tile]), (done - 1) & 1, abort, a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            tmem_after();
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 8) {
+              tmem_load8(O + c, y);
+              tmem_loaded();
+              settle8(y);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+              tmem_store8(O + c, y);
+            }
+          }
+          tmem_stored();
+          const __half2 f2 = __float2half2_rn(f);
+#pragma unroll 1
+          for (int c = 0; c < (page ? 32 : 0); c += 8) {
+            tmem_load8(S + c, y);
+            tmem_loaded();
+            settle8(y);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const __half2 z = __hmul2(*reinterpret_cast<__half2*>(&y[k]), f2);
+              y[k] = *reinterpret_cast<const uint32_t*>(&z);
+            }
+            tmem_store8(S + c, y);
+          }
+        };
+        if (__any_sync(0xffffffffu, M == -INFINITY)) {  // no reference yet: the step's maximum
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int hf = 0; hf < halves; ++hf) {
+            fetch(hf);
+            top = fmaxf(top, largest());
+          }
+          if (M == -INFINITY) M = top;
+        }
+        float up = kUp - (M == -INFINITY ? 0.f : M);
 #pragma unroll 1
         for (int hf = 0; hf < halves; ++hf) {
-          tmem_load32(S + hf * kPart + 32, xb);
-          const int vis = vis_of(hf);
+          fetch(hf);
+          uint32_t p[32];
+          float sum[4];
+          for (;;) {
+#pragma unroll
+            for (int grp = 0; grp < 4; ++grp) {
+              const uint64_t k2 = twice(grp == 0 ? fac.x : grp == 1 ? fac.y : grp == 2 ? fac.z : fac.w);
+              const uint64_t c2 = twice((grp == 0 ? vlog.x : grp == 1 ? vlog.y : grp == 2 ? vlog.z : vlog.w) + up);
+              uint64_t sum2[2] = {0, 0};
+#pragma unroll
+              for (int c = 0; c < 16; c += 2) {
+                float y0, y1;
+                unpack2(fma2(pack2(x[grp * 16 + c], x[grp * 16 + c + 1]), k2, c2), y0, y1);
+                y0 = ex2(y0);
+                y1 = ex2(y1);
+                sum2[c >> 1 & 1] = add2(sum2[c >> 1 & 1], pack2(__float_as_uint(y0), __float_as_uint(y1)));
+                p[grp * 8 + c / 2] = pack_half2(y0, y1);
+              }
+              float s0, s1;
+              unpack2(add2(sum2[0], sum2[1]), s0, s1);
+              sum[grp] = s0 + s1;
+            }
+            const bool over = (sum[0] + sum[1]) + (sum[2] + sum[3]) > kMostSum && !poison;
+            if (!__any_sync(0xffffffffu, over)) break;
+            // Rare. The reference goes up by whole powers of two to the page's maximum, for the rows that need it.
+            fetch(hf);
+            const float d = over ? ceilf(largest() - M) : 0.f;
+            M += d;
+            up -= d;
+            rescale(ex2(-d), hf == 1);
+          }
+          const float4 vinv = *reinterpret_cast<const float4*>(&me.vinv[4 * hf]);
+          L += fmaf(sum[0], vinv.x, sum[1] * vinv.y) + fmaf(sum[2], vinv.z, sum[3] * vinv.w);
+          tmem_store16(S + hf * kPart, p);  // half of the columns that the scores had
+          tmem_store16(S + hf * kPart + 16, p + 16);
+        }
+        if (!ok) continue;
+        // tokens that make NaN of the rows that see them
+        for (int hf = 0; hf < halves; ++hf) {
           uint2 bad = *reinterpret_cast<const uint2*>(&me.bad_keys[4 * hf]);
           if (s.from + 2 * step + hf == s.u.pages) {
             const uint2 more = *reinterpret_cast<const uint2*>(&me.bad_vals[4 * hf]);
             bad = make_uint2(bad.x | more.x, bad.y | more.y);
           }
+          const int vis = tokens(hf);
           if (bad.x | bad.y)
             poison |= ((vis < 32 ? bad.x & ((1u << max(vis, 0)) - 1u) : bad.x) |
                        (vis < 64 ? bad.y & ((1u << max(vis - 32, 0)) - 1u) : bad.y)) != 0;
-          const bool some = __any_sync(0xffffffffu, vis < kPart);
-          if (some) hide(xa, vis);
-          largest(xa, hf * 4);
-          tmem_loaded();
-          settle32(xb);
-          tmem_load32(hf + 1 < halves ? S + kPart : S, xa);  // the next page, or the first again
-          if (some) hide(xb, vis - 32);
-          largest(xb, hf * 4 + 2);
-          tmem_loaded();
-          settle32(xa);
-        }
-        top = fmaxf(M, top);
-        if (!(top > M + kSlack || (M == -INFINITY && top != -INFINITY))) top = M;
-        if (__any_sync(0xffffffffu, top != M)) {
-          const float f = top == M ? 1.f : ex2(M - top);  // 0 for a row that saw nothing yet
-          if (step > 0) {  // rare after the first step: the output so far, once its products are done
-            ok = ok && mbar_wait(smem_u32(&sm.pv_done[tile]), (done - 1) & 1, abort, a.err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) continue;
-            tmem_after();
-#pragma unroll 1
-            for (int c = 0; c < kD; c += 16) {
-              uint32_t y[16];
-              tmem_load16(O + c, y);
-              tmem_loaded();
-              settle16(y);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
-              tmem_store16(O + c, y);
-            }
-            tmem_stored();
-          }
-          L *= f;
-          M = top;
-        }
-        const float ref = (M == -INFINITY ? 0.f : M) - kUp;
-        auto weigh = [&](const uint32_t* x, int g, uint32_t to) {  // fp16 weights of 32 scores, into 16 columns
-          const float2 k = factors(g), v = *reinterpret_cast<const float2*>(&me.vlog[g]);
-          const float2 w = *reinterpret_cast<const float2*>(&me.vinv[g]);
-          uint32_t p[16];
-#pragma unroll
-          for (int grp = 0; grp < 2; ++grp) {
-            const uint64_t k2 = twice(grp ? k.y : k.x), c2 = twice((grp ? v.y : v.x) - ref);
-            uint64_t sum2 = 0;
-#pragma unroll
-            for (int c = 0; c < 16; c += 2) {
-              float y0, y1;
-              unpack2(fma2(pack2(x[grp * 16 + c], x[grp * 16 + c + 1]), k2, c2), y0, y1);
-              y0 = ex2(y0);
-              y1 = ex2(y1);
-              sum2 = add2(sum2, pack2(__float_as_uint(y0), __float_as_uint(y1)));
-              p[grp * 8 + c / 2] = pack_half2(y0, y1);
-            }
-            float s0, s1;
-            unpack2(sum2, s0, s1);
-            L = fmaf(s0 + s1, grp ? w.y : w.x, L);
-          }
-          tmem_store16(to, p);
-        };
-#pragma unroll 1
-        for (int hf = 0; hf < halves; ++hf) {  // into the first 32 columns of the page's scores
-          tmem_load32(S + hf * kPart + 32, xb);
-          const int vis = vis_of(hf);
-          const bool some = __any_sync(0xffffffffu, vis < kPart);
-          if (some) hide(xa, vis);
-          weigh(xa, hf * 4, S + hf * kPart);
-          tmem_loaded();
-          settle32(xb);
-          if (hf + 1 < halves) tmem_load32(S + kPart, xa);
-          if (some) hide(xb, vis - 32);
-          weigh(xb, hf * 4 + 2, S + hf * kPart + 16);
-          tmem_loaded();
-          settle32(xa);
         }
         tmem_stored();
         tmem_before();
@@ -493,7 +510,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
     // ------------------------------ loaders: four warps of keys, four of values ------------------------------
     // Warp w has rows 16 w .. 16 w + 15 of every page. In load x, eight lanes have 64 bytes of two neighbouring
     // rows each: their 16-byte stores then fall on eight different columns of the swizzle.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int half = warp >= kValueWarp ? 1 : 0;
     const int w4 = warp & 3, c4 = lane & 3, row0 = w4 * 16 + (lane >> 3) * 2 + (lane >> 2 & 1);
     const uint32_t operand0 = half ? sv : sk;
