@@ -299,15 +299,8 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
     }
     if (lane == 0) *record = open;
     // No copy may be in flight when the CTA's shared memory goes. The consumers wait for every slot
-    // that was filled, unless a wait ran out: then the phase in flight, if any, is waited for here.
-    if (lane == 0 && !ok) {
-      const unsigned long long t0 = now_ns();
-      for (int x = 0; x < Dec<MT>::kSlots; ++x)
-        while (now_ns() - t0 < kWaitNs / 4 && !mbar_try(smem_u32(&sm.full[x]), 0) && !mbar_try(smem_u32(&sm.full[x]), 1)) {
-        }
-      while (now_ns() - t0 < kWaitNs / 4) {
-      }
-    }
+    // that was filled, unless a wait ran out.
+    if (lane == 0 && !ok) settle_down();
     return;
   }
 

@@ -76,7 +76,11 @@ struct Smem {
 constexpr size_t kQBytes = (size_t)kBlockRows * kD * 2;       // 64 KB: [tile][2 planes][128 rows][128 bytes]
 constexpr size_t kKvBytes = (size_t)2 * kPlane;               // 64 KB each
 constexpr size_t kSmemBytes = 1024 + kQBytes + 2 * kKvBytes + sizeof(Smem);
-static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
+// 196 KB with the 1 KB that the system takes: the next size of the SM's shared memory would leave the L1
+// too small to have the loaders' loads in flight (11% slower, with few rows 25%).
+static_assert(kSmemBytes + 1024 <= 196 * 1024, "shared memory of a CTA");
+constexpr int kWeights = 4096;  // requests' weights, in Q's place before there is a Q
+static_assert(kWeights * 8 <= kQBytes, "");
 
 // Shared memory descriptor of a 128-byte swizzled operand: 8-row groups `sbo` bytes apart, and for an
 // operand whose rows are the depth, 64-element blocks `lbo` bytes apart.
@@ -253,23 +257,39 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tmem_before();
+  // Requests' weights, a warp each; beyond kWeights requests, a thread each, twice over.
+  const bool few = a.B <= kWeights;
+  int64_t* weights = reinterpret_cast<int64_t*>(base);
+  if (few) {
+    for (int b = warp; b < a.B; b += kThreads / 32) {
+      Unit u = request_of(a, b, cta == 0 && lane == 0);
+      const int blocks = (int)(((int64_t)u.n_new * a.G + kBlockRows - 1) / kBlockRows);
+      int64_t sum = 0;
+      for (int k = lane; k < blocks; k += 32) {
+        set_rows(a, u, k * kBlockRows, kBlockRows, topk);
+        sum += u.weight;
+      }
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) weights[b] = sum * a.Hkv;
+    }
+    __syncthreads();
+  }
   const Place pl = locate(
-      a.B, sm.scratch, [&](int x, bool first) { return blocks_weight(a, x, topk, first && cta == 0); },
+      a.B, sm.scratch, [&](int x, bool first) { return few ? weights[x] : blocks_weight(a, x, topk, first && cta == 0); },
       [&](int64_t total) { return share_start(total, cta, ctas); });
   tmem_after();
   const uint32_t tmem = sm.tmem;
   bool ok = true;
   uint32_t seg = 0;  // segments read so far
   auto next = [&]() {  // the next segment is there and is not the end
-    ok = ok && mbar_wait(smem_u32(&sm.seg_full[seg % kSegments]), seg / kSegments & 1, abort, a.err);
-    ok = __all_sync(0xffffffffu, ok);
+    warp_wait(ok, smem_u32(&sm.seg_full[seg % kSegments]), seg / kSegments & 1, abort, a.err);
     return ok && sm.segs[seg % kSegments].steps > 0;
   };
-  // 640 threads x 96 registers at launch = 256 x 144 + 256 x 72 + 128 x 48.
+  // 640 threads x 96 registers at launch = 256 x 128 + 256 x 80 + 128 x 64.
 
   if (warp < kKeyWarp) {
     // ------------------------------ softmax, a row a thread ------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     const int tile = warp >> 2, quad = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t S = lanes + kColS + tile * kTile, O = lanes + kColO + tile * kTile;
@@ -285,28 +305,38 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       bool poison = false;  // the row's result is NaN
       const int my_steps = s.limit(tile) ? max(0, (min(s.to, s.limit(tile)) - s.from + 1) / 2) : 0;
       if (my_steps) {
-        // the row: 64 words, its largest element, fp16 with the factor in qs; scale's sign goes here
-        const uint4* src = reinterpret_cast<const uint4*>(q.p + (int64_t)(s.u.row0 + i) * q.ts + (int64_t)head * q.hs);
-        uint4 w[16];
-        uint32_t top = 0;
+        // The warp's 32 rows, two at a time: 16 lanes have 16 bytes each of a row, whose largest element gives
+        // the power of two that puts it into fp16's range (and back out: qs). scale's sign goes here too.
+        const uint64_t mine_at = reinterpret_cast<uint64_t>(q.p + (int64_t)(s.u.row0 + i) * q.ts + (int64_t)head * q.hs);
+        const int r2 = lane >> 4, c16 = lane & 15;
+#pragma unroll 1
+        for (int y = 0; y < 16; y += 4) {
+          uint4 w[4];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          w[x] = mine ? src[x] : make_uint4(0, 0, 0, 0);
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[x].x & 0x7fff7fffu, w[x].y & 0x7fff7fffu),
-                                       __vmaxu2(w[x].z & 0x7fff7fffu, w[x].w & 0x7fff7fffu)));
+          for (int x = 0; x < 4; ++x) {
+            const uint64_t at = __shfl_sync(0xffffffffu, mine_at, 2 * (y + x) + r2);
+            const bool there = __shfl_sync(0xffffffffu, (int)mine, 2 * (y + x) + r2);
+            w[x] = there ? reinterpret_cast<const uint4*>(at)[c16] : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t top = __vmaxu2(__vmaxu2(w[x].x & 0x7fff7fffu, w[x].y & 0x7fff7fffu), __vmaxu2(w[x].z & 0x7fff7fffu, w[x].w & 0x7fff7fffu));
+            top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int e = half_exponent(top);
+            const float f = scale < 0.f ? -pow2(15 - e) : pow2(15 - e);
+            const int r = quad * 32 + 2 * (y + x) + r2;
+            sts128(sq + tile * (kTile * kD * 2) + (c16 >> 3) * (kTile * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4),
+                   pack_half2(lo_f(w[x].x) * f, hi_f(w[x].x) * f), pack_half2(lo_f(w[x].y) * f, hi_f(w[x].y) * f),
+                   pack_half2(lo_f(w[x].z) * f, hi_f(w[x].z) * f), pack_half2(lo_f(w[x].w) * f, hi_f(w[x].w) * f));
+            const uint32_t own = __shfl_sync(0xffffffffu, top, (lane & 1) << 4);
+            if (lane >> 1 == y + x) {
+              qs = own >= 0x7f80u ? 1.f : pow2(half_exponent(own) - 15);
+              poison = own >= 0x7f80u;
+            }
+          }
         }
-        top = max(top & 0xffffu, top >> 16);
-        const int e = half_exponent(top);
-        const float f = scale < 0.f ? -pow2(15 - e) : pow2(15 - e);
-        qs = top >= 0x7f80u ? 1.f : pow2(e - 15);
-        poison = top >= 0x7f80u;
-        const int r = quad * 32 + lane;
-        const uint32_t dst = sq + tile * (kTile * kD * 2) + r * 128;
-#pragma unroll
-        for (int x = 0; x < 16; ++x)
-          sts128(dst + (x >> 3) * (kTile * 128) + (((x & 7) ^ (r & 7)) << 4), pack_half2(lo_f(w[x].x) * f, hi_f(w[x].x) * f),
-                 pack_half2(lo_f(w[x].y) * f, hi_f(w[x].y) * f), pack_half2(lo_f(w[x].z) * f, hi_f(w[x].z) * f),
-                 pack_half2(lo_f(w[x].w) * f, hi_f(w[x].w) * f));
         proxy_fence();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[tile]));
@@ -314,15 +344,13 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
 
       float M = -INFINITY, L = 0.f;
       for (int step = 0; step < my_steps; ++step, ++done) {
-        ok = ok && mbar_wait(smem_u32(&sm.s_full[tile]), done & 1, abort, a.err);
-        ok = __all_sync(0xffffffffu, ok);
+        warp_wait(ok, smem_u32(&sm.s_full[tile]), done & 1, abort, a.err);
         if (!ok) continue;
         const StepMeta& me = sm.meta[(count + step) & 3];
         const int halves = s.from + 2 * step + 1 < s.to ? 2 : 1;
         if (s.from + 2 * step + halves > s.u.pages) {  // the tail's values have a scale of their own, known once loaded
           const uint32_t c = count + step;
-          ok = ok && mbar_wait(smem_u32(&sm.v_full[c & 1]), c >> 1 & 1, abort, a.err);
-          ok = __all_sync(0xffffffffu, ok);
+          warp_wait(ok, smem_u32(&sm.v_full[c & 1]), c >> 1 & 1, abort, a.err);
           if (!ok) continue;
         }
         tmem_after();
@@ -364,8 +392,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           L *= f;
           uint32_t y[8];
           if (step > 0) {
-            ok = ok && mbar_wait(smem_u32(&sm.pv_done[tile]), (done - 1) & 1, abort, a.err);
-            ok = __all_sync(0xffffffffu, ok);
+            warp_wait(ok, smem_u32(&sm.pv_done[tile]), (done - 1) & 1, abort, a.err);
             if (!ok) return;
             tmem_after();
 #pragma unroll 1
@@ -465,40 +492,68 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       if (poison) L = __uint_as_float(0x7fc00000u);
       if (s.limit(tile)) {
         if (my_steps) {
-          ok = ok && mbar_wait(smem_u32(&sm.pv_done[tile]), (done - 1) & 1, abort, a.err);
-          ok = __all_sync(0xffffffffu, ok);
+          warp_wait(ok, smem_u32(&sm.pv_done[tile]), (done - 1) & 1, abort, a.err);
           tmem_after();
         }
         const bool whole = s.from == 0 && s.to == s.u.items;
-        const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
-        float* part = partials + ((int64_t)(2 * cta + (s.from == 0 ? 1 : 0)) * kBlockRows + tile * kTile + quad * 32 + lane) * kPartialStride;
-        if (!whole && mine) *reinterpret_cast<float2*>(part) = make_float2(M, L);
+        float* part = partials + ((int64_t)(2 * cta + (s.from == 0 ? 1 : 0)) * kBlockRows + tile * kTile + quad * 32) * kPartialStride;
+        if (!whole && mine) *reinterpret_cast<float2*>(part + lane * kPartialStride) = make_float2(M, L);
         __syncwarp();
         if (my_steps && ok) {
-          uint16_t* dst = out.p + (int64_t)(s.u.row0 + i) * out.ts + (int64_t)head * out.hs;
-          for (int c = 0; c < kD; c += 32) {
-            uint32_t y[32];
-            tmem_load32(O + c, y);
-            tmem_loaded();
-            settle32(y);
-            if (mine && whole) {
+          // Rows go through the warp's own rows of Q, which no product reads any more, so that they are stored in
+          // runs of whole rows: 16-byte chunk c of row r at c ^ (r & 7), as everywhere.
+          const uint32_t stage = sq + tile * (kTile * kD * 2) + quad * 32 * 128;
+          if (whole) {
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t y[32];
+              tmem_load32(O + c * 32, y);
+              tmem_loaded();
+              settle32(y);
 #pragma unroll
-              for (int k = 0; k < 32; k += 8) {
+              for (int k = 0; k < 4; ++k) {
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(y[k + 2 * e]) * inv, __uint_as_float(y[k + 2 * e + 1]) * inv);
+                  const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(y[k * 8 + 2 * e]) * inv, __uint_as_float(y[k * 8 + 2 * e + 1]) * inv);
                   w[e] = *reinterpret_cast<const uint32_t*>(&v);
                 }
-                *reinterpret_cast<uint4*>(dst + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                sts128(stage + (c >> 1) * (kTile * 128) + lane * 128 + ((((c & 1) * 4 + k) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
               }
-            } else if (mine) {
-#pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                *reinterpret_cast<uint4*>(part + 4 + c + k) = make_uint4(y[k], y[k + 1], y[k + 2], y[k + 3]);
             }
             __syncwarp();
+            const uint64_t mine_at = reinterpret_cast<uint64_t>(out.p + (int64_t)(s.u.row0 + i) * out.ts + (int64_t)head * out.hs);
+            const int r2 = lane >> 4, c16 = lane & 15;
+#pragma unroll 4
+            for (int x = 0; x < 16; ++x) {
+              const int r = 2 * x + r2;
+              const uint64_t at = __shfl_sync(0xffffffffu, mine_at, r);
+              const bool there = __shfl_sync(0xffffffffu, (int)mine, r);
+              const uint4 v = lds128(stage + (c16 >> 3) * (kTile * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4));
+              if (there) reinterpret_cast<uint4*>(at)[c16] = v;
+            }
+          } else {
+            const int rows = min(32, s.u.n_new * a.G - (s.first_row + tile * kTile + quad * 32));  // the warp's
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t y[32];
+              tmem_load32(O + c * 32, y);
+              tmem_loaded();
+              settle32(y);
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 8; ++k) sts128(stage + lane * 128 + ((k ^ (lane & 7)) << 4), y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const int r = 4 * x + (lane >> 3), k = lane & 7;
+                const uint4 v = lds128(stage + r * 128 + ((k ^ (r & 7)) << 4));
+                if (r < rows) *reinterpret_cast<uint4*>(part + r * kPartialStride + 4 + c * 32 + k * 4) = v;
+              }
+            }
           }
+          __syncwarp();
           tmem_before();
         }
       }
@@ -510,7 +565,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
     // ------------------------------ loaders: four warps of keys, four of values ------------------------------
     // Warp w has rows 16 w .. 16 w + 15 of every page. In load x, eight lanes have 64 bytes of two neighbouring
     // rows each: their 16-byte stores then fall on eight different columns of the swizzle.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     const int half = warp >= kValueWarp ? 1 : 0;
     const int w4 = warp & 3, c4 = lane & 3, row0 = w4 * 16 + (lane >> 3) * 2 + (lane >> 2 & 1);
     const uint32_t operand0 = half ? sv : sk;
@@ -621,8 +676,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         const uint32_t slot = count & 1, at = operand0 + slot * 16384;
         const int it = s.from + 2 * step, tail = s.u.pages - it;  // the tail's place, if it is in this step
         StepMeta& me = sm.meta[count & 3];
-        ok = ok && mbar_wait(smem_u32(&empty[slot]), (count >> 1 & 1) ^ 1, abort, a.err);
-        ok = __all_sync(0xffffffffu, ok);
+        warp_wait(ok, smem_u32(&empty[slot]), (count >> 1 & 1) ^ 1, abort, a.err);
         if (ok) {
           if (!half) {  // what the softmax has to know of the pages
 #pragma unroll
@@ -660,12 +714,11 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
     }
   } else {
     // ------------------------------ products ------------------------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == kMmaWarp) {
       const uint32_t leader = elect();
       auto wait = [&](const uint64_t& bar, uint32_t parity) {
-        ok = ok && mbar_wait(smem_u32(&bar), parity, abort, a.err);
-        ok = __all_sync(0xffffffffu, ok);
+        warp_wait(ok, smem_u32(&bar), parity, abort, a.err);
       };
       uint32_t count = 0, q_phase = 0, p_phase = 0;  // phases: a bit per tile
       const uint64_t dq = operand(sq, 16, 1024), dk = operand(sk, 16, 1024), dv = operand(sv, kPlane, 1024);
@@ -685,17 +738,15 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         if (add) mma_ts<true>(leader, d, p, v0, shape(kD, true));
         else mma_ts<false>(leader, d, p, v0, shape(kD, true));
 #pragma unroll
-        for (int k = 1; k < 4; ++k) mma_ts<true>(leader, d, p + k * 8, v0 + k * (2048 >> 4), shape(kD, true));
-        if (pages == 2) {
-#pragma unroll
-          for (int k = 4; k < 8; ++k) mma_ts<true>(leader, d, p + kPart + (k - 4) * 8, v0 + k * (2048 >> 4), shape(kD, true));
-        }
+        for (int k = 1; k < 8; ++k) if (k < 4 * pages)
+          mma_ts<true>(leader, d, p + (k >> 2) * kPart + (k & 3) * 8, v0 + k * (2048 >> 4), shape(kD, true));
         mma_commit(leader, smem_u32(&sm.pv_done[tile]));
       };
       while (next()) {
         const Segment& s = sm.segs[seg % kSegments];
         auto pages_of = [&](int step) { return min(2, s.to - s.from - 2 * step); };
         wait(sm.k_full[count & 1], count >> 1 & 1);
+#pragma unroll 1
         for (int t = 0; t < 2; ++t)
           if (s.active(t, 0)) {
             wait(sm.q_full[t], q_phase >> t & 1);
@@ -709,6 +760,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           const bool more = step + 1 < s.steps;
           wait(sm.v_full[count & 1], count >> 1 & 1);
           if (more) wait(sm.k_full[(count + 1) & 1], (count + 1) >> 1 & 1);
+#pragma unroll 1
           for (int t = 0; t < 2; ++t) {
             if (s.active(t, step)) {
               wait(sm.p_full[t], p_phase >> t & 1);
@@ -731,9 +783,32 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         wait(sm.v_empty[(count - 1) & 1], (count - 1) >> 1 & 1);
       }
     }
+    int block = 0;
+    int64_t before = pl.before;
+    if (warp == kPlanWarp && pl.b < a.B) {  // the share's first block, 32 at a time
+      const int64_t at = share_start(pl.total, cta, ctas);
+      Unit u = request_of(a, pl.b, false);
+      for (;; block += 32) {
+        set_rows(a, u, min((int64_t)(block + lane) * kBlockRows, (int64_t)0x7fffff00), kBlockRows, topk);
+        const int64_t mine = (int64_t)u.weight * a.Hkv;
+        int64_t sum = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += x;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, mine == 0 || at < before + sum);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          before += __shfl_sync(0xffffffffu, sum - mine, l);
+          block += l;
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, sum, 31);
+      }
+    }
     if (warp == kPlanWarp && lane == 0) {
-      int b = pl.b, block = 0;
-      int64_t at = share_start(pl.total, cta, ctas), before = pl.before;
+      int b = pl.b;
+      int64_t at = share_start(pl.total, cta, ctas);
       const int64_t stop = share_start(pl.total, cta + 1, ctas);
       JoinRecord open = JoinRecord{};
       Segment s;
@@ -784,11 +859,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
   __syncthreads();
   tmem_after();
   if (warp == kMmaWarp) {
-    if (*abort) {  // products may be in flight: give them time to end before their memory goes
-      const unsigned long long t0 = now_ns();
-      while (now_ns() - t0 < kWaitNs / 8) {
-      }
-    }
+    if (*abort) settle_down();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }

@@ -35,27 +35,27 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-__device__ __forceinline__ unsigned long long now_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
+// A try that may suspend the thread for up to a microsecond.
+__device__ __forceinline__ bool mbar_try_1us(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000)
+      : "memory");
+  return ok != 0;
 }
 
-constexpr unsigned long long kWaitNs = 2000000000ull;
-
-// Waits until the phase with this parity has completed. Bounded: after kWaitNs, or once another
-// wait of the CTA has run out, it returns false with *abort (shared memory) set. A try suspends the
-// thread for a while by itself; the timer, which is slow to read, is looked at every 1024 of them.
+// Waits until the phase with this parity has completed. Bounded: after 2^21 tries (of about a
+// microsecond at most), or once another wait of the CTA has run out, it returns false with *abort
+// (shared memory) set.
 __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
-  unsigned long long t0 = 0;
-  for (uint32_t it = 1; it < (1u << 30); ++it) {
-    if (mbar_try(bar, parity)) return true;
-    if ((it & 1023u) == 0) {
-      if (*abort) return false;
-      const unsigned long long t = now_ns();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > kWaitNs) break;
-    }
+#pragma unroll 1
+  for (uint32_t it = 0; it < (1u << 21); ++it) {
+    if (mbar_try_1us(bar, parity)) return true;
+    if (*abort) return false;
   }
   *abort = 1;
   atomicOr(err, (uint32_t)kErrTimeout);
@@ -65,6 +65,18 @@ __device__ __forceinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, vo
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   if (mbar_try(bar, parity)) return true;
   return mbar_wait_slow(bar, parity, abort, err);
+}
+
+// After a wait has run out: copies and products in flight are given a quarter of a second to end before
+// the memory that they use goes.
+__device__ __forceinline__ void settle_down() {
+  for (int i = 0; i < 250000; ++i) __nanosleep(1000);
+}
+
+// The same by a whole warp; `ok` is one for all lanes, and no wait succeeds once it is false.
+__device__ __forceinline__ void warp_wait(bool& ok, uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+  const bool there = mbar_try(bar, parity);
+  if (!__all_sync(0xffffffffu, there && ok)) ok = __all_sync(0xffffffffu, ok && mbar_wait_slow(bar, parity, abort, err));
 }
 
 // A whole page [2][64] rows of 128 bytes, 16-byte chunk c of row r at chunk c ^ (r & 7).
