@@ -18,6 +18,9 @@
 //   17        walks the CTA's share of the work and announces its segments;
 //   16        issues the products: P_0 V, S_0, P_1 V, S_1 of each step, so that one tile's softmax
 //             runs under the other's products.
+// A block of at most 128 rows (drafted tokens, the end of a prompt) is held by both tiles, which take the
+// steps in turn, so that the one's softmax still runs under the other's products; tile 1's result is
+// joined to tile 0's through shared memory at the end.
 // Tensor memory: O_0, O_1, S_0, S_1 of 128 columns each. Shared memory: Q_0, Q_1 and two steps of
 // K and of V, 32 KB each.
 //
@@ -47,8 +50,9 @@ struct Segment {
   Unit u;
   int b, h, first_row, from, to;
   int steps;           // of two items each; 0: the share is done
-  int limit0, limit1;  // items that a tile's last row may see; 0: the tile has no rows
+  int limit0, limit1;  // items that a tile's last row may see; limit1 0: it has none, and the tiles share tile 0's
   __device__ __forceinline__ int limit(int tile) const { return tile ? limit1 : limit0; }
+  __device__ __forceinline__ bool shared() const { return limit1 == 0; }
   __device__ __forceinline__ bool active(int tile, int step) const { return from + 2 * step < min(to, limit(tile)); }
 };
 constexpr int kSegments = 4;  // announced ahead
@@ -297,13 +301,15 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
     uint32_t count = 0;   // steps of the CTA so far
     while (next()) {
       const Segment& s = sm.segs[seg % kSegments];
-      const int row = s.first_row + tile * kTile + quad * 32 + lane;
+      const bool shared = s.shared();  // both tiles have tile 0's rows, and every second step
+      const int row = s.first_row + (shared ? 0 : tile * kTile) + quad * 32 + lane;
       const bool mine = row < s.u.n_new * a.G;
       const int i = row / a.G, head = s.h * a.G + row - i * a.G;
       const int see = mine ? s.u.past + i + 1 : 0x7fffffff;  // rows that are not there see all: no masks for them
       float qs = 1.f;
       bool poison = false;  // the row's result is NaN
-      const int my_steps = s.limit(tile) ? max(0, (min(s.to, s.limit(tile)) - s.from + 1) / 2) : 0;
+      const int all_steps = max(0, (min(s.to, shared ? s.limit0 : s.limit(tile)) - s.from + 1) / 2);
+      const int my_steps = shared ? (all_steps - tile + 1) / 2 : all_steps;
       if (my_steps) {
         // The warp's 32 rows, two at a time: 16 lanes have 16 bytes each of a row, whose largest element gives
         // the power of two that puts it into fp16's range (and back out: qs). scale's sign goes here too.
@@ -343,7 +349,8 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       }
 
       float M = -INFINITY, L = 0.f;
-      for (int step = 0; step < my_steps; ++step, ++done) {
+      for (int turn = 0; turn < my_steps; ++turn, ++done) {
+        const int step = shared ? 2 * turn + tile : turn;
         warp_wait(ok, smem_u32(&sm.s_full[tile]), done & 1, abort, a.err);
         if (!ok) continue;
         const StepMeta& me = sm.meta[(count + step) & 3];
@@ -391,7 +398,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         auto rescale = [&](float f, bool page) {
           L *= f;
           uint32_t y[8];
-          if (step > 0) {
+          if (turn > 0) {
             warp_wait(ok, smem_u32(&sm.pv_done[tile]), (done - 1) & 1, abort, a.err);
             if (!ok) return;
             tmem_after();
@@ -490,73 +497,115 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
 
       // ---- the row's end ----
       if (poison) L = __uint_as_float(0x7fc00000u);
-      if (s.limit(tile)) {
-        if (my_steps) {
-          warp_wait(ok, smem_u32(&sm.pv_done[tile]), (done - 1) & 1, abort, a.err);
-          tmem_after();
+      if (my_steps) {
+        warp_wait(ok, smem_u32(&sm.pv_done[tile]), (done - 1) & 1, abort, a.err);
+        tmem_after();
+      }
+      // Rows go through the warp's own rows of Q, which no product reads any more, so that they are stored in
+      // runs of whole rows: 16-byte chunk c of row r at c ^ (r & 7), as everywhere.
+      const uint32_t stage = sq + tile * (kTile * kD * 2) + quad * 32 * 128;
+      // Tile 1's half of a shared block crosses over there too, 32 columns at a time, between the two warps of
+      // a row: M and L in the second plane, the output in the first.
+      const uint32_t other = sq + kTile * kD * 2 + quad * 32 * 128;
+      auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); };
+      float f0 = 1.f, f1 = 0.f;  // the tiles' weights
+      if (shared && tile == 1) {
+        asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(other + kTile * 128 + lane * 8), "f"(M), "f"(L) : "memory");
+        pair_sync();
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t y[32];
+          tmem_load32(O + c * 32, y);
+          tmem_loaded();
+          settle32(y);
+          if (c) pair_sync();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sts128(other + lane * 128 + ((k ^ (lane & 7)) << 4), y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+          pair_sync();
         }
+      } else if (shared) {
+        pair_sync();
+        float m1, l1;
+        asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(m1), "=f"(l1) : "r"(other + kTile * 128 + lane * 8));
+        const float top = fmaxf(M, m1), at = top == -INFINITY ? 0.f : top;
+        f0 = ex2(M - at);
+        f1 = ex2(m1 - at);
+        L = L * f0 + l1 * f1;
+        M = top;
+      }
+      // 32 columns of the row's output
+      auto columns = [&](int c, uint32_t* y) {
+        tmem_load32(O + c * 32, y);
+        tmem_loaded();
+        settle32(y);
+        if (!shared) return;
+        pair_sync();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint4 v = lds128(other + lane * 128 + ((k ^ (lane & 7)) << 4));
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // (a tile that has seen nothing has nothing in its columns)
+            const float y0 = f0 == 0.f ? 0.f : __uint_as_float(y[4 * k + e]) * f0, y1 = f1 == 0.f ? 0.f : __uint_as_float(w[e]) * f1;
+            y[4 * k + e] = __float_as_uint(y0 + y1);
+          }
+        }
+        if (c < 3) pair_sync();
+      };
+      if (shared ? tile == 0 : s.limit(tile) > 0) {
         const bool whole = s.from == 0 && s.to == s.u.items;
         float* part = partials + ((int64_t)(2 * cta + (s.from == 0 ? 1 : 0)) * kBlockRows + tile * kTile + quad * 32) * kPartialStride;
         if (!whole && mine) *reinterpret_cast<float2*>(part + lane * kPartialStride) = make_float2(M, L);
         __syncwarp();
-        if (my_steps && ok) {
-          // Rows go through the warp's own rows of Q, which no product reads any more, so that they are stored in
-          // runs of whole rows: 16-byte chunk c of row r at c ^ (r & 7), as everywhere.
-          const uint32_t stage = sq + tile * (kTile * kD * 2) + quad * 32 * 128;
-          if (whole) {
-            const float inv = L == 0.f ? 0.f : 1.f / L;
+        if (whole) {
+          const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t y[32];
-              tmem_load32(O + c * 32, y);
-              tmem_loaded();
-              settle32(y);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t y[32];
+            columns(c, y);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint32_t w[4];
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(y[k * 8 + 2 * e]) * inv, __uint_as_float(y[k * 8 + 2 * e + 1]) * inv);
-                  w[e] = *reinterpret_cast<const uint32_t*>(&v);
-                }
-                sts128(stage + (c >> 1) * (kTile * 128) + lane * 128 + ((((c & 1) * 4 + k) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(y[k * 8 + 2 * e]) * inv, __uint_as_float(y[k * 8 + 2 * e + 1]) * inv);
+                w[e] = *reinterpret_cast<const uint32_t*>(&v);
               }
-            }
-            __syncwarp();
-            const uint64_t mine_at = reinterpret_cast<uint64_t>(out.p + (int64_t)(s.u.row0 + i) * out.ts + (int64_t)head * out.hs);
-            const int r2 = lane >> 4, c16 = lane & 15;
-#pragma unroll 4
-            for (int x = 0; x < 16; ++x) {
-              const int r = 2 * x + r2;
-              const uint64_t at = __shfl_sync(0xffffffffu, mine_at, r);
-              const bool there = __shfl_sync(0xffffffffu, (int)mine, r);
-              const uint4 v = lds128(stage + (c16 >> 3) * (kTile * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4));
-              if (there) reinterpret_cast<uint4*>(at)[c16] = v;
-            }
-          } else {
-            const int rows = min(32, s.u.n_new * a.G - (s.first_row + tile * kTile + quad * 32));  // the warp's
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t y[32];
-              tmem_load32(O + c * 32, y);
-              tmem_loaded();
-              settle32(y);
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 8; ++k) sts128(stage + lane * 128 + ((k ^ (lane & 7)) << 4), y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-              __syncwarp();
-#pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                const int r = 4 * x + (lane >> 3), k = lane & 7;
-                const uint4 v = lds128(stage + r * 128 + ((k ^ (r & 7)) << 4));
-                if (r < rows) *reinterpret_cast<uint4*>(part + r * kPartialStride + 4 + c * 32 + k * 4) = v;
-              }
+              sts128(stage + (c >> 1) * (kTile * 128) + lane * 128 + ((((c & 1) * 4 + k) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
             }
           }
           __syncwarp();
-          tmem_before();
+          const uint64_t mine_at = reinterpret_cast<uint64_t>(out.p + (int64_t)(s.u.row0 + i) * out.ts + (int64_t)head * out.hs);
+          const int r2 = lane >> 4, c16 = lane & 15;
+#pragma unroll 4
+          for (int x = 0; x < 16; ++x) {
+            const int r = 2 * x + r2;
+            const uint64_t at = __shfl_sync(0xffffffffu, mine_at, r);
+            const bool there = __shfl_sync(0xffffffffu, (int)mine, r);
+            const uint4 v = lds128(stage + (c16 >> 3) * (kTile * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4));
+            if (there && ok) reinterpret_cast<uint4*>(at)[c16] = v;
+          }
+        } else {
+          const int rows = min(32, s.u.n_new * a.G - (s.first_row + tile * kTile + quad * 32));  // the warp's
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t y[32];
+            columns(c, y);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sts128(stage + lane * 128 + ((k ^ (lane & 7)) << 4), y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const int r = 4 * x + (lane >> 3), k = lane & 7;
+              const uint4 v = lds128(stage + r * 128 + ((k ^ (r & 7)) << 4));
+              if (r < rows && my_steps) *reinterpret_cast<uint4*>(part + r * kPartialStride + 4 + c * 32 + k * 4) = v;
+            }
+          }
         }
+        __syncwarp();
       }
+      tmem_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[seg % kSegments]));
       ++seg;
@@ -745,6 +794,38 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       while (next()) {
         const Segment& s = sm.segs[seg % kSegments];
         auto pages_of = [&](int step) { return min(2, s.to - s.from - 2 * step); };
+        if (s.shared()) {  // the tiles take the steps in turn
+          const int steps = s.steps;
+#pragma unroll 1
+          for (int step = -2; step < steps; ++step) {
+            const int t = step & 1;
+            if (step >= 0) {
+              const uint32_t c = count + step;
+              wait(sm.v_full[c & 1], c >> 1 & 1);
+              wait(sm.p_full[t], p_phase >> t & 1);
+              p_phase ^= 1u << t;
+              tmem_after();
+              if (ok) values(t, c, pages_of(step), step >= 2);
+              if (ok) mma_commit(leader, smem_u32(&sm.v_empty[c & 1]));
+            }
+            if (step + 2 < steps) {
+              const uint32_t c = count + step + 2;
+              wait(sm.k_full[c & 1], c >> 1 & 1);
+              if (step < 0) {
+                wait(sm.q_full[t], q_phase >> t & 1);
+                q_phase ^= 1u << t;
+                tmem_after();
+              }
+              if (ok) scores(t, c, pages_of(step + 2));
+              if (ok) mma_commit(leader, smem_u32(&sm.k_empty[c & 1]));
+            }
+          }
+          count += steps;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[seg % kSegments]));
+          ++seg;
+          continue;
+        }
         wait(sm.k_full[count & 1], count >> 1 & 1);
 #pragma unroll 1
         for (int t = 0; t < 2; ++t)
