@@ -646,18 +646,13 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         }
       };
       uint4 raw[8];  // of two pages, four loads each
-      auto load = [&](int step) {  // (32 items are a whole number of steps)
-        const int it = s.from + 2 * step;
-        if (it >= id_base + 32) look(it);
+      auto load = [&](int it, int pg) {
+        const int page = it < pages ? __shfl_sync(0xffffffffu, id, it - id_base) : -1;
+        const uint8_t* src = a.pages + (int64_t)page * kKv8PageBytes + half * kKv8HalfBytes + row0 * kD + c4 * 16;
 #pragma unroll
-        for (int pg = 0; pg < 2; ++pg) {
-          const int page = it + pg < pages ? __shfl_sync(0xffffffffu, id, it + pg - id_base) : -1;
-          const uint8_t* src = a.pages + (int64_t)page * kKv8PageBytes + half * kKv8HalfBytes + row0 * kD + c4 * 16;
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            raw[pg * 4 + x] = page >= 0 ? __ldcg(reinterpret_cast<const uint4*>(src + (x >> 1) * 8 * kD + (x & 1) * 64))
-                                        : make_uint4(0, 0, 0, 0);
-        }
+        for (int x = 0; x < 4; ++x)
+          raw[pg * 4 + x] = page >= 0 ? __ldcg(reinterpret_cast<const uint4*>(src + (x >> 1) * 8 * kD + (x & 1) * 64))
+                                      : make_uint4(0, 0, 0, 0);
       };
       auto put_page = [&](uint32_t at, int pg) {
 #pragma unroll
@@ -720,7 +715,8 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         }
       };
       look(s.from);
-      load(0);
+      load(s.from, 0);
+      load(s.from + 1, 1);
       for (int step = 0; step < s.steps; ++step, ++count) {
         const uint32_t slot = count & 1, at = operand0 + slot * 16384;
         const int it = s.from + 2 * step, tail = s.u.pages - it;  // the tail's place, if it is in this step
@@ -748,14 +744,18 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
               }
             }
           }
+          // (32 items are a whole number of steps) the next step's loads, each as soon as its registers are free
+          const bool more = it + 2 < pages;
+          if (more && it + 2 >= id_base + 32) look(it + 2);
           if (tail > 0) put_page(at, 0);
+          if (more) load(it + 2, 0);
           if (tail > 1 && it + 1 < s.to) put_page(at, 1);
+          if (more) load(it + 3, 1);
           if (tail <= 1 && it + tail < s.to) put_tail(at, tail, me);
           proxy_fence();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&full[slot]));
         }
-        if (step + 1 < s.steps) load(step + 1);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[seg % kSegments]));
