@@ -2,20 +2,22 @@
 // and values to the 8-bit paged cache, in one launch.
 //
 // A pair (x0, x1) at position n turns by n * f_j: y0 = x0 cos - x1 sin, y1 = x0 sin + x1 cos.
-// The angle is n * step mod 2^64 in 2^-64 turns. Its top 8 bits pick one of 256 tabulated angles
-// a, the rest is |d| <= 2 pi / 512, and cos(a + d) = cos a + (cos a (cos d - 1) - sin a sin d)
-// with short Taylor sums of cos d - 1 and sin d: as a pair (16 tabulated bits, a float), cos and
-// sin are right to 2^-30. Keys use the pair (16 bits x 8 bits of a bf16 are exact in fp32), so
-// that a key's bf16, and through it the page's codes, is the exact product's rounding in all but
-// about 2^-17 of the elements; queries use the plain fp32 sum.
+// The angle is n * step mod 2^64 in 2^-64 turns. Its top 6 bits pick one of 64 tabulated angles a, the
+// rest is |d| <= 2 pi / 128, and cos(a + d) = cos a + (cos a (cos d - 1) - sin a sin d) with short
+// Taylor sums of cos d - 1 and sin d: as a pair (16 tabulated bits, a float), cos and sin are right to
+// 2^-28. Keys use the pair (16 bits x 8 bits of a bf16 are exact in fp32), so that a key's bf16, and
+// through it the page's codes, is the exact product's rounding in all but about 2^-16 of the
+// elements; queries use the plain fp32 sum. (A table of 256 entries has 2 bits more, and its gathers touch
+// four times the L1 lines.)
 //
 // The work is memory bound: a prompt token reads (Hq + 2 Hkv) rows of 256 bytes and writes Hq
 // rows and 2 Hkv rows of 128. Two kinds of CTAs share the launch:
+//   rows (one warp per token and some of its heads): queries, and the keys and values that stay in
+//     bf16. Eight lanes a row, so a lane's angles serve all heads of its token; two passes' loads at
+//     a time;
 //   page items (one CTA per completed page and KV head): 64 rows of keys and values in registers,
 //     8 lanes a row with 16 elements each, one maximum over them, codes out. The page's maximum
-//     is what its elements wait for, so nothing is read twice;
-//   rows (one warp per token and some of its heads): queries, and the keys and values that stay in
-//     bf16. Eight lanes a row again, so a lane's angles serve all heads of its token.
+//     is what its elements wait for, so nothing is read twice.
 // A request that completes a page leaves its remaining rows to the page item of its first
 // completed page, which has read the old tail by then: no other CTA touches that tail.
 #include "kv8.cuh"
@@ -26,12 +28,15 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// cos and sin of 2 pi i / 256: hi a multiple of 2^-15, lo the rest.
+constexpr int kTurnBits = 6;
+constexpr int kTurns = 1 << kTurnBits;
+
+// cos and sin of 2 pi i / kTurns: hi a multiple of 2^-15, lo the rest.
 struct Turn {
   float ch, cl, sh, sl;
 };
 struct alignas(16) TurnTable {
-  Turn t[256];
+  Turn t[kTurns];
 };
 
 constexpr double taylor(double x, bool sine) {
@@ -47,12 +52,12 @@ constexpr double hi_part(double x) { return (double)(long long)(x * 32768.0) / 3
 
 constexpr TurnTable make_turns() {
   TurnTable r{};
-  for (int i = 0; i < 256; ++i) {
+  for (int i = 0; i < kTurns; ++i) {
     // the first octant's values, mirrored: exact zeros and ones on the axes
-    const int q = i >> 6, m = i & 63;
-    const double step = 6.283185307179586476925 / 256.0;
-    const double a = m <= 32 ? taylor(m * step, false) : taylor((64 - m) * step, true);
-    const double b = m <= 32 ? taylor(m * step, true) : taylor((64 - m) * step, false);
+    const int quarter = kTurns / 4, q = i / quarter, m = i % quarter;
+    const double step = 6.283185307179586476925 / kTurns;
+    const double a = 2 * m <= quarter ? taylor(m * step, false) : taylor((quarter - m) * step, true);
+    const double b = 2 * m <= quarter ? taylor(m * step, true) : taylor((quarter - m) * step, false);
     const double c = q == 0 ? a : q == 1 ? -b : q == 2 ? -a : b;
     const double s = q == 0 ? b : q == 1 ? a : q == 2 ? -b : -a;
     r.t[i].ch = (float)hi_part(c);
@@ -66,10 +71,10 @@ constexpr TurnTable make_turns() {
 __device__ const TurnTable g_turns = make_turns();
 
 __device__ __forceinline__ Turn turn_of(uint64_t phase) {
-  const uint32_t i = (uint32_t)((phase + (1ull << 55)) >> 56);  // nearest tabulated angle, mod 256
-  const int64_t d = (int64_t)(phase - ((uint64_t)i << 56));     // [-2^55, 2^55) turns / 2^64
-  const float4 t = __ldg(reinterpret_cast<const float4*>(&g_turns.t[i & 255]));
-  const float x = (float)(int32_t)(d >> 24) * (6.2831853071795865f / 1099511627776.f);  // radians; 2^40
+  const uint32_t i = (uint32_t)((phase + (1ull << (63 - kTurnBits))) >> (64 - kTurnBits));  // nearest, mod kTurns
+  const int64_t d = (int64_t)(phase - ((uint64_t)i << (64 - kTurnBits)));                   // within half a step
+  const float4 t = __ldg(reinterpret_cast<const float4*>(&g_turns.t[i & (kTurns - 1)]));
+  const float x = (float)(int32_t)(d >> 26) * (6.2831853071795865f / 274877906944.f);  // radians; 2^38
   const float x2 = x * x;
   const float sd = fmaf(x * x2, fmaf(x2, 1.f / 120.f, -1.f / 6.f), x);
   const float cd = x2 * fmaf(x2, 1.f / 24.f, -0.5f);  // cos d - 1
@@ -123,15 +128,9 @@ __device__ __forceinline__ void lane_chunks(const RopeArgs& r, int i, int& c0, i
   }
 }
 
-__device__ __forceinline__ void lane_turns(const RopeArgs& r, int i, int64_t pos, Turn (&t)[8]) {
-  if (8 * i < r.half) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) t[j] = turn_of((uint64_t)pos * r.step[8 * i + j]);
-  }
-}
-
-template <bool EXACT>
-__device__ __forceinline__ void lane_rotate(const RopeArgs& r, int i, const Turn (&t)[8], uint4& a, uint4& b) {
+// The lane's pairs of a row, turned: pair j of turn(j).
+template <bool EXACT, typename T>
+__device__ __forceinline__ void lane_rotate(const RopeArgs& r, int i, T turn, uint4& a, uint4& b) {
   if (8 * i >= r.half) return;
   uint32_t* wa = reinterpret_cast<uint32_t*>(&a);
   uint32_t* wb = reinterpret_cast<uint32_t*>(&b);
@@ -139,21 +138,36 @@ __device__ __forceinline__ void lane_rotate(const RopeArgs& r, int i, const Turn
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float y0, y1;
-      rotate_pair<EXACT>(lo_f(wa[j]), hi_f(wa[j]), t[j], y0, y1);
+      rotate_pair<EXACT>(lo_f(wa[j]), hi_f(wa[j]), turn(j), y0, y1);
       wa[j] = pack(y0, y1);
-      rotate_pair<EXACT>(lo_f(wb[j]), hi_f(wb[j]), t[4 + j], y0, y1);
+      rotate_pair<EXACT>(lo_f(wb[j]), hi_f(wb[j]), turn(4 + j), y0, y1);
       wb[j] = pack(y0, y1);
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float y0, y1, z0, z1;
-      rotate_pair<EXACT>(lo_f(wa[j]), lo_f(wb[j]), t[2 * j], y0, y1);
-      rotate_pair<EXACT>(hi_f(wa[j]), hi_f(wb[j]), t[2 * j + 1], z0, z1);
+      rotate_pair<EXACT>(lo_f(wa[j]), lo_f(wb[j]), turn(2 * j), y0, y1);
+      rotate_pair<EXACT>(hi_f(wa[j]), hi_f(wb[j]), turn(2 * j + 1), z0, z1);
       wa[j] = pack(y0, z0);
       wb[j] = pack(y1, z1);
     }
   }
+}
+
+// A key's row: the angles are worked out one by one, which holds few registers. One copy of it: a short call is
+// over before the code of four would have been fetched.
+struct TwoChunks {
+  uint4 a, b;
+};
+__device__ __noinline__ TwoChunks rotate_key(const RopeArgs& r, int i, int64_t pos, TwoChunks x) {
+  lane_rotate<true>(r, i, [&](int j) { return turn_of((uint64_t)pos * r.step[8 * i + j]); }, x.a, x.b);
+  return x;
+}
+__device__ __forceinline__ void lane_rotate_key(const RopeArgs& r, int i, int64_t pos, uint4& a, uint4& b) {
+  const TwoChunks y = rotate_key(r, i, pos, TwoChunks{a, b});
+  a = y.a;
+  b = y.b;
 }
 
 // The largest b in [0, B) with f(b) <= x, for ascending f with f(0) <= x; any b in range otherwise.
@@ -222,25 +236,27 @@ __device__ __forceinline__ int64_t position(const RopeArgs& r, int row, int64_t 
   return r.positions ? (int64_t)r.positions[row] : fallback;
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 kv8_append_kernel(const Kv8Args a, const __grid_constant__ RopeArgs r, const Rows q, const Rows q_out, const Rows k,
-                  const Rows v, int page_items, int iters) {
+                  const Rows v, int row_ctas, int iters) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int i8 = lane & 7;
   int c0, c1;
   lane_chunks(r, i8, c0, c1);
 
-  if ((int)blockIdx.x < page_items) {
+  if ((int)blockIdx.x >= row_ctas) {
     // ---- a completed page of one head ----
     // Request b owns the items cu[b] / 64 + b .. : its completed pages are at most
-    // (63 + new) / 64, which is no more than the items before request b + 1.
+    // (63 + new) / 64, which is no more than the items before request b + 1. With one new token a
+    // request at most, request b has item b.
     __shared__ uint32_t s_max[2][kThreads / 32];
     __shared__ __align__(16) uint16_t s_keys[kPart * kD];
-    const int item = (int)blockIdx.x / a.Hkv, h = (int)blockIdx.x - item * a.Hkv;
-    const int b = warp_find(a.B, item, [&](int x) { return (a.cu[x] >> 6) + x; });
+    const int place = (int)blockIdx.x - row_ctas, item = place / a.Hkv, h = place - item * a.Hkv;
+    const bool single = a.max_new == 1;
+    const int b = single ? item : warp_find(a.B, item, [&](int x) { return (a.cu[x] >> 6) + x; });
     int row0, n_new, past;
     if (!kv8_request(a, b, false, row0, n_new, past)) return;
-    const int j = item - ((row0 >> 6) + b);
+    const int j = single ? 0 : item - ((row0 >> 6) + b);
     const int old = past & (kPart - 1);             // rows in the tail
     const int p0 = past >> 6;
     const int n_done = (old + n_new) >> 6;          // pages completed by this step
@@ -275,9 +291,7 @@ kv8_append_kernel(const Kv8Args a, const __grid_constant__ RopeArgs r, const Row
       const int row = u * 32 + (tid >> 3);
       const int t = j * kPart + row - old;
       if (t >= 0) {
-        Turn turns[8];
-        lane_turns(r, i8, position(r, row0 + t, (int64_t)past + t), turns);
-        lane_rotate<true>(r, i8, turns, kk[u][0], kk[u][1]);
+        lane_rotate_key(r, i8, position(r, row0 + t, (int64_t)past + t), kk[u][0], kk[u][1]);
       }
       mk = abs_max(abs_max(mk, kk[u][0]), kk[u][1]);
       mv = abs_max(abs_max(mv, vv[u][0]), vv[u][1]);
@@ -326,9 +340,7 @@ kv8_append_kernel(const Kv8Args a, const __grid_constant__ RopeArgs r, const Row
       for (int row = tid >> 3; row < rest; row += kThreads / 8) {
         const int t = n_done * kPart + row - old;
         uint4 x0 = *chunk(k, row0 + t, h, c0), x1 = *chunk(k, row0 + t, h, c1);
-        Turn turns[8];
-        lane_turns(r, i8, position(r, row0 + t, (int64_t)past + t), turns);
-        lane_rotate<true>(r, i8, turns, x0, x1);
+        lane_rotate_key(r, i8, position(r, row0 + t, (int64_t)past + t), x0, x1);
         uint4* dst = reinterpret_cast<uint4*>(tail + row * kD);
         dst[c0] = x0;
         dst[c1] = x1;
@@ -340,10 +352,10 @@ kv8_append_kernel(const Kv8Args a, const __grid_constant__ RopeArgs r, const Row
   }
 
   // ---- rows: queries, and keys and values of requests that complete no page ----
-  const int n_q = q.p ? a.Hq : 0;
-  const int groups = (n_q + 2 * a.Hkv + 3) / 4;  // of 4 rows: one warp pass
+  const int n_q = q.p ? a.Hq : 0, q_groups = (n_q + 3) / 4;  // of 4 rows: one warp pass
+  const int groups = q_groups + (2 * a.Hkv + 3) / 4;
   const int per_token = (groups + iters - 1) / iters;
-  const int64_t w = ((int64_t)blockIdx.x - page_items) * (kThreads / 32) + warp;
+  const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + warp;
   const int t = (int)(w / per_token);
   if (t >= a.total_new) return;
   const int part = (int)(w - (int64_t)t * per_token);
@@ -353,30 +365,51 @@ kv8_append_kernel(const Kv8Args a, const __grid_constant__ RopeArgs r, const Row
   int row0, n_new, past;
   const bool good = kv8_request(a, b, part == 0 && lane == 0, row0, n_new, past);
   if (!good || t < row0 || t >= row0 + n_new) return;  // padding, or a request that is left out
-  const bool stays = (past & (kPart - 1)) + n_new < kPart;
-  Turn turns[8];
-  lane_turns(r, i8, position(r, t, (int64_t)past + (t - row0)), turns);
-  const int g_end = min(groups, (part + 1) * iters);
-#pragma unroll 2
-  for (int g = part * iters; g < g_end; ++g) {
-    int row = g * 4 + (lane >> 3);
-    if (row < n_q) {
-      uint4 x0 = *chunk(q, t, row, c0), x1 = *chunk(q, t, row, c1);
-      lane_rotate<false>(r, i8, turns, x0, x1);
-      uint4* dst = reinterpret_cast<uint4*>(q_out.p + (int64_t)t * q_out.ts + (int64_t)row * q_out.hs);
-      dst[c0] = x0;
-      dst[c1] = x1;
-      continue;
+  const int64_t pos = position(r, t, (int64_t)past + (t - row0));
+  const int first = part * iters, last = min(groups, first + iters), sub = lane >> 3;
+  if (first < q_groups) {
+    float2 turns[8];
+    if (8 * i8 < r.half) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const Turn x = turn_of((uint64_t)pos * r.step[8 * i8 + j]);
+        turns[j] = make_float2(x.ch + x.cl, x.sh + x.sl);
+      }
     }
-    row -= n_q;
-    if (!stays || row >= 2 * a.Hkv) continue;
+    auto turn = [&](int j) { return Turn{turns[j].x, 0.f, turns[j].y, 0.f}; };
+    for (int g = first; g < min(last, q_groups); g += 2) {
+      uint4 x[2][2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = (g + k) * 4 + sub;
+        if (g + k < last && row < n_q) {
+          x[k][0] = *chunk(q, t, row, c0);
+          x[k][1] = *chunk(q, t, row, c1);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = (g + k) * 4 + sub;
+        if (g + k < last && row < n_q) {
+          lane_rotate<false>(r, i8, turn, x[k][0], x[k][1]);
+          uint4* dst = reinterpret_cast<uint4*>(q_out.p + (int64_t)t * q_out.ts + (int64_t)row * q_out.hs);
+          dst[c0] = x[k][0];
+          dst[c1] = x[k][1];
+        }
+      }
+    }
+  }
+  if ((past & (kPart - 1)) + n_new >= kPart) return;  // the page items take the keys and values
+  for (int g = max(first, q_groups); g < last; ++g) {
+    const int row = (g - q_groups) * 4 + sub;
+    if (row >= 2 * a.Hkv) continue;
     const int h = row < a.Hkv ? row : row - a.Hkv;
     uint16_t* tail = a.tails + ((int64_t)b * a.Hkv + h) * kPageElems + ((past & (kPart - 1)) + (t - row0)) * kD;
     uint4 x0, x1;
     if (row < a.Hkv) {
       x0 = *chunk(k, t, h, c0);
       x1 = *chunk(k, t, h, c1);
-      lane_rotate<true>(r, i8, turns, x0, x1);
+      lane_rotate_key(r, i8, pos, x0, x1);
     } else {
       x0 = *chunk(v, t, h, c0);
       x1 = *chunk(v, t, h, c1);
@@ -391,18 +424,17 @@ kv8_append_kernel(const Kv8Args a, const __grid_constant__ RopeArgs r, const Row
 
 cudaError_t launch_kv8_append(const Kv8Args& a, const RopeArgs& r, const Rows& q, const Rows& q_out, const Rows& k,
                               const Rows& v, int sm_count, cudaStream_t st) {
-  const int64_t page_items = ((int64_t)a.total_new / kPart + a.B) * a.Hkv;
-  const int groups = ((q.p ? a.Hq : 0) + 2 * a.Hkv + 3) / 4;
-  // Few tokens: spread a token's rows over warps, one pass each. Many: a warp keeps its
-  // token's angles for all of its rows.
-  const int64_t warps_wanted = (int64_t)sm_count * 64;
+  const int64_t page_items = (a.max_new == 1 ? (int64_t)a.B : (int64_t)a.total_new / kPart + a.B) * a.Hkv;
+  const int groups = ((q.p ? a.Hq : 0) + 3) / 4 + (2 * a.Hkv + 3) / 4;
+  // Few tokens: spread a token's rows over warps, one pass each. Many: a warp keeps its token's angles
+  // for more of its rows, as long as there are some waves of warps.
+  const int64_t warps_wanted = (int64_t)sm_count * 128;
   int64_t iters = (int64_t)a.total_new * groups / warps_wanted;
   iters = iters < 1 ? 1 : iters > groups ? groups : iters;
   const int64_t per_token = (groups + iters - 1) / iters;
   const int64_t row_ctas = ((int64_t)a.total_new * per_token + kThreads / 32 - 1) / (kThreads / 32);
   if (page_items + row_ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  kv8_append_kernel<<<(unsigned)(page_items + row_ctas), kThreads, 0, st>>>(a, r, q, q_out, k, v, (int)page_items,
-                                                                           (int)iters);
+  kv8_append_kernel<<<(unsigned)(page_items + row_ctas), kThreads, 0, st>>>(a, r, q, q_out, k, v, (int)row_ctas, (int)iters);
   return cudaGetLastError();
 }
 
