@@ -26,9 +26,8 @@ kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ 
   if (n == 0) return;
   const int rows = min(part_rows, r.n_new * G - r.first_row);
   const int64_t part_floats = (int64_t)part_rows * kPartialStride;
-  const int share = c % ctas;  // of its tile
   auto empty = [&](int x) {    // with fewer places than CTAs some shares are
-    return share_start(r.total, share + x, ctas) >= share_start(r.total, share + x + 1, ctas);
+    return share_start(r.total, c + x, ctas) >= share_start(r.total, c + x + 1, ctas);
   };
   auto part = [&](int x, int row) {
     return partials + (int64_t)(2 * (c + x) + (x == 0 ? 1 : 0)) * part_floats + (int64_t)row * kPartialStride;
@@ -118,10 +117,10 @@ kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ 
 
 }  // namespace
 
-cudaError_t launch_kv8_join(const Kv8Args& a, const Rows& out, int ctas, int tiles, int rows, void* workspace,
+cudaError_t launch_kv8_join(const Kv8Args& a, const Rows& out, int ctas, int rows, void* workspace,
                             int part_rows, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(ctas * tiles), (unsigned)rows);
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)rows);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];

@@ -958,7 +958,7 @@ cudaError_t launch_kv8_prefill(const Kv8Args& a, const Rows& q, const Rows& out,
                                                          reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes));
   e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
-  return launch_kv8_join(a, out, ctas, 1, 16, workspace, kBlockRows, st);
+  return launch_kv8_join(a, out, ctas, 16, workspace, kBlockRows, st);
 }
 
 }  // namespace spin

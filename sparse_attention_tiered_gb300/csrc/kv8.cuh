@@ -60,8 +60,8 @@ cudaError_t launch_kv8_attend(const Kv8Args& a, const Rows& q, const Rows& out, 
                               int topk, void* workspace, int sm_count, cudaStream_t st);
 cudaError_t launch_kv8_prefill(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const int32_t* sel,
                                int topk, void* workspace, int sm_count, cudaStream_t st);
-// Joins what the shares of `tiles` x `ctas` CTAs left in the workspace; `rows`: CTAs per share.
-cudaError_t launch_kv8_join(const Kv8Args& a, const Rows& out, int ctas, int tiles, int rows, void* workspace,
+// Joins what the shares of `ctas` CTAs left in the workspace, with `rows` CTAs for each.
+cudaError_t launch_kv8_join(const Kv8Args& a, const Rows& out, int ctas, int rows, void* workspace,
                             int part_rows, cudaStream_t st);
 int64_t kv8_attend_workspace(const Kv8Args& a);
 int64_t kv8_prefill_workspace();

@@ -201,6 +201,20 @@ struct Place {
 template <typename Weight, typename At>
 __device__ __forceinline__ Place locate(int requests, int64_t* scratch, Weight weight, At at) {
   const int tid = threadIdx.x, n = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = n >> 5;
+  if (requests <= 32) {  // every warp for itself
+    const int64_t mine = lane < requests ? weight(lane, true) : 0;
+    int64_t sum = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, sum, 31), want = at(total);
+    const uint32_t holds = __ballot_sync(0xffffffffu, want >= sum - mine && want < sum);
+    const int b = holds ? __ffs(holds) - 1 : requests;
+    const int64_t before = __shfl_sync(0xffffffffu, sum - mine, holds ? b : 0);
+    __syncthreads();  // as below: the caller counts on one
+    return Place{total, b, holds ? before : total};
+  }
   const int run = (requests + n - 1) / n, b0 = min(requests, tid * run), b1 = min(requests, b0 + run);
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) mine += weight(b, true);
