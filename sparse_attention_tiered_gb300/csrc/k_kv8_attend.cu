@@ -647,7 +647,7 @@ cudaError_t launch_decode(const Kv8Args& a, const CUtensorMap& map, const Rows& 
                                                            reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes));
   e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
-  return launch_kv8_join(a, out, ctas, 8 * R, workspace, kMostRows, st);
+  return launch_kv8_join(a, out, ctas, a.max_new * a.G, workspace, kMostRows, st);
 }
 
 }  // namespace

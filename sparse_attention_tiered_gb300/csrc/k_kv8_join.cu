@@ -11,10 +11,17 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+static_assert(kThreads >= kMaxCtas, "a thread a part");
 
-// CTA (c, y): rows y, y + gridDim.y, .. (or as many warps' rows) of the unit that share c begins.
+__device__ __forceinline__ void add(float4& o, const float4& y, float f) {
+  if (f != 0.f) o = make_float4(o.x + y.x * f, o.y + y.y * f, o.z + y.z * f, o.w + y.w * f);
+}
+
+// CTA (c, y): rows y, y + gridDim.y, .. (or as many warps' rows) of the unit that share c begins. What it
+// takes is the chain of loads (the record, then a row's parts, all at once), so no load hangs on a value
+// that another one brings: a part that nobody wrote is loaded too, and left out.
 __global__ void __launch_bounds__(kThreads)
 kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ records, const float* __restrict__ partials,
                 int part_rows) {
@@ -26,8 +33,8 @@ kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ 
   if (n == 0) return;
   const int rows = min(part_rows, r.n_new * G - r.first_row);
   const int64_t part_floats = (int64_t)part_rows * kPartialStride;
-  auto empty = [&](int x) {    // with fewer places than CTAs some shares are
-    return share_start(r.total, c + x, ctas) >= share_start(r.total, c + x + 1, ctas);
+  auto empty = [&](int x) {    // with fewer places than CTAs some shares are, and wrote nothing
+    return r.total < ctas && share_start(r.total, c + x, ctas) >= share_start(r.total, c + x + 1, ctas);
   };
   auto part = [&](int x, int row) {
     return partials + (int64_t)(2 * (c + x) + (x == 0 ? 1 : 0)) * part_floats + (int64_t)row * kPartialStride;
@@ -45,10 +52,14 @@ kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ 
       for (int x = 0; x < 4; ++x) {
         ml[x] = make_float2(-INFINITY, 0.f);
         y[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (x < n && !empty(x)) {
+        if (x < n) {
           ml[x] = *reinterpret_cast<const float2*>(part(x, row));
-          y[x] = *reinterpret_cast<const float4*>(part(x, row) + 4 + 4 * lane);  // (not written where nothing was seen)
+          y[x] = *reinterpret_cast<const float4*>(part(x, row) + 4 + 4 * lane);
         }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (x < n && empty(x)) ml[x] = make_float2(-INFINITY, 0.f);
         M = fmaxf(M, ml[x].x);
       }
       const float base = M == -INFINITY ? 0.f : M;
@@ -57,7 +68,7 @@ kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ 
       for (int x = 0; x < 4; ++x) {
         const float f = ex2(ml[x].x - base);
         L += ml[x].y * f;
-        if (f != 0.f) o = make_float4(o.x + y[x].x * f, o.y + y[x].y * f, o.z + y[x].z * f, o.w + y[x].w * f);
+        add(o, y[x], f);
       }
       const float inv = L == 0.f ? 0.f : 1.f / L;
       const __nv_bfloat162 v0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), v1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
@@ -67,51 +78,53 @@ kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ 
     return;
   }
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {  // a row a CTA
-    constexpr int kMost = (kMaxCtas + kThreads - 1) / kThreads;
-    float2 ml[kMost];
-    float M = -INFINITY, L = 0.f;
+    constexpr int kFirst = 5;  // parts of a warp that are on their way before the weights are known
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (tid < n) ml = *reinterpret_cast<const float2*>(part(tid, row));
+    float4 y[kFirst];
 #pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-      const int x = i * kThreads + tid;
-      ml[i] = make_float2(-INFINITY, 0.f);
-      if (x < n && !empty(x)) ml[i] = *reinterpret_cast<const float2*>(part(x, row));
-      M = fmaxf(M, ml[i].x);
+    for (int i = 0; i < kFirst; ++i) {
+      const int x = warp + i * kWarps;
+      if (x < n) y[i] = *reinterpret_cast<const float4*>(part(x, row) + 4 + 4 * lane);
     }
+    if (tid < n && empty(tid)) ml = make_float2(-INFINITY, 0.f);
+    float M = ml.x;
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     __syncthreads();  // the last row's sums have been read
     if (lane == 0) s_m[warp] = M;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
-    const float base = M == -INFINITY ? 0.f : M;
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-      const int x = i * kThreads + tid;
-      const float f = ex2(ml[i].x - base);
-      L += ml[i].y * f;
-      if (x < n) s_w[x] = f;
-    }
+    const float f = ex2(ml.x - (M == -INFINITY ? 0.f : M));
+    if (tid < n) s_w[tid] = f;
+    float L = ml.y * f;
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if (lane == 0) s_l[warp] = L;
     __syncthreads();
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int x = warp; x < n; x += kWarps) {
-      const float f = s_w[x];
-      if (f == 0.f) continue;  // nothing seen there, or an empty share, which wrote nothing
-      const float4 y = *reinterpret_cast<const float4*>(part(x, row) + 4 + 4 * lane);
-      o = make_float4(o.x + y.x * f, o.y + y.y * f, o.z + y.z * f, o.w + y.w * f);
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i)
+      if (warp + i * kWarps < n) add(o, y[i], s_w[warp + i * kWarps]);
+    for (int x = warp + kFirst * kWarps; x < n; x += kFirst * kWarps) {
+#pragma unroll
+      for (int i = 0; i < kFirst; ++i)
+        if (x + i * kWarps < n) y[i] = *reinterpret_cast<const float4*>(part(x + i * kWarps, row) + 4 + 4 * lane);
+#pragma unroll
+      for (int i = 0; i < kFirst; ++i)
+        if (x + i * kWarps < n) add(o, y[i], s_w[x + i * kWarps]);
     }
     *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = o;
     __syncthreads();
-    float sum = 0.f, x = 0.f;
+    if (tid < kD) {
+      float sum = 0.f, x = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      sum += s_l[w];
-      x += s_o[w][tid];
+      for (int w = 0; w < kWarps; ++w) {
+        sum += s_l[w];
+        x += s_o[w][tid];
+      }
+      const __nv_bfloat16 v = __float2bfloat16_rn(sum == 0.f ? 0.f : x / sum);
+      dst(row)[tid] = *reinterpret_cast<const uint16_t*>(&v);
     }
-    const __nv_bfloat16 y = __float2bfloat16_rn(sum == 0.f ? 0.f : x / sum);
-    dst(row)[tid] = *reinterpret_cast<const uint16_t*>(&y);
   }
 }
 

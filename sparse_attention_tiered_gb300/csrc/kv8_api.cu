@@ -170,7 +170,7 @@ int spin_kv8_append(const spin_kv8* cache, const spin_kv8_step* step, const spin
     if (!std::isfinite(f)) return refuse(SPIN_ERR_INVALID, "%s: inv_freq[%d] is not finite", who, j);
     double turn = f * 0.15915494309189533577;  // 1 / (2 pi)
     turn -= std::floor(turn);
-    const double scaled = std::ldexp(turn, 64);
+    const double scaled = turn * 18446744073709551616.0;  // 2^64
     r.step[j] = scaled < 18446744073709551616.0 ? (uint64_t)scaled : 0;
   }
   OnDevice dev(cache->device);

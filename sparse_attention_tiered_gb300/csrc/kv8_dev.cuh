@@ -151,7 +151,7 @@ __device__ __forceinline__ float scale_log2(float s) {
 // kUnitCost places that stand for the work of beginning and ending it, and CTA c of P takes the places
 // from c W / P on.
 // ---------------------------------------------------------------------------
-constexpr int kUnitCost = 4;
+constexpr int kUnitCost = 8;
 
 struct Unit {  // of one request: the same for all of its heads
   int row0, n_new, past;

@@ -9,9 +9,15 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional, Sequence
 
 from . import _binding as B
+
+
+_SCALE = 1.0 / math.sqrt(B.HEAD_DIM)
+_ROWS2, _ROWS4 = struct.Struct("Pqq" * 2), struct.Struct("Pqq" * 4)  # spin_rows, so many of them
+_ROW_BYTES = ctypes.sizeof(B.spin_rows)
 
 
 def _tensor(name, t, dtype, shape=None, device=None):
@@ -58,8 +64,16 @@ class SpinKV8Step:
         _tensor("cu_new", cu_new, torch.int32, (past.numel() + 1,), past.device.index)
         self.past, self.cu_new = past, cu_new
         self.batch, self.device = past.numel(), past.device.index
-        self.total_new, self.max_new = int(total_new), int(max_new)
-        self.c = B.spin_kv8_step(past.data_ptr(), cu_new.data_ptr(), self.total_new, self.max_new)
+        self.c = B.spin_kv8_step(past.data_ptr(), cu_new.data_ptr(), int(total_new), int(max_new))
+        self._at = ctypes.addressof(self.c)
+
+    @property
+    def total_new(self) -> int:
+        return self.c.total_new
+
+    @property
+    def max_new(self) -> int:
+        return self.c.max_new
 
 
 class SpinKV8:
@@ -106,57 +120,63 @@ class SpinKV8:
                             None if self.summaries is None else self.summaries.data_ptr(), self.table.data_ptr(),
                             self.error.data_ptr(), self.device, self.rope.dim, int(self.rope.interleaved), 0,
                             ctypes.addressof(self.rope._c))
-        self._lib = B.load()
+        lib = B.load()
+        self._append, self._attend = lib.spin_kv8_append, lib.spin_kv8_attend
         self._c_at = ctypes.addressof(self.c)
         self.workspace = self.new_workspace()
-        self._rows = [B.spin_rows() for _ in range(4)]
-        self._rows_at = [ctypes.addressof(r) for r in self._rows]
+        self._bf16 = torch.bfloat16
+        self._rows = (ctypes.c_char * (4 * _ROW_BYTES))()
+        at = ctypes.addressof(self._rows)
+        self._rows_at = tuple(at + i * _ROW_BYTES for i in range(4))
 
     def new_workspace(self):
         """Workspace for one stream of attend calls; the handle has one of its own."""
         n = B.spin_kv8_workspace(self.c)
         return self._torch.empty(n, dtype=self._torch.uint8, device=self._torch.device("cuda", self.device))
 
-    def _put(self, i, name, t, rows, heads):
-        if t.dtype is not self._torch.bfloat16 or not t.is_cuda or t.device.index != self.device:
+    def _row(self, name, t, rows, heads):
+        """The three words of a spin_rows."""
+        if t.dtype is not self._bf16 or t.get_device() != self.device:
             raise ValueError(f"{name}: need a bfloat16 tensor on cuda:{self.device}, got {t.dtype} on {t.device}")
-        shape = t.shape
-        if len(shape) != 3 or shape[0] != rows or shape[1] != heads or shape[2] != B.HEAD_DIM:
-            raise ValueError(f"{name}: need shape {(rows, heads, B.HEAD_DIM)}, got {tuple(shape)}")
+        if t.shape != (rows, heads, 128):
+            raise ValueError(f"{name}: need shape {(rows, heads, 128)}, got {tuple(t.shape)}")
         ts, hs, es = t.stride()
         if es != 1:
             raise ValueError(f"{name}: the head dimension must be contiguous")
         if heads <= 1:  # a stride that nothing steps over
-            hs = B.HEAD_DIM
+            hs = 128
         if rows <= 1:
             ts = hs * heads
-        r = self._rows[i]
-        r.ptr, r.token_stride, r.head_stride = t.data_ptr(), ts, hs
-        return self._rows_at[i]
+        return t.data_ptr(), ts, hs
 
     def _step(self, step):
         if step.batch != self.batch or step.device != self.device:
             raise ValueError(f"the step is for {step.batch} requests on cuda:{step.device}, the cache for {self.batch} "
                              f"on cuda:{self.device}")
-        return ctypes.addressof(step.c)
+        return step._at, step.c.total_new
 
     def append(self, step: SpinKV8Step, q, k, v, q_out=None, positions=None, stream: int = 0):
         """Rotates q [total_new][q_heads][128] into q_out (q itself when q_out is None; q None:
         keys and values alone), rotates k and appends k and v [total_new][kv_heads][128], all
         bf16. positions: int32 [total_new] instead of past + i. Returns q_out."""
-        sp, n = self._step(step), step.total_new
-        qp = qop = None
+        sp, n = self._step(step)
+        hq, hk = self.q_heads, self.kv_heads
+        at_q, at_out, at_k, at_v = self._rows_at
         if q is not None:
             q_out = q if q_out is None else q_out
-            qp = self._put(0, "q", q, n, self.q_heads)
-            qop = self._put(1, "q_out", q_out, n, self.q_heads)
+            _ROWS4.pack_into(self._rows, 0, *self._row("q", q, n, hq), *self._row("q_out", q_out, n, hq),
+                             *self._row("k", k, n, hk), *self._row("v", v, n, hk))
         elif q_out is not None:
             raise ValueError("q_out needs q")
-        kp, vp = self._put(2, "k", k, n, self.kv_heads), self._put(3, "v", v, n, self.kv_heads)
+        else:
+            at_q = at_out = None
+            _ROWS2.pack_into(self._rows, 2 * _ROW_BYTES, *self._row("k", k, n, hk), *self._row("v", v, n, hk))
         pos = None
         if positions is not None:
             pos = _tensor("positions", positions, self._torch.int32, (n,), self.device).data_ptr()
-        B._check(self._lib.spin_kv8_append(self._c_at, sp, qp, qop, kp, vp, pos, stream))
+        rc = self._append(self._c_at, sp, at_q, at_out, at_k, at_v, pos, stream)
+        if rc:
+            B._check(rc)
         return q_out
 
     def attend(self, step: SpinKV8Step, q, out, scale: Optional[float] = None, sel=None, workspace=None,
@@ -164,8 +184,8 @@ class SpinKV8:
         """out [total_new][q_heads][128] = attention of the rotated q over the cache as it is after
         the step's append, each row up to its own token. scale: 1/sqrt(128) by default. sel: int32
         [batch * kv_heads][topk], the pages to attend (with the tail) instead of all."""
-        sp, n = self._step(step), step.total_new
-        qp, op = self._put(0, "q", q, n, self.q_heads), self._put(1, "out", out, n, self.q_heads)
+        sp, n = self._step(step)
+        _ROWS2.pack_into(self._rows, 0, *self._row("q", q, n, self.q_heads), *self._row("out", out, n, self.q_heads))
         sel_ptr, topk = None, 0
         if sel is not None:
             if sel.dim() != 2:
@@ -173,8 +193,10 @@ class SpinKV8:
             topk = sel.shape[1]
             sel_ptr = _tensor("sel", sel, self._torch.int32, (self.batch * self.kv_heads, topk), self.device).data_ptr()
         ws = self.workspace if workspace is None else _tensor("workspace", workspace, self._torch.uint8, None, self.device)
-        B._check(self._lib.spin_kv8_attend(self._c_at, sp, qp, op, 1.0 / math.sqrt(B.HEAD_DIM) if scale is None else scale,
-                                           sel_ptr, topk, ws.data_ptr(), ws.numel(), stream))
+        rc = self._attend(self._c_at, sp, self._rows_at[0], self._rows_at[1], _SCALE if scale is None else scale, sel_ptr, topk,
+                          ws.data_ptr(), ws.numel(), stream)
+        if rc:
+            B._check(rc)
         return out
 
     def check(self, stream: int = 0):
