@@ -626,11 +626,16 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       const int64_t unit = (int64_t)s.b * a.Hkv + s.h;
       const int pages = min(s.to, s.u.pages);
       int id = -1, pos = -1, id_base = s.from;
-      float2 sc = make_float2(1.f, 1.f);
-      auto look = [&](int first) {  // page ids of 32 items, and for the keys' warps their scales
+      // Page ids of 32 items, a lane each, and for the keys' warps what the softmax has to know of the pages.
+      float kfac = 0.f, vlog = 0.f, vinv = 1.f;
+      bool bad = false;
+      auto look = [&](int first) {
         id_base = first;
         const int it = first + lane;
         id = pos = -1;
+        kfac = vlog = 0.f;
+        vinv = 1.f;
+        bad = false;
         if (it < pages) {
           const int p = topk ? sel[unit * topk + it] : it;
           if (p >= 0 && p < s.u.full) {
@@ -640,7 +645,13 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
               id = -1;
             } else {
               pos = p * kPart;
-              if (!half) sc = *reinterpret_cast<const float2*>(a.scales + 2 * (int64_t)id);
+              if (!half) {
+                const float2 sc = *reinterpret_cast<const float2*>(a.scales + 2 * (int64_t)id);
+                bad = !(sc.x == sc.x && sc.y == sc.y);
+                kfac = bad ? 0.f : sc.x * fabsf(scale) * kLog2e;
+                vlog = bad ? 0.f : scale_log2(sc.y);
+                vinv = bad ? 1.f : 1.f / sc.y;
+              }
             }
           }
         }
@@ -724,29 +735,22 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         warp_wait(ok, smem_u32(&empty[slot]), (count >> 1 & 1) ^ 1, abort, a.err);
         if (ok) {
           if (!half) {  // what the softmax has to know of the pages
-#pragma unroll
-            for (int pg = 0; pg < 2; ++pg) {
-              if (it + pg < pages) {
-                const int p = __shfl_sync(0xffffffffu, pos, it + pg - id_base);
-                const float kx = __shfl_sync(0xffffffffu, sc.x, it + pg - id_base);
-                const float vx = __shfl_sync(0xffffffffu, sc.y, it + pg - id_base);
-                if (lane == 0) {
-                  const bool good = p >= 0 && kx == kx && vx == vx;
-                  me.kfac[pg * 4 + w4] = good ? kx * fabsf(scale) * kLog2e : 0.f;
-                  me.vlog[pg * 4 + w4] = good ? scale_log2(vx) : 0.f;
-                  me.vinv[pg * 4 + w4] = good ? 1.f / vx : 1.f;
-                  me.bad_keys[pg * 4 + w4] = p >= 0 && !good ? 0xffffu : 0u;
-                  if (w4 == 0) me.count[pg] = p >= 0 ? kPart : 0, me.pos[pg] = max(p, 0);
-                }
-              } else if (w4 == 0 && lane == 0) {
-                me.count[pg] = it + pg < s.to ? s.u.tail : 0;
-                me.pos[pg] = s.u.full * kPart;
-              }
+            const int x = lane - (it - id_base);
+            if ((x & ~1) == 0 && it + x < pages) {
+              me.kfac[x * 4 + w4] = kfac;
+              me.vlog[x * 4 + w4] = vlog;
+              me.vinv[x * 4 + w4] = vinv;
+              me.bad_keys[x * 4 + w4] = bad ? 0xffffu : 0u;
+              if (w4 == 0) me.count[x] = pos >= 0 ? kPart : 0, me.pos[x] = max(pos, 0);
+            }
+            if (w4 == 0 && lane < 2 && it + lane >= pages) {
+              me.count[lane] = it + lane < s.to ? s.u.tail : 0;
+              me.pos[lane] = s.u.full * kPart;
             }
           }
-          // (32 items are a whole number of steps) the next step's loads, each as soon as its registers are free
+          // The next step's loads, each as soon as its registers are free.
           const bool more = it + 2 < pages;
-          if (more && it + 2 >= id_base + 32) look(it + 2);
+          if (more && it + 2 >= id_base + 32) look(it + 2);  // (32 items are a whole number of steps)
           if (tail > 0) put_page(at, 0);
           if (more) load(it + 2, 0);
           if (tail > 1 && it + 1 < s.to) put_page(at, 1);
