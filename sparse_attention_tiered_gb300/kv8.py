@@ -82,11 +82,14 @@ class SpinKV8:
     Tensors that are not given are allocated: a pool of n_pages pages, zeroed scales and tails,
     and (summaries=True) the fp32 mean keys that Select scores. The table (int32
     [batch][kv_heads][max_pages]) says which pool page holds page p of a head; the caller fills
-    it, before the call that completes or reads the page."""
+    it, before the call that completes or reads the page.
+
+    workspace: another handle's, or new_workspace()'s, for attend (some 43 MB). The layers of a model,
+    whose calls follow one another on a stream, need one between them."""
 
     def __init__(self, batch: int, q_heads: int, kv_heads: int, max_pages: int, n_pages: Optional[int] = None, *,
                  rope: Optional[SpinRope] = None, pages=None, scales=None, tails=None, table=None, summaries=False,
-                 device: Optional[int] = None):
+                 workspace=None, device: Optional[int] = None):
         import torch
         self._torch = torch
         given = [t for t in (table, pages, scales, tails) if t is not None]
@@ -123,7 +126,7 @@ class SpinKV8:
         lib = B.load()
         self._append, self._attend = lib.spin_kv8_append, lib.spin_kv8_attend
         self._c_at = ctypes.addressof(self.c)
-        self.workspace = self.new_workspace()
+        self.workspace = self.new_workspace() if workspace is None else _tensor("workspace", workspace, torch.uint8, None, self.device)
         self._bf16 = torch.bfloat16
         self._rows = (ctypes.c_char * (4 * _ROW_BYTES))()
         at = ctypes.addressof(self._rows)

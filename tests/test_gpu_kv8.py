@@ -225,6 +225,15 @@ def test_append_far_positions():
     p.check_cache()
 
 
+def test_append_positions_with_rows_behind():
+    """positions has a row for every row of k, those behind the last request's among them."""
+    p = Pair(2, 1, 2, 2, seed=8)
+    pos = torch.tensor([5, 6, 70, 1, 0, 9, 10, 11, 12, 13, 2 ** 30, -1, 8, 8, 8])
+    p.append([4, 6], pad=5, positions=pos)
+    p.check_queries(pos)
+    p.check_cache()
+
+
 def test_append_strided_and_in_place():
     """q, k and v as slices of one projection, q rotated in place, heads-first keys."""
     p = Pair(2, 2, 3, 3, seed=6)
@@ -341,6 +350,77 @@ def test_attend_scales(scale):
     p.append([250])
     p.append([1])
     p.check_attend(scale=scale)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1.0])
+def test_attend_scales_of_many_rows(scale):
+    p = Pair(2, 2, 4, 5, seed=53)
+    p.append([200, 30])
+    p.append([40, 9])
+    p.check_attend(scale=scale)
+
+
+@pytest.mark.parametrize("new", [1, 3, 30, 90], ids=["one", "few", "shared", "many"])
+@pytest.mark.parametrize("steep", [8.0, 40.0, -40.0])
+def test_attend_scores_that_rise_and_fall(new, steep):
+    """Scores along the cache rise (or fall) by up to 2^60 in weight from page to page, and the values' scales
+    jump: what was added up so far is scaled down again and again, and a page may outweigh all before it."""
+    p = Pair(1, 2, 5, 12, rot=0, seed=54)
+    n = 64 * 10 + 37 + new
+    u = p.rand(1, 1, D).sign().float()
+    along = torch.linspace(0, 1, n)[:, None, None]
+    k = u * along * steep + torch.randn((n, 2, D), generator=p.g)
+    size = torch.exp2(torch.randint(-25, 25, (12,), generator=p.g).float()).repeat_interleave(64)[:n, None, None]
+    v = torch.randn((n, 2, D), generator=p.g) * size
+    k, v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+    p.append([n - new], k=k[:-new], v=v[:-new])
+    p.append([new], k=k[-new:], v=v[-new:])
+    p.check_attend(q=(u * torch.ones(new, 10, 1) + 0.3 * torch.randn((new, 10, D), generator=p.g)).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("new", [[2, 1], [30, 5], [90, 3]], ids=str)
+@pytest.mark.parametrize("x", [math.nan, math.inf, -math.inf])
+def test_attend_queries_that_are_not_finite(new, x):
+    """NaN for the rows whose query holds one, and for no other."""
+    p = Pair(2, 2, 3, 6, seed=55)
+    p.append([300, 100])
+    p.append(new)
+    q = p.rand(sum(new), 6, D)
+    q[1, 4, 17] = q[sum(new) - 1, 0, 127] = x
+    s, cu, _, _, past = p.last
+    out = torch.empty_like(q, device="cuda")
+    p.c.attend(s, q.cuda(), out)
+    got = out.cpu().double()
+    hit = torch.zeros(got.shape[:2], dtype=torch.bool)
+    hit[1, 4] = hit[-1, 0] = True
+    assert torch.isnan(got[hit]).all()
+    want, tol = R.attend(torch.nan_to_num(q, nan=0.0, posinf=0.0, neginf=0.0), *p.state(), past, cu, 1 / math.sqrt(D))
+    assert ((got - want).abs() <= tol)[~hit].all()
+
+
+@pytest.mark.parametrize("batch,most", [(32, 1), (33, 1), (400, 1), (700, 3), (40, 17), (700, 17), (4100, 17)])
+def test_attend_many_requests(batch, most):
+    """More requests than threads, than warps' lanes, than the many-row launch plans at once; most of them short,
+    some without new tokens."""
+    p = Pair(batch, 1, 2, 3, rot=0, seed=batch + most)
+    past = torch.randint(0, 140, (batch,), generator=p.g).tolist()
+    new = [[1, 0, 1, 1, 2][i % 5] if most > 1 else [1, 1, 0][i % 3] for i in range(batch)]
+    if most > 1:
+        new[batch // 2] = new[batch - 2] = most
+    p.append(past)
+    p.append(new, pad=1)
+    p.check_attend()
+
+
+@pytest.mark.parametrize("bound", [8, 40, 2000])
+def test_attend_within_a_larger_bound(bound):
+    """max_new is a bound: what a captured step of drafts or chunks does when it replays with fewer tokens."""
+    p = Pair(3, 2, 4, 9, seed=56)
+    p.append([300, 64, 0])
+    p.append([1, 0, 5], pad=4)
+    _, cu, _, _, past = p.last
+    s, _ = step_of(past, [1, 0, 5], pad=4, max_new=bound)
+    p.check_attend(step=s, cu=cu, past=past)
 
 
 @pytest.mark.parametrize("new", [[1, 1, 1], [4, 1, 9]])
@@ -589,6 +669,24 @@ def test_two_streams_with_workspaces_of_their_own():
         ps[0].c.attend(ps[0].last[0], q[0], o[1], workspace=ws, stream=streams[1].cuda_stream)
     torch.cuda.synchronize()
     assert torch.equal(o[0], alone[0]) and torch.equal(o[1], alone[0])
+
+
+def test_layers_share_a_workspace():
+    """Caches whose calls follow one another on a stream need one workspace between them."""
+    a = Pair(3, 2, 4, 30, seed=45)
+    b = spin().SpinKV8(3, 8, 2, 30, a.c.n_pages, rope=spin().SpinRope(a.f), pages=a.c.pages, scales=a.c.scales, tails=a.c.tails,
+                       table=a.c.table, workspace=a.c.workspace)
+    assert b.workspace is a.c.workspace
+    a.append([1500, 60, 700])
+    a.append([3, 1, 2])
+    q = a.rand(6, 8, D).cuda()
+    outs = [torch.empty_like(q) for _ in range(4)]
+    for i, o in enumerate(outs):
+        (a.c, b)[i % 2].attend(a.last[0], q, o)
+    want, tol = R.attend(q.cpu(), *a.state(), a.last[4], a.last[1], 1 / math.sqrt(D))
+    for o in outs:
+        assert torch.equal(o, outs[0])
+    assert ((outs[0].cpu().double() - want).abs() <= tol).all()
 
 
 def test_shared_prefix_pages():
