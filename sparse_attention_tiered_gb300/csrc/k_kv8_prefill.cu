@@ -118,6 +118,12 @@ __device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, 
       : "memory");
 }
 
+// 16 bytes to shared memory without a register on the way; zeros where `there` is not (`from` is not read then).
+__device__ __forceinline__ void copy16(uint32_t to, uint64_t from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copied() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // The barrier is arrived at once all products issued so far are done.
 __device__ __forceinline__ void mma_commit(uint32_t leader, uint32_t bar) {
   asm volatile(
@@ -311,37 +317,39 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       const int all_steps = max(0, (min(s.to, shared ? s.limit0 : s.limit(tile)) - s.from + 1) / 2);
       const int my_steps = shared ? (all_steps - tile + 1) / 2 : all_steps;
       if (my_steps) {
-        // The warp's 32 rows, two at a time: 16 lanes have 16 bytes each of a row, whose largest element gives
-        // the power of two that puts it into fp16's range (and back out: qs). scale's sign goes here too.
+        // The warp's 32 rows go to their places as they are, 16 lanes a row, all on their way at once. Then each lane
+        // turns its row into fp16, scaled by the power of two that the largest element asks for (and back out: qs).
+        // scale's sign goes here too.
+        const uint32_t rows = sq + tile * (kTile * kD * 2) + quad * 32 * 128;
         const uint64_t mine_at = reinterpret_cast<uint64_t>(q.p + (int64_t)(s.u.row0 + i) * q.ts + (int64_t)head * q.hs);
-        const int r2 = lane >> 4, c16 = lane & 15;
-#pragma unroll 1
-        for (int y = 0; y < 16; y += 4) {
-          uint4 w[4];
+        const int c16 = lane & 15;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint64_t at = __shfl_sync(0xffffffffu, mine_at, 2 * (y + x) + r2);
-            const bool there = __shfl_sync(0xffffffffu, (int)mine, 2 * (y + x) + r2);
-            w[x] = there ? reinterpret_cast<const uint4*>(at)[c16] : make_uint4(0, 0, 0, 0);
-          }
+        for (int y = 0; y < 16; ++y) {
+          const int r = 2 * y + (lane >> 4);
+          const uint64_t at = __shfl_sync(0xffffffffu, mine_at, r);
+          const bool there = __shfl_sync(0xffffffffu, (int)mine, r);
+          copy16(rows + (c16 >> 3) * (kTile * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4),
+                 there ? at + c16 * 16 : reinterpret_cast<uint64_t>(q.p), there);
+        }
+        copied();
+        __syncwarp();
+        auto place = [&](int c) { return rows + (c >> 3) * (kTile * 128) + lane * 128 + (((c & 7) ^ (lane & 7)) << 4); };
+        uint32_t top = 0;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t top = __vmaxu2(__vmaxu2(w[x].x & 0x7fff7fffu, w[x].y & 0x7fff7fffu), __vmaxu2(w[x].z & 0x7fff7fffu, w[x].w & 0x7fff7fffu));
-            top = max(top & 0xffffu, top >> 16);
+        for (int c = 0; c < 16; ++c) {
+          const uint4 w = lds128(place(c));
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+        }
+        top = max(top & 0xffffu, top >> 16);
+        const int e = half_exponent(top);
+        const float f = scale < 0.f ? -pow2(15 - e) : pow2(15 - e);
+        poison = top >= 0x7f80u;
+        qs = poison ? 1.f : pow2(e - 15);
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int e = half_exponent(top);
-            const float f = scale < 0.f ? -pow2(15 - e) : pow2(15 - e);
-            const int r = quad * 32 + 2 * (y + x) + r2;
-            sts128(sq + tile * (kTile * kD * 2) + (c16 >> 3) * (kTile * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4),
-                   pack_half2(lo_f(w[x].x) * f, hi_f(w[x].x) * f), pack_half2(lo_f(w[x].y) * f, hi_f(w[x].y) * f),
-                   pack_half2(lo_f(w[x].z) * f, hi_f(w[x].z) * f), pack_half2(lo_f(w[x].w) * f, hi_f(w[x].w) * f));
-            const uint32_t own = __shfl_sync(0xffffffffu, top, (lane & 1) << 4);
-            if (lane >> 1 == y + x) {
-              qs = own >= 0x7f80u ? 1.f : pow2(half_exponent(own) - 15);
-              poison = own >= 0x7f80u;
-            }
-          }
+        for (int c = 0; c < 16; ++c) {
+          const uint4 w = lds128(place(c));
+          sts128(place(c), pack_half2(lo_f(w.x) * f, hi_f(w.x) * f), pack_half2(lo_f(w.y) * f, hi_f(w.y) * f),
+                 pack_half2(lo_f(w.z) * f, hi_f(w.z) * f), pack_half2(lo_f(w.w) * f, hi_f(w.w) * f));
         }
         proxy_fence();
         __syncwarp();
@@ -523,6 +531,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           for (int k = 0; k < 8; ++k) sts128(other + lane * 128 + ((k ^ (lane & 7)) << 4), y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
           pair_sync();
         }
+        pair_sync();  // the next block's rows come here only once these have been read
       } else if (shared) {
         pair_sync();
         float m1, l1;
@@ -550,7 +559,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
             y[4 * k + e] = __float_as_uint(y0 + y1);
           }
         }
-        if (c < 3) pair_sync();
+        pair_sync();
       };
       if (shared ? tile == 0 : s.limit(tile) > 0) {
         const bool whole = s.from == 0 && s.to == s.u.items;
