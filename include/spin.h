@@ -410,13 +410,15 @@ int spin_kv8_workspace(const spin_kv8* cache, int64_t* bytes);
 /* Attention of the step's queries over the cache as it is after the step's append: row i
  * of request b sees the tokens at 0 .. past[b] + i. sel (device int32
  * [batch * kv_heads][topk], may be NULL): only the pages listed for the unit, and the
- * tail; -1, and any page that is not complete, is no page; a page must not be listed twice.
+ * tail; -1, and any page that is not complete, is no page; a page listed twice counts twice.
  * q: rotated bf16 [total_new][q_heads]; out: bf16 [total_new][q_heads] = softmax(scale *
- * q K^T) V, zeros where a row sees nothing. Softmax statistics and sums are fp32; the
+ * q K^T) V, zeros where a row sees nothing, NaN where its query is not finite. out may be q
+ * itself, with its strides; otherwise they must not overlap. Softmax statistics and sums are fp32; the
  * products run on fp16 operands, which hold e4m3 codes exactly, queries and tail rows to
  * 2^-24 of their row's or 16-token group's largest value, and probabilities to 2^-11 of themselves.
- * workspace: device memory of spin_kv8_workspace bytes, 16-byte aligned; needs no
- * initialisation and holds nothing between calls. */
+ * workspace: device memory of spin_kv8_workspace bytes (some 43 MB, whatever the cache), 16-byte
+ * aligned; needs no initialisation and holds nothing between calls: the layers of a model
+ * need one between them. */
 int spin_kv8_attend(const spin_kv8* cache, const spin_kv8_step* step, const spin_rows* q, const spin_rows* out,
                     float scale, const int32_t* sel, int32_t topk, void* workspace, int64_t workspace_bytes,
                     spin_stream_t stream);

@@ -201,6 +201,8 @@ int spin_kv8_attend(const spin_kv8* cache, const spin_kv8_step* step, const spin
   if (!rc) rc = check_rows(who, "out", out, step->total_new);
   if (!rc) rc = check_apart(who, "out", out, step->total_new, cache->q_heads);
   if (rc) return rc;
+  if (q->ptr == out->ptr && (q->token_stride != out->token_stride || q->head_stride != out->head_stride))
+    return refuse(SPIN_ERR_INVALID, "%s: out in place of q must have its strides", who);
   if (!std::isfinite(scale)) return refuse(SPIN_ERR_INVALID, "%s: scale must be finite", who);
   if ((sel != nullptr) != (topk != 0) || topk < 0 || topk > (1 << 24))
     return refuse(SPIN_ERR_INVALID, "%s: sel needs topk between 1 and 2^24, no sel needs topk 0", who);

@@ -147,9 +147,11 @@ __device__ __forceinline__ float scale_log2(float s) {
 // ---------------------------------------------------------------------------
 // The split of a call's work. A unit is one (request, KV head); a tile is a block of its rows (row r:
 // token r / G, head r % G). Per tile, a unit's items are the pages that the tile's last token may see
-// (or its list of pages), then the tail. The items of all units lie in one row, each unit's behind
-// kUnitCost places that stand for the work of beginning and ending it, and CTA c of P takes the places
-// from c W / P on.
+// (or its list of pages), and the tail; the few-row kernel takes the tail first, the other one last. The items
+// of all units lie in one row, each unit's behind kUnitCost places that stand for the work of beginning
+// and ending it, and CTA c of P takes the places from c W / P on. With 8 places, 48 requests of 0 to
+// 16384 tokens take 29.0 us; with 4, 6, 10 and 14 places 34.5, 35.2, 29.3 and 29.1; prompts of 300 to 6000
+// tokens 632 us, with 6, 11, 14 and 18 places 614, 631, 638 and 668.
 // ---------------------------------------------------------------------------
 constexpr int kUnitCost = 8;
 

@@ -185,8 +185,9 @@ class SpinKV8:
     def attend(self, step: SpinKV8Step, q, out, scale: Optional[float] = None, sel=None, workspace=None,
                stream: int = 0):
         """out [total_new][q_heads][128] = attention of the rotated q over the cache as it is after
-        the step's append, each row up to its own token. scale: 1/sqrt(128) by default. sel: int32
-        [batch * kv_heads][topk], the pages to attend (with the tail) instead of all."""
+        the step's append, each row up to its own token. out may be q itself. scale: 1/sqrt(128) by default.
+        sel: int32 [batch * kv_heads][topk], the pages to attend (with the tail) instead of all; -1 is
+        none. workspace: instead of the handle's own."""
         sp, n = self._step(step)
         _ROWS2.pack_into(self._rows, 0, *self._row("q", q, n, self.q_heads), *self._row("out", out, n, self.q_heads))
         sel_ptr, topk = None, 0

@@ -689,6 +689,32 @@ def test_layers_share_a_workspace():
     assert ((outs[0].cpu().double() - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("new", [[1, 1, 1], [3, 0, 2], [40, 1, 7], [200, 90, 3]], ids=str)
+def test_attend_in_place(new):
+    """out may be q itself: a unit's rows are written once all that reads them has."""
+    p = Pair(3, 2, 5, 60, seed=57)
+    p.append([3000, 64, 500])
+    p.append(new)
+    q = p.rand(sum(new), 10, D).cuda()
+    out = torch.empty_like(q)
+    p.c.attend(p.last[0], q, out)
+    assert p.c.attend(p.last[0], q, q) is q
+    assert torch.equal(q, out)
+
+
+def test_a_page_listed_twice_counts_twice():
+    p = Pair(1, 1, 2, 6, rot=0, seed=58)
+    p.append([64 * 4])
+    p.append([1])
+    sel = torch.tensor([[2, 0, 2]], dtype=torch.int32)
+    s, cu, _, _, past = p.last
+    q = p.rand(1, 2, D)
+    out = torch.empty((1, 2, D), dtype=torch.bfloat16, device="cuda")
+    p.c.attend(s, q.cuda(), out, sel=sel.cuda())
+    want, tol = R.attend(q, *p.state(), past, cu, 1 / math.sqrt(D), sel)
+    assert ((out.cpu().double() - want).abs() <= tol).all()
+
+
 def test_shared_prefix_pages():
     """Two requests whose tables share the pages of a prompt."""
     p = Pair(2, 2, 4, 6, seed=50)

@@ -85,6 +85,11 @@ def test_overlapping_outputs(strides):
     refused(attend, "overlap", out=rows(**strides))
 
 
+@pytest.mark.parametrize("strides", [dict(token_stride=2048), dict(token_stride=128, head_stride=1024)], ids=str)
+def test_other_strides_in_place(strides):
+    refused(attend, "in place", q=rows(ptr=2 * A), out=rows(ptr=2 * A, **strides))
+
+
 @pytest.mark.parametrize("bad,word", [(dict(rot_dim=8), "rot_dim"), (dict(rot_dim=144), "rot_dim"), (dict(rot_dim=-16), "rot_dim"),
                                       (dict(inv_freq=None), "inv_freq"), (dict(interleaved=2), "interleaved")], ids=str)
 def test_bad_rotations(bad, word):
