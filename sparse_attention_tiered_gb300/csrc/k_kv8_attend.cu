@@ -5,25 +5,27 @@
 // built to keep the memory busy. One persistent CTA per SM takes an equal share of all pages of
 // all units in order (a unit may begin and end inside CTAs' shares). A plan warp walks the share, and
 // works out each unit's query operands ahead of their use; a producer warp streams pages into rings
-// of 16 KB slots with one TMA copy each; twelve consumer warps take them, four to a page with 16 tokens
+// of 16 KB slots with one TMA copy each; groups of consumer warps take them, four to a page with 16 tokens
 // each, every warp with a softmax state and output of its own. Those are joined through shared
 // memory at the end of a unit, and over CTAs by a second launch. A unit's tail, whose bf16 rows take
 // longest, comes first, under its pages.
 //
-// Arithmetic. m16n8k16 products on fp16 operands with fp32 sums: rows x dimensions x tokens for
-// the scores, rows x tokens x dimensions for the output. Codes go to fp16 exactly; queries and
-// tail rows are scaled by a power of two into fp16's range. Each 64-token page has scales k and v:
-// with z = score * k * log2(e) + log2(v), the running maximum M of z (not of the score) and
-// P = 2^(z - M + 14), the output's weight is P and the softmax sum's is P / v. So blocks whose
-// values differ by any factor share one fp16 range, whose 28 binary orders below the largest weight
-// are normal numbers.
+// Arithmetic. m16n8k16 products on fp16 operands with fp32 sums: tokens x dimensions x rows for the
+// scores, dimensions x tokens x rows for the output. Rows are the narrow side, so eight of them, the usual
+// group, waste nothing. Codes go to fp16 exactly; queries and tail rows are scaled by a power of two into
+// fp16's range. Each 64-token page has scales k and v: with z = score * k * log2(e) + log2(v), a reference M
+// that is never more than 1 below the largest z so far, and P = 2^(z - M + 14), the output's weight is P
+// and the softmax sum's is P / v. So blocks whose values differ by any factor share one fp16 range, whose 28
+// binary orders below the largest weight are normal numbers. M moves only where a z passes it by more than
+// 1 (P may reach 2^15), so that a page costs one vote in place of a maximum over lanes.
 //
-// Operand layout. The k index of a product and the n index may be permuted as long as both
-// operands agree, which is chosen so that no byte has to move between lanes: a lane's 16-byte chunk
-// of a key row is its own k indices of four products, and 16 bytes of a value row its n index of 16
-// products. With the copy's 128-byte swizzle and tokens in the order 0 5 2 7 4 1 6 3, all of these
-// 16-byte loads touch every bank once. Values need two tokens of one dimension side by side: one
-// byte permutation for two such pairs.
+// Operand layout. The k index of a product and its two outer ones may be permuted as long as the operands
+// agree, which is chosen so that no byte has to move between lanes: a lane's 16-byte chunk of a key row is
+// its own k indices of four products, and 16 bytes of a value row its dimensions of 8 products. With the
+// copy's 128-byte swizzle and tokens in the order 0 5 2 7 4 1 6 3, all of these 16-byte loads touch every
+// bank once. Values need two tokens of one dimension side by side: one byte permutation for two such
+// pairs. Weights come out of the first product with a token a lane group and go into the second with a
+// row a lane group: an 8 x 8 transposition each.
 #include "kv8_dev.cuh"
 
 namespace spin {
@@ -33,15 +35,21 @@ namespace {
 using namespace kv8;
 
 constexpr int kMostRows = 16;       // of a unit: a token's group, or a few tokens of a small one
-constexpr int kGroups = 3;          // of four consumer warps: as many as the registers have room for
-constexpr int kPer = 3;             // slots of a group's ring, 16 KB each
-constexpr int kSlots = kGroups * kPer;
-constexpr int kConsWarps = 4 * kGroups;
-constexpr int kProducer = kConsWarps, kPlanner = kConsWarps + 1;
-constexpr int kThreads = (kConsWarps + 4) * 32;
 constexpr int kUnits = 4;           // announced ahead
-constexpr int kAccPad = 144;        // floats of a row in the join: 4 x (32 + 4)
-constexpr float kShift = 14.f;      // weights reach 2^14
+constexpr float kShift = 14.f;      // weights reach 2^14, and 2^15 before the reference moves
+
+// By the number of 8-row tiles of a unit. A group is four consumer warps: as many as the registers have room
+// for; a ring of 16 KB slots each (a tail takes two).
+template <int R>
+struct Cfg {
+  static constexpr int kGroups = R == 1 ? 4 : 3, kPer = R == 1 ? 2 : 3;
+  static constexpr int kSlots = kGroups * kPer, kConsWarps = 4 * kGroups;
+  static constexpr int kProducer = kConsWarps, kPlanner = kConsWarps + 1;
+  static constexpr int kThreads = (kConsWarps + 4) * 32;
+  static constexpr size_t kRingBytes = (size_t)kSlots * kKv8PageBytes;
+  static constexpr size_t kJoinBytes = (size_t)kConsWarps * 8 * kD * 4;
+  static constexpr size_t kQueryBytes = (size_t)kUnits * R * 8 * 32 * 8;
+};
 
 struct SlotMeta {
   float kfac;  // score factor: page scale * softmax scale * log2(e)
@@ -56,7 +64,9 @@ struct Task {
   int b, h, from, to;  // items [from, to); none: the share is done
 };
 
+template <int R>
 struct Smem {
+  static constexpr int kSlots = Cfg<R>::kSlots, kConsWarps = Cfg<R>::kConsWarps;
   uint64_t full[kSlots], empty[kSlots];
   uint64_t task_full[kUnits], q_full[kUnits], task_empty[kUnits];
   SlotMeta meta[kSlots];
@@ -67,89 +77,99 @@ struct Smem {
   float m[kConsWarps][8], l[kConsWarps][8];
   int abort;
 };
+template <int R>
+constexpr size_t kSmemBytes = 1024 + Cfg<R>::kRingBytes + Cfg<R>::kJoinBytes + Cfg<R>::kQueryBytes + sizeof(Smem<R>);
+static_assert(kSmemBytes<1> <= 232448 && kSmemBytes<2> <= 232448, "shared memory of a CTA");
 
-constexpr size_t kRingBytes = (size_t)kSlots * kKv8PageBytes;
-constexpr size_t kJoinBytes = (size_t)kConsWarps * 8 * kAccPad * 4;
-constexpr size_t kQueryBytes = (size_t)kUnits * 8 * 32 * 16;
-constexpr size_t kSmemBytes = 1024 + kRingBytes + kJoinBytes + kQueryBytes + sizeof(Smem);
-static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
-
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsWarps * 32) : "memory"); }
+template <int N>
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
 
 // The same, and whether all of them are well.
+template <int N>
 __device__ __forceinline__ bool consumers_agree(bool ok) {
   int all;
   asm volatile(
       "{\n.reg .pred p, r;\nsetp.ne.s32 p, %1, 0;\nbarrier.cta.red.and.pred r, 1, %2, p;\nselp.s32 %0, 1, 0, r;\n}"
       : "=r"(all)
-      : "r"((int)ok), "n"(kConsWarps * 32)
+      : "r"((int)ok), "n"(N)
       : "memory");
   return all != 0;
 }
 
-// A warp's softmax state of 16 rows: lane (g, t) has rows g and g + 8, and of them dimensions
-// 32 t .. 32 t + 31 of the output: element e of o[j] is row g + 8 (e / 2), dimension
-// 32 t + 16 (e % 2) + j. With R = 1 (at most 8 rows, the usual group) the upper rows are left alone.
+// A warp's softmax state. Lane (g, t) has rows 8 r + 2 t and 8 r + 2 t + 1 (index e), and of them dimensions
+// 16 g .. 16 g + 15 of the output: 2 j and 2 j + 1 of those are o[r][j][e] and o[r][j][2 + e].
+template <int R>
 struct State {
-  float o[16][4];
-  float m[2], l[2];
+  float o[R][8][4];
+  float m[R][2], l[R][2];  // l: of the lane's own tokens
 };
 
-// Takes the lane's scores z (four tokens of each of its rows) into the state; fp16 weights come out.
-template <int R>
-__device__ __forceinline__ uint4 softmax_step(State& st, float (&z)[2][4], float vinv) {
-  float top[R];
-  bool grew = false;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    float x = fmaxf(fmaxf(z[0][2 * r], z[0][2 * r + 1]), fmaxf(z[1][2 * r], z[1][2 * r + 1]));
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-    top[r] = fmaxf(st.m[r], x);
-    grew |= top[r] > st.m[r];
-  }
-  if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float f = top[r] == -INFINITY ? 1.f : ex2(st.m[r] - top[r]);
-      st.m[r] = top[r];
-      st.l[r] *= f;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        st.o[j][2 * r] *= f;
-        st.o[j][2 * r + 1] *= f;
-      }
-    }
-  }
-  uint32_t w[2][2] = {};  // [row half][token tile]
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const float base = st.m[r] == -INFINITY ? -kShift : st.m[r] - kShift;
-    float y[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = ex2(z[e >> 1][2 * r + (e & 1)] - base);  // a hidden token's z is -inf
-    const float s = (y[0] + y[1]) + (y[2] + y[3]);
-    st.l[r] += s == 0.f ? 0.f : s * vinv;  // a row that sees nothing here takes nothing of a NaN page
-    w[r][0] = pack_half2(y[0], y[1]);
-    w[r][1] = pack_half2(y[2], y[3]);
-  }
-  return make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]);
+// The transposed 8 x 8 matrix of 16-bit elements.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
-// z = score * factor + vlog for the tokens a row may see, else -inf. `tok`: position of the warp's first token.
+// Takes the lane's scores z (of its rows: tokens g, g, g + 8, g + 8 in the permuted order, e alternating) into
+// the state; fp16 weights come out, p[r] for the tokens' halves.
 template <int R>
-__device__ __forceinline__ void finish_scores(float (&z)[2][4], const float (&qs)[2], float kfac, float vlog, bool masked,
-                                              int tok, const int (&see)[2], int t) {
+__device__ __forceinline__ void softmax_step(State<R>& st, const float (&z)[R][4], float vinv, uint32_t (&p)[R][2]) {
+  bool over = false;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) over |= fmaxf(z[r][e], z[r][2 + e]) > st.m[r][e] + 1.f;
+  if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = fmaxf(z[r][e], z[r][2 + e]);
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        x = fmaxf(x, st.m[r][e]);
+        const float f = x == -INFINITY ? 1.f : ex2(st.m[r][e] - x);
+        st.m[r][e] = x;
+        st.l[r][e] *= f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          st.o[r][j][e] *= f;
+          st.o[r][j][2 + e] *= f;
+        }
+      }
+  }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const float f = kfac * qs[r];
+    float y[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float& x = z[e >> 1][2 * r + (e & 1)];
-      x = fmaf(x, f, vlog);
-      if (masked && tok + (e >> 1) * 8 + ((e & 1) ? (2 * t) ^ 5 : 2 * t) >= see[r]) x = -INFINITY;
+      const float m = st.m[r][e & 1];
+      y[e] = ex2(z[r][e] - (m == -INFINITY ? -kShift : m - kShift));  // a hidden token's z is -inf
     }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float s = y[e] + y[2 + e];
+      st.l[r][e] += s == 0.f ? 0.f : s * vinv;  // a row that sees nothing here takes nothing of a NaN page
+    }
+    p[r][0] = transposed(pack_half2(y[0], y[1]));
+    p[r][1] = transposed(pack_half2(y[2], y[3]));
   }
+}
+
+// z = score * factor + vlog for the tokens a row may see, else -inf. `tok`: position of the lane's first token.
+template <int R>
+__device__ __forceinline__ void finish_scores(float (&z)[R][4], const float2 (&qs)[R], float kfac, float vlog, bool masked,
+                                              int tok, const int2 (&see)[R]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float& x = z[r][e];
+      x = fmaf(x, kfac * (e & 1 ? qs[r].y : qs[r].x), vlog);
+      if (masked && tok + (e >> 1) * 8 >= (e & 1 ? see[r].y : see[r].x)) x = -INFINITY;
+    }
 }
 
 // Clears what is not finite of eight bf16; whether there was any; the largest of the others, folded into `top`.
@@ -168,14 +188,17 @@ __device__ __forceinline__ bool clean(uint4& w, uint32_t& top) {
 }
 
 template <int R>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<R>::kThreads, 1)
 kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, const Rows q, const Rows out, float scale,
                   const int32_t* __restrict__ sel, int topk, JoinRecord* __restrict__ records, float* __restrict__ partials) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  float* join = reinterpret_cast<float*>(ring + kRingBytes);                 // [warps][8 rows][kAccPad]
-  uint4* queries = reinterpret_cast<uint4*>(ring + kRingBytes + kJoinBytes);  // [kUnits][8][32]
-  Smem& sm = *reinterpret_cast<Smem*>(ring + kRingBytes + kJoinBytes + kQueryBytes);
+  using C = Cfg<R>;
+  constexpr int kGroups = C::kGroups, kPer = C::kPer, kSlots = C::kSlots, kConsWarps = C::kConsWarps;
+  constexpr int kProducer = C::kProducer, kPlanner = C::kPlanner;
+  float* join = reinterpret_cast<float*>(ring + C::kRingBytes);                  // [warps][8 rows][128]
+  uint2* queries = reinterpret_cast<uint2*>(ring + C::kRingBytes + C::kJoinBytes);  // [kUnits][R][8][32]
+  Smem<R>& sm = *reinterpret_cast<Smem<R>*>(ring + C::kRingBytes + C::kJoinBytes + C::kQueryBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kRows = 8 * R;
   volatile int* abort = &sm.abort;
@@ -201,9 +224,10 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
   bool ok = true;
   uint32_t task = 0;  // units of the share so far
 
-  // Registers: 512 threads x 128 at launch = 128 x 56 + 384 x 152.
+  // Registers: 640 threads x 96 at launch = 128 x 64 + 512 x 104; 512 x 128 = 128 x 56 + 384 x 152.
   if (warp >= kConsWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (R == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == kPlanner) {
       // ------------------------------ plan, and query operands ------------------------------
       const int g = lane >> 2, t = lane & 3;
@@ -266,11 +290,9 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
             sm.see[slot][row] = there ? x.u.past + i + 1 : 0;
           }
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            uint32_t* dst = reinterpret_cast<uint32_t*>(&queries[(slot * 8 + (k >> 1)) * 32 + lane]) + (k & 1) * 2;
-            dst[r] = pack_half2(lo_f(w[k]) * f, hi_f(w[k]) * f);
-            if (R == 1) dst[1] = 0;
-          }
+          for (int k = 0; k < 8; ++k)
+            queries[((slot * R + r) * 8 + k) * 32 + lane] = make_uint2(pack_half2(lo_f(w[2 * k]) * f, hi_f(w[2 * k]) * f),
+                                                                       pack_half2(lo_f(w[2 * k + 1]) * f, hi_f(w[2 * k + 1]) * f));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[slot]));
@@ -378,11 +400,12 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
   }
 
   // ------------------------------ consumers ------------------------------
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+  if (R == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+  else asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
   const int g = lane >> 2, t = lane & 3;
   const int group = warp >> 2, quarter = warp & 3;
   const int pg = (g & 1) ? g ^ 4 : g;        // token order 0 5 2 7 4 1 6 3
-  State st;
+  State<R> st;
   uint32_t slot = group * kPer, parity = 0;  // of the group's own ring
   auto step = [&]() {
     if (++slot == (group + 1) * kPer) slot = group * kPer, parity ^= 1;
@@ -391,21 +414,26 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
   for (;; ++task) {
     const uint32_t ts = task % kUnits;
     warp_wait(ok, smem_u32(&sm.q_full[ts]), task / kUnits & 1, abort, a.err);
-    ok = consumers_agree(ok);  // no warp is left alone at the barriers below; and the join area is free again
+    ok = consumers_agree<kConsWarps * 32>(ok);  // no warp is left alone at the barriers below; and the join area is free again
     if (!ok) break;
     const Task& x = sm.tasks[ts];
     const int from = x.from, to = x.to;
     if (from >= to) break;
     const int tail_items = x.u.items - x.u.pages, past = x.u.past;
-    const float qs[2] = {sm.qs[ts][g], R == 2 ? sm.qs[ts][g + 8] : 1.f};
-    const int see[2] = {sm.see[ts][g], R == 2 ? sm.see[ts][g + 8] : 0};
-    auto query = [&](int k) -> uint4 { return queries[(ts * 8 + k) * 32 + lane]; };
+    float2 qs[R];
+    int2 see[R];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      st.m[r] = -INFINITY;
-      st.l[r] = 0.f;
+    for (int r = 0; r < R; ++r) {
+      qs[r] = *reinterpret_cast<const float2*>(&sm.qs[ts][8 * r + 2 * t]);
+      see[r] = *reinterpret_cast<const int2*>(&sm.see[ts][8 * r + 2 * t]);
+    }
+    auto query = [&](int r, int k) -> uint2 { return queries[((ts * R + r) * 8 + k) * 32 + lane]; };
 #pragma unroll
-      for (int j = 0; j < 16; ++j) st.o[j][2 * r] = st.o[j][2 * r + 1] = 0.f;
+    for (int r = 0; r < R; ++r) {
+      st.m[r][0] = st.m[r][1] = -INFINITY;
+      st.l[r][0] = st.l[r][1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) st.o[r][j][0] = st.o[r][j][1] = st.o[r][j][2] = st.o[r][j][3] = 0.f;
     }
 
     for (int it = from; it < to; ++it, turn = turn + 1 == kGroups ? 0 : turn + 1) {
@@ -423,32 +451,35 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
             kr[i][0] = lds128(at + ((t ^ pg) << 4));
             kr[i][1] = lds128(at + (((t + 4) ^ pg) << 4));
           }
-          float z[2][4], z1[2][4];  // even and odd products apart: shorter chains
+          float z[R][4], z1[R][4];  // even and odd products apart: shorter chains
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[i][e] = z1[i][e] = 0.f;
+            for (int e = 0; e < 4; ++e) z[r][e] = z1[r][e] = 0.f;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const uint4 qk = query(k);
+            const uint32_t w0 = reinterpret_cast<const uint32_t*>(&kr[0][k >> 2])[k & 3];
+            const uint32_t w1 = reinterpret_cast<const uint32_t*>(&kr[1][k >> 2])[k & 3];
+            const uint4 keys4 = make_uint4(e4m3x2_half2(w0, false), e4m3x2_half2(w1, false), e4m3x2_half2(w0, true), e4m3x2_half2(w1, true));
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t w = reinterpret_cast<const uint32_t*>(&kr[i][k >> 2])[k & 3];
-              mma_f16(k & 1 ? z1[i] : z[i], qk, e4m3x2_half2(w, false), e4m3x2_half2(w, true));
+            for (int r = 0; r < R; ++r) {
+              const uint2 b = query(r, k);
+              mma_f16(k & 1 ? z1[r] : z[r], keys4, b.x, b.y);
             }
           }
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int e = 0; e < 2 * R; ++e) z[i][e] += z1[i][e];
+            for (int e = 0; e < 4; ++e) z[r][e] += z1[r][e];
           uint4 vr[4];  // value rows 2 t, (2 t) ^ 5, and those 8 further
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int row = (x & 1) ? (2 * t) ^ 5 : 2 * t;
             vr[x] = lds128(vals + ((x >> 1) * 8 + row) * kD + ((g ^ row) << 4));
           }
-          finish_scores<R>(z, qs, me.kfac, me.vlog, me.pos0 + kPart > past + 1, me.pos0 + quarter * 16, see, t);
-          const uint4 p = softmax_step<R>(st, z, me.vinv);
+          finish_scores<R>(z, qs, me.kfac, me.vlog, me.pos0 + kPart > past + 1, me.pos0 + quarter * 16 + pg, see);
+          uint32_t p[R][2];
+          softmax_step<R>(st, z, me.vinv, p);
           const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vr[0]);
           const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vr[1]);
           const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vr[2]);
@@ -459,8 +490,9 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
             for (int y = 0; y < 2; ++y) {  // dimensions 4 x + 2 y, 4 x + 2 y + 1 of the lane's 16
               const uint32_t lo = __byte_perm(v0[x], v1[x], y ? 0x7362 : 0x5140);
               const uint32_t hi = __byte_perm(v2[x], v3[x], y ? 0x7362 : 0x5140);
+              const uint4 vals4 = make_uint4(e4m3x2_half2(lo, false), e4m3x2_half2(lo, true), e4m3x2_half2(hi, false), e4m3x2_half2(hi, true));
 #pragma unroll
-              for (int e = 0; e < 2; ++e) mma_f16(st.o[4 * x + 2 * y + e], p, e4m3x2_half2(lo, e), e4m3x2_half2(hi, e));
+              for (int r = 0; r < R; ++r) mma_f16(st.o[r][2 * x + y], vals4, p[r][0], p[r][1]);
             }
         }
         __syncwarp();
@@ -478,7 +510,7 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
       if (ok && have > 0) {
         const uint32_t keys = smem_u32(ring) + s0 * kKv8PageBytes + quarter * 16 * kD * 2;
         const uint32_t vals = smem_u32(ring) + slot * kKv8PageBytes + quarter * 16 * kD * 2;
-        uint32_t bad[2][2];  // tokens of the lane's columns that hold something not finite
+        bool bad[2];  // the lane's tokens that hold something not finite
         // keys: per token tile, 16 + 16 dimensions of the lane's token
         uint4 kr[2][4];
         uint32_t top = 0;
@@ -491,22 +523,28 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
             if (i * 8 + pg < have) kr[i][x] = lds128(keys + (i * 8 + pg) * kD * 2 + ((x >> 1) * 8 + 2 * t + (x & 1)) * 16);
             wrong |= clean(kr[i][x], top);
           }
-          const uint32_t who = __ballot_sync(0xffffffffu, wrong);
-          bad[i][0] = who >> (8 * t) & 0xfu;
-          bad[i][1] = who >> (8 * t + 4) & 0xfu;
+          bad[i] = (__ballot_sync(0xffffffffu, wrong) >> (4 * g) & 0xfu) != 0;
         }
         top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
         const int ke = half_exponent(top);
         const float kf = pow2(15 - ke);
-        float z[2][4];
+        float z[R][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          z[i][0] = z[i][1] = z[i][2] = z[i][3] = 0.f;
+        for (int r = 0; r < R; ++r) z[r][0] = z[r][1] = z[r][2] = z[r][3] = 0.f;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t* ww = reinterpret_cast<const uint32_t*>(&kr[i][k >> 1]);
-            const uint32_t w0 = ww[(k & 1) * 2], w1 = ww[(k & 1) * 2 + 1];
-            mma_f16(z[i], query(k), pack_half2(lo_f(w0) * kf, hi_f(w0) * kf), pack_half2(lo_f(w1) * kf, hi_f(w1) * kf));
+        for (int k = 0; k < 8; ++k) {
+          uint32_t w[2][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t x = reinterpret_cast<const uint32_t*>(&kr[i][k >> 1])[(k & 1) * 2 + y];
+              w[i][y] = pack_half2(lo_f(x) * kf, hi_f(x) * kf);
+            }
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const uint2 b = query(r, k);
+            mma_f16(z[r], make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]), b.x, b.y);
           }
         }
         // values: four tokens' 16 dimensions
@@ -522,26 +560,30 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
             if (row < have) vr[x][y] = lds128(vals + row * kD * 2 + (2 * g + y) * 16);
             wrong |= clean(vr[x][y], top);
           }
-          bad[x >> 1][x & 1] |= __ballot_sync(0xffffffffu, wrong) & (0x11111111u << t);
+          const uint32_t who = __ballot_sync(0xffffffffu, wrong);
+          if ((x & 1) == (g & 1)) bad[x >> 1] |= (who & 0x11111111u << (g >> 1)) != 0;
         }
         top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
         const int ve = half_exponent(top);
         const float vf = pow2(15 - ve);
-        finish_scores<R>(z, qs, me.kfac * pow2(ke - 15), (float)(ve - 15), true, me.pos0 + quarter * 16, see, t);
+        finish_scores<R>(z, qs, me.kfac * pow2(ke - 15), (float)(ve - 15), true, me.pos0 + quarter * 16 + pg, see);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int e = 0; e < 2 * R; ++e)
-            if (bad[i][e & 1] && z[i][e] != -INFINITY) z[i][e] = __uint_as_float(0x7fc00000u);
-        const uint4 p = softmax_step<R>(st, z, vf);
+          for (int e = 0; e < 4; ++e)
+            if (bad[e >> 1] && z[r][e] != -INFINITY) z[r][e] = __uint_as_float(0x7fc00000u);
+        uint32_t p[R][2];
+        softmax_step<R>(st, z, vf, p);
 #pragma unroll
         for (int y = 0; y < 8; ++y) {  // words of two dimensions
           const uint32_t w0 = reinterpret_cast<const uint32_t*>(&vr[0][y >> 2])[y & 3];
           const uint32_t w1 = reinterpret_cast<const uint32_t*>(&vr[1][y >> 2])[y & 3];
           const uint32_t w2 = reinterpret_cast<const uint32_t*>(&vr[2][y >> 2])[y & 3];
           const uint32_t w3 = reinterpret_cast<const uint32_t*>(&vr[3][y >> 2])[y & 3];
-          mma_f16(st.o[2 * y], p, pack_half2(lo_f(w0) * vf, lo_f(w1) * vf), pack_half2(lo_f(w2) * vf, lo_f(w3) * vf));
-          mma_f16(st.o[2 * y + 1], p, pack_half2(hi_f(w0) * vf, hi_f(w1) * vf), pack_half2(hi_f(w2) * vf, hi_f(w3) * vf));
+          const uint4 vals4 = make_uint4(pack_half2(lo_f(w0) * vf, lo_f(w1) * vf), pack_half2(hi_f(w0) * vf, hi_f(w1) * vf),
+                                         pack_half2(lo_f(w2) * vf, lo_f(w3) * vf), pack_half2(hi_f(w2) * vf, hi_f(w3) * vf));
+#pragma unroll
+          for (int r = 0; r < R; ++r) mma_f16(st.o[r][y], vals4, p[r][0], p[r][1]);
         }
       }
       __syncwarp();
@@ -559,22 +601,25 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (r * 8 >= rows) break;
-      if (r) consumers_sync();
-      float l = st.l[r];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (t == 0) {
-        sm.m[warp][g] = st.m[r];
-        sm.l[warp][g] = l;
+      if (r) consumers_sync<kConsWarps * 32>();
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = st.l[r][e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (g == 0) {
+          sm.m[warp][2 * t + e] = st.m[r][e];
+          sm.l[warp][2 * t + e] = l;
+        }
+        // chunk c of four dimensions of row x lies at c ^ (x >> 1)
+        float* dst = join + (warp * 8 + 2 * t + e) * kD;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(dst + ((4 * g + i) ^ t) * 4) =
+              make_float4(st.o[r][2 * i][e], st.o[r][2 * i][2 + e], st.o[r][2 * i + 1][e], st.o[r][2 * i + 1][2 + e]);
       }
-      float* dst = join + (warp * 8 + g) * kAccPad + t * 36;
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int j = 0; j < 16; j += 4)
-          *reinterpret_cast<float4*>(dst + 16 * e + j) =
-              make_float4(st.o[j][2 * r + e], st.o[j + 1][2 * r + e], st.o[j + 2][2 * r + e], st.o[j + 3][2 * r + e]);
-      consumers_sync();
+      consumers_sync<kConsWarps * 32>();
       const int d0 = lane * 4, row = r * 8 + warp;  // a warp a row, four dimensions a lane
       if (warp < 8 && row < rows) {
         float M = -INFINITY;
@@ -587,7 +632,7 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
         for (int w = 0; w < kConsWarps; ++w) {
           const float f = ex2(sm.m[w][warp] - base);
           L += sm.l[w][warp] * f;
-          const float4 y = *reinterpret_cast<const float4*>(join + (w * 8 + warp) * kAccPad + (d0 >> 5) * 36 + (d0 & 31));
+          const float4 y = *reinterpret_cast<const float4*>(join + (w * 8 + warp) * kD + (lane ^ (warp >> 1)) * 4);
           o = make_float4(o.x + y.x * f, o.y + y.y * f, o.z + y.z * f, o.w + y.w * f);
         }
         if (whole) {
@@ -641,9 +686,9 @@ template <int R>
 cudaError_t launch_decode(const Kv8Args& a, const CUtensorMap& map, const Rows& q, const Rows& out, float scale,
                           const int32_t* sel, int topk, void* workspace, int sm_count, cudaStream_t st) {
   const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
-  cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<R>);
   if (e != cudaSuccess) return e;
-  kv8_decode_kernel<R><<<ctas, kThreads, kSmemBytes, st>>>(a, map, q, out, scale, sel, topk, static_cast<JoinRecord*>(workspace),
+  kv8_decode_kernel<R><<<ctas, Cfg<R>::kThreads, kSmemBytes<R>, st>>>(a, map, q, out, scale, sel, topk, static_cast<JoinRecord*>(workspace),
                                                            reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes));
   e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
