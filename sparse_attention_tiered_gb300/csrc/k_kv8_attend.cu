@@ -38,18 +38,14 @@ constexpr int kMostRows = 16;       // of a unit: a token's group, or a few toke
 constexpr int kUnits = 4;           // announced ahead
 constexpr float kShift = 14.f;      // weights reach 2^14, and 2^15 before the reference moves
 
-// By the number of 8-row tiles of a unit. A group is four consumer warps: as many as the registers have room
-// for; a ring of 16 KB slots each (a tail takes two).
-template <int R>
-struct Cfg {
-  static constexpr int kGroups = R == 1 ? 4 : 3, kPer = R == 1 ? 2 : 3;
-  static constexpr int kSlots = kGroups * kPer, kConsWarps = 4 * kGroups;
-  static constexpr int kProducer = kConsWarps, kPlanner = kConsWarps + 1;
-  static constexpr int kThreads = (kConsWarps + 4) * 32;
-  static constexpr size_t kRingBytes = (size_t)kSlots * kKv8PageBytes;
-  static constexpr size_t kJoinBytes = (size_t)kConsWarps * 8 * kD * 4;
-  static constexpr size_t kQueryBytes = (size_t)kUnits * R * 8 * 32 * 8;
-};
+// A group is four consumer warps: as many groups as the registers have room for. A ring of 16 KB slots each (a
+// tail takes two). For 8 requests of 32768 tokens on 8 heads, 3 groups of 3 slots take 93 us; 4 of 2
+// (104 registers a thread) 99, 2 of 5 96, 2 of 4 97.
+constexpr int kGroups = 3, kPer = 3, kSlots = kGroups * kPer;
+constexpr int kConsWarps = 4 * kGroups, kProducer = kConsWarps, kPlanner = kConsWarps + 1;
+constexpr int kThreads = (kConsWarps + 4) * 32;
+constexpr size_t kRingBytes = (size_t)kSlots * kKv8PageBytes;
+constexpr size_t kJoinBytes = (size_t)kConsWarps * 8 * kD * 4;
 
 struct SlotMeta {
   float kfac;  // score factor: page scale * softmax scale * log2(e)
@@ -64,9 +60,7 @@ struct Task {
   int b, h, from, to;  // items [from, to); none: the share is done
 };
 
-template <int R>
 struct Smem {
-  static constexpr int kSlots = Cfg<R>::kSlots, kConsWarps = Cfg<R>::kConsWarps;
   uint64_t full[kSlots], empty[kSlots];
   uint64_t task_full[kUnits], q_full[kUnits], task_empty[kUnits];
   SlotMeta meta[kSlots];
@@ -77,21 +71,19 @@ struct Smem {
   float m[kConsWarps][8], l[kConsWarps][8];
   int abort;
 };
-template <int R>
-constexpr size_t kSmemBytes = 1024 + Cfg<R>::kRingBytes + Cfg<R>::kJoinBytes + Cfg<R>::kQueryBytes + sizeof(Smem<R>);
-static_assert(kSmemBytes<1> <= 232448 && kSmemBytes<2> <= 232448, "shared memory of a CTA");
+constexpr size_t kQueryBytes = (size_t)kUnits * 2 * 8 * 32 * 8;
+constexpr size_t kSmemBytes = 1024 + kRingBytes + kJoinBytes + kQueryBytes + sizeof(Smem);
+static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 
-template <int N>
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsWarps * 32) : "memory"); }
 
 // The same, and whether all of them are well.
-template <int N>
 __device__ __forceinline__ bool consumers_agree(bool ok) {
   int all;
   asm volatile(
       "{\n.reg .pred p, r;\nsetp.ne.s32 p, %1, 0;\nbarrier.cta.red.and.pred r, 1, %2, p;\nselp.s32 %0, 1, 0, r;\n}"
       : "=r"(all)
-      : "r"((int)ok), "n"(N)
+      : "r"((int)ok), "n"(kConsWarps * 32)
       : "memory");
   return all != 0;
 }
@@ -188,17 +180,14 @@ __device__ __forceinline__ bool clean(uint4& w, uint32_t& top) {
 }
 
 template <int R>
-__global__ void __launch_bounds__(Cfg<R>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, const Rows q, const Rows out, float scale,
                   const int32_t* __restrict__ sel, int topk, JoinRecord* __restrict__ records, float* __restrict__ partials) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  using C = Cfg<R>;
-  constexpr int kGroups = C::kGroups, kPer = C::kPer, kSlots = C::kSlots, kConsWarps = C::kConsWarps;
-  constexpr int kProducer = C::kProducer, kPlanner = C::kPlanner;
-  float* join = reinterpret_cast<float*>(ring + C::kRingBytes);                  // [warps][8 rows][128]
-  uint2* queries = reinterpret_cast<uint2*>(ring + C::kRingBytes + C::kJoinBytes);  // [kUnits][R][8][32]
-  Smem<R>& sm = *reinterpret_cast<Smem<R>*>(ring + C::kRingBytes + C::kJoinBytes + C::kQueryBytes);
+  float* join = reinterpret_cast<float*>(ring + kRingBytes);                 // [warps][8 rows][128]
+  uint2* queries = reinterpret_cast<uint2*>(ring + kRingBytes + kJoinBytes);  // [kUnits][R][8][32]
+  Smem& sm = *reinterpret_cast<Smem*>(ring + kRingBytes + kJoinBytes + kQueryBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kRows = 8 * R;
   volatile int* abort = &sm.abort;
@@ -224,10 +213,9 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
   bool ok = true;
   uint32_t task = 0;  // units of the share so far
 
-  // Registers: 640 threads x 96 at launch = 128 x 64 + 512 x 104; 512 x 128 = 128 x 56 + 384 x 152.
+  // Registers: 512 threads x 128 at launch = 128 x 56 + 384 x 152.
   if (warp >= kConsWarps) {
-    if (R == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == kPlanner) {
       // ------------------------------ plan, and query operands ------------------------------
       const int g = lane >> 2, t = lane & 3;
@@ -248,8 +236,6 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
           const Part p = part_of(x.u, at - before, stop - at);
           at += p.took;
           if (p.from >= p.to) continue;
-          if (p.from == 0 && p.to < x.u.items)
-            open = record_of(x.u, p.h, 0, pl.total, before + (int64_t)(p.h + 1) * x.u.weight, cta, ctas);
           x.h = p.h;
           x.from = p.from;
           x.to = p.to;
@@ -296,6 +282,8 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[slot]));
+        if (more && x.from == 0 && x.to < x.u.items)  // (once at most: the last of the share)
+          open = record_of(x.u, x.h, 0, pl.total, before + (int64_t)(x.h + 1) * x.u.weight, cta, ctas);
       }
       if (lane == 0) records[cta] = open;
       return;
@@ -400,8 +388,7 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
   }
 
   // ------------------------------ consumers ------------------------------
-  if (R == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-  else asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
   const int g = lane >> 2, t = lane & 3;
   const int group = warp >> 2, quarter = warp & 3;
   const int pg = (g & 1) ? g ^ 4 : g;        // token order 0 5 2 7 4 1 6 3
@@ -414,7 +401,7 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
   for (;; ++task) {
     const uint32_t ts = task % kUnits;
     warp_wait(ok, smem_u32(&sm.q_full[ts]), task / kUnits & 1, abort, a.err);
-    ok = consumers_agree<kConsWarps * 32>(ok);  // no warp is left alone at the barriers below; and the join area is free again
+    ok = consumers_agree(ok);  // no warp is left alone at the barriers below; and the join area is free again
     if (!ok) break;
     const Task& x = sm.tasks[ts];
     const int from = x.from, to = x.to;
@@ -601,7 +588,7 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       if (r * 8 >= rows) break;
-      if (r) consumers_sync<kConsWarps * 32>();
+      if (r) consumers_sync();
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float l = st.l[r][e];
@@ -619,7 +606,7 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
           *reinterpret_cast<float4*>(dst + ((4 * g + i) ^ t) * 4) =
               make_float4(st.o[r][2 * i][e], st.o[r][2 * i][2 + e], st.o[r][2 * i + 1][e], st.o[r][2 * i + 1][2 + e]);
       }
-      consumers_sync<kConsWarps * 32>();
+      consumers_sync();
       const int d0 = lane * 4, row = r * 8 + warp;  // a warp a row, four dimensions a lane
       if (warp < 8 && row < rows) {
         float M = -INFINITY;
@@ -686,9 +673,9 @@ template <int R>
 cudaError_t launch_decode(const Kv8Args& a, const CUtensorMap& map, const Rows& q, const Rows& out, float scale,
                           const int32_t* sel, int topk, void* workspace, int sm_count, cudaStream_t st) {
   const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
-  cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<R>);
+  cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
-  kv8_decode_kernel<R><<<ctas, Cfg<R>::kThreads, kSmemBytes<R>, st>>>(a, map, q, out, scale, sel, topk, static_cast<JoinRecord*>(workspace),
+  kv8_decode_kernel<R><<<ctas, kThreads, kSmemBytes, st>>>(a, map, q, out, scale, sel, topk, static_cast<JoinRecord*>(workspace),
                                                            reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes));
   e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;

@@ -203,19 +203,34 @@ struct Place {
 template <typename Weight, typename At>
 __device__ __forceinline__ Place locate(int requests, int64_t* scratch, Weight weight, At at) {
   const int tid = threadIdx.x, n = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = n >> 5;
-  if (requests <= 32) {  // every warp for itself
-    const int64_t mine = lane < requests ? weight(lane, true) : 0;
+  if (requests <= 128) {  // every warp for itself, up to four requests a lane
+    const int run = (requests + 31) >> 5;
+    int64_t m[4], mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int x = lane * run + i;
+      m[i] = i < run && x < requests ? weight(x, true) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine += m[i];
     int64_t sum = mine;
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += x;
     }
     const int64_t total = __shfl_sync(0xffffffffu, sum, 31), want = at(total);
-    const uint32_t holds = __ballot_sync(0xffffffffu, want >= sum - mine && want < sum);
-    const int b = holds ? __ffs(holds) - 1 : requests;
-    const int64_t before = __shfl_sync(0xffffffffu, sum - mine, holds ? b : 0);
+    int64_t before = sum - mine;
+    int b = lane * run;
+    const uint32_t holds = __ballot_sync(0xffffffffu, want >= before && want < sum);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (want >= before + m[i]) before += m[i], ++b;
+      else break;
+    const int from = holds ? __ffs(holds) - 1 : 0;
+    b = __shfl_sync(0xffffffffu, b, from);
+    before = __shfl_sync(0xffffffffu, before, from);
     __syncthreads();  // as below: the caller counts on one
-    return Place{total, b, holds ? before : total};
+    return holds ? Place{total, b, before} : Place{total, requests, total};
   }
   const int run = (requests + n - 1) / n, b0 = min(requests, tid * run), b1 = min(requests, b0 + run);
   int64_t mine = 0;
@@ -255,9 +270,15 @@ __device__ __forceinline__ Place locate(int requests, int64_t* scratch, Weight w
   return Place{total, (int)scratch[32], scratch[33]};
 }
 
+// a / b of numbers that are not negative: a division in 32 bits takes a third of the one in 64, which is on the way
+// to a CTA's first load.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // The first place of CTA c's share of n, and the CTA whose share has place x.
-__device__ __forceinline__ int64_t share_start(int64_t total, int c, int n) { return total * c / n; }
-__device__ __forceinline__ int share_of(int64_t total, int64_t x, int n) { return (int)(((x + 1) * n - 1) / total); }
+__device__ __forceinline__ int64_t share_start(int64_t total, int c, int n) { return quotient(total * c, n); }
+__device__ __forceinline__ int share_of(int64_t total, int64_t x, int n) { return (int)quotient((x + 1) * n - 1, total); }
 
 // What a CTA does of the unit that holds the place `at` of its request (or row block), with `left` of its share to go.
 struct Part {
@@ -267,7 +288,7 @@ struct Part {
 
 __device__ __forceinline__ Part part_of(const Unit& u, int64_t at, int64_t left) {
   Part x;
-  x.h = (int)(at / u.weight);
+  x.h = (int)quotient(at, u.weight);
   const int f = (int)(at - (int64_t)x.h * u.weight), t = (int)min((int64_t)u.weight, f + left);
   x.took = t - f;
   x.from = max(0, f - kUnitCost);
