@@ -26,6 +26,11 @@
 // bank once. Values need two tokens of one dimension side by side: one byte permutation for two such
 // pairs. Weights come out of the first product with a token a lane group and go into the second with a
 // row a lane group: an 8 x 8 transposition each.
+//
+// Measured: 32 requests of 32768 tokens, 8 KV heads in groups of 5: 2.15 GB in 319 us, 6.74 TB/s, what a plain
+// copy reaches on this GPU. HBM bounds it; a page costs 375 instructions a warp, and the schedulers issue in
+// 41% of the cycles. Rows as the products' wide side, with 16 rows' registers for 8, took 352 us. Small calls
+// are bound by the chain to the first page (lengths, table, scale, copy: 3 us of 8 for one request of 4096).
 #include "kv8_dev.cuh"
 
 namespace spin {

@@ -2,7 +2,8 @@
 // an attention launch shared. A CTA that begins such a unit leaves a record of it; every sharer
 // leaves a partial (M, L, -, -, o[128]) per row: weights relative to 2^M, their sum, the weighted
 // values. Parts are added in a fixed order. The launch waits for the attention launch by a programmatic
-// dependency, so it is resident when that ends.
+// dependency, so it is resident when that ends. It takes 4 us, a launch and three loads that wait for one
+// another; with weights before the parts' loads it took 7.
 #include "kv8_dev.cuh"
 
 namespace spin {

@@ -148,12 +148,17 @@ __device__ __forceinline__ float scale_log2(float s) {
 // The split of a call's work. A unit is one (request, KV head); a tile is a block of its rows (row r:
 // token r / G, head r % G). Per tile, a unit's items are the pages that the tile's last token may see
 // (or its list of pages), and the tail; the few-row kernel takes the tail first, the other one last. The items
-// of all units lie in one row, each unit's behind kUnitCost places that stand for the work of beginning
-// and ending it, and CTA c of P takes the places from c W / P on. With 8 places, 48 requests of 0 to
-// 16384 tokens take 29.0 us; with 4, 6, 10 and 14 places 34.5, 35.2, 29.3 and 29.1; prompts of 300 to 6000
-// tokens 632 us, with 6, 11, 14 and 18 places 614, 631, 638 and 668.
+// of all units lie in one row, each unit's behind unit_cost places that stand for the work of beginning
+// and ending it, and CTA c of P takes the places from c W / P on. The cost is in pages: 8 for the few-row
+// kernel (48 requests of 0 to 16384 tokens take 29.9 us; with 4, 6 and 11 places 34.3, 32.8 and 29.8); 6
+// where the many-row kernel's two tiles have rows of their own, and 11 where they share a block and pass a
+// page in half of the time (prompts of 300 to 6000 tokens take 573 us with 6 places, 590 with 8, 598 with 11;
+// drafts of 5 tokens 144, 143 and 139).
 // ---------------------------------------------------------------------------
-constexpr int kUnitCost = 8;
+constexpr int kTileRows = 128;  // of the many-row kernel
+__device__ __forceinline__ int unit_cost(int block_rows, int rows_there) {
+  return block_rows < kTileRows ? 8 : rows_there > kTileRows ? 6 : 11;
+}
 
 struct Unit {  // of one request: the same for all of its heads
   int row0, n_new, past;
@@ -161,7 +166,7 @@ struct Unit {  // of one request: the same for all of its heads
   int tail;     // tokens of the tail
   int pages;    // entries of the page list
   int items;    // pages, and one for the tail if the tile sees it
-  int weight;   // items + kUnitCost, or 0
+  int weight;   // items + unit_cost, or 0
 };
 
 // A request's numbers; n_new and the rest 0 where they are out of range.
@@ -183,7 +188,7 @@ __device__ __forceinline__ void set_rows(const Kv8Args& a, Unit& u, int first_ro
   const int seen = u.past + last;
   u.pages = topk ? topk : min(u.full, (seen + kPart - 1) >> 6);
   u.items = u.pages + (u.tail && seen > u.full * kPart ? 1 : 0);
-  u.weight = u.items ? u.items + kUnitCost : 0;
+  u.weight = u.items ? u.items + unit_cost(rows, u.n_new * a.G - first_row) : 0;
 }
 
 __device__ __forceinline__ Unit unit_of(const Kv8Args& a, int b, int first_row, int rows, int topk, bool report) {
@@ -291,8 +296,8 @@ __device__ __forceinline__ Part part_of(const Unit& u, int64_t at, int64_t left)
   x.h = (int)quotient(at, u.weight);
   const int f = (int)(at - (int64_t)x.h * u.weight), t = (int)min((int64_t)u.weight, f + left);
   x.took = t - f;
-  x.from = max(0, f - kUnitCost);
-  x.to = max(0, t - kUnitCost);
+  x.from = max(0, f - (u.weight - u.items));
+  x.to = max(0, t - (u.weight - u.items));
   return x;
 }
 
