@@ -225,13 +225,13 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
       // ------------------------------ plan, and query operands ------------------------------
       const int g = lane >> 2, t = lane & 3;
       JoinRecord open = JoinRecord{};
-      Task x;
+      Task x = Task{};
       x.b = pl.b;
       int64_t at = share_start(pl.total, cta, ctas), before = pl.before;
       const int64_t stop = share_start(pl.total, cta + 1, ctas);
       for (bool more = true; more && ok; ++task) {
         x.from = x.to = 0;
-        while (at < stop) {
+        while (at < stop && x.b < a.B) {
           x.u = unit_of(a, x.b, 0, kRows, topk, false);
           if (x.u.weight == 0 || at >= before + (int64_t)x.u.weight * a.Hkv) {
             before += (int64_t)x.u.weight * a.Hkv;
