@@ -210,6 +210,8 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // The launch may begin before what is before it on the stream has ended; nothing in memory is touched until then.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int ctas = gridDim.x, cta = blockIdx.x;
   const Place pl = locate(
@@ -680,9 +682,18 @@ cudaError_t launch_decode(const Kv8Args& a, const CUtensorMap& map, const Rows& 
   const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
   cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
-  kv8_decode_kernel<R><<<ctas, kThreads, kSmemBytes, st>>>(a, map, q, out, scale, sel, topk, static_cast<JoinRecord*>(workspace),
-                                                           reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes));
-  e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv8_decode_kernel<R>, a, map, q, out, scale, sel, topk, static_cast<JoinRecord*>(workspace),
+                         reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes));
   if (e != cudaSuccess || ctas == 1) return e;
   return launch_kv8_join(a, out, ctas, a.max_new * a.G, workspace, kMostRows, st);
 }

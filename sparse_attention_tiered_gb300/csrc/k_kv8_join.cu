@@ -28,6 +28,7 @@ kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ 
                 int part_rows) {
   __shared__ float s_w[kMaxCtas], s_m[kWarps], s_l[kWarps], s_o[kWarps][kD];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this launch must not end before the first
   const JoinRecord r = records[c];
   const int n = r.parts;

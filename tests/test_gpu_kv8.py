@@ -640,6 +640,84 @@ def test_captured_step_replays_with_new_lengths():
     p.c.check()
 
 
+@pytest.mark.parametrize("before", ["nothing", "memset", "copy", "kernel", "event", "append", "attend"])
+@pytest.mark.parametrize("new", [1, 40])
+def test_captured_behind_other_work(before, new):
+    """The attention's first launch as the successor of each kind of node, and of none."""
+    p = Pair(2, 2, 4, 30, seed=47)
+    p.append([23 * 64, 70])  # no page is completed below, so that an append of the same rows changes nothing
+    p.append([new, 1])
+    s = p.last[0]
+    q = p.rand(new + 1, 8, D).cuda()
+    k, v = p.rand(new + 1, 2, D).cuda(), p.rand(new + 1, 2, D).cuda()
+    q2 = torch.zeros_like(q)
+    want, out = torch.empty_like(q), torch.zeros_like(q)
+    if before == "append":
+        p.c.append(s, None, k, v)
+    p.c.attend(s, q, want)
+    torch.cuda.synchronize()
+    st, other = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        src = q
+        if before == "memset":
+            out.zero_()
+        elif before == "copy":
+            q2.copy_(q)
+            src = q2
+        elif before == "kernel":
+            torch.add(q, 0, out=q2)
+            src = q2
+        elif before == "event":
+            other.wait_stream(st)
+            with torch.cuda.stream(other):
+                q2.copy_(q)
+            st.wait_stream(other)
+            src = q2
+        elif before == "append":
+            p.c.append(s, None, k, v, stream=st.cuda_stream)
+        elif before == "attend":
+            p.c.attend(s, q, q2, stream=st.cuda_stream)
+        p.c.attend(s, src, out, stream=st.cuda_stream)
+    for _ in range(3):
+        out.fill_(5.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    p.c.check()
+
+
+def test_attend_follows_what_writes_its_inputs():
+    """Calls back to back: each reads what the one before it wrote, the append among them."""
+    p, e = Pair(2, 2, 4, 30, rot=0, seed=48), Pair(2, 2, 4, 30, rot=0, seed=48)
+    q0 = p.rand(2, 8, D)
+    k, v = p.rand(60, 2, D), p.rand(60, 2, D)
+    for c in (p, e):
+        c.append([1000, 70], k=k.repeat(18, 1, 1)[:1070], v=v.repeat(18, 1, 1)[:1070])
+    chain, steps = q0.cuda(), []
+    past = [1000, 70]
+    for i in range(20):
+        steps.append(step_of(past, [1, 1])[0])
+        past = [n + 1 for n in past]
+    kd, vd = k.cuda(), v.cuda()
+    kp = [kd[2 * i:2 * i + 2] for i in range(20)]
+    vp = [vd[2 * i:2 * i + 2] for i in range(20)]
+    torch.cuda.synchronize()
+    for i in range(20):
+        p.c.append(steps[i], None, kp[i], vp[i])
+        p.c.attend(steps[i], chain, chain)
+    torch.cuda.synchronize()
+    slow = q0.cuda()
+    for i in range(20):
+        e.c.append(steps[i], None, kp[i], vp[i])
+        torch.cuda.synchronize()
+        e.c.attend(steps[i], slow, slow)
+        torch.cuda.synchronize()
+    assert torch.equal(chain, slow) and torch.equal(p.c.pages, e.c.pages)
+
+
 def test_two_streams_with_workspaces_of_their_own():
     """Two caches' attention at once, on two streams."""
     ps = [Pair(4, 2, 8, 50, seed=40 + i) for i in range(2)]
