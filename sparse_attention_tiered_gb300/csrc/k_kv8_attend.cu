@@ -27,10 +27,11 @@
 // pairs. Weights come out of the first product with a token a lane group and go into the second with a
 // row a lane group: an 8 x 8 transposition each.
 //
-// Measured: 32 requests of 32768 tokens, 8 KV heads in groups of 5: 2.15 GB in 319 us, 6.74 TB/s, what a plain
+// Measured: 32 requests of 32768 tokens, 8 KV heads in groups of 5: 2.15 GB in 316 us, 6.80 TB/s, what a plain
 // copy reaches on this GPU. HBM bounds it; a page costs 375 instructions a warp, and the schedulers issue in
 // 41% of the cycles. Rows as the products' wide side, with 16 rows' registers for 8, took 352 us. Small calls
-// are bound by the chain to the first page (lengths, table, scale, copy: 3 us of 8 for one request of 4096).
+// are bound by the chain to the first page (lengths, table, scale, copy): one request of 4096
+// tokens takes 8.5 us a call, 10.3 without the launch that begins while the last one ends.
 #include "kv8_dev.cuh"
 
 namespace spin {
@@ -682,18 +683,8 @@ cudaError_t launch_decode(const Kv8Args& a, const CUtensorMap& map, const Rows& 
   const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
   cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv8_decode_kernel<R>, a, map, q, out, scale, sel, topk, static_cast<JoinRecord*>(workspace),
-                         reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes));
+  e = launch_early(kv8_decode_kernel<R>, dim3((unsigned)ctas), kThreads, kSmemBytes, st, a, map, q, out, scale, sel, topk,
+                   static_cast<JoinRecord*>(workspace), reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes));
   if (e != cudaSuccess || ctas == 1) return e;
   return launch_kv8_join(a, out, ctas, a.max_new * a.G, workspace, kMostRows, st);
 }

@@ -134,17 +134,9 @@ kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ 
 
 cudaError_t launch_kv8_join(const Kv8Args& a, const Rows& out, int ctas, int rows, void* workspace,
                             int part_rows, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)rows);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_join_kernel, a.G, out, ctas, (const JoinRecord*)workspace,
-                            (const float*)(static_cast<uint8_t*>(workspace) + kRecordBytes), part_rows);
+  return launch_early(kv8_join_kernel, dim3((unsigned)ctas, (unsigned)rows), kThreads, 0, st, a.G, out, ctas,
+                      static_cast<const JoinRecord*>(workspace),
+                      reinterpret_cast<const float*>(static_cast<uint8_t*>(workspace) + kRecordBytes), part_rows);
 }
 
 }  // namespace spin

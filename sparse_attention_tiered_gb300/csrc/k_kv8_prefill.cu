@@ -27,12 +27,12 @@
 // The arithmetic is that of the few-row kernel: z = score * k * log2(e) + log2(v) per page, weights
 // 2^(z - M + 6), the softmax sum takes weight / v. M is the reference: weights up to 2^15 are let pass.
 //
-// Measured: 2048 tokens onto 30000, 4 KV heads in groups of 8: 2.08 TFLOP in 1993 us, 1.04 PFLOP/s. A step of two
+// Measured: 2048 tokens onto 30000, 4 KV heads in groups of 8: 2.08 TFLOP in 2000 us, 1.04 PFLOP/s. A step of two
 // tiles takes 4930 clocks. Its 32 products need 2048 at the tensor cores' rate; their operands share the shared
 // memory with the loaders' stores, and they take 3300. The rest is a softmax that the other tile's products do not
 // cover. A block costs another 5 us for its queries, its first step and its output: prompts of 300 to 6000
 // tokens run at 0.7 PFLOP/s. Queries that go to shared memory through registers, four rows a time, cost 5 us
-// a block more. Drafts of 5 tokens in groups of 8 (40 of a tile's 128 rows) read 0.33 GB in 138 us: a tile's
+// a block more. Drafts of 5 tokens in groups of 8 (40 of a tile's 128 rows) read 0.33 GB in 136 us: a tile's
 // products take as long for 40 rows as for 128.
 #include "kv8_dev.cuh"
 
@@ -269,6 +269,8 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // The launch may begin before what is before it on the stream has ended; nothing in memory is touched until then.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -975,9 +977,8 @@ cudaError_t launch_kv8_prefill(const Kv8Args& a, const Rows& q, const Rows& out,
   const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
   cudaError_t e = cudaFuncSetAttribute(kv8_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
-  kv8_prefill_kernel<<<ctas, kThreads, kSmemBytes, st>>>(a, q, out, scale, sel, topk, static_cast<JoinRecord*>(workspace),
-                                                         reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes));
-  e = cudaGetLastError();
+  e = launch_early(kv8_prefill_kernel, dim3((unsigned)ctas), kThreads, kSmemBytes, st, a, q, out, scale, sel, topk,
+                   static_cast<JoinRecord*>(workspace), reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes));
   if (e != cudaSuccess || ctas == 1) return e;
   return launch_kv8_join(a, out, ctas, 16, workspace, kBlockRows, st);
 }

@@ -60,6 +60,23 @@ cudaError_t launch_kv8_attend(const Kv8Args& a, const Rows& q, const Rows& out, 
                               int topk, void* workspace, int sm_count, cudaStream_t st);
 cudaError_t launch_kv8_prefill(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const int32_t* sel,
                                int topk, void* workspace, int sm_count, cudaStream_t st);
+// Launches a kernel that may begin while the launch before it on the stream ends: each of its CTAs waits for
+// that one's end (griddepcontrol.wait) before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t shared, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = shared;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // Joins what the shares of `ctas` CTAs left in the workspace, with `rows` CTAs for each.
 cudaError_t launch_kv8_join(const Kv8Args& a, const Rows& out, int ctas, int rows, void* workspace,
                             int part_rows, cudaStream_t st);
