@@ -28,10 +28,10 @@
 // row a lane group: an 8 x 8 transposition each.
 //
 // Measured: 32 requests of 32768 tokens, 8 KV heads in groups of 5: 2.15 GB in 316 us, 6.80 TB/s, what a plain
-// copy reaches on this GPU. HBM bounds it; a page costs 375 instructions a warp, and the schedulers issue in
-// 41% of the cycles. Rows as the products' wide side, with 16 rows' registers for 8, took 352 us. Small calls
-// are bound by the chain to the first page (lengths, table, scale, copy): one request of 4096
-// tokens takes 8.5 us a call, 10.3 without the launch that begins while the last one ends.
+// copy reaches on this GPU. HBM bounds it; the schedulers issue in 37% of the cycles, the tensor pipe works in
+// 17%. With rows as the products' wide side (16 rows' registers and products for 8) it took 352 us. Small calls are
+// bound by the chain to the first page (lengths, table, scale, copy): one request of 4096 tokens takes 8.5 us a
+// call, 10.3 without the launch that begins while the last one ends.
 #include "kv8_dev.cuh"
 
 namespace spin {
