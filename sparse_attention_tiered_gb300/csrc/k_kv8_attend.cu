@@ -638,7 +638,7 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
               make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
         } else {
           float* part = partials + ((int64_t)pslot * kMostRows + row) * kPartialStride;
-          if (lane == 0) *reinterpret_cast<float2*>(part) = make_float2(M, L);
+          if (lane == 0) *reinterpret_cast<float4*>(part) = make_float4(M, L, 0.f, 0.f);
           *reinterpret_cast<float4*>(part + 4 + d0) = o;
         }
       }

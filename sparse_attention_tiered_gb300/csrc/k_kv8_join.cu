@@ -1,7 +1,7 @@
 // The join of partial attention results over the 8-bit paged cache, for the units that several CTAs of
 // an attention launch shared. A CTA that begins such a unit leaves a record of it; every sharer
-// leaves a partial (M, L, -, -, o[128]) per row: weights relative to 2^M, their sum, the weighted
-// values. Parts are added in a fixed order. The launch waits for the attention launch by a programmatic
+// leaves a partial (M, L, V, -, o[128]) per row: weights relative to 2^(M + V), their sum, the weighted
+// values. M is a score and may be of any size, V is small: M's differences are taken first. Parts are added in a fixed order. The launch waits for the attention launch by a programmatic
 // dependency, so it is resident when that ends. It takes 4 us, a launch and three loads that wait for one
 // another; with weights before the parts' loads it took 7.
 #include "kv8_dev.cuh"
@@ -20,13 +20,18 @@ __device__ __forceinline__ void add(float4& o, const float4& y, float f) {
   if (f != 0.f) o = make_float4(o.x + y.x * f, o.y + y.y * f, o.z + y.z * f, o.w + y.w * f);
 }
 
+__device__ __forceinline__ float3 load_mlv(const float* part) {
+  const float4 x = *reinterpret_cast<const float4*>(part);
+  return make_float3(x.x, x.y, x.z);
+}
+
 // CTA (c, y): rows y, y + gridDim.y, .. (or as many warps' rows) of the unit that share c begins. What it
 // takes is the chain of loads (the record, then a row's parts, all at once), so no load hangs on a value
 // that another one brings: a part that nobody wrote is loaded too, and left out.
 __global__ void __launch_bounds__(kThreads)
 kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ records, const float* __restrict__ partials,
                 int part_rows) {
-  __shared__ float s_w[kMaxCtas], s_m[kWarps], s_l[kWarps], s_o[kWarps][kD];
+  __shared__ float s_w[kMaxCtas], s_m[kWarps], s_v[kWarps], s_l[kWarps], s_o[kWarps][kD];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this launch must not end before the first
@@ -47,29 +52,35 @@ kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ 
   };
   if (n <= 4) {  // a row a warp
     for (int row = blockIdx.y * kWarps + warp; row < rows; row += gridDim.y * kWarps) {
-      float M = -INFINITY, L = 0.f;
-      float2 ml[4];
+      float M = -INFINITY, V = -INFINITY, L = 0.f;
+      float3 mlv[4];
       float4 y[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        ml[x] = make_float2(-INFINITY, 0.f);
+        mlv[x] = make_float3(-INFINITY, 0.f, 0.f);
         y[x] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (x < n) {
-          ml[x] = *reinterpret_cast<const float2*>(part(x, row));
+          mlv[x] = load_mlv(part(x, row));
           y[x] = *reinterpret_cast<const float4*>(part(x, row) + 4 + 4 * lane);
         }
       }
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        if (x < n && empty(x)) ml[x] = make_float2(-INFINITY, 0.f);
-        M = fmaxf(M, ml[x].x);
+        if (x < n && empty(x)) mlv[x] = make_float3(-INFINITY, 0.f, 0.f);
+        M = fmaxf(M, mlv[x].x);
       }
       const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        mlv[x].x = (mlv[x].x - base) + mlv[x].z;
+        V = fmaxf(V, mlv[x].x);
+      }
+      if (V == -INFINITY) V = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const float f = ex2(ml[x].x - base);
-        L += ml[x].y * f;
+        const float f = ex2(mlv[x].x - V);
+        L += mlv[x].y * f;
         add(o, y[x], f);
       }
       const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -81,25 +92,28 @@ kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ 
   }
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {  // a row a CTA
     constexpr int kFirst = 5;  // parts of a warp that are on their way before the weights are known
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (tid < n) ml = *reinterpret_cast<const float2*>(part(tid, row));
+    float3 mlv = make_float3(-INFINITY, 0.f, 0.f);
+    if (tid < n) mlv = load_mlv(part(tid, row));
     float4 y[kFirst];
 #pragma unroll
     for (int i = 0; i < kFirst; ++i) {
       const int x = warp + i * kWarps;
       if (x < n) y[i] = *reinterpret_cast<const float4*>(part(x, row) + 4 + 4 * lane);
     }
-    if (tid < n && empty(tid)) ml = make_float2(-INFINITY, 0.f);
-    float M = ml.x;
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (tid < n && empty(tid)) mlv = make_float3(-INFINITY, 0.f, 0.f);
     __syncthreads();  // the last row's sums have been read
-    if (lane == 0) s_m[warp] = M;
-    __syncthreads();
+    auto largest = [&](float x, float* s) {  // of the CTA; 0 where there is none
+      for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+      if (lane == 0) s[warp] = x;
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
-    const float f = ex2(ml.x - (M == -INFINITY ? 0.f : M));
+      for (int w = 0; w < kWarps; ++w) x = fmaxf(x, s[w]);
+      return x == -INFINITY ? 0.f : x;
+    };
+    const float a = (mlv.x - largest(mlv.x, s_m)) + mlv.z;
+    const float f = ex2(a - largest(a, s_v));
     if (tid < n) s_w[tid] = f;
-    float L = ml.y * f;
+    float L = mlv.y * f;
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if (lane == 0) s_l[warp] = L;
     __syncthreads();

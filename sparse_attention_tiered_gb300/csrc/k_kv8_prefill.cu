@@ -10,7 +10,7 @@
 //   0-3, 4-7  softmax of tile 0 and 1, one row a thread: scores out of tensor memory, fp16 weights back into
 //             it, relative to a reference that is the maximum of the row's first step. A later step looks
 //             for no maximum: its sums say whether a weight may have left fp16's range, and then,
-//             which is rare, the reference is raised and what was added up so far scaled. Rows are
+//             which is rare, the reference is raised, once, and what was added up so far scaled. Rows are
 //             stored at the end;
 //   8-11      keys from HBM to fp16 in shared memory, 128-byte swizzled. A step's loads are in registers
 //             one step ahead of their use, so no shared memory holds codes;
@@ -24,8 +24,12 @@
 // Tensor memory: O_0, O_1, S_0, S_1 of 128 columns each. Shared memory: Q_0, Q_1 and two steps of
 // K and of V, 32 KB each.
 //
-// The arithmetic is that of the few-row kernel: z = score * k * log2(e) + log2(v) per page, weights
-// 2^(z - M + 6), the softmax sum takes weight / v. M is the reference: weights up to 2^15 are let pass.
+// The arithmetic is that of the few-row kernel: with s = score * k * log2(e) per page, weights are
+// 2^((s - M) + (log2(v) - V) + 6), the softmax sum takes weight / v. The reference is a pair, a score M and the
+// log2 of a values' scale V: scores may be of any size, where one sum of the two would lose V (and the shift) to
+// the sum's rounding. Weights up to 2^15 are let pass. Up to |M| = 2^11 an exponent is one fused operation,
+// s + (log2(v) - V + 6 - M), off by at most 2^-12; a page of a row beyond it, or one that raises the reference, is
+// taken again with s - M first, which is exact near the reference.
 //
 // Measured: 2048 tokens onto 30000, 4 KV heads in groups of 8: 2.08 TFLOP in 2000 us, 1.04 PFLOP/s. A step of two
 // tiles takes 4930 clocks. Its 32 products need 2048 at the tensor cores' rate; their operands share the shared
@@ -50,6 +54,7 @@ constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16, kPlanWarp = 17;
 constexpr int kSegReaders = 17;  // warps that read a segment: softmax, loaders, products
 constexpr float kUp = 6.f;          // a weight at the reference is 2^kUp
 constexpr float kMostSum = 32768.f;  // of 64 weights: none of them is above it
+constexpr float kFar = 2048.f;      // a reference from which on differences are taken before anything is added
 constexpr int kPlane = 32768;  // K or V: [2 planes of 64 dimensions][2 steps][128 tokens][128 bytes]
 constexpr uint32_t kColO = 0, kColS = 256;
 
@@ -366,7 +371,13 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[tile]));
       }
 
-      float M = -INFINITY, L = 0.f;
+      float M = -INFINITY, V = 0.f, L = 0.f;  // the row's reference, and the sum relative to it
+      // What the exponents take, and a page's sum from which on its weights are worked out again. Both follow the reference.
+      float up = kUp, limit = poison ? INFINITY : kMostSum;
+      auto aim = [&]() {
+        up = kUp - V - (M == -INFINITY ? 0.f : M);
+        limit = poison ? INFINITY : M != -INFINITY && !(fabsf(M) < kFar) ? -1.f : kMostSum;
+      };
       for (int turn = 0; turn < my_steps; ++turn, ++done) {
         const int step = shared ? 2 * turn + tile : turn;
         warp_wait(ok, smem_u32(&sm.s_full[tile]), done & 1, abort, a.err);
@@ -401,15 +412,17 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
             for (int c = 0; c < kPart; ++c) x[c] = c < vis ? x[c] : 0xff800000u;
           }
         };
-        auto largest = [&]() {
-          float m[4];
+        // Puts (tm, tv) at the page's largest weight, if that is above it.
+        auto largest = [&](float& tm, float& tv) {
 #pragma unroll
           for (int grp = 0; grp < 4; ++grp) {
-            m[grp] = __uint_as_float(x[grp * 16]);
+            float s = __uint_as_float(x[grp * 16]);
 #pragma unroll
-            for (int c = 1; c < 16; ++c) m[grp] = fmaxf(m[grp], __uint_as_float(x[grp * 16 + c]));
+            for (int c = 1; c < 16; ++c) s = fmaxf(s, __uint_as_float(x[grp * 16 + c]));
+            s = __fmul_rn(s, grp == 0 ? fac.x : grp == 1 ? fac.y : grp == 2 ? fac.z : fac.w);
+            const float l = grp == 0 ? vlog.x : grp == 1 ? vlog.y : grp == 2 ? vlog.z : vlog.w;
+            if ((s - tm) + (l - tv) > 0.f) tm = s, tv = l;
           }
-          return fmaxf(fmaxf(fmaf(m[0], fac.x, vlog.x), fmaf(m[1], fac.y, vlog.y)), fmaxf(fmaf(m[2], fac.z, vlog.z), fmaf(m[3], fac.w, vlog.w)));
         };
         // What was added up so far, times f: L, the output once its products are done, the weights of the step's
         // first page if that is done. (f is 1 for some rows, a power of two for the others.)
@@ -446,25 +459,26 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           }
         };
         if (__any_sync(0xffffffffu, M == -INFINITY)) {  // no reference yet: the step's maximum
-          float top = -INFINITY;
+          float tm = M, tv = V;
 #pragma unroll 1
           for (int hf = 0; hf < halves; ++hf) {
             fetch(hf);
-            top = fmaxf(top, largest());
+            largest(tm, tv);
           }
-          if (M == -INFINITY) M = top;
+          if (M == -INFINITY) M = tm, V = tv;
+          aim();
         }
-        float up = kUp - (M == -INFINITY ? 0.f : M);
 #pragma unroll 1
         for (int hf = 0; hf < halves; ++hf) {
           fetch(hf);
           uint32_t p[32];
           float sum[4];
-          for (;;) {
+          float shift = up, most = limit;
+          for (;;) {  // twice at most: no sum is above the second time's limit
 #pragma unroll
             for (int grp = 0; grp < 4; ++grp) {
               const uint64_t k2 = twice(grp == 0 ? fac.x : grp == 1 ? fac.y : grp == 2 ? fac.z : fac.w);
-              const uint64_t c2 = twice((grp == 0 ? vlog.x : grp == 1 ? vlog.y : grp == 2 ? vlog.z : vlog.w) + up);
+              const uint64_t c2 = twice((grp == 0 ? vlog.x : grp == 1 ? vlog.y : grp == 2 ? vlog.z : vlog.w) + shift);
               uint64_t sum2[2] = {0, 0};
 #pragma unroll
               for (int c = 0; c < 16; c += 2) {
@@ -479,14 +493,31 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
               unpack2(add2(sum2[0], sum2[1]), s0, s1);
               sum[grp] = s0 + s1;
             }
-            const bool over = (sum[0] + sum[1]) + (sum[2] + sum[3]) > kMostSum && !poison;
-            if (!__any_sync(0xffffffffu, over)) break;
-            // Rare. The reference goes up by whole powers of two to the page's maximum, for the rows that need it.
+            if (!__any_sync(0xffffffffu, (sum[0] + sum[1]) + (sum[2] + sum[3]) > most)) break;
+            most = INFINITY;
+            // Rare. The reference goes to the page's largest weight, for the rows where that is far above it: by a whole
+            // power of two, which fp16 weights take exactly, unless nothing is left of them. Then every exponent is at
+            // most kUp + 3, with the score's difference taken first.
             fetch(hf);
-            const float d = over ? ceilf(largest() - M) : 0.f;
-            M += d;
-            up -= d;
-            rescale(ex2(-d), hf == 1);
+            float tm = M, tv = V, d = 0.f;
+            largest(tm, tv);
+            const float above = (tm - M) + (tv - V);
+            if (above > 3.f && !poison) {
+              d = above < 64.f ? ceilf(above) : above;
+              V = above < 64.f ? V + (d - (tm - M)) : tv;
+              M = tm;
+            }
+            if (__any_sync(0xffffffffu, d > 0.f)) rescale(ex2(-d), hf == 1);
+            aim();
+            const float at = M == -INFINITY ? 0.f : M;
+            auto apart = [&](int grp, float f) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                x[grp * 16 + c] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(x[grp * 16 + c]), f), at));
+            };
+            apart(0, fac.x), apart(1, fac.y), apart(2, fac.z), apart(3, fac.w);
+            fac = make_float4(1.f, 1.f, 1.f, 1.f);
+            shift = kUp - V;
           }
           const float4 vinv = *reinterpret_cast<const float4*>(&me.vinv[4 * hf]);
           L += fmaf(sum[0], vinv.x, sum[1] * vinv.y) + fmaf(sum[2], vinv.z, sum[3] * vinv.w);
@@ -523,12 +554,12 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       // runs of whole rows: 16-byte chunk c of row r at c ^ (r & 7), as everywhere.
       const uint32_t stage = sq + tile * (kTile * kD * 2) + quad * 32 * 128;
       // Tile 1's half of a shared block crosses over there too, 32 columns at a time, between the two warps of
-      // a row: M and L in the second plane, the output in the first.
+      // a row: M, L and V in the second plane, the output in the first.
       const uint32_t other = sq + kTile * kD * 2 + quad * 32 * 128;
       auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); };
       float f0 = 1.f, f1 = 0.f;  // the tiles' weights
       if (shared && tile == 1) {
-        asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(other + kTile * 128 + lane * 8), "f"(M), "f"(L) : "memory");
+        sts128(other + kTile * 128 + lane * 16, __float_as_uint(M), __float_as_uint(L), __float_as_uint(V), 0u);
         pair_sync();
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -544,11 +575,13 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         pair_sync();  // the next block's rows come here only once these have been read
       } else if (shared) {
         pair_sync();
-        float m1, l1;
-        asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(m1), "=f"(l1) : "r"(other + kTile * 128 + lane * 8));
+        const uint4 w = lds128(other + kTile * 128 + lane * 16);
+        const float m1 = __uint_as_float(w.x), l1 = __uint_as_float(w.y), v1 = __uint_as_float(w.z);
         const float top = fmaxf(M, m1), at = top == -INFINITY ? 0.f : top;
-        f0 = ex2(M - at);
-        f1 = ex2(m1 - at);
+        const float a0 = (M - at) + V, a1 = (m1 - at) + v1;
+        V = top == -INFINITY ? 0.f : fmaxf(a0, a1);
+        f0 = ex2(a0 - V);
+        f1 = ex2(a1 - V);
         L = L * f0 + l1 * f1;
         M = top;
       }
@@ -574,7 +607,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       if (shared ? tile == 0 : s.limit(tile) > 0) {
         const bool whole = s.from == 0 && s.to == s.u.items;
         float* part = partials + ((int64_t)(2 * cta + (s.from == 0 ? 1 : 0)) * kBlockRows + tile * kTile + quad * 32) * kPartialStride;
-        if (!whole && mine) *reinterpret_cast<float2*>(part + lane * kPartialStride) = make_float2(M, L);
+        if (!whole && mine) *reinterpret_cast<float4*>(part + lane * kPartialStride) = make_float4(M, L, V, 0.f);
         __syncwarp();
         if (whole) {
           const float inv = L == 0.f ? 0.f : 1.f / L;
