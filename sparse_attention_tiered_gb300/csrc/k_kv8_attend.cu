@@ -13,11 +13,12 @@
 // Arithmetic. m16n8k16 products on fp16 operands with fp32 sums: tokens x dimensions x rows for the
 // scores, dimensions x tokens x rows for the output. Rows are the narrow side, so eight of them, the usual
 // group, waste nothing. Codes go to fp16 exactly; queries and tail rows are scaled by a power of two into
-// fp16's range. Each 64-token page has scales k and v: with z = score * k * log2(e) + log2(v), a reference M
-// that is never more than 1 below the largest z so far, and P = 2^(z - M + 14), the output's weight is P
-// and the softmax sum's is P / v. So blocks whose values differ by any factor share one fp16 range, whose 28
-// binary orders below the largest weight are normal numbers. M moves only where a z passes it by more than
-// 1 (P may reach 2^15), so that a page costs one vote in place of a maximum over lanes.
+// fp16's range. Each 64-token page has scales k and v: with s = score * k * log2(e) and P = 2^((s - M) + (log2(v) - V) + 14),
+// the output's weight is P and the softmax sum's is P / v. So blocks whose values differ by any factor share one
+// fp16 range, whose 28 binary orders below the largest weight are normal numbers. The reference is a pair, a token's
+// s and its log2(v), so that scores may be of any size: s - M is exact near the reference, where s - (M - 14) would be
+// rounded to a step of M. It moves only where a weight passes it by more than a factor of 2 (P may reach 2^15), so
+// that a page costs one vote in place of a maximum over lanes.
 //
 // Operand layout. The k index of a product and its two outer ones may be permuted as long as the operands
 // agree, which is chosen so that no byte has to move between lanes: a lane's 16-byte chunk of a key row is
@@ -43,6 +44,8 @@ using namespace kv8;
 constexpr int kMostRows = 16;       // of a unit: a token's group, or a few tokens of a small one
 constexpr int kUnits = 4;           // announced ahead
 constexpr float kShift = 14.f;      // weights reach 2^14, and 2^15 before the reference moves
+constexpr float kFar = 2048.f;      // a sum of two exponents is right to 2^-13 below it
+constexpr float kNone = -3e38f;     // below all scores, and finite: a hidden token's -inf less this is -inf
 
 // A group is four consumer warps: as many groups as the registers have room for. A ring of 16 KB slots each (a
 // tail takes two). For 8 requests of 32768 tokens on 8 heads, 3 groups of 3 slots take 93 us; 4 of 2
@@ -54,7 +57,7 @@ constexpr size_t kRingBytes = (size_t)kSlots * kKv8PageBytes;
 constexpr size_t kJoinBytes = (size_t)kConsWarps * 8 * kD * 4;
 
 struct SlotMeta {
-  float kfac;  // score factor: page scale * softmax scale * log2(e)
+  float kfac;  // score factor: page scale * softmax scale * log2(e); NaN where one of the page's scales is
   float vlog;  // log2 of the values' scale
   float vinv;  // 1 / the values' scale
   int pos0;    // position of its first token; -1: nothing to do
@@ -74,7 +77,7 @@ struct Smem {
   float qs[kUnits][kMostRows];   // a row's score factor
   int see[kUnits][kMostRows];    // tokens that a row sees
   int64_t scratch[36];
-  float m[kConsWarps][8], l[kConsWarps][8];
+  float m[kConsWarps][8], v[kConsWarps][8], both[kConsWarps][8], l[kConsWarps][8];
   int abort;
 };
 constexpr size_t kQueryBytes = (size_t)kUnits * 2 * 8 * 32 * 8;
@@ -99,7 +102,8 @@ __device__ __forceinline__ bool consumers_agree(bool ok) {
 template <int R>
 struct State {
   float o[R][8][4];
-  float m[R][2], l[R][2];  // l: of the lane's own tokens
+  float m[R][2], w[R][2];  // the reference: a score (kNone: nothing seen yet), and kShift - log2 of its values' scale
+  float l[R][2];           // of the lane's own tokens
 };
 
 // The transposed 8 x 8 matrix of 16-bit elements.
@@ -110,26 +114,35 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 }
 
 // Takes the lane's scores z (of its rows: tokens g, g, g + 8, g + 8 in the permuted order, e alternating) into
-// the state; fp16 weights come out, p[r] for the tokens' halves.
+// the state; fp16 weights come out, p[r] for the tokens' halves. vlog, vinv: of the values' scale.
 template <int R>
-__device__ __forceinline__ void softmax_step(State<R>& st, const float (&z)[R][4], float vinv, uint32_t (&p)[R][2]) {
-  bool over = false;
+__device__ __forceinline__ void softmax_step(State<R>& st, const float (&z)[R][4], float vlog, float vinv, uint32_t (&p)[R][2]) {
+  float x[R][4];  // exponents
+  for (float most = kShift + 1.f;; most = INFINITY) {  // twice at most: nothing is above the second limit
+    float top = -INFINITY;
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) over |= fmaxf(z[r][e], z[r][2 + e]) > st.m[r][e] + 1.f;
-  if (__any_sync(0xffffffffu, over)) {
+      for (int e = 0; e < 4; ++e) {
+        x[r][e] = (z[r][e] - st.m[r][e & 1]) + (vlog + st.w[r][e & 1]);
+        top = fmaxf(top, x[r][e]);
+      }
+    if (!__any_sync(0xffffffffu, top > most)) break;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float x = fmaxf(z[r][e], z[r][2 + e]);
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-        x = fmaxf(x, st.m[r][e]);
-        const float f = x == -INFINITY ? 1.f : ex2(st.m[r][e] - x);
-        st.m[r][e] = x;
+        float score = fmaxf(z[r][e], z[r][2 + e]);
+        score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, 4));
+        score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, 8));
+        score = fmaxf(score, __shfl_xor_sync(0xffffffffu, score, 16));
+        const float above = (score - st.m[r][e]) + (vlog + st.w[r][e]);
+        float f = 1.f;
+        if (above > kShift) {
+          f = ex2(kShift - above);
+          st.m[r][e] = score;
+          st.w[r][e] = kShift - vlog;
+        }
         st.l[r][e] *= f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -142,10 +155,7 @@ __device__ __forceinline__ void softmax_step(State<R>& st, const float (&z)[R][4
   for (int r = 0; r < R; ++r) {
     float y[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float m = st.m[r][e & 1];
-      y[e] = ex2(z[r][e] - (m == -INFINITY ? -kShift : m - kShift));  // a hidden token's z is -inf
-    }
+    for (int e = 0; e < 4; ++e) y[e] = ex2(x[r][e]);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float s = y[e] + y[2 + e];
@@ -156,18 +166,26 @@ __device__ __forceinline__ void softmax_step(State<R>& st, const float (&z)[R][4
   }
 }
 
-// z = score * factor + vlog for the tokens a row may see, else -inf. `tok`: position of the lane's first token.
+// z = score * factor for the tokens a row may see, else -inf. `tok`: position of the lane's first token.
 template <int R>
-__device__ __forceinline__ void finish_scores(float (&z)[R][4], const float2 (&qs)[R], float kfac, float vlog, bool masked,
-                                              int tok, const int2 (&see)[R]) {
+__device__ __forceinline__ void finish_scores(float (&z)[R][4], const float2 (&qs)[R], float kfac, bool masked, int tok,
+                                              const int* see) {
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float& x = z[r][e];
-      x = fmaf(x, kfac * (e & 1 ? qs[r].y : qs[r].x), vlog);
-      if (masked && tok + (e >> 1) * 8 >= (e & 1 ? see[r].y : see[r].x)) x = -INFINITY;
+      x = __fmul_rn(x, kfac * (e & 1 ? qs[r].y : qs[r].x));  // rounded before the reference is taken off
     }
+  if (masked) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int2 s = *reinterpret_cast<const int2*>(see + 8 * r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (tok + (e >> 1) * 8 >= (e & 1 ? s.y : s.x)) z[r][e] = -INFINITY;
+    }
+  }
 }
 
 // Clears what is not finite of eight bf16; whether there was any; the largest of the others, folded into `top`.
@@ -378,7 +396,9 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
             ok = ok && mbar_wait(smem_u32(&sm.empty[slot]), parity ^ 1, abort, a.err);
             if (ok) {
               if (my_id >= 0) tma_page(smem_u32(ring) + slot * kKv8PageBytes, &map, my_id, full);
-              sm.meta[slot] = SlotMeta{my_sc.x * scale * kLog2e, scale_log2(my_sc.y), 1.f / my_sc.y, my_pos};
+              const bool bad = my_sc.x != my_sc.x || my_sc.y != my_sc.y;  // (a hidden token's -inf stays: it is set later)
+              sm.meta[slot] = SlotMeta{bad ? __uint_as_float(0x7fc00000u) : my_sc.x * scale * kLog2e, bad ? 0.f : scale_log2(my_sc.y),
+                                       bad ? 1.f : 1.f / my_sc.y, my_pos};
               mbar_arrive_expect_tx(full, my_id >= 0 ? kKv8PageBytes : 0);
             }
           }
@@ -416,16 +436,16 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
     if (from >= to) break;
     const int tail_items = x.u.items - x.u.pages, past = x.u.past;
     float2 qs[R];
-    int2 see[R];
+    const int* see = &sm.see[ts][2 * t];  // rows 8 r, and the next
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       qs[r] = *reinterpret_cast<const float2*>(&sm.qs[ts][8 * r + 2 * t]);
-      see[r] = *reinterpret_cast<const int2*>(&sm.see[ts][8 * r + 2 * t]);
     }
     auto query = [&](int r, int k) -> uint2 { return queries[((ts * R + r) * 8 + k) * 32 + lane]; };
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      st.m[r][0] = st.m[r][1] = -INFINITY;
+      st.m[r][0] = st.m[r][1] = kNone;
+      st.w[r][0] = st.w[r][1] = kShift;
       st.l[r][0] = st.l[r][1] = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) st.o[r][j][0] = st.o[r][j][1] = st.o[r][j][2] = st.o[r][j][3] = 0.f;
@@ -472,9 +492,9 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
             const int row = (x & 1) ? (2 * t) ^ 5 : 2 * t;
             vr[x] = lds128(vals + ((x >> 1) * 8 + row) * kD + ((g ^ row) << 4));
           }
-          finish_scores<R>(z, qs, me.kfac, me.vlog, me.pos0 + kPart > past + 1, me.pos0 + quarter * 16 + pg, see);
+          finish_scores<R>(z, qs, me.kfac, me.pos0 + kPart > past + 1, me.pos0 + quarter * 16 + pg, see);
           uint32_t p[R][2];
-          softmax_step<R>(st, z, me.vinv, p);
+          softmax_step<R>(st, z, me.vlog, me.vinv, p);
           const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vr[0]);
           const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vr[1]);
           const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vr[2]);
@@ -561,14 +581,14 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
         top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
         const int ve = half_exponent(top);
         const float vf = pow2(15 - ve);
-        finish_scores<R>(z, qs, me.kfac * pow2(ke - 15), (float)(ve - 15), true, me.pos0 + quarter * 16 + pg, see);
+        finish_scores<R>(z, qs, me.kfac * pow2(ke - 15), true, me.pos0 + quarter * 16 + pg, see);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (bad[e >> 1] && z[r][e] != -INFINITY) z[r][e] = __uint_as_float(0x7fc00000u);
         uint32_t p[R][2];
-        softmax_step<R>(st, z, vf, p);
+        softmax_step<R>(st, z, (float)(ve - 15), vf, p);
 #pragma unroll
         for (int y = 0; y < 8; ++y) {  // words of two dimensions
           const uint32_t w0 = reinterpret_cast<const uint32_t*>(&vr[0][y >> 2])[y & 3];
@@ -604,7 +624,10 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
         if (g == 0) {
+          const float v = kShift - st.w[r][e];
           sm.m[warp][2 * t + e] = st.m[r][e];
+          sm.v[warp][2 * t + e] = v;
+          sm.both[warp][2 * t + e] = st.m[r][e] + v;
           sm.l[warp][2 * t + e] = l;
         }
         // chunk c of four dimensions of row x lies at c ^ (x >> 1)
@@ -617,15 +640,29 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
       consumers_sync();
       const int d0 = lane * 4, row = r * 8 + warp;  // a warp a row, four dimensions a lane
       if (warp < 8 && row < rows) {
-        float M = -INFINITY;
+        float rel[kConsWarps], M = -INFINITY, V = 0.f;
 #pragma unroll
-        for (int w = 0; w < kConsWarps; ++w) M = fmaxf(M, sm.m[w][warp]);
-        const float base = M == -INFINITY ? 0.f : M;
+        for (int w = 0; w < kConsWarps; ++w) {
+          rel[w] = sm.both[w][warp];
+          M = fmaxf(M, rel[w]);
+        }
+        float base = M;
+        if (fabsf(M) >= kFar) {  // differences of scores first
+          M = V = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kConsWarps; ++w) M = fmaxf(M, sm.m[w][warp]);
+#pragma unroll
+          for (int w = 0; w < kConsWarps; ++w) {
+            rel[w] = (sm.m[w][warp] - M) + sm.v[w][warp];
+            V = fmaxf(V, rel[w]);
+          }
+          base = V;
+        }
         float L = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kConsWarps; ++w) {
-          const float f = ex2(sm.m[w][warp] - base);
+          const float f = ex2(rel[w] - base);
           L += sm.l[w][warp] * f;
           const float4 y = *reinterpret_cast<const float4*>(join + (w * 8 + warp) * kD + (lane ^ (warp >> 1)) * 4);
           o = make_float4(o.x + y.x * f, o.y + y.y * f, o.z + y.z * f, o.w + y.w * f);
@@ -638,7 +675,7 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
               make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
         } else {
           float* part = partials + ((int64_t)pslot * kMostRows + row) * kPartialStride;
-          if (lane == 0) *reinterpret_cast<float4*>(part) = make_float4(M, L, 0.f, 0.f);
+          if (lane == 0) *reinterpret_cast<float4*>(part) = make_float4(M, L, V, 0.f);
           *reinterpret_cast<float4*>(part + 4 + d0) = o;
         }
       }

@@ -15,6 +15,7 @@ using namespace kv8;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 static_assert(kThreads >= kMaxCtas, "a thread a part");
+constexpr float kFar = 2048.f;  // a sum of two exponents is right to 2^-13 below it
 
 __device__ __forceinline__ void add(float4& o, const float4& y, float f) {
   if (f != 0.f) o = make_float4(o.x + y.x * f, o.y + y.y * f, o.z + y.z * f, o.w + y.w * f);
@@ -101,7 +102,8 @@ kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ 
       if (x < n) y[i] = *reinterpret_cast<const float4*>(part(x, row) + 4 + 4 * lane);
     }
     if (tid < n && empty(tid)) mlv = make_float3(-INFINITY, 0.f, 0.f);
-    __syncthreads();  // the last row's sums have been read
+    // Where scores are small, one maximum does; the barrier also says that the last row's sums have been read.
+    const bool far = __syncthreads_or(mlv.x != -INFINITY && !(fabsf(mlv.x) < kFar));
     auto largest = [&](float x, float* s) {  // of the CTA; 0 where there is none
       for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
       if (lane == 0) s[warp] = x;
@@ -110,7 +112,7 @@ kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ 
       for (int w = 0; w < kWarps; ++w) x = fmaxf(x, s[w]);
       return x == -INFINITY ? 0.f : x;
     };
-    const float a = (mlv.x - largest(mlv.x, s_m)) + mlv.z;
+    const float a = (far ? mlv.x - largest(mlv.x, s_m) : mlv.x) + mlv.z;
     const float f = ex2(a - largest(a, s_v));
     if (tid < n) s_w[tid] = f;
     float L = mlv.y * f;

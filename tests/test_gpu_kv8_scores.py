@@ -125,3 +125,36 @@ def test_many_rows_one_large_score(new, at):
 @pytest.mark.parametrize("new", MANY)
 def test_many_rows_large_softmax_scale(new):
     check_scale(new, 64 * 9 + 5 + new)
+
+
+FEW = [1, 2, 4, 5, 8]  # new tokens, of groups of 2: units of up to 8 rows, and of up to 16
+
+
+@pytest.mark.parametrize("new", FEW)
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size", [1536, 2560, 2 ** 14])
+def test_few_rows_equal_scores(new, sign, size):
+    check_equal(new, size, sign, 64 * 7 + 21 + new, 1)
+
+
+@pytest.mark.parametrize("new", [1, 6])
+def test_few_rows_equal_scores_of_many_requests(new):
+    check_equal(new, 2560, 1, 150, 90)
+
+
+@pytest.mark.parametrize("new", FEW)
+@pytest.mark.parametrize("falling", [False, True])
+@pytest.mark.parametrize("size", [1536, 2560])
+def test_few_rows_scores_in_steps(new, falling, size):
+    check_steps(new, size, 64 * 7, falling)
+
+
+@pytest.mark.parametrize("new", FEW)
+@pytest.mark.parametrize("at", [0, 100, 300, 447])
+def test_few_rows_one_large_score(new, at):
+    check_jump(new, 2560, 64 * 7 + 2, at)
+
+
+@pytest.mark.parametrize("new", FEW)
+def test_few_rows_large_softmax_scale(new):
+    check_scale(new, 64 * 9 + 5 + new)
