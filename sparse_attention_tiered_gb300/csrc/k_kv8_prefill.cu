@@ -320,7 +320,18 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
     const uint32_t S = lanes + kColS + tile * kTile, O = lanes + kColO + tile * kTile;
     uint32_t done = 0;    // steps of this tile so far
     uint32_t count = 0;   // steps of the CTA so far
-    while (next()) {
+    // The two tiles' warps of the same 32 rows meet at barriers in a shared block, so they go into a segment together
+    // or not at all: one of them alone may have lost `ok` to a wait that ran out.
+    auto both = [&](bool well) {
+      int all;
+      asm volatile(
+          "{\n\t.reg .pred p, r;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.cta.red.and.pred r, %2, 64, p;\n\tselp.s32 %0, 1, 0, r;\n\t}"
+          : "=r"(all)
+          : "r"((int)well), "r"(1 + quad)
+          : "memory");
+      return all != 0;
+    };
+    while (both(next())) {
       const Segment& s = sm.segs[seg % kSegments];
       const bool shared = s.shared();  // both tiles have tile 0's rows, and every second step
       const int row = s.first_row + (shared ? 0 : tile * kTile) + quad * 32 + lane;
