@@ -683,6 +683,8 @@ kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, cons
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.task_empty[ts]));
   }
+  // The producer may have left before the wait ran out, with its last copies still in flight.
+  if (!ok) settle_down();
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

@@ -59,3 +59,23 @@ def test_the_two_tiles_warps_leave_together():
 def test_they_would_not_without_the_vote():
     """The restatement sees what the vote is for."""
     assert not all(all_losses(agree=False))
+
+
+SETTLE, LANDED = 0.25, 0.01  # seconds: settle_down(), and when any copy has landed
+
+
+def end_of_cta(issued, ran_out, consumers_settle):
+    """When the last warp of a CTA of k_kv8_attend.cu leaves: copies issued at these times, a consumer's wait that runs
+    out at another. The producer leaves with its last copy; it settles only if it has seen the abort by then."""
+    producer = max(issued) if max(issued) <= ran_out else ran_out + SETTLE
+    return max(producer, ran_out + (SETTLE if consumers_settle else 0.0))
+
+
+@pytest.mark.parametrize("last", [0.0, 1.0, 1.995, 1.9999, 2.0])
+def test_no_copy_is_in_flight_when_a_cta_ends(last):
+    issued = [t for t in (0.0, 0.5, 1.5) if t < last] + [last]
+    assert end_of_cta(issued, 2.0, True) >= last + LANDED
+
+
+def test_one_would_be_if_the_consumers_did_not_settle():
+    assert end_of_cta([0.0, 1.9999], 2.0, False) < 1.9999 + LANDED
