@@ -206,7 +206,7 @@ __device__ __forceinline__ bool clean(uint4& w, uint32_t& top) {
 template <int R>
 __global__ void __launch_bounds__(kThreads, 1)
 kv8_decode_kernel(const Kv8Args a, const __grid_constant__ CUtensorMap map, const Rows q, const Rows out, float scale,
-                  const int32_t* __restrict__ sel, int topk, JoinRecord* __restrict__ records, float* __restrict__ partials) {
+                  const int32_t* sel, int topk, JoinRecord* records, float* partials) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   float* join = reinterpret_cast<float*>(ring + kRingBytes);                 // [warps][8 rows][128]

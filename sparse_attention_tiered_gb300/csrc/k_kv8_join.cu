@@ -30,7 +30,7 @@ __device__ __forceinline__ float3 load_mlv(const float* part) {
 // takes is the chain of loads (the record, then a row's parts, all at once), so no load hangs on a value
 // that another one brings: a part that nobody wrote is loaded too, and left out.
 __global__ void __launch_bounds__(kThreads)
-kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* __restrict__ records, const float* __restrict__ partials,
+kv8_join_kernel(int G, const Rows out, int ctas, const JoinRecord* records, const float* partials,
                 int part_rows) {
   __shared__ float s_w[kMaxCtas], s_m[kWarps], s_v[kWarps], s_l[kWarps], s_o[kWarps][kD];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;

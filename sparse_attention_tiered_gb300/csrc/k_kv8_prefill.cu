@@ -246,8 +246,8 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, ui
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __global__ void __launch_bounds__(kThreads, 1)
-kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, const int32_t* __restrict__ sel, int topk,
-                   JoinRecord* __restrict__ records, float* __restrict__ partials) {
+kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, const int32_t* sel, int topk,
+                   JoinRecord* records, float* partials) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sq = smem_u32(base), sk = sq + (uint32_t)kQBytes, sv = sk + (uint32_t)kKvBytes;

@@ -61,7 +61,9 @@ cudaError_t launch_kv8_attend(const Kv8Args& a, const Rows& q, const Rows& out, 
 cudaError_t launch_kv8_prefill(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const int32_t* sel,
                                int topk, void* workspace, int sm_count, cudaStream_t st);
 // Launches a kernel that may begin while the launch before it on the stream ends: each of its CTAs waits for
-// that one's end (griddepcontrol.wait) before it touches memory.
+// that one's end (griddepcontrol.wait) before it touches memory. No pointer of such a kernel is __restrict__: what a
+// pointer to const with it points to counts as unchanged while the kernel runs, so its loads could be moved to
+// before the wait, or go through a cache that is not coherent.
 template <typename... P, typename... A>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t shared, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
