@@ -412,7 +412,7 @@ int spin_kv8_workspace(const spin_kv8* cache, int64_t* bytes);
  * [batch * kv_heads][topk], may be NULL): only the pages listed for the unit, and the
  * tail; -1, and any page that is not complete, is no page; a page listed twice counts twice.
  * q: rotated bf16 [total_new][q_heads]; out: bf16 [total_new][q_heads] = softmax(scale *
- * q K^T) V, zeros where a row sees nothing, NaN where its query is not finite. out may be q
+ * q K^T) V; zeros where a row sees nothing, whatever its query; else NaN where its query is not finite. out may be q
  * itself, with its strides; otherwise they must not overlap. Softmax statistics and sums are fp32; the
  * products run on fp16 operands, which hold e4m3 codes exactly, queries and tail rows to
  * 2^-24 of their row's or 16-token group's largest value, and probabilities to 2^-11 of themselves.

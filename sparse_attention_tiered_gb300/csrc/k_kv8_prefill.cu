@@ -339,6 +339,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       const int i = row / a.G, head = s.h * a.G + row - i * a.G;
       const int see = mine ? s.u.past + i + 1 : 0x7fffffff;  // rows that are not there see all: no masks for them
       float qs = 1.f;
+      bool wrong = false;   // the row's query is not finite: NaN, if it sees a token
       bool poison = false;  // the row's result is NaN
       const int all_steps = max(0, (min(s.to, shared ? s.limit0 : s.limit(tile)) - s.from + 1) / 2);
       const int my_steps = shared ? (all_steps - tile + 1) / 2 : all_steps;
@@ -369,8 +370,8 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         top = max(top & 0xffffu, top >> 16);
         const int e = half_exponent(top);
         const float f = scale < 0.f ? -pow2(15 - e) : pow2(15 - e);
-        poison = top >= 0x7f80u;
-        qs = poison ? 1.f : pow2(e - 15);
+        wrong = top >= 0x7f80u;
+        qs = wrong ? 1.f : pow2(e - 15);
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
           const uint4 w = lds128(place(c));
@@ -384,10 +385,10 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
 
       float M = -INFINITY, V = 0.f, L = 0.f;  // the row's reference, and the sum relative to it
       // What the exponents take, and a page's sum from which on its weights are worked out again. Both follow the reference.
-      float up = kUp, limit = poison ? INFINITY : kMostSum;
+      float up = kUp, limit = wrong ? INFINITY : kMostSum;
       auto aim = [&]() {
         up = kUp - V - (M == -INFINITY ? 0.f : M);
-        limit = poison ? INFINITY : M != -INFINITY && !(fabsf(M) < kFar) ? -1.f : kMostSum;
+        limit = wrong ? INFINITY : M != -INFINITY && !(fabsf(M) < kFar) ? -1.f : kMostSum;
       };
       for (int turn = 0; turn < my_steps; ++turn, ++done) {
         const int step = shared ? 2 * turn + tile : turn;
@@ -513,7 +514,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
             float tm = M, tv = V, d = 0.f;
             largest(tm, tv);
             const float above = (tm - M) + (tv - V);
-            if (above > 3.f && !poison) {
+            if (above > 3.f && !wrong) {
               d = above < 64.f ? ceilf(above) : above;
               V = above < 64.f ? V + (d - (tm - M)) : tv;
               M = tm;
@@ -544,6 +545,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
             bad = make_uint2(bad.x | more.x, bad.y | more.y);
           }
           const int vis = tokens(hf);
+          poison |= wrong && vis > 0;
           if (bad.x | bad.y)
             poison |= ((vis < 32 ? bad.x & ((1u << max(vis, 0)) - 1u) : bad.x) |
                        (vis < 64 ? bad.y & ((1u << max(vis - 32, 0)) - 1u) : bad.y)) != 0;
