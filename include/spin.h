@@ -332,7 +332,10 @@ int spin_measure_host_read(const void* host, int64_t bytes, int32_t ctas_per_sm,
  * rotation on the way and attended in place. No counterpart on the SPIN pages; its pages
  * are per KV head and hold one 64-token partition, as everywhere in this library, so the
  * partitions that Select picks (spin_select_noalloc, over the summaries the append writes)
- * go straight into the attention as a page list.
+ * are a page list of the attention. Select takes one count of partitions a call, and dense
+ * rows of them: requests with the same number of complete pages are selected by one call,
+ * others by calls of their own, over a dense copy of the summaries of their complete pages.
+ * What lies behind those is not the request's, and must not be scored.
  *
  * One spin_kv8 describes one layer's cache. The caller owns every array of it; the calls
  * allocate nothing, keep nothing between calls, and may be captured into CUDA graphs.
@@ -357,15 +360,16 @@ typedef struct spin_kv8 {
   int32_t kv_heads;         /* 1 <= Hkv <= 4096 */
   int32_t max_pages;        /* entries of a table row, 1 .. 2^24: a request may hold 64 * max_pages + 63 tokens */
   int64_t n_pages;          /* pages of the pool, 1 .. 2^24 */
-  uint8_t* pages;           /* [n_pages][2][64][128] e4m3, keys then values; 128-byte aligned */
+  uint8_t* pages;           /* [n_pages][2][64][128] e4m3 (without its NaN), keys then values; 128-byte aligned */
   float* scales;            /* [n_pages][2]: value = code * scale. The append writes the smallest power of two
-                               s >= 2^-64 with max|x| <= 448 s; the attention takes any positive scale. NaN:
-                               the half held a value that was not finite, and every query that sees a token of
-                               the page gets NaN. 8-byte aligned */
+                               s >= 2^-64 with max|x| <= 448 s; the attention takes any scale of 2^-64 or more. A
+                               token whose values' scale is 2^-100 or less of another's that its row sees may count
+                               for too little in the softmax sum. NaN: the half held a value that was not finite,
+                               and every query that sees a token of the page gets NaN. 8-byte aligned */
   uint16_t* tails;          /* bf16 [batch][kv_heads][2][64][128], keys then values; a value that is not finite makes
                                NaN of every query that sees its token. 16-byte aligned */
-  float* summaries;         /* fp32 [batch][kv_heads][max_pages][128]: the mean (rotated, bf16) key of each page, in the
-                               layout spin_select_noalloc reads; NULL: not wanted. 16-byte aligned */
+  float* summaries;         /* fp32 [batch][kv_heads][max_pages][128]: the mean (rotated, bf16) key of each page; rows of
+                               other pages are left as they are. NULL: not wanted. 16-byte aligned */
   const int32_t* table;     /* [batch][kv_heads][max_pages] page ids. The append needs the entries of the pages it
                                completes (each its own page), the attention those of every page it attends;
                                other entries are not read */
@@ -412,10 +416,14 @@ int spin_kv8_workspace(const spin_kv8* cache, int64_t* bytes);
  * [batch * kv_heads][topk], may be NULL): only the pages listed for the unit, and the
  * tail; -1, and any page that is not complete, is no page; a page listed twice counts twice.
  * q: rotated bf16 [total_new][q_heads]; out: bf16 [total_new][q_heads] = softmax(scale *
- * q K^T) V; zeros where a row sees nothing, whatever its query; else NaN where its query is not finite. out may be q
- * itself, with its strides; otherwise they must not overlap. Softmax statistics and sums are fp32; the
- * products run on fp16 operands, which hold e4m3 codes exactly, queries and tail rows to
- * 2^-24 of their row's or 16-token group's largest value, and probabilities to 2^-11 of themselves.
+ * q K^T) V; zeros where a row sees nothing, whatever its query; else NaN where its query is
+ * not finite. out may be q itself, with its strides; otherwise they must not overlap.
+ * Scores and softmax sums are fp32; scores may be of any size that fp32 holds, and are as
+ * exact as it holds them. The products run on fp16 operands, which hold e4m3 codes exactly,
+ * and queries and tail rows to 2^-24 of their row's or 16-token group's largest value (or
+ * to 2^-100, if that is more). A weight is a probability times its values' scale, held to
+ * 2^-10 of itself down to 2^-28 of its row's largest (2^-19 where max_new * Hq / Hkv > 16),
+ * and below that to 2^-39 (2^-30) of the largest.
  * workspace: device memory of spin_kv8_workspace bytes (some 43 MB, whatever the cache), 16-byte
  * aligned; needs no initialisation and holds nothing between calls: the layers of a model
  * need one between them. */
@@ -425,7 +433,9 @@ int spin_kv8_attend(const spin_kv8* cache, const spin_kv8_step* step, const spin
 
 /* Waits for `stream`, then turns the error word into a status: SPIN_ERR_CAPACITY (a
  * request outgrew its table row), SPIN_ERR_INVALID (lengths or page ids out of range),
- * SPIN_ERR_TIMEOUT (a bounded device wait ran out), else SPIN_OK. The word stays set. */
+ * SPIN_ERR_TIMEOUT (a bounded device wait ran out; also where a CTA's part of one unit takes
+ * more than some two seconds, which is hundreds of millions of tokens), else SPIN_OK. The
+ * word stays set. */
 int spin_kv8_status(const spin_kv8* cache, spin_stream_t stream);
 
 /* Releases everything the context owns (synchronises first). NULL is a no-op. */

@@ -80,7 +80,8 @@ class SpinKV8:
     """One layer's cache: the page pool, scales, tails and table, and the calls on them.
 
     Tensors that are not given are allocated: a pool of n_pages pages, zeroed scales and tails,
-    and (summaries=True) the fp32 mean keys that Select scores. The table (int32
+    and (summaries=True) the fp32 mean keys that Select scores, a dense copy of the complete pages' rows at a
+    time. The table (int32
     [batch][kv_heads][max_pages]) says which pool page holds page p of a head; the caller fills
     it, before the call that completes or reads the page.
 
