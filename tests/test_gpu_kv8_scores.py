@@ -158,3 +158,15 @@ def test_few_rows_one_large_score(new, at):
 @pytest.mark.parametrize("new", FEW)
 def test_few_rows_large_softmax_scale(new):
     check_scale(new, 64 * 9 + 5 + new)
+
+
+@pytest.mark.parametrize("new", [1, 5, 40, 300])
+@pytest.mark.parametrize("scale", [3.0, 30.0, 100.0, 1000.0])
+def test_scores_on_both_sides_of_where_differences_come_first(new, scale):
+    """Rows' largest scores from some hundred to some ten thousands, in base 2, in one block, over pages whose values'
+    scales differ: what is worked out in one operation and what takes the difference first, side by side."""
+    g = torch.Generator().manual_seed(new)
+    n = 64 * 20 + 30 + new
+    p = build(new, torch.randn((n, D), generator=g), values_of(n, n), seed=new + 4)
+    q = torch.randn((new, 2, D), generator=g) * torch.exp2(torch.randint(-3, 2, (new, 2, 1), generator=g).float())
+    p.check_attend(q=q.to(torch.bfloat16), scale=scale)
