@@ -20,8 +20,9 @@
 //     is what its elements wait for, so nothing is read twice.
 // Measured: a prompt of 8191 tokens, 40 query and 8 KV heads: 218 MB in 51 us, 4.3 TB/s, 0.63 of the copy's rate (53 us
 // without the launch that begins while the last one ends).
-// Half of the issue slots are used, by sines, rotations and rounding; more CTAs an SM (48 registers a thread) spill
-// and take 12% longer, page items between the rows 5%, before them the same. 256 requests of one token: 9.5 us,
+// Nothing is saturated (DRAM 45%, issue slots 49%, by sines, rotations and rounding): a warp of the rows has two
+// passes' loads in flight, and none while it computes. More CTAs an SM (48 registers a thread) spill and take 12%
+// longer, page items between the rows 5%, before them the same. 256 requests of one token: 9.5 us,
 // one chain of dependent loads.
 // A request that completes a page leaves its remaining rows to the page item of its first
 // completed page, which has read the old tail by then: no other CTA touches that tail.

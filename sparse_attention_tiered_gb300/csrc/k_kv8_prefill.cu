@@ -29,15 +29,16 @@
 // log2 of a values' scale V: scores may be of any size, where one sum of the two would lose V (and the shift) to
 // the sum's rounding. Weights up to 2^15 are let pass. Up to |M| = 2^11 an exponent is one fused operation,
 // s + (log2(v) - V + 6 - M), off by at most 2^-12; a page of a row beyond it, or one that raises the reference, is
-// taken again with s - M first, which is exact near the reference.
+// taken again with s - M first, which is exact near the reference. (The chunk below takes 3340 us where all rows are beyond.)
 //
-// Measured: 2048 tokens onto 30000, 4 KV heads in groups of 8: 2.08 TFLOP in 2000 us, 1.04 PFLOP/s. A step of two
+// Measured: 2048 tokens onto 30000, 8 KV heads in groups of 8: 2.08 TFLOP in 2000 us, 1.04 PFLOP/s. A step of two
 // tiles takes 4930 clocks. Its 32 products need 2048 at the tensor cores' rate; their operands share the shared
 // memory with the loaders' stores, and they take 3300. The rest is a softmax that the other tile's products do not
 // cover. A block costs another 5 us for its queries, its first step and its output: prompts of 300 to 6000
 // tokens run at 0.7 PFLOP/s. Queries that go to shared memory through registers, four rows a time, cost 5 us
-// a block more. Drafts of 5 tokens in groups of 8 (40 of a tile's 128 rows) read 0.33 GB in 136 us: a tile's
-// products take as long for 40 rows as for 128.
+// a block more. Drafts of 5 tokens in groups of 8 (40 of a tile's 128 rows) read 0.33 GB in 135 us: 66 steps a CTA
+// that are a chain of load, conversion, product, softmax and product with one step's codes in flight. Nothing is
+// saturated there (DRAM 31%, the tensor pipe 27%, issue slots 36%).
 #include "kv8_dev.cuh"
 
 namespace spin {

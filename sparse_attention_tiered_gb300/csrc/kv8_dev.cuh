@@ -150,10 +150,11 @@ __device__ __forceinline__ float scale_log2(float s) {
 // (or its list of pages), and the tail; the few-row kernel takes the tail first, the other one last. The items
 // of all units lie in one row, each unit's behind unit_cost places that stand for the work of beginning
 // and ending it, and CTA c of P takes the places from c W / P on. The cost is in pages: 8 for the few-row
-// kernel (48 requests of 0 to 16384 tokens take 29.9 us; with 4, 6 and 11 places 34.3, 32.8 and 29.8); 6
-// where the many-row kernel's two tiles have rows of their own, and 11 where they share a block and pass a
-// page in half of the time (prompts of 300 to 6000 tokens take 573 us with 6 places, 590 with 8, 598 with 11;
-// drafts of 5 tokens 144, 143 and 139).
+// kernel (48 requests of 0 to 16384 tokens take 26.1 us; with 4, 6 and 11 places 30.2, 29.3 and 25.4; lists of 32
+// pages 33.9, and 34.3, 34.1 and 33.7); 6 where the many-row kernel's two tiles have rows of their own, and 11
+// where they share a block and pass a page in half of the time (prompts of 300 to 6000 tokens take 575 us with 6
+// places, 587 with 8, 592 with 11; drafts of 5 tokens 139, 137 and 136). Measured at those sizes, not derived: a unit's
+// beginning and end in page times, which a longer tail or a shorter list moves little.
 // ---------------------------------------------------------------------------
 constexpr int kTileRows = 128;  // of the many-row kernel
 __device__ __forceinline__ int unit_cost(int block_rows, int rows_there) {
