@@ -36,9 +36,9 @@ def _case(name, op, batch, kv_heads, past, new=(1, 1), group=1, topk=0, drift=0.
 def listed():
     return [
         # the measured serving configuration: the next token of 32 requests of 32K
-        _case("select 32K, 32 requests", "select", 32, 8, (32767, 32767), group=5, topk=32, drift=0.9),
+        _case("select 32K of 32 requests", "select", 32, 8, (32767, 32767), group=5, topk=32, drift=0.9),
         # one very long request's next token: few rows, many pages
-        _case("select 1M, one request", "select", 1, 8, (1048575, 1048575), group=5, topk=128, drift=0.9),
+        _case("select 1M of one request", "select", 1, 8, (1048575, 1048575), group=5, topk=128, drift=0.9),
         # one chunk of a long prompt: many rows over the same pages
         _case("select chunk 2048 onto 30000", "select", 1, 8, (30000, 30000), (2048, 2048), group=8, topk=32, drift=0.95),
         # five drafted tokens verified at once, each over its own pages
@@ -48,7 +48,7 @@ def listed():
         # one chunk of a long prompt onto the 30,000 tokens before it
         _case("attend chunk 2048 onto 30000", "attend", 1, 8, (30000, 30000), (2048, 2048), group=8, topk=32, drift=0.95),
         # the decode step of a full serving batch: a page now and then, nothing but latency
-        _case("reserve one token, 256 requests", "reserve", 256, 8, (8192, 32768), pool=4),
+        _case("reserve one token of 256 requests", "reserve", 256, 8, (8192, 32768), pool=4),
         # prompt chunks of many requests at once
         _case("reserve ragged chunks", "reserve", 24, 8, (0, 20000), (1, 2048), pool=16),
         # one prompt sampled eight times: the copies share its pages
