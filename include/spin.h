@@ -372,7 +372,7 @@ typedef struct spin_kv8 {
                                other pages are left as they are. NULL: not wanted. 16-byte aligned */
   const int32_t* table;     /* [batch][kv_heads][max_pages] page ids. The append needs the entries of the pages it
                                completes (each its own page), the attention those of every page it attends;
-                               other entries are not read */
+                               other entries are not read. Written by the calls on the pool alone */
   uint32_t* error;          /* device error word; bits are only ever set */
   int32_t device;           /* CUDA device ordinal of all of these */
   int32_t rot_dim;          /* dimensions of a head that are rotated: 0 .. 128, a multiple of 16 */
@@ -431,8 +431,43 @@ int spin_kv8_attend(const spin_kv8* cache, const spin_kv8_step* step, const spin
                     float scale, const int32_t* sel, int32_t topk, void* workspace, int64_t workspace_bytes,
                     spin_stream_t stream);
 
+/* The pool of a cache's pages. refs (device int32 [n_pages], the caller's) is for each page the
+ * number of table entries that name it; 0: the page is free. A table entry that names no page is
+ * -1. A new cache has refs of zeros and a table of -1; from then on these calls keep both, and the
+ * table may not be written by anybody else. free_pages (device int32, may be NULL): the number of
+ * free pages after the call. What a call does follows from its arguments alone: pages are
+ * given in ascending order of their ids, to entries in the order request, head, page. These calls
+ * must be ordered with the others on the cache like calls that write it. */
+
+/* Bytes of device workspace (16-byte aligned) of spin_kv8_reserve and spin_kv8_compact. */
+int spin_kv8_pool_workspace(const spin_kv8* cache, int64_t* bytes);
+
+/* Before a step's append: takes free pages for the pages that the step completes, of every head,
+ * past[b] / 64 .. (past[b] + new) / 64 - 1. An entry that names a page already keeps it, so a
+ * step may be reserved ahead, in parts or twice. Where the free pages do not suffice for the
+ * whole batch nothing is taken by any request, and the error word says so (SPIN_ERR_CAPACITY). A request whose past or
+ * cu_new are out of range is left out. */
+int spin_kv8_reserve(const spin_kv8* cache, const spin_kv8_step* step, int32_t* refs, int32_t* free_pages, void* workspace,
+                     int64_t workspace_bytes, spin_stream_t stream);
+
+/* Between steps: request b becomes what request src[b] was before the call, for all b at once
+ * (src: device int32 [batch], len: device int32 [batch], tokens in the cache; both arrays
+ * distinct). src[b] = b: stays as it is; src[b] = -1: becomes empty. len follows. A request that changes drops all
+ * of its entries, and names the complete pages of its source: they are shared, and free again
+ * once nobody names them. Its tail rows 0 .. len % 64 - 1 are copied (later rows are left as they are), and where the
+ * cache has summaries, those of pages that the two did not share before. Pages that the source has reserved and
+ * not completed stay its own. A request whose src, or whose source's len, is out of range stays as it is, and
+ * the error word says so. */
+int spin_kv8_fork(const spin_kv8* cache, int32_t* refs, int32_t* len, const int32_t* src, spin_stream_t stream);
+
+/* Moves pages so that those in use, U of them, have the ids 0 .. U - 1: the j-th of those with an id
+ * of U or more goes to the j-th free one, with its scales and its count, and all entries follow.
+ * Pages U .. n_pages - 1 are then free. Entries that name a page that is not in use are left, and the error word says so. */
+int spin_kv8_compact(const spin_kv8* cache, int32_t* refs, int32_t* free_pages, void* workspace, int64_t workspace_bytes,
+                     spin_stream_t stream);
+
 /* Waits for `stream`, then turns the error word into a status: SPIN_ERR_CAPACITY (a
- * request outgrew its table row), SPIN_ERR_INVALID (lengths or page ids out of range),
+ * request outgrew its table row, or the pool had too few free pages), SPIN_ERR_INVALID (lengths or page ids out of range),
  * SPIN_ERR_TIMEOUT (a bounded device wait ran out; also where a CTA's part of one unit takes
  * more than some two seconds, which is hundreds of millions of tokens), else SPIN_OK. The
  * word stays set. */

@@ -83,6 +83,11 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sh
 cudaError_t launch_kv8_join(const Kv8Args& a, const Rows& out, int ctas, int rows, void* workspace,
                             int part_rows, cudaStream_t st);
 int64_t kv8_attend_workspace(const Kv8Args& a);
+// The page pool (k_kv8_pool.cu): refs is the number of table entries that name each page.
+int64_t kv8_pool_workspace(const Kv8Args& a);
+cudaError_t launch_kv8_reserve(const Kv8Args& a, int32_t* refs, int32_t* free_pages, void* workspace, cudaStream_t st);
+cudaError_t launch_kv8_fork(const Kv8Args& a, int32_t* refs, int32_t* len, const int32_t* src, int sm_count, cudaStream_t st);
+cudaError_t launch_kv8_compact(const Kv8Args& a, int32_t* refs, int32_t* free_pages, void* workspace, int sm_count, cudaStream_t st);
 int64_t kv8_prefill_workspace();
 
 }  // namespace spin

@@ -88,6 +88,12 @@ int check_apart(const char* who, const char* name, const spin_rows* r, int32_t t
   return ok ? SPIN_OK : refuse(SPIN_ERR_INVALID, "%s: the rows of %s overlap", who, name);
 }
 
+int check_pool(const char* who, const int32_t* refs, const int32_t* free_pages) {
+  if (!refs || off(refs, 4) || off(free_pages, 4))
+    return refuse(SPIN_ERR_INVALID, "%s: refs must not be NULL; refs and free_pages must be 4-byte aligned", who);
+  return SPIN_OK;
+}
+
 Kv8Args make_args(const spin_kv8* c, const spin_kv8_step* s) {
   Kv8Args a;
   a.B = c->batch;
@@ -218,6 +224,62 @@ int spin_kv8_attend(const spin_kv8* cache, const spin_kv8_step* step, const spin
                                          static_cast<cudaStream_t>(stream)));
 }
 
+int spin_kv8_pool_workspace(const spin_kv8* cache, int64_t* bytes) {
+  using namespace spin;
+  const int rc = check_cache("spin_kv8_pool_workspace", cache);
+  if (rc) return rc;
+  if (!bytes) return refuse(SPIN_ERR_INVALID, "spin_kv8_pool_workspace: bytes is NULL");
+  *bytes = kv8_pool_workspace(make_args(cache, nullptr));
+  return SPIN_OK;
+}
+
+int spin_kv8_reserve(const spin_kv8* cache, const spin_kv8_step* step, int32_t* refs, int32_t* free_pages, void* workspace,
+                     int64_t workspace_bytes, spin_stream_t stream) {
+  using namespace spin;
+  const char* who = "spin_kv8_reserve";
+  int rc = check_cache(who, cache);
+  if (!rc) rc = check_step(who, step);
+  if (!rc) rc = check_pool(who, refs, free_pages);
+  if (rc) return rc;
+  const Kv8Args a = make_args(cache, step);
+  if (!workspace || off(workspace, 16) || workspace_bytes < kv8_pool_workspace(a))
+    return refuse(SPIN_ERR_INVALID, "%s: workspace must be 16-byte aligned and of spin_kv8_pool_workspace bytes", who);
+  OnDevice dev(cache->device);
+  int sms = 0;
+  if ((rc = ready(who, dev, cache->device, &sms))) return rc;
+  return launched(who, launch_kv8_reserve(a, refs, free_pages, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int spin_kv8_fork(const spin_kv8* cache, int32_t* refs, int32_t* len, const int32_t* src, spin_stream_t stream) {
+  using namespace spin;
+  const char* who = "spin_kv8_fork";
+  int rc = check_cache(who, cache);
+  if (!rc) rc = check_pool(who, refs, nullptr);
+  if (rc) return rc;
+  if (!len || !src || off(len, 4) || off(src, 4) || len == src)
+    return refuse(SPIN_ERR_INVALID, "%s: len and src must be two arrays, not NULL and 4-byte aligned", who);
+  OnDevice dev(cache->device);
+  int sms = 0;
+  if ((rc = ready(who, dev, cache->device, &sms))) return rc;
+  return launched(who, launch_kv8_fork(make_args(cache, nullptr), refs, len, src, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int spin_kv8_compact(const spin_kv8* cache, int32_t* refs, int32_t* free_pages, void* workspace, int64_t workspace_bytes,
+                     spin_stream_t stream) {
+  using namespace spin;
+  const char* who = "spin_kv8_compact";
+  int rc = check_cache(who, cache);
+  if (!rc) rc = check_pool(who, refs, free_pages);
+  if (rc) return rc;
+  const Kv8Args a = make_args(cache, nullptr);
+  if (!workspace || off(workspace, 16) || workspace_bytes < kv8_pool_workspace(a))
+    return refuse(SPIN_ERR_INVALID, "%s: workspace must be 16-byte aligned and of spin_kv8_pool_workspace bytes", who);
+  OnDevice dev(cache->device);
+  int sms = 0;
+  if ((rc = ready(who, dev, cache->device, &sms))) return rc;
+  return launched(who, launch_kv8_compact(a, refs, free_pages, workspace, sms, static_cast<cudaStream_t>(stream)));
+}
+
 int spin_kv8_status(const spin_kv8* cache, spin_stream_t stream) {
   using namespace spin;
   const char* who = "spin_kv8_status";
@@ -234,7 +296,7 @@ int spin_kv8_status(const spin_kv8* cache, spin_stream_t stream) {
     return refuse(SPIN_ERR_CUDA, "%s: reading the error word failed: %s", who, cudaGetErrorString(e));
   }
   if (w & kErrTimeout) return refuse(SPIN_ERR_TIMEOUT, "%s: a bounded device wait ran out (device error 0x%x)", who, w);
-  if (w & kErrCapacity) return refuse(SPIN_ERR_CAPACITY, "%s: a request outgrew its table row (device error 0x%x)", who, w);
+  if (w & kErrCapacity) return refuse(SPIN_ERR_CAPACITY, "%s: a request outgrew its table row, or the pool has too few free pages (device error 0x%x)", who, w);
   if (w) return refuse(SPIN_ERR_INVALID, "%s: lengths or page ids out of range (device error 0x%x)", who, w);
   return SPIN_OK;
 }

@@ -83,14 +83,15 @@ class SpinKV8:
     and (summaries=True) the fp32 mean keys that Select scores, a dense copy of the complete pages' rows at a
     time. The table (int32
     [batch][kv_heads][max_pages]) says which pool page holds page p of a head; the caller fills
-    it, before the call that completes or reads the page.
+    it, before the call that completes or reads the page, or leaves it to the pool's calls (reserve, fork,
+    compact). Those keep refs (int32 [n_pages]: the table entries that name each page; refs=True: zeros, for a new cache).
 
     workspace: another handle's, or new_workspace()'s, for attend (some 43 MB). The layers of a model,
     whose calls follow one another on a stream, need one between them."""
 
     def __init__(self, batch: int, q_heads: int, kv_heads: int, max_pages: int, n_pages: Optional[int] = None, *,
                  rope: Optional[SpinRope] = None, pages=None, scales=None, tails=None, table=None, summaries=False,
-                 workspace=None, device: Optional[int] = None):
+                 refs=False, workspace=None, device: Optional[int] = None):
         import torch
         self._torch = torch
         given = [t for t in (table, pages, scales, tails) if t is not None]
@@ -117,6 +118,9 @@ class SpinKV8:
         if summaries is not False:
             self.summaries = own("summaries", None if summaries is True else summaries, torch.float32,
                                  unit + (self.max_pages, D), torch.zeros)
+        self.refs = None
+        if refs is not False:
+            self.refs = own("refs", None if refs is True else refs, torch.int32, (self.n_pages,), torch.zeros)
         self.error = torch.zeros(1, dtype=torch.int32, device=dev)
         self.rope = rope or SpinRope([])
         self.c = B.spin_kv8(self.batch, self.q_heads, self.kv_heads, self.max_pages, self.n_pages, self.pages.data_ptr(),
@@ -126,6 +130,9 @@ class SpinKV8:
                             ctypes.addressof(self.rope._c))
         lib = B.load()
         self._append, self._attend = lib.spin_kv8_append, lib.spin_kv8_attend
+        self._reserve, self._fork, self._compact = lib.spin_kv8_reserve, lib.spin_kv8_fork, lib.spin_kv8_compact
+        self._pool_bytes = B.spin_kv8_pool_workspace(self.c)
+        self._spaces = {}  # workspaces of the handle's own, by kind: the last of each list is in use
         self._c_at = ctypes.addressof(self.c)
         self.workspace = self.new_workspace() if workspace is None else _tensor("workspace", workspace, torch.uint8, None, self.device)
         self._bf16 = torch.bfloat16
@@ -203,6 +210,56 @@ class SpinKV8:
         if rc:
             B._check(rc)
         return out
+
+    def _space(self, kind, nbytes, given):
+        """(address, bytes) of the given workspace, or of one of the handle's own that is large enough. Those that were
+        outgrown stay, for the graphs that were captured with them."""
+        if given is not None:
+            _tensor("workspace", given, self._torch.uint8, None, self.device)
+            return given.data_ptr(), given.numel()
+        held = self._spaces.setdefault(kind, [])
+        if not held or held[-1].numel() < nbytes:
+            torch, dev = self._torch, self._torch.device("cuda", self.device)
+            if torch.cuda.is_current_stream_capturing():
+                raise ValueError(f"the handle's workspace of {kind} has to grow: call it once at this size before capturing, "
+                                 "or give one")
+            held.append(torch.empty(nbytes, dtype=torch.uint8, device=dev))
+            torch.cuda.synchronize(dev)  # nothing on another stream uses that memory any more
+        return held[-1].data_ptr(), held[-1].numel()
+
+    def _counts(self, free_pages):
+        if self.refs is None:
+            raise ValueError("the pool's calls need a handle with refs")
+        return None if free_pages is None else _tensor("free_pages", free_pages, self._torch.int32, (1,), self.device).data_ptr()
+
+    def reserve(self, step: SpinKV8Step, free_pages=None, workspace=None, stream: int = 0):
+        """Before the step's append: takes free pages of the pool for the pages that the step completes. Entries that name a page
+        already keep it. With too few free pages nothing is taken (check() raises). free_pages: int32 [1], gets the number of
+        those that are left."""
+        sp, _ = self._step(step)
+        count = self._counts(free_pages)
+        at, n = self._space("pool", self._pool_bytes, workspace)
+        rc = self._reserve(self._c_at, sp, self.refs.data_ptr(), count, at, n, stream)
+        if rc:
+            B._check(rc)
+
+    def fork(self, lengths, src, stream: int = 0):
+        """Between steps: request b becomes what request src[b] was, all at once; -1: empty, and its pages are free unless others
+        share them. src, lengths (tokens in the cache; updated): int32 [batch]."""
+        self._counts(None)
+        at = [_tensor(n, t, self._torch.int32, (self.batch,), self.device).data_ptr() for n, t in (("lengths", lengths), ("src", src))]
+        rc = self._fork(self._c_at, self.refs.data_ptr(), *at, stream)
+        if rc:
+            B._check(rc)
+
+    def compact(self, free_pages=None, workspace=None, stream: int = 0):
+        """Moves the pages in use to the front of the pool, and the table's entries with them. free_pages: int32 [1], gets the
+        number of the others."""
+        count = self._counts(free_pages)
+        at, n = self._space("pool", self._pool_bytes, workspace)
+        rc = self._compact(self._c_at, self.refs.data_ptr(), count, at, n, stream)
+        if rc:
+            B._check(rc)
 
     def check(self, stream: int = 0):
         """Waits for the stream; raises where a call on this cache met what only the device can see."""
