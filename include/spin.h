@@ -431,6 +431,21 @@ int spin_kv8_attend(const spin_kv8* cache, const spin_kv8_step* step, const spin
                     float scale, const int32_t* sel, int32_t topk, void* workspace, int64_t workspace_bytes,
                     spin_stream_t stream);
 
+/* Bytes of device workspace that spin_kv8_select needs for steps of up to total_new rows: 12 for
+ * each row, KV head and page of max_pages, up to about 1 GB (more rows are taken in turns). */
+int spin_kv8_select_workspace(const spin_kv8* cache, int32_t total_new, int64_t* bytes);
+
+/* Select for every new token: of the pages that row i of request b sees whole, those with
+ * 64 (p + 1) <= past[b] + i + 1, the topk with the largest (sum of the group's rotated queries) . summaries[b][h][p]. The
+ * scores are compared as exact numbers to 64 bits, equal ones go to the lower page, and one that is no number (the
+ * page holds something not finite, or the query is) counts as -infinity: how tokens are split into calls does not matter.
+ * q: rotated bf16 [total_new][q_heads]. sel: device int32 [total_new][kv_heads][topk], pages in ascending
+ * order, then -1. Rows of padding, and of requests whose numbers are out of range, are not written. 1 <= topk <= 512. The
+ * cache's summaries must be there for all complete pages. workspace: 16-byte aligned, of
+ * spin_kv8_select_workspace bytes; needs no initialisation and holds nothing between calls. */
+int spin_kv8_select(const spin_kv8* cache, const spin_kv8_step* step, const spin_rows* q, int32_t topk, int32_t* sel,
+                    void* workspace, int64_t workspace_bytes, spin_stream_t stream);
+
 /* The pool of a cache's pages. refs (device int32 [n_pages], the caller's) is for each page the
  * number of table entries that name it; 0: the page is free. A table entry that names no page is
  * -1. A new cache has refs of zeros and a table of -1; from then on these calls keep both, and the

@@ -40,7 +40,7 @@ SPIN_NOALLOC_MAX_SCORES_DEFAULT = 1 << 20  # SPIN_NOALLOC_MAX_SCORES in include/
 EXPORTS = ("spin_create", "spin_index_offload", "spin_index_offload_parts", "spin_append_kv", "spin_set_buffer", "spin_decode_step", "spin_decode_step_host", "spin_stats",
            "spin_debug_export", "spin_debug_read_page", "spin_debug_summaries", "spin_destroy", "spin_last_error",
            "spin_select_noalloc", "spin_measure_host_read", "spin_kv8_append", "spin_kv8_workspace", "spin_kv8_attend",
-           "spin_kv8_pool_workspace", "spin_kv8_reserve", "spin_kv8_fork", "spin_kv8_compact", "spin_kv8_status")
+           "spin_kv8_select_workspace", "spin_kv8_select", "spin_kv8_pool_workspace", "spin_kv8_reserve", "spin_kv8_fork", "spin_kv8_compact", "spin_kv8_status")
 
 
 class SpinError(RuntimeError):
@@ -187,6 +187,10 @@ def load(build_if_missing: bool = True):
             L.spin_kv8_workspace.restype = ctypes.c_int
             L.spin_kv8_attend.argtypes = [vp, vp, vp, vp, ctypes.c_float, vp, i32, vp, i64, vp]
             L.spin_kv8_attend.restype = ctypes.c_int
+            L.spin_kv8_select_workspace.argtypes = [vp, i32, ctypes.POINTER(i64)]
+            L.spin_kv8_select_workspace.restype = ctypes.c_int
+            L.spin_kv8_select.argtypes = [vp, vp, vp, i32, vp, vp, i64, vp]
+            L.spin_kv8_select.restype = ctypes.c_int
             L.spin_kv8_pool_workspace.argtypes = [vp, ctypes.POINTER(i64)]
             L.spin_kv8_pool_workspace.restype = ctypes.c_int
             L.spin_kv8_reserve.argtypes = [vp, vp, vp, vp, vp, i64, vp]
@@ -302,6 +306,16 @@ def spin_kv8_attend(cache, step, q, out, scale: float, sel_ptr, topk: int, works
                     stream: int = 0):
     _check(load().spin_kv8_attend(_at(cache), _at(step), _at(q), _at(out), scale, sel_ptr, topk, workspace_ptr,
                                   workspace_bytes, stream))
+
+
+def spin_kv8_select_workspace(cache, total_new: int) -> int:
+    n = ctypes.c_int64(0)
+    _check(load().spin_kv8_select_workspace(_at(cache), total_new, ctypes.byref(n)))
+    return n.value
+
+
+def spin_kv8_select(cache, step, q, topk: int, sel_ptr, workspace_ptr, workspace_bytes: int, stream: int = 0):
+    _check(load().spin_kv8_select(_at(cache), _at(step), _at(q), topk, sel_ptr, workspace_ptr, workspace_bytes, stream))
 
 
 def spin_kv8_pool_workspace(cache) -> int:

@@ -83,6 +83,10 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sh
 cudaError_t launch_kv8_join(const Kv8Args& a, const Rows& out, int ctas, int rows, void* workspace,
                             int part_rows, cudaStream_t st);
 int64_t kv8_attend_workspace(const Kv8Args& a);
+// The pages that each token selects (k_kv8_select.cu).
+int64_t kv8_select_workspace(const Kv8Args& a);
+cudaError_t launch_kv8_select(const Kv8Args& a, const Rows& q, int topk, int32_t* sel, void* workspace, int sm_count,
+                              cudaStream_t st);
 // The page pool (k_kv8_pool.cu): refs is the number of table entries that name each page.
 int64_t kv8_pool_workspace(const Kv8Args& a);
 cudaError_t launch_kv8_reserve(const Kv8Args& a, int32_t* refs, int32_t* free_pages, void* workspace, cudaStream_t st);

@@ -130,8 +130,10 @@ class SpinKV8:
                             ctypes.addressof(self.rope._c))
         lib = B.load()
         self._append, self._attend = lib.spin_kv8_append, lib.spin_kv8_attend
+        self._select = lib.spin_kv8_select
         self._reserve, self._fork, self._compact = lib.spin_kv8_reserve, lib.spin_kv8_fork, lib.spin_kv8_compact
         self._pool_bytes = B.spin_kv8_pool_workspace(self.c)
+        self._sizes = {}
         self._spaces = {}  # workspaces of the handle's own, by kind: the last of each list is in use
         self._c_at = ctypes.addressof(self.c)
         self.workspace = self.new_workspace() if workspace is None else _tensor("workspace", workspace, torch.uint8, None, self.device)
@@ -226,6 +228,31 @@ class SpinKV8:
             held.append(torch.empty(nbytes, dtype=torch.uint8, device=dev))
             torch.cuda.synchronize(dev)  # nothing on another stream uses that memory any more
         return held[-1].data_ptr(), held[-1].numel()
+
+    def _lists(self, sel, rows):
+        """topk of a list of pages for each row and KV head."""
+        if sel.dim() != 3:
+            raise ValueError("sel: need shape [total_new][kv_heads][topk]")
+        _tensor("sel", sel, self._torch.int32, (rows, self.kv_heads, sel.shape[2]), self.device)
+        return sel.shape[2]
+
+    def select(self, step: SpinKV8Step, q, sel, workspace=None, stream: int = 0):
+        """sel int32 [total_new][kv_heads][topk] = the topk pages of those that each row of the rotated q [total_new][q_heads][128]
+        sees whole, by the products of its group's queries with the summaries; ascending, -1 behind the last. After the step's
+        append. Returns sel."""
+        sp, n = self._step(step)
+        topk = self._lists(sel, n)
+        _ROWS2.pack_into(self._rows, 0, *self._row("q", q, n, self.q_heads), 0, 0, 0)
+        at, size = self._space("select", self._select_bytes(n) if workspace is None else 0, workspace)
+        rc = self._select(self._c_at, sp, self._rows_at[0], topk, sel.data_ptr(), at, size, stream)
+        if rc:
+            B._check(rc)
+        return sel
+
+    def _select_bytes(self, n):
+        if n not in self._sizes:
+            self._sizes[n] = B.spin_kv8_select_workspace(self.c, n)
+        return self._sizes[n]
 
     def _counts(self, free_pages):
         if self.refs is None:
