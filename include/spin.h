@@ -446,6 +446,19 @@ int spin_kv8_select_workspace(const spin_kv8* cache, int32_t total_new, int64_t*
 int spin_kv8_select(const spin_kv8* cache, const spin_kv8_step* step, const spin_rows* q, int32_t topk, int32_t* sel,
                     void* workspace, int64_t workspace_bytes, spin_stream_t stream);
 
+/* Bytes of device workspace that spin_kv8_attend_rows needs for steps of up to total_new rows with lists of topk. */
+int spin_kv8_attend_rows_workspace(const spin_kv8* cache, int32_t total_new, int32_t topk, int64_t* bytes);
+
+/* Attention of the step's queries where every token has its own list of pages for each KV head: sel, device
+ * int32 [total_new][kv_heads][topk], as spin_kv8_select writes it. Row i of request b sees the tokens of the
+ * listed pages p with 64 (p + 1) <= past[b] + i + 1, each page once however often it is listed and in any order; other
+ * entries (-1, a page that it does not see whole) are no page. And it sees its newest tokens, those at
+ * 64 ((past[b] + i + 1) / 64) .. past[b] + i, wherever they are by now. Everything else is as in spin_kv8_attend.
+ * 1 <= topk <= 512. workspace: of spin_kv8_attend_rows_workspace bytes, 16-byte aligned;
+ * needs no initialisation and holds nothing between calls. */
+int spin_kv8_attend_rows(const spin_kv8* cache, const spin_kv8_step* step, const spin_rows* q, const spin_rows* out, float scale,
+                         const int32_t* sel, int32_t topk, void* workspace, int64_t workspace_bytes, spin_stream_t stream);
+
 /* The pool of a cache's pages. refs (device int32 [n_pages], the caller's) is for each page the
  * number of table entries that name it; 0: the page is free. A table entry that names no page is
  * -1. A new cache has refs of zeros and a table of -1; from then on these calls keep both, and the

@@ -40,6 +40,7 @@ SPIN_NOALLOC_MAX_SCORES_DEFAULT = 1 << 20  # SPIN_NOALLOC_MAX_SCORES in include/
 EXPORTS = ("spin_create", "spin_index_offload", "spin_index_offload_parts", "spin_append_kv", "spin_set_buffer", "spin_decode_step", "spin_decode_step_host", "spin_stats",
            "spin_debug_export", "spin_debug_read_page", "spin_debug_summaries", "spin_destroy", "spin_last_error",
            "spin_select_noalloc", "spin_measure_host_read", "spin_kv8_append", "spin_kv8_workspace", "spin_kv8_attend",
+           "spin_kv8_attend_rows_workspace", "spin_kv8_attend_rows",
            "spin_kv8_select_workspace", "spin_kv8_select", "spin_kv8_pool_workspace", "spin_kv8_reserve", "spin_kv8_fork", "spin_kv8_compact", "spin_kv8_status")
 
 
@@ -187,6 +188,10 @@ def load(build_if_missing: bool = True):
             L.spin_kv8_workspace.restype = ctypes.c_int
             L.spin_kv8_attend.argtypes = [vp, vp, vp, vp, ctypes.c_float, vp, i32, vp, i64, vp]
             L.spin_kv8_attend.restype = ctypes.c_int
+            L.spin_kv8_attend_rows_workspace.argtypes = [vp, i32, i32, ctypes.POINTER(i64)]
+            L.spin_kv8_attend_rows_workspace.restype = ctypes.c_int
+            L.spin_kv8_attend_rows.argtypes = [vp, vp, vp, vp, ctypes.c_float, vp, i32, vp, i64, vp]
+            L.spin_kv8_attend_rows.restype = ctypes.c_int
             L.spin_kv8_select_workspace.argtypes = [vp, i32, ctypes.POINTER(i64)]
             L.spin_kv8_select_workspace.restype = ctypes.c_int
             L.spin_kv8_select.argtypes = [vp, vp, vp, i32, vp, vp, i64, vp]
@@ -306,6 +311,18 @@ def spin_kv8_attend(cache, step, q, out, scale: float, sel_ptr, topk: int, works
                     stream: int = 0):
     _check(load().spin_kv8_attend(_at(cache), _at(step), _at(q), _at(out), scale, sel_ptr, topk, workspace_ptr,
                                   workspace_bytes, stream))
+
+
+def spin_kv8_attend_rows_workspace(cache, total_new: int, topk: int) -> int:
+    n = ctypes.c_int64(0)
+    _check(load().spin_kv8_attend_rows_workspace(_at(cache), total_new, topk, ctypes.byref(n)))
+    return n.value
+
+
+def spin_kv8_attend_rows(cache, step, q, out, scale: float, sel_ptr, topk: int, workspace_ptr, workspace_bytes: int,
+                         stream: int = 0):
+    _check(load().spin_kv8_attend_rows(_at(cache), _at(step), _at(q), _at(out), scale, sel_ptr, topk, workspace_ptr,
+                                       workspace_bytes, stream))
 
 
 def spin_kv8_select_workspace(cache, total_new: int) -> int:

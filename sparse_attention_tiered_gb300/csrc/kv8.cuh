@@ -83,6 +83,10 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sh
 cudaError_t launch_kv8_join(const Kv8Args& a, const Rows& out, int ctas, int rows, void* workspace,
                             int part_rows, cudaStream_t st);
 int64_t kv8_attend_workspace(const Kv8Args& a);
+// Attention over a list of pages for each token (k_kv8_rows.cu).
+int64_t kv8_rows_workspace(const Kv8Args& a, int topk);
+cudaError_t launch_kv8_rows(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const int32_t* sel, int topk,
+                            void* workspace, int sm_count, cudaStream_t st);
 // The pages that each token selects (k_kv8_select.cu).
 int64_t kv8_select_workspace(const Kv8Args& a);
 cudaError_t launch_kv8_select(const Kv8Args& a, const Rows& q, int topk, int32_t* sel, void* workspace, int sm_count,

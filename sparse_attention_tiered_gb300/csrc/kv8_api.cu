@@ -257,6 +257,45 @@ int spin_kv8_select(const spin_kv8* cache, const spin_kv8_step* step, const spin
   return launched(who, launch_kv8_select(a, make_rows(q), topk, sel, workspace, sms, static_cast<cudaStream_t>(stream)));
 }
 
+int spin_kv8_attend_rows_workspace(const spin_kv8* cache, int32_t total_new, int32_t topk, int64_t* bytes) {
+  using namespace spin;
+  const char* who = "spin_kv8_attend_rows_workspace";
+  const int rc = check_cache(who, cache);
+  if (rc) return rc;
+  if (!bytes || total_new < 0 || topk < 1 || topk > kMaxTopk)
+    return refuse(SPIN_ERR_INVALID, "%s: bytes must not be NULL, total_new must be >= 0 and topk 1 .. %d", who, kMaxTopk);
+  Kv8Args a = make_args(cache, nullptr);
+  a.total_new = total_new;
+  *bytes = kv8_rows_workspace(a, topk);
+  return SPIN_OK;
+}
+
+int spin_kv8_attend_rows(const spin_kv8* cache, const spin_kv8_step* step, const spin_rows* q, const spin_rows* out, float scale,
+                         const int32_t* sel, int32_t topk, void* workspace, int64_t workspace_bytes, spin_stream_t stream) {
+  using namespace spin;
+  const char* who = "spin_kv8_attend_rows";
+  int rc = check_cache(who, cache);
+  if (!rc) rc = check_step(who, step);
+  if (!rc) rc = check_rows(who, "q", q, step->total_new);
+  if (!rc) rc = check_rows(who, "out", out, step->total_new);
+  if (!rc) rc = check_apart(who, "out", out, step->total_new, cache->q_heads);
+  if (rc) return rc;
+  if (q->ptr == out->ptr && (q->token_stride != out->token_stride || q->head_stride != out->head_stride))
+    return refuse(SPIN_ERR_INVALID, "%s: out in place of q must have its strides", who);
+  if (!std::isfinite(scale)) return refuse(SPIN_ERR_INVALID, "%s: scale must be finite", who);
+  if (topk < 1 || topk > kMaxTopk) return refuse(SPIN_ERR_INVALID, "%s: topk must be 1 .. %d", who, kMaxTopk);
+  if ((!sel && step->total_new > 0) || off(sel, 4)) return refuse(SPIN_ERR_INVALID, "%s: sel must not be NULL, and 4-byte aligned", who);
+  const Kv8Args a = make_args(cache, step);
+  if (!workspace || off(workspace, 16) || workspace_bytes < kv8_rows_workspace(a, topk))
+    return refuse(SPIN_ERR_INVALID, "%s: workspace must be 16-byte aligned and of spin_kv8_attend_rows_workspace bytes", who);
+  OnDevice dev(cache->device);
+  int sms = 0;
+  if ((rc = ready(who, dev, cache->device, &sms))) return rc;
+  if (step->total_new == 0) return SPIN_OK;
+  return launched(who, launch_kv8_rows(a, make_rows(q), make_rows(out), scale, sel, topk, workspace, sms,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
 int spin_kv8_pool_workspace(const spin_kv8* cache, int64_t* bytes) {
   using namespace spin;
   const int rc = check_cache("spin_kv8_pool_workspace", cache);

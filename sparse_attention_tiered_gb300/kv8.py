@@ -130,7 +130,7 @@ class SpinKV8:
                             ctypes.addressof(self.rope._c))
         lib = B.load()
         self._append, self._attend = lib.spin_kv8_append, lib.spin_kv8_attend
-        self._select = lib.spin_kv8_select
+        self._select, self._attend_rows = lib.spin_kv8_select, lib.spin_kv8_attend_rows
         self._reserve, self._fork, self._compact = lib.spin_kv8_reserve, lib.spin_kv8_fork, lib.spin_kv8_compact
         self._pool_bytes = B.spin_kv8_pool_workspace(self.c)
         self._sizes = {}
@@ -243,16 +243,31 @@ class SpinKV8:
         sp, n = self._step(step)
         topk = self._lists(sel, n)
         _ROWS2.pack_into(self._rows, 0, *self._row("q", q, n, self.q_heads), 0, 0, 0)
-        at, size = self._space("select", self._select_bytes(n) if workspace is None else 0, workspace)
+        at, size = self._space("select", self._bytes(B.spin_kv8_select_workspace, n) if workspace is None else 0, workspace)
         rc = self._select(self._c_at, sp, self._rows_at[0], topk, sel.data_ptr(), at, size, stream)
         if rc:
             B._check(rc)
         return sel
 
-    def _select_bytes(self, n):
-        if n not in self._sizes:
-            self._sizes[n] = B.spin_kv8_select_workspace(self.c, n)
-        return self._sizes[n]
+    def attend_rows(self, step: SpinKV8Step, q, out, sel, scale: Optional[float] = None, workspace=None, stream: int = 0):
+        """out [total_new][q_heads][128] = attention of the rotated q over the pages that each row lists for each KV head
+        (sel int32 [total_new][kv_heads][topk], as select writes it) and its newest tokens up to itself. After the step's append.
+        out may be q itself. scale: 1/sqrt(128) by default."""
+        sp, n = self._step(step)
+        topk = self._lists(sel, n)
+        _ROWS2.pack_into(self._rows, 0, *self._row("q", q, n, self.q_heads), *self._row("out", out, n, self.q_heads))
+        at, size = self._space("attend_rows", self._bytes(B.spin_kv8_attend_rows_workspace, n, topk) if workspace is None else 0, workspace)
+        rc = self._attend_rows(self._c_at, sp, self._rows_at[0], self._rows_at[1], _SCALE if scale is None else scale,
+                               sel.data_ptr(), topk, at, size, stream)
+        if rc:
+            B._check(rc)
+        return out
+
+    def _bytes(self, of, *sizes):
+        key = (of, *sizes)
+        if key not in self._sizes:
+            self._sizes[key] = of(self.c, *sizes)
+        return self._sizes[key]
 
     def _counts(self, free_pages):
         if self.refs is None:
