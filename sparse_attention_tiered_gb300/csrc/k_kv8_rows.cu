@@ -1,7 +1,35 @@
 // spin_kv8_attend_rows: attention where every token has its own list of pages.
 //
-// A first launch makes the lists of tiles of tokens out of those of tokens (kv8_rows.cuh), a second attends them.
+// A first launch makes the lists of tiles of tokens out of those of tokens (kv8_rows.cuh), a second attends them, the third
+// of spin_kv8_attend joins what CTAs shared.
+//
+// Products. A tile has up to 32 rows, an item is a page of 64 tokens: the tokens are the products' wide side, and the codes of
+// the pages are their operands as they lie in memory, e4m3 by a copy into shared memory, so that no key or value is
+// ever converted. What is not e4m3 is split: a number is a sum of e4m3 numbers of falling size, exactly for a
+// bf16 query (8 bits: two pieces, the second times 16) and an fp16 weight (11 bits: three pieces, the second times 8, the
+// third times 64). Pieces are columns of their own on the narrow side, where columns are nearly free, and are added
+// up in fp32. A step takes two pages:
+//   S[128 tokens x 64] = K (shared memory) Q^T, 32 rows in two pieces, 4 products of depth 32,
+//   O[128 dimensions x 96] += V^T P^T (shared memory, both with the tokens as rows), 32 rows in three pieces, 4 products.
+// (The tensor cores' sums were measured against exact ones: off by 2^-20.7 of the sum of the terms' sizes at most.)
+//
+// A weight's pieces cost no conversion either: an fp16 number below 2 has its exponent's top bit clear, and the seven bits
+// below are the e4m3 code of 256 times it, cut to 4 bits, subnormal numbers included. What was cut is subtracted, exactly,
+// and so on. Weights are kept below 1: 2^-3 at the reference, which is raised when one passes 1. Below 2^-14 they lose
+// bits; what is below 2^-23 of 1 is lost.
+//
+// Arithmetic as in the few-row kernel of spin_kv8_attend: with s = score * k * log2(e) per page, weights are
+// 2^((s - M) + (log2(v) - V)), the softmax sum takes weight / v; M, V per row.
+//
+// Roles, by warp:
+//   0-3, 4-7  softmax, every second step each, a token a thread, with a reference, sums and an output of their own;
+//   8         copies pages, one step's keys and values a stage, five stages;
+//   9         issues the products;
+//   10        walks the CTA's share of the items and splits the queries;
+//   11, 12    the tail: bf16 rows to two e4m3 pieces, 64 tokens as 128 rows; scores of both pieces are added, and the
+//             weights of the second are 1/16 of the first's.
 #include "kv8_rows.cuh"
+#include "kv8_tc.cuh"
 
 namespace spin {
 
@@ -14,7 +42,7 @@ constexpr int kWindow = 2048;  // pages that are marked at a time
 // A warp a tile. The tokens' pages are marked in a window of shared memory, a bit a token, and read out in order; what lies
 // beyond the window waits for the next, which begins at the lowest page that is left.
 __global__ void __launch_bounds__(32)
-kv8_rows_lists(const Kv8Args a, const int32_t* sel, int topk, RowsSpace s) {
+kv8_rows_lists(const Kv8Args a, const Rows rows, const int32_t* sel, int topk, RowsSpace s) {
   __shared__ __align__(16) uint32_t marks[kWindow];
   __shared__ int64_t scratch[36];
   const int lane = threadIdx.x, T = tile_tokens(a.G);
@@ -70,20 +98,22 @@ kv8_rows_lists(const Kv8Args a, const int32_t* sel, int topk, RowsSpace s) {
     most = __reduce_max_sync(0xffffffffu, most);
     for (int x = 0; x <= most; x += 32) {
       uint32_t bits = marks[x + lane];
+      int page = 0;
+      if (bits) {
+        page = table[base + x + lane];
+        if (page < 0 || (int64_t)page >= a.n_pages) {
+          atomicOr(a.err, (uint32_t)kErrIndex);
+          bits = 0;
+        }
+      }
       const uint32_t there = __ballot_sync(0xffffffffu, bits != 0);
       if (bits) {
-        const int p = base + x + lane, page = table[p];
         Item it;
-        it.pos = p * kPart;
+        it.pos = (base + x + lane) * kPart;
         it.page = page;
         it.rows = 0;
         it.reserved = 0;
-        const uint32_t group = a.G < 32 ? (1u << a.G) - 1u : 0xffffffffu;
-        for (; bits; bits &= bits - 1) it.rows |= group << ((__ffs(bits) - 1) * a.G);
-        if (page < 0 || (int64_t)page >= a.n_pages) {
-          atomicOr(a.err, (uint32_t)kErrIndex);
-          it.page = -1;
-        }
+        for (; bits; bits &= bits - 1) it.rows |= ((1u << a.G) - 1u) << ((__ffs(bits) - 1) * a.G);
         out[count + __popc(there & ((1u << lane) - 1u))] = it;
       }
       count += __popc(there);
@@ -91,84 +121,762 @@ kv8_rows_lists(const Kv8Args a, const int32_t* sel, int topk, RowsSpace s) {
     base = next;
     __syncwarp();
   }
+  t.listed = count;
   t.items = count + (t.tail && t.see0 + t.tokens - 1 > t.full * kPart ? 1 : 0);
   if (lane == 0) s.tiles[blockIdx.x] = t;
+  if (t.items == 0)  // its rows see nothing
+    for (int i = 0; i < t.tokens; ++i)
+      for (int x = lane; x < a.G * 16; x += 32)
+        reinterpret_cast<uint4*>(rows.p + (int64_t)(t.token0 + i) * rows.ts + (int64_t)(h * a.G + (x >> 4)) * rows.hs)[x & 15] =
+            make_uint4(0, 0, 0, 0);
 }
 
-// A CTA a tile, a warp a row at a time, a token at a time.
-constexpr int kThreads = 256;
+constexpr int kThreads = 416;
+constexpr int kProducer = 8, kMmaWarp = 9, kPlanner = 10, kTailKeys = 11;  // and the values' after it
+constexpr int kStages = 5, kTasks = 4, kReaders = 8 + 1 + 1 + 2;  // of a task: softmax, producer, products, tails
+constexpr int kStageBytes = 2 * kKv8PageBytes;                    // two pages' keys, then their values
+constexpr int kQueryBytes = 2 * kRowsOfTile * kD;                 // [piece][row][128]
+constexpr int kWeightBytes = 2 * kPart * 128;                     // [token][piece][row], 128 bytes a token
+constexpr uint32_t kColS = 0, kColO = 128;                        // tensor memory: S of both, 64 columns each; O, 128 each
+constexpr float kShift = -3.f;                                    // log2 of a weight at the reference
+constexpr float kNone = -3e38f;                                   // below all scores, and finite
+constexpr int kUnitCost = 6;                                      // pages that beginning and ending a tile cost
 
-__global__ void __launch_bounds__(kThreads)
-kv8_rows_attend(const Kv8Args a, const Rows q, const Rows out, float scale, int topk, RowsSpace s) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+struct Task {
+  Tile t;
+  int from, to;  // items; none: the share is done
+};
+
+// Steps of a task: its pages two by two, and the tail.
+__device__ __forceinline__ int task_pages(const Task& x) { return max(0, min(x.to, x.t.listed) - x.from); }
+__device__ __forceinline__ int task_steps(const Task& x) { return ((task_pages(x) + 1) >> 1) + (x.to > x.t.listed ? 1 : 0); }
+
+struct StageMeta {  // of a step's two pages
+  float kfac[2], vlog[2], vinv[2];
+  int pos[2];
+  uint32_t rows[2];
+};
+
+struct Smem {
+  uint64_t full[kStages], empty[kStages], tail_go[kStages];
+  uint64_t task_full[kTasks], task_empty[kTasks], q_full[kTasks], q_empty[2];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  Task tasks[kTasks];
+  StageMeta meta[kStages];
+  float tail_kfac[kStages][kPart], tail_vlog[kStages][kPart], tail_vinv[kStages][kPart];
+  alignas(16) float qs[kTasks][kRowsOfTile];
+  // Per softmax group and row: minus the reference's score, kShift - log2 of its values' scale, what a raised one leaves of sums.
+  alignas(16) float neg_m[2][kRowsOfTile], w[2][kRowsOfTile], f[2][kRowsOfTile];
+  float sum[2][kRowsOfTile];
+  int top[2][4][kRowsOfTile];
+  int64_t scratch[36];
+  uint32_t tmem;
+  int abort;
+};
+constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + 2 * kQueryBytes + 2 * kWeightBytes + sizeof(Smem);
+static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
+
+// e4m3 x e4m3 -> fp32, M = 128; rows_depth: both operands are stored with their depth as rows.
+constexpr uint32_t shape(int n, bool rows_depth) {
+  return 1u << 4 | (rows_depth ? 3u << 15 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(leader)
+      : "memory");
+}
+
+// Four numbers below 2^8 as two e4m3 pieces each: x = high + low / 16, exactly for 8 bits.
+__device__ __forceinline__ void two_pieces(const float (&x)[4], uint32_t& high, uint32_t& low) {
+  uint16_t h[2], l[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+    const uint32_t back = e4m3x2_half2(h[i], false);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l[i]) : "f"((x[2 * i + 1] - f.y) * 16.f), "f"((x[2 * i] - f.x) * 16.f));
+  }
+  high = h[0] | (uint32_t)h[1] << 16;
+  low = l[0] | (uint32_t)l[1] << 16;
+}
+
+// Largest absolute value of a warp's bf16 pairs, its bits.
+__device__ __forceinline__ uint32_t largest_of(uint2 w) {
+  const uint32_t top = __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
+  return __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+}
+
+// Numbers whose order as signed integers is that of the floats.
+__device__ __forceinline__ int order_of(float x) {
+  const int b = __float_as_int(x);
+  return b ^ (b >> 31 & 0x7fffffff);
+}
+__device__ __forceinline__ float float_of(int k) { return __int_as_float(k ^ (k >> 31 & 0x7fffffff)); }
+
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t x;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(addr));
+  return x;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const Rows q, const Rows out, float scale, int topk,
+                RowsSpace s, JoinRecord* records, float* partials) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t ring = smem_u32(base), sq = ring + kStages * kStageBytes, sp = sq + 2 * kQueryBytes;
+  Smem& sm = *reinterpret_cast<Smem*>(base + kStages * kStageBytes + 2 * kQueryBytes + 2 * kWeightBytes);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  volatile int* abort = &sm.abort;
+  const int ctas = gridDim.x, cta = blockIdx.x;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&sm.full[i]), 2);
+      mbar_init(smem_u32(&sm.empty[i]), 1);
+      mbar_init(smem_u32(&sm.tail_go[i]), 1);
+    }
+    for (int i = 0; i < kTasks; ++i) {
+      mbar_init(smem_u32(&sm.task_full[i]), 1);
+      mbar_init(smem_u32(&sm.task_empty[i]), kReaders);
+      mbar_init(smem_u32(&sm.q_full[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.q_empty[i]), 1);
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.p_full[i]), 4);
+      mbar_init(smem_u32(&sm.pv_done[i]), 1);
+    }
+    sm.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // The launch may begin before what is before it on the stream has ended; nothing in memory is touched until then.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if ((int)blockIdx.x >= *s.tiles_there) return;
-  const Tile t = s.tiles[blockIdx.x];
-  const int64_t unit = (int64_t)t.b * a.Hkv + t.h;
-  const Item* items = s.items + place_of(t, a.Hkv, topk);
-  const int listed = t.items - (t.tail && t.see0 + t.tokens - 1 > t.full * kPart ? 1 : 0);
-  for (int r = warp; r < t.tokens * a.G; r += kThreads / 32) {
-    const int i = r / a.G, head = t.h * a.G + r - i * a.G, see = t.see0 + i;
-    const uint2 w = *reinterpret_cast<const uint2*>(q.p + (int64_t)(t.token0 + i) * q.ts + (int64_t)head * q.hs + lane * 4);
-    const float qv[4] = {lo_f(w.x), hi_f(w.x), lo_f(w.y), hi_f(w.y)};
-    bool poison = false;
-    const bool wrong = __any_sync(0xffffffffu, !(fabsf(qv[0]) < INFINITY && fabsf(qv[1]) < INFINITY && fabsf(qv[2]) < INFINITY && fabsf(qv[3]) < INFINITY));
-    float M = -INFINITY, L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    auto token = [&](const float* k, const float* v, float kf, float vf) {
-      float x = qv[0] * k[0] + qv[1] * k[1] + qv[2] * k[2] + qv[3] * k[3];
-      for (int y = 16; y; y >>= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
-      x *= kf * scale;
-      const float top = fmaxf(M, x), f = M == top ? 1.f : exp2f((M - top) * kLog2e), p = exp2f((x - top) * kLog2e);
-      M = top;
-      L = L * f + p;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = o[e] * f + p * (v[e] * vf);
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tmem_before();
+  const int n_tiles = *s.tiles_there;
+  auto weight = [&](int x) {
+    const int n = s.tiles[x].items;
+    return n ? n + kUnitCost : 0;
+  };
+  const Place pl = locate(
+      n_tiles, sm.scratch, [&](int x, bool) { return (int64_t)weight(x); },
+      [&](int64_t total) { return share_start(total, cta, ctas); });
+  __syncthreads();
+  tmem_after();
+  const uint32_t tmem = sm.tmem;
+  bool ok = true;
+  uint32_t task = 0;   // tasks so far
+  uint32_t step = 0;   // steps so far, of all tasks: stage step % kStages
+  auto stage_of = [&](uint32_t n) { return n % kStages; };
+  auto turn_of = [&](uint32_t n) { return n / kStages & 1; };
+  auto next = [&]() {  // the next task is there and is not the end
+    warp_wait(ok, smem_u32(&sm.task_full[task % kTasks]), task / kTasks & 1, abort, a.err);
+    return ok && sm.tasks[task % kTasks].from < sm.tasks[task % kTasks].to;
+  };
+  auto done = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.task_empty[task % kTasks]));
+    ++task;
+  };
+
+  if (warp < 8) {
+    // ------------------------------ softmax, a token a thread ------------------------------
+    const int grp = warp >> 2, quad = warp & 3, token = quad * 32 + lane, half = quad >> 1;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t S = lanes + kColS + grp * 64, O = lanes + kColO + grp * 128;
+    const uint32_t weights = sp + grp * kWeightBytes;
+    float* neg_m = sm.neg_m[grp];
+    float* w = sm.w[grp];
+    uint32_t phase = 0;   // of s_full, p_full and pv_done: this group's steps so far
+    auto group_any = [&](bool x) {
+      int any;
+      asm volatile(
+          "{\n\t.reg .pred p, r;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.cta.red.or.pred r, %2, 128, p;\n\tselp.s32 %0, 1, 0, r;\n\t}"
+          : "=r"(any)
+          : "r"((int)x), "r"(2 + grp)
+          : "memory");
+      return any != 0;
     };
-    for (int it = 0; it < t.items; ++it) {
-      if (it < listed) {
-        const Item x = items[it];
-        if (!(x.rows >> r & 1) || x.page < 0) continue;
-        const float2 sc = *reinterpret_cast<const float2*>(a.scales + 2 * (int64_t)x.page);
-        poison |= !(sc.x == sc.x && sc.y == sc.y);
-        for (int j = 0; j < kPart && x.pos + j < see; ++j) {
-          const uint32_t* at = reinterpret_cast<const uint32_t*>(a.pages + (int64_t)x.page * kKv8PageBytes + j * kD) + lane;
-          float kv[2][4];
+    auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(2 + grp) : "memory"); };
+    auto both_sync = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    auto both_well = [&](bool well) {  // no warp is left alone at a barrier
+      int all;
+      asm volatile(
+          "{\n\t.reg .pred p, r;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.cta.red.and.pred r, 1, 256, p;\n\tselp.s32 %0, 1, 0, r;\n\t}"
+          : "=r"(all)
+          : "r"((int)well)
+          : "memory");
+      return all != 0;
+    };
+    for (;;) {
+      const bool more = next();
+      if (ok) warp_wait(ok, smem_u32(&sm.q_full[task % kTasks]), task / kTasks & 1, abort, a.err);
+      ok = both_well(ok);
+      if (!ok || !more) break;
+      const Task& x = sm.tasks[task % kTasks];
+      const float* qs = sm.qs[task % kTasks];
+      const int steps = task_steps(x), rows_there = x.t.tokens * a.G;
+      const bool has_tail = x.to > x.t.listed;
+      uint64_t l[16];  // softmax sums of the thread's own tokens, rows two by two
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint32_t c = at[half * (kKv8HalfBytes / 4)];
+      for (int i = 0; i < 16; ++i) l[i] = 0;
+      if (quad == 0) {
+        neg_m[lane] = -kNone;
+        w[lane] = kShift;
+      }
+      group_sync();
+      int mine = 0;  // steps of this group in the task
+      for (int n = grp; n < steps; n += 2, ++mine, ++phase) {
+        const uint32_t at = step + n, stage = stage_of(at);
+        warp_wait(ok, smem_u32(&sm.s_full[grp]), phase & 1, abort, a.err);
+        warp_wait(ok, smem_u32(&sm.full[stage]), turn_of(at), abort, a.err);
+        tmem_after();
+        const bool tail = has_tail && n == steps - 1;
+        const StageMeta& me = sm.meta[stage];
+        float kfac, vlog, vinv;
+        uint32_t allowed;
+        int pos;
+        if (tail) {
+          const int j = token & (kPart - 1);
+          kfac = sm.tail_kfac[stage][j];
+          vlog = sm.tail_vlog[stage][j];
+          vinv = token < kPart ? sm.tail_vinv[stage][j] : 0.f;  // a token counts once
+          pos = x.t.full * kPart + j;
+          allowed = rows_there < 32 ? (1u << rows_there) - 1u : 0xffffffffu;
+        } else {
+          kfac = me.kfac[half];
+          vlog = me.vlog[half];
+          vinv = me.vinv[half];
+          pos = me.pos[half] + (token & (kPart - 1));
+          allowed = me.rows[half];
+        }
+        const int late = pos - x.t.see0 + 1;  // tokens of the tile that do not see it
+        if (late > 0) allowed = late < x.t.tokens ? allowed & 0xffffffffu << late * a.G : 0u;
+        if (!ok) allowed = 0;
+        // Scores, rows 16 g .. 16 g + 15, without the row's factor and the page's: two by two.
+        auto scores = [&](int g, uint64_t (&z)[8]) {
+          uint32_t hi[16], lo[16];
+          tmem_load16(S + g * 16, hi);
+          tmem_load16(S + 32 + g * 16, lo);
+          tmem_loaded();
+          settle16(hi);
+          settle16(lo);
+          const uint64_t sixteenth = twice(0.0625f);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t f2 = e4m3x2_half2(c, y);
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f2));
-              kv[half][2 * y] = f.x;
-              kv[half][2 * y + 1] = f.y;
+          for (int i = 0; i < 8; ++i) z[i] = fma2(pack2(lo[2 * i], lo[2 * i + 1]), sixteenth, pack2(hi[2 * i], hi[2 * i + 1]));
+        };
+        // The tail's: the other piece's thread has the rest. Its scores stay where the weights go.
+        auto mine_at = [&](int r, int tok) { return weights + (r * 128 + tok) * 4; };
+        if (tail) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint64_t z[8];
+            scores(g, z);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float z0, z1;
+              unpack2(z[i], z0, z1);
+              sts32(mine_at(g * 16 + 2 * i, token), __float_as_uint(z0));
+              sts32(mine_at(g * 16 + 2 * i + 1, token), __float_as_uint(z1));
             }
           }
-          token(kv[0], kv[1], sc.x, sc.y);
+          group_sync();
         }
-      } else {
-        const uint16_t* at = a.tails + unit * kPageElems + lane * 4;
-        for (int j = 0; t.full * kPart + j < see; ++j) {
-          float kv[2][4];
-          bool bad = false;
+        auto tail_scores = [&](int g, uint64_t (&z)[8]) {
+          const int first = token & (kPart - 1);
+          const uint64_t sixteenth = twice(0.0625f);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint2 c = *reinterpret_cast<const uint2*>(at + (half * kPart + j) * kD);
-            kv[half][0] = lo_f(c.x), kv[half][1] = hi_f(c.x), kv[half][2] = lo_f(c.y), kv[half][3] = hi_f(c.y);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) bad |= !(fabsf(kv[half][e]) < INFINITY);
+          for (int i = 0; i < 8; ++i) {
+            const int r = g * 16 + 2 * i;
+            z[i] = fma2(pack2(lds32(mine_at(r, first + kPart)), lds32(mine_at(r + 1, first + kPart))), sixteenth,
+                        pack2(lds32(mine_at(r, first)), lds32(mine_at(r + 1, first))));
           }
-          poison |= __any_sync(0xffffffffu, bad);
-          token(kv[0], kv[1], 1.f, 1.f);
+        };
+        // Scaled scores, rounded before a reference is taken off. (A packed product and a packed sum become one operation.)
+        auto times = [&](uint64_t x, uint64_t y) {
+          float x0, x1, y0, y1;
+          unpack2(x, x0, x1);
+          unpack2(y, y0, y1);
+          return pack2(__float_as_uint(__fmul_rn(x0, y0)), __float_as_uint(__fmul_rn(x1, y1)));
+        };
+        auto scaled = [&](int g, uint64_t (&z)[8]) {
+          if (tail) tail_scores(g, z);
+          else scores(g, z);
+          const uint64_t k2 = twice(kfac);
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(qs + g * 16 + 2 * i);
+            z[i] = times(z[i], mul2(f.x, k2));
+            z[i + 1] = times(z[i + 1], mul2(f.y, k2));
+          }
+        };
+        float e[32];  // exponents
+        for (bool again = false;; again = true) {
+          float top = -INFINITY;
+          const uint64_t v2 = twice(vlog);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint64_t z[8];
+            scaled(g, z);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(neg_m + g * 16 + 2 * i);
+              const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(w + g * 16 + 2 * i);
+              float* y = e + g * 16 + 2 * i;
+              unpack2(add2(add2(z[i], m.x), add2(ww.x, v2)), y[0], y[1]);
+              unpack2(add2(add2(z[i + 1], m.y), add2(ww.y, v2)), y[2], y[3]);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                y[c] = allowed >> (g * 16 + 2 * i + c) & 1 ? y[c] : -INFINITY;
+                top = fmaxf(top, y[c]);
+              }
+            }
+          }
+          if (!group_any(top > 0.f || !ok) || again) break;
+          if (group_any(!ok)) {
+            ok = false;
+            break;
+          }
+          // Rare, but for a task's first step. The reference goes to the largest weight of the step, for the rows in which one has
+          // passed 1: first its score, then, with differences of scores, its values' scale.
+          auto largest = [&](auto of) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              uint64_t z[8];
+              scaled(g, z);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float z0, z1;
+                unpack2(z[i >> 1], z0, z1);
+                const int r = g * 16 + i;
+                const float y = of(i & 1 ? z1 : z0, r);
+                const int most = __reduce_max_sync(0xffffffffu, order_of(allowed >> r & 1 ? y : -INFINITY));
+                if (lane == 0) sm.top[grp][quad][r] = most;
+              }
+            }
+            group_sync();
+            const int (*t)[kRowsOfTile] = sm.top[grp];
+            const float y = float_of(max(max(t[0][lane], t[1][lane]), max(t[2][lane], t[3][lane])));
+            group_sync();
+            return y;  // of row `lane`
+          };
+          const float score = largest([&](float z, int) { return z; });
+          const float before = -neg_m[lane];
+          float* f = sm.f[grp];
+          if (quad == 0) f[lane] = score;
+          group_sync();
+          const float values = largest([&](float z, int r) { return (z - f[r]) + vlog; });
+          const float old = w[lane];
+          const bool raise = score != -INFINITY && !((score - before) + (values + old) <= 0.f);
+          const float now = kShift - values, factor = raise ? ex2((before - score) + (now - old)) : 1.f;
+          group_sync();
+          if (quad == 0) {
+            f[lane] = factor;
+            if (raise) neg_m[lane] = -score, w[lane] = now;
+          }
+          group_sync();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) l[i] = mul2(l[i], *reinterpret_cast<const uint64_t*>(f + 2 * i));
+          if (mine > 0) {  // (its last products are done: this step's were issued after them)
+#pragma unroll 1
+            for (int c = 0; c < 96; c += 8) {
+              uint32_t y[8];
+              tmem_load8(O + c, y);
+              tmem_loaded();
+              settle8(y);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float g = f[(c & 31) + k];
+                y[k] = __float_as_uint(g == 1.f ? __uint_as_float(y[k]) : __uint_as_float(y[k]) * g);
+              }
+              tmem_store8(O + c, y);
+            }
+            tmem_stored();
+          }
+        }
+        if (!ok) continue;
+        if (tail) group_sync();  // the scores have been read
+        const uint64_t u2 = twice(vinv);
+        const __half2 eight = __float2half2_rn(8.f), part = __float2half2_rn(tail && token >= kPart ? 0.0625f : 1.f);
+        const uint32_t row = weights + token * 128;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          uint32_t piece[3][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // four rows
+            uint32_t h[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float y0 = ex2(e[g * 16 + 4 * i + 2 * c]), y1 = ex2(e[g * 16 + 4 * i + 2 * c + 1]);
+              uint64_t& sum = l[g * 8 + 2 * i + c];
+              sum = fma2(pack2(__float_as_uint(y0), __float_as_uint(y1)), u2, sum);
+              h[c] = pack_half2(y0, y1);
+              if (tail) {
+                const __half2 z = __hmul2(*reinterpret_cast<__half2*>(&h[c]), part);
+                h[c] = *reinterpret_cast<const uint32_t*>(&z);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+              piece[k][i] = __byte_perm(h[0] << 1, h[1] << 1, 0x7531);
+              if (k == 2) break;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t cut = h[c] & 0xff80ff80u;
+                const __half2 z = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&h[c]), *reinterpret_cast<const __half2*>(&cut)), eight);
+                h[c] = *reinterpret_cast<const uint32_t*>(&z);
+              }
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            sts128(row + (((2 * k + g) ^ (token & 7)) << 4), piece[k][0], piece[k][1], piece[k][2], piece[k][3]);
+        }
+        proxy_fence();
+        tmem_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[grp]));
+      }
+      step += steps;
+
+      // ---- the task's end: sums over tokens, then the groups' outputs ----
+      if (mine) warp_wait(ok, smem_u32(&sm.pv_done[grp]), (phase - 1) & 1, abort, a.err);
+      tmem_after();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float l0, l1;
+        unpack2(l[i], l0, l1);
+        sts32(weights + (2 * i * 128 + token) * 4, __float_as_uint(l0));
+        sts32(weights + ((2 * i + 1) * 128 + token) * 4, __float_as_uint(l1));
+      }
+      group_sync();
+      {
+        const int r = token >> 2, part = token & 3;
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) sum += __uint_as_float(lds32(weights + (r * 128 + part * 32 + ((k + lane) & 31)) * 4));
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (part == 0) sm.sum[grp][r] = sum;
+      }
+      group_sync();
+      uint32_t o[32];
+#pragma unroll
+      for (int r = 0; r < 32; ++r) o[r] = 0;
+      if (mine && ok) {
+        const uint64_t eighth = twice(0.125f);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          uint32_t p0[16], p1[16], p2[16];
+          tmem_load16(O + g * 16, p0);
+          tmem_load16(O + 32 + g * 16, p1);
+          tmem_load16(O + 64 + g * 16, p2);
+          tmem_loaded();
+          settle16(p0);
+          settle16(p1);
+          settle16(p2);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const uint64_t y = fma2(fma2(pack2(p2[i], p2[i + 1]), eighth, pack2(p1[i], p1[i + 1])), eighth, pack2(p0[i], p0[i + 1]));
+            float y0, y1;
+            unpack2(y, y0, y1);
+            o[g * 16 + i] = __float_as_uint(y0);
+            o[g * 16 + i + 1] = __float_as_uint(y1);
+          }
         }
       }
+      if (grp == 1) {
+#pragma unroll
+        for (int r = 0; r < 32; ++r) sts32(weights + (r * 128 + token) * 4, o[r]);
+      }
+      both_sync();
+      if (grp == 0) {
+        const bool whole = x.from == 0 && x.to == x.t.items;
+        float* part = partials + (int64_t)(2 * cta + (x.from == 0 ? 1 : 0)) * kRowsOfTile * kPartialStride;
+        const uint32_t other = sp + kWeightBytes;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+          if (r >= rows_there) break;
+          // 2^(M - w) is the unit of a group's numbers: differences of scores first.
+          const float m0 = -sm.neg_m[0][r], m1 = -sm.neg_m[1][r], top = fmaxf(m0, m1);
+          const float e0 = (m0 - top) - sm.w[0][r], e1 = (m1 - top) - sm.w[1][r], most = fmaxf(e0, e1);
+          const float f0 = ex2(e0 - most), f1 = ex2(e1 - most);
+          const float L = sm.sum[0][r] * f0 + sm.sum[1][r] * f1;
+          const float y = (__uint_as_float(o[r]) * f0 + __uint_as_float(lds32(other + (r * 128 + token) * 4)) * f1) * 0x1p-8f;  // (codes are 256 times their fp16 number)
+          if (whole) {
+            const int i = r / a.G;
+            uint16_t* to = out.p + (int64_t)(x.t.token0 + i) * out.ts + (int64_t)(x.t.h * a.G + r - i * a.G) * out.hs + token;
+            const __nv_bfloat16 v = __float2bfloat16_rn(L == 0.f ? 0.f : y / L);
+            if (ok) *to = *reinterpret_cast<const uint16_t*>(&v);
+          } else {
+            float* p = part + r * kPartialStride;
+            if (token == 0) *reinterpret_cast<float4*>(p) = make_float4(top, L, most, 0.f);
+            p[4 + token] = y;
+          }
+        }
+      }
+      both_sync();  // the other group's output has been read
+      done();
     }
-    poison |= wrong && (L != 0.f);
-    const float inv = poison ? __uint_as_float(0x7fc00000u) : L == 0.f ? 0.f : 1.f / L;
-    const __nv_bfloat162 v0 = __floats2bfloat162_rn(o[0] * inv, o[1] * inv), v1 = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
-    *reinterpret_cast<uint2*>(out.p + (int64_t)(t.token0 + i) * out.ts + (int64_t)head * out.hs + lane * 4) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
+  } else if (warp == kProducer) {
+    // ------------------------------ pages ------------------------------
+    if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map)) : "memory");
+    while (next()) {
+      const Task x = sm.tasks[task % kTasks];
+      done();
+      const Item* items = s.items + place_of(x.t, a.Hkv, topk) + x.from;
+      const int pages = task_pages(x);
+      Item it;
+      float2 sc;
+      auto look = [&](int i) {
+        it.page = -1;
+        if (i < pages) {
+          const uint4 v = *reinterpret_cast<const uint4*>(items + i);
+          it.page = (int)v.x;
+          it.pos = (int)v.y;
+          it.rows = v.z;
+          sc = *reinterpret_cast<const float2*>(a.scales + 2 * (int64_t)it.page);
+        }
+      };
+      look(lane);
+      for (int p0 = 0; p0 < pages; p0 += 32) {
+        const Item my = it;
+        const float2 my_sc = sc;
+        look(p0 + 32 + lane);
+        const int n = min(32, pages - p0);
+        for (int i = 0; i < n; i += 2, ++step) {
+          const uint32_t stage = stage_of(step), full = smem_u32(&sm.full[stage]);
+          warp_wait(ok, smem_u32(&sm.empty[stage]), turn_of(step) ^ 1, abort, a.err);
+          if (!ok) break;
+          StageMeta& me = sm.meta[stage];
+          const int c = lane - i;
+          if (c == 0 || c == 1) {
+            const bool there = lane < n, bad = there && (my_sc.x != my_sc.x || my_sc.y != my_sc.y);
+            me.kfac[c] = !there ? 0.f : bad ? __uint_as_float(0x7fc00000u) : my_sc.x * scale * kLog2e;
+            me.vlog[c] = !there || bad ? 0.f : scale_log2(my_sc.y);
+            me.vinv[c] = !there || bad ? 1.f : 1.f / my_sc.y;
+            me.pos[c] = there ? my.pos : 0;
+            me.rows[c] = there ? my.rows : 0u;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_expect_tx(full, i + 1 < n ? 2 * kKv8PageBytes : kKv8PageBytes);
+            mbar_arrive(full);
+          }
+          __syncwarp();
+          if ((c == 0 || c == 1) && lane < n) {
+            const uint32_t to = ring + stage * kStageBytes + c * kKv8HalfBytes;
+            tma_half(to, &map, my.page, 0, full);
+            tma_half(to + kKv8PageBytes, &map, my.page, 1, full);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      if (!ok) break;
+      if (x.to > x.t.listed) {  // the tail warps, which pass over all other stages, must not take an earlier turn of one for theirs
+        const uint32_t stage = stage_of(step);
+        warp_wait(ok, smem_u32(&sm.empty[stage]), turn_of(step) ^ 1, abort, a.err);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(smem_u32(&sm.tail_go[stage]));
+        ++step;
+      }
+    }
+    // What was copied last has landed before the CTA's shared memory goes: the products wait for it, unless a wait ran out.
+  } else if (warp == kMmaWarp) {
+    // ------------------------------ products ------------------------------
+    const uint32_t leader = elect();
+    const uint64_t dring = operand(ring, 16, 1024), dq = operand(sq, 16, 1024), dp = operand(sp, 16, 1024);
+    uint32_t p_phase[2] = {0, 0}, last[2] = {0, 0};
+    while (next()) {
+      const Task x = sm.tasks[task % kTasks];
+      const int pages = task_pages(x), steps = task_steps(x);
+      warp_wait(ok, smem_u32(&sm.q_full[task % kTasks]), task / kTasks & 1, abort, a.err);
+      for (int n = -2; n < steps; ++n) {
+        if (n >= 0) {  // the weights of step n are there: its output, and the scores' place is free
+          const uint32_t g = n & 1, stage = stage_of(step + n);
+          warp_wait(ok, smem_u32(&sm.p_full[g]), p_phase[g]++ & 1, abort, a.err);
+          tmem_after();
+          if (!ok) break;
+          const uint64_t v = dring + ((stage * kStageBytes + kKv8PageBytes) >> 4), p = dp + (g * kWeightBytes >> 4);
+          const uint32_t d = tmem + kColO + g * 128;
+          const bool one = 2 * n + 1 == pages;  // a page alone
+          mma_f8(leader, d, v, p, shape(96, true), n >= 2);
+          mma_f8(leader, d, v + (4096 >> 4), p + (4096 >> 4), shape(96, true), 1);
+          if (!one) {
+            mma_f8(leader, d, v + (8192 >> 4), p + (8192 >> 4), shape(96, true), 1);
+            mma_f8(leader, d, v + (12288 >> 4), p + (12288 >> 4), shape(96, true), 1);
+          }
+          mma_commit(leader, smem_u32(&sm.empty[stage]));
+          mma_commit(leader, smem_u32(&sm.pv_done[g]));
+          last[g] = 1;
+        }
+        if (n + 2 < steps) {
+          const uint32_t g = n & 1, at = step + n + 2, stage = stage_of(at);
+          warp_wait(ok, smem_u32(&sm.full[stage]), turn_of(at), abort, a.err);
+          tmem_after();
+          if (!ok) break;
+          const uint64_t k = dring + (stage * kStageBytes >> 4), b = dq + ((task & 1) * kQueryBytes >> 4);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mma_f8(leader, tmem + kColS + g * 64, k + 2 * c, b + 2 * c, shape(64, false), c > 0);
+          mma_commit(leader, smem_u32(&sm.s_full[g]));
+          if (n + 3 == steps) mma_commit(leader, smem_u32(&sm.q_empty[task & 1]));
+        }
+      }
+      step += steps;
+      done();
+    }
+    // The last arrivals have landed before the CTA's shared memory goes.
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+      if (last[g]) warp_wait(ok, smem_u32(&sm.pv_done[g]), (p_phase[g] - 1) & 1, abort, a.err);
+  } else if (warp == kPlanner) {
+    // ------------------------------ plan, and query operands ------------------------------
+    JoinRecord open = JoinRecord{};
+    int64_t at = share_start(pl.total, cta, ctas), before = pl.before;
+    const int64_t stop = share_start(pl.total, cta + 1, ctas);
+    int tile = pl.b;
+    for (bool more = true; more && ok; ++task) {
+      Task x;
+      x.from = x.to = 0;
+      while (at < stop && tile < n_tiles) {
+        const int wgt = weight(tile);
+        if (wgt == 0 || at >= before + wgt) {
+          before += wgt;
+          ++tile;
+          continue;
+        }
+        x.t = s.tiles[tile];
+        const int f = (int)(at - before), t = (int)min((int64_t)wgt, f + (stop - at));
+        at += t - f;
+        x.from = max(0, f - kUnitCost);
+        x.to = max(0, t - kUnitCost);
+        if (x.from < x.to) break;
+      }
+      more = x.from < x.to;
+      const uint32_t slot = task % kTasks;
+      warp_wait(ok, smem_u32(&sm.task_empty[slot]), (task / kTasks & 1) ^ 1, abort, a.err);
+      if (!ok) break;
+      if (lane == 0) {
+        sm.tasks[slot] = x;
+        mbar_arrive(smem_u32(&sm.task_full[slot]));
+      }
+      if (more) warp_wait(ok, smem_u32(&sm.q_empty[task & 1]), (task >> 1 & 1) ^ 1, abort, a.err);
+      if (!ok) break;
+      const int rows = more ? x.t.tokens * a.G : 0;
+      const uint32_t to = sq + (task & 1) * kQueryBytes;
+#pragma unroll 1
+      for (int r0 = 0; more && r0 < kRowsOfTile; r0 += 8) {
+        uint2 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + i, y = r / a.G;
+          v[i] = make_uint2(0, 0);
+          if (r < rows)
+            v[i] = *reinterpret_cast<const uint2*>(q.p + (int64_t)(x.t.token0 + y) * q.ts + (int64_t)(x.t.h * a.G + r - y * a.G) * q.hs + lane * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + i;
+          const uint32_t top = largest_of(v[i]);
+          const int e = half_exponent(top);
+          const float f = pow2(8 - e);
+          const float y[4] = {lo_f(v[i].x) * f, hi_f(v[i].x) * f, lo_f(v[i].y) * f, hi_f(v[i].y) * f};
+          uint32_t high, low;
+          two_pieces(y, high, low);
+          const uint32_t place = to + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+          sts32(place, high);
+          sts32(place + kRowsOfTile * 128, low);
+          if (lane == 0) sm.qs[slot][r] = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e - 8);
+        }
+      }
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[slot]));
+      if (more && x.from == 0 && x.to < x.t.items) {  // (once at most: the last of the share)
+        open.total = pl.total;
+        open.parts = share_of(pl.total, before + weight(tile) - 1, ctas) - cta + 1;
+        open.row0 = x.t.token0;
+        open.n_new = x.t.tokens;
+        open.h = x.t.h;
+        open.first_row = 0;
+      }
+    }
+    if (lane == 0) records[cta] = open;
+  } else {
+    // ------------------------------ tails ------------------------------
+    const int half = warp - kTailKeys;
+    uint32_t gone = 0;  // a bit per stage: the parity of its tails so far
+    while (next()) {
+      const Task x = sm.tasks[task % kTasks];
+      done();
+      const int steps = task_steps(x);
+      step += steps;
+      if (x.to <= x.t.listed) continue;
+      const uint32_t at = step - 1, stage = stage_of(at);
+      warp_wait(ok, smem_u32(&sm.tail_go[stage]), gone >> stage & 1, abort, a.err);
+      if (!ok) break;
+      gone ^= 1u << stage;
+      const uint32_t to = ring + stage * kStageBytes + half * kKv8PageBytes;
+      const uint16_t* src = a.tails + ((int64_t)x.t.b * a.Hkv + x.t.h) * kPageElems + half * kPart * kD + lane * 4;
+#pragma unroll 1
+      for (int r0 = 0; r0 < kPart; r0 += 8) {
+        uint2 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = r0 + i < x.t.tail ? *reinterpret_cast<const uint2*>(src + (r0 + i) * kD) : make_uint2(0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + i;
+          bool wrong = false;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t& y = k ? v[i].y : v[i].x;
+            const bool lo = (y & 0x7f80u) == 0x7f80u, hi = (y & 0x7f800000u) == 0x7f800000u;
+            wrong |= lo | hi;
+            if (lo) y &= 0xffff0000u;
+            if (hi) y &= 0x0000ffffu;
+          }
+          wrong = __any_sync(0xffffffffu, wrong);
+          const int e = half_exponent(largest_of(v[i]));
+          const float f = pow2(8 - e);
+          const float y[4] = {lo_f(v[i].x) * f, hi_f(v[i].x) * f, lo_f(v[i].y) * f, hi_f(v[i].y) * f};
+          uint32_t high, low;
+          two_pieces(y, high, low);
+          const uint32_t place = to + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+          sts32(place, high);
+          sts32(place + kKv8HalfBytes, low);
+          if (lane == 0) {
+            const float nan = __uint_as_float(0x7fc00000u);
+            if (half == 0) {
+              sm.tail_kfac[stage][r] = wrong ? nan : scale * kLog2e * pow2(e - 8);
+            } else {
+              sm.tail_vlog[stage][r] = wrong ? nan : (float)(e - 8);
+              sm.tail_vinv[stage][r] = f;
+            }
+          }
+        }
+      }
+      proxy_fence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.full[stage]));
+    }
+  }
+  tmem_before();
+  __syncthreads();
+  tmem_after();
+  if (warp == kMmaWarp) {
+    if (*abort) settle_down();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
 
@@ -177,9 +885,11 @@ int64_t most_tiles(const Kv8Args& a) {
   return (n / tile_tokens(a.G) + (a.B < n ? a.B : n)) * a.Hkv;
 }
 
+constexpr int64_t kPartialBytes = (int64_t)2 * kMaxCtas * kRowsOfTile * kPartialStride * 4;
+
 RowsSpace space_of(const Kv8Args& a, void* workspace) {
   RowsSpace s;
-  s.tiles_there = static_cast<int32_t*>(workspace);
+  s.tiles_there = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kRecordBytes + kPartialBytes);
   s.tiles = reinterpret_cast<Tile*>(s.tiles_there + 4);
   s.items = reinterpret_cast<Item*>(s.tiles + most_tiles(a));
   return s;
@@ -188,16 +898,23 @@ RowsSpace space_of(const Kv8Args& a, void* workspace) {
 }  // namespace
 
 int64_t kv8_rows_workspace(const Kv8Args& a, int topk) {
-  return 16 + most_tiles(a) * (int64_t)sizeof(Tile) + (int64_t)a.total_new * a.Hkv * (topk + 1) * (int64_t)sizeof(Item);
+  return (int64_t)kRecordBytes + kPartialBytes + 16 + most_tiles(a) * (int64_t)sizeof(Tile) +
+         (int64_t)a.total_new * a.Hkv * (topk + 1) * (int64_t)sizeof(Item);
 }
 
 cudaError_t launch_kv8_rows(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const int32_t* sel, int topk,
                             void* workspace, int sm_count, cudaStream_t st) {
   const RowsSpace s = space_of(a, workspace);
-  const unsigned tiles = (unsigned)most_tiles(a);
-  cudaError_t e = launch_early(kv8_rows_lists, dim3(tiles), 32, 0, st, a, sel, topk, s);
+  CUtensorMap map;
+  cudaError_t e = kv8_page_map(a, kPart, &map);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kv8_rows_attend, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (e == cudaSuccess) e = launch_early(kv8_rows_lists, dim3((unsigned)most_tiles(a)), 32, 0, st, a, out, sel, topk, s);
   if (e != cudaSuccess) return e;
-  return launch_early(kv8_rows_attend, dim3(tiles), kThreads, 0, st, a, q, out, scale, topk, s);
+  const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+  e = launch_early(kv8_rows_attend, dim3((unsigned)ctas), kThreads, kSmemBytes, st, a, map, q, out, scale, topk, s,
+                   static_cast<JoinRecord*>(workspace), reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes));
+  if (e != cudaSuccess || ctas == 1) return e;
+  return launch_kv8_join(a, out, ctas, kRowsOfTile, workspace, kRowsOfTile, st);
 }
 
 }  // namespace spin

@@ -17,9 +17,11 @@ struct alignas(16) Tile {
   int32_t token0, tokens;  // rows of q and out: tokens [token0, token0 + tokens)
   int32_t see0;            // what the first of them sees: tokens 0 .. see0 - 1; the next one more, and so on
   int32_t full, tail;      // the request's complete pages, and tokens behind them
-  int32_t items;           // pages listed, and one more for the tail if a row sees it
+  int32_t listed;          // pages
+  int32_t items;           // those, and one more for the tail if a row sees it
+  int32_t reserved[3];
 };
-static_assert(sizeof(Tile) == 32, "");
+static_assert(sizeof(Tile) == 48, "");
 
 struct alignas(16) Item {
   int32_t page;   // of the pool
