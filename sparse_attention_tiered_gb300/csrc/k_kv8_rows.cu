@@ -6,8 +6,8 @@
 // Products. A tile has up to 32 rows, an item is a page of 64 tokens: the tokens are the products' wide side, and the codes of
 // the pages are their operands as they lie in memory, e4m3 by a copy into shared memory, so that no key or value is
 // ever converted. What is not e4m3 is split: a number is a sum of e4m3 numbers of falling size, exactly for a
-// bf16 query (8 bits: two pieces, the second times 16) and an fp16 weight (11 bits: three pieces, the second times 8, the
-// third times 64). Pieces are columns of their own on the narrow side, where columns are nearly free, and are added
+// bf16 query (8 bits: two pieces, the second times 16) and an fp16 weight (11 bits: three pieces, times 1, 16 and
+// 256). Pieces are columns of their own on the narrow side, where columns are nearly free, and are added
 // up in fp32. A step takes two pages:
 //   S[128 tokens x 64] = K (shared memory) Q^T, 32 rows in two pieces, 4 products of depth 32,
 //   O[128 dimensions x 96] += V^T P^T (shared memory, both with the tokens as rows), 32 rows in three pieces, 4 products.
@@ -15,8 +15,8 @@
 //
 // A weight's pieces cost no conversion either: an fp16 number below 2 has its exponent's top bit clear, and the seven bits
 // below are the e4m3 code of 256 times it, cut to 4 bits, subnormal numbers included. What was cut is subtracted, exactly,
-// and so on. Weights are kept below 1: 2^-3 at the reference, which is raised when one passes 1. Below 2^-14 they lose
-// bits; what is below 2^-23 of 1 is lost.
+// and so on. Weights are kept up to 1, so that what was cut is below 1 again when it is taken 16 times: 2^-5 at the
+// reference, which is raised when one passes 1. Below 2^-14 they lose bits; what is below 2^-25 of 1 is lost.
 //
 // Arithmetic as in the few-row kernel of spin_kv8_attend: with s = score * k * log2(e) per page, weights are
 // 2^((s - M) + (log2(v) - V)), the softmax sum takes weight / v; M, V per row.
@@ -131,14 +131,15 @@ kv8_rows_lists(const Kv8Args a, const Rows rows, const int32_t* sel, int topk, R
             make_uint4(0, 0, 0, 0);
 }
 
-constexpr int kThreads = 416;
+constexpr int kThreads = 512;  // three warps idle: registers are given to four warps at a time
 constexpr int kProducer = 8, kMmaWarp = 9, kPlanner = 10, kTailKeys = 11;  // and the values' after it
 constexpr int kStages = 5, kTasks = 4, kReaders = 8 + 1 + 1 + 2;  // of a task: softmax, producer, products, tails
 constexpr int kStageBytes = 2 * kKv8PageBytes;                    // two pages' keys, then their values
 constexpr int kQueryBytes = 2 * kRowsOfTile * kD;                 // [piece][row][128]
 constexpr int kWeightBytes = 2 * kPart * 128;                     // [token][piece][row], 128 bytes a token
 constexpr uint32_t kColS = 0, kColO = 128;                        // tensor memory: S of both, 64 columns each; O, 128 each
-constexpr float kShift = -3.f;                                    // log2 of a weight at the reference
+constexpr float kShift = -5.f;                                    // log2 of a weight at the reference
+constexpr float kFar = 2048.f;                                    // a sum of two exponents is right to 2^-13 below it
 constexpr float kNone = -3e38f;                                   // below all scores, and finite
 constexpr int kUnitCost = 6;                                      // pages that beginning and ending a tile cost
 
@@ -169,6 +170,7 @@ struct Smem {
   alignas(16) float neg_m[2][kRowsOfTile], w[2][kRowsOfTile], f[2][kRowsOfTile];
   float sum[2][kRowsOfTile];
   int top[2][4][kRowsOfTile];
+  uint32_t over[2][4];
   int64_t scratch[36];
   uint32_t tmem;
   int abort;
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const Rows q, const Rows out, float scale, int topk,
                 RowsSpace s, JoinRecord* records, float* partials) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* base = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (through an integer it would be a pointer to anywhere)
   const uint32_t ring = smem_u32(base), sq = ring + kStages * kStageBytes, sp = sq + 2 * kQueryBytes;
   Smem& sm = *reinterpret_cast<Smem*>(base + kStages * kStageBytes + 2 * kQueryBytes + 2 * kWeightBytes);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -289,6 +291,12 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
     ++task;
   };
 
+  // Registers: 512 threads x 128 at launch = 256 x 168 + 256 x 80, and some.
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  }
   if (warp < 8) {
     // ------------------------------ softmax, a token a thread ------------------------------
     const int grp = warp >> 2, quad = warp & 3, token = quad * 32 + lane, half = quad >> 1;
@@ -447,8 +455,67 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
             ok = false;
             break;
           }
-          // Rare, but for a task's first step. The reference goes to the largest weight of the step, for the rows in which one has
-          // passed 1: first its score, then, with differences of scores, its values' scale.
+          // A weight has passed 1. In few rows, as a rule, and by little: those take a power of two off.
+          uint32_t over = 0;
+#pragma unroll
+          for (int r = 0; r < 32; ++r) over |= (e[r] > 0.f ? 1u : 0u) << r;
+          over = __reduce_or_sync(0xffffffffu, over);
+          if (lane == 0) sm.over[grp][quad] = over;
+          group_sync();
+          over = sm.over[grp][0] | sm.over[grp][1] | sm.over[grp][2] | sm.over[grp][3];
+#pragma unroll
+          for (int r = 0; r < 32; ++r)
+            if (over >> r & 1) {
+              const int most = __reduce_max_sync(0xffffffffu, order_of(e[r]));
+              if (lane == 0) sm.top[grp][quad][r] = most;
+            }
+          group_sync();
+          float* f = sm.f[grp];
+          auto largest_row = [&]() {
+            const int (*t)[kRowsOfTile] = sm.top[grp];
+            return float_of(max(max(t[0][lane], t[1][lane]), max(t[2][lane], t[3][lane])));
+          };
+          // The products' sums so far of row r's group of 8.
+          auto rescale = [&](int c) {
+            uint32_t y[8];
+            tmem_load8(O + c, y);
+            tmem_loaded();
+            settle8(y);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float g = f[(c & 31) + k];
+              y[k] = __float_as_uint(g == 1.f ? __uint_as_float(y[k]) : __uint_as_float(y[k]) * g);
+            }
+            tmem_store8(O + c, y);
+          };
+          const bool raised = over >> lane & 1;
+          const float passed = raised ? largest_row() : 0.f;
+          group_sync();
+          if (!__any_sync(0xffffffffu, !(passed < 64.f))) {
+            const float d = raised ? ceilf(passed) - kShift : 0.f;
+            if (quad == 0) {
+              f[lane] = pow2(-(int)d);
+              w[lane] -= d;
+            }
+            group_sync();
+#pragma unroll
+            for (int r = 0; r < 32; ++r)
+              if (over >> r & 1) e[r] -= __shfl_sync(0xffffffffu, d, r);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (over >> (2 * i) & 3) l[i] = mul2(l[i], *reinterpret_cast<const uint64_t*>(f + 2 * i));
+            if (mine > 0) {  // (its last products are done: this step's were issued after them)
+#pragma unroll 1
+              for (int c = 0; c < 96; c += 8)
+                if (over >> (c & 31) & 0xffu) rescale(c);
+              tmem_stored();
+            }
+            group_sync();  // f has been read
+            break;
+          }
+          // The first step, or a score far above all others: the reference goes to the largest weight of the step. Where scores are
+          // so large that adding the values' scale would lose it, first to its score and then, with differences of scores,
+          // to its values' scale.
           auto largest = [&](auto of) {
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
@@ -465,17 +532,18 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
               }
             }
             group_sync();
-            const int (*t)[kRowsOfTile] = sm.top[grp];
-            const float y = float_of(max(max(t[0][lane], t[1][lane]), max(t[2][lane], t[3][lane])));
+            const float y = largest_row();
             group_sync();
             return y;  // of row `lane`
           };
-          const float score = largest([&](float z, int) { return z; });
+          float score = largest([&](float z, int) { return z + vlog; }), values = 0.f;
+          if (__any_sync(0xffffffffu, score != -INFINITY && !(fabsf(score) < kFar))) {
+            score = largest([&](float z, int) { return z; });
+            if (quad == 0) f[lane] = score;
+            group_sync();
+            values = largest([&](float z, int r) { return (z - f[r]) + vlog; });
+          }
           const float before = -neg_m[lane];
-          float* f = sm.f[grp];
-          if (quad == 0) f[lane] = score;
-          group_sync();
-          const float values = largest([&](float z, int r) { return (z - f[r]) + vlog; });
           const float old = w[lane];
           const bool raise = score != -INFINITY && !((score - before) + (values + old) <= 0.f);
           const float now = kShift - values, factor = raise ? ex2((before - score) + (now - old)) : 1.f;
@@ -487,27 +555,16 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
           group_sync();
 #pragma unroll
           for (int i = 0; i < 16; ++i) l[i] = mul2(l[i], *reinterpret_cast<const uint64_t*>(f + 2 * i));
-          if (mine > 0) {  // (its last products are done: this step's were issued after them)
+          if (mine > 0) {
 #pragma unroll 1
-            for (int c = 0; c < 96; c += 8) {
-              uint32_t y[8];
-              tmem_load8(O + c, y);
-              tmem_loaded();
-              settle8(y);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float g = f[(c & 31) + k];
-                y[k] = __float_as_uint(g == 1.f ? __uint_as_float(y[k]) : __uint_as_float(y[k]) * g);
-              }
-              tmem_store8(O + c, y);
-            }
+            for (int c = 0; c < 96; c += 8) rescale(c);
             tmem_stored();
           }
         }
         if (!ok) continue;
         if (tail) group_sync();  // the scores have been read
         const uint64_t u2 = twice(vinv);
-        const __half2 eight = __float2half2_rn(8.f), part = __float2half2_rn(tail && token >= kPart ? 0.0625f : 1.f);
+        const __half2 sixteen = __float2half2_rn(16.f), part = __float2half2_rn(tail && token >= kPart ? 0.0625f : 1.f);
         const uint32_t row = weights + token * 128;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
@@ -533,7 +590,7 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 const uint32_t cut = h[c] & 0xff80ff80u;
-                const __half2 z = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&h[c]), *reinterpret_cast<const __half2*>(&cut)), eight);
+                const __half2 z = __hmul2(__hsub2(*reinterpret_cast<__half2*>(&h[c]), *reinterpret_cast<const __half2*>(&cut)), sixteen);
                 h[c] = *reinterpret_cast<const uint32_t*>(&z);
               }
             }
@@ -574,7 +631,7 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
 #pragma unroll
       for (int r = 0; r < 32; ++r) o[r] = 0;
       if (mine && ok) {
-        const uint64_t eighth = twice(0.125f);
+        const uint64_t sixteenth = twice(0.0625f);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           uint32_t p0[16], p1[16], p2[16];
@@ -587,7 +644,7 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
           settle16(p2);
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const uint64_t y = fma2(fma2(pack2(p2[i], p2[i + 1]), eighth, pack2(p1[i], p1[i + 1])), eighth, pack2(p0[i], p0[i + 1]));
+            const uint64_t y = fma2(fma2(pack2(p2[i], p2[i + 1]), sixteenth, pack2(p1[i], p1[i + 1])), sixteenth, pack2(p0[i], p0[i + 1]));
             float y0, y1;
             unpack2(y, y0, y1);
             o[g * 16 + i] = __float_as_uint(y0);
@@ -602,26 +659,35 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
       both_sync();
       if (grp == 0) {
         const bool whole = x.from == 0 && x.to == x.t.items;
-        float* part = partials + (int64_t)(2 * cta + (x.from == 0 ? 1 : 0)) * kRowsOfTile * kPartialStride;
         const uint32_t other = sp + kWeightBytes;
+        // Lane r has row r's factors and place. 2^(M - w) is the unit of a group's numbers: differences of scores first.
+        const float m0 = -sm.neg_m[0][lane], m1 = -sm.neg_m[1][lane], top = fmaxf(m0, m1);
+        const float e0 = (m0 - top) - sm.w[0][lane], e1 = (m1 - top) - sm.w[1][lane], most = fmaxf(e0, e1);
+        float f0 = ex2(e0 - most), f1 = ex2(e1 - most);
+        const float L = sm.sum[0][lane] * f0 + sm.sum[1][lane] * f1;
+        const float unit = whole ? L == 0.f ? 0.f : 0x1p-8f / L : 0x1p-8f;  // (codes are 256 times their fp16 number)
+        f0 *= unit;
+        f1 *= unit;
+        uint64_t to;
+        if (whole) {
+          const int i = lane / a.G;
+          to = reinterpret_cast<uint64_t>(out.p + (int64_t)(x.t.token0 + i) * out.ts + (int64_t)(x.t.h * a.G + lane - i * a.G) * out.hs);
+        } else {
+          float* p = partials + ((int64_t)(2 * cta + (x.from == 0 ? 1 : 0)) * kRowsOfTile + lane) * kPartialStride;
+          if (quad == 0 && lane < rows_there) *reinterpret_cast<float4*>(p) = make_float4(top, L, most, 0.f);
+          to = reinterpret_cast<uint64_t>(p + 4);
+        }
 #pragma unroll
         for (int r = 0; r < 32; ++r) {
-          if (r >= rows_there) break;
-          // 2^(M - w) is the unit of a group's numbers: differences of scores first.
-          const float m0 = -sm.neg_m[0][r], m1 = -sm.neg_m[1][r], top = fmaxf(m0, m1);
-          const float e0 = (m0 - top) - sm.w[0][r], e1 = (m1 - top) - sm.w[1][r], most = fmaxf(e0, e1);
-          const float f0 = ex2(e0 - most), f1 = ex2(e1 - most);
-          const float L = sm.sum[0][r] * f0 + sm.sum[1][r] * f1;
-          const float y = (__uint_as_float(o[r]) * f0 + __uint_as_float(lds32(other + (r * 128 + token) * 4)) * f1) * 0x1p-8f;  // (codes are 256 times their fp16 number)
+          const float y = __uint_as_float(o[r]) * __shfl_sync(0xffffffffu, f0, r) +
+                          __uint_as_float(lds32(other + (r * 128 + token) * 4)) * __shfl_sync(0xffffffffu, f1, r);
+          const uint64_t at = __shfl_sync(0xffffffffu, to, r);
+          if (r >= rows_there || !ok) continue;
           if (whole) {
-            const int i = r / a.G;
-            uint16_t* to = out.p + (int64_t)(x.t.token0 + i) * out.ts + (int64_t)(x.t.h * a.G + r - i * a.G) * out.hs + token;
-            const __nv_bfloat16 v = __float2bfloat16_rn(L == 0.f ? 0.f : y / L);
-            if (ok) *to = *reinterpret_cast<const uint16_t*>(&v);
+            const __nv_bfloat16 v = __float2bfloat16_rn(y);
+            reinterpret_cast<uint16_t*>(at)[token] = *reinterpret_cast<const uint16_t*>(&v);
           } else {
-            float* p = part + r * kPartialStride;
-            if (token == 0) *reinterpret_cast<float4*>(p) = make_float4(top, L, most, 0.f);
-            p[4 + token] = y;
+            reinterpret_cast<float*>(at)[token] = y;
           }
         }
       }
@@ -813,7 +879,7 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
       }
     }
     if (lane == 0) records[cta] = open;
-  } else {
+  } else if (warp < kTailKeys + 2) {
     // ------------------------------ tails ------------------------------
     const int half = warp - kTailKeys;
     uint32_t gone = 0;  // a bit per stage: the parity of its tails so far
