@@ -137,10 +137,9 @@ constexpr int kStages = 5, kTasks = 4, kReaders = 8 + 1 + 1 + 2;  // of a task: 
 constexpr int kStageBytes = 2 * kKv8PageBytes;                    // two pages' keys, then their values
 constexpr int kQueryBytes = 2 * kRowsOfTile * kD;                 // [piece][row][128]
 constexpr int kWeightBytes = 2 * kPart * 128;                     // [token][piece][row], 128 bytes a token
-constexpr uint32_t kColS = 0, kColO = 128;                        // tensor memory: S of both, 64 columns each; O, 128 each
+constexpr uint32_t kColS = 0, kColO = 256;                        // tensor memory: S, two of 64 columns each; O, 128 each
 constexpr float kShift = -5.f;                                    // log2 of a weight at the reference
 constexpr float kFar = 2048.f;                                    // a sum of two exponents is right to 2^-13 below it
-constexpr float kNone = -3e38f;                                   // below all scores, and finite
 constexpr int kUnitCost = 6;                                      // pages that beginning and ending a tile cost
 
 struct Task {
@@ -155,25 +154,30 @@ __device__ __forceinline__ int task_steps(const Task& x) { return ((task_pages(x
 struct StageMeta {  // of a step's two pages
   float kfac[2], vlog[2], vinv[2];
   int pos[2];
-  uint32_t rows[2];
+  uint32_t rows[2], bad[2];  // bad: a row that sees a token of it is NaN (the other numbers are finite all the same)
+};
+struct WarpRows {  // of a softmax warp, a row each: minus the reference's score (without the query's factor), its other part
+  float neg_m[kRowsOfTile], w[kRowsOfTile], f[kRowsOfTile];  // with the page's, and what a raised reference leaves of sums
 };
 
 struct Smem {
   uint64_t full[kStages], empty[kStages], tail_go[kStages];
   uint64_t task_full[kTasks], task_empty[kTasks], q_full[kTasks], q_empty[2];
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t s_full[2][2], p_full[2], pv_done[2];
   Task tasks[kTasks];
   StageMeta meta[kStages];
   float tail_kfac[kStages][kPart], tail_vlog[kStages][kPart], tail_vinv[kStages][kPart];
+  uint8_t tail_bad[kStages][2][kPart];
   alignas(16) float qs[kTasks][kRowsOfTile];
-  // Per softmax group and row: minus the reference's score, kShift - log2 of its values' scale, what a raised one leaves of sums.
-  alignas(16) float neg_m[2][kRowsOfTile], w[2][kRowsOfTile], f[2][kRowsOfTile];
-  float sum[2][kRowsOfTile];
+  alignas(16) WarpRows rows[8];
+  uint32_t wrong[kTasks];          // rows whose query is not finite
+  float m[2][kRowsOfTile], w[2][kRowsOfTile], sum[2][kRowsOfTile];
+  uint32_t poison[2][4], over[2][4];
   int top[2][4][kRowsOfTile];
-  uint32_t over[2][4];
   int64_t scratch[36];
   uint32_t tmem;
   int abort;
+  float minus_zero;
 };
 constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + 2 * kQueryBytes + 2 * kWeightBytes + sizeof(Smem);
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
@@ -250,11 +254,13 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.q_empty[i]), 1);
-      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.s_full[i][0]), 1);
+      mbar_init(smem_u32(&sm.s_full[i][1]), 1);
       mbar_init(smem_u32(&sm.p_full[i]), 4);
       mbar_init(smem_u32(&sm.pv_done[i]), 1);
     }
     sm.abort = 0;
+    *(volatile float*)&sm.minus_zero = -0.f;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // The launch may begin before what is before it on the stream has ended; nothing in memory is touched until then.
@@ -301,11 +307,11 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
     // ------------------------------ softmax, a token a thread ------------------------------
     const int grp = warp >> 2, quad = warp & 3, token = quad * 32 + lane, half = quad >> 1;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t S = lanes + kColS + grp * 64, O = lanes + kColO + grp * 128;
+    const uint32_t S0 = lanes + kColS + grp * 128, O = lanes + kColO + grp * 128;
     const uint32_t weights = sp + grp * kWeightBytes;
-    float* neg_m = sm.neg_m[grp];
-    float* w = sm.w[grp];
-    uint32_t phase = 0;   // of s_full, p_full and pv_done: this group's steps so far
+    WarpRows& my = sm.rows[warp];
+    uint32_t phase = 0;  // this group's steps so far
+    const uint64_t zero2 = twice(*(volatile float*)&sm.minus_zero);
     auto group_any = [&](bool x) {
       int any;
       asm volatile(
@@ -335,240 +341,215 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
       const float* qs = sm.qs[task % kTasks];
       const int steps = task_steps(x), rows_there = x.t.tokens * a.G;
       const bool has_tail = x.to > x.t.listed;
+      const float my_qs = qs[lane];
       uint64_t l[16];  // softmax sums of the thread's own tokens, rows two by two
 #pragma unroll
       for (int i = 0; i < 16; ++i) l[i] = 0;
-      if (quad == 0) {
-        neg_m[lane] = -kNone;
-        w[lane] = kShift;
-      }
-      group_sync();
+      // Lane r of every warp has row r's reference: a score, without the query's factor, and kShift - log2 of its values' scale
+      // (infinite: there is none yet).
+      float M = 0.f, w = INFINITY;
+      uint32_t poison = 0;  // rows that see, here, what makes them NaN
+      my.neg_m[lane] = 0.f;
       int mine = 0;  // steps of this group in the task
       for (int n = grp; n < steps; n += 2, ++mine, ++phase) {
-        const uint32_t at = step + n, stage = stage_of(at);
-        warp_wait(ok, smem_u32(&sm.s_full[grp]), phase & 1, abort, a.err);
+        const uint32_t at = step + n, stage = stage_of(at), S = S0 + (phase & 1) * 64;
+        warp_wait(ok, smem_u32(&sm.s_full[grp][phase & 1]), phase >> 1 & 1, abort, a.err);
         warp_wait(ok, smem_u32(&sm.full[stage]), turn_of(at), abort, a.err);
+        // The group's last products: done, its weights' place is free and its output at rest.
+        auto settled = [&]() {
+          if (mine) warp_wait(ok, smem_u32(&sm.pv_done[grp]), (phase - 1) & 1, abort, a.err);
+          tmem_after();
+        };
         tmem_after();
         const bool tail = has_tail && n == steps - 1;
         const StageMeta& me = sm.meta[stage];
-        float kfac, vlog, vinv;
-        uint32_t allowed;
-        int pos;
-        if (tail) {
-          const int j = token & (kPart - 1);
-          kfac = sm.tail_kfac[stage][j];
-          vlog = sm.tail_vlog[stage][j];
-          vinv = token < kPart ? sm.tail_vinv[stage][j] : 0.f;  // a token counts once
-          pos = x.t.full * kPart + j;
-          allowed = rows_there < 32 ? (1u << rows_there) - 1u : 0xffffffffu;
-        } else {
-          kfac = me.kfac[half];
-          vlog = me.vlog[half];
-          vinv = me.vinv[half];
-          pos = me.pos[half] + (token & (kPart - 1));
-          allowed = me.rows[half];
-        }
+        const int j = token & (kPart - 1);
+        const float kfac = tail ? sm.tail_kfac[stage][j] : me.kfac[half], vlog = tail ? sm.tail_vlog[stage][j] : me.vlog[half];
+        const float vinv = !tail ? me.vinv[half] : token < kPart ? sm.tail_vinv[stage][j] : 0.f;  // a token counts once
+        const int pos = (tail ? x.t.full * kPart : me.pos[half]) + j;
+        const uint32_t rows = !tail ? me.rows[half] : rows_there < 32 ? (1u << rows_there) - 1u : 0xffffffffu;
         const int late = pos - x.t.see0 + 1;  // tokens of the tile that do not see it
-        if (late > 0) allowed = late < x.t.tokens ? allowed & 0xffffffffu << late * a.G : 0u;
+        uint32_t allowed = late <= 0 ? rows : late < x.t.tokens ? rows & 0xffffffffu << late * a.G : 0u;
         if (!ok) allowed = 0;
-        // Scores, rows 16 g .. 16 g + 15, without the row's factor and the page's: two by two.
-        auto scores = [&](int g, uint64_t (&z)[8]) {
-          uint32_t hi[16], lo[16];
-          tmem_load16(S + g * 16, hi);
-          tmem_load16(S + 32 + g * 16, lo);
-          tmem_loaded();
-          settle16(hi);
-          settle16(lo);
-          const uint64_t sixteenth = twice(0.0625f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = fma2(pack2(lo[2 * i], lo[2 * i + 1]), sixteenth, pack2(hi[2 * i], hi[2 * i + 1]));
-        };
-        // The tail's: the other piece's thread has the rest. Its scores stay where the weights go.
-        auto mine_at = [&](int r, int tok) { return weights + (r * 128 + tok) * 4; };
-        if (tail) {
-#pragma unroll
+        if (tail ? (sm.tail_bad[stage][0][j] | sm.tail_bad[stage][1][j]) != 0 : me.bad[half] != 0) poison |= allowed;
+        const bool own = __any_sync(0xffffffffu, tail || late > 0);  // tokens have factors or masks of their own
+        if (tail) {  // both pieces' scores are added, through the weights' place, and put back
+          auto place = [&](int r, int tok) { return weights + (r * 128 + tok) * 4; };
+          settled();
+#pragma unroll 1
           for (int g = 0; g < 2; ++g) {
-            uint64_t z[8];
-            scores(g, z);
+            uint32_t hi[16], lo[16];
+            tmem_load16(S + g * 16, hi);
+            tmem_load16(S + 32 + g * 16, lo);
+            tmem_loaded();
+            settle16(hi);
+            settle16(lo);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float z0, z1;
-              unpack2(z[i], z0, z1);
-              sts32(mine_at(g * 16 + 2 * i, token), __float_as_uint(z0));
-              sts32(mine_at(g * 16 + 2 * i + 1, token), __float_as_uint(z1));
-            }
+            for (int i = 0; i < 16; ++i) sts32(place(g * 16 + i, token), __float_as_uint(fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]))));
           }
           group_sync();
-        }
-        auto tail_scores = [&](int g, uint64_t (&z)[8]) {
-          const int first = token & (kPart - 1);
-          const uint64_t sixteenth = twice(0.0625f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = g * 16 + 2 * i;
-            z[i] = fma2(pack2(lds32(mine_at(r, first + kPart)), lds32(mine_at(r + 1, first + kPart))), sixteenth,
-                        pack2(lds32(mine_at(r, first)), lds32(mine_at(r + 1, first))));
-          }
-        };
-        // Scaled scores, rounded before a reference is taken off. (A packed product and a packed sum become one operation.)
-        auto times = [&](uint64_t x, uint64_t y) {
-          float x0, x1, y0, y1;
-          unpack2(x, x0, x1);
-          unpack2(y, y0, y1);
-          return pack2(__float_as_uint(__fmul_rn(x0, y0)), __float_as_uint(__fmul_rn(x1, y1)));
-        };
-        auto scaled = [&](int g, uint64_t (&z)[8]) {
-          if (tail) tail_scores(g, z);
-          else scores(g, z);
-          const uint64_t k2 = twice(kfac);
-#pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(qs + g * 16 + 2 * i);
-            z[i] = times(z[i], mul2(f.x, k2));
-            z[i + 1] = times(z[i + 1], mul2(f.y, k2));
-          }
-        };
-        float e[32];  // exponents
-        for (bool again = false;; again = true) {
-          float top = -INFINITY;
-          const uint64_t v2 = twice(vlog);
-#pragma unroll
+#pragma unroll 1
           for (int g = 0; g < 2; ++g) {
-            uint64_t z[8];
-            scaled(g, z);
+            uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(neg_m + g * 16 + 2 * i);
-              const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(w + g * 16 + 2 * i);
-              float* y = e + g * 16 + 2 * i;
-              unpack2(add2(add2(z[i], m.x), add2(ww.x, v2)), y[0], y[1]);
-              unpack2(add2(add2(z[i + 1], m.y), add2(ww.y, v2)), y[2], y[3]);
+            for (int i = 0; i < 16; ++i) {
+              hi[i] = __float_as_uint(fmaf(__uint_as_float(lds32(place(g * 16 + i, j + kPart))), 0.0625f, __uint_as_float(lds32(place(g * 16 + i, j)))));
+              lo[i] = 0;
+            }
+            tmem_store16(S + g * 16, hi);
+            tmem_store16(S + 32 + g * 16, lo);
+          }
+          tmem_stored();
+          group_sync();  // before the weights come
+        }
+        // Scores are multiplied by the page's factor and rounded before a reference is taken off: a product and a sum that
+        // follows would be one operation, and the largest score less itself not 0. (zero2 holds them apart.)
+        float e[32];  // exponents: (t - M) * qs + (w + vlog)
+        for (bool again = false;; again = true) {
+          my.w[lane] = rows >> lane & 1 ? w + (tail ? 0.f : vlog) : -INFINITY;
+          __syncwarp();
+          float top = -INFINITY;
+          if (rows == 0) {  // no page: what lies in its place is not looked at
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                y[c] = allowed >> (g * 16 + 2 * i + c) & 1 ? y[c] : -INFINITY;
-                top = fmaxf(top, y[c]);
+            for (int r = 0; r < 32; ++r) e[r] = -INFINITY;
+          } else {
+            const uint64_t sixteenth = twice(0.0625f), k2 = twice(kfac);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              uint32_t hi[16], lo[16];
+              tmem_load16(S + g * 16, hi);
+              tmem_load16(S + 32 + g * 16, lo);
+              tmem_loaded();
+              settle16(hi);
+              settle16(lo);
+#pragma unroll
+              for (int i = 0; i < 8; i += 2) {
+                const ulonglong2 m2 = *reinterpret_cast<const ulonglong2*>(my.neg_m + g * 16 + 2 * i);
+                const ulonglong2 w2 = *reinterpret_cast<const ulonglong2*>(my.w + g * 16 + 2 * i);
+                const ulonglong2 q2 = *reinterpret_cast<const ulonglong2*>(qs + g * 16 + 2 * i);
+                auto exponents = [&](int c, uint64_t m, uint64_t q, uint64_t ww, float* y) {
+                  const uint64_t t = fma2(fma2(pack2(lo[c], lo[c + 1]), sixteenth, pack2(hi[c], hi[c + 1])), k2, zero2);
+                  unpack2(fma2(add2(t, m), q, ww), y[0], y[1]);
+                };
+                exponents(2 * i, m2.x, q2.x, w2.x, e + g * 16 + 2 * i);
+                exponents(2 * i + 2, m2.y, q2.y, w2.y, e + g * 16 + 2 * i + 2);
               }
             }
+            if (own) {
+#pragma unroll
+              for (int r = 0; r < 32; ++r) e[r] = allowed >> r & 1 ? tail ? e[r] + vlog : e[r] : -INFINITY;
+            }
+#pragma unroll
+            for (int r = 0; r < 32; ++r) top = fmaxf(top, e[r]);
           }
           if (!group_any(top > 0.f || !ok) || again) break;
-          if (group_any(!ok)) {
-            ok = false;
-            break;
-          }
-          // A weight has passed 1. In few rows, as a rule, and by little: those take a power of two off.
+          // A weight has passed 1. The rows in which one has, and the largest exponent of each: what is not found in registers (by
+          // an index that is not known before) is read again.
           uint32_t over = 0;
 #pragma unroll
           for (int r = 0; r < 32; ++r) over |= (e[r] > 0.f ? 1u : 0u) << r;
           over = __reduce_or_sync(0xffffffffu, over);
-          if (lane == 0) sm.over[grp][quad] = over;
-          group_sync();
-          over = sm.over[grp][0] | sm.over[grp][1] | sm.over[grp][2] | sm.over[grp][3];
-#pragma unroll
-          for (int r = 0; r < 32; ++r)
-            if (over >> r & 1) {
-              const int most = __reduce_max_sync(0xffffffffu, order_of(e[r]));
+          auto product = [&](int r) {  // t of row r
+            uint32_t hi, lo;
+            tmem_load1(S + r, hi);
+            tmem_load1(S + 32 + r, lo);
+            tmem_loaded();
+            asm volatile("" : "+r"(hi), "+r"(lo));
+            return __fmul_rn(fmaf(__uint_as_float(lo), 0.0625f, __uint_as_float(hi)), kfac);
+          };
+          auto largest = [&](uint32_t which, auto of) {  // over the warp's tokens
+#pragma unroll 2
+            for (uint32_t left = which; left; left &= left - 1) {
+              const int r = __ffs(left) - 1;
+              const float y = of(product(r), r);
+              const int most = __reduce_max_sync(0xffffffffu, order_of(allowed >> r & 1 ? y : -INFINITY));
               if (lane == 0) sm.top[grp][quad][r] = most;
             }
-          group_sync();
-          float* f = sm.f[grp];
-          auto largest_row = [&]() {
-            const int (*t)[kRowsOfTile] = sm.top[grp];
-            return float_of(max(max(t[0][lane], t[1][lane]), max(t[2][lane], t[3][lane])));
           };
-          // The products' sums so far of row r's group of 8.
-          auto rescale = [&](int c) {
-            uint32_t y[8];
-            tmem_load8(O + c, y);
-            tmem_loaded();
-            settle8(y);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float g = f[(c & 31) + k];
-              y[k] = __float_as_uint(g == 1.f ? __uint_as_float(y[k]) : __uint_as_float(y[k]) * g);
-            }
-            tmem_store8(O + c, y);
-          };
-          const bool raised = over >> lane & 1;
-          const float passed = raised ? largest_row() : 0.f;
-          group_sync();
-          if (!__any_sync(0xffffffffu, !(passed < 64.f))) {
-            const float d = raised ? ceilf(passed) - kShift : 0.f;
-            if (quad == 0) {
-              f[lane] = pow2(-(int)d);
-              w[lane] -= d;
-            }
-            group_sync();
-#pragma unroll
-            for (int r = 0; r < 32; ++r)
-              if (over >> r & 1) e[r] -= __shfl_sync(0xffffffffu, d, r);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (over >> (2 * i) & 3) l[i] = mul2(l[i], *reinterpret_cast<const uint64_t*>(f + 2 * i));
-            if (mine > 0) {  // (its last products are done: this step's were issued after them)
-#pragma unroll 1
-              for (int c = 0; c < 96; c += 8)
-                if (over >> (c & 31) & 0xffu) rescale(c);
-              tmem_stored();
-            }
-            group_sync();  // f has been read
+          largest(over, [&](float t, int r) { return fmaf(t + my.neg_m[r], qs[r], my.w[r] + (tail ? vlog : 0.f)); });
+          if (lane == 0) sm.over[grp][quad] = over;
+          settled();
+          if (group_any(!ok)) {
+            ok = false;
             break;
           }
-          // The first step, or a score far above all others: the reference goes to the largest weight of the step. Where scores are
-          // so large that adding the values' scale would lose it, first to its score and then, with differences of scores,
-          // to its values' scale.
-          auto largest = [&](auto of) {
+          float passed = 0.f, factor = 1.f;
+          over = 0;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              uint64_t z[8];
-              scaled(g, z);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t o = sm.over[grp][k];
+            over |= o;
+            if (o >> lane & 1) passed = fmaxf(passed, float_of(sm.top[grp][k][lane]));
+          }
+          if (__all_sync(0xffffffffu, passed < 64.f)) {  // by little: those rows take a power of two off
+            const float d = over >> lane & 1 ? ceilf(passed) - kShift : 0.f;
+            factor = pow2(-(int)d);
+            w -= d;
+          } else {
+            // The first step, or a score far above all others: the reference goes to the largest weight of the step. Where scores
+            // are so large that adding the values' scale would lose it, first to its score and then, with differences of
+            // scores, to its values' scale.
+            auto of_group = [&](auto of) {  // of row `lane`
+              group_sync();
+              largest(rows, of);
+              for (uint32_t left = ~rows; left; left &= left - 1)
+                if (lane == 0) sm.top[grp][quad][__ffs(left) - 1] = order_of(-INFINITY);
+              group_sync();
+              const int (*t)[kRowsOfTile] = sm.top[grp];
+              return float_of(max(max(t[0][lane], t[1][lane]), max(t[2][lane], t[3][lane])));
+            };
+            float score = of_group([&](float t, int r) { return fmaf(t, qs[r], vlog); }), values = 0.f;
+            const bool none = score == -INFINITY;
+            if (__any_sync(0xffffffffu, !none && !(fabsf(score) < kFar))) {
+              score = of_group([&](float t, int) { return t; });
+              my.neg_m[lane] = -score;
+              __syncwarp();
+              values = of_group([&](float t, int r) { return fmaf(t + my.neg_m[r], qs[r], vlog); });
+            } else {
+              score /= my_qs;  // a power of two
+            }
+            const bool raise = !none && !(fmaf(score - M, my_qs, values + w) <= 0.f);
+            if (raise) {
+              factor = w == INFINITY ? 0.f : ex2(fmaf(M - score, my_qs, kShift - values - w));
+              M = score;
+              w = kShift - values;
+            }
+            my.neg_m[lane] = -M;
+            over = __ballot_sync(0xffffffffu, raise);
+          }
+          my.f[lane] = factor;
+          __syncwarp();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float z0, z1;
-                unpack2(z[i >> 1], z0, z1);
-                const int r = g * 16 + i;
-                const float y = of(i & 1 ? z1 : z0, r);
-                const int most = __reduce_max_sync(0xffffffffu, order_of(allowed >> r & 1 ? y : -INFINITY));
-                if (lane == 0) sm.top[grp][quad][r] = most;
+          for (int i = 0; i < 16; i += 2) {
+            const ulonglong2 f2 = *reinterpret_cast<const ulonglong2*>(my.f + 2 * i);
+            l[i] = mul2(l[i], f2.x);
+            l[i + 1] = mul2(l[i + 1], f2.y);
+          }
+          if (mine) {
+#pragma unroll 1
+            for (uint32_t left = over; left; left &= left - 1) {
+              const int r = __ffs(left) - 1;
+              const float f = my.f[r];
+              uint32_t y[3];
+#pragma unroll
+              for (int k = 0; k < 3; ++k) tmem_load1(O + k * 32 + r, y[k]);
+              tmem_loaded();
+#pragma unroll
+              for (int k = 0; k < 3; ++k) {
+                asm volatile("" : "+r"(y[k]));
+                tmem_store1(O + k * 32 + r, __float_as_uint(__uint_as_float(y[k]) * f));
               }
             }
-            group_sync();
-            const float y = largest_row();
-            group_sync();
-            return y;  // of row `lane`
-          };
-          float score = largest([&](float z, int) { return z + vlog; }), values = 0.f;
-          if (__any_sync(0xffffffffu, score != -INFINITY && !(fabsf(score) < kFar))) {
-            score = largest([&](float z, int) { return z; });
-            if (quad == 0) f[lane] = score;
-            group_sync();
-            values = largest([&](float z, int r) { return (z - f[r]) + vlog; });
-          }
-          const float before = -neg_m[lane];
-          const float old = w[lane];
-          const bool raise = score != -INFINITY && !((score - before) + (values + old) <= 0.f);
-          const float now = kShift - values, factor = raise ? ex2((before - score) + (now - old)) : 1.f;
-          group_sync();
-          if (quad == 0) {
-            f[lane] = factor;
-            if (raise) neg_m[lane] = -score, w[lane] = now;
-          }
-          group_sync();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) l[i] = mul2(l[i], *reinterpret_cast<const uint64_t*>(f + 2 * i));
-          if (mine > 0) {
-#pragma unroll 1
-            for (int c = 0; c < 96; c += 8) rescale(c);
             tmem_stored();
           }
         }
         if (!ok) continue;
-        if (tail) group_sync();  // the scores have been read
         const uint64_t u2 = twice(vinv);
         const __half2 sixteen = __float2half2_rn(16.f), part = __float2half2_rn(tail && token >= kPart ? 0.0625f : 1.f);
         const uint32_t row = weights + token * 128;
+        uint32_t piece[2][3][4];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          uint32_t piece[3][4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // four rows
             uint32_t h[2];
@@ -585,7 +566,7 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
             }
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
-              piece[k][i] = __byte_perm(h[0] << 1, h[1] << 1, 0x7531);
+              piece[g][k][i] = __byte_perm(h[0] << 1, h[1] << 1, 0x7531);
               if (k == 2) break;
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
@@ -595,10 +576,14 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
               }
             }
           }
+        }
+        settled();
+        if (!ok) continue;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
 #pragma unroll
           for (int k = 0; k < 3; ++k)
-            sts128(row + (((2 * k + g) ^ (token & 7)) << 4), piece[k][0], piece[k][1], piece[k][2], piece[k][3]);
-        }
+            sts128(row + (((2 * k + g) ^ (token & 7)) << 4), piece[g][k][0], piece[g][k][1], piece[g][k][2], piece[g][k][3]);
         proxy_fence();
         tmem_before();
         __syncwarp();
@@ -626,15 +611,17 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         if (part == 0) sm.sum[grp][r] = sum;
       }
-      group_sync();
-      uint32_t o[32];
-#pragma unroll
-      for (int r = 0; r < 32; ++r) o[r] = 0;
-      if (mine && ok) {
-        const uint64_t sixteenth = twice(0.0625f);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t p0[16], p1[16], p2[16];
+      poison = __reduce_or_sync(0xffffffffu, poison);
+      if (lane == 0) sm.poison[grp][quad] = poison;
+      if (quad == 0) {
+        sm.m[grp][lane] = w == INFINITY ? -INFINITY : M * my_qs;
+        sm.w[grp][lane] = w;
+      }
+      group_sync();  // the sums have been read
+#pragma unroll 1
+      for (int g = 0; g < 2; ++g) {
+        uint32_t p0[16], p1[16], p2[16];
+        if (mine && ok) {
           tmem_load16(O + g * 16, p0);
           tmem_load16(O + 32 + g * 16, p1);
           tmem_load16(O + 64 + g * 16, p2);
@@ -642,29 +629,26 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
           settle16(p0);
           settle16(p1);
           settle16(p2);
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const uint64_t y = fma2(fma2(pack2(p2[i], p2[i + 1]), sixteenth, pack2(p1[i], p1[i + 1])), sixteenth, pack2(p0[i], p0[i + 1]));
-            float y0, y1;
-            unpack2(y, y0, y1);
-            o[g * 16 + i] = __float_as_uint(y0);
-            o[g * 16 + i + 1] = __float_as_uint(y1);
-          }
         }
-      }
-      if (grp == 1) {
 #pragma unroll
-        for (int r = 0; r < 32; ++r) sts32(weights + (r * 128 + token) * 4, o[r]);
+        for (int i = 0; i < 16; ++i) {
+          const float y = fmaf(fmaf(__uint_as_float(p2[i]), 0.0625f, __uint_as_float(p1[i])), 0.0625f, __uint_as_float(p0[i]));
+          sts32(weights + ((g * 16 + i) * 128 + token) * 4, mine && ok ? __float_as_uint(y) : 0u);
+        }
       }
       both_sync();
       if (grp == 0) {
         const bool whole = x.from == 0 && x.to == x.t.items;
-        const uint32_t other = sp + kWeightBytes;
         // Lane r has row r's factors and place. 2^(M - w) is the unit of a group's numbers: differences of scores first.
-        const float m0 = -sm.neg_m[0][lane], m1 = -sm.neg_m[1][lane], top = fmaxf(m0, m1);
-        const float e0 = (m0 - top) - sm.w[0][lane], e1 = (m1 - top) - sm.w[1][lane], most = fmaxf(e0, e1);
+        const float m0 = sm.m[0][lane], m1 = sm.m[1][lane], top = fmaxf(m0, m1), at = top == -INFINITY ? 0.f : top;
+        const float e0 = m0 == -INFINITY ? m0 : (m0 - at) - sm.w[0][lane], e1 = m1 == -INFINITY ? m1 : (m1 - at) - sm.w[1][lane];
+        const float most = top == -INFINITY ? 0.f : fmaxf(e0, e1);
         float f0 = ex2(e0 - most), f1 = ex2(e1 - most);
-        const float L = sm.sum[0][lane] * f0 + sm.sum[1][lane] * f1;
+        float L = sm.sum[0][lane] * f0 + sm.sum[1][lane] * f1;
+        uint32_t bad = L != 0.f ? sm.wrong[task % kTasks] : 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) bad |= sm.poison[0][k] | sm.poison[1][k];
+        if (bad >> lane & 1) L = __uint_as_float(0x7fc00000u);
         const float unit = whole ? L == 0.f ? 0.f : 0x1p-8f / L : 0x1p-8f;  // (codes are 256 times their fp16 number)
         f0 *= unit;
         f1 *= unit;
@@ -677,17 +661,18 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
           if (quad == 0 && lane < rows_there) *reinterpret_cast<float4*>(p) = make_float4(top, L, most, 0.f);
           to = reinterpret_cast<uint64_t>(p + 4);
         }
-#pragma unroll
-        for (int r = 0; r < 32; ++r) {
-          const float y = __uint_as_float(o[r]) * __shfl_sync(0xffffffffu, f0, r) +
-                          __uint_as_float(lds32(other + (r * 128 + token) * 4)) * __shfl_sync(0xffffffffu, f1, r);
-          const uint64_t at = __shfl_sync(0xffffffffu, to, r);
-          if (r >= rows_there || !ok) continue;
+#pragma unroll 4
+        for (int r = 0; r < rows_there; ++r) {
+          const uint32_t at = weights + (r * 128 + token) * 4;
+          const float y = __uint_as_float(lds32(at)) * __shfl_sync(0xffffffffu, f0, r) +
+                          __uint_as_float(lds32(at + kWeightBytes)) * __shfl_sync(0xffffffffu, f1, r);
+          const uint64_t place = __shfl_sync(0xffffffffu, to, r);
+          if (!ok) continue;
           if (whole) {
             const __nv_bfloat16 v = __float2bfloat16_rn(y);
-            reinterpret_cast<uint16_t*>(at)[token] = *reinterpret_cast<const uint16_t*>(&v);
+            reinterpret_cast<uint16_t*>(place)[token] = *reinterpret_cast<const uint16_t*>(&v);
           } else {
-            reinterpret_cast<float*>(at)[token] = y;
+            reinterpret_cast<float*>(place)[token] = y;
           }
         }
       }
@@ -728,7 +713,8 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
           const int c = lane - i;
           if (c == 0 || c == 1) {
             const bool there = lane < n, bad = there && (my_sc.x != my_sc.x || my_sc.y != my_sc.y);
-            me.kfac[c] = !there ? 0.f : bad ? __uint_as_float(0x7fc00000u) : my_sc.x * scale * kLog2e;
+            me.kfac[c] = !there || bad ? 0.f : my_sc.x * scale * kLog2e;
+            me.bad[c] = bad;
             me.vlog[c] = !there || bad ? 0.f : scale_log2(my_sc.y);
             me.vinv[c] = !there || bad ? 1.f : 1.f / my_sc.y;
             me.pos[c] = there ? my.pos : 0;
@@ -763,15 +749,16 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
     // ------------------------------ products ------------------------------
     const uint32_t leader = elect();
     const uint64_t dring = operand(ring, 16, 1024), dq = operand(sq, 16, 1024), dp = operand(sp, 16, 1024);
-    uint32_t p_phase[2] = {0, 0}, last[2] = {0, 0};
+    uint32_t outs[2] = {0, 0}, ins[2] = {0, 0};  // steps of each group so far, by their outputs and by their scores
     while (next()) {
       const Task x = sm.tasks[task % kTasks];
       const int pages = task_pages(x), steps = task_steps(x);
       warp_wait(ok, smem_u32(&sm.q_full[task % kTasks]), task / kTasks & 1, abort, a.err);
-      for (int n = -2; n < steps; ++n) {
-        if (n >= 0) {  // the weights of step n are there: its output, and the scores' place is free
+      // Scores are made three steps ahead: a group's next ones are there when it comes to them.
+      for (int n = -3; n < steps; ++n) {
+        if (n >= 0) {  // the weights of step n are there, and the place of its scores is free
           const uint32_t g = n & 1, stage = stage_of(step + n);
-          warp_wait(ok, smem_u32(&sm.p_full[g]), p_phase[g]++ & 1, abort, a.err);
+          warp_wait(ok, smem_u32(&sm.p_full[g]), outs[g]++ & 1, abort, a.err);
           tmem_after();
           if (!ok) break;
           const uint64_t v = dring + ((stage * kStageBytes + kKv8PageBytes) >> 4), p = dp + (g * kWeightBytes >> 4);
@@ -785,18 +772,18 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
           }
           mma_commit(leader, smem_u32(&sm.empty[stage]));
           mma_commit(leader, smem_u32(&sm.pv_done[g]));
-          last[g] = 1;
         }
-        if (n + 2 < steps) {
-          const uint32_t g = n & 1, at = step + n + 2, stage = stage_of(at);
+        if (n + 3 < steps) {
+          const uint32_t at = step + n + 3, stage = stage_of(at), g = (n + 3) & 1, buffer = ins[g]++ & 1;
           warp_wait(ok, smem_u32(&sm.full[stage]), turn_of(at), abort, a.err);
           tmem_after();
           if (!ok) break;
           const uint64_t k = dring + (stage * kStageBytes >> 4), b = dq + ((task & 1) * kQueryBytes >> 4);
+          const uint32_t d = tmem + kColS + g * 128 + buffer * 64;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) mma_f8(leader, tmem + kColS + g * 64, k + 2 * c, b + 2 * c, shape(64, false), c > 0);
-          mma_commit(leader, smem_u32(&sm.s_full[g]));
-          if (n + 3 == steps) mma_commit(leader, smem_u32(&sm.q_empty[task & 1]));
+          for (int c = 0; c < 4; ++c) mma_f8(leader, d, k + 2 * c, b + 2 * c, shape(64, false), c > 0);
+          mma_commit(leader, smem_u32(&sm.s_full[g][buffer]));
+          if (n + 4 == steps) mma_commit(leader, smem_u32(&sm.q_empty[task & 1]));
         }
       }
       step += steps;
@@ -805,7 +792,7 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
     // The last arrivals have landed before the CTA's shared memory goes.
 #pragma unroll
     for (int g = 0; g < 2; ++g)
-      if (last[g]) warp_wait(ok, smem_u32(&sm.pv_done[g]), (p_phase[g] - 1) & 1, abort, a.err);
+      if (outs[g]) warp_wait(ok, smem_u32(&sm.pv_done[g]), (outs[g] - 1) & 1, abort, a.err);
   } else if (warp == kPlanner) {
     // ------------------------------ plan, and query operands ------------------------------
     JoinRecord open = JoinRecord{};
@@ -841,20 +828,26 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
       if (!ok) break;
       const int rows = more ? x.t.tokens * a.G : 0;
       const uint32_t to = sq + (task & 1) * kQueryBytes;
+      uint32_t wrong = 0;
 #pragma unroll 1
-      for (int r0 = 0; more && r0 < kRowsOfTile; r0 += 8) {
-        uint2 v[8];
+      for (int r0 = 0; more && r0 < kRowsOfTile; r0 += 4) {
+        uint2 v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const int r = r0 + i, y = r / a.G;
           v[i] = make_uint2(0, 0);
           if (r < rows)
             v[i] = *reinterpret_cast<const uint2*>(q.p + (int64_t)(x.t.token0 + y) * q.ts + (int64_t)(x.t.h * a.G + r - y * a.G) * q.hs + lane * 4);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const int r = r0 + i;
-          const uint32_t top = largest_of(v[i]);
+          uint32_t top = largest_of(v[i]);
+          if (top >= 0x7f80u) {  // not finite: the row is NaN if it sees anything
+            wrong |= 1u << r;
+            v[i] = make_uint2(0, 0);
+            top = 0x3f80u;
+          }
           const int e = half_exponent(top);
           const float f = pow2(8 - e);
           const float y[4] = {lo_f(v[i].x) * f, hi_f(v[i].x) * f, lo_f(v[i].y) * f, hi_f(v[i].y) * f};
@@ -863,9 +856,10 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
           const uint32_t place = to + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
           sts32(place, high);
           sts32(place + kRowsOfTile * 128, low);
-          if (lane == 0) sm.qs[slot][r] = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e - 8);
+          if (lane == 0) sm.qs[slot][r] = pow2(e - 8);
         }
       }
+      if (lane == 0) sm.wrong[slot] = wrong;
       proxy_fence();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[slot]));
@@ -896,12 +890,12 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
       const uint32_t to = ring + stage * kStageBytes + half * kKv8PageBytes;
       const uint16_t* src = a.tails + ((int64_t)x.t.b * a.Hkv + x.t.h) * kPageElems + half * kPart * kD + lane * 4;
 #pragma unroll 1
-      for (int r0 = 0; r0 < kPart; r0 += 8) {
-        uint2 v[8];
+      for (int r0 = 0; r0 < kPart; r0 += 4) {
+        uint2 v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = r0 + i < x.t.tail ? *reinterpret_cast<const uint2*>(src + (r0 + i) * kD) : make_uint2(0, 0);
+        for (int i = 0; i < 4; ++i) v[i] = r0 + i < x.t.tail ? *reinterpret_cast<const uint2*>(src + (r0 + i) * kD) : make_uint2(0, 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const int r = r0 + i;
           bool wrong = false;
 #pragma unroll
@@ -922,11 +916,11 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
           sts32(place, high);
           sts32(place + kKv8HalfBytes, low);
           if (lane == 0) {
-            const float nan = __uint_as_float(0x7fc00000u);
+            sm.tail_bad[stage][half][r] = wrong;
             if (half == 0) {
-              sm.tail_kfac[stage][r] = wrong ? nan : scale * kLog2e * pow2(e - 8);
+              sm.tail_kfac[stage][r] = scale * kLog2e * pow2(e - 8);
             } else {
-              sm.tail_vlog[stage][r] = wrong ? nan : (float)(e - 8);
+              sm.tail_vlog[stage][r] = (float)(e - 8);
               sm.tail_vinv[stage][r] = f;
             }
           }

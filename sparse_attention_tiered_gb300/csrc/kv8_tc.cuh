@@ -60,6 +60,14 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* r) {
 
 __device__ __forceinline__ void settle16(uint32_t* r) { asm volatile("" : SPIN_R8(r, 0), SPIN_R8(r, 8)); }
 
+// One column of the warp's lanes. The value is there after tmem_loaded().
+__device__ __forceinline__ void tmem_load1(uint32_t addr, uint32_t& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_store1(uint32_t addr, uint32_t r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%1], {%0};" ::"r"(r), "r"(addr) : "memory");
+}
+
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::SPIN_I8(r, 0),
