@@ -151,10 +151,11 @@ struct Task {
 __device__ __forceinline__ int task_pages(const Task& x) { return max(0, min(x.to, x.t.listed) - x.from); }
 __device__ __forceinline__ int task_steps(const Task& x) { return ((task_pages(x) + 1) >> 1) + (x.to > x.t.listed ? 1 : 0); }
 
-struct StageMeta {  // of a step's two pages
-  float kfac[2], vlog[2], vinv[2];
-  int pos[2];
-  uint32_t rows[2], bad[2];  // bad: a row that sees a token of it is NaN (the other numbers are finite all the same)
+struct alignas(16) PageMeta {  // of a page of a step
+  float kfac, vlog, vinv;
+  int pos;
+  uint32_t rows, bad;  // bad: a row that sees a token of it is NaN (the other numbers are finite all the same)
+  uint32_t reserved[2];
 };
 struct WarpRows {  // of a softmax warp, a row each: minus the reference's score (without the query's factor), its other part
   float neg_m[kRowsOfTile], w[kRowsOfTile], f[kRowsOfTile];  // with the page's, and what a raised reference leaves of sums
@@ -165,15 +166,15 @@ struct Smem {
   uint64_t task_full[kTasks], task_empty[kTasks], q_full[kTasks], q_empty[2];
   uint64_t s_full[2][2], p_full[2], pv_done[2];
   Task tasks[kTasks];
-  StageMeta meta[kStages];
+  PageMeta meta[kStages][2];
   float tail_kfac[kStages][kPart], tail_vlog[kStages][kPart], tail_vinv[kStages][kPart];
   uint8_t tail_bad[kStages][2][kPart];
   alignas(16) float qs[kTasks][kRowsOfTile];
   alignas(16) WarpRows rows[8];
   uint32_t wrong[kTasks];          // rows whose query is not finite
   float m[2][kRowsOfTile], w[2][kRowsOfTile], sum[2][kRowsOfTile];
-  uint32_t poison[2][4], over[2][4];
-  int top[2][4][kRowsOfTile];
+  uint32_t poison[2][4];
+  int top[2][kRowsOfTile];
   int64_t scratch[36];
   uint32_t tmem;
   int abort;
@@ -345,16 +346,22 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
       uint64_t l[16];  // softmax sums of the thread's own tokens, rows two by two
 #pragma unroll
       for (int i = 0; i < 16; ++i) l[i] = 0;
-      // Lane r of every warp has row r's reference: a score, without the query's factor, and kShift - log2 of its values' scale
-      // (infinite: there is none yet).
-      float M = 0.f, w = INFINITY;
+      // Lane r of every warp has row r's reference: a score, without the query's factor, and kShift - log2 of its values' scale.
+      float M = 0.f, w = 0.f;
+      uint32_t seen = 0;    // rows that have one. Before that exponents are scores, with the values' scale
       uint32_t poison = 0;  // rows that see, here, what makes them NaN
       my.neg_m[lane] = 0.f;
       int mine = 0;  // steps of this group in the task
       for (int n = grp; n < steps; n += 2, ++mine, ++phase) {
         const uint32_t at = step + n, stage = stage_of(at), S = S0 + (phase & 1) * 64;
-        warp_wait(ok, smem_u32(&sm.s_full[grp][phase & 1]), phase >> 1 & 1, abort, a.err);
-        warp_wait(ok, smem_u32(&sm.full[stage]), turn_of(at), abort, a.err);
+        {  // (both tries are on their way at once)
+          const uint32_t bars[2] = {smem_u32(&sm.s_full[grp][phase & 1]), smem_u32(&sm.full[stage])};
+          const bool there = mbar_try(bars[0], phase >> 1 & 1) & mbar_try(bars[1], turn_of(at));
+          if (!__all_sync(0xffffffffu, there && ok)) {
+            warp_wait(ok, bars[0], phase >> 1 & 1, abort, a.err);
+            warp_wait(ok, bars[1], turn_of(at), abort, a.err);
+          }
+        }
         // The group's last products: done, its weights' place is free and its output at rest.
         auto settled = [&]() {
           if (mine) warp_wait(ok, smem_u32(&sm.pv_done[grp]), (phase - 1) & 1, abort, a.err);
@@ -362,16 +369,23 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
         };
         tmem_after();
         const bool tail = has_tail && n == steps - 1;
-        const StageMeta& me = sm.meta[stage];
         const int j = token & (kPart - 1);
-        const float kfac = tail ? sm.tail_kfac[stage][j] : me.kfac[half], vlog = tail ? sm.tail_vlog[stage][j] : me.vlog[half];
-        const float vinv = !tail ? me.vinv[half] : token < kPart ? sm.tail_vinv[stage][j] : 0.f;  // a token counts once
-        const int pos = (tail ? x.t.full * kPart : me.pos[half]) + j;
-        const uint32_t rows = !tail ? me.rows[half] : rows_there < 32 ? (1u << rows_there) - 1u : 0xffffffffu;
+        PageMeta me = sm.meta[stage][half];
+        if (tail) {
+          me.kfac = sm.tail_kfac[stage][j];
+          me.vlog = sm.tail_vlog[stage][j];
+          me.vinv = token < kPart ? sm.tail_vinv[stage][j] : 0.f;  // a token counts once
+          me.pos = x.t.full * kPart;
+          me.rows = rows_there < 32 ? (1u << rows_there) - 1u : 0xffffffffu;
+          me.bad = sm.tail_bad[stage][0][j] | sm.tail_bad[stage][1][j];
+        }
+        const float kfac = me.kfac, vlog = me.vlog;
+        const uint32_t rows = me.rows;
+        const int pos = me.pos + j;
         const int late = pos - x.t.see0 + 1;  // tokens of the tile that do not see it
         uint32_t allowed = late <= 0 ? rows : late < x.t.tokens ? rows & 0xffffffffu << late * a.G : 0u;
         if (!ok) allowed = 0;
-        if (tail ? (sm.tail_bad[stage][0][j] | sm.tail_bad[stage][1][j]) != 0 : me.bad[half] != 0) poison |= allowed;
+        if (me.bad) poison |= allowed;
         const bool own = __any_sync(0xffffffffu, tail || late > 0);  // tokens have factors or masks of their own
         if (tail) {  // both pieces' scores are added, through the weights' place, and put back
           auto place = [&](int r, int tok) { return weights + (r * 128 + tok) * 4; };
@@ -442,80 +456,80 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
 #pragma unroll
             for (int r = 0; r < 32; ++r) top = fmaxf(top, e[r]);
           }
-          if (!group_any(top > 0.f || !ok) || again) break;
-          // A weight has passed 1. The rows in which one has, and the largest exponent of each: what is not found in registers (by
-          // an index that is not known before) is read again.
-          uint32_t over = 0;
-#pragma unroll
-          for (int r = 0; r < 32; ++r) over |= (e[r] > 0.f ? 1u : 0u) << r;
-          over = __reduce_or_sync(0xffffffffu, over);
-          auto product = [&](int r) {  // t of row r
-            uint32_t hi, lo;
-            tmem_load1(S + r, hi);
-            tmem_load1(S + 32 + r, lo);
-            tmem_loaded();
-            asm volatile("" : "+r"(hi), "+r"(lo));
-            return __fmul_rn(fmaf(__uint_as_float(lo), 0.0625f, __uint_as_float(hi)), kfac);
-          };
-          auto largest = [&](uint32_t which, auto of) {  // over the warp's tokens
-#pragma unroll 2
-            for (uint32_t left = which; left; left &= left - 1) {
-              const int r = __ffs(left) - 1;
-              const float y = of(product(r), r);
-              const int most = __reduce_max_sync(0xffffffffu, order_of(allowed >> r & 1 ? y : -INFINITY));
-              if (lane == 0) sm.top[grp][quad][r] = most;
-            }
-          };
-          largest(over, [&](float t, int r) { return fmaf(t + my.neg_m[r], qs[r], my.w[r] + (tail ? vlog : 0.f)); });
-          if (lane == 0) sm.over[grp][quad] = over;
+          if (again) break;
+          const bool news = top > 0.f || (rows & ~seen);
+          if (!group_any(news || !ok)) break;
+          // A weight has passed 1, or a row has no reference: the rows, and the largest exponent of each. As a rule few threads
+          // have one to tell.
+          int* most = sm.top[grp];
+          if (quad == 0) most[lane] = order_of(-INFINITY);
           settled();
           if (group_any(!ok)) {
             ok = false;
             break;
           }
-          float passed = 0.f, factor = 1.f;
-          over = 0;
+          if (__any_sync(0xffffffffu, rows & ~seen)) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t o = sm.over[grp][k];
-            over |= o;
-            if (o >> lane & 1) passed = fmaxf(passed, float_of(sm.top[grp][k][lane]));
-          }
-          if (__all_sync(0xffffffffu, passed < 64.f)) {  // by little: those rows take a power of two off
-            const float d = over >> lane & 1 ? ceilf(passed) - kShift : 0.f;
-            factor = pow2(-(int)d);
-            w -= d;
-          } else {
-            // The first step, or a score far above all others: the reference goes to the largest weight of the step. Where scores
-            // are so large that adding the values' scale would lose it, first to its score and then, with differences of
-            // scores, to its values' scale.
-            auto of_group = [&](auto of) {  // of row `lane`
-              group_sync();
-              largest(rows, of);
-              for (uint32_t left = ~rows; left; left &= left - 1)
-                if (lane == 0) sm.top[grp][quad][__ffs(left) - 1] = order_of(-INFINITY);
-              group_sync();
-              const int (*t)[kRowsOfTile] = sm.top[grp];
-              return float_of(max(max(t[0][lane], t[1][lane]), max(t[2][lane], t[3][lane])));
-            };
-            float score = of_group([&](float t, int r) { return fmaf(t, qs[r], vlog); }), values = 0.f;
-            const bool none = score == -INFINITY;
-            if (__any_sync(0xffffffffu, !none && !(fabsf(score) < kFar))) {
-              score = of_group([&](float t, int) { return t; });
-              my.neg_m[lane] = -score;
-              __syncwarp();
-              values = of_group([&](float t, int r) { return fmaf(t + my.neg_m[r], qs[r], vlog); });
-            } else {
-              score /= my_qs;  // a power of two
+            for (int r = 0; r < 32; ++r) {
+              const int y = __reduce_max_sync(0xffffffffu, order_of(e[r]));
+              if (lane == r) atomicMax(most + r, y);
             }
-            const bool raise = !none && !(fmaf(score - M, my_qs, values + w) <= 0.f);
+          } else if (top > 0.f) {
+#pragma unroll
+            for (int r = 0; r < 32; ++r)
+              if (e[r] > 0.f) atomicMax(most + r, __float_as_int(e[r]));
+          }
+          group_sync();
+          float passed = float_of(most[lane]), factor = 1.f;
+          if (seen >> lane & 1 && !(passed > 0.f)) passed = -INFINITY;
+          uint32_t over = __ballot_sync(0xffffffffu, passed != -INFINITY);
+          const bool fresh = !(seen >> lane & 1), there = passed != -INFINITY;
+          if (__all_sync(0xffffffffu, !there || (fresh ? fabsf(passed) < kFar : passed < 64.f))) {
+            if (there && fresh) {
+              M = passed / my_qs;  // a power of two
+              w = kShift;
+              factor = 0.f;
+              my.neg_m[lane] = -M;
+            } else if (there) {  // by little: the row takes a power of two off
+              const float d = ceilf(passed) - kShift;
+              factor = pow2(-(int)d);
+              w -= d;
+            }
+            seen |= over;
+          } else {
+            // A score far from 0, or far above all others: the reference goes to the step's largest score and then, with
+            // differences of scores, to the largest values' scale: their sum would lose it.
+            auto of_group = [&](auto of) {  // of row `lane`; rows that are not known before are read again
+              group_sync();
+              if (quad == 0) most[lane] = order_of(-INFINITY);
+              group_sync();
+#pragma unroll 1
+              for (int r = 0; r < 32; ++r) {
+                uint32_t hi, lo;
+                tmem_load1(S + r, hi);
+                tmem_load1(S + 32 + r, lo);
+                tmem_loaded();
+                asm volatile("" : "+r"(hi), "+r"(lo));
+                const float y = of(__fmul_rn(fmaf(__uint_as_float(lo), 0.0625f, __uint_as_float(hi)), kfac), r);
+                const int top = __reduce_max_sync(0xffffffffu, order_of(allowed >> r & 1 ? y : -INFINITY));
+                if (lane == 0) atomicMax(most + r, top);
+              }
+              group_sync();
+              return float_of(most[lane]);
+            };
+            const float score = of_group([&](float t, int) { return t; });
+            my.neg_m[lane] = -score;
+            __syncwarp();
+            const float values = of_group([&](float t, int r) { return fmaf(t + my.neg_m[r], qs[r], vlog); });
+            const bool raise = score != -INFINITY && (fresh || !(fmaf(score - M, my_qs, values + w) <= 0.f));
             if (raise) {
-              factor = w == INFINITY ? 0.f : ex2(fmaf(M - score, my_qs, kShift - values - w));
+              factor = fresh ? 0.f : ex2(fmaf(M - score, my_qs, kShift - values - w));
               M = score;
               w = kShift - values;
             }
             my.neg_m[lane] = -M;
             over = __ballot_sync(0xffffffffu, raise);
+            seen |= over;
           }
           my.f[lane] = factor;
           __syncwarp();
@@ -544,7 +558,7 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
           }
         }
         if (!ok) continue;
-        const uint64_t u2 = twice(vinv);
+        const uint64_t u2 = twice(me.vinv);
         const __half2 sixteen = __float2half2_rn(16.f), part = __float2half2_rn(tail && token >= kPart ? 0.0625f : 1.f);
         const uint32_t row = weights + token * 128;
         uint32_t piece[2][3][4];
@@ -614,7 +628,7 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
       poison = __reduce_or_sync(0xffffffffu, poison);
       if (lane == 0) sm.poison[grp][quad] = poison;
       if (quad == 0) {
-        sm.m[grp][lane] = w == INFINITY ? -INFINITY : M * my_qs;
+        sm.m[grp][lane] = seen >> lane & 1 ? M * my_qs : -INFINITY;
         sm.w[grp][lane] = w;
       }
       group_sync();  // the sums have been read
@@ -709,16 +723,16 @@ kv8_rows_attend(const Kv8Args a, const __grid_constant__ CUtensorMap map, const 
           const uint32_t stage = stage_of(step), full = smem_u32(&sm.full[stage]);
           warp_wait(ok, smem_u32(&sm.empty[stage]), turn_of(step) ^ 1, abort, a.err);
           if (!ok) break;
-          StageMeta& me = sm.meta[stage];
           const int c = lane - i;
           if (c == 0 || c == 1) {
+            PageMeta& me = sm.meta[stage][c];
             const bool there = lane < n, bad = there && (my_sc.x != my_sc.x || my_sc.y != my_sc.y);
-            me.kfac[c] = !there || bad ? 0.f : my_sc.x * scale * kLog2e;
-            me.bad[c] = bad;
-            me.vlog[c] = !there || bad ? 0.f : scale_log2(my_sc.y);
-            me.vinv[c] = !there || bad ? 1.f : 1.f / my_sc.y;
-            me.pos[c] = there ? my.pos : 0;
-            me.rows[c] = there ? my.rows : 0u;
+            me.kfac = !there || bad ? 0.f : my_sc.x * scale * kLog2e;
+            me.bad = bad;
+            me.vlog = !there || bad ? 0.f : scale_log2(my_sc.y);
+            me.vinv = !there || bad ? 1.f : 1.f / my_sc.y;
+            me.pos = there ? my.pos : 0;
+            me.rows = there ? my.rows : 0u;
           }
           __syncwarp();
           if (lane == 0) {
