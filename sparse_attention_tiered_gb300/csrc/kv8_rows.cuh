@@ -1,4 +1,5 @@
-// Attention where every token has its own list of pages (spin_kv8_attend_rows): the tiles of tokens that its kernels share.
+// Attention where every token has its own list of pages (spin_kv8_attend_rows): blocks of rows, and the pages that any of a
+// block's tokens lists.
 #pragma once
 
 #include "kv8_dev.cuh"
@@ -6,40 +7,40 @@
 namespace spin {
 namespace kv8 {
 
-// A tile: as many neighbouring tokens of a request as have at most 32 rows of one head between them. Neighbours list much
-// the same pages, so a tile's items are the pages that any of its rows lists, each with a bit per row; and a page
-// costs a tile of 32 rows little more than it costs one of 8.
-constexpr int kRowsOfTile = 32;
-__host__ __device__ __forceinline__ int tile_tokens(int G) { return kRowsOfTile / G; }
+// Rows of a block: the many-row kernel's two tiles, or as many as 64 tokens have, so that a page's tokens are two words of
+// bits. (256 rows of one head are 32 tokens of a group of 8.)
+__host__ __device__ __forceinline__ int list_rows(int G) { return G < 4 ? 64 * G : 2 * kTileRows; }
+// Tokens that have rows in a block, at most.
+__host__ __device__ __forceinline__ int list_tokens(int G) { return list_rows(G) % G ? (list_rows(G) - 1) / G + 2 : list_rows(G) / G; }
 
-struct alignas(16) Tile {
-  int32_t b, h;
-  int32_t token0, tokens;  // rows of q and out: tokens [token0, token0 + tokens)
-  int32_t see0;            // what the first of them sees: tokens 0 .. see0 - 1; the next one more, and so on
-  int32_t full, tail;      // the request's complete pages, and tokens behind them
-  int32_t listed;          // pages
-  int32_t items;           // those, and one more for the tail if a row sees it
-  int32_t reserved[3];
-};
-static_assert(sizeof(Tile) == 48, "");
-
-struct alignas(16) Item {
-  int32_t page;   // of the pool
-  int32_t pos;    // of its first token
-  uint32_t rows;  // row r of the tile attends it: bit r
+struct alignas(16) RowBlock {
+  int32_t b, h, first_row;
+  int32_t row0, n_new;    // of the request, n_new as if the block were its last
+  int32_t past, full, tail;
+  int32_t pages, items;   // listed; and one more for the tail if a row sees it
+  int32_t weight;         // items, and what beginning and ending the block costs; 0: it has none
   int32_t reserved;
+  int64_t place;          // of its items
+  int64_t reserved2;
+};
+static_assert(sizeof(RowBlock) == 64, "");
+
+struct alignas(16) RowItem {
+  int32_t page;        // of the pool
+  int32_t number;      // of the request
+  uint32_t tokens[2];  // of the block, that list it: bit per token
 };
 
-struct RowsSpace {
-  int32_t* tiles_there;  // number of tiles
-  Tile* tiles;
-  Item* items;           // of a tile: from place_of() on, in the order of the pages
+struct RowLists {
+  int32_t* n_blocks;
+  RowBlock* blocks;
+  RowItem* items;
 };
-
-// A tile has room for what its tokens list one by one, and the page that each is in.
-__device__ __forceinline__ int64_t place_of(const Tile& t, int Hkv, int topk) {
-  return ((int64_t)t.token0 * Hkv + (int64_t)t.h * t.tokens) * (topk + 1);
-}
 
 }  // namespace kv8
+
+// Attention of blocks over their lists (k_kv8_prefill.cu).
+cudaError_t launch_kv8_prefill_lists(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const kv8::RowLists& lists,
+                                     void* workspace, int sm_count, cudaStream_t st);
+
 }  // namespace spin
