@@ -100,6 +100,23 @@ kv8_select_scores(const Kv8Args a, const Rows q, SelectSpace s, int X) {
   const int pages = (past + (first - row0) + tokens) >> 6;
   // Whole strips are read, so that a strip has one norm whoever writes it.
   const int full = (past + a.cu[pl.b + 1] - row0) >> 6;
+  const int64_t unit = (int64_t)pl.b * a.Hkv + h;
+  const float* summaries = a.summaries + unit * a.max_pages * kD;
+  // Lane (g, t) has dimensions 16 j + 4 t .. + 3 of pages g and g + 8 of a strip. The first strip is on its way while the queries
+  // are added up.
+  float4 v[2][8];
+  auto load = [&](int p0) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int p = p0 + r * 8 + g;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[r][j] = p < full ? *reinterpret_cast<const float4*>(summaries + (int64_t)p * kD + j * 16 + t * 4)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  int p0 = (x * kWarps + warp) * kStrip;
+  load(p0 < pages ? p0 : full);
   // The tokens' queries, summed over the group: 16 lanes a token, eight dimensions each.
   for (int i = tid >> 4; i < kTokens; i += kThreads / 16) {
     float v[8], abs[8];
@@ -107,15 +124,22 @@ kv8_select_scores(const Kv8Args a, const Rows q, SelectSpace s, int X) {
     for (int e = 0; e < 8; ++e) v[e] = abs[e] = 0.f;
     if (i < tokens) {
       const uint16_t* src = q.p + (int64_t)(first + i) * q.ts + (int64_t)h * a.G * q.hs + (tid & 15) * 8;
-      for (int k = 0; k < a.G; ++k) {
-        const uint4 w = *reinterpret_cast<const uint4*>(src + k * q.hs);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll 1
+      for (int k = 0; k < a.G; k += 4) {  // (four loads on their way)
+        uint4 w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[2 * e] += lo_f(ww[e]);
-          v[2 * e + 1] += hi_f(ww[e]);
-          abs[2 * e] += fabsf(lo_f(ww[e]));
-          abs[2 * e + 1] += fabsf(hi_f(ww[e]));
+        for (int c = 0; c < 4; ++c)
+          w[c] = k + c < a.G ? *reinterpret_cast<const uint4*>(src + (k + c) * q.hs) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t ww[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[2 * e] += lo_f(ww[e]);
+            v[2 * e + 1] += hi_f(ww[e]);
+            abs[2 * e] += fabsf(lo_f(ww[e]));
+            abs[2 * e + 1] += fabsf(hi_f(ww[e]));
+          }
         }
       }
     }
@@ -137,21 +161,10 @@ kv8_select_scores(const Kv8Args a, const Rows q, SelectSpace s, int X) {
       s.qnorms[(int64_t)(first + i - s.t0) * a.Hkv + h] = norm_of(sum) + norm_of(sum_abs) * 0.03125f;
   }
   __syncthreads();
-  const int64_t unit = (int64_t)pl.b * a.Hkv + h;
-  const float* summaries = a.summaries + unit * a.max_pages * kD;
   float* rows = s.scores + ((int64_t)(first - s.t0) * a.Hkv + h) * s.pitch;
   const int64_t row_step = a.Hkv * s.pitch;
-  for (int p0 = (x * kWarps + warp) * kStrip; p0 < pages; p0 += X * kWarps * kStrip) {
-    // Lane (g, t) has dimensions 16 j + 4 t .. + 3 of pages g and g + 8.
-    float4 v[2][8];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int p = p0 + r * 8 + g;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[r][j] = p < full ? *reinterpret_cast<const float4*>(summaries + (int64_t)p * kD + j * 16 + t * 4)
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+  for (bool more = false; p0 < pages; p0 += X * kWarps * kStrip, more = true) {
+    if (more) load(p0);
     float c[NT][4], d[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -211,7 +224,8 @@ __device__ __forceinline__ uint64_t key_of(double x) {
 // The threads that share a row: a warp, or kWide threads. Thread r of them has pages r, r + T, ..
 template <int T>
 struct Team {
-  int32_t* s;  // shared memory of a wide team: [2][warps] counts, a turn each
+  int32_t* s;      // shared memory of a wide team: [2][warps] counts, a turn each
+  uint64_t* keys;  // and [32] keys
   int turn = 0;
   __device__ __forceinline__ int rank() const { return T == 32 ? threadIdx.x & 31 : threadIdx.x; }
   template <typename Op>
@@ -331,7 +345,9 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
   // [low, high]: the doubtful ones, of which `want` are taken.
   uint32_t low = lo, high = 0;
   int want = 0;
-  uint64_t border = 0;  // doubtful ones above it are taken, and the first `equal` of those that equal it
+  bool few = false;     // up to 32 of them:
+  uint32_t taken = 0;   // a bit each, in the order of the pages. Else:
+  uint64_t border = 0;  // those above it are taken, and the first `equal` of those that equal it
   int equal = 0;
   if (!clean) {
     const float x = score_of(lo);
@@ -353,40 +369,70 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
         const uint2 w = *reinterpret_cast<const uint2*>(in.q + g * in.hs + lane * 4);
         qd[0] += (double)lo_f(w.x), qd[1] += (double)hi_f(w.x), qd[2] += (double)lo_f(w.y), qd[3] += (double)hi_f(w.y);
       }
+      auto exact = [&](int p) {  // by a warp
+        const float4 v = *reinterpret_cast<const float4*>(in.summaries + (int64_t)p * kD + lane * 4);
+        double x = qd[0] * (double)v.x + qd[1] * (double)v.y + qd[2] * (double)v.z + qd[3] * (double)v.w;
+        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        return key_of(x);
+      };
+      few = within <= 32;
+      uint64_t mine = 0;
+      int told = 0;
+#pragma unroll 1
       for (int i = 0; i < turns; ++i) {
         const uint32_t y = key(i);
-        uint32_t left = __ballot_sync(0xffffffffu, y >= low && y <= high);
-        uint64_t mine = 0;
-        while (left) {  // the warp's pages one after the other
+        const bool doubt = y >= low && y <= high;
+        uint32_t left = __ballot_sync(0xffffffffu, doubt);
+        int total, number = 0;
+        if (T == 32 && few) number = told, told += __popc(left);
+        else if (few) number = told + team.before(doubt, total), told += total;
+        uint64_t own = 0;
+        for (; left; left &= left - 1) {  // the warp's pages one after the other
           const int l = __ffs(left) - 1;
-          left &= left - 1;
-          const int p = __shfl_sync(0xffffffffu, me, l) + i * T;
-          const float4 v = *reinterpret_cast<const float4*>(in.summaries + (int64_t)p * kD + lane * 4);
-          double x = qd[0] * (double)v.x + qd[1] * (double)v.y + qd[2] * (double)v.z + qd[3] * (double)v.w;
-          for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-          if (lane == l) mine = key_of(x);
+          const uint64_t x = exact(__shfl_sync(0xffffffffu, me, l) + i * T);
+          if (T == 32 && few) {  // in the order of the pages, a lane each
+            if (lane == number) mine = x;
+            ++number;
+          } else if (lane == l) {
+            own = x;
+          }
         }
+        if (T != 32 && few && doubt) team.keys[number] = own;
         const int p = me + i * T;
-        if (p < in.pages) in.exact[p] = mine;  // 0: not doubtful. Read by this thread alone
+        if (!few && p < in.pages) in.exact[p] = own;  // 0: not doubtful. Read by this thread alone
       }
-      auto each_exact = [&](auto f) {
-        for (int i = 0; i < turns; ++i) {
-          const int p = me + i * T;
-          if (p < in.pages) f(in.exact[p]);
+      if (few) {
+        if constexpr (T != 32) {
+          __syncthreads();
+          mine = lane < within ? team.keys[lane] : 0;
         }
-      };
-      // Bisection again, from the top bit down: `border` is the largest number that `want` keys or more reach.
-      for (int bit = 63; bit >= 0; --bit) {
-        const uint64_t mid = border | 1ull << bit;
-        int n = 0;
-        each_exact([&](uint64_t x) { n += x >= mid; });
-        n = team.sum(n);
-        if (n >= want) border = mid;
-        if (n == want) break;
+        int above_mine = 0;
+        for (int j = 0; j < within; ++j) {
+          const uint64_t x = __shfl_sync(0xffffffffu, mine, j);
+          above_mine += x > mine || (x == mine && j < lane);
+        }
+        taken = __ballot_sync(0xffffffffu, lane < within && above_mine < want);
+      } else {
+        auto each_exact = [&](auto f) {
+#pragma unroll 4
+          for (int i = 0; i < turns; ++i) {
+            const int p = me + i * T;
+            if (p < in.pages) f(in.exact[p]);
+          }
+        };
+        // Bisection again, from the top bit down: `border` is the largest number that `want` keys or more reach.
+        for (int bit = 63; bit >= 0; --bit) {
+          const uint64_t mid = border | 1ull << bit;
+          int n = 0;
+          each_exact([&](uint64_t x) { n += x >= mid; });
+          n = team.sum(n);
+          if (n >= want) border = mid;
+          if (n == want) break;
+        }
+        int over = 0;
+        each_exact([&](uint64_t x) { over += x > border; });
+        equal = want - team.sum(over);
       }
-      int over = 0;
-      each_exact([&](uint64_t x) { over += x > border; });
-      equal = want - team.sum(over);
     }
   }
   // In the order of the pages.
@@ -397,13 +443,14 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
     if (take && rank < in.k) in.out[rank] = me + i * T;
   };
   if (high >= low && !clean) {
+#pragma unroll 1
     for (int i = 0; i < turns; ++i) {
       const uint32_t y = key(i);
       const bool doubt = y >= low && y <= high;
-      const uint64_t x = doubt ? in.exact[me + i * T] : 0;
-      const int rank = ties + team.before(doubt && x == border, total);
+      const uint64_t x = doubt && !few ? in.exact[me + i * T] : 0;
+      const int rank = ties + team.before(few ? doubt : doubt && x == border, total);
       ties += total;
-      put(i, y > high || (doubt && (x > border || (x == border && rank < equal))));
+      put(i, y > high || (doubt && (few ? taken >> rank & 1 : x > border || (x == border && rank < equal))));
     }
   } else {
     each([&](int i, uint32_t y) { put(i, y >= low && y != 0); });
@@ -415,10 +462,11 @@ template <int T>
 __global__ void __launch_bounds__(T == 32 ? kThreads : T)
 kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* sel) {
   __shared__ int32_t counts[T == 32 ? 1 : 2 * (T / 32)];
+  __shared__ uint64_t keys[T == 32 ? 1 : 32];
   const int lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t row = T == 32 ? (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t row = T == 32 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
   if (row >= (int64_t)(s.t1 - s.t0) * a.Hkv) return;
   const int token = s.t0 + (int)(row / a.Hkv), h = (int)(row % a.Hkv);
   if (token >= a.cu[a.B]) return;  // padding
@@ -450,14 +498,16 @@ kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* se
   in.q = q.p + (int64_t)token * q.ts + (int64_t)h * a.G * q.hs;
   in.hs = q.hs;
   in.G = a.G;
-  Team<T> team{counts};
+  Team<T> team{counts, keys};
   if constexpr (T == 32) {
     if (in.pages <= 256) pick<T, 8>(team, in);
     else if (in.pages <= 512) pick<T, 16>(team, in);
     else if (in.pages <= 1024) pick<T, 32>(team, in);
     else pick<T, 64>(team, in);
   } else {
-    pick<T, 0>(team, in);
+    if (in.pages <= 8 * T) pick<T, 8>(team, in);
+    else if (in.pages <= 32 * T) pick<T, 32>(team, in);
+    else pick<T, 0>(team, in);
   }
 }
 
@@ -465,10 +515,11 @@ template <int NT>
 cudaError_t launch_scores(const Kv8Args& a, const Rows& q, const SelectSpace& s, int sm_count, cudaStream_t st) {
   const int64_t tokens = s.t1 - s.t0;
   const int64_t tiles = tokens / (8 * NT) + (a.B < tokens ? a.B : tokens);  // at most: each request's last one may be short
-  // Enough CTAs for four of an SM, where the pages allow it.
+  // As many CTAs as two of an SM, where there are not more without: all of them start at once.
   const int64_t runs = ((int64_t)a.max_pages + kWarps * kStrip - 1) / (kWarps * kStrip);
-  int64_t X = (4 * (int64_t)sm_count + tiles * a.Hkv - 1) / (tiles * a.Hkv);
+  int64_t X = 2 * (int64_t)sm_count / (tiles * a.Hkv);
   X = X < runs ? X : runs;
+  X = X > 1 ? X : 1;
   return launch_early(kv8_select_scores<NT>, dim3((unsigned)(tiles * a.Hkv * X)), kThreads, 0, st, a, q, s, (int)X);
 }
 
@@ -494,8 +545,9 @@ cudaError_t launch_kv8_select(const Kv8Args& a, const Rows& q, int topk, int32_t
     cudaError_t e = a.max_new <= 8 ? launch_scores<1>(a, q, s, sm_count, st) : launch_scores<4>(a, q, s, sm_count, st);
     if (e != cudaSuccess) return e;
     const int64_t n = (int64_t)(s.t1 - s.t0) * a.Hkv;
+    const int warps = n >= 8 * kWarps * sm_count ? kWarps : 2;  // few rows are spread over the SMs
     e = a.max_pages <= kNarrowPages
-            ? launch_early(kv8_select_pick<32>, dim3((unsigned)((n + kWarps - 1) / kWarps)), kThreads, 0, st, a, q, s, topk, sel)
+            ? launch_early(kv8_select_pick<32>, dim3((unsigned)((n + warps - 1) / warps)), warps * 32, 0, st, a, q, s, topk, sel)
             : launch_early(kv8_select_pick<kWide>, dim3((unsigned)n), kWide, 0, st, a, q, s, topk, sel);
     if (e != cudaSuccess) return e;
   }
