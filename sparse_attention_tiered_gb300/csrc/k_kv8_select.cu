@@ -29,7 +29,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kStrip = 16;               // pages of a warp's product
 constexpr int kPitch = kD + 16;          // bf16 elements of a query row in shared memory: no two rows of 8 on one bank
 constexpr int kWide = 512;               // threads of a row of many pages
-constexpr int kNarrowPages = 2048;       // a warp's, 64 a lane
 constexpr int64_t kSlabBytes = 1ll << 30;
 
 struct SelectSpace {
@@ -76,7 +75,7 @@ __device__ __forceinline__ int tokens_of(const Kv8Args& a, const SelectSpace& s,
 
 // CTA (tile, head, x): 8 NT tokens of a request, and every X-th run of eight strips of the pages that the last of them sees.
 template <int NT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 kv8_select_scores(const Kv8Args a, const Rows q, SelectSpace s, int X) {
   constexpr int kTokens = 8 * NT;
   __shared__ __align__(16) uint16_t sq[2][kTokens][kPitch];
@@ -215,6 +214,11 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t u = __float_as_uint(x != x ? -INFINITY : x == 0.f ? 0.f : x);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+// The same of first scores, none of which is missing unless all are doubtful: any key but 0 will do for it.
+__device__ __forceinline__ uint32_t quick_key(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return max(u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u), 1u);
+}
 __device__ __forceinline__ float score_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 __device__ __forceinline__ uint64_t key_of(double x) {
   const uint64_t u = (uint64_t)__double_as_longlong(x != x ? -INFINITY : x == 0.0 ? 0.0 : x);
@@ -293,12 +297,12 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int p = me + i * T;
-      held[i] = p < in.pages ? key_of(in.scores[p]) : 0;  // 0: no score's key
+      held[i] = p < in.pages ? quick_key(in.scores[p]) : 0;  // 0: no score's key
     }
   }
   auto key = [&](int i) -> uint32_t {  // from memory, where that is rare or there are too many
     const int p = me + i * T;
-    return p < in.pages ? key_of(in.scores[p]) : 0;
+    return p < in.pages ? quick_key(in.scores[p]) : 0;
   };
   auto each = [&](auto f) {
     if constexpr (N > 0) {
@@ -314,6 +318,7 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
     hi = max(hi, x);
     lo = min(lo, x ? x : 0xffffffffu);
   });
+  if (in.k <= T && in.pages >= T) lo = hi;  // the least of the threads' largest ones: T of them reach it
   lo = team.smallest(lo);
   hi = team.largest(hi);
   float top = 0.f;
@@ -457,8 +462,9 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
   }
 }
 
-// A row: a token and a KV head. T = 32: a warp a row, eight a CTA; else a CTA a row.
-template <int T>
+// A row: a token and a KV head. T = 32: a warp a row; else a CTA a row. N: pages a thread that it holds in registers, if
+// that is enough.
+template <int T, int N>
 __global__ void __launch_bounds__(T == 32 ? kThreads : T)
 kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* sel) {
   __shared__ int32_t counts[T == 32 ? 1 : 2 * (T / 32)];
@@ -499,16 +505,9 @@ kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* se
   in.hs = q.hs;
   in.G = a.G;
   Team<T> team{counts, keys};
-  if constexpr (T == 32) {
-    if (in.pages <= 256) pick<T, 8>(team, in);
-    else if (in.pages <= 512) pick<T, 16>(team, in);
-    else if (in.pages <= 1024) pick<T, 32>(team, in);
-    else pick<T, 64>(team, in);
-  } else {
-    if (in.pages <= 8 * T) pick<T, 8>(team, in);
-    else if (in.pages <= 32 * T) pick<T, 32>(team, in);
-    else pick<T, 0>(team, in);
-  }
+  if (in.pages <= N / 2 * T) pick<T, N / 2>(team, in);
+  else if (in.pages <= N * T) pick<T, N>(team, in);
+  else pick<T, 0>(team, in);
 }
 
 template <int NT>
@@ -546,9 +545,10 @@ cudaError_t launch_kv8_select(const Kv8Args& a, const Rows& q, int topk, int32_t
     if (e != cudaSuccess) return e;
     const int64_t n = (int64_t)(s.t1 - s.t0) * a.Hkv;
     const int warps = n >= 8 * kWarps * sm_count ? kWarps : 2;  // few rows are spread over the SMs
-    e = a.max_pages <= kNarrowPages
-            ? launch_early(kv8_select_pick<32>, dim3((unsigned)((n + warps - 1) / warps)), warps * 32, 0, st, a, q, s, topk, sel)
-            : launch_early(kv8_select_pick<kWide>, dim3((unsigned)n), kWide, 0, st, a, q, s, topk, sel);
+    const dim3 narrow((unsigned)((n + warps - 1) / warps));
+    e = a.max_pages <= 512    ? launch_early(kv8_select_pick<32, 16>, narrow, warps * 32, 0, st, a, q, s, topk, sel)
+        : a.max_pages <= 2048 ? launch_early(kv8_select_pick<32, 64>, narrow, warps * 32, 0, st, a, q, s, topk, sel)
+                              : launch_early(kv8_select_pick<kWide, 32>, dim3((unsigned)n), kWide, 0, st, a, q, s, topk, sel);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
