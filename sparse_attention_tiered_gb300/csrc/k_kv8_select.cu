@@ -229,30 +229,32 @@ __device__ __forceinline__ uint64_t key_of(double x) {
 template <int T>
 struct Team {
   int32_t* s;      // shared memory of a wide team: [2][warps] counts, a turn each
-  uint64_t* keys;  // and [32] keys
+  uint64_t* keys;  // [32] keys
+  uint16_t* found;  // and a count for each warp and turn
   int turn = 0;
   __device__ __forceinline__ int rank() const { return T == 32 ? threadIdx.x & 31 : threadIdx.x; }
-  template <typename Op>
-  __device__ __forceinline__ uint32_t all(uint32_t x, Op op) {
-    if constexpr (T == 32) {
-      return x;
-    } else {
-      int32_t* at = s + (turn ^= 1) * (T / 32);
-      if ((threadIdx.x & 31) == 0) at[threadIdx.x >> 5] = (int32_t)x;
-      __syncthreads();
-      x = (uint32_t)at[0];
-      for (int w = 1; w < T / 32; ++w) x = op(x, (uint32_t)at[w]);
-      return x;
-    }
+  // What the warps' values are; `none` for lanes that stand for no warp.
+  __device__ __forceinline__ uint32_t told(uint32_t x, uint32_t none) {
+    int32_t* at = s + (turn ^= 1) * (T / 32);
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) at[threadIdx.x >> 5] = (int32_t)x;
+    __syncthreads();
+    return lane < T / 32 ? (uint32_t)at[lane] : none;
   }
   __device__ __forceinline__ int sum(int x) {
-    return (int)all(__reduce_add_sync(0xffffffffu, (uint32_t)x), [](uint32_t p, uint32_t q) { return p + q; });
+    uint32_t y = __reduce_add_sync(0xffffffffu, (uint32_t)x);
+    if constexpr (T > 32) y = __reduce_add_sync(0xffffffffu, told(y, 0));
+    return (int)y;
   }
   __device__ __forceinline__ uint32_t smallest(uint32_t x) {
-    return all(__reduce_min_sync(0xffffffffu, x), [](uint32_t p, uint32_t q) { return min(p, q); });
+    x = __reduce_min_sync(0xffffffffu, x);
+    if constexpr (T > 32) x = __reduce_min_sync(0xffffffffu, told(x, 0xffffffffu));
+    return x;
   }
   __device__ __forceinline__ uint32_t largest(uint32_t x) {
-    return all(__reduce_max_sync(0xffffffffu, x), [](uint32_t p, uint32_t q) { return max(p, q); });
+    x = __reduce_max_sync(0xffffffffu, x);
+    if constexpr (T > 32) x = __reduce_max_sync(0xffffffffu, told(x, 0));
+    return x;
   }
   // How many of the threads before this one have `flag`, and how many of all.
   __device__ __forceinline__ int before(bool flag, int& total) {
@@ -457,6 +459,32 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
       ties += total;
       put(i, y > high || (doubt && (few ? taken >> rank & 1 : x > border || (x == border && rank < equal))));
     }
+  } else if constexpr (T > 32 && N > 0) {
+    // All counts first, so that the CTA meets three times and not once a turn.
+    const int warp = threadIdx.x >> 5, warps = T / 32;
+    each([&](int i, uint32_t y) {
+      const uint32_t vote = __ballot_sync(0xffffffffu, y >= low && y != 0);
+      if (lane == 0) team.found[i * warps + warp] = (uint16_t)__popc(vote);
+    });
+    __syncthreads();
+    static_assert(N * (T / 32) <= T, "a thread a count");
+    int mine = me < N * warps ? team.found[me] : 0;
+    int before = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+    }
+    const int last = (int)team.told(__shfl_sync(0xffffffffu, before, 31), 0);
+    before += (int)__reduce_add_sync(0xffffffffu, lane < warp ? (uint32_t)last : 0u) - mine;
+    if (me < N * warps) team.found[me] = (uint16_t)before;
+    __syncthreads();
+    each([&](int i, uint32_t y) {
+      const bool take = y >= low && y != 0;
+      const uint32_t vote = __ballot_sync(0xffffffffu, take);
+      const int rank = team.found[i * warps + warp] + __popc(vote & ((1u << lane) - 1u));
+      if (take && rank < in.k) in.out[rank] = me + i * T;
+    });
+    return;  // (k pages are taken)
   } else {
     each([&](int i, uint32_t y) { put(i, y >= low && y != 0); });
   }
@@ -469,6 +497,7 @@ __global__ void __launch_bounds__(T == 32 ? kThreads : T)
 kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* sel) {
   __shared__ int32_t counts[T == 32 ? 1 : 2 * (T / 32)];
   __shared__ uint64_t keys[T == 32 ? 1 : 32];
+  __shared__ uint16_t found[T == 32 ? 1 : N * (T / 32)];
   const int lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -504,7 +533,7 @@ kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* se
   in.q = q.p + (int64_t)token * q.ts + (int64_t)h * a.G * q.hs;
   in.hs = q.hs;
   in.G = a.G;
-  Team<T> team{counts, keys};
+  Team<T> team{counts, keys, found};
   if (in.pages <= N / 2 * T) pick<T, N / 2>(team, in);
   else if (in.pages <= N * T) pick<T, N>(team, in);
   else pick<T, 0>(team, in);
