@@ -230,6 +230,8 @@ template <int T>
 struct Team {
   int32_t* s;      // shared memory of a wide team: [2][warps] counts, a turn each
   uint64_t* keys;  // [32] keys
+  int32_t* pages;  // [32] and their pages
+  int32_t* listed;  // how many there are, 0 at the start
   uint16_t* found;  // and a count for each warp and turn
   int turn = 0;
   __device__ __forceinline__ int rank() const { return T == 32 ? threadIdx.x & 31 : threadIdx.x; }
@@ -352,8 +354,9 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
   // [low, high]: the doubtful ones, of which `want` are taken.
   uint32_t low = lo, high = 0;
   int want = 0;
-  bool few = false;     // up to 32 of them:
-  uint32_t taken = 0;   // a bit each, in the order of the pages. Else:
+  bool few = false;     // up to 32 of them: a lane each,
+  int page = -1;        // of the lane, and
+  uint32_t taken = 0;   // a bit a lane. Else:
   uint64_t border = 0;  // those above it are taken, and the first `equal` of those that equal it
   int equal = 0;
   if (!clean) {
@@ -372,54 +375,68 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
     else {
       // The group's queries in 64 bits: four dimensions a lane.
       double qd[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
       for (int g = 0; g < in.G; ++g) {
         const uint2 w = *reinterpret_cast<const uint2*>(in.q + g * in.hs + lane * 4);
         qd[0] += (double)lo_f(w.x), qd[1] += (double)hi_f(w.x), qd[2] += (double)lo_f(w.y), qd[3] += (double)hi_f(w.y);
       }
-      auto exact = [&](int p) {  // by a warp
-        const float4 v = *reinterpret_cast<const float4*>(in.summaries + (int64_t)p * kD + lane * 4);
+      auto row = [&](int p) { return *reinterpret_cast<const float4*>(in.summaries + (int64_t)p * kD + lane * 4); };
+      auto exact = [&](float4 v) {  // by a warp
         double x = qd[0] * (double)v.x + qd[1] * (double)v.y + qd[2] * (double)v.z + qd[3] * (double)v.w;
         for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         return key_of(x);
       };
       few = within <= 32;
-      uint64_t mine = 0;
-      int told = 0;
-#pragma unroll 1
-      for (int i = 0; i < turns; ++i) {
-        const uint32_t y = key(i);
-        const bool doubt = y >= low && y <= high;
-        uint32_t left = __ballot_sync(0xffffffffu, doubt);
-        int total, number = 0;
-        if (T == 32 && few) number = told, told += __popc(left);
-        else if (few) number = told + team.before(doubt, total), told += total;
-        uint64_t own = 0;
-        for (; left; left &= left - 1) {  // the warp's pages one after the other
-          const int l = __ffs(left) - 1;
-          const uint64_t x = exact(__shfl_sync(0xffffffffu, me, l) + i * T);
-          if (T == 32 && few) {  // in the order of the pages, a lane each
-            if (lane == number) mine = x;
-            ++number;
-          } else if (lane == l) {
-            own = x;
+      if (few) {  // a lane each, in any order
+        int n = 0;
+        each([&](int i, uint32_t y) {
+          const bool doubt = y >= low && y <= high;
+          if constexpr (T == 32) {
+            for (uint32_t left = __ballot_sync(0xffffffffu, doubt); left; left &= left - 1, ++n)
+              if (lane == n) page = __ffs(left) - 1 + i * T;
+          } else if (doubt) {
+            team.pages[atomicAdd(team.listed, 1)] = me + i * T;
           }
-        }
-        if (T != 32 && few && doubt) team.keys[number] = own;
-        const int p = me + i * T;
-        if (!few && p < in.pages) in.exact[p] = own;  // 0: not doubtful. Read by this thread alone
-      }
-      if (few) {
-        if constexpr (T != 32) {
+        });
+        uint64_t mine = 0;
+        if constexpr (T == 32) {
+          for (int j = 0; j < within; j += 2) {  // two rows on their way
+            const int p0 = __shfl_sync(0xffffffffu, page, j), p1 = __shfl_sync(0xffffffffu, page, min(j + 1, within - 1));
+            const float4 v0 = row(p0), v1 = row(p1);
+            const uint64_t x0 = exact(v0), x1 = exact(v1);
+            if (lane == j) mine = x0;
+            if (lane == j + 1) mine = x1;
+          }
+        } else {
           __syncthreads();
+          for (int j = threadIdx.x >> 5; j < within; j += T / 32) {
+            const uint64_t x = exact(row(team.pages[j]));
+            if (lane == 0) team.keys[j] = x;
+          }
+          __syncthreads();
+          page = lane < within ? team.pages[lane] : 0;
           mine = lane < within ? team.keys[lane] : 0;
         }
-        int above_mine = 0;
+        int better = 0;
         for (int j = 0; j < within; ++j) {
           const uint64_t x = __shfl_sync(0xffffffffu, mine, j);
-          above_mine += x > mine || (x == mine && j < lane);
+          const int p = __shfl_sync(0xffffffffu, page, j);
+          better += x > mine || (x == mine && p < page);
         }
-        taken = __ballot_sync(0xffffffffu, lane < within && above_mine < want);
+        taken = __ballot_sync(0xffffffffu, lane < within && better < want);
       } else {
+#pragma unroll 1
+        for (int i = 0; i < turns; ++i) {
+          const uint32_t y = key(i);
+          uint64_t own = 0;
+          for (uint32_t left = __ballot_sync(0xffffffffu, y >= low && y <= high); left; left &= left - 1) {  // one after the other
+            const int l = __ffs(left) - 1;
+            const uint64_t x = exact(row(__shfl_sync(0xffffffffu, me, l) + i * T));
+            if (lane == l) own = x;
+          }
+          const int p = me + i * T;
+          if (p < in.pages) in.exact[p] = own;  // 0: not doubtful. Read by this thread alone
+        }
         auto each_exact = [&](auto f) {
 #pragma unroll 4
           for (int i = 0; i < turns; ++i) {
@@ -449,21 +466,33 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
     at += total;
     if (take && rank < in.k) in.out[rank] = me + i * T;
   };
-  if (high >= low && !clean) {
+  const bool settle = high >= low && !clean;
+  auto takes = [&](int i, uint32_t y) {  // but where there are many doubtful ones
+    if (!settle) return y >= low && y != 0;
+    uint32_t doubt = __ballot_sync(0xffffffffu, y >= low && y <= high);
+    bool take = y > high;
+    for (; doubt; doubt &= doubt - 1) {
+      const int l = __ffs(doubt) - 1, p = __shfl_sync(0xffffffffu, me, l) + i * T;
+      const bool its = __ballot_sync(0xffffffffu, page == p && (taken >> lane & 1)) != 0;
+      if (lane == l) take = its;
+    }
+    return take;
+  };
+  if (settle && !few) {
 #pragma unroll 1
     for (int i = 0; i < turns; ++i) {
       const uint32_t y = key(i);
       const bool doubt = y >= low && y <= high;
-      const uint64_t x = doubt && !few ? in.exact[me + i * T] : 0;
-      const int rank = ties + team.before(few ? doubt : doubt && x == border, total);
+      const uint64_t x = doubt ? in.exact[me + i * T] : 0;
+      const int rank = ties + team.before(doubt && x == border, total);
       ties += total;
-      put(i, y > high || (doubt && (few ? taken >> rank & 1 : x > border || (x == border && rank < equal))));
+      put(i, y > high || (doubt && (x > border || (x == border && rank < equal))));
     }
   } else if constexpr (T > 32 && N > 0) {
     // All counts first, so that the CTA meets three times and not once a turn.
     const int warp = threadIdx.x >> 5, warps = T / 32;
     each([&](int i, uint32_t y) {
-      const uint32_t vote = __ballot_sync(0xffffffffu, y >= low && y != 0);
+      const uint32_t vote = __ballot_sync(0xffffffffu, takes(i, y));
       if (lane == 0) team.found[i * warps + warp] = (uint16_t)__popc(vote);
     });
     __syncthreads();
@@ -479,14 +508,14 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
     if (me < N * warps) team.found[me] = (uint16_t)before;
     __syncthreads();
     each([&](int i, uint32_t y) {
-      const bool take = y >= low && y != 0;
+      const bool take = takes(i, y);
       const uint32_t vote = __ballot_sync(0xffffffffu, take);
       const int rank = team.found[i * warps + warp] + __popc(vote & ((1u << lane) - 1u));
       if (take && rank < in.k) in.out[rank] = me + i * T;
     });
     return;  // (k pages are taken)
   } else {
-    each([&](int i, uint32_t y) { put(i, y >= low && y != 0); });
+    each([&](int i, uint32_t y) { put(i, takes(i, y)); });
   }
 }
 
@@ -497,6 +526,8 @@ __global__ void __launch_bounds__(T == 32 ? kThreads : T)
 kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* sel) {
   __shared__ int32_t counts[T == 32 ? 1 : 2 * (T / 32)];
   __shared__ uint64_t keys[T == 32 ? 1 : 32];
+  __shared__ int32_t pages[T == 32 ? 1 : 32], listed;
+  if (threadIdx.x == 0) listed = 0;
   __shared__ uint16_t found[T == 32 ? 1 : N * (T / 32)];
   const int lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -533,7 +564,7 @@ kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* se
   in.q = q.p + (int64_t)token * q.ts + (int64_t)h * a.G * q.hs;
   in.hs = q.hs;
   in.G = a.G;
-  Team<T> team{counts, keys, found};
+  Team<T> team{counts, keys, pages, &listed, found};
   if (in.pages <= N / 2 * T) pick<T, N / 2>(team, in);
   else if (in.pages <= N * T) pick<T, N>(team, in);
   else pick<T, 0>(team, in);
