@@ -68,7 +68,6 @@ struct Segment {
   int b, h, first_row, from, to;
   int steps;           // of two items each; 0: the share is done
   int limit0, limit1;  // items that a tile's last row may see; limit1 0: it has none, and the tiles share tile 0's
-  int64_t place;       // of its items in the lists, if it has some
   __device__ __forceinline__ int limit(int tile) const { return tile ? limit1 : limit0; }
   __device__ __forceinline__ bool shared() const { return limit1 == 0; }
   __device__ __forceinline__ bool active(int tile, int step) const { return from + 2 * step < min(to, limit(tile)); }
@@ -96,11 +95,12 @@ struct Smem {
   uint64_t seg_full[kSegments], seg_empty[kSegments];
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2];
   StepMeta meta[4];  // by step mod 4: a softmax warp may be two steps behind the loaders, which run one ahead
-  std::conditional_t<LISTS, ListMeta, NoMeta> lists[4];
   Segment segs[kSegments];
   int64_t scratch[36];
   uint32_t tmem;
   int abort;
+  std::conditional_t<LISTS, ListMeta, NoMeta> lists[4];             // as meta
+  std::conditional_t<LISTS, int64_t, NoMeta> places[kSegments];     // of the segments' items
 };
 
 constexpr size_t kQBytes = (size_t)kBlockRows * kD * 2;       // 64 KB: [tile][2 planes][128 rows][128 bytes]
@@ -337,10 +337,13 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         // vectors, once: a warp alone on its scheduler waits for every dependent instruction.
         uint32_t x[kPart];
         float4 fac, vlog;
-        auto listed = [&](int hf) -> bool {
-          if constexpr (LISTS) return !mine || (sm.lists[(count + step) & 3].tokens[hf][at_token >> 5] >> (at_token & 31) & 1);
-          return true;
-        };
+        uint32_t who = 3, warp_who = 3;  // a bit a page: the row lists it, a row of the warp does
+        if constexpr (LISTS) {
+          const ListMeta& li = sm.lists[(count + step) & 3];
+          who = mine ? (li.tokens[0][at_token >> 5] >> (at_token & 31) & 1u) | (li.tokens[1][at_token >> 5] >> (at_token & 31) & 1u) << 1 : 0u;
+          warp_who = __reduce_or_sync(0xffffffffu, who);
+        }
+        auto listed = [&](int hf) -> bool { return !LISTS || (who >> hf & 1); };
         auto tokens = [&](int hf) { return listed(hf) ? min(see - me.pos[hf], me.count[hf]) : 0; };  // that the row sees
         auto fetch = [&](int hf) {
           tmem_load32(S + hf * kPart, x);
@@ -405,7 +408,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
             tmem_store8(S + c, y);
           }
         };
-        if (__any_sync(0xffffffffu, M == -INFINITY && (!LISTS || tokens(0) > 0 || (halves > 1 && tokens(1) > 0)))) {
+        if (__any_sync(0xffffffffu, M == -INFINITY && (!LISTS || who))) {
           float tm = M, tv = V;  // no reference yet: the step's maximum
 #pragma unroll 1
           for (int hf = 0; hf < halves; ++hf) {
@@ -419,7 +422,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         for (int hf = 0; hf < halves; ++hf) {
           uint32_t p[32];
           const bool on = listed(hf);
-          if (LISTS && !__any_sync(0xffffffffu, on)) {  // nobody's page
+          if (LISTS && !(warp_who >> hf & 1)) {  // nobody's page
 #pragma unroll
             for (int c = 0; c < 16; ++c) p[c] = 0;
             tmem_store16(S + hf * kPart, p);
@@ -648,7 +651,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         if (it < pages) {
           int p = 0;
           if constexpr (LISTS) {
-            const uint4 v = *reinterpret_cast<const uint4*>(lists.items + s.place + it);
+            const uint4 v = *reinterpret_cast<const uint4*>(lists.items + sm.places[seg % kSegments] + it);
             id = (int)v.x;
             p = (int)v.y;
             who[0] = v.z;
@@ -917,6 +920,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       int64_t at = share_start(pl.total, cta, ctas);
       const int64_t stop = share_start(pl.total, cta + 1, ctas);
       JoinRecord open = JoinRecord{};
+      int64_t place = 0;
       Segment s;
       if (!LISTS) s.u = request_of(a, min(b, a.B - 1), false);
       for (bool more = true; more && ok; ++seg) {
@@ -937,7 +941,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           s.b = r.b;
           s.h = r.h;
           s.first_row = r.first_row;
-          s.place = r.place;
+          place = r.place;
           s.from = x.from;
           s.to = x.to;
           s.steps = (x.to - x.from + 1) / 2;
@@ -979,6 +983,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         ok = ok && mbar_wait(smem_u32(&sm.seg_empty[seg % kSegments]), (seg / kSegments & 1) ^ 1, abort, a.err);
         if (!ok) break;
         sm.segs[seg % kSegments] = s;
+        if constexpr (LISTS) sm.places[seg % kSegments] = place;
         mbar_arrive(smem_u32(&sm.seg_full[seg % kSegments]));
       }
       records[cta] = open;
