@@ -41,6 +41,11 @@ class Case:
                         pick = sorted(rng.sample(range(seen), min(k, seen)))
                     elif lists == "near":  # what neighbours have in common
                         pick = sorted({(j * 7 + (i // 5 if j % 3 == 0 else 0)) % seen for j in range(k)}) if seen else []
+                    elif lists == "apart":  # the first 16 tokens of 32, and the others, have nothing in common; some have nothing
+                        lo, hi = (0, seen // 3) if i % 32 < 16 else (seen // 3, seen)
+                        pick = sorted(rng.sample(range(lo, hi), min(k if i % 7 else 0, hi - lo)))
+                    elif lists == "late":  # the first 16 tokens of 32 list nothing
+                        pick = sorted(rng.sample(range(seen), min(k, seen))) if i % 32 >= 16 else []
                     elif lists == "wild":  # any order, twice, outside, in the future
                         pick = [rng.choice([-1, -5, seen, seen + 1, 10 ** 9, rng.randrange(seen) if seen else -1, 0]) for _ in range(k)]
                     else:
@@ -112,6 +117,13 @@ def test_batches_of_single_tokens(batch):
 
 def test_a_chunk():
     check(2, 8, [1500, 0], [150, 90], 8, lists="near", seed=9, pad=5, max_new=2000)
+
+
+@pytest.mark.parametrize("lists", ["apart", "late", "near", "random"])
+@pytest.mark.parametrize("group,new,k", [(8, 32, 9), (8, 70, 2), (5, 60, 7), (16, 40, 5), (1, 200, 3), (3, 90, 6)])
+def test_tiles_with_pages_of_their_own(lists, group, new, k):
+    """Blocks of two tiles: pages of both, of one, of the other, and tiles that attend nothing."""
+    check(1, group, [1984, 70], [new, 3], k, lists=lists, seed=group + new)
 
 
 def test_one_long_list():
