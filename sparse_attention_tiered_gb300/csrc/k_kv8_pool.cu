@@ -20,8 +20,6 @@ struct PoolSpace {  // the workspace of a call
   uint32_t* free_bits;  // [chunks][32]
   int32_t* free_in;     // [chunks]
   int32_t* wanted;      // [B] pages that a request needs
-  int32_t* place;       // [n_pages] where a page goes
-  int32_t* movers;      // [n_pages] the pages that go, in order
 };
 
 __host__ __device__ __forceinline__ int64_t chunks_of(int64_t n_pages) { return (n_pages + kChunk - 1) / kChunk; }
@@ -32,8 +30,6 @@ PoolSpace space_of(const Kv8Args& a, void* workspace) {
   s.free_bits = static_cast<uint32_t*>(workspace);
   s.free_in = reinterpret_cast<int32_t*>(s.free_bits + 32 * chunks);
   s.wanted = s.free_in + chunks;
-  s.place = s.wanted + a.B;
-  s.movers = s.place + a.n_pages;
   return s;
 }
 
@@ -106,22 +102,24 @@ __device__ int prefix_sums(const int32_t* in, int n, int32_t* out, int32_t* scra
   return before;
 }
 
-// The j-th free page, j below their number.
-__device__ __forceinline__ int nth_free(const PoolSpace& s, const int32_t* sums, int chunks, int j) {
+// The j-th free page, or the j-th that is not free, j below their number.
+template <bool FREE>
+__device__ __forceinline__ int nth_page(const PoolSpace& s, const int32_t* sums, int chunks, int j) {
+  auto before = [&](int c) { return FREE ? sums[c] : c * kChunk - sums[c]; };
   int lo = 0, hi = chunks;  // the last chunk with no more than j before it
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (sums[mid] <= j) lo = mid;
+    if (before(mid) <= j) lo = mid;
     else hi = mid;
   }
-  int rest = j - sums[lo];
+  int rest = j - before(lo);
   const uint4* words = reinterpret_cast<const uint4*>(s.free_bits + (int64_t)lo * 32);
   int at = 0;
   uint32_t bits = 0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const uint4 v = words[k];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t w[4] = {FREE ? v.x : ~v.x, FREE ? v.y : ~v.y, FREE ? v.z : ~v.z, FREE ? v.w : ~v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int n = __popc(w[e]);
@@ -132,6 +130,24 @@ __device__ __forceinline__ int nth_free(const PoolSpace& s, const int32_t* sums,
   rest += 0x10000;
   for (; rest > 0; --rest) bits &= bits - 1;
   return lo * kChunk + at * 32 + (__ffs(bits) - 1);
+}
+
+// Free pages below this one (which is in the pool).
+__device__ __forceinline__ int free_before(const PoolSpace& s, const int32_t* sums, int page) {
+  const int c = page / kChunk, last = page >> 5 & 31;
+  int n = sums[c];
+  const uint4* words = reinterpret_cast<const uint4*>(s.free_bits + (int64_t)c * 32);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint4 v = words[k];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int x = k * 4 + e;
+      n += x < last ? __popc(w[e]) : x == last ? __popc(w[e] & ((1u << (page & 31)) - 1u)) : 0;
+    }
+  }
+  return n;
 }
 
 // A CTA a request.
@@ -191,19 +207,21 @@ kv8_pool_reserve(const Kv8Args a, int32_t* refs, PoolSpace s, int32_t* free_page
     }
     __syncthreads();
     if (want && j < free) {
-      const int page = nth_free(s, sums, chunks, j);
+      const int page = nth_page<true>(s, sums, chunks, j);
       *entry = page;
       refs[page] = 1;
     }
   }
 }
 
-// Of the U pages in use those with ids of U and more go to the free ones below U, in order. A CTA some chunks, a page a
-// thread; what the pages hold is copied by the next launch.
+// Of the U pages in use those with ids of U and more go to the free ones below U, in order: the j-th of them is the j-th page
+// in use behind those below U, and its place is the j-th free one, so every CTA finds both ends of what it copies for itself,
+// all of them at once. A CTA a page at a time, 16 bytes a thread and load, four on their way. The table's entries follow by the same rule.
 __global__ void __launch_bounds__(kThreads)
-kv8_pool_place(const Kv8Args a, int32_t* refs, PoolSpace s, int32_t* free_pages) {
+kv8_pool_move(const Kv8Args a, int32_t* refs, PoolSpace s, int32_t* free_pages) {
   extern __shared__ int32_t sums[];  // [chunks]
   __shared__ int32_t scratch[kWarps];
+  __shared__ int2 ends[kThreads];
   const int tid = threadIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -211,42 +229,16 @@ kv8_pool_place(const Kv8Args a, int32_t* refs, PoolSpace s, int32_t* free_pages)
   const int free = prefix_sums(s.free_in, chunks, sums, scratch);
   const int used = (int)a.n_pages - free;
   if (blockIdx.x == 0 && tid == 0 && free_pages) *free_pages = free;
-  auto free_before = [&](int page) {  // free pages below it
-    const int c = page / kChunk, w = (page & (kChunk - 1)) >> 5;
-    int n = sums[c] + __popc(s.free_bits[page >> 5] & ((1u << (page & 31)) - 1u));
-    for (int k = 0; k < w; ++k) n += __popc(s.free_bits[c * 32 + k]);
-    return n;
-  };
-  const int holes = used < a.n_pages ? free_before(used) : 0;  // as many as pages that go
-  for (int64_t page = (int64_t)used + (int64_t)blockIdx.x * kThreads + tid; page < a.n_pages; page += (int64_t)gridDim.x * kThreads) {
-    if (s.free_bits[page >> 5] >> (page & 31) & 1) continue;
-    const int j = ((int)page - free_before((int)page)) - (used - holes);
-    const int to = nth_free(s, sums, chunks, j);
-    s.place[page] = to;
-    s.movers[j] = (int)page;
-    refs[to] = refs[page];
-    refs[page] = 0;
-  }
-}
-
-// The table's entries follow, and what the pages hold is copied: a CTA a page at a time, 16 bytes a thread and load, four on
-// their way.
-__global__ void __launch_bounds__(kThreads)
-kv8_pool_move(const Kv8Args a, PoolSpace s) {
-  extern __shared__ int32_t sums[];
-  __shared__ int32_t scratch[kWarps];
-  const int tid = threadIdx.x;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int chunks = (int)chunks_of(a.n_pages);
-  const int used = (int)a.n_pages - prefix_sums(s.free_in, chunks, sums, scratch);
-  if (used < a.n_pages) {
-    int holes = sums[used / kChunk];
-    for (int k = used / kChunk * 32; k < used >> 5; ++k) holes += __popc(s.free_bits[k]);
-    holes += __popc(s.free_bits[used >> 5] & ((1u << (used & 31)) - 1u));
-    constexpr int kVec = kKv8PageBytes / 16 / kThreads;
-    for (int j = blockIdx.x; j < holes; j += gridDim.x) {
-      const int from = s.movers[j], to = s.place[from];
+  const int holes = used < a.n_pages ? free_before(s, sums, used) : 0;  // as many as pages that go
+  constexpr int kVec = kKv8PageBytes / 16 / kThreads;
+  for (int64_t first = blockIdx.x; first < holes; first += (int64_t)kThreads * gridDim.x) {  // a thread a page, for its ends
+    const int64_t j = first + (int64_t)tid * gridDim.x;
+    __syncthreads();
+    if (j < holes) ends[tid] = make_int2(nth_page<false>(s, sums, chunks, used - holes + (int)j), nth_page<true>(s, sums, chunks, (int)j));
+    __syncthreads();
+    const int n = (int)min((int64_t)kThreads, (holes - first + gridDim.x - 1) / gridDim.x);
+    for (int i = 0; i < n; ++i) {
+      const int from = ends[i].x, to = ends[i].y;
       const uint4* src = reinterpret_cast<const uint4*>(a.pages + (int64_t)from * kKv8PageBytes);
       uint4* dst = reinterpret_cast<uint4*>(a.pages + (int64_t)to * kKv8PageBytes);
       uint4 v[kVec];
@@ -255,6 +247,7 @@ kv8_pool_move(const Kv8Args a, PoolSpace s) {
 #pragma unroll
       for (int k = 0; k < kVec; ++k) dst[k * kThreads + tid] = v[k];
       if (tid == 0) *reinterpret_cast<float2*>(a.scales + 2 * (int64_t)to) = *reinterpret_cast<const float2*>(a.scales + 2 * (int64_t)from);
+      if (tid == 32) refs[to] = refs[from], refs[from] = 0;
     }
   }
   const int64_t entries = (int64_t)a.B * a.Hkv * a.max_pages;
@@ -263,7 +256,7 @@ kv8_pool_move(const Kv8Args a, PoolSpace s) {
     const int e = table[x];
     if (e < 0) continue;
     if (e >= a.n_pages || (s.free_bits[e >> 5] >> (e & 31) & 1)) atomicOr(a.err, (uint32_t)kErrIndex);  // a page that is not in use
-    else if (e >= used) table[x] = s.place[e];
+    else if (e >= used) table[x] = nth_page<true>(s, sums, chunks, e - free_before(s, sums, e) - (used - holes));
   }
 }
 
@@ -276,6 +269,7 @@ kv8_pool_move(const Kv8Args a, PoolSpace s) {
 constexpr int kForkThreads = 512;
 constexpr int kHeld = 32;         // 32-bit registers a thread, of the columns that pass through it
 constexpr int kColumns = 8;       // pages of an item
+constexpr int kMostRows = kHeld / 4 * kForkThreads;  // that a CTA can hold 16 bytes each of
 
 struct Move {
   int32_t to, from, len;  // `from` -1: emptied
@@ -346,7 +340,9 @@ __device__ void copy_tails(const Kv8Args& a, const Move* moves, int n_moves, int
 
 constexpr int kTailBytes = 2048;  // of an item
 
-__global__ void __launch_bounds__(kForkThreads)
+// MANY: batches of more requests than a CTA can hold 16 bytes each of.
+template <bool MANY>
+__global__ void __launch_bounds__(kForkThreads, MANY ? 1 : 2)
 kv8_pool_fork(const Kv8Args a, int32_t* refs, const int32_t* len, const int32_t* src) {
   extern __shared__ Move moves[];  // [B], and a byte each
   __shared__ int n_moves;
@@ -375,7 +371,8 @@ kv8_pool_fork(const Kv8Args a, int32_t* refs, const int32_t* len, const int32_t*
   __syncthreads();
   const int n = n_moves;
   if (n == 0) return;
-  const bool narrow = n > kHeld / 4 * kForkThreads;  // more rows than a CTA can hold 16 bytes each of
+  constexpr int kEntries = MANY ? kHeld : kHeld / 4;  // table entries that a thread holds
+  const bool narrow = MANY && n > kMostRows;
   const int groups = (a.max_pages + kColumns - 1) / kColumns, tail_items = kPageElems * 2 / kTailBytes;
   const int64_t items = (int64_t)a.Hkv * (groups + tail_items);
   int32_t* table = const_cast<int32_t*>(a.table);
@@ -384,64 +381,65 @@ kv8_pool_fork(const Kv8Args a, int32_t* refs, const int32_t* len, const int32_t*
     const int h = (int)(item % a.Hkv), g = (int)(item / a.Hkv);
     if (g < tail_items) {
       const int64_t off = (int64_t)h * kPageElems * 2 + (int64_t)g * kTailBytes;
-      if (narrow) copy_tails<uint32_t>(a, moves, n, off, kTailBytes);
-      else copy_tails<uint4>(a, moves, n, off, kTailBytes);
+      if constexpr (MANY) {
+        if (narrow) copy_tails<uint32_t>(a, moves, n, off, kTailBytes);
+      }
+      if (!narrow) copy_tails<uint4>(a, moves, n, off, kTailBytes);
       continue;
     }
     const int p0 = (g - tail_items) * kColumns, pages = min(kColumns, a.max_pages - p0);
     auto entry = [&](int b, int p) { return table + ((int64_t)b * a.Hkv + h) * a.max_pages + p; };
-    if (a.summaries) {
-      bool some = false;
-      for (int m = tid; m < n; m += kForkThreads) {
-        const Move v = moves[m];
-        uint32_t bits = 0;
-        if (v.from >= 0) {
-          int mine[kColumns], other[kColumns];
-#pragma unroll
-          for (int k = 0; k < kColumns; ++k) {
-            const bool there = k < pages && p0 + k < v.len >> 6;
-            mine[k] = there ? *entry(v.to, p0 + k) : 0;
-            other[k] = there ? *entry(v.from, p0 + k) : 0;
-          }
-#pragma unroll
-          for (int k = 0; k < kColumns; ++k) bits |= (mine[k] != other[k]) << k;
-        }
-        need[m] = (uint8_t)bits;
-        some |= bits != 0;
-      }
-      if (__syncthreads_or(some)) {
-        const int64_t stride = (int64_t)a.Hkv * a.max_pages * kD * 4, off = ((int64_t)h * a.max_pages + p0) * kD * 4;
-        if (narrow) copy_columns<uint32_t>(a, moves, n, need, a.summaries, stride, off, pages * kD * 4, p0);
-        else copy_columns<uint4>(a, moves, n, need, a.summaries, stride, off, pages * kD * 4, p0);
-      }
-    }
-    int lw = 3;  // entries: 8 of a request, fewer where there are too many requests
-    while (lw > 0 && (int64_t)n << lw > kHeld * kForkThreads) --lw;
+    // Entries: 8 of a request at a time, fewer where there are too many requests. Sources are read before any entry is written.
+    int lw = 3;
+    while (lw > 0 && (int64_t)n << lw > kEntries * kForkThreads) --lw;
+    bool some = false;
     for (int x = 0; x < pages; x += 1 << lw) {
       __syncthreads();
-      pass<int32_t>(
-          n, lw,
-          [&](int m, int c) {
-            const Move mv = moves[m];
-            const int p = p0 + x + c;
-            return mv.from >= 0 && p < a.max_pages && p < mv.len >> 6 ? *entry(mv.from, p) : -1;
-          },
-          [&](int m, int c, int32_t v) {
-            const int p = p0 + x + c;
-            if (p >= a.max_pages) return;
-            int32_t* e = entry(moves[m].to, p);
-            const int old = *e;
-            if (old == v) return;
-            *e = v;
-            if (old >= 0) {
-              if (old < a.n_pages) atomicSub(refs + old, 1);
-              else atomicOr(a.err, (uint32_t)kErrIndex);
-            }
-            if (v >= 0) {
-              if (v < a.n_pages) atomicAdd(refs + v, 1);
-              else atomicOr(a.err, (uint32_t)kErrIndex);
-            }
-          });
+      int32_t v[kEntries];
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k) {
+        if (k * kForkThreads >= n << lw) break;
+        const int i = tid + k * kForkThreads, m = i >> lw, c = i & ((1 << lw) - 1), p = p0 + x + c;
+        bool differs = false;
+        v[k] = -1;
+        if (m < n && p < a.max_pages) {
+          const Move mv = moves[m];
+          const int old = *entry(mv.to, p);
+          if (mv.from >= 0 && p < mv.len >> 6) {
+            v[k] = *entry(mv.from, p);
+            differs = v[k] != old;
+          }
+        }
+        const uint32_t bits = __ballot_sync(0xffffffffu, differs) >> (tid & 31 & ~((1 << lw) - 1)) & ((1u << (1 << lw)) - 1u);
+        if (m < n && c == 0) need[m] = (uint8_t)(x ? need[m] | bits << x : bits);
+        some |= differs;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kEntries; ++k) {
+        if (k * kForkThreads >= n << lw) break;
+        const int i = tid + k * kForkThreads, m = i >> lw, p = p0 + x + (i & ((1 << lw) - 1));
+        if (m >= n || p >= a.max_pages) continue;
+        int32_t* e = entry(moves[m].to, p);
+        const int old = *e;
+        if (old == v[k]) continue;
+        *e = v[k];
+        if (old >= 0) {
+          if (old < a.n_pages) atomicSub(refs + old, 1);
+          else atomicOr(a.err, (uint32_t)kErrIndex);
+        }
+        if (v[k] >= 0) {
+          if (v[k] < a.n_pages) atomicAdd(refs + v[k], 1);
+          else atomicOr(a.err, (uint32_t)kErrIndex);
+        }
+      }
+    }
+    if (a.summaries && __syncthreads_or(some)) {
+      const int64_t stride = (int64_t)a.Hkv * a.max_pages * kD * 4, off = ((int64_t)h * a.max_pages + p0) * kD * 4;
+      if constexpr (MANY) {
+        if (narrow) copy_columns<uint32_t>(a, moves, n, need, a.summaries, stride, off, pages * kD * 4, p0);
+      }
+      if (!narrow) copy_columns<uint4>(a, moves, n, need, a.summaries, stride, off, pages * kD * 4, p0);
     }
   }
 }
@@ -481,7 +479,7 @@ cudaError_t count(const Kv8Args& a, const int32_t* refs, const PoolSpace& s, int
 
 }  // namespace
 
-int64_t kv8_pool_workspace(const Kv8Args& a) { return 4 * (33 * chunks_of(a.n_pages) + a.B + 2 * a.n_pages); }
+int64_t kv8_pool_workspace(const Kv8Args& a) { return 4 * (33 * chunks_of(a.n_pages) + a.B); }
 
 cudaError_t launch_kv8_reserve(const Kv8Args& a, int32_t* refs, int32_t* free_pages, void* workspace, cudaStream_t st) {
   const PoolSpace s = space_of(a, workspace);
@@ -495,23 +493,22 @@ cudaError_t launch_kv8_reserve(const Kv8Args& a, int32_t* refs, int32_t* free_pa
 cudaError_t launch_kv8_compact(const Kv8Args& a, int32_t* refs, int32_t* free_pages, void* workspace, int sm_count, cudaStream_t st) {
   const PoolSpace s = space_of(a, workspace);
   const size_t bytes = chunks_of(a.n_pages) * 4;
-  cudaError_t e = shared_bytes(reinterpret_cast<const void*>(kv8_pool_place), bytes);
-  if (e == cudaSuccess) e = shared_bytes(reinterpret_cast<const void*>(kv8_pool_move), bytes);
+  cudaError_t e = shared_bytes(reinterpret_cast<const void*>(kv8_pool_move), bytes);
   if (e == cudaSuccess) e = count(a, refs, s, 0, st);
   if (e != cudaSuccess) return e;
-  const unsigned grid = at_most((a.n_pages + kThreads - 1) / kThreads, (int64_t)sm_count * 4);
-  e = launch_early(kv8_pool_place, dim3(grid), kThreads, bytes, st, a, refs, s, free_pages);
-  if (e != cudaSuccess) return e;
-  return launch_early(kv8_pool_move, dim3((unsigned)sm_count * 8), kThreads, bytes, st, a, s);
+  return launch_early(kv8_pool_move, dim3((unsigned)sm_count * 8), kThreads, bytes, st, a, refs, s, free_pages);
 }
 
 cudaError_t launch_kv8_fork(const Kv8Args& a, int32_t* refs, int32_t* len, const int32_t* src, int sm_count, cudaStream_t st) {
   const size_t bytes = (size_t)a.B * (sizeof(Move) + 1);
-  cudaError_t e = shared_bytes(reinterpret_cast<const void*>(kv8_pool_fork), bytes);
+  const bool many = a.B > kMostRows;
+  cudaError_t e = many ? shared_bytes(reinterpret_cast<const void*>(kv8_pool_fork<true>), bytes)
+                       : shared_bytes(reinterpret_cast<const void*>(kv8_pool_fork<false>), bytes);
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)a.Hkv * ((a.max_pages + kColumns - 1) / kColumns + kPageElems * 2 / kTailBytes);
-  e = launch_early(kv8_pool_fork, dim3(at_most(items, (int64_t)sm_count * 3)), kForkThreads, bytes, st, a, refs,
-                   static_cast<const int32_t*>(len), src);
+  const int32_t* lengths = len;
+  e = many ? launch_early(kv8_pool_fork<true>, dim3(at_most(items, sm_count)), kForkThreads, bytes, st, a, refs, lengths, src)
+           : launch_early(kv8_pool_fork<false>, dim3(at_most(items, (int64_t)sm_count * 2)), kForkThreads, bytes, st, a, refs, lengths, src);
   if (e != cudaSuccess) return e;
   return launch_early(kv8_pool_lengths, dim3(1), 1024, 0, st, a, len, src);
 }
