@@ -39,9 +39,6 @@
 // a block more. Drafts of 5 tokens in groups of 8 (40 of a tile's 128 rows) read 0.33 GB in 135 us: 66 steps a CTA
 // that are a chain of load, conversion, product, softmax and product with one step's codes in flight. Nothing is
 // saturated there (DRAM 31%, the tensor pipe 27%, issue slots 36%).
-#include <type_traits>
-
-#include "kv8_rows.cuh"
 #include "kv8_tc.cuh"
 
 namespace spin {
@@ -84,13 +81,6 @@ struct alignas(16) StepMeta {
   int pos[2], count[2];  // position of each page's first token, tokens it holds (0: no page)
 };
 
-// Which tokens of the block list each page of a step: bit per token. All of them see the tail, as far as it is theirs to see.
-struct ListMeta {
-  uint32_t tokens[2][2];
-};
-struct NoMeta {};
-
-template <bool LISTS>
 struct Smem {
   uint64_t seg_full[kSegments], seg_empty[kSegments];
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2];
@@ -99,17 +89,14 @@ struct Smem {
   int64_t scratch[36];
   uint32_t tmem;
   int abort;
-  std::conditional_t<LISTS, ListMeta, NoMeta> lists[4];             // as meta
-  std::conditional_t<LISTS, int64_t, NoMeta> places[kSegments];     // of the segments' items
 };
 
 constexpr size_t kQBytes = (size_t)kBlockRows * kD * 2;       // 64 KB: [tile][2 planes][128 rows][128 bytes]
 constexpr size_t kKvBytes = (size_t)2 * kPlane;               // 64 KB each
-template <bool LISTS>
-constexpr size_t kSmemBytes = 1024 + kQBytes + 2 * kKvBytes + sizeof(Smem<LISTS>);
+constexpr size_t kSmemBytes = 1024 + kQBytes + 2 * kKvBytes + sizeof(Smem);
 // 196 KB with the 1 KB that the system takes: the next size of the SM's shared memory would leave the L1
 // too small to have the loaders' loads in flight (11% slower, with few rows 25%).
-static_assert(kSmemBytes<false> + 1024 <= 196 * 1024 && kSmemBytes<true> + 1024 <= 196 * 1024, "shared memory of a CTA");
+static_assert(kSmemBytes + 1024 <= 196 * 1024, "shared memory of a CTA");
 constexpr int kWeights = 4096;  // requests' weights, in Q's place before there is a Q
 static_assert(kWeights * 8 <= kQBytes, "");
 
@@ -167,15 +154,13 @@ __device__ __forceinline__ int64_t blocks_weight(const Kv8Args& a, int b, int to
   return sum * a.Hkv;
 }
 
-// LISTS: blocks of rows and their items are those of `lists` (kv8_rows.cuh), and a row attends the pages that its token lists.
-template <bool LISTS>
 __global__ void __launch_bounds__(kThreads, 1)
 kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, const int32_t* sel, int topk,
-                   JoinRecord* records, float* partials, const RowLists lists) {
+                   JoinRecord* records, float* partials) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sq = smem_u32(base), sk = sq + (uint32_t)kQBytes, sv = sk + (uint32_t)kKvBytes;
-  Smem<LISTS>& sm = *reinterpret_cast<Smem<LISTS>*>(base + kQBytes + 2 * kKvBytes);
+  Smem& sm = *reinterpret_cast<Smem*>(base + kQBytes + 2 * kKvBytes);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   volatile int* abort = &sm.abort;
   const int ctas = gridDim.x, cta = blockIdx.x;
@@ -207,7 +192,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tmem_before();
   // Requests' weights, a warp each; beyond kWeights requests, a thread each, twice over.
-  const bool few = !LISTS && a.B <= kWeights;
+  const bool few = a.B <= kWeights;
   int64_t* weights = reinterpret_cast<int64_t*>(base);
   if (few) {
     for (int b = warp; b < a.B; b += kThreads / 32) {
@@ -223,14 +208,9 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
     }
     __syncthreads();
   }
-  const int requests = LISTS ? *lists.n_blocks : a.B;  // or blocks, each for itself
   const Place pl = locate(
-      requests, sm.scratch,
-      [&](int x, bool first) {
-        return LISTS ? (int64_t)lists.blocks[x].weight : few ? weights[x] : blocks_weight(a, x, topk, first && cta == 0);
-      },
+      a.B, sm.scratch, [&](int x, bool first) { return few ? weights[x] : blocks_weight(a, x, topk, first && cta == 0); },
       [&](int64_t total) { return share_start(total, cta, ctas); });
-  if (LISTS) __syncthreads();
   tmem_after();
   const uint32_t tmem = sm.tmem;
   bool ok = true;
@@ -266,7 +246,6 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       const int row = s.first_row + (shared ? 0 : tile * kTile) + quad * 32 + lane;
       const bool mine = row < s.u.n_new * a.G;
       const int i = row / a.G, head = s.h * a.G + row - i * a.G;
-      const int at_token = mine ? i - s.first_row / a.G : 0;  // of the block
       const int see = mine ? s.u.past + i + 1 : 0x7fffffff;  // rows that are not there see all: no masks for them
       float qs = 1.f;
       bool wrong = false;   // the row's query is not finite: NaN, if it sees a token
@@ -304,8 +283,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         qs = wrong ? 1.f : pow2(e - 15);
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          uint4 w = lds128(place(c));
-          if (LISTS && wrong) w = make_uint4(0, 0, 0, 0);  // what it does not list must not make it NaN
+          const uint4 w = lds128(place(c));
           sts128(place(c), pack_half2(lo_f(w.x) * f, hi_f(w.x) * f), pack_half2(lo_f(w.y) * f, hi_f(w.y) * f),
                  pack_half2(lo_f(w.z) * f, hi_f(w.z) * f), pack_half2(lo_f(w.w) * f, hi_f(w.w) * f));
         }
@@ -337,14 +315,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         // vectors, once: a warp alone on its scheduler waits for every dependent instruction.
         uint32_t x[kPart];
         float4 fac, vlog;
-        uint32_t who = 3, warp_who = 3;  // a bit a page: the row lists it, a row of the warp does
-        if constexpr (LISTS) {
-          const ListMeta& li = sm.lists[(count + step) & 3];
-          who = mine ? (li.tokens[0][at_token >> 5] >> (at_token & 31) & 1u) | (li.tokens[1][at_token >> 5] >> (at_token & 31) & 1u) << 1 : 0u;
-          warp_who = __reduce_or_sync(0xffffffffu, who);
-        }
-        auto listed = [&](int hf) -> bool { return !LISTS || (who >> hf & 1); };
-        auto tokens = [&](int hf) { return listed(hf) ? min(see - me.pos[hf], me.count[hf]) : 0; };  // that the row sees
+        auto tokens = [&](int hf) { return min(see - me.pos[hf], me.count[hf]); };  // that the row sees
         auto fetch = [&](int hf) {
           tmem_load32(S + hf * kPart, x);
           tmem_load32(S + hf * kPart + 32, x + 32);
@@ -352,7 +323,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
           vlog = *reinterpret_cast<const float4*>(&me.vlog[4 * hf]);
           // not 0, which would make NaN of a hidden token's -inf
           fac = make_float4(fmaxf(fac.x * qs, 1e-37f), fmaxf(fac.y * qs, 1e-37f), fmaxf(fac.z * qs, 1e-37f), fmaxf(fac.w * qs, 1e-37f));
-          const int vis = LISTS && !listed(hf) ? kPart : tokens(hf);  // a row that does not list the page has a weight of 0 all the same
+          const int vis = tokens(hf);
           const bool some = __any_sync(0xffffffffu, vis < kPart);
           tmem_loaded();
           settle32(x);
@@ -408,30 +379,22 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
             tmem_store8(S + c, y);
           }
         };
-        if (__any_sync(0xffffffffu, M == -INFINITY && (!LISTS || who))) {
-          float tm = M, tv = V;  // no reference yet: the step's maximum
+        if (__any_sync(0xffffffffu, M == -INFINITY)) {  // no reference yet: the step's maximum
+          float tm = M, tv = V;
 #pragma unroll 1
           for (int hf = 0; hf < halves; ++hf) {
             fetch(hf);
-            if (!LISTS || listed(hf)) largest(tm, tv);
+            largest(tm, tv);
           }
           if (M == -INFINITY) M = tm, V = tv;
           aim();
         }
 #pragma unroll 1
         for (int hf = 0; hf < halves; ++hf) {
-          uint32_t p[32];
-          const bool on = listed(hf);
-          if (LISTS && !(warp_who >> hf & 1)) {  // nobody's page
-#pragma unroll
-            for (int c = 0; c < 16; ++c) p[c] = 0;
-            tmem_store16(S + hf * kPart, p);
-            tmem_store16(S + hf * kPart + 16, p);
-            continue;
-          }
           fetch(hf);
+          uint32_t p[32];
           float sum[4];
-          float shift = on ? up : -INFINITY, most = limit;
+          float shift = up, most = limit;
           for (;;) {  // twice at most: no sum is above the second time's limit
 #pragma unroll
             for (int grp = 0; grp < 4; ++grp) {
@@ -458,7 +421,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
             // most kUp + 3, with the score's difference taken first.
             fetch(hf);
             float tm = M, tv = V, d = 0.f;
-            if (on) largest(tm, tv);
+            largest(tm, tv);
             const float above = (tm - M) + (tv - V);
             if (above > 3.f && !wrong) {
               d = above < 64.f ? ceilf(above) : above;
@@ -475,7 +438,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
             };
             apart(0, fac.x), apart(1, fac.y), apart(2, fac.z), apart(3, fac.w);
             fac = make_float4(1.f, 1.f, 1.f, 1.f);
-            shift = on ? kUp - V : -INFINITY;
+            shift = kUp - V;
           }
           const float4 vinv = *reinterpret_cast<const float4*>(&me.vinv[4 * hf]);
           L += fmaf(sum[0], vinv.x, sum[1] * vinv.y) + fmaf(sum[2], vinv.z, sum[3] * vinv.w);
@@ -640,7 +603,6 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       // Page ids of 32 items, a lane each, and for the keys' warps what the softmax has to know of the pages.
       float kfac = 0.f, vlog = 0.f, vinv = 1.f;
       bool bad = false;
-      uint32_t who[2] = {0, 0};  // tokens that list the page
       auto look = [&](int first) {
         id_base = first;
         const int it = first + lane;
@@ -649,19 +611,10 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         vinv = 1.f;
         bad = false;
         if (it < pages) {
-          int p = 0;
-          if constexpr (LISTS) {
-            const uint4 v = *reinterpret_cast<const uint4*>(lists.items + sm.places[seg % kSegments] + it);
-            id = (int)v.x;
-            p = (int)v.y;
-            who[0] = v.z;
-            who[1] = v.w;
-          } else {
-            p = topk ? sel[unit * topk + it] : it;
-          }
-          if (LISTS || (p >= 0 && p < s.u.full)) {
-            if (!LISTS) id = a.table[unit * a.max_pages + p];
-            if (!LISTS && (id < 0 || (int64_t)id >= a.n_pages)) {
+          const int p = topk ? sel[unit * topk + it] : it;
+          if (p >= 0 && p < s.u.full) {
+            id = a.table[unit * a.max_pages + p];
+            if (id < 0 || (int64_t)id >= a.n_pages) {
               if (w4 == 0) atomicOr(a.err, (uint32_t)kErrIndex);
               id = -1;
             } else {
@@ -763,13 +716,10 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
               me.vinv[x * 4 + w4] = vinv;
               me.bad_keys[x * 4 + w4] = bad ? 0xffffu : 0u;
               if (w4 == 0) me.count[x] = pos >= 0 ? kPart : 0, me.pos[x] = max(pos, 0);
-              if constexpr (LISTS)
-                if (w4 == 0) sm.lists[count & 3].tokens[x][0] = who[0], sm.lists[count & 3].tokens[x][1] = who[1];
             }
             if (w4 == 0 && lane < 2 && it + lane >= pages) {
               me.count[lane] = it + lane < s.to ? s.u.tail : 0;
               me.pos[lane] = s.u.full * kPart;
-              if constexpr (LISTS) sm.lists[count & 3].tokens[lane][0] = sm.lists[count & 3].tokens[lane][1] = 0xffffffffu;
             }
           }
           // The next step's loads, each as soon as its registers are free.
@@ -894,7 +844,7 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
     }
     int block = 0;
     int64_t before = pl.before;
-    if (!LISTS && warp == kPlanWarp && pl.b < a.B) {  // the share's first block, 32 at a time
+    if (warp == kPlanWarp && pl.b < a.B) {  // the share's first block, 32 at a time
       const int64_t at = share_start(pl.total, cta, ctas);
       Unit u = request_of(a, pl.b, false);
       for (;; block += 32) {
@@ -920,36 +870,11 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
       int64_t at = share_start(pl.total, cta, ctas);
       const int64_t stop = share_start(pl.total, cta + 1, ctas);
       JoinRecord open = JoinRecord{};
-      int64_t place = 0;
       Segment s;
-      if (!LISTS) s.u = request_of(a, min(b, a.B - 1), false);
+      s.u = request_of(a, min(b, a.B - 1), false);
       for (bool more = true; more && ok; ++seg) {
         s.steps = 0;
-        while (LISTS && at < stop && b < requests) {
-          const RowBlock& r = lists.blocks[b];
-          if (r.weight == 0 || at >= before + r.weight) {
-            before += r.weight;
-            ++b;
-            continue;
-          }
-          s.u = Unit{r.row0, r.n_new, r.past, r.full, r.tail, r.pages, r.items, r.weight};
-          const Part x = part_of(s.u, at - before, stop - at);
-          at += x.took;
-          if (x.from >= x.to) continue;
-          if (x.from == 0 && x.to < s.u.items)
-            open = record_of(s.u, r.h, r.first_row, pl.total, before + s.u.weight, cta, ctas);
-          s.b = r.b;
-          s.h = r.h;
-          s.first_row = r.first_row;
-          place = r.place;
-          s.from = x.from;
-          s.to = x.to;
-          s.steps = (x.to - x.from + 1) / 2;
-          s.limit0 = s.u.items;
-          s.limit1 = r.n_new * a.G - r.first_row > kTile ? s.u.items : 0;
-          break;
-        }
-        while (!LISTS && at < stop && b < a.B) {
+        while (at < stop && b < a.B) {
           set_rows(a, s.u, block * kBlockRows, kBlockRows, topk);
           if (s.u.weight == 0) {  // the request has no more rows
             if (++b < a.B) s.u = request_of(a, b, false);
@@ -983,7 +908,6 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
         ok = ok && mbar_wait(smem_u32(&sm.seg_empty[seg % kSegments]), (seg / kSegments & 1) ^ 1, abort, a.err);
         if (!ok) break;
         sm.segs[seg % kSegments] = s;
-        if constexpr (LISTS) sm.places[seg % kSegments] = place;
         mbar_arrive(smem_u32(&sm.seg_full[seg % kSegments]));
       }
       records[cta] = open;
@@ -1003,30 +927,15 @@ kv8_prefill_kernel(const Kv8Args a, const Rows q, const Rows out, float scale, c
 
 int64_t kv8_prefill_workspace() { return (int64_t)2 * kMaxCtas * kBlockRows * kPartialStride * 4; }
 
-namespace {
-
-template <bool LISTS>
-cudaError_t launch(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const int32_t* sel, int topk,
-                   const RowLists& lists, void* workspace, int sm_count, cudaStream_t st) {
-  const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
-  cudaError_t e = cudaFuncSetAttribute(kv8_prefill_kernel<LISTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<LISTS>);
-  if (e != cudaSuccess) return e;
-  e = launch_early(kv8_prefill_kernel<LISTS>, dim3((unsigned)ctas), kThreads, kSmemBytes<LISTS>, st, a, q, out, scale, sel, topk,
-                   static_cast<JoinRecord*>(workspace), reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes), lists);
-  if (e != cudaSuccess || ctas == 1) return e;
-  return launch_kv8_join(a, out, ctas, 16, workspace, kBlockRows, st);
-}
-
-}  // namespace
-
 cudaError_t launch_kv8_prefill(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const int32_t* sel,
                                int topk, void* workspace, int sm_count, cudaStream_t st) {
-  return launch<false>(a, q, out, scale, sel, topk, RowLists{}, workspace, sm_count, st);
-}
-
-cudaError_t launch_kv8_prefill_lists(const Kv8Args& a, const Rows& q, const Rows& out, float scale, const RowLists& lists,
-                                     void* workspace, int sm_count, cudaStream_t st) {
-  return launch<true>(a, q, out, scale, nullptr, 0, lists, workspace, sm_count, st);
+  const int ctas = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+  cudaError_t e = cudaFuncSetAttribute(kv8_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  e = launch_early(kv8_prefill_kernel, dim3((unsigned)ctas), kThreads, kSmemBytes, st, a, q, out, scale, sel, topk,
+                   static_cast<JoinRecord*>(workspace), reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kRecordBytes));
+  if (e != cudaSuccess || ctas == 1) return e;
+  return launch_kv8_join(a, out, ctas, 16, workspace, kBlockRows, st);
 }
 
 }  // namespace spin

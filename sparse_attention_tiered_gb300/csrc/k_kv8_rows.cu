@@ -1,11 +1,8 @@
 // spin_kv8_attend_rows: attention where every token has its own list of pages.
 //
 // One token a request: its list goes to the few-row kernel as it is, but in order and without pages twice. More than one:
-// neighbouring tokens list much the same pages, so a block of 256 rows attends the pages that any of its tokens lists, with
-// the many-row kernel, in which a row that does not list a page has weights of 0 there and a warp of 32 such rows passes
-// it over. A launch before makes the blocks' lists. (A token at a time, the few-row kernel takes 720 clocks a
-// page and token; a block takes 2500 a page for all of its tokens. 32 tokens with 32 pages each list 60 to 210 pages
-// between them if neighbours have 0.97 or 0.9 of their likes in common, and 430 of 480 if nothing.)
+// blocks of rows attend the pages that any of their tokens lists (k_kv8_lists.cu). The lists are made here, by a launch
+// before. (A token at a time, the few-row kernel takes 720 clocks a page and token.)
 #include "kv8_rows.cuh"
 
 namespace spin {
@@ -17,6 +14,7 @@ using namespace kv8;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kWindow = 2048;  // pages that are marked at a time
+constexpr int kUnitSteps = 8;  // steps that beginning and ending a block costs
 
 // A CTA a block and head. The tokens' pages are marked in a window of shared memory, a bit a token, and read out in order;
 // what lies beyond the window waits for the next, which begins at the lowest page that is left.
@@ -24,7 +22,7 @@ __global__ void __launch_bounds__(kThreads)
 kv8_rows_blocks(const Kv8Args a, const Rows out, const int32_t* sel, int topk, int64_t cap, RowLists s) {
   __shared__ __align__(16) uint32_t marks[2][kWindow];
   __shared__ int64_t scratch[36];
-  __shared__ int found[kWarps], next[kWarps], most[kWarps];
+  __shared__ int found[kWarps][2], next[kWarps], most[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = list_rows(a.G);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -51,12 +49,16 @@ kv8_rows_blocks(const Kv8Args a, const Rows out, const int32_t* sel, int topk, i
   t.reserved2 = 0;
   t.place = (int64_t)blockIdx.x * cap;
   const int i0 = t.first_row / a.G, tokens = t.n_new - i0;
+  // Tokens that have rows in the first tile of 128, [0, in0), and in the second, from from1 on.
+  const int skip = t.first_row - i0 * a.G, rows = min(R, t.n_new * a.G - t.first_row);
+  t.shared = rows <= kTileRows;
+  const int in0 = min(tokens, (kTileRows - 1 + skip) / a.G + 1), from1 = (kTileRows + skip) / a.G;
   const int64_t unit = (int64_t)t.b * a.Hkv + h;
   const int32_t* table = a.table + unit * a.max_pages;
   const int32_t* lists = sel + ((int64_t)(row0 + i0) * a.Hkv + h) * topk;
   const int64_t step = (int64_t)a.Hkv * topk;
   RowItem* items = s.items + t.place;
-  int count = 0;
+  int count[2] = {0, 0};  // pages of each tile; shared: of the block, the first alone
   for (int base = 0; base != 0x7fffffff;) {
     for (int x = tid * 4; x < 2 * kWindow; x += 4 * kThreads) *reinterpret_cast<uint4*>(marks[0] + x) = make_uint4(0, 0, 0, 0);
     __syncthreads();
@@ -94,27 +96,48 @@ kv8_rows_blocks(const Kv8Args a, const Rows out, const int32_t* sel, int topk, i
           there = false;
         }
       }
-      const uint32_t vote = __ballot_sync(0xffffffffu, there);
-      if (lane == 0) found[warp] = __popc(vote);
-      __syncthreads();
-      int at = count + __popc(vote & ((1u << lane) - 1u));
+      // For the tiles that have such tokens.
+      const uint64_t who = (uint64_t)it.tokens[1] << 32 | it.tokens[0];
+      const bool in[2] = {there && (t.shared || (who & (in0 < 64 ? (1ull << in0) - 1 : ~0ull)) != 0), there && !t.shared && from1 < 64 && who >> from1 != 0};
+      uint32_t vote[2];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) at += found[w];
-        count += found[w];
+      for (int k = 0; k < 2; ++k) {
+        vote[k] = __ballot_sync(0xffffffffu, in[k]);
+        if (lane == 0) found[warp][k] = __popc(vote[k]);
       }
-      if (there && at < cap) *reinterpret_cast<uint4*>(items + at) = make_uint4(it.page, it.number, it.tokens[0], it.tokens[1]);
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        int at = count[k] + __popc(vote[k] & ((1u << lane) - 1u));
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) at += found[w][k];
+          count[k] += found[w][k];
+        }
+        at = t.shared ? at : 2 * at + k;
+        if (in[k] && at < cap) *reinterpret_cast<uint4*>(items + at) = make_uint4(it.page, it.number, it.tokens[0], it.tokens[1]);
+      }
       __syncthreads();
     }
     base = beyond;
     __syncthreads();
   }
-  t.pages = count;
-  t.items = count + (t.tail && past + t.n_new > t.full * kPart ? 1 : 0);
-  t.weight = t.items ? t.items + unit_cost(2 * kTileRows, t.n_new * a.G - t.first_row) : 0;
+  // The tail is the last page of every tile that sees some of it; then what is missing to whole steps.
+  const int first_sees = past + i0 + in0;  // what the first tile's last token sees
+  if (tid < 2 && !(t.shared && tid)) {
+    const bool sees = t.tail && (t.shared || tid ? past + t.n_new : first_sees) > t.full * kPart;
+    const int at = t.shared ? count[0] : 2 * count[tid] + tid;
+    if (sees && at < cap) *reinterpret_cast<uint4*>(items + at) = make_uint4((uint32_t)kTailItem, t.full, 0xffffffffu, 0xffffffffu);
+  }
+  if (t.tail && past + t.n_new > t.full * kPart) ++count[t.shared ? 0 : 1];
+  if (!t.shared && t.tail && first_sees > t.full * kPart) ++count[0];
+  t.steps = t.shared ? (count[0] + 1) / 2 : max(count[0], count[1]);
+  t.weight = t.steps ? t.steps + kUnitSteps : 0;
+  for (int x = (t.shared ? count[0] : 2 * min(count[0], count[1])) + tid; x < 2 * t.steps; x += kThreads)
+    if ((t.shared || x >> 1 >= count[x & 1]) && x < cap)
+      *reinterpret_cast<uint4*>(items + x) = make_uint4((uint32_t)kNoItem, 0, 0, 0);
   if (tid == 0) s.blocks[blockIdx.x] = t;
-  if (t.items == 0) {  // its rows see nothing
-    const int rows = min(R, t.n_new * a.G - t.first_row);
+  if (t.steps == 0) {  // its rows see nothing
     for (int x = tid; x < rows * 16; x += kThreads) {
       const int row = t.first_row + (x >> 4), i = row / a.G;
       reinterpret_cast<uint4*>(out.p + (int64_t)(row0 + i) * out.ts + (int64_t)(h * a.G + row - i * a.G) * out.hs)[x & 15] =
@@ -175,7 +198,7 @@ int64_t most_blocks(const Kv8Args& a) {  // of each head
 
 int64_t most_items(const Kv8Args& a, int topk) {  // of a block
   const int64_t n = (int64_t)list_tokens(a.G) * (topk + 1);
-  return n < a.max_pages ? n : a.max_pages;
+  return 2 * ((n < a.max_pages ? n : a.max_pages) + 1);  // of each tile, and the tail
 }
 
 }  // namespace
@@ -201,7 +224,7 @@ cudaError_t launch_kv8_rows(const Kv8Args& a, const Rows& q, const Rows& out, fl
   s.items = reinterpret_cast<RowItem*>(s.blocks + blocks);
   const cudaError_t e = launch_early(kv8_rows_blocks, dim3((unsigned)blocks), kThreads, 0, st, a, out, sel, topk,
                                      most_items(a, topk), s);
-  return e != cudaSuccess ? e : launch_kv8_prefill_lists(a, q, out, scale, s, workspace, sm_count, st);
+  return e != cudaSuccess ? e : launch_kv8_lists(a, q, out, scale, s, workspace, sm_count, st);
 }
 
 }  // namespace spin
