@@ -60,7 +60,7 @@ struct alignas(16) StepMeta {
 
 struct Smem {
   uint64_t seg_full[kSegments], seg_empty[kSegments];
-  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2], pv_done[2];
+  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2], pv_done[2][2];
   StepMeta meta[4];  // by step mod 4: the loaders are at most that far ahead of a softmax warp
   Segment segs[kSegments];
   int64_t scratch[36];
@@ -131,7 +131,8 @@ kv8_lists_attend(const Kv8Args a, const Rows q, const Rows out, float scale, con
       mbar_init(smem_u32(&sm.v_empty[i]), 1);
       mbar_init(smem_u32(&sm.s_full[i][0]), 1);
       mbar_init(smem_u32(&sm.s_full[i][1]), 1);
-      mbar_init(smem_u32(&sm.pv_done[i]), 1);
+      mbar_init(smem_u32(&sm.pv_done[i][0]), 1);
+      mbar_init(smem_u32(&sm.pv_done[i][1]), 1);
     }
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -285,7 +286,7 @@ kv8_lists_attend(const Kv8Args a, const Rows q, const Rows out, float scale, con
         auto rescale = [&](float f) {
           L *= f;
           if (turn == 0) return;
-          warp_wait(ok, smem_u32(&sm.pv_done[tile]), (c - 1) & 1, abort, a.err);
+          warp_wait(ok, smem_u32(&sm.pv_done[tile][(c - 1) & 1]), (c - 1) >> 1 & 1, abort, a.err);
           if (!ok) return;
           tmem_after();
           uint32_t y[8];
@@ -385,10 +386,8 @@ kv8_lists_attend(const Kv8Args a, const Rows q, const Rows out, float scale, con
 
       // ---- the row's end ----
       if (poison) L = __uint_as_float(0x7fc00000u);
-      // The last two products: of the second last nothing has been heard yet, and a barrier says only whether the last phase or
-      // the one before is over.
-      warp_wait(ok, smem_u32(&sm.pv_done[tile]), count & 1, abort, a.err);
-      warp_wait(ok, smem_u32(&sm.pv_done[tile]), (count - 1) & 1, abort, a.err);
+      // (The second last product may be done or not: with a barrier for both, neither phase could be waited for.)
+      warp_wait(ok, smem_u32(&sm.pv_done[tile][(count - 1) & 1]), (count - 1) >> 1 & 1, abort, a.err);
       tmem_after();
       // Rows go through the warp's own rows of Q, which no product reads any more, so that they are stored in
       // runs of whole rows: 16-byte chunk c of row r at c ^ (r & 7), as everywhere.
@@ -690,7 +689,7 @@ kv8_lists_attend(const Kv8Args a, const Rows q, const Rows out, float scale, con
         else mma_ts<false>(leader, d, p, v0, shape(kD, true));
 #pragma unroll
         for (int k = 1; k < 4; ++k) mma_ts<true>(leader, d, p + k * 8, v0 + k * (2048 >> 4), shape(kD, true));
-        mma_commit(leader, smem_u32(&sm.pv_done[t]));
+        mma_commit(leader, smem_u32(&sm.pv_done[t][c & 1]));
       };
       constexpr std::integral_constant<int, 0> kTile0;
       constexpr std::integral_constant<int, 1> kTile1;

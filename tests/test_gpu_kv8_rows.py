@@ -243,6 +243,22 @@ def test_results_do_not_change_from_run_to_run():
         assert torch.equal(c.run(), first)
 
 
+@pytest.mark.parametrize("group,new", [(8, 96), (16, 9), (8, 20)])
+def test_many_calls_in_a_row(group, new):
+    """Blocks of many and of few steps, shared and not, on CTAs that are never in the same state: no wait runs out."""
+    c = Case(2, group, [2500, 300, 64], [new, 7, 2], 16, lists="near", seed=new)
+    first = c.run()
+    st, _ = step_of(c.past, c.new)
+    q, sel = c.q.cuda(), c.sel.cuda()
+    outs = [torch.zeros_like(q) for _ in range(16)]
+    for n in range(400):
+        c.c.attend_rows(st, q, outs[n % 16], sel)
+    torch.cuda.synchronize()
+    c.c.check()
+    for out in outs:
+        assert torch.equal(out.cpu(), first)
+
+
 def test_streams_and_graphs():
     c = Case(2, 4, [900, 1700], [3, 1], 6, seed=4)
     first = c.run()
