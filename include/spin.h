@@ -483,7 +483,7 @@ int spin_kv8_reserve(const spin_kv8* cache, const spin_kv8_step* step, int32_t* 
  * distinct). src[b] = b: stays as it is; src[b] = -1: becomes empty. len follows. A request that changes drops all
  * of its entries, and names the complete pages of its source: they are shared, and free again
  * once nobody names them. Its tail rows 0 .. len % 64 - 1 are copied (later rows are left as they are), and where the
- * cache has summaries, those of pages that the two did not share before. Pages that the source has reserved and
+ * cache has summaries, those of its complete pages. Pages that the source has reserved and
  * not completed stay its own. A request whose src, or whose source's len, is out of range stays as it is, and
  * the error word says so. */
 int spin_kv8_fork(const spin_kv8* cache, int32_t* refs, int32_t* len, const int32_t* src, spin_stream_t stream);

@@ -263,12 +263,10 @@ kv8_pool_move(const Kv8Args a, int32_t* refs, PoolSpace s, int32_t* free_pages) 
 // ---------------------------------------------------------------------------
 // Forking. Requests' rows change places among themselves, in place: a CTA takes a range of columns of all moved
 // requests, reads every source into registers, and only then writes. No copy of the rows has to be kept anywhere, and
-// any map of requests to requests will do. Of the summaries only those go that belong to another page than the one that
-// the entry names already (beams that part late share nearly all of theirs).
+// any map of requests to requests will do. Summaries go along whichever page an entry named before.
 // ---------------------------------------------------------------------------
 constexpr int kForkThreads = 512;
 constexpr int kHeld = 32;         // 32-bit registers a thread, of the columns that pass through it
-constexpr int kColumns = 8;       // pages of an item
 constexpr int kMostRows = kHeld / 4 * kForkThreads;  // that a CTA can hold 16 bytes each of
 
 struct Move {
@@ -303,15 +301,17 @@ __device__ __forceinline__ int log_width(int moves, int most) {  // lanes a row:
 }
 
 template <typename E>
-__device__ void copy_columns(const Kv8Args& a, const Move* moves, int n_moves, const uint8_t* need, float* base, int64_t stride,
-                             int64_t off, int bytes, int page0) {
-  // base + b * stride + off .. + bytes of all moves' requests, where bit (byte / 512) of need[m] is set
+__device__ void copy_summaries(const Kv8Args& a, const Move* moves, int n_moves, int h, int page0, int bytes) {
+  // head h's rows from page0 on, `bytes` of them, of all moves' requests, as far as the source has pages that are whole
+  const int64_t stride = (int64_t)a.Hkv * a.max_pages * kD * 4, off = ((int64_t)h * a.max_pages + page0) * kD * 4;
   const int lw = log_width<E>(n_moves, bytes / (int)sizeof(E));
   for (int x = 0; x < bytes; x += (int)sizeof(E) << lw) {
     __syncthreads();
-    auto there = [&](int m, int c) { return need[m] >> ((x + c * (int)sizeof(E)) >> 9) & 1; };
+    auto there = [&](int m, int c) {
+      return moves[m].from >= 0 && page0 + (x + c * (int)sizeof(E)) / (kD * 4) < moves[m].len / kPart;
+    };
     auto at = [&](int b, int c) {
-      return reinterpret_cast<E*>(reinterpret_cast<uint8_t*>(base) + b * stride + off + x + c * (int64_t)sizeof(E));
+      return reinterpret_cast<E*>(reinterpret_cast<uint8_t*>(a.summaries) + b * stride + off + x + c * (int64_t)sizeof(E));
     };
     pass<E>(
         n_moves, lw, [&](int m, int c) { return there(m, c) ? *at(moves[m].from, c) : E{}; },
@@ -343,12 +343,11 @@ constexpr int kTailBytes = 2048;  // of an item
 // MANY: batches of more requests than a CTA can hold 16 bytes each of.
 template <bool MANY>
 __global__ void __launch_bounds__(kForkThreads, MANY ? 1 : 2)
-kv8_pool_fork(const Kv8Args a, int32_t* refs, const int32_t* len, const int32_t* src) {
-  extern __shared__ Move moves[];  // [B], and a byte each
-  __shared__ int n_moves;
+kv8_pool_fork(const Kv8Args a, int32_t* refs, const int32_t* len, const int32_t* src, int log_columns) {
+  extern __shared__ Move moves[];  // [B]
+  __shared__ int n_moves, most_pages;
   const int tid = threadIdx.x;
-  uint8_t* need = reinterpret_cast<uint8_t*>(moves + a.B);
-  if (tid == 0) n_moves = 0;
+  if (tid == 0) n_moves = most_pages = 0;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
@@ -367,13 +366,14 @@ kv8_pool_fork(const Kv8Args a, int32_t* refs, const int32_t* len, const int32_t*
       continue;
     }
     moves[atomicAdd(&n_moves, 1)] = Move{b, from, n};
+    atomicMax(&most_pages, n / kPart);
   }
   __syncthreads();
   const int n = n_moves;
   if (n == 0) return;
   constexpr int kEntries = MANY ? kHeld : kHeld / 4;  // table entries that a thread holds
   const bool narrow = MANY && n > kMostRows;
-  const int groups = (a.max_pages + kColumns - 1) / kColumns, tail_items = kPageElems * 2 / kTailBytes;
+  const int columns = 1 << log_columns, groups = (a.max_pages + columns - 1) / columns, tail_items = kPageElems * 2 / kTailBytes;
   const int64_t items = (int64_t)a.Hkv * (groups + tail_items);
   int32_t* table = const_cast<int32_t*>(a.table);
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
@@ -387,12 +387,11 @@ kv8_pool_fork(const Kv8Args a, int32_t* refs, const int32_t* len, const int32_t*
       if (!narrow) copy_tails<uint4>(a, moves, n, off, kTailBytes);
       continue;
     }
-    const int p0 = (g - tail_items) * kColumns, pages = min(kColumns, a.max_pages - p0);
+    const int p0 = (g - tail_items) * columns, pages = min(columns, a.max_pages - p0);
     auto entry = [&](int b, int p) { return table + ((int64_t)b * a.Hkv + h) * a.max_pages + p; };
-    // Entries: 8 of a request at a time, fewer where there are too many requests. Sources are read before any entry is written.
-    int lw = 3;
+    // Entries: all of an item's of a request at a time, fewer where there are too many requests. Sources are read before any entry is written.
+    int lw = log_columns;
     while (lw > 0 && (int64_t)n << lw > kEntries * kForkThreads) --lw;
-    bool some = false;
     for (int x = 0; x < pages; x += 1 << lw) {
       __syncthreads();
       int32_t v[kEntries];
@@ -400,19 +399,8 @@ kv8_pool_fork(const Kv8Args a, int32_t* refs, const int32_t* len, const int32_t*
       for (int k = 0; k < kEntries; ++k) {
         if (k * kForkThreads >= n << lw) break;
         const int i = tid + k * kForkThreads, m = i >> lw, c = i & ((1 << lw) - 1), p = p0 + x + c;
-        bool differs = false;
         v[k] = -1;
-        if (m < n && p < a.max_pages) {
-          const Move mv = moves[m];
-          const int old = *entry(mv.to, p);
-          if (mv.from >= 0 && p < mv.len >> 6) {
-            v[k] = *entry(mv.from, p);
-            differs = v[k] != old;
-          }
-        }
-        const uint32_t bits = __ballot_sync(0xffffffffu, differs) >> (tid & 31 & ~((1 << lw) - 1)) & ((1u << (1 << lw)) - 1u);
-        if (m < n && c == 0) need[m] = (uint8_t)(x ? need[m] | bits << x : bits);
-        some |= differs;
+        if (m < n && p < a.max_pages && moves[m].from >= 0 && p < moves[m].len / kPart) v[k] = *entry(moves[m].from, p);
       }
       __syncthreads();
 #pragma unroll
@@ -434,12 +422,11 @@ kv8_pool_fork(const Kv8Args a, int32_t* refs, const int32_t* len, const int32_t*
         }
       }
     }
-    if (a.summaries && __syncthreads_or(some)) {
-      const int64_t stride = (int64_t)a.Hkv * a.max_pages * kD * 4, off = ((int64_t)h * a.max_pages + p0) * kD * 4;
+    if (a.summaries && p0 < most_pages) {
       if constexpr (MANY) {
-        if (narrow) copy_columns<uint32_t>(a, moves, n, need, a.summaries, stride, off, pages * kD * 4, p0);
+        if (narrow) copy_summaries<uint32_t>(a, moves, n, h, p0, pages * kD * 4);
       }
-      if (!narrow) copy_columns<uint4>(a, moves, n, need, a.summaries, stride, off, pages * kD * 4, p0);
+      if (!narrow) copy_summaries<uint4>(a, moves, n, h, p0, pages * kD * 4);
     }
   }
 }
@@ -500,15 +487,21 @@ cudaError_t launch_kv8_compact(const Kv8Args& a, int32_t* refs, int32_t* free_pa
 }
 
 cudaError_t launch_kv8_fork(const Kv8Args& a, int32_t* refs, int32_t* len, const int32_t* src, int sm_count, cudaStream_t st) {
-  const size_t bytes = (size_t)a.B * (sizeof(Move) + 1);
+  const size_t bytes = (size_t)a.B * sizeof(Move);
   const bool many = a.B > kMostRows;
   cudaError_t e = many ? shared_bytes(reinterpret_cast<const void*>(kv8_pool_fork<true>), bytes)
                        : shared_bytes(reinterpret_cast<const void*>(kv8_pool_fork<false>), bytes);
   if (e != cudaSuccess) return e;
-  const int64_t items = (int64_t)a.Hkv * ((a.max_pages + kColumns - 1) / kColumns + kPageElems * 2 / kTailBytes);
+  // Pages of an item: 8, or 4 or 2 where the GPU could not be filled by items of 8. (64 of 128 requests of 15 to 125 pages:
+  // 18.5 us with 2 or 4, 20.6 with 8; of 7 to 15 pages 13.0, 13.3 and 18.6; 7 of 8 requests of 469 pages: 23.9 with 2, 18.4 with 4,
+  // 14.8 with 8.)
+  int log_columns = 3;
+  auto groups = [&] { return (int64_t)a.Hkv * ((a.max_pages + (1 << log_columns) - 1) >> log_columns); };
+  while (log_columns > 1 && groups() < (int64_t)sm_count * 2) --log_columns;
+  const int64_t items = groups() + (int64_t)a.Hkv * (kPageElems * 2 / kTailBytes);
   const int32_t* lengths = len;
-  e = many ? launch_early(kv8_pool_fork<true>, dim3(at_most(items, sm_count)), kForkThreads, bytes, st, a, refs, lengths, src)
-           : launch_early(kv8_pool_fork<false>, dim3(at_most(items, (int64_t)sm_count * 2)), kForkThreads, bytes, st, a, refs, lengths, src);
+  e = many ? launch_early(kv8_pool_fork<true>, dim3(at_most(items, sm_count)), kForkThreads, bytes, st, a, refs, lengths, src, log_columns)
+           : launch_early(kv8_pool_fork<false>, dim3(at_most(items, (int64_t)sm_count * 2)), kForkThreads, bytes, st, a, refs, lengths, src, log_columns);
   if (e != cudaSuccess) return e;
   return launch_early(kv8_pool_lengths, dim3(1), 1024, 0, st, a, len, src);
 }

@@ -57,7 +57,7 @@ class Pool:
                     if new >= 0:
                         self.refs[new] += 1
                     self.table[b][h][p] = new
-                    if sums and a >= 0 and p < n // PAGE and mine != new:
+                    if sums and a >= 0 and p < n // PAGE:
                         self.summaries[b][h][p] = sums[a][h][p]
                 if tails and a >= 0:
                     for half in (0, 1):
