@@ -12,8 +12,15 @@
 // A chain of 8 products on one accumulator takes 760 clocks however few columns it has, so a tile has two places for scores, and
 // those of the step after next are made under a step's softmax. (A tile may so be done with two steps before the products'
 // warp has looked for the first: what is done has a barrier for each place.)
-// Roles, by warp: 0-3, 4-7 softmax of tile 0 and 1, a row a thread; 8-11 keys to fp16 in shared memory, loads one step
-// ahead in registers; 12-15 values; 16 the products; 17 walks the CTA's share of the work.
+// Roles, by warp: 0-3, 4-7 softmax of tile 0 and 1, a row a thread; 8-11 keys to fp16 in shared memory; 12-15 values; 16 the
+// products; 17 walks the CTA's share of the work. A loader warp copies its 2 KB of a step's pages to shared memory in bulk, takes
+// them into registers as soon as they are there, and has the next step's under way while it waits, converts and stores.
+//
+// A step of two pages takes some 2,350 clocks where nothing else is in the way (96 more pages a tile on 512 blocks of 152 CTAs:
+// 400 us). The products alone take 1,430 and the exponents and conversions, at 32 a clock, 1,280; what they share is the shared memory, 256 KB a
+// step at 128 bytes a clock: Q for the scores 64 KB, K and V 64, their stores 64, the codes in and out 64. (Conversions made five times
+// cheaper change nothing. With loads straight into registers the chunk of 2048 tokens onto 30000 takes the same 514 us, and five
+// drafts of 16 requests, whose pages come from HBM, 79 us instead of 70.)
 //
 // A row that does not list the page of a step has an exponent of -infinity there, and a warp of 32 such rows stores zeros
 // and goes on. Which pages those are costs two shared loads and a vote a step.
@@ -61,6 +68,7 @@ struct alignas(16) StepMeta {
 struct Smem {
   uint64_t seg_full[kSegments], seg_empty[kSegments];
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2], pv_done[2][2];
+  uint64_t codes[2][4][2];  // of keys and values, by loader warp: its rows of each tile's page are there
   StepMeta meta[4];  // by step mod 4: the loaders are at most that far ahead of a softmax warp
   Segment segs[kSegments];
   int64_t scratch[36];
@@ -70,8 +78,10 @@ struct Smem {
 
 constexpr size_t kQBytes = (size_t)kBlockRows * kD * 2;  // 64 KB: [tile][2 planes][128 rows][128 bytes]
 constexpr size_t kKvBytes = (size_t)2 * kPlane;          // 64 KB each
-constexpr size_t kSmemBytes = 1024 + kQBytes + 2 * kKvBytes + sizeof(Smem);
-static_assert(kSmemBytes + 1024 <= 196 * 1024, "the next size of the SM's shared memory leaves the L1 too small for the loads");
+constexpr int kRun = 16 * kD;                             // bytes of codes: a loader warp's rows of a page
+constexpr size_t kCodeBytes = 2 * 4 * 2 * kRun;            // 32 KB: [keys, values][warp][page]
+constexpr size_t kSmemBytes = 1024 + kQBytes + 2 * kKvBytes + kCodeBytes + sizeof(Smem);
+static_assert(kSmemBytes <= 227 * 1024, "a CTA has 227 KB");
 
 // fp16 x fp16 -> fp32, M = 128; b_rows_depth: B is stored with its depth as rows.
 constexpr uint32_t shape(int n, bool b_rows_depth) {
@@ -111,7 +121,7 @@ kv8_lists_attend(const Kv8Args a, const Rows q, const Rows out, float scale, con
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + (-smem_u32(smem_raw) & 1023u);
   const uint32_t sq = smem_u32(base), sk = sq + (uint32_t)kQBytes, sv = sk + (uint32_t)kKvBytes;
-  Smem& sm = *reinterpret_cast<Smem*>(base + kQBytes + 2 * kKvBytes);
+  Smem& sm = *reinterpret_cast<Smem*>(base + kQBytes + 2 * kKvBytes + kCodeBytes);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   volatile int* abort = &sm.abort;
   const int ctas = gridDim.x, cta = blockIdx.x;
@@ -133,6 +143,7 @@ kv8_lists_attend(const Kv8Args a, const Rows q, const Rows out, float scale, con
       mbar_init(smem_u32(&sm.s_full[i][1]), 1);
       mbar_init(smem_u32(&sm.pv_done[i][0]), 1);
       mbar_init(smem_u32(&sm.pv_done[i][1]), 1);
+      for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&sm.codes[i][w][0]), 1), mbar_init(smem_u32(&sm.codes[i][w][1]), 1);
     }
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -158,11 +169,11 @@ kv8_lists_attend(const Kv8Args a, const Rows q, const Rows out, float scale, con
     warp_wait(ok, smem_u32(&sm.seg_full[seg % kSegments]), seg / kSegments & 1, abort, a.err);
     return ok && sm.segs[seg % kSegments].from < sm.segs[seg % kSegments].to;
   };
-  // 640 threads x 96 registers at launch = 256 x 128 + 256 x 80 + 128 x 64.
+  // 640 threads x 96 registers at launch = 256 x 120 + 256 x 88 + 128 x 64.
 
   if (warp < kKeyWarp) {
     // ------------------------------ softmax, a row a thread ------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     const int tile = warp >> 2, quad = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t S0 = lanes + kColS + tile * kTile, O = lanes + kColO + tile * kTile;
@@ -504,10 +515,14 @@ kv8_lists_attend(const Kv8Args a, const Rows q, const Rows out, float scale, con
   } else if (warp < kMmaWarp) {
     // ------------------------------ loaders: four warps of keys, four of values ------------------------------
     // Warp w has rows 16 w .. 16 w + 15 of every page. In load x, eight lanes have 64 bytes of two neighbouring
-    // rows each: their 16-byte stores then fall on eight different columns of the swizzle.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // rows each, the odd row's from its other half, so that both the loads and the 16-byte stores fall on
+    // eight different columns.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     const int half = warp >= kValueWarp ? 1 : 0;
-    const int w4 = warp & 3, c4 = lane & 3, row0 = w4 * 16 + (lane >> 3) * 2 + (lane >> 2 & 1);
+    const int w4 = warp & 3, c4 = lane & 3, odd = lane >> 2 & 1, row0 = (lane >> 3) * 2 + odd;
+    const uint32_t run = sv + (uint32_t)kKvBytes + (half * 4 + w4) * 2 * kRun;
+    uint64_t* codes = sm.codes[half][w4];
+    uint32_t turn = 0;  // bit per page: the parity of its next codes
     const uint32_t operand0 = half ? sv : sk;
     uint64_t* full = half ? sm.v_full : sm.k_full;
     uint64_t* empty = half ? sm.v_empty : sm.k_empty;
@@ -519,7 +534,8 @@ kv8_lists_attend(const Kv8Args a, const Rows q, const Rows out, float scale, con
       const RowItem* items = lists.items + u.place;
       const int end = 2 * s.to;
       int id = -1, pos = -1, id_base = 2 * s.from;
-      // Page ids of 32 items, a lane each, and for the keys' warps what the softmax has to know of the pages.
+      // Page ids of 32 items, a lane each (the last two are looked up again with the next), and for the keys' warps
+      // what the softmax has to know of the pages.
       float kfac = 0.f, vlog = 0.f, vinv = 1.f;
       bool bad = false;
       uint32_t who[2] = {0, 0};  // tokens that list the page
@@ -547,21 +563,28 @@ kv8_lists_attend(const Kv8Args a, const Rows q, const Rows out, float scale, con
           }
         }
       };
-      uint4 raw[8];  // of two pages, four loads each
-      auto load = [&](int it, int pg) {
-        const int page = __shfl_sync(0xffffffffu, id, it - id_base);
-        const uint8_t* src = a.pages + (int64_t)page * kKv8PageBytes + half * kKv8HalfBytes + row0 * kD + c4 * 16;
+      // The codes of a page come in one copy, which is under way again as soon as they are in registers.
+      uint4 raw[8];
+      auto load = [&](int pg, int page) {
+        if (page < 0 || lane) return;
+        mbar_arrive_expect_tx(smem_u32(&codes[pg]), kRun);
+        bulk_copy(run + pg * kRun, a.pages + (int64_t)page * kKv8PageBytes + half * kKv8HalfBytes + w4 * kRun, kRun, smem_u32(&codes[pg]));
+      };
+      auto take = [&](int pg, int page) {
+        if (page >= 0) {
+          warp_wait(ok, smem_u32(&codes[pg]), turn >> pg & 1, abort, a.err);
+          turn ^= 1u << pg;
+        }
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          raw[pg * 4 + x] = page >= 0 ? __ldcg(reinterpret_cast<const uint4*>(src + (x >> 1) * 8 * kD + (x & 1) * 64))
-                                      : make_uint4(0, 0, 0, 0);
+          raw[pg * 4 + x] = page >= 0 ? lds128(run + pg * kRun + (row0 + (x >> 1) * 8) * kD + ((x & 1) ^ odd) * 64 + c4 * 16) : make_uint4(0, 0, 0, 0);
       };
       auto put_page = [&](uint32_t at, int pg) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int row = row0 + (x >> 1) * 8;
+          const int row = w4 * 16 + row0 + (x >> 1) * 8;
           const uint4 v = raw[pg * 4 + x];
-          const uint32_t dst = at + (x & 1) * kPlane + (pg * kPart + row) * 128;
+          const uint32_t dst = at + ((x & 1) ^ odd) * kPlane + (pg * kPart + row) * 128;
           sts128(dst + (((c4 * 2 + 0) ^ (row & 7)) << 4), e4m3x2_half2(v.x, false), e4m3x2_half2(v.x, true),
                  e4m3x2_half2(v.y, false), e4m3x2_half2(v.y, true));
           sts128(dst + (((c4 * 2 + 1) ^ (row & 7)) << 4), e4m3x2_half2(v.z, false), e4m3x2_half2(v.z, true),
@@ -617,43 +640,52 @@ kv8_lists_attend(const Kv8Args a, const Rows q, const Rows out, float scale, con
         }
       };
       look(2 * s.from);
-      load(2 * s.from, 0);
-      load(2 * s.from + 1, 1);
-      for (int it = 2 * s.from; it < end; it += 2, ++count) {
+      auto id_of = [&](int it) { return __shfl_sync(0xffffffffu, id, it - id_base); };
+      int id0 = id_of(2 * s.from), id1 = id_of(2 * s.from + 1);
+      load(0, id0);
+      load(1, id1);
+      for (int it = 2 * s.from; it < end && ok; it += 2, ++count) {
         const uint32_t slot = count & 1, at = operand0 + slot * 16384;
         StepMeta& me = sm.meta[count & 3];
-        warp_wait(ok, smem_u32(&empty[slot]), (count >> 1 & 1) ^ 1, abort, a.err);
-        if (ok) {
-          const int x = lane - (it - id_base);
-          if (!half && (x & ~1) == 0) {  // what the softmax has to know of the pages
-            if (id != kTailItem) {
-              me.kfac[x * 4 + w4] = kfac;
-              me.vlog[x * 4 + w4] = vlog;
-              me.vinv[x * 4 + w4] = vinv;
-              me.bad_keys[x * 4 + w4] = bad ? 0xffffu : 0u;
-            }
-            if (w4 == 0) {
-              me.tail[x] = id == kTailItem;
-              me.count[x] = id == kTailItem ? u.tail : id >= 0 ? kPart : 0;
-              me.pos[x] = pos;
-              me.tokens[x][0] = who[0];
-              me.tokens[x][1] = who[1];
-            }
-          }
-          const int id0 = __shfl_sync(0xffffffffu, id, it - id_base), id1 = __shfl_sync(0xffffffffu, id, it + 1 - id_base);
-          // The next step's loads, each as soon as its registers are free.
-          const bool more = it + 2 < end;
-          if (more && it + 2 >= id_base + 32) look(it + 2);  // (32 items are a whole number of steps)
-          if (id0 == kTailItem) put_tail(at, 0, me);
-          else put_page(at, 0);
-          if (more) load(it + 2, 0);
-          if (id1 == kTailItem) put_tail(at, 1, me);
-          else put_page(at, 1);
-          if (more) load(it + 3, 1);
-          proxy_fence();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&full[slot]));
+        const int now0 = id0, now1 = id1;
+        id0 = id1 = kNoItem;
+        if (it + 2 < end) {
+          if (it + 2 >= id_base + 32) look(it);
+          id0 = id_of(it + 2);
+          id1 = id_of(it + 3);
         }
+        take(0, now0);
+        take(1, now1);
+        proxy_fence();  // what was read is read before the next copy writes
+        __syncwarp();
+        if (!ok) break;
+        load(0, id0);
+        load(1, id1);
+        warp_wait(ok, smem_u32(&empty[slot]), (count >> 1 & 1) ^ 1, abort, a.err);
+        if (!ok) break;
+        const int x = lane - (it - id_base);
+        if (!half && (x & ~1) == 0) {  // what the softmax has to know of the pages
+          if (id != kTailItem) {
+            me.kfac[x * 4 + w4] = kfac;
+            me.vlog[x * 4 + w4] = vlog;
+            me.vinv[x * 4 + w4] = vinv;
+            me.bad_keys[x * 4 + w4] = bad ? 0xffffu : 0u;
+          }
+          if (w4 == 0) {
+            me.tail[x] = id == kTailItem;
+            me.count[x] = id == kTailItem ? u.tail : id >= 0 ? kPart : 0;
+            me.pos[x] = pos;
+            me.tokens[x][0] = who[0];
+            me.tokens[x][1] = who[1];
+          }
+        }
+        if (now0 == kTailItem) put_tail(at, 0, me);
+        else put_page(at, 0);
+        if (now1 == kTailItem) put_tail(at, 1, me);
+        else put_page(at, 1);
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&full[slot]));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[seg % kSegments]));
