@@ -703,21 +703,18 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-}  // namespace
-
-cudaError_t kv8_page_map(const Kv8Args& a, int rows, CUtensorMap* m) {
+// The pool as [n_pages][128 rows][128 bytes], a box of one page.
+cudaError_t page_map(const Kv8Args& a, CUtensorMap* m) {
   const EncodeTiledFn fn = encode_fn();
   if (!fn) return cudaErrorSymbolNotFound;
   const cuuint64_t dims[3] = {kD, 2 * kPart, (cuuint64_t)a.n_pages};
   const cuuint64_t strides[2] = {kD, kKv8PageBytes};
-  const cuuint32_t box[3] = {kD, (cuuint32_t)rows, 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {kD, 2 * kPart, 1}, step[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.pages, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
 }
-
-namespace {
 
 template <int R>
 cudaError_t launch_decode(const Kv8Args& a, const CUtensorMap& map, const Rows& q, const Rows& out, float scale,
@@ -743,7 +740,7 @@ cudaError_t launch_kv8_attend(const Kv8Args& a, const Rows& q, const Rows& out, 
   const int64_t rows = (int64_t)a.max_new * a.G;  // of a unit, at most
   if (rows > kMostRows) return launch_kv8_prefill(a, q, out, scale, sel, topk, workspace, sm_count, st);
   CUtensorMap map;
-  const cudaError_t e = kv8_page_map(a, 2 * kPart, &map);
+  const cudaError_t e = page_map(a, &map);
   if (e != cudaSuccess) return e;
   return rows <= 8 ? launch_decode<1>(a, map, q, out, scale, sel, topk, workspace, sm_count, st)
                    : launch_decode<2>(a, map, q, out, scale, sel, topk, workspace, sm_count, st);

@@ -14,7 +14,9 @@ using namespace kv8;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kWindow = 2048;  // pages that are marked at a time
-constexpr int kUnitSteps = 8;  // steps that beginning and ending a block costs
+// Steps that beginning and ending a block costs. (Six ragged prompts: 68.1 us with 1, 58.4 with 4, 57.8 with 8, 60.8 with 20; one long
+// chunk, whose blocks are alike, 513 to 521.)
+constexpr int kUnitSteps = 8;
 
 // A CTA a block and head. The tokens' pages are marked in a window of shared memory, a bit a token, and read out in order;
 // what lies beyond the window waits for the next, which begins at the lowest page that is left.

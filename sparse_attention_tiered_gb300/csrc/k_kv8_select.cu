@@ -29,6 +29,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kStrip = 16;               // pages of a warp's product
 constexpr int kPitch = kD + 16;          // bf16 elements of a query row in shared memory: no two rows of 8 on one bank
 constexpr int kWide = 512;               // threads of a row of many pages
+constexpr int kRows = 2;                 // a CTA, of few pages each
 constexpr int64_t kSlabBytes = 1ll << 30;
 
 struct SelectSpace {
@@ -519,10 +520,10 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
   }
 }
 
-// A row: a token and a KV head. T = 32: a warp a row; else a CTA a row. N: pages a thread that it holds in registers, if
+// A row: a token and a KV head. T = 32: a warp a row, kRows of them a CTA (with 8 the time is the same); else a CTA a row. N: pages a thread that it holds in registers, if
 // that is enough.
 template <int T, int N>
-__global__ void __launch_bounds__(T == 32 ? kThreads : T)
+__global__ void __launch_bounds__(T == 32 ? kRows * 32 : T)
 kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* sel) {
   __shared__ int32_t counts[T == 32 ? 1 : 2 * (T / 32)];
   __shared__ uint64_t keys[T == 32 ? 1 : 32];
@@ -532,7 +533,7 @@ kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* se
   const int lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t row = T == 32 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t row = T == 32 ? (int64_t)blockIdx.x * kRows + (threadIdx.x >> 5) : blockIdx.x;
   if (row >= (int64_t)(s.t1 - s.t0) * a.Hkv) return;
   const int token = s.t0 + (int)(row / a.Hkv), h = (int)(row % a.Hkv);
   if (token >= a.cu[a.B]) return;  // padding
@@ -601,13 +602,16 @@ cudaError_t launch_kv8_select(const Kv8Args& a, const Rows& q, int topk, int32_t
   for (int64_t t = 0; t < a.total_new; t += slab) {
     s.t0 = (int)t;
     s.t1 = (int)(t + slab < a.total_new ? t + slab : a.total_new);
+    // 8 tokens a CTA or 32: 32 requests of 512 pages with 8 tokens each 27.4 and 35.4 us, with 12 38.3 and 36.2, with 64 112 and 84.
     cudaError_t e = a.max_new <= 8 ? launch_scores<1>(a, q, s, sm_count, st) : launch_scores<4>(a, q, s, sm_count, st);
     if (e != cudaSuccess) return e;
     const int64_t n = (int64_t)(s.t1 - s.t0) * a.Hkv;
-    const int warps = n >= 8 * kWarps * sm_count ? kWarps : 2;  // few rows are spread over the SMs
-    const dim3 narrow((unsigned)((n + warps - 1) / warps));
-    e = a.max_pages <= 512    ? launch_early(kv8_select_pick<32, 16>, narrow, warps * 32, 0, st, a, q, s, topk, sel)
-        : a.max_pages <= 2048 ? launch_early(kv8_select_pick<32, 64>, narrow, warps * 32, 0, st, a, q, s, topk, sel)
+    // A warp a row, holding 16 or 64 scores a lane, or a CTA a row. Up to 512 pages: 32 requests 23.4, 25.9 and 35.0 us, a chunk of
+    // 2048 tokens 78, 118 and 595. 1000 pages: 4 requests 20.4 with a warp a row and 23.9 with a CTA, a chunk 156 and 651;
+    // 2048 pages: 1 request 26.0 and 23.0, 32 requests 80.9 and 70.5, a chunk 322 and 729. A warp cannot hold more.
+    const dim3 narrow((unsigned)((n + kRows - 1) / kRows));
+    e = a.max_pages <= 512    ? launch_early(kv8_select_pick<32, 16>, narrow, kRows * 32, 0, st, a, q, s, topk, sel)
+        : a.max_pages <= 2048 ? launch_early(kv8_select_pick<32, 64>, narrow, kRows * 32, 0, st, a, q, s, topk, sel)
                               : launch_early(kv8_select_pick<kWide, 32>, dim3((unsigned)n), kWide, 0, st, a, q, s, topk, sel);
     if (e != cudaSuccess) return e;
   }

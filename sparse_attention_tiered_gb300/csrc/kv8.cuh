@@ -79,8 +79,6 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sh
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
-// The pool as [n_pages][128 rows][128 bytes] for copies of boxes of `rows` rows: 128 a page, 64 its keys or values.
-cudaError_t kv8_page_map(const Kv8Args& a, int rows, CUtensorMap* m);
 // Joins what the shares of `ctas` CTAs left in the workspace, with `rows` CTAs for each.
 cudaError_t launch_kv8_join(const Kv8Args& a, const Rows& out, int ctas, int rows, void* workspace,
                             int part_rows, cudaStream_t st);

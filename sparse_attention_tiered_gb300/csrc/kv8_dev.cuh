@@ -88,15 +88,6 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// Its keys or values alone, 64 such rows.
-__device__ __forceinline__ void tma_half(uint32_t dst, const CUtensorMap* map, int page, int half, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(half * kPart), "r"(page), "r"(bar)
-      : "memory");
-}
-
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)

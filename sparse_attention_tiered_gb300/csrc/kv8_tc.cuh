@@ -50,24 +50,6 @@ __device__ __forceinline__ void settle32(uint32_t* r) {
   asm volatile("" : SPIN_R8(r, 0), SPIN_R8(r, 8), SPIN_R8(r, 16), SPIN_R8(r, 24));
 }
 
-__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : SPIN_W8(r, 0), SPIN_W8(r, 8)
-      : "r"(addr)
-      : "memory");
-}
-
-__device__ __forceinline__ void settle16(uint32_t* r) { asm volatile("" : SPIN_R8(r, 0), SPIN_R8(r, 8)); }
-
-// One column of the warp's lanes. The value is there after tmem_loaded().
-__device__ __forceinline__ void tmem_load1(uint32_t addr, uint32_t& r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void tmem_store1(uint32_t addr, uint32_t r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%1], {%0};" ::"r"(r), "r"(addr) : "memory");
-}
-
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::SPIN_I8(r, 0),
@@ -102,11 +84,6 @@ __device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
 __device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
   return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
