@@ -86,8 +86,9 @@ class SpinKV8:
     it, before the call that completes or reads the page, or leaves it to the pool's calls (reserve, fork,
     compact). Those keep refs (int32 [n_pages]: the table entries that name each page; refs=True: zeros, for a new cache).
 
-    workspace: another handle's, or new_workspace()'s, for attend (some 43 MB). The layers of a model,
-    whose calls follow one another on a stream, need one between them."""
+    workspace: another handle's, or new_workspace()'s, for attend (some 43 MB); or the other handle itself, for all calls'. The
+    layers of a model, whose calls follow one another on a stream, need one between them. Calls that may run at the same time,
+    of one handle or of two that share, need one each: every call but fork takes one of its own."""
 
     def __init__(self, batch: int, q_heads: int, kv_heads: int, max_pages: int, n_pages: Optional[int] = None, *,
                  rope: Optional[SpinRope] = None, pages=None, scales=None, tails=None, table=None, summaries=False,
@@ -134,7 +135,9 @@ class SpinKV8:
         self._reserve, self._fork, self._compact = lib.spin_kv8_reserve, lib.spin_kv8_fork, lib.spin_kv8_compact
         self._pool_bytes = B.spin_kv8_pool_workspace(self.c)
         self._sizes = {}
-        self._spaces = {}  # workspaces of the handle's own, by kind: the last of each list is in use
+        self._spaces = {}  # workspaces of the other calls, by kind: the last of each list is in use
+        if isinstance(workspace, SpinKV8):
+            self._spaces, workspace = workspace._spaces, workspace.workspace
         self._c_at = ctypes.addressof(self.c)
         self.workspace = self.new_workspace() if workspace is None else _tensor("workspace", workspace, torch.uint8, None, self.device)
         self._bf16 = torch.bfloat16

@@ -279,6 +279,41 @@ def test_streams_and_graphs():
     c.same(out.cpu())
 
 
+def test_layers_share_what_their_calls_need():
+    """A handle given as the workspace: the two have one between them, whichever of them makes it grow."""
+    small, large = Case(2, 4, [900], [2], 6, seed=4), Case(2, 4, [900, 1700], [130, 1], 6, seed=5)
+    wants = [small.run(), large.run()]
+    handles = []
+    for c in (large, small):
+        handles.append(spin().SpinKV8(len(c.past), c.H * c.G, c.H, c.table.shape[2], pages=c.c.pages, scales=c.c.scales, tails=c.c.tails,
+                                      table=c.c.table, workspace=handles[0] if handles else None))
+    assert handles[0].workspace is handles[1].workspace
+    for _ in range(2):
+        for c, h, want in zip((small, large), handles[::-1], wants):
+            q = c.q.cuda()
+            assert torch.equal(h.attend_rows(step_of(c.past, c.new)[0], q, torch.full_like(q, 7.0), c.sel.cuda()).cpu(), want)
+    assert len(handles[0]._spaces["attend_rows"]) == 2
+
+
+def test_calls_at_the_same_time_with_workspaces_of_their_own():
+    s = spin()
+    c = Case(2, 8, [5000, 300], [40, 7], 30, lists="near", seed=1)
+    want = c.run()
+    st, _ = step_of(c.past, c.new)
+    q, sel, n = c.q.cuda(), c.sel.cuda(), s.spin_kv8_attend_rows_workspace(c.c.c, sum(c.new), 30)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    spaces = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in streams]
+    outs = [torch.zeros_like(q) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for x, w, o in zip(streams, spaces, outs):
+            c.c.attend_rows(st, q, o, sel, workspace=w, stream=x.cuda_stream)
+    torch.cuda.synchronize()
+    c.c.check()
+    for o in outs:
+        assert torch.equal(o.cpu(), want)
+
+
 def test_the_handle_refuses():
     c = Case(2, 2, [100], [1], 3)
     c.run()
