@@ -521,9 +521,9 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
 }
 
 // A row: a token and a KV head. T = 32: a warp a row, kRows of them a CTA (with 8 the time is the same); else a CTA a row. N: pages a thread that it holds in registers, if
-// that is enough.
+// that is enough; 64 or 96 registers, for 32 or 20 warps an SM.
 template <int T, int N>
-__global__ void __launch_bounds__(T == 32 ? kRows * 32 : T)
+__global__ void __launch_bounds__(T == 32 ? kRows * 32 : T, T == 32 ? (N == 16 ? 16 : 10) : 1)
 kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* sel) {
   __shared__ int32_t counts[T == 32 ? 1 : 2 * (T / 32)];
   __shared__ uint64_t keys[T == 32 ? 1 : 32];
@@ -607,8 +607,8 @@ cudaError_t launch_kv8_select(const Kv8Args& a, const Rows& q, int topk, int32_t
     if (e != cudaSuccess) return e;
     const int64_t n = (int64_t)(s.t1 - s.t0) * a.Hkv;
     // A warp a row, holding 16 or 64 scores a lane, or a CTA a row. Up to 512 pages: 32 requests 23.4, 25.9 and 35.0 us, a chunk of
-    // 2048 tokens 78, 118 and 595. 1000 pages: 4 requests 20.4 with a warp a row and 23.9 with a CTA, a chunk 156 and 651;
-    // 2048 pages: 1 request 26.0 and 23.0, 32 requests 80.9 and 70.5, a chunk 322 and 729. A warp cannot hold more.
+    // 2048 tokens 77, 118 and 595. 1000 pages: 4 requests 20.4 with a warp a row and 23.9 with a CTA, a chunk 145 and 651;
+    // 2048 pages: 1 request 26.0 and 23.0, 32 requests 80.9 and 70.5, a chunk 305 and 729. A warp cannot hold more.
     const dim3 narrow((unsigned)((n + kRows - 1) / kRows));
     e = a.max_pages <= 512    ? launch_early(kv8_select_pick<32, 16>, narrow, kRows * 32, 0, st, a, q, s, topk, sel)
         : a.max_pages <= 2048 ? launch_early(kv8_select_pick<32, 64>, narrow, kRows * 32, 0, st, a, q, s, topk, sel)
