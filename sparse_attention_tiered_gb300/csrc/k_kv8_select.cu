@@ -296,7 +296,8 @@ struct RowIn {
 template <int T, int N>
 __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
   const int me = team.rank(), lane = threadIdx.x & 31;
-  const int turns = (in.pages + T - 1) / T;
+  const int turns = (in.pages + T - 1) / T, strips = (in.pages + kStrip - 1) / kStrip;
+  float top = me < strips ? in.norms[me] : 0.f;  // (on its way with the scores)
   uint32_t held[N ? N : 1];
   if constexpr (N > 0) {
 #pragma unroll
@@ -326,8 +327,7 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
   if (in.k <= T && in.pages >= T) lo = hi;  // the least of the threads' largest ones: T of them reach it
   lo = team.smallest(lo);
   hi = team.largest(hi);
-  float top = 0.f;
-  for (int i = me; i < (in.pages + kStrip - 1) / kStrip; i += T) top = fmaxf(top, in.norms[i]);
+  for (int i = me + T; i < strips; i += T) top = fmaxf(top, in.norms[i]);
   top = __uint_as_float(team.largest(__float_as_uint(top)));
   const float size = in.qnorm * top;
   const bool sure = size < 1e30f;  // else nothing is known of the scores
@@ -489,32 +489,56 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
       ties += total;
       put(i, y > high || (doubt && (x > border || (x == border && rank < equal))));
     }
-  } else if constexpr (T > 32 && N > 0) {
-    // All counts first, so that the CTA meets three times and not once a turn.
-    const int warp = threadIdx.x >> 5, warps = T / 32;
+  } else if constexpr (N > 0) {
+    // A bit a page, 32 turns a word.
+    constexpr int kWords = (N + 31) / 32;
+    uint32_t take[kWords];
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) take[w] = 0;
     each([&](int i, uint32_t y) {
-      const uint32_t vote = __ballot_sync(0xffffffffu, takes(i, y));
-      if (lane == 0) team.found[i * warps + warp] = (uint16_t)__popc(vote);
+      if (settle ? y > high : y >= low && y != 0) take[i >> 5] |= 1u << (i & 31);
     });
-    __syncthreads();
-    static_assert(N * (T / 32) <= T, "a thread a count");
-    int mine = me < N * warps ? team.found[me] : 0;
-    int before = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += y;
+    for (uint32_t left = settle ? taken : 0; left; left &= left - 1) {
+      const int p = __shfl_sync(0xffffffffu, page, __ffs(left) - 1);
+      if (p % T == me) {
+#pragma unroll
+        for (int w = 0; w < kWords; ++w)
+          if (p / T / 32 == w) take[w] |= 1u << (p / T & 31);
+      }
     }
-    const int last = (int)team.told(__shfl_sync(0xffffffffu, before, 31), 0);
-    before += (int)__reduce_add_sync(0xffffffffu, lane < warp ? (uint32_t)last : 0u) - mine;
-    if (me < N * warps) team.found[me] = (uint16_t)before;
-    __syncthreads();
-    each([&](int i, uint32_t y) {
-      const bool take = takes(i, y);
-      const uint32_t vote = __ballot_sync(0xffffffffu, take);
-      const int rank = team.found[i * warps + warp] + __popc(vote & ((1u << lane) - 1u));
-      if (take && rank < in.k) in.out[rank] = me + i * T;
-    });
-    return;  // (k pages are taken)
+    if constexpr (T == 32) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) put(i, take[i >> 5] >> (i & 31) & 1);
+    } else {
+      // Lane i has the votes on turn i, and the number of pages that are taken before them: the CTA meets three times, not once a turn.
+      static_assert(N <= 32 && N * (T / 32) <= T, "a lane a turn, a thread a count");
+      const int warp = threadIdx.x >> 5, warps = T / 32;
+      uint32_t votes = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t vote = __ballot_sync(0xffffffffu, take[0] >> i & 1);
+        if (lane == i) votes = vote;
+      }
+      if (lane < N) team.found[lane * warps + warp] = (uint16_t)__popc(votes);
+      __syncthreads();
+      const int mine = me < N * warps ? team.found[me] : 0;
+      int before = mine;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+      }
+      const int last = (int)team.told(__shfl_sync(0xffffffffu, before, 31), 0);
+      before += (int)__reduce_add_sync(0xffffffffu, lane < warp ? (uint32_t)last : 0u) - mine;
+      if (me < N * warps) team.found[me] = (uint16_t)before;
+      __syncthreads();
+      const int first = lane < N ? team.found[lane * warps + warp] : 0;
+      for (uint32_t any = __reduce_or_sync(0xffffffffu, take[0]); any; any &= any - 1) {
+        const int i = __ffs(any) - 1;
+        const uint32_t vote = __shfl_sync(0xffffffffu, votes, i);
+        const int rank = __shfl_sync(0xffffffffu, first, i) + __popc(vote & ((1u << lane) - 1u));
+        if ((take[0] >> i & 1) && rank < in.k) in.out[rank] = me + i * T;
+      }
+    }
   } else {
     each([&](int i, uint32_t y) { put(i, takes(i, y)); });
   }
@@ -567,8 +591,8 @@ kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* se
   in.G = a.G;
   Team<T> team{counts, keys, pages, &listed, found};
   if (in.pages <= N / 2 * T) pick<T, N / 2>(team, in);
-  else if (in.pages <= N * T) pick<T, N>(team, in);
-  else pick<T, 0>(team, in);
+  else if (T == 32 || in.pages <= N * T) pick<T, N>(team, in);
+  else if constexpr (T > 32) pick<T, 0>(team, in);
 }
 
 template <int NT>
