@@ -547,7 +547,7 @@ __device__ __forceinline__ void pick(Team<T>& team, const RowIn& in) {
 // A row: a token and a KV head. T = 32: a warp a row, kRows of them a CTA (with 8 the time is the same); else a CTA a row. N: pages a thread that it holds in registers, if
 // that is enough; 64 or 96 registers, for 32 or 20 warps an SM.
 template <int T, int N>
-__global__ void __launch_bounds__(T == 32 ? kRows * 32 : T, T == 32 ? (N == 16 ? 16 : 10) : 1)
+__global__ void __launch_bounds__(T == 32 ? kRows * 32 : T, T == 32 ? (N == 16 ? 16 : 10) : 2)
 kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* sel) {
   __shared__ int32_t counts[T == 32 ? 1 : 2 * (T / 32)];
   __shared__ uint64_t keys[T == 32 ? 1 : 32];
