@@ -17,13 +17,10 @@
 // them into registers as soon as they are there, and has the next step's under way while it waits, converts and stores.
 //
 // A step of two pages takes some 2,350 clocks where nothing else is in the way (96 more pages a tile on 512 blocks of 152 CTAs:
-// 400 us). The products alone take 1,430 and the exponents and conversions, at 32 a clock, 1,280; what they share is the shared memory, 256 KB a
-// step at 128 bytes a clock: Q for the scores 64 KB, K and V 64, their stores 64, the codes in and out 64. (Conversions made five times
+// 400 us). The products alone take 1,430; what bounds it is the shared memory, 256 KB a step at 128 bytes a clock: Q for the
+// scores 64 KB, K and V for the products 64, their stores 64, the codes in and out 64. (Conversions made several times
 // cheaper change nothing. With loads straight into registers the chunk of 2048 tokens onto 30000 takes the same 514 us, and five
 // drafts of 16 requests, whose pages come from HBM, 79 us instead of 70.)
-//
-// A row that does not list the page of a step has an exponent of -infinity there, and a warp of 32 such rows stores zeros
-// and goes on. Which pages those are costs two shared loads and a vote a step.
 #include <type_traits>
 
 #include "kv8_rows.cuh"

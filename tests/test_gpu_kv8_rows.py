@@ -279,6 +279,39 @@ def test_streams_and_graphs():
     c.same(out.cpu())
 
 
+def test_a_captured_call_keeps_the_workspace_that_it_was_captured_with():
+    """Two graphs and eager calls of one handle, before and after its workspace grows; a capture that would make it grow is refused."""
+    c = Case(2, 8, [2000, 300], [60, 7], 12, lists="near", seed=3)
+    few, many = Case(2, 8, [2000, 300], [2, 0], 12, lists="near", seed=4), c
+    want = many.run()
+    h = spin().SpinKV8(2, 16, 2, c.table.shape[2], pages=c.c.pages, scales=c.c.scales, tails=c.c.tails, table=c.c.table)
+    side, graphs, outs = torch.cuda.Stream(), [], []
+    st, _ = step_of(few.past, few.new)
+    q, sel = few.q.cuda(), few.sel.cuda()
+    small = h.attend_rows(st, q, torch.zeros_like(q), sel).clone()
+    large, lq, lsel = step_of(many.past, many.new)[0], many.q.cuda(), many.sel.cuda()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        outs.append(torch.zeros_like(q))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            h.attend_rows(st, q, outs[-1], sel, stream=side.cuda_stream)
+    refused = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(refused, stream=side):
+        with pytest.raises(ValueError, match="before capturing"):
+            h.attend_rows(large, lq, torch.empty_like(lq), lsel, stream=side.cuda_stream)
+    got = torch.zeros_like(lq)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+        h.attend_rows(large, lq, got, lsel, stream=torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got.cpu(), want)
+        for o in outs:
+            assert torch.equal(o, small)
+            o.zero_()
+
+
 def test_layers_share_what_their_calls_need():
     """A handle given as the workspace: the two have one between them, whichever of them makes it grow."""
     small, large = Case(2, 4, [900], [2], 6, seed=4), Case(2, 4, [900, 1700], [130, 1], 6, seed=5)
