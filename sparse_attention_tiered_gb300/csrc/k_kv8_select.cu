@@ -669,12 +669,14 @@ cudaError_t launch_kv8_select(const Kv8Args& a, const Rows& q, int topk, int32_t
     cudaError_t e = a.max_new <= 8 ? launch_scores<1>(a, q, s, sm_count, st) : launch_scores<4>(a, q, s, sm_count, st);
     if (e != cudaSuccess) return e;
     const int64_t n = (int64_t)(s.t1 - s.t0) * a.Hkv;
-    // A warp a row, holding 16 or 64 scores a lane, or a CTA a row. Up to 512 pages: 32 requests 23.4, 25.9 and 35.0 us, a chunk of
-    // 2048 tokens 77, 118 and 595. 1000 pages: 4 requests 20.4 with a warp a row and 23.9 with a CTA, a chunk 145 and 651;
-    // 2048 pages: 1 request 26.0 and 23.0, 32 requests 80.9 and 70.5, a chunk 305 and 729. A warp cannot hold more.
+    // A warp a row, holding 16 or 64 scores a lane, or a CTA a row. Up to 512 pages: 32 requests of 8 heads 22.9, 24.9 and 31.3 us, a
+    // chunk of 2048 tokens 77, 102 and 635. 1000 pages: 4 requests 19.3 with a warp a row and 20.6 with a CTA, 32 requests 43.6 and
+    // 46.1, a chunk 138 and 529. 2048 pages: 1 request 26.6 and 19.9, 75 requests 134 and 127, 120 requests 206 and 208, a chunk 291
+    // and 609: a CTA passes a row in a third of a warp's time, which pays for three turns of two an SM. A warp cannot hold more.
+    const bool warps = a.max_pages <= 1024 || (a.max_pages <= 2048 && n > 6 * (int64_t)sm_count);
     const dim3 narrow((unsigned)((n + kRows - 1) / kRows));
     e = a.max_pages <= 512    ? launch_early(kv8_select_pick<32, 16>, narrow, kRows * 32, 0, st, a, q, s, topk, sel)
-        : a.max_pages <= 2048 ? launch_early(kv8_select_pick<32, 64>, narrow, kRows * 32, 0, st, a, q, s, topk, sel)
+        : warps               ? launch_early(kv8_select_pick<32, 64>, narrow, kRows * 32, 0, st, a, q, s, topk, sel)
                               : launch_early(kv8_select_pick<kWide, 32>, dim3((unsigned)n), kWide, 0, st, a, q, s, topk, sel);
     if (e != cudaSuccess) return e;
   }

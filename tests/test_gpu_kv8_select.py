@@ -81,6 +81,12 @@ def test_long_requests(pages, new):
     case(2, 2, 3, [pages * PAGE - new, 500], [new, 1], 65, seed=pages)
 
 
+@pytest.mark.parametrize("batch,new", [(1, 700), (170, 1)])
+def test_many_rows_of_up_to_2048_pages(batch, new):
+    """More rows than a CTA each would pay for: a warp a row, 64 scores a lane."""
+    case(batch, 6 if batch > 1 else 2, 3, [2048 * PAGE - new - 7 * i for i in range(batch)], [new] * batch, 40, seed=batch, pages=2048)
+
+
 def test_a_chunk():
     case(2, 2, 8, [3001, 0], [700, 333], 12, seed=5, pad=9)
 
