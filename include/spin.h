@@ -454,6 +454,8 @@ int spin_kv8_attend_rows_workspace(const spin_kv8* cache, int32_t total_new, int
  * listed pages p with 64 (p + 1) <= past[b] + i + 1, each page once however often it is listed and in any order; other
  * entries (-1, a page that it does not see whole) are no page. And it sees its newest tokens, those at
  * 64 ((past[b] + i + 1) / 64) .. past[b] + i, wherever they are by now. Everything else is as in spin_kv8_attend.
+ * Where cu_new descends, which the error word tells, requests may name the same rows: with max_new above 1 one that begins
+ * before the end of another before it that is in range is left out too; with max_new 1 the row holds the answer of one of them.
  * 1 <= topk <= 512. workspace: of spin_kv8_attend_rows_workspace bytes, 16-byte aligned;
  * needs no initialisation and holds nothing between calls. */
 int spin_kv8_attend_rows(const spin_kv8* cache, const spin_kv8_step* step, const spin_rows* q, const spin_rows* out, float scale,

@@ -25,17 +25,17 @@ __global__ void __launch_bounds__(kThreads)
 kv8_rows_blocks(const Kv8Args a, const Rows out, const int32_t* sel, int topk, int64_t cap, RowLists s) {
   __shared__ __align__(16) uint32_t marks[2][kWindow];
   __shared__ int64_t scratch[36];
+  __shared__ uint32_t bits[kMaxRequests / 32];
   __shared__ int found[kWarps][2], next[kWarps], most[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = list_rows(a.G);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int h = blockIdx.x % a.Hkv, number = blockIdx.x / a.Hkv;
   int row0, n_new, past;
-  const Place pl = locate(
-      a.B, scratch,
-      [&](int b, bool report) {
-        return kv8_request(a, b, report && blockIdx.x == 0, row0, n_new, past) ? ((int64_t)n_new * a.G + R - 1) / R : 0ll;
-      },
+  bool strange;
+  // Requests that count share no row, so that their blocks are no more than were launched and have a place (most_blocks).
+  const Place pl = locate_rows(
+      a, scratch, bits, blockIdx.x == 0, strange, [&](int, int n, int) { return ((int64_t)n * a.G + R - 1) / R; },
       [&](int64_t) { return (int64_t)number; });
   if (blockIdx.x == 0 && tid == 0) *s.n_blocks = (int)pl.total * a.Hkv;
   if (pl.b >= a.B || !kv8_request(a, pl.b, false, row0, n_new, past)) return;

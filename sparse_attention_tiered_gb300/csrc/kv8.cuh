@@ -8,6 +8,7 @@ namespace spin {
 
 constexpr int kKv8HalfBytes = kPart * kD;         // the keys (or values) of a page, e4m3
 constexpr int kKv8PageBytes = 2 * kKv8HalfBytes;  // 16384
+constexpr int kMaxRequests = 16384;               // of a batch
 constexpr int kKv8MinScaleExp = -64;              // the append's smallest scale is 2^-64
 
 struct Rows {  // spin_rows with a bf16 pointer

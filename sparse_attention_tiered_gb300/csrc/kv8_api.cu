@@ -45,7 +45,7 @@ bool off(const void* p, uintptr_t align) { return (reinterpret_cast<uintptr_t>(p
 
 int check_cache(const char* who, const spin_kv8* c) {
   if (!c) return refuse(SPIN_ERR_INVALID, "%s: cache is NULL", who);
-  if (c->batch < 1 || c->batch > 16384) return refuse(SPIN_ERR_INVALID, "%s: batch must be 1 .. 16384", who);
+  if (c->batch < 1 || c->batch > kMaxRequests) return refuse(SPIN_ERR_INVALID, "%s: batch must be 1 .. %d", who, kMaxRequests);
   if (c->kv_heads < 1 || c->kv_heads > 4096 || c->q_heads < 1 || c->q_heads % c->kv_heads != 0 ||
       c->q_heads / c->kv_heads > kMaxGroup)
     return refuse(SPIN_ERR_INVALID, "%s: q_heads must be a multiple of kv_heads (1 .. 4096) with a group of at most %d", who,

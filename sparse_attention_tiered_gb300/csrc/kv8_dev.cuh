@@ -276,6 +276,60 @@ __device__ __forceinline__ Place locate(int requests, int64_t* scratch, Weight w
   return Place{total, (int)scratch[32], scratch[33]};
 }
 
+// ---------------------------------------------------------------------------
+// Requests that count where a call has room for no more than its total_new rows (blocks, tiles, a place a row). While cu_new
+// ascends no two requests have a row in common, and those in range have total_new between them at most. Where it descends
+// they may name rows twice, each of them in range by itself. So a request counts if it is in range and begins behind
+// the end of every one before it that is and has rows: those that count never share a row. (Where cu_new descends there is a request
+// that ends before it begins, so the error word tells.)
+// ---------------------------------------------------------------------------
+// f(b, counts, row0, n_new) for all requests, a lane each, by a warp.
+template <typename F>
+__device__ __forceinline__ void each_request(const Kv8Args& a, F f) {
+  const int lane = threadIdx.x & 31;
+  int end = 0;  // of the requests so far
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    int row0 = 0, n_new = 0, past;
+    const bool ok = b0 + lane < a.B && kv8_request(a, b0 + lane, false, row0, n_new, past);
+    int most = ok && n_new ? row0 + n_new : 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, most, o);
+      if (lane >= o) most = max(most, y);
+    }
+    const int before = __shfl_up_sync(0xffffffffu, most, 1);
+    f(b0 + lane, ok && row0 >= max(end, lane ? before : 0), row0, n_new);
+    end = max(end, __shfl_sync(0xffffffffu, most, 31));
+  }
+}
+
+// As locate, where a request that counts has weight(row0, n_new, past) places and the others none. `strange`: some
+// request is out of range; only then there are any that might not count (bits: kMaxRequests / 32 words of shared memory).
+template <typename Weight, typename At>
+__device__ __forceinline__ Place locate_rows(const Kv8Args& a, int64_t* scratch, uint32_t* bits, bool report, bool& strange, Weight weight, At at) {
+  bool mine = false;
+  strange = false;
+  for (;;) {
+    const Place p = locate(
+        a.B, scratch,
+        [&](int b, bool first) {
+          int row0, n_new, past;
+          const bool ok = kv8_request(a, b, first && report, row0, n_new, past);
+          mine |= !ok;
+          return ok && (!strange || (bits[b >> 5] >> (b & 31) & 1)) ? weight(row0, n_new, past) : (int64_t)0;
+        },
+        at);
+    if (strange || !__syncthreads_or(mine)) return p;
+    strange = true;
+    if (threadIdx.x < 32)
+      each_request(a, [&](int b, bool counts, int, int) {
+        const uint32_t word = __ballot_sync(0xffffffffu, counts);
+        if ((b & 31) == 0) bits[b >> 5] = word;
+      });
+    __syncthreads();
+  }
+}
+
 // a / b of numbers that are not negative: a division in 32 bits takes a third of the one in 64, which is on the way
 // to a CTA's first load.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
