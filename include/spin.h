@@ -440,7 +440,8 @@ int spin_kv8_select_workspace(const spin_kv8* cache, int32_t total_new, int64_t*
  * scores are compared as exact numbers to 64 bits, equal ones go to the lower page, and one that is no number (the
  * page holds something not finite, or the query is) counts as -infinity: how tokens are split into calls does not matter.
  * q: rotated bf16 [total_new][q_heads]. sel: device int32 [total_new][kv_heads][topk], pages in ascending
- * order, then -1. Rows of padding, and of requests whose numbers are out of range, are not written. 1 <= topk <= 512. The
+ * order, then -1. Rows of padding, and of requests whose numbers are out of range, are not written; where cu_new descends, which
+ * the error word tells, nor are those of a request that begins before the end of another before it that is in range. 1 <= topk <= 512. The
  * cache's summaries must be there for all complete pages. workspace: 16-byte aligned, of
  * spin_kv8_select_workspace bytes; needs no initialisation and holds nothing between calls. */
 int spin_kv8_select(const spin_kv8* cache, const spin_kv8_step* step, const spin_rows* q, int32_t topk, int32_t* sel,

@@ -38,6 +38,7 @@ struct SelectSpace {
   uint64_t* exact;  // [rows][pitch]: keys of exact scores, where there are many to be settled
   float* norms;     // [units][pitch / 16] largest norm of a strip's summaries
   float* qnorms;    // [rows]
+  int32_t* strange; // whether some request is out of range
   int64_t pitch;    // pages of a row
   int t0, t1;       // tokens of this slab: row (t - t0) * Hkv + h
 };
@@ -68,11 +69,19 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ float norm_of(float sum_of_squares) { return sqrtf(sum_of_squares) * 1.0001f + 1e-21f; }
 
 // A request's tokens in [t0, t1): the first, and how many.
-__device__ __forceinline__ int tokens_of(const Kv8Args& a, const SelectSpace& s, int b, bool report, int& first, int& row0, int& past) {
-  int n_new;
-  if (!kv8_request(a, b, report, row0, n_new, past)) return 0;
+__device__ __forceinline__ int tokens_of(const SelectSpace& s, int row0, int n_new, int& first) {
   first = max(row0, s.t0);
   return max(0, min(row0 + n_new, s.t1) - first);
+}
+
+// The request that a token belongs to, of those that count, or -1: by a warp. The slow way, where cu_new may not ascend.
+__device__ __noinline__ int owner_of(const Kv8Args a, int token) {
+  int owner = -1;
+  each_request(a, [&](int b, bool counts, int row0, int n_new) {
+    const uint32_t its = __ballot_sync(0xffffffffu, counts && token >= row0 && token < row0 + n_new);
+    if (its) owner = b - (int)(threadIdx.x & 31) + __ffs(its) - 1;
+  });
+  return owner;
 }
 
 // CTA (tile, head, x): 8 NT tokens of a request, and every X-th run of eight strips of the pages that the last of them sees.
@@ -82,25 +91,27 @@ kv8_select_scores(const Kv8Args a, const Rows q, SelectSpace s, int X) {
   constexpr int kTokens = 8 * NT;
   __shared__ __align__(16) uint16_t sq[2][kTokens][kPitch];
   __shared__ int64_t scratch[36];
+  __shared__ uint32_t bits[kMaxRequests / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int x = blockIdx.x % X, th = blockIdx.x / X, h = th % a.Hkv, tile = th / a.Hkv;
-  int first, row0, past;
-  const Place pl = locate(
-      a.B, scratch,
-      [&](int b, bool report) {
-        return (int64_t)(tokens_of(a, s, b, report && blockIdx.x == 0, first, row0, past) + kTokens - 1) / kTokens;
-      },
+  int first, row0, n_new, past;
+  bool strange;
+  // Requests that count share no row: as many tiles as were launched are enough, and no two write one row's scores.
+  const Place pl = locate_rows(
+      a, scratch, bits, blockIdx.x == 0, strange,
+      [&](int row, int n, int) { return (int64_t)(tokens_of(s, row, n, first) + kTokens - 1) / kTokens; },
       [&](int64_t) { return (int64_t)tile; });
-  if (pl.b >= a.B) return;
-  int tokens = tokens_of(a, s, pl.b, false, first, row0, past);
+  if (blockIdx.x == 0 && tid == 0) *s.strange = strange;
+  if (pl.b >= a.B || !kv8_request(a, pl.b, false, row0, n_new, past)) return;
+  int tokens = tokens_of(s, row0, n_new, first);
   const int skip = (int)(tile - pl.before) * kTokens;
   first += skip;
   tokens = min(tokens - skip, kTokens);
   const int pages = (past + (first - row0) + tokens) >> 6;
   // Whole strips are read, so that a strip has one norm whoever writes it.
-  const int full = (past + a.cu[pl.b + 1] - row0) >> 6;
+  const int full = (past + n_new) >> 6;
   const int64_t unit = (int64_t)pl.b * a.Hkv + h;
   const float* summaries = a.summaries + unit * a.max_pages * kD;
   // Lane (g, t) has dimensions 16 j + 4 t .. + 3 of pages g and g + 8 of a strip. The first strip is on its way while the queries
@@ -599,7 +610,8 @@ kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* se
   const int64_t row = T == 32 ? (int64_t)blockIdx.x * kRows + (threadIdx.x >> 5) : blockIdx.x;
   if (row >= (int64_t)(s.t1 - s.t0) * a.Hkv) return;
   const int token = s.t0 + (int)(row / a.Hkv), h = (int)(row % a.Hkv);
-  if (token >= a.cu[a.B]) return;  // padding
+  const int32_t strange = *s.strange;  // (on its way with the others)
+  if (token >= a.cu[a.B] && !strange) return;  // padding
   // The last request that begins at the token or before it: 32 places a look.
   int lo = 0, n = a.B;
   while (n > 1) {
@@ -610,7 +622,12 @@ kv8_select_pick(const Kv8Args a, const Rows q, SelectSpace s, int k, int32_t* se
     n = min(step, n - w * step);
   }
   int row0, n_new, past;
-  if (!kv8_request(a, lo, false, row0, n_new, past) || token < row0 || token >= row0 + n_new) return;
+  bool its = kv8_request(a, lo, false, row0, n_new, past) && token >= row0 && token < row0 + n_new;
+  if (strange) {  // the search may have gone astray
+    lo = owner_of(a, token);
+    its = lo >= 0 && kv8_request(a, lo, false, row0, n_new, past);
+  }
+  if (!its) return;
   const int64_t unit = (int64_t)lo * a.Hkv + h;
   RowIn in;
   in.pages = (past + token - row0 + 1) >> 6;
@@ -650,7 +667,7 @@ cudaError_t launch_scores(const Kv8Args& a, const Rows& q, const SelectSpace& s,
 
 int64_t kv8_select_workspace(const Kv8Args& a) {
   const int64_t pitch = pitch_of(a.max_pages), rows = slab_tokens(a) * a.Hkv;
-  return rows * (pitch * 12 + 4) + (int64_t)a.B * a.Hkv * (pitch / kStrip) * 4;
+  return rows * (pitch * 12 + 4) + (int64_t)a.B * a.Hkv * (pitch / kStrip) * 4 + 4;
 }
 
 cudaError_t launch_kv8_select(const Kv8Args& a, const Rows& q, int topk, int32_t* sel, void* workspace, int sm_count,
@@ -662,6 +679,7 @@ cudaError_t launch_kv8_select(const Kv8Args& a, const Rows& q, int topk, int32_t
   s.scores = reinterpret_cast<float*>(s.exact + rows * s.pitch);
   s.norms = s.scores + rows * s.pitch;
   s.qnorms = s.norms + (int64_t)a.B * a.Hkv * (s.pitch / kStrip);
+  s.strange = reinterpret_cast<int32_t*>(s.qnorms + rows);
   for (int64_t t = 0; t < a.total_new; t += slab) {
     s.t0 = (int)t;
     s.t1 = (int)(t + slab < a.total_new ? t + slab : a.total_new);

@@ -319,7 +319,8 @@ __device__ __forceinline__ Place locate_rows(const Kv8Args& a, int64_t* scratch,
           return ok && (!strange || (bits[b >> 5] >> (b & 31) & 1)) ? weight(row0, n_new, past) : (int64_t)0;
         },
         at);
-    if (strange || !__syncthreads_or(mine)) return p;
+    // (locate has every warp look at up to 128 requests)
+    if (strange || !(a.B <= 128 ? __any_sync(0xffffffffu, mine) : __syncthreads_or(mine))) return p;
     strange = true;
     if (threadIdx.x < 32)
       each_request(a, [&](int b, bool counts, int, int) {

@@ -9,6 +9,7 @@ pytestmark = pytest.mark.gpu
 import kv8_rows_ref as R  # noqa: E402
 from test_gpu_kv8 import D, PAGE, ints, spin  # noqa: E402
 from test_gpu_kv8_rows import SCALE, Case  # noqa: E402
+from test_gpu_kv8_select import handle, rand, want  # noqa: E402
 from test_kv8_requests_in_order import in_range, that_count  # noqa: E402
 
 
@@ -56,3 +57,48 @@ def test_attention_over_lists(cu, total, group):
         left -= set(range(r0, r1))
     assert (out[sorted(left)] == 7.0).all()
     assert int(h.error) == (0 if all(ok) else 32)
+
+
+@pytest.mark.parametrize("pages,turns", [(30, False), (700, False), (2100, False), (1 << 20, True)])
+@pytest.mark.parametrize("cu,total", STEPS, ids=lambda x: str(x)[:30])
+def test_select(cu, total, pages, turns):
+    B, most, group, heads, k = len(cu) - 1, max(2, total), 2, 1, 5
+    if turns and B > 20:
+        pytest.skip("the summaries would be large")
+    rng = random.Random(total + pages)
+    seen = min(pages, 2100) - (total + 63) // PAGE - 1
+    past = [rng.choice([0, 100, rng.randint(0, seen * PAGE)]) for _ in range(B)]
+    s = rand(1, B, heads, min(pages, 2100), D)
+    if turns:
+        wide = torch.empty((B, heads, pages, D), device="cuda")
+        wide[:, :, : s.shape[2]] = s
+        c = handle(B, heads, group, wide)
+    else:
+        c = handle(B, heads, group, s)
+    q = rand(2, total, heads * group, D).to(torch.bfloat16)
+    sel = torch.full((total, heads, k), -77, dtype=torch.int32, device="cuda")
+    step = spin().SpinKV8Step(ints(past), ints(cu), total, most)
+    for _ in range(2):  # what the workspace holds of the last call does not matter
+        c.select(step, q, sel)
+    left = set(range(total))
+    for b in that_count(cu, total, most):
+        r0, r1 = cu[b], cu[b + 1]
+        assert torch.equal(sel[r0:r1], want(q[r0:r1], s[b:b + 1], [past[b]], [r1 - r0], group, k)), b
+        left -= set(range(r0, r1))
+    assert (sel[sorted(left)] == -77).all()
+    assert int(c.error) == (0 if all(in_range(cu, total, most)) else 32)
+
+
+def test_select_in_order_after_a_step_that_was_not():
+    s, past, q = rand(1, 3, 1, 40, D), [2000, 1000, 2300], rand(2, 6, 2, D).to(torch.bfloat16)
+    c = handle(3, 1, 2, s)
+    sel = torch.full((6, 1, 4), -77, dtype=torch.int32, device="cuda")
+    cu = ints([0, 4, 2, 6])
+    step = spin().SpinKV8Step(ints(past), cu, 6, 6)
+    c.select(step, q, sel)
+    assert (sel[4:] == -77).all() and (sel[:4] >= 0).all()
+    cu.copy_(ints([0, 2, 4, 6]))
+    c.error.zero_()
+    c.select(step, q, sel)
+    assert torch.equal(sel, want(q, s, past, [2, 2, 2], 2, 4))
+    c.check()

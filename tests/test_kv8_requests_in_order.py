@@ -9,7 +9,7 @@ import re
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sparse_attention_tiered_gb300", "csrc")
-KERNELS = [("k_kv8_rows.cu", "kv8_rows_blocks")]
+KERNELS = [("k_kv8_rows.cu", "kv8_rows_blocks"), ("k_kv8_select.cu", "kv8_select_scores")]
 
 
 def in_range(cu, total, max_new):
@@ -75,3 +75,34 @@ def test_the_kernels_lay_out_those_alone(file, kernel):
     body = source[source.index(kernel + "("):]
     body = body[: body.index("__global__") if "__global__" in body else len(body)]
     assert "locate_rows(" in body and not re.search(r"\blocate\(", body)
+
+
+def last_that_begins(cu, token):
+    """A search of cu_new by halves, 32 parts at a time, which counts the places that do not lie behind the token."""
+    lo, n = 0, len(cu) - 1
+    while n > 1:
+        step = (n + 31) // 32
+        w = max(0, sum(i * step < n and cu[lo + i * step] <= token for i in range(32)) - 1)
+        lo, n = lo + w * step, min(step, n - w * step)
+    return lo
+
+
+def test_a_search_finds_a_tokens_request_only_while_all_are_in_range():
+    """Request 2 of these is in range and shares no row, but the search for its token ends at request 1."""
+    cu = [0, 9, 4, 6]
+    assert that_count(cu, 6, 6) == [2] and last_that_begins(cu, 4) == 1
+    for seed in range(200):
+        rng = random.Random(seed)
+        cu = [0] + sorted(rng.randint(0, 90) for _ in range(rng.randint(1, 70)))
+        for token in range(cu[-1]):
+            b = last_that_begins(cu, token)
+            assert cu[b] <= token < cu[b + 1]
+
+
+def test_select_searches_only_while_all_are_in_range():
+    source = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "k_kv8_select.cu")).read())
+    body = source[source.index("kv8_select_pick("):]
+    search = re.sub(r"\s+", " ", body[: body.index("RowIn in;")])
+    assert search.endswith("if (strange) { lo = owner_of(a, token); its = lo >= 0 && kv8_request(a, lo, false, row0, n_new, past); } "
+                           "if (!its) return; const int64_t unit = (int64_t)lo * a.Hkv + h; ")
+    assert [m for m in re.findall(r"if \(([^{;]*)\) return;", search)][1:] == ["token >= a.cu[a.B] && !strange", "!its"]
