@@ -463,8 +463,9 @@ kv8_pool_lengths(const Kv8Args a, int32_t* len, const int32_t* src) {
 
 unsigned at_most(int64_t n, int64_t limit) { return (unsigned)(n < 1 ? 1 : n < limit ? n : limit); }
 
+// A launch may have 48 KB of shared memory unasked, the kernel's own included: 2.1 KB at most here.
 cudaError_t shared_bytes(const void* kernel, size_t bytes) {
-  return bytes <= 48 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  return bytes <= 40 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 cudaError_t count(const Kv8Args& a, const int32_t* refs, const PoolSpace& s, int requests, cudaStream_t st) {

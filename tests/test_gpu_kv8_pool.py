@@ -259,3 +259,42 @@ def test_captured_calls_replay():
         ref.compact()
         assert r.c.table.tolist() == ref.table and r.c.refs.tolist() == ref.refs and lengths.tolist() == n
     r.c.check()
+
+
+@pytest.mark.parametrize("batch", [3413, 3414, 4094, 4095, 4096, 4097])
+def test_fork_batches_at_the_borders_of_shared_memory(batch):
+    """40 and 48 KB of a CTA's list of moves, and the last batch that a CTA holds 16 bytes each of."""
+    rng = random.Random(batch)
+    r = Both(batch, 1, 1, batch, [rng.randint(0, 127) for _ in range(batch)], seed=batch)
+    src = [rng.choice([-1, rng.randrange(batch)]) for _ in range(batch)]
+    src[0], src[-1] = batch - 1, 0
+    r.fork(src)
+    r.same()
+
+
+@pytest.mark.parametrize("n_pages", [10485760, 10486784, 12050000, 12300000, 12545000, 12582912, 12583936, 1 << 24])
+def test_large_pools(n_pages):
+    """Pools whose sums take 40, 48 and 64 KB. No page moves, so that there need be none: their counts alone are looked at."""
+    from sparse_attention_tiered_gb300 import _binding as B
+
+    refs = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+    h = spin().SpinKV8(2, 1, 1, 4, 8, table=ints([[[0, 1, -1, -1], [2, -1, -1, -1]]]).view(2, 1, 4))
+    refs[:3] = 1
+    c = h.c
+    c.n_pages = n_pages
+    free, ws = ints([0]), torch.empty(B.spin_kv8_pool_workspace(c), dtype=torch.uint8, device="cuda")
+    step, _ = step_of([128, 64], [64, 128])
+    B.spin_kv8_compact(c, refs.data_ptr(), free.data_ptr(), ws.data_ptr(), ws.numel())
+    assert int(free) == n_pages - 3
+    B.spin_kv8_reserve(c, step.c, refs.data_ptr(), free.data_ptr(), ws.data_ptr(), ws.numel())
+    assert int(free) == n_pages - 6
+    B.spin_kv8_compact(c, refs.data_ptr(), free.data_ptr(), ws.data_ptr(), ws.numel())
+    assert int(free) == n_pages - 6
+    assert h.table.flatten().tolist() == [0, 1, 3, -1, 2, 4, 5, -1]
+    refs[:] = 1  # the last page is the one that is left
+    refs[-1] = 0
+    h.table[0, 0, 3] = -1
+    one, _ = step_of([192, 0], [64, 0])
+    B.spin_kv8_reserve(c, one.c, refs.data_ptr(), free.data_ptr(), ws.data_ptr(), ws.numel())
+    assert int(free) == 0 and int(h.table[0, 0, 3]) == n_pages - 1 and int(refs.min()) == 1
+    B.spin_kv8_status(c)
