@@ -218,7 +218,8 @@ class SpinKV8:
 
     def _space(self, kind, nbytes, given):
         """(address, bytes) of the given workspace, or of one of the handle's own that is large enough. Those that were
-        outgrown stay, for the graphs that were captured with them."""
+        outgrown stay, for the graphs that were captured with them; each is at least twice the one before, so that a batch that
+        grows a row at a time makes few, and all of them hold less than four times the most that was asked for."""
         if given is not None:
             _tensor("workspace", given, self._torch.uint8, None, self.device)
             return given.data_ptr(), given.numel()
@@ -228,7 +229,7 @@ class SpinKV8:
             if torch.cuda.is_current_stream_capturing():
                 raise ValueError(f"the handle's workspace of {kind} has to grow: call it once at this size before capturing, "
                                  "or give one")
-            held.append(torch.empty(nbytes, dtype=torch.uint8, device=dev))
+            held.append(torch.empty(max(nbytes, 2 * held[-1].numel() if held else 0), dtype=torch.uint8, device=dev))
             torch.cuda.synchronize(dev)  # nothing on another stream uses that memory any more
         return held[-1].data_ptr(), held[-1].numel()
 

@@ -254,3 +254,21 @@ def test_the_handle_refuses():
         c.select(st, q, sel, workspace=torch.zeros(8, device="cuda"))
     with pytest.raises(spin().SpinError, match="workspace"):
         c.select(st, q, sel, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+
+
+def test_a_batch_that_grows_a_request_at_a_time():
+    """The handle's workspaces stay in proportion to what the largest call needs."""
+    from sparse_attention_tiered_gb300 import _binding as B
+
+    P, most = 4000, 48
+    s = rand(1, 1, 1, P, D).expand(most, -1, -1, -1).contiguous()
+    c, q = handle(most, 1, 2, s), rand(2, most, 2, D).to(torch.bfloat16)
+    expect = want(q, s, [P * PAGE - 1] * most, [1] * most, 2, 7)
+    for n in range(1, most + 1):
+        st, _ = step_of([P * PAGE - 1] * most, [1] * n + [0] * (most - n))
+        sel = torch.full((n, 1, 7), -77, dtype=torch.int32, device="cuda")
+        c.select(st, q[:n], sel)
+        assert torch.equal(sel, expect[:n])
+        assert sum(t.numel() for t in c._spaces["select"]) < 4 * B.spin_kv8_select_workspace(c.c, n)
+    assert len(c._spaces["select"]) <= 7
+    c.check()
