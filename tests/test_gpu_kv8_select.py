@@ -272,3 +272,74 @@ def test_a_batch_that_grows_a_request_at_a_time():
         assert sum(t.numel() for t in c._spaces["select"]) < 4 * B.spin_kv8_select_workspace(c.c, n)
     assert len(c._spaces["select"]) <= 7
     c.check()
+
+
+@pytest.mark.parametrize("k", [1, 17, 512])
+@pytest.mark.parametrize("pages", [8191, 8192, 8193, 12000, 16383, 16384, 16385, 40000])
+def test_numbers_of_pages_of_a_wide_row(pages, k):
+    """16 or 32 keys a thread, and more than it holds."""
+    case(2, 1, 2, [pages * PAGE - 1, pages * PAGE + 30], [1, 3], k, seed=pages)
+
+
+@pytest.mark.parametrize("k", [11, 512])
+@pytest.mark.parametrize("pages", [5000, 12000, 19900])
+@pytest.mark.parametrize("kind", ["same", "two kinds", "zero", "close", "few kinds"])
+def test_ties_of_a_wide_row(kind, pages, k):
+    """More doubtful pages than a lane each: 64-bit keys, a search of their bits, and ties by rank."""
+    base = rand(3, 1, 1, 1, D)
+    s = base.expand(1, 1, pages, D).clone()
+    if kind == "two kinds":
+        s[:, :, ::3] = rand(4, 1, 1, 1, D)
+    elif kind == "zero":
+        s.zero_()
+    elif kind == "close":
+        s[0, 0, :, 5] = torch.nextafter(s[0, 0, :, 5], torch.where(torch.arange(pages, device="cuda") % 7 == 3, math.inf, s[0, 0, :, 5]))
+    elif kind == "few kinds":
+        s = rand(4, 1, 1, 5, D)[:, :, torch.arange(pages, device="cuda") * 7919 % 5].contiguous()
+    q = rand(6, 1, 4, D).to(torch.bfloat16)
+    past = [pages * PAGE - 1]
+    assert torch.equal(run(q, s, past, [1], 4, k), want(q, s, past, [1], 4, k))
+
+
+@pytest.mark.parametrize("spread", [2, 20, 33, 300])
+@pytest.mark.parametrize("pages", [600, 1500, 3000, 12000, 19900])
+def test_doubtful_pages_around_the_last_place(pages, spread):
+    """So many pages that the first scores cannot tell apart, at the k-th place: fewer than a lane each, and more."""
+    q = rand(6, 1, 4, D).to(torch.bfloat16)
+    s = rand(3, 1, 1, pages, D)
+    order = (s[0, 0].double() @ q.double().sum(1)[0]).sort(descending=True).indices
+    k = 60
+    some = order[k - spread // 2 - 1:][:spread] if spread < 2 * k else order[:spread]
+    s[0, 0, some] = s[0, 0, order[k - 1]].clone()
+    s[0, 0, some[::2], 7] = torch.nextafter(s[0, 0, some[::2], 7], torch.full_like(s[0, 0, some[::2], 7], math.inf))
+    past = [pages * PAGE - 1]
+    assert torch.equal(run(q, s, past, [1], 4, k), want(q, s, past, [1], 4, k))
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("pages", [5000, 12000, 19900])
+def test_numbers_that_are_not_finite_in_a_wide_row(value, pages):
+    s = rand(1, 1, 2, pages, D)
+    s[0, 0, 3, 17] = s[0, 0, pages - 2, 1] = value
+    s[0, 1, :, 5] = value
+    q = rand(2, 2, 4, D).to(torch.bfloat16)
+    q[1, 1, 9] = value
+    past = [pages * PAGE - 2]
+    for k in (5, 512):
+        assert torch.equal(run(q, s, past, [2], 2, k), want(q, s, past, [2], 2, k))
+
+
+@pytest.mark.parametrize("size", [1e-42, 1e-18, 1e25, 3e38])
+@pytest.mark.parametrize("pages", [12000, 19900])
+def test_sizes_of_a_wide_row(size, pages):
+    s = (rand(1, 1, 1, pages, D).clamp(-1, 1).double() * size).float()
+    q = rand(2, 2, 2, D).to(torch.bfloat16)
+    past = [pages * PAGE - 2]
+    assert torch.equal(run(q, s, past, [2], 2, 99), want(q, s, past, [2], 2, 99))
+
+
+@pytest.mark.parametrize("width", [513, 1025, 2049, 8193, 16385, 70000])
+def test_tables_wider_than_the_requests(width):
+    """Rows of all lengths in a table made for longer ones."""
+    past, new = [0, 63, 700, 300 * PAGE - 2, 500 * PAGE, 5000], [1, 1, 70, 4, 1, 0]
+    case(6, 2, 3, past, new, 20, seed=width, pages=width, pad=3)
