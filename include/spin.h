@@ -447,7 +447,9 @@ int spin_kv8_select_workspace(const spin_kv8* cache, int32_t total_new, int64_t*
 int spin_kv8_select(const spin_kv8* cache, const spin_kv8_step* step, const spin_rows* q, int32_t topk, int32_t* sel,
                     void* workspace, int64_t workspace_bytes, spin_stream_t stream);
 
-/* Bytes of device workspace that spin_kv8_attend_rows needs for steps of up to total_new rows with lists of topk. */
+/* Bytes of device workspace that spin_kv8_attend_rows needs for steps of up to total_new rows with lists of topk:
+ * spin_kv8_workspace's, and what holds the lists of neighbouring tokens if they have nothing in common (9 MB for 2048 tokens
+ * of 8 groups of 8 heads, lists of 32 pages and tables of 500; up to about 4 GB, more tokens are taken in turns). */
 int spin_kv8_attend_rows_workspace(const spin_kv8* cache, int32_t total_new, int32_t topk, int64_t* bytes);
 
 /* Attention of the step's queries where every token has its own list of pages for each KV head: sel, device

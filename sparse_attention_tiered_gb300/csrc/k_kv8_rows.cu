@@ -17,12 +17,15 @@ constexpr int kWindow = 2048;  // pages that are marked at a time
 // Steps that beginning and ending a block costs. (Six ragged prompts: 68.1 us with 1, 58.4 with 4, 57.8 with 8, 60.8 with 20; one long
 // chunk, whose blocks are alike, 513 to 521.)
 constexpr int kUnitSteps = 8;
+// Of the blocks that are laid out at a time, and their items. A block's are sized for lists that have nothing in common, so tokens
+// by the ten thousand take turns: three launches each, which is little beside the attention of that many.
+constexpr int64_t kTurnBytes = 4ll << 30;
 
-// A CTA a block and head. The tokens' pages are marked in a window of shared memory, a bit a token, and read out in order;
+// A CTA a block and head, of the rows of tokens t0 .. t1 - 1. The tokens' pages are marked in a window of shared memory, a bit a token, and read out in order;
 // what lies beyond the window waits for the next, which begins at the lowest page that is left. One chain of loads (lengths,
 // lists, table) and no more than a GPU's worth of CTAs for 512 tokens of 8 heads: 10 us alone, cold, whatever the lists.
 __global__ void __launch_bounds__(kThreads)
-kv8_rows_blocks(const Kv8Args a, const Rows out, const int32_t* sel, int topk, int64_t cap, RowLists s) {
+kv8_rows_blocks(const Kv8Args a, const Rows out, const int32_t* sel, int topk, int64_t cap, int t0, int t1, RowLists s) {
   __shared__ __align__(16) uint32_t marks[2][kWindow];
   __shared__ int64_t scratch[36];
   __shared__ uint32_t bits[kMaxRequests / 32];
@@ -35,16 +38,17 @@ kv8_rows_blocks(const Kv8Args a, const Rows out, const int32_t* sel, int topk, i
   bool strange;
   // Requests that count share no row, so that their blocks are no more than were launched and have a place (most_blocks).
   const Place pl = locate_rows(
-      a, scratch, bits, blockIdx.x == 0, strange, [&](int, int n, int) { return ((int64_t)n * a.G + R - 1) / R; },
+      a, scratch, bits, blockIdx.x == 0, strange,
+      [&](int row, int n, int) { return ((int64_t)max(0, min(row + n, t1) - max(row, t0)) * a.G + R - 1) / R; },
       [&](int64_t) { return (int64_t)number; });
   if (blockIdx.x == 0 && tid == 0) *s.n_blocks = (int)pl.total * a.Hkv;
   if (pl.b >= a.B || !kv8_request(a, pl.b, false, row0, n_new, past)) return;
   RowBlock t;
   t.b = pl.b;
   t.h = h;
-  t.first_row = (int)(number - pl.before) * R;
+  t.first_row = max(0, t0 - row0) * a.G + (int)(number - pl.before) * R;
   t.row0 = row0;
-  t.n_new = (int)(min((int64_t)n_new * a.G, (int64_t)t.first_row + R) + a.G - 1) / a.G;
+  t.n_new = (int)(min((int64_t)min(n_new, t1 - row0) * a.G, (int64_t)t.first_row + R) + a.G - 1) / a.G;
   t.past = past;
   t.full = (past + n_new) >> 6;
   t.tail = (past + n_new) & (kPart - 1);
@@ -194,9 +198,8 @@ kv8_rows_single(const Kv8Args a, const int32_t* sel, int topk, int32_t* lists) {
   for (int x = count + lane; x < topk; x += 32) out[x] = -1;
 }
 
-int64_t most_blocks(const Kv8Args& a) {  // of each head
-  const int64_t n = a.total_new;
-  return n * a.G / list_rows(a.G) + (a.B < n ? a.B : n);
+int64_t most_blocks(const Kv8Args& a, int64_t tokens) {  // of each head
+  return tokens * a.G / list_rows(a.G) + (a.B < tokens ? a.B : tokens);
 }
 
 int64_t most_items(const Kv8Args& a, int topk) {  // of a block
@@ -204,11 +207,23 @@ int64_t most_items(const Kv8Args& a, int topk) {  // of a block
   return 2 * ((n < a.max_pages ? n : a.max_pages) + 1);  // of each tile, and the tail
 }
 
+int64_t block_bytes(const Kv8Args& a, int topk) {  // of all heads'
+  return a.Hkv * ((int64_t)sizeof(RowBlock) + most_items(a, topk) * (int64_t)sizeof(RowItem));
+}
+
+// Tokens of a turn: as many as have no more blocks than kTurnBytes hold, by either bound on the requests among them.
+int64_t turn_tokens(const Kv8Args& a, int topk) {
+  const int64_t blocks = kTurnBytes / block_bytes(a, topk), R = list_rows(a.G);
+  const int64_t few = (blocks - a.B) * R / a.G, many = blocks * R / (R + a.G);
+  const int64_t n = few > many ? few : many > 1 ? many : 1;
+  return n < a.total_new ? n : a.total_new;
+}
+
 }  // namespace
 
 int64_t kv8_rows_workspace(const Kv8Args& a, int topk) {
-  const int64_t blocks = most_blocks(a) * a.Hkv, lists = (int64_t)a.B * a.Hkv * topk * 4;
-  const int64_t many = 16 + blocks * ((int64_t)sizeof(RowBlock) + most_items(a, topk) * (int64_t)sizeof(RowItem));
+  const int64_t lists = (int64_t)a.B * a.Hkv * topk * 4;
+  const int64_t many = 16 + most_blocks(a, turn_tokens(a, topk)) * block_bytes(a, topk);
   return kv8_attend_workspace(a) + (many > lists ? many : lists);
 }
 
@@ -220,14 +235,19 @@ cudaError_t launch_kv8_rows(const Kv8Args& a, const Rows& q, const Rows& out, fl
     const cudaError_t e = launch_early(kv8_rows_single, dim3((unsigned)(a.B * a.Hkv)), 32, 0, st, a, sel, topk, lists);
     return e != cudaSuccess ? e : launch_kv8_attend(a, q, out, scale, lists, topk, workspace, sm_count, st);
   }
+  const int64_t turn = turn_tokens(a, topk), most = most_blocks(a, turn) * a.Hkv;
   RowLists s;
-  const int64_t blocks = most_blocks(a) * a.Hkv;
   s.n_blocks = reinterpret_cast<int32_t*>(rest);
   s.blocks = reinterpret_cast<RowBlock*>(rest + 16);
-  s.items = reinterpret_cast<RowItem*>(s.blocks + blocks);
-  const cudaError_t e = launch_early(kv8_rows_blocks, dim3((unsigned)blocks), kThreads, 0, st, a, out, sel, topk,
-                                     most_items(a, topk), s);
-  return e != cudaSuccess ? e : launch_kv8_lists(a, q, out, scale, s, workspace, sm_count, st);
+  s.items = reinterpret_cast<RowItem*>(s.blocks + most);
+  for (int64_t t = 0; t < a.total_new; t += turn) {
+    const int64_t tokens = t + turn < a.total_new ? turn : a.total_new - t, blocks = most_blocks(a, tokens) * a.Hkv;
+    cudaError_t e = launch_early(kv8_rows_blocks, dim3((unsigned)blocks), kThreads, 0, st, a, out, sel, topk, most_items(a, topk), (int)t,
+                                 (int)(t + tokens), s);
+    if (e == cudaSuccess) e = launch_kv8_lists(a, q, out, scale, s, workspace, sm_count, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace spin
