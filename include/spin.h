@@ -331,11 +331,10 @@ int spin_measure_host_read(const void* host, int64_t bytes, int32_t ctas_per_sm,
  * The 8-bit paged cache: keys and values that stay in HBM, appended with the position
  * rotation on the way and attended in place. No counterpart on the SPIN pages; its pages
  * are per KV head and hold one 64-token partition, as everywhere in this library, so the
- * partitions that Select picks (spin_select_noalloc, over the summaries the append writes)
- * are a page list of the attention. Select takes one count of partitions a call, and dense
- * rows of them: requests with the same number of complete pages are selected by one call,
- * others by calls of their own, over a dense copy of the summaries of their complete pages.
- * What lies behind those is not the request's, and must not be scored.
+ * partitions that Select picks over the summaries the append writes are a page list of the
+ * attention. spin_kv8_select takes a step of requests of any lengths. (spin_select_noalloc does for
+ * requests with the same number of complete pages a call, over a dense copy of the summaries of those;
+ * what lies behind them is not the request's, and must not be scored.)
  *
  * One spin_kv8 describes one layer's cache. The caller owns every array of it; the calls
  * allocate nothing, keep nothing between calls, and may be captured into CUDA graphs.
@@ -439,6 +438,7 @@ int spin_kv8_select_workspace(const spin_kv8* cache, int32_t total_new, int64_t*
  * 64 (p + 1) <= past[b] + i + 1, the topk with the largest (sum of the group's rotated queries) . summaries[b][h][p]. The
  * scores are compared as exact numbers to 64 bits, equal ones go to the lower page, and one that is no number (the
  * page holds something not finite, or the query is) counts as -infinity: how tokens are split into calls does not matter.
+ * (Its time follows max_pages as well as the lengths: many rows take several times as long in a table of more than 2048 pages.)
  * q: rotated bf16 [total_new][q_heads]. sel: device int32 [total_new][kv_heads][topk], pages in ascending
  * order, then -1. Rows of padding, and of requests whose numbers are out of range, are not written; where cu_new descends, which
  * the error word tells, nor are those of a request that begins before the end of another before it that is in range. 1 <= topk <= 512. The
@@ -448,13 +448,14 @@ int spin_kv8_select(const spin_kv8* cache, const spin_kv8_step* step, const spin
                     void* workspace, int64_t workspace_bytes, spin_stream_t stream);
 
 /* Bytes of device workspace that spin_kv8_attend_rows needs for steps of up to total_new rows with lists of topk:
- * spin_kv8_workspace's, and what holds the lists of neighbouring tokens if they have nothing in common (9 MB for 2048 tokens
+ * spin_kv8_workspace's, and what holds the lists of neighbouring tokens if they have nothing in common (8 MB for 2048 tokens
  * of 8 groups of 8 heads, lists of 32 pages and tables of 500; up to about 4 GB, more tokens are taken in turns). */
 int spin_kv8_attend_rows_workspace(const spin_kv8* cache, int32_t total_new, int32_t topk, int64_t* bytes);
 
 /* Attention of the step's queries where every token has its own list of pages for each KV head: sel, device
  * int32 [total_new][kv_heads][topk], as spin_kv8_select writes it. Row i of request b sees the tokens of the
- * listed pages p with 64 (p + 1) <= past[b] + i + 1, each page once however often it is listed and in any order; other
+ * listed pages p with 64 (p + 1) <= past[b] + i + 1, each page once however often it is listed (spin_kv8_attend counts a
+ * page as often as it is listed) and in any order; other
  * entries (-1, a page that it does not see whole) are no page. And it sees its newest tokens, those at
  * 64 ((past[b] + i + 1) / 64) .. past[b] + i, wherever they are by now. Everything else is as in spin_kv8_attend.
  * Where cu_new descends, which the error word tells, requests may name the same rows: with max_new above 1 one that begins

@@ -7,7 +7,7 @@
 //
 // All but the moving of many pages is a chain of dependent loads and two launches, the second of which begins under the first.
 // Reserving one token of 256 requests from a pool of 858,000 pages, 3.4 MB of counts, takes 16 us through the Python call; the
-// chunks of 24 requests, from a small pool, take 14.
+// chunks of 24 requests, from a small pool, take 13 (both with a copy of some 3 us that puts the state back).
 #include "kv8_dev.cuh"
 
 namespace spin {
@@ -270,8 +270,8 @@ kv8_pool_move(const Kv8Args a, int32_t* refs, PoolSpace s, int32_t* free_pages) 
 // Forking. Requests' rows change places among themselves, in place: a CTA takes a range of columns of all moved
 // requests, reads every source into registers, and only then writes. No copy of the rows has to be kept anywhere, and
 // any map of requests to requests will do. Summaries go along whichever page an entry named before.
-// One prompt of 469 pages into 7 others, 29 MB: 14.8 us a call; 64 of 128 requests of 20 to 98 pages, 35 MB: 17.0 us, of which the
-// lengths' launch takes 3: they may change only when every CTA has read them.
+// One prompt of 469 pages into 7 others, 29 MB: 14 to 17 us a call; 64 of 128 requests of 20 to 98 pages, 35 MB: 20.5 us (both with a
+// copy of some 3 us that puts the state back). The lengths' launch takes 3: they may change only when every CTA has read them.
 // ---------------------------------------------------------------------------
 constexpr int kForkThreads = 512;
 constexpr int kHeld = 32;         // 32-bit registers a thread, of the columns that pass through it

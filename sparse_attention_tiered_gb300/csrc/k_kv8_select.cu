@@ -15,8 +15,8 @@
 // bound by HBM, and for a chunk's tokens from L2. A lane's 16-byte piece of a summary row is its k indices of one product:
 // the k index may be permuted as long as the queries agree, so nothing moves between lanes. The second finds the k-th largest
 // of a row's scores by bisection on their bits: a warp a row, the scores in registers, a count a step, and done once a
-// step leaves k of them above it, some 8 steps. Alone, with cold caches: 32 requests of 512 pages, 67 MB, 17 us and 17; a chunk of
-// 2048 tokens over 500 pages, 8 heads, 52 us (tensor pipe 24%, issue slots 33%: 520 CTAs are 1.7 turns) and 40 (issue slots 59%).
+// step leaves k of them above it, some 8 steps. Alone, with cold caches: 32 requests of 512 pages, 67 MB, 19 us and 18; a chunk of
+// 2048 tokens over 500 pages, 8 heads, 53 us (tensor pipe 22%, issue slots 32%: 520 CTAs are 1.7 turns) and 39 (issue slots 65%).
 #include "kv8_dev.cuh"
 
 namespace spin {
@@ -683,14 +683,16 @@ cudaError_t launch_kv8_select(const Kv8Args& a, const Rows& q, int topk, int32_t
   for (int64_t t = 0; t < a.total_new; t += slab) {
     s.t0 = (int)t;
     s.t1 = (int)(t + slab < a.total_new ? t + slab : a.total_new);
-    // 8 tokens a CTA or 32: 32 requests of 512 pages with 8 tokens each 27.4 and 35.4 us, with 12 38.3 and 36.2, with 64 112 and 84.
+    // 8 tokens a CTA or 32 (here and below: calls back to back, 8 KV heads, inputs larger than L2): 32 requests of 512 pages with 1 token
+    // each 28.1 and 34.7 us, with 8 32.4 and 39.7, with 12 41.3 and 40.6, with 64 112 and 83.
     cudaError_t e = a.max_new <= 8 ? launch_scores<1>(a, q, s, sm_count, st) : launch_scores<4>(a, q, s, sm_count, st);
     if (e != cudaSuccess) return e;
     const int64_t n = (int64_t)(s.t1 - s.t0) * a.Hkv;
-    // A warp a row, holding 16 or 64 scores a lane, or a CTA a row. Up to 512 pages: 32 requests of 8 heads 22.9, 24.9 and 31.3 us, a
-    // chunk of 2048 tokens 77, 102 and 635. 1000 pages: 4 requests 19.3 with a warp a row and 20.6 with a CTA, 32 requests 43.6 and
-    // 46.1, a chunk 138 and 529. 2048 pages: 1 request 26.6 and 19.9, 75 requests 134 and 127, 120 requests 206 and 208, a chunk 291
-    // and 609: a CTA passes a row in a third of a warp's time, which pays for three turns of two an SM. A warp cannot hold more.
+    // A warp a row, holding 16 or 64 scores a lane, or a CTA a row. Up to 512 pages: 32 requests 28.2, 30.9 and 35.6 us, a
+    // chunk of 2048 tokens 82, 108 and 641. 1000 pages: 4 requests 18.2 with a warp a row and 20.9 with a CTA, 32 requests 43.4 and
+    // 47.5, a chunk 143 and 535. 2048 pages: 1 request 25.6 and 18.4, 75 requests 134 and 129, 120 requests 206 and 209, a chunk 304
+    // and 620: a CTA passes a row in a third of a warp's time, which pays for three turns of two an SM. A warp cannot hold more.
+    // What is known here is the table's width, not the rows': short rows of a table of more than 2048 pages take a CTA each, too.
     const bool warps = a.max_pages <= 1024 || (a.max_pages <= 2048 && n > 6 * (int64_t)sm_count);
     const dim3 narrow((unsigned)((n + kRows - 1) / kRows));
     e = a.max_pages <= 512    ? launch_early(kv8_select_pick<32, 16>, narrow, kRows * 32, 0, st, a, q, s, topk, sel)
